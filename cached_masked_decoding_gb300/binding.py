@@ -23,6 +23,9 @@ CACHE_NONE, CACHE_PREFIX, CACHE_DUAL = 0, 1, 2
 MODES = {"none": CACHE_NONE, "prefix": CACHE_PREFIX, "dual": CACHE_DUAL}
 SEL_THRESHOLD, SEL_FIXED_K, SEL_FACTOR, SEL_BUDGET, SEL_SCHEDULE = 0, 1, 2, 3, 4
 PREC_SPLIT, PREC_BF16 = 0, 1
+DTYPES = {"f32": 0, "bf16": 1, "f16": 2}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "by_parts": 3}
 TENSOR_IDS = {"embed": 1, "attn_norm": 2, "wq": 3, "wk": 4, "wv": 5, "wo": 6, "ffn_norm": 7, "wg": 8, "wu": 9,
               "wd": 10, "final_norm": 11, "lm_head": 12}
 KERNEL_CLASSES = ("embed", "qkv_gemm", "attention", "o_gemm", "gateup_gemm", "down_gemm", "lm_head_gemm",
@@ -59,6 +62,19 @@ class Stats(ctypes.Structure):
 
     def as_dict(self) -> dict:
         return {f: getattr(self, f) for f, _ in self._fields_}
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("orig_len", ctypes.c_double), ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("amplitude", ctypes.c_double)]
+
+
+class Kv8(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("b", ctypes.c_int32), ("H_kv", ctypes.c_int32),
+                ("T", ctypes.c_int32), ("hd", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
@@ -109,6 +125,13 @@ SIGNATURES = {
     "dllm_op_check": (_I32, [ctypes.POINTER(_I32), _P]),
     "dllm_op_wait_probe": (_I32, [_P, _I32, _I32, _P]),
     "dllm_op_select_commit": (_I32, [_P, _P, _P, _I32, _I32, _I32, _I32, _I32, ctypes.POINTER(Select), _P, _P]),
+    "dllm_op_rope": (_I32, [_P, _P, _P, _I32, _I32, _I32, _I64, _I64, _I64, _I64, _I32, ctypes.POINTER(Rope), _P]),
+    "dllm_op_kv8_store": (_I32, [ctypes.POINTER(Kv8), _P, _P, _I64, _I64, _I32, _I32, _P, _P, _P]),
+    "dllm_op_kv8_load": (_I32, [ctypes.POINTER(Kv8), _P, _P, _I64, _I64, _I32, _I32, _P, _P, _P]),
+    "dllm_op_attention_kv8": (_I32, [_P, _I64, ctypes.POINTER(Kv8), _P, _F, _P, _I64, _I32, _I32, _P, _I64, _P]),
+    "dllm_op_attention_kv8_workspace": (_I32, [_I32, _I32, _I32, _I32, _I32, _I32, ctypes.POINTER(_I64)]),
+    "dllm_op_quantise8": (_I32, [_P, _I64, _I32, _I32, _I32, _P, _P, _P]),
+    "dllm_op_gemm8": (_I32, [_P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _P]),
     "dllm_last_error": (ctypes.c_char_p, []),
     "dllm_status_string": (ctypes.c_char_p, [_I32]),
     "dllm_version": (_I32, []),
@@ -424,3 +447,66 @@ def op_select_commit(conf_ptr: int, arg_ptr: int, x_ptr: int, b: int, T: int, bl
     check(lib().dllm_op_select_commit(ctypes.c_void_p(conf_ptr), ctypes.c_void_p(arg_ptr), ctypes.c_void_p(x_ptr),
                                       b, T, blk_start, B, mask_id, ctypes.byref(sel), ctypes.c_void_p(count_ptr),
                                       ctypes.c_void_p(stream)))
+
+
+# ------------------------------------------------------------------ 8-bit forms
+
+def make_rope(rot_dim: int, layout: str = "half", theta: float = 1e4, scaling: str = "none", factor: float = 1.0,
+              orig_len: float = 4096.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+              amplitude: float = 0.0) -> Rope:
+    """Rotary positions of the first rot_dim elements of a head; amplitude 0
+    takes the scaling's own."""
+    return Rope(ROPE_LAYOUTS[layout], rot_dim, ROPE_SCALINGS[scaling], 0, theta, factor, orig_len, beta_fast,
+                beta_slow, amplitude)
+
+
+def make_kv8(k_ptr: int, v_ptr: int, k_scale_ptr: int, v_scale_ptr: int, b: int, H_kv: int, T: int, hd: int) -> Kv8:
+    """An 8-bit cache over the caller's device memory: codes [b][H_kv][T][hd],
+    scale bytes [b][H_kv][T]."""
+    return Kv8(k_ptr, v_ptr, k_scale_ptr, v_scale_ptr, b, H_kv, T, hd)
+
+
+def op_rope(x_ptr: int, out_ptr: int, positions_ptr: int, rows: int, heads: int, hd: int, dtype: str, rope: Rope,
+            x_row_stride: int = 0, x_head_stride: int = 0, out_row_stride: int = 0, out_head_stride: int = 0,
+            stream: int = 0):
+    check(lib().dllm_op_rope(x_ptr, out_ptr, positions_ptr, rows, heads, hd, x_row_stride, x_head_stride,
+                             out_row_stride, out_head_stride, DTYPES[dtype], rope, stream))
+
+
+def op_kv8_store(cache: Kv8, k_ptr: int, v_ptr: int, dtype: str, R: int, starts_ptr: int = 0, counts_ptr: int = 0,
+                 k_row_stride: int = 0, v_row_stride: int = 0, stream: int = 0):
+    check(lib().dllm_op_kv8_store(cache, k_ptr, v_ptr, k_row_stride, v_row_stride, DTYPES[dtype], R, starts_ptr,
+                                  counts_ptr, stream))
+
+
+def op_kv8_load(cache: Kv8, k_ptr: int, v_ptr: int, dtype: str, R: int, starts_ptr: int = 0, counts_ptr: int = 0,
+                k_row_stride: int = 0, v_row_stride: int = 0, stream: int = 0):
+    check(lib().dllm_op_kv8_load(cache, k_ptr, v_ptr, k_row_stride, v_row_stride, DTYPES[dtype], R, starts_ptr,
+                                 counts_ptr, stream))
+
+
+def attention_kv8_workspace(b: int, H: int, H_kv: int, hd: int, R: int, T: int) -> int:
+    """Bytes of device workspace op_attention_kv8 needs for this shape on the
+    current device."""
+    n = ctypes.c_int64()
+    check(lib().dllm_op_attention_kv8_workspace(b, H, H_kv, hd, R, T, ctypes.byref(n)))
+    return n.value
+
+
+def op_attention_kv8(q_ptr: int, cache: Kv8, out_ptr: int, H: int, R: int, limits_ptr: int = 0,
+                     scale: float | None = None, ws_ptr: int = 0, ws_bytes: int = 0, q_row_stride: int = 0,
+                     out_row_stride: int = 0, stream: int = 0):
+    """scale None takes 1/sqrt(hd)."""
+    check(lib().dllm_op_attention_kv8(q_ptr, q_row_stride, cache, limits_ptr,
+                                      cache.hd ** -0.5 if scale is None else scale, out_ptr, out_row_stride, H, R,
+                                      ws_ptr, ws_bytes, stream))
+
+
+def op_quantise8(x_ptr: int, dtype: str, rows: int, K: int, codes_ptr: int, scales_ptr: int, row_stride: int = 0,
+                 stream: int = 0):
+    check(lib().dllm_op_quantise8(x_ptr, row_stride, DTYPES[dtype], rows, K, codes_ptr, scales_ptr, stream))
+
+
+def op_gemm8(W_ptr: int, W_scale_ptr: int, X_ptr: int, X_scale_ptr: int, Y_ptr: int, y_dtype: str, M: int, N: int,
+             K: int, stream: int = 0):
+    check(lib().dllm_op_gemm8(W_ptr, W_scale_ptr, X_ptr, X_scale_ptr, Y_ptr, DTYPES[y_dtype], M, N, K, stream))

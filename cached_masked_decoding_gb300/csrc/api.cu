@@ -28,6 +28,7 @@
 
 #include "../../include/dllm.h"
 #include "launch.h"
+#include "ops8.h"
 #include "small_kernels.cuh"
 
 using namespace dllm;
@@ -2428,6 +2429,43 @@ extern "C" dllm_status dllm_op_attention_tc_ex(const uint16_t* q, const uint16_t
                          false));
   return DLLM_OK;
 }
+
+// ---------------------------------------------------------------- shared with the 8-bit operators (ops8.h)
+namespace dllm {
+
+dllm_status op_fail(dllm_status st, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof(g_err), fmt, ap);
+  va_end(ap);
+  return st;
+}
+
+dllm_status op_cuda_fail(cudaError_t e, const char* what) {
+  return op_fail(DLLM_ECUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+int op_device_sms() { return device_sms(); }
+
+dllm_status op_map_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t planes,
+                      uint64_t row_stride, uint64_t plane_stride, uint32_t box_inner, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return op_fail(DLLM_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t dims[3] = {inner, rows, planes};
+  cuuint64_t strides[2] = {row_stride, plane_stride};
+  cuuint32_t box[3] = {box_inner, box_rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        box_inner == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return op_fail(DLLM_ECUDA, "cuTensorMapEncodeTiled(u8, %llu x %llu x %llu) failed: %d", (unsigned long long)inner,
+                   (unsigned long long)rows, (unsigned long long)planes, (int)r);
+  return DLLM_OK;
+}
+
+}  // namespace dllm
 
 // ---------------------------------------------------------------- bounded-wait probe
 namespace dllm {

@@ -1,0 +1,165 @@
+// The 8-bit K/V cache: quantising rows as they are written, and reading them
+// back.  One scale for each row of hd elements (a token's head), see q8.cuh.
+//
+// Both directions are bound by HBM (store reads 2 hd elements and writes
+// 2 hd + 2 bytes a token and head).  A group of hd / 8 lanes owns a row: each
+// lane takes one 16-byte vector of 16-bit elements, the row's largest value
+// is a shuffle reduction within the group, and a row's codes are one
+// contiguous write of hd bytes.  K and V go in one launch.
+#include "ops8.h"
+#include "q8.cuh"
+
+namespace dllm {
+
+struct Kv8Params {
+  dllm_kv8 c;
+  const void* in[2];     // store: rows of K and V
+  void* out[2];          // load: rows of K and V
+  long long rs[2];       // their row strides, elements
+  const int32_t* starts; // [b] position of a sequence's first row, or null (0)
+  const int32_t* counts; // [b] rows of a sequence that take part, or null (R)
+  int R;
+};
+
+// (sequence, row, head, K or V) of a thread group's item and its cache slot;
+// false where the row takes no part.
+struct Kv8Item {
+  int s, i, h, which;
+  long long slot;        // (s * H_kv + h) * T + position
+  __device__ __forceinline__ bool init(const Kv8Params& p, long long g) {
+    which = (int)(g & 1);
+    g >>= 1;
+    h = (int)(g % p.c.H_kv);
+    g /= p.c.H_kv;
+    i = (int)(g % p.R);
+    g /= p.R;
+    if (g >= p.c.b) return false;
+    s = (int)g;
+    const int n = p.counts ? p.counts[s] : p.R;
+    if (i >= n) return false;
+    const long long pos = (long long)(p.starts ? p.starts[s] : 0) + i;
+    if (pos < 0 || pos >= p.c.T) return false;
+    slot = ((long long)s * p.c.H_kv + h) * p.c.T + pos;
+    return true;
+  }
+};
+
+template <typename E, int HD>
+__global__ void __launch_bounds__(256) kv8_store_kernel(const __grid_constant__ Kv8Params p) {
+  constexpr int L = HD / 8;
+  const long long tid = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int l = (int)(tid % L);
+  Kv8Item it;
+  const bool on = it.init(p, tid / L);
+  float x[8] = {};
+  if (on)
+    E::load8(static_cast<const typename E::T*>(p.in[it.which]) + ((long long)it.s * p.R + it.i) * p.rs[it.which] +
+                 (long long)it.h * HD + l * 8,
+             x);
+  uint32_t m = abs_bits8(x);
+#pragma unroll
+  for (int d = L / 2; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+  if (!on) return;
+  const int byte = scale_byte(m);
+  uint2 codes = make_uint2(0, 0);
+  if (byte != kScaleNan) codes = encode8(x, scale_inverse(byte));
+  *reinterpret_cast<uint2*>((it.which ? p.c.v : p.c.k) + it.slot * HD + l * 8) = codes;
+  if (l == 0) (it.which ? p.c.v_scale : p.c.k_scale)[it.slot] = (uint8_t)byte;
+}
+
+template <typename E, int HD>
+__global__ void __launch_bounds__(256) kv8_load_kernel(const __grid_constant__ Kv8Params p) {
+  constexpr int L = HD / 8;
+  const long long tid = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int l = (int)(tid % L);
+  Kv8Item it;
+  if (!it.init(p, tid / L)) return;
+  const uint2 codes = *reinterpret_cast<const uint2*>((it.which ? p.c.v : p.c.k) + it.slot * HD + l * 8);
+  float x[8];
+  decode8(codes, scale_value((it.which ? p.c.v_scale : p.c.k_scale)[it.slot]), x);
+  E::store8(static_cast<typename E::T*>(p.out[it.which]) + ((long long)it.s * p.R + it.i) * p.rs[it.which] +
+                (long long)it.h * HD + l * 8,
+            x);
+}
+
+dllm_status kv8_check(const dllm_kv8* c, const char* who) {
+  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || c->b < 1 || c->H_kv < 1 || c->T < 1 ||
+      (c->hd != 64 && c->hd != 128) || !op_aligned(c->k, 16) || !op_aligned(c->v, 16))
+    return op_fail(DLLM_EINVAL, "%s: bad cache (b, H_kv, T >= 1, hd 64 or 128, codes 16-byte aligned)%s", who,
+                   c ? "" : ": null");
+  if ((__int128)c->b * c->H_kv * c->T > ((__int128)1 << 48))
+    return op_fail(DLLM_EINVAL, "%s: a cache of b=%d H_kv=%d T=%d is too large", who, c->b, c->H_kv, c->T);
+  return DLLM_OK;
+}
+
+namespace {
+
+template <typename E>
+cudaError_t launch_kv8(const Kv8Params& p, bool store, unsigned grid, cudaStream_t st) {
+  if (store) {
+    if (p.c.hd == 64)
+      kv8_store_kernel<E, 64><<<grid, 256, 0, st>>>(p);
+    else
+      kv8_store_kernel<E, 128><<<grid, 256, 0, st>>>(p);
+  } else {
+    if (p.c.hd == 64)
+      kv8_load_kernel<E, 64><<<grid, 256, 0, st>>>(p);
+    else
+      kv8_load_kernel<E, 128><<<grid, 256, 0, st>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+dllm_status kv8_rows(const dllm_kv8* cache, bool store, const void* k, const void* v, int64_t k_rs, int64_t v_rs,
+                     int32_t dtype, int32_t R, const int32_t* starts, const int32_t* counts, void* stream) {
+  const char* who = store ? "kv8_store" : "kv8_load";
+  if (const dllm_status s = kv8_check(cache, who); s != DLLM_OK) return s;
+  const int es = op_dtype_size(dtype);
+  if (!k || !v || R < 1 || es == 0 || !op_aligned(k, 16) || !op_aligned(v, 16) || !op_aligned(starts, 4) ||
+      !op_aligned(counts, 4))
+    return op_fail(DLLM_EINVAL, "bad %s arguments: R=%d dtype=%d (k and v 16-byte aligned)", who, R, dtype);
+  const long long width = (long long)cache->H_kv * cache->hd;
+  Kv8Params p = {};
+  p.c = *cache;
+  p.rs[0] = k_rs ? k_rs : width;
+  p.rs[1] = v_rs ? v_rs : width;
+  for (const long long rs : p.rs)
+    if (rs < width || rs > (1LL << 40) || (rs * es) % 16)
+      return op_fail(DLLM_EINVAL, "%s: row stride %lld (0, or at least H_kv * hd = %lld and a multiple of 16 bytes)",
+                     who, rs, width);
+  p.in[0] = k;
+  p.in[1] = v;
+  p.out[0] = const_cast<void*>(k);
+  p.out[1] = const_cast<void*>(v);
+  p.starts = starts;
+  p.counts = counts;
+  p.R = R;
+  const __int128 groups = (__int128)2 * cache->b * R * cache->H_kv;
+  const __int128 blocks = (groups * (cache->hd / 8) + 255) / 256;
+  if (blocks > 0x7fffffff)
+    return op_fail(DLLM_EINVAL, "%s: b=%d R=%d H_kv=%d are too many rows for one call", who, cache->b, R, cache->H_kv);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  switch (dtype) {
+    case DLLM_F32: OP_CK(launch_kv8<ElemF32>(p, store, (unsigned)blocks, st)); break;
+    case DLLM_BF16: OP_CK(launch_kv8<ElemBf16>(p, store, (unsigned)blocks, st)); break;
+    default: OP_CK(launch_kv8<ElemF16>(p, store, (unsigned)blocks, st)); break;
+  }
+  return DLLM_OK;
+}
+
+}  // namespace
+}  // namespace dllm
+
+using namespace dllm;
+
+extern "C" dllm_status dllm_op_kv8_store(const dllm_kv8* cache, const void* k, const void* v, int64_t k_row_stride,
+                                         int64_t v_row_stride, int32_t dtype, int32_t R, const int32_t* starts,
+                                         const int32_t* counts, void* stream) {
+  return kv8_rows(cache, true, k, v, k_row_stride, v_row_stride, dtype, R, starts, counts, stream);
+}
+
+extern "C" dllm_status dllm_op_kv8_load(const dllm_kv8* cache, void* k, void* v, int64_t k_row_stride,
+                                        int64_t v_row_stride, int32_t dtype, int32_t R, const int32_t* starts,
+                                        const int32_t* counts, void* stream) {
+  return kv8_rows(cache, false, k, v, k_row_stride, v_row_stride, dtype, R, starts, counts, stream);
+}

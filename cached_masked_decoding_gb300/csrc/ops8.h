@@ -1,0 +1,35 @@
+// Shared by the translation units of the 8-bit operators: error reporting of
+// the C entries, and what each unit gives dllm_op_check.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/dllm.h"
+
+namespace dllm {
+
+// Set this thread's dllm_last_error() message (printf style); returns st.
+dllm_status op_fail(dllm_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+dllm_status op_cuda_fail(cudaError_t e, const char* what);
+
+// SMs of the current device.
+int op_device_sms();
+
+// 8-bit tensor map over [planes][rows][inner] bytes (rows `row_stride`, planes
+// `plane_stride` bytes apart, multiples of 16), box [1][box_rows][box_inner],
+// swizzle over box_inner = 64 or 128 bytes.  Out-of-range elements read 0.
+dllm_status op_map_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t planes,
+                      uint64_t row_stride, uint64_t plane_stride, uint32_t box_inner, uint32_t box_rows);
+
+inline bool op_aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+inline int op_dtype_size(int32_t t) { return t == DLLM_F32 ? 4 : (t == DLLM_BF16 || t == DLLM_F16) ? 2 : 0; }
+
+}  // namespace dllm
+
+#define OP_CK(call)                                                  \
+  do {                                                               \
+    const cudaError_t e_ = (call);                                   \
+    if (e_ != cudaSuccess) return ::dllm::op_cuda_fail(e_, #call);   \
+  } while (0)

@@ -462,6 +462,132 @@ dllm_status dllm_op_select_commit(const float* conf, const int32_t* arg, int32_t
                                   int32_t mask_id, const dllm_select* sel, int32_t* count,
                                   void* cuda_stream);
 
+/* --------------------------------------------------------------- 8-bit forms
+ *
+ * A decode step streams two things: the weights and the K/V cache.  These
+ * entry points are their 8-bit forms, from the projection to the attention
+ * output:  dllm_op_quantise8 + dllm_op_gemm8 (projections), dllm_op_rope
+ * (positions), dllm_op_kv8_store / _load (the cache), dllm_op_attention_kv8
+ * (attention over it).  They allocate nothing, keep nothing between calls and
+ * can be captured into a CUDA graph; calls on different streams do not
+ * disturb one another as long as their outputs and workspaces differ.  Device
+ * pointers belong to the current device, and so does the stream.  Outputs do not overlap inputs
+ * unless the text says so.  The pages have no counterpart: they quantise nothing.
+ *
+ * Codes are e4m3 (sign, 4 exponent, 3 mantissa bits; largest value 448).  A
+ * block of values shares the scale 2^(byte - 127), one byte: the smallest with
+ * max|x| / scale <= 448, at least 2^-127; 1 for a block of zeros.  A code is
+ * x / scale rounded to nearest, ties to even.  The division by a power of two
+ * is exact, so codes do not depend on the arithmetic that forms them, and
+ * since e4m3 is a floating type the power of two costs no precision.  A block
+ * that holds a NaN or an infinity gets the byte 255 and codes 0: every value
+ * of it reads back as NaN. */
+
+typedef enum dllm_dtype { DLLM_F32 = 0, DLLM_BF16 = 1, DLLM_F16 = 2 } dllm_dtype;
+
+typedef enum dllm_rope_layout {
+    DLLM_ROPE_HALF = 0,        /* pair i is elements i and i + rot_dim/2 (rotate-half) */
+    DLLM_ROPE_INTERLEAVED = 1  /* pair i is elements 2i and 2i + 1 */
+} dllm_rope_layout;
+
+/* Turning rate of pair i, radians a position, f_i = theta^(-2i/rot_dim), and
+ * its forms for contexts `factor` times as long: */
+typedef enum dllm_rope_scaling {
+    DLLM_ROPE_UNSCALED = 0,
+    DLLM_ROPE_LINEAR = 1,      /* f_i / factor (position interpolation) */
+    DLLM_ROPE_BASE = 2,        /* theta * factor^(rot_dim / (rot_dim - 2)) in place of theta */
+    DLLM_ROPE_BY_PARTS = 3     /* YaRN: f_i where the pair turns at least beta_fast times within orig_len
+                                  positions, f_i / factor where fewer than beta_slow, a linear ramp over
+                                  the pair index between: from floor to ceil of
+                                  rot_dim ln(orig_len / (2 pi beta)) / (2 ln theta), kept within
+                                  0..rot_dim/2 - 1 */
+} dllm_rope_scaling;
+
+typedef struct dllm_rope {
+    int32_t layout, rot_dim;   /* the first rot_dim elements of a head turn (even, 2..256), the rest is copied */
+    int32_t scaling, reserved;
+    double theta, factor;      /* >= 1; factor is unused when unscaled */
+    double orig_len, beta_fast, beta_slow;   /* by parts only */
+    double amplitude;          /* multiplies cosine and sine; 0: 1, or 0.1 ln(factor) + 1 by parts */
+} dllm_rope;
+
+/* Rotary positions: out = x with the pairs of every head turned by
+ * positions[row] * f_i.  x, out: [rows][heads][hd] of dtype (dllm_dtype), hd
+ * even, 2..1024, with strides in elements between rows and heads (0: dense);
+ * a head's elements are contiguous; a fused [rows][q|k|v] buffer or a
+ * head-major one is covered by strides.  out may be x with the same strides.
+ * positions: device int32 [rows], any value.  Angles are reduced exactly
+ * (64-bit fixed-point turns), so far positions lose nothing; the products
+ * are float32, rounded once.  The rates reach the device with the launch:
+ * *rope may be reused at once. */
+dllm_status dllm_op_rope(const void* x, void* out, const int32_t* positions, int32_t rows, int32_t heads, int32_t hd,
+                         int64_t x_row_stride, int64_t x_head_stride, int64_t out_row_stride,
+                         int64_t out_head_stride, int32_t dtype, const dllm_rope* rope, void* cuda_stream);
+
+/* An 8-bit K/V cache in the caller's device memory: codes [b][H_kv][T][hd]
+ * (16-byte aligned) and scale bytes [b][H_kv][T], one scale for each row of hd
+ * (a token's head).  hd in {64, 128}.  The struct is read during the call. */
+typedef struct dllm_kv8 {
+    uint8_t *k, *v, *k_scale, *v_scale;
+    int32_t b, H_kv, T, hd;
+} dllm_kv8;
+
+/* Quantise rows of K and V into the cache.  k, v: [b*R][H_kv][hd] of dtype,
+ * 16-byte aligned, rows k_row_stride / v_row_stride elements apart (0: dense;
+ * else a multiple of 16 bytes).  Row i of sequence s goes to position
+ * starts[s] + i for i < counts[s] (device int32 [b]; NULL starts: 0, NULL
+ * counts: R).  Rows from counts[s] on are padding, and rows whose position lies outside
+ * [0, T) have no slot: neither is written, every other slot stays as it was. */
+dllm_status dllm_op_kv8_store(const dllm_kv8* cache, const void* k, const void* v, int64_t k_row_stride,
+                              int64_t v_row_stride, int32_t dtype, int32_t R, const int32_t* starts,
+                              const int32_t* counts, void* cuda_stream);
+
+/* Read rows back: the inverse of dllm_op_kv8_store with the same arguments,
+ * code * scale rounded to dtype (exact in float32 and bf16 down to their
+ * subnormals; in f16 where it is in range).  Rows without a slot are left as
+ * they were in k and v. */
+dllm_status dllm_op_kv8_load(const dllm_kv8* cache, void* k, void* v, int64_t k_row_stride, int64_t v_row_stride,
+                             int32_t dtype, int32_t R, const int32_t* starts, const int32_t* counts,
+                             void* cuda_stream);
+
+/* Attention over the 8-bit cache: for sequence s, row i, head h
+ *   out[s*R+i][h] = sum_t softmax_t(scale * q . K[s][g][t]) V[s][g][t],
+ * over t < limits[s*R+i], g = h / (H / H_kv) (grouped heads; H a multiple of
+ * H_kv).  q, out: bf16 [b*R][H][hd], 16-byte aligned, rows q_row_stride /
+ * out_row_stride elements apart (0: dense; else a multiple of 8).  limits:
+ * device int32 [b][R], the number of keys the row sees (values over T count
+ * as T); NULL: all T.  So lengths, causal, block-causal and padded batches are
+ * limits, and R = 1 is single-token decoding.  A row with limit <= 0 gives
+ * zeros.  What lies in the cache at or past every limit of its sequence is
+ * never used, whatever its bytes; a key or value row with scale byte 255
+ * turns the rows that see it into NaN and no others.  Scores, softmax
+ * statistics and sums are float32; probabilities enter the value product as
+ * bf16.  scale: finite, > 0.  workspace: device memory for the partial results of
+ * split keys, 16-byte aligned, at least dllm_op_attention_kv8_workspace
+ * bytes (0: may be NULL), contents irrelevant; calls that may run at the same
+ * time need one each. */
+dllm_status dllm_op_attention_kv8(const uint16_t* q, int64_t q_row_stride, const dllm_kv8* cache,
+                                  const int32_t* limits, float scale, uint16_t* out, int64_t out_row_stride,
+                                  int32_t H, int32_t R, void* workspace, int64_t workspace_bytes,
+                                  void* cuda_stream);
+dllm_status dllm_op_attention_kv8_workspace(int32_t b, int32_t H, int32_t H_kv, int32_t hd, int32_t R, int32_t T,
+                                            int64_t* bytes);
+
+/* Quantise rows in blocks of 128 along K (the last block of a row may be
+ * shorter): x [rows][K] of dtype, rows row_stride elements apart (0: dense), to
+ * codes [rows][K] (16-byte aligned) and scales [ceil(K/128)][rows].
+ * K % 16 == 0.  Weights and activations take the same form. */
+dllm_status dllm_op_quantise8(const void* x, int64_t row_stride, int32_t dtype, int32_t rows, int32_t K,
+                              uint8_t* codes, uint8_t* scales, void* cuda_stream);
+
+/* Y[N][M] = X[N][K] * W[M][K]^T of quantised operands: codes 16-byte aligned,
+ * row-major; scales as dllm_op_quantise8 lays them out, W_scale
+ * [ceil(K/128)][M], X_scale [ceil(K/128)][N].  K % 16 == 0.  Y is float32 or bf16
+ * (y_dtype), 16-byte aligned, rounded once from a float32 sum.  A block with scale byte 255
+ * makes its row of X (column of Y for W) NaN. */
+dllm_status dllm_op_gemm8(const uint8_t* W, const uint8_t* W_scale, const uint8_t* X, const uint8_t* X_scale, void* Y,
+                          int32_t y_dtype, int32_t M, int32_t N, int32_t K, void* cuda_stream);
+
 /* Cache staleness diagnostics for block block_idx of the current canvas (the
  * Fast-dLLM notes, section 14, Algorithm 4 steps 4-5: compare fresh and
  * cached representations and predictions at the positions about to be
