@@ -2447,6 +2447,14 @@ dllm_status op_cuda_fail(cudaError_t e, const char* what) {
 
 int op_device_sms() { return device_sms(); }
 
+cudaError_t op_smem_once(const void* kernel, int bytes) {
+  try {
+    return smem_attrs_once(kernel, bytes);
+  } catch (...) {   // the set of done kernels could not grow
+    return cudaErrorMemoryAllocation;
+  }
+}
+
 dllm_status op_map_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t planes,
                       uint64_t row_stride, uint64_t plane_stride, uint32_t box_inner, uint32_t box_rows) {
   EncodeTiledFn fn = encode_fn();
@@ -2582,23 +2590,28 @@ extern "C" dllm_status dllm_op_attention_noalloc(const uint16_t* q, const uint16
 extern "C" dllm_status dllm_op_check(int32_t* site, void* stream) {
   int dev = 0;
   CK(cudaGetDevice(&dev));
-  int words[2] = {0, 0};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  OpWorkspace* w = nullptr;
+  // error words: the library's workspace, the no-alloc scratch, the 8-bit kernels
+  int* word[3] = {};
+  int code_of[3] = {0, 0, 0};
   {
     std::lock_guard<std::mutex> lk(g_op_mu);
     auto it = g_op_ws.find(dev);
-    if (it != g_op_ws.end() && it->second.err) w = &it->second;
+    if (it != g_op_ws.end()) word[0] = it->second.err;
   }
   NoAllocScratch sc;
   CKS(noalloc_scratch(&sc));
-  if (w) CK(cudaMemcpyAsync(&words[0], w->err, 4, cudaMemcpyDeviceToHost, st));
-  CK(cudaMemcpyAsync(&words[1], sc.err, 4, cudaMemcpyDeviceToHost, st));
+  word[1] = sc.err;
+  CK(gemm8_err_word(&word[2]));
+  for (int i = 0; i < 3; ++i)
+    if (word[i]) CK(cudaMemcpyAsync(&code_of[i], word[i], 4, cudaMemcpyDeviceToHost, st));
   CK(cudaStreamSynchronize(st));
-  if (w) CK(cudaMemsetAsync(w->err, 0, 4, st));
-  CK(cudaMemsetAsync(sc.err, 0, 4, st));
+  for (int* w : word)
+    if (w) CK(cudaMemsetAsync(w, 0, 4, st));
   CK(cudaStreamSynchronize(st));
-  const int code = words[0] ? words[0] : words[1];
+  int code = 0;
+  for (int c : code_of)
+    if (code == 0) code = c;
   if (site) *site = code;
   if (code != 0) {
     set_error("a kernel-level call gave up a bounded wait (site %d)", code);

@@ -1,7 +1,9 @@
 // 8-bit matrix product with a scale for each block of 128 along K, and the
 // quantiser of its operands (see q8.cuh):
 //   Y[n][m] = sum_B 2^(ex[B][n] + ew[B][m]) * sum_{k in block B} X[n][k] W[m][k]
+#include "gemm.cuh"
 #include "ops8.h"
+#include "ptx8.cuh"
 #include "q8.cuh"
 
 namespace dllm {
@@ -44,45 +46,223 @@ __global__ void __launch_bounds__(256) quantise8_kernel(const void* x_, long lon
 
 // ---------------------------------------------------------------- product
 struct Gemm8Params {
-  const uint8_t *w, *ws, *x, *xs;
+  const uint8_t *ws, *xs;
   void* y;
-  int M, N, K, kb, out_bf16;
+  int M, N, K, kb, n_tiles, split, out_bf16;
 };
 
-// One 16 x 16 tile of Y a block, a block of 128 along K at a time.
-__global__ void __launch_bounds__(256) gemm8_tile_kernel(const __grid_constant__ Gemm8Params p) {
-  __shared__ float sw[16][kQBlock + 1], sx[16][kQBlock + 1];
-  const int m0 = blockIdx.x * 16, n0 = blockIdx.y * 16;
-  const int tm = threadIdx.x & 15, tn = threadIdx.x >> 4;
-  float acc = 0.0f;
-  for (int B = 0; B < p.kb; ++B) {
-    __syncthreads();
-    for (int e = threadIdx.x; e < 16 * 64; e += 256) {
-      const int r = e >> 6, c = (e & 63) * 2, k = B * kQBlock + c;
-      float2 w = make_float2(0.f, 0.f), x = w;
-      if (k < p.K && m0 + r < p.M)
-        w = f16x2_to_f32(cvt_f16x2_e4m3x2(*reinterpret_cast<const uint16_t*>(p.w + (long long)(m0 + r) * p.K + k)));
-      if (k < p.K && n0 + r < p.N)
-        x = f16x2_to_f32(cvt_f16x2_e4m3x2(*reinterpret_cast<const uint16_t*>(p.x + (long long)(n0 + r) * p.K + k)));
-      sw[r][c] = w.x;
-      sw[r][c + 1] = w.y;
-      sx[r][c] = x.x;
-      sx[r][c + 1] = x.y;
+// Set by a kernel that gave up a bounded wait; read by dllm_op_check.
+static __device__ int g_gemm8_err[1];
+
+template <int BN>
+struct Gemm8Cfg {
+  static constexpr int A_BYTES = 128 * kQBlock;
+  static constexpr int B_BYTES = BN * kQBlock;
+  static constexpr int SFB_ATOMS = (BN + 127) / 128;
+  static constexpr int SF_BYTES = 512 * (1 + SFB_ATOMS);
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SF_BYTES;
+  static constexpr int STAGES = BN == 32 ? 5 : BN == 64 ? 4 : 3;   // two CTAs an SM
+  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + (2 * STAGES + 1) * 8 + 16;
+  static constexpr int SF_COL = BN;                       // scale columns behind the accumulator
+  static constexpr int SF_COLS = 4 * (1 + SFB_ATOMS);     // a stage's
+  static constexpr int TMEM_COLS = BN + STAGES * SF_COLS <= 128 ? 128 : 256;
+  static_assert(BN + STAGES * SF_COLS <= TMEM_COLS, "tensor memory");
+  static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs an SM");
+  static_assert(STAGES * STAGE_BYTES >= BN * 128 * 4, "the ring holds the partial tile");
+};
+
+// Weights are the 128-row A operand, BN activation rows the B operand, both in
+// 128-byte swizzled TMA tiles of one scale block (128 codes) of K.  The
+// scales never meet the CUDA cores as numbers: UE8M0 bytes go to tensor
+// memory and the block-scaled tcgen05.mma applies them, so blocks accumulate
+// in one float32 accumulator.  A CTA computes a share of one tile's K; the
+// `split` CTAs of a cluster share a tile and join their partial tiles through
+// distributed shared memory in rank order.
+//   warp 0     TMA: weight and activation codes
+//   warp 1     one thread issues scale copies and MMAs
+//   warps 2-5  epilogue
+//   warp 6     scale bytes: one row's byte replicated over a 32-bit word, in the
+//              512-byte layout tcgen05.cp wants (row r at (r % 32) * 16 + (r / 32) * 4)
+template <int BN>
+__global__ void __launch_bounds__(224, 2)
+    gemm8_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                 const __grid_constant__ Gemm8Params p) {
+  using C = Gemm8Cfg<BN>;
+  constexpr int S = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + S * C::A_BYTES;
+  uint8_t* sF = sB + S * C::B_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sF + S * C::SF_BYTES);
+  uint64_t* empty = full + S;
+  uint64_t* done = empty + S;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* err = g_gemm8_err;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = p.split, rank = split > 1 ? (int)cluster_rank() : 0;
+  const int tile = (int)(blockIdx.x / (unsigned)split);
+  const int m0 = tile / p.n_tiles * 128, n0 = tile % p.n_tiles * BN;
+  const int c0 = (int)((long long)p.kb * rank / split), c1 = (int)((long long)p.kb * (rank + 1) / split);
+  const int nc = c1 - c0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 2);
+      mbar_init(&empty[s], 1);
     }
-    __syncthreads();
-    float d = 0.0f;
-    for (int k = 0; k < kQBlock; ++k) d += sw[tm][k] * sx[tn][k];
-    if (m0 + tm < p.M && n0 + tn < p.N)
-      acc += d * scale_value(p.ws[(long long)B * p.M + m0 + tm]) * scale_value(p.xs[(long long)B * p.N + n0 + tn]);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&tmW);
+    prefetch_tensormap(&tmX);
   }
-  if (m0 + tm < p.M && n0 + tn < p.N) {
-    const long long o = (long long)(n0 + tn) * p.M + m0 + tm;
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
+      RingPos r{0, 0u};
+      int issued = 0;
+      for (int i = 0; i < nc; ++i) {
+        if (i >= S && !mbar_wait(&empty[r.s], r.par ^ 1u, abort_flag, err, ERR_GEMM_EMPTY)) break;
+        mbar_arrive_expect_tx(&full[r.s], C::A_BYTES + C::B_BYTES);
+        tma_load_3d(sA + r.s * C::A_BYTES, &tmW, &full[r.s], (c0 + i) * kQBlock, m0, 0, pol_w);
+        tma_load_3d(sB + r.s * C::B_BYTES, &tmX, &full[r.s], (c0 + i) * kQBlock, n0, 0, pol_x);
+        r.next(S);
+        issued = i + 1;
+      }
+      if (*abort_flag)   // let copies in flight land before the CTA's shared memory goes away
+        for (int i = issued > S ? issued - S : 0; i < issued; ++i)
+          mbar_wait(&full[i % S], (uint32_t)(i / S) & 1u, nullptr, err, ERR_GEMM_DRAIN);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_mxf8(128, BN);
+      RingPos r{0, 0u};
+      for (int i = 0; i < nc; ++i) {
+        if (!mbar_wait(&full[r.s], r.par, abort_flag, err, ERR_GEMM_FULL)) break;
+        tc_fence_after();
+        const uint32_t a0 = smem_u32(sA + r.s * C::A_BYTES), b0 = smem_u32(sB + r.s * C::B_BYTES);
+        const uint32_t f0 = smem_u32(sF + r.s * C::SF_BYTES);
+        // a stage's scale columns are rewritten only once its MMAs are done (the empty barrier)
+        const uint32_t sfa = tmem + (uint32_t)(C::SF_COL + r.s * C::SF_COLS), sfb = sfa + 4;
+        tmem_cp_scales(sfa, sdesc_scales(f0));
+#pragma unroll
+        for (int t = 0; t < C::SFB_ATOMS; ++t) tmem_cp_scales(sfb + 4 * t, sdesc_scales(f0 + 512 * (t + 1)));
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_mxf8_ss(tmem, sdesc_sw128(a0 + kk * 32), sdesc_sw128(b0 + kk * 32), idesc, sfa, sfb,
+                      (i > 0 || kk > 0) ? 1u : 0u);
+        mma_commit(&empty[r.s]);
+        r.next(S);
+      }
+      mma_commit(done);
+    }
+  } else if (warp == 6) {
+    RingPos r{0, 0u};
+    for (int i = 0; i < nc; ++i) {
+      const long long B = c0 + i;
+      uint32_t wa[4], wb[4 * C::SFB_ATOMS];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int m = m0 + lane + 32 * j;
+        wa[j] = m < p.M ? __ldg(p.ws + B * p.M + m) : 127u;
+      }
+#pragma unroll
+      for (int j = 0; j < 4 * C::SFB_ATOMS; ++j) {
+        const int n = n0 + lane + 32 * j;
+        wb[j] = 32 * j < BN && n < p.N ? __ldg(p.xs + B * p.N + n) : 127u;
+      }
+      if (i >= S && !__all_sync(0xffffffffu, mbar_wait(&empty[r.s], r.par ^ 1u, abort_flag, err, ERR_GEMM_EMPTY))) break;
+      uint4* f = reinterpret_cast<uint4*>(sF + r.s * C::SF_BYTES) + lane;
+      constexpr uint32_t rep = 0x01010101u;
+      f[0] = make_uint4(wa[0] * rep, wa[1] * rep, wa[2] * rep, wa[3] * rep);
+#pragma unroll
+      for (int t = 0; t < C::SFB_ATOMS; ++t)
+        f[32 * (t + 1)] = make_uint4(wb[4 * t] * rep, wb[4 * t + 1] * rep, wb[4 * t + 2] * rep, wb[4 * t + 3] * rep);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[r.s]);
+      r.next(S);
+    }
+  }
+  __syncwarp();
+
+  // epilogue: thread = weight row, columns = activation rows
+  const int q = warp & 3, l128 = q * 32 + lane, m = m0 + l128;
+  const bool epi = warp >= 2 && warp < 6;
+  const int cols = min(BN, p.N - n0);
+  auto put = [&](int n, float v) {
+    const long long o = (long long)(n0 + n) * p.M + m;
     if (p.out_bf16)
-      static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(acc);
+      static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(v);
     else
-      static_cast<float*>(p.y)[o] = acc;
+      static_cast<float*>(p.y)[o] = v;
+  };
+  if (epi) {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(done, 0u, abort_flag, err, ERR_GEMM_TFULL));
+    (void)ok;   // after a wait that gave up the outputs are invalid and reported as such
+    tc_fence_after();
+  }
+  if (split == 1) {
+    if (epi) {
+      for (int n = 0; n < cols; n += 32) {
+        float v[32];
+        tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + n, v);
+        if (m < p.M) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (n + j < cols) put(n + j, v[j]);
+        }
+      }
+    }
+  } else {
+    // every CTA's MMAs and copies are done: the rings hold partial tiles now.
+    // Rank r owns the columns r, r + split, ... and gets each from every rank.
+    float* part = reinterpret_cast<float*>(smem);        // [source rank][owned column][128]
+    const int own = (BN + split - 1) / split;
+    const uint32_t base = smem_u32(part) + 4u * (uint32_t)(rank * own * 128 + l128);
+    cluster_sync();
+    if (epi) {
+      for (int n = 0; n < cols; n += 32) {
+        float v[32];
+        tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + n, v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (n + j < cols)
+            cluster_store(cluster_addr(base + 4u * (uint32_t)((n + j) / split * 128), (uint32_t)((n + j) % split)), v[j]);
+      }
+    }
+    cluster_sync();
+    if (epi && m < p.M) {
+      for (int i = 0; i * split + rank < cols; ++i) {
+        float v = 0.0f;
+        for (int s = 0; s < split; ++s) v += part[(s * own + i) * 128 + l128];
+        put(i * split + rank, v);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
+
+cudaError_t gemm8_err_word(int** p) { return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_gemm8_err); }
 
 namespace {
 
@@ -95,6 +275,15 @@ cudaError_t launch_quantise8(const void* x, long long rs, int rows, int K, uint8
   else
     quantise8_kernel<E, false><<<grid, 256, 0, st>>>(x, rs, rows, K, kb, codes, scales);
   return cudaGetLastError();
+}
+
+template <int BN>
+cudaError_t launch_gemm8(const CUtensorMap& tw, const CUtensorMap& tx, const Gemm8Params& p, unsigned grid,
+                         cudaStream_t st) {
+  using C = Gemm8Cfg<BN>;
+  const cudaError_t e = op_smem_once(reinterpret_cast<const void*>(gemm8_kernel<BN>), C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  return op_launch(gemm8_kernel<BN>, dim3(grid), dim3(224), C::SMEM_BYTES, st, p.split, tw, tx, p);
 }
 
 }  // namespace
@@ -132,10 +321,33 @@ extern "C" dllm_status dllm_op_gemm8(const uint8_t* W, const uint8_t* W_scale, c
                    "bad gemm8 arguments: M=%d N=%d K=%d (K %% 16 == 0) y_dtype=%d (float32 or bf16), W, X and Y "
                    "16-byte aligned",
                    M, N, K, y_dtype);
-  if ((N + 15) / 16 > 65535) return op_fail(DLLM_EINVAL, "gemm8: N=%d is too large", N);
-  Gemm8Params p = {W, W_scale, X, X_scale, Y, M, N, K, (K + kQBlock - 1) / kQBlock, y_dtype == DLLM_BF16};
-  gemm8_tile_kernel<<<dim3((unsigned)((M + 15) / 16), (unsigned)((N + 15) / 16)), 256, 0,
-                      static_cast<cudaStream_t>(stream)>>>(p);
-  OP_CK(cudaGetLastError());
+  Gemm8Params p = {};
+  p.ws = W_scale;
+  p.xs = X_scale;
+  p.y = Y;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.kb = (K + kQBlock - 1) / kQBlock;
+  p.out_bf16 = y_dtype == DLLM_BF16;
+  const int bn = N <= 32 ? 32 : N <= 64 ? 64 : 128;
+  p.n_tiles = (N + bn - 1) / bn;
+  const long long tiles = (long long)((M + 127LL) / 128) * p.n_tiles;
+  // Split a tile's K over a cluster while all CTAs fit on the GPU at once, two
+  // an SM: bound by HBM they then share its bandwidth evenly and finish
+  // together.  Each keeps at least two blocks of K.
+  p.split = 1;
+  while (p.split < 8 && tiles * p.split * 2 <= 2LL * op_device_sms() && p.kb >= 4 * p.split) p.split *= 2;
+  if (tiles * p.split > 0x7fffffffLL) return op_fail(DLLM_EINVAL, "gemm8: M=%d N=%d are too large", M, N);
+  CUtensorMap tw, tx;
+  if (const dllm_status s = op_map_u8(&tw, W, K, M, 1, K, (uint64_t)K * M, 128, 128); s != DLLM_OK) return s;
+  if (const dllm_status s = op_map_u8(&tx, X, K, N, 1, K, (uint64_t)K * N, 128, bn); s != DLLM_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const unsigned grid = (unsigned)(tiles * p.split);
+  switch (bn) {
+    case 32: OP_CK(launch_gemm8<32>(tw, tx, p, grid, st)); break;
+    case 64: OP_CK(launch_gemm8<64>(tw, tx, p, grid, st)); break;
+    default: OP_CK(launch_gemm8<128>(tw, tx, p, grid, st)); break;
+  }
   return DLLM_OK;
 }

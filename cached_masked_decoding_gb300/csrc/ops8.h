@@ -23,6 +23,36 @@ int op_device_sms();
 dllm_status op_map_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint64_t planes,
                       uint64_t row_stride, uint64_t plane_stride, uint32_t box_inner, uint32_t box_rows);
 
+// Allow a kernel `bytes` of dynamic shared memory on the current device, once.
+cudaError_t op_smem_once(const void* kernel, int bytes);
+
+// Error words of the kernels with bounded waits (device addresses).
+cudaError_t gemm8_err_word(int** p);
+
+// Launch with programmatic dependent launch: the kernel's prologue overlaps the
+// end of the kernel before it in the stream, and griddepcontrol.wait in the
+// kernel orders everything that touches global memory behind that kernel.
+// cluster > 1: that many consecutive CTAs form a cluster.
+template <typename Kern, typename... Args>
+inline cudaError_t op_launch(Kern kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t st, int cluster,
+                             const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 inline bool op_aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline int op_dtype_size(int32_t t) { return t == DLLM_F32 ? 4 : (t == DLLM_BF16 || t == DLLM_F16) ? 2 : 0; }
 
