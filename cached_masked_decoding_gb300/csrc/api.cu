@@ -2592,8 +2592,8 @@ extern "C" dllm_status dllm_op_check(int32_t* site, void* stream) {
   CK(cudaGetDevice(&dev));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // error words: the library's workspace, the no-alloc scratch, the 8-bit kernels
-  int* word[3] = {};
-  int code_of[3] = {0, 0, 0};
+  int* word[4] = {};
+  int code_of[4] = {};
   {
     std::lock_guard<std::mutex> lk(g_op_mu);
     auto it = g_op_ws.find(dev);
@@ -2603,7 +2603,8 @@ extern "C" dllm_status dllm_op_check(int32_t* site, void* stream) {
   CKS(noalloc_scratch(&sc));
   word[1] = sc.err;
   CK(gemm8_err_word(&word[2]));
-  for (int i = 0; i < 3; ++i)
+  CK(attn_kv8_err_word(&word[3]));
+  for (int i = 0; i < 4; ++i)
     if (word[i]) CK(cudaMemcpyAsync(&code_of[i], word[i], 4, cudaMemcpyDeviceToHost, st));
   CK(cudaStreamSynchronize(st));
   for (int* w : word)

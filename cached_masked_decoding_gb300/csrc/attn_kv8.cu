@@ -2,71 +2,63 @@
 //   out[s, i, h] = sum_t p_t V[s, g, t],  p = softmax over t < limit[s, i] of
 //   scale * q[s, i, h] . K[s, g, t],      g = h / (H / H_kv)
 // K = k * 2^ek and V = v * 2^ev with one exponent a row.  A row whose limit is
-// 0 or less sees nothing and gives zeros.
-//
-// One warp per (sequence, row, head) walks its keys with a running maximum and
-// sum; the scores, statistics and output are 32-bit.
+// 0 or less sees nothing and gives zeros.  The kernels are in attn_kv8_rows.cuh;
+// here is which runs, and on what.
+#include <algorithm>
 #include <cmath>
 
-#include "ops8.h"
-#include "q8.cuh"
+#include "attn_kv8_rows.cuh"
 
 namespace dllm {
 
 dllm_status kv8_check(const dllm_kv8* c, const char* who);
 
-struct AttnKv8Params {
-  dllm_kv8 c;
-  const uint16_t* q;
-  uint16_t* out;
-  const int32_t* limits;
-  long long q_rs, o_rs;
-  int H, R, group;
-  float scale_log2;
+cudaError_t attn_kv8_err_word(int** p) { return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_attn_kv8_err); }
+
+namespace {
+
+struct AttnKv8Plan {
+  int N, row_tiles, splits;
+  long long items;
+  size_t ws_bytes;
 };
 
-template <int HD>
-__global__ void __launch_bounds__(128) attn_kv8_row_kernel(const __grid_constant__ AttnKv8Params p) {
-  constexpr int D = HD / 32;
-  const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int h = (int)(item % p.H);
-  const long long row = item / p.H;
-  if (row >= (long long)p.c.b * p.R) return;
-  const int s = (int)(row / p.R);
-  const int lim = p.limits ? min(p.limits[row], p.c.T) : p.c.T;
-  const long long plane = ((long long)s * p.c.H_kv + h / p.group) * p.c.T;
-  float q[D], o[D] = {};
-  for (int d = 0; d < D; ++d)
-    q[d] = __uint_as_float((uint32_t)p.q[row * p.q_rs + (long long)h * HD + lane * D + d] << 16) * p.scale_log2;
-  float m = -INFINITY, l = 0.0f;
-  for (int t = 0; t < lim; ++t) {
-    const uint8_t* kr = p.c.k + (plane + t) * HD + lane * D;
-    const uint8_t* vr = p.c.v + (plane + t) * HD + lane * D;
-    const float ks = scale_value(p.c.k_scale[plane + t]), vs = scale_value(p.c.v_scale[plane + t]);
-    float z = 0.0f, v[D];
-    for (int d = 0; d < D; d += 2) {
-      const float2 kf = f16x2_to_f32(cvt_f16x2_e4m3x2((uint16_t)(kr[d] | (kr[d + 1] << 8))));
-      const float2 vf = f16x2_to_f32(cvt_f16x2_e4m3x2((uint16_t)(vr[d] | (vr[d + 1] << 8))));
-      z += q[d] * kf.x + q[d + 1] * kf.y;
-      v[d] = vf.x * vs;
-      v[d + 1] = vf.y * vs;
-    }
-    for (int w = 16; w >= 1; w >>= 1) z += __shfl_xor_sync(0xffffffffu, z, w);
-    z *= ks;
-    const float mn = z > m ? z : m;
-    const float corr = exp2f(m - mn), e = exp2f(z - mn);
-    l = l * corr + e;
-    for (int d = 0; d < D; ++d) o[d] = o[d] * corr + e * v[d];
-    m = mn;
-  }
-  const float il = lim > 0 ? 1.0f / l : 0.0f;
-  for (int d = 0; d < D; ++d) {
-    const __nv_bfloat16 r = __float2bfloat16_rn(o[d] * il);
-    p.out[row * p.o_rs + (long long)h * HD + lane * D + d] = *reinterpret_cast<const uint16_t*>(&r);
-  }
+// Rows of one cached head (R rows of H / H_kv heads) in tiles of N; the keys in
+// splits while the CTAs fit on the GPU at once, two an SM, each with at least
+// one tile of 128 keys.
+AttnKv8Plan plan_attn_kv8(long long b, long long H_kv, long long rows, int hd, int T) {
+  AttnKv8Plan a;
+  a.N = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  a.row_tiles = (int)((rows + a.N - 1) / a.N);
+  a.items = b * H_kv * a.row_tiles;
+  const long long tiles = (T + 127LL) / 128;
+  a.splits = (int)std::max(1LL, std::min({tiles, 2LL * op_device_sms() / a.items, 64LL}));
+  a.ws_bytes = a.splits > 1 ? (size_t)a.items * a.splits * a.N * (hd + 2) * 4 : 0;
+  return a;
 }
 
+template <int HD, int N>
+cudaError_t launch_attn_rows(const CUtensorMap& tk, const CUtensorMap& tv, const AttnKv8Params& p, unsigned grid,
+                             cudaStream_t st) {
+  using C = AttnRowsCfg<HD, N>;
+  const cudaError_t e = op_smem_once(reinterpret_cast<const void*>(attn_kv8_rows_kernel<HD, N>), C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  return op_launch(attn_kv8_rows_kernel<HD, N>, dim3(grid), dim3(192), C::SMEM_BYTES, st, 1, tk, tv, p);
+}
+
+template <int HD>
+cudaError_t launch_attn(const CUtensorMap& tk, const CUtensorMap& tv, const AttnKv8Params& p, const AttnKv8Plan& a,
+                        cudaStream_t st) {
+  const unsigned grid = (unsigned)(a.items * a.splits);
+  cudaError_t e = a.N == 16   ? launch_attn_rows<HD, 16>(tk, tv, p, grid, st)
+                  : a.N == 32 ? launch_attn_rows<HD, 32>(tk, tv, p, grid, st)
+                              : launch_attn_rows<HD, 64>(tk, tv, p, grid, st);
+  if (e != cudaSuccess || a.splits == 1) return e;
+  const long long rows = (long long)p.c.b * p.R * p.H;
+  return op_launch(attn_kv8_join_kernel<HD>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, 1, p, a.N);
+}
+
+}  // namespace
 }  // namespace dllm
 
 using namespace dllm;
@@ -75,7 +67,10 @@ extern "C" dllm_status dllm_op_attention_kv8_workspace(int32_t b, int32_t H, int
                                                        int32_t T, int64_t* bytes) {
   if (!bytes || b < 1 || H < 1 || H_kv < 1 || H % H_kv || (hd != 64 && hd != 128) || R < 1 || T < 1)
     return op_fail(DLLM_EINVAL, "bad attention shape: b=%d H=%d H_kv=%d hd=%d R=%d T=%d", b, H, H_kv, hd, R, T);
-  *bytes = 0;
+  const long long rows = (long long)R * (H / H_kv);
+  if (rows > (1LL << 30) || (__int128)b * R * H > (1LL << 31))
+    return op_fail(DLLM_EINVAL, "attention_kv8: b=%d R=%d H=%d are too many rows", b, R, H);
+  *bytes = (int64_t)plan_attn_kv8(b, H_kv, rows, hd, T).ws_bytes;
   return DLLM_OK;
 }
 
@@ -105,13 +100,28 @@ extern "C" dllm_status dllm_op_attention_kv8(const uint16_t* q, int64_t q_row_st
   p.R = R;
   p.group = H / cache->H_kv;
   p.scale_log2 = scale * 1.4426950408889634f;
-  const __int128 blocks = ((__int128)cache->b * R * H + 3) / 4;
-  if (blocks > 0x7fffffff) return op_fail(DLLM_EINVAL, "attention_kv8: b=%d R=%d H=%d are too many rows", cache->b, R, H);
+  int64_t need = 0;
+  if (const dllm_status s = dllm_op_attention_kv8_workspace(cache->b, H, cache->H_kv, cache->hd, R, cache->T, &need);
+      s != DLLM_OK)
+    return s;
+  if (need > 0 && (!workspace || workspace_bytes < need || !op_aligned(workspace, 16)))
+    return op_fail(DLLM_EINVAL, "attention_kv8: a 16-byte aligned workspace of %lld bytes is needed, got %lld",
+                   (long long)need, workspace ? (long long)workspace_bytes : 0LL);
+  p.rows = R * p.group;
+  const AttnKv8Plan a = plan_attn_kv8(cache->b, cache->H_kv, p.rows, cache->hd, cache->T);
+  p.row_tiles = a.row_tiles;
+  p.splits = a.splits;
+  p.ws_o = static_cast<float*>(workspace);
+  p.ws_ml = p.ws_o + (a.splits > 1 ? a.items * a.splits * a.N * cache->hd : 0);
+  const uint64_t planes = (uint64_t)cache->b * cache->H_kv, plane = (uint64_t)cache->T * cache->hd;
+  CUtensorMap tk, tv;
+  if (const dllm_status s = op_map_u8(&tk, cache->k, cache->hd, cache->T, planes, cache->hd, plane, cache->hd, 128);
+      s != DLLM_OK)
+    return s;
+  if (const dllm_status s = op_map_u8(&tv, cache->v, cache->hd, cache->T, planes, cache->hd, plane, cache->hd, 128);
+      s != DLLM_OK)
+    return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (cache->hd == 64)
-    attn_kv8_row_kernel<64><<<(unsigned)blocks, 128, 0, st>>>(p);
-  else
-    attn_kv8_row_kernel<128><<<(unsigned)blocks, 128, 0, st>>>(p);
-  OP_CK(cudaGetLastError());
+  OP_CK(cache->hd == 64 ? launch_attn<64>(tk, tv, p, a, st) : launch_attn<128>(tk, tv, p, a, st));
   return DLLM_OK;
 }

@@ -1,0 +1,582 @@
+// Attention over the 8-bit cache for few query rows a cached head (a token, a
+// block, grouped heads): the codes go from HBM to the tensor cores untouched.
+//
+// Keys are the 128-row operand.  A tile of 128 keys gives
+//   S^T[key][row] = K Q^T          (kind::f8f6f4, e4m3 x e4m3)
+//   O^T[dim][row] += V^T P^T       (kind::mxf8f6f4, V read MN-major from its TMA tile)
+// with N = 16, 32 or 64 rows as the narrow operand, so the products cost N / 128
+// of a 128-row tile's and the kernel is bound by the codes it reads: 2 (hd + 1)
+// bytes a key and cached head.
+//
+// 8 bits lose nothing on the query side: a bf16 q scaled by a power of two to at
+// most 448 is hi + lo of two e4m3 codes (8 significant bits are 4 + 4; below
+// 2^-10 of the row's largest element an error of 2^-18 of that element), two
+// products into one accumulator.  A probability is hi + lo as well, each with
+// the block scale that the MMA applies to the 32 keys of a warp, so a loud key
+// elsewhere does not push the others under e4m3's range.  Its error is 2^-8 of
+// itself (a bf16 rounding), or 2^-21 of the block's largest where that is more:
+// scaled into [128, 256), hi leaves at most 2^-4 of a value (2^-10 below 2^-6),
+// and lo, 2^4 finer, is off by 2^-4 of that or by 2^-14.
+// The value scale 2^ev of a key is folded into its probability.
+//
+// Softmax runs with one key a thread and all rows in its registers: nothing is
+// reduced across threads per tile but the 32-key maximum of each row (one
+// redux).  Rows share a reference maximum that moves only when a score exceeds
+// it by 2^40 (float32 sums and block scales have the range); sums l are kept
+// per key lane and joined once at the end.
+//
+//   warp 0     TMA: K and V tiles through a ring of 128-key slots
+//   warp 1     one thread issues scale copies and MMAs
+//   warps 2-5  softmax, one key a thread; the query tile before, the output after
+// Keys are split over CTAs when there are few (sequence, head) items; every
+// split leaves its normalised output and (m, l), and a second small kernel joins them.
+#pragma once
+
+#include "gemm.cuh"
+#include "ops8.h"
+#include "ptx8.cuh"
+#include "q8.cuh"
+
+namespace dllm {
+
+struct AttnKv8Params {
+  dllm_kv8 c;
+  const uint16_t* q;
+  uint16_t* out;
+  const int32_t* limits;
+  long long q_rs, o_rs;
+  int H, R, group;        // group = H / H_kv query heads share a cached head
+  int rows, row_tiles;    // R * group rows of an item, in tiles of N
+  int splits;
+  float scale_log2;
+  float *ws_o, *ws_ml;    // [item][split][N][hd] and [item][split][N][2]
+};
+
+static __device__ int g_attn_kv8_err[1];
+
+template <int HD, int N>
+struct AttnRowsCfg {
+  static constexpr int KT = 128;
+  static constexpr int SLOT = KT * HD;                  // one K or V tile
+  static constexpr int Q_BYTES = N * HD;                // hi or lo
+  static constexpr int P_ROW = 2 * N;                   // a key's hi codes, then its lo codes
+  static constexpr int P_BYTES = KT * P_ROW;
+  static constexpr int SLOTS = HD == 64 ? 8 : N == 16 ? 6 : N == 32 ? 5 : 4;
+  static constexpr int P_BUFS = N == 64 ? 1 : 2;
+  static constexpr int S_BUFS = N == 64 ? 1 : 2;
+  static constexpr int SF_BYTES = 512;
+  static constexpr int STAT_FLOATS = 4 * N + 4 + 3 * N;  // warp maxima, warp value exponents, m, qf, limits
+  static constexpr int SMEM_BYTES = 1024 + SLOTS * SLOT + 2 * Q_BYTES + P_BUFS * P_BYTES + (P_BUFS + 1) * SF_BYTES +
+                                    STAT_FLOATS * 4 + (2 * SLOTS + 10) * 8 + 16;
+  static constexpr int S_COL = 0;
+  static constexpr int O_COL = S_BUFS * N;              // 2 N columns: hi and lo products
+  static constexpr int SFA_COL = O_COL + 2 * N;
+  static constexpr int SFB_COL = SFA_COL + 4;
+  static constexpr int TMEM_COLS = SFB_COL + 4 * P_BUFS <= 128 ? 128 : 256;
+  static_assert(SFB_COL + 4 * P_BUFS <= TMEM_COLS, "tensor memory");
+  static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs an SM");
+};
+
+// Order-preserving map of a float's bits to a signed integer (NaN above +inf).
+__device__ __forceinline__ int float_order(float x) {
+  const int b = __float_as_int(x);
+  return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float order_float(int o) { return __int_as_float(o ^ ((o >> 31) & 0x7fffffff)); }
+
+// 2^x; results below the normal range are 0
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+constexpr float kRefSlack = 40.0f;   // log2 a score or a value scale may exceed its reference by
+
+template <int HD, int N>
+__global__ void __launch_bounds__(192, 2)
+    attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                         const __grid_constant__ AttnKv8Params p) {
+  using C = AttnRowsCfg<HD, N>;
+  constexpr int KT = C::KT;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sKV = smem;
+  uint8_t* sQ = sKV + C::SLOTS * C::SLOT;               // hi, lo
+  uint8_t* sP = sQ + 2 * C::Q_BYTES;
+  uint8_t* sSF = sP + C::P_BUFS * C::P_BYTES;           // ones, then a probability scale atom a P buffer
+  float* s_wmax = reinterpret_cast<float*>(sSF + (C::P_BUFS + 1) * C::SF_BYTES);   // [4][N]
+  int* s_wev = reinterpret_cast<int*>(s_wmax + 4 * N);                             // [4]
+  float* s_m = reinterpret_cast<float*>(s_wev + 4);     // [N] reference maxima
+  float* s_qf = s_m + N;                                // [N] scale * log2 e * 2^eq
+  int* s_lim = reinterpret_cast<int*>(s_qf + N);        // [N]
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_lim + N);
+  uint64_t* empty = full + C::SLOTS;
+  uint64_t* qready = empty + C::SLOTS;
+  uint64_t* sfull = qready + 1;                         // [2]
+  uint64_t* sfree = sfull + 2;                          // [2]
+  uint64_t* pready = sfree + 2;                         // [2]  (one is unused with single buffers)
+  uint64_t* pvdone = pready + 2;                        // [2]  the product that read a P buffer is done
+  uint64_t* mdone = pvdone + 2;                         // every MMA is done (before tensor memory is freed)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdone + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* err = g_attn_kv8_err;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = (int)(blockIdx.x % (unsigned)p.splits);
+  const int item = (int)(blockIdx.x / (unsigned)p.splits);
+  const int rt = item % p.row_tiles, plane = item / p.row_tiles;      // plane = seq * H_kv + cached head
+  const int seq = plane / p.c.H_kv, g = plane % p.c.H_kv;
+  const int n_rows = min(N, p.rows - rt * N);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::SLOTS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(qready, 4);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sfull[s], 1);
+      mbar_init(&sfree[s], 4);
+      mbar_init(&pready[s], 4);
+      mbar_init(&pvdone[s], 1);
+    }
+    mbar_init(mdone, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  griddep_launch_dependents();
+  griddep_wait();
+  // limits of the tile's rows; rows past the last see what row 0 sees and are not stored
+  if (threadIdx.x < N) {
+    const int n = (int)threadIdx.x < n_rows ? (int)threadIdx.x : 0;
+    const int i = (rt * N + n) / p.group;
+    const int lim = p.limits ? p.limits[(long long)seq * p.R + i] : p.c.T;
+    s_lim[threadIdx.x] = min(max(lim, 0), p.c.T);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  int lim_max, lim_min;
+  {
+    int hi = s_lim[lane & (N - 1)], lo = hi;
+    if constexpr (N == 64) {
+      hi = max(hi, s_lim[lane + 32]);
+      lo = min(lo, s_lim[lane + 32]);
+    }
+    lim_max = __reduce_max_sync(0xffffffffu, hi);
+    lim_min = __reduce_min_sync(0xffffffffu, lo);
+  }
+  // this split's keys: whole tiles, shared out evenly over the keys some row sees
+  const int tiles = (lim_max + KT - 1) / KT;
+  const int t0 = (int)((long long)tiles * split / p.splits), t1 = (int)((long long)tiles * (split + 1) / p.splits);
+  const int nt = t1 - t0;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol = p.row_tiles > 1 ? policy_evict_last() : policy_evict_first();
+      RingPos r{0, 0u};
+      int issued = 0;
+      for (int u = 0; u < 2 * nt; ++u) {
+        if (u >= C::SLOTS && !mbar_wait(&empty[r.s], r.par ^ 1u, abort_flag, err, ERR_ATTN_FULL)) break;
+        mbar_arrive_expect_tx(&full[r.s], C::SLOT);
+        tma_load_3d(sKV + r.s * C::SLOT, (u & 1) ? &tmV : &tmK, &full[r.s], 0, (t0 + (u >> 1)) * KT, plane, pol);
+        r.next(C::SLOTS);
+        issued = u + 1;
+      }
+      if (*abort_flag)   // let copies in flight land before the CTA's shared memory goes away
+        for (int u = issued > C::SLOTS ? issued - C::SLOTS : 0; u < issued; ++u)
+          mbar_wait(&full[u % C::SLOTS], (uint32_t)(u / C::SLOTS) & 1u, nullptr, err, ERR_ATTN_FULL);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && nt > 0 && mbar_wait(qready, 0u, abort_flag, err, ERR_ATTN_FULL)) {
+      tc_fence_after();
+      constexpr uint32_t idesc_s = idesc_f8(128, N);
+      // V and P MN-major; P's scale byte kk belongs to keys 32 kk .. 32 kk + 31
+      constexpr uint32_t idesc_o = idesc_mxf8(128, 2 * N) | (1u << 15) | (1u << 16);
+      const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV), p0 = smem_u32(sP), f0 = smem_u32(sSF);
+      tmem_cp_scales(tmem + C::SFA_COL, sdesc_scales(f0));
+      int ns = 0, np = 0;
+      unsigned long long idle_since = 0;
+      uint32_t spins = 0;
+      while (np < nt) {
+        bool did = false;
+        if (np < ns) {
+          const int u = 2 * np + 1, slot = u % C::SLOTS, pb = C::P_BUFS == 2 ? np & 1 : 0;
+          const uint32_t pk = (uint32_t)(C::P_BUFS == 2 ? np >> 1 : np) & 1u;
+          if (mbar_test_wait(smem_u32(&pready[pb]), pk) &&
+              mbar_test_wait(smem_u32(&full[slot]), (uint32_t)(u / C::SLOTS) & 1u)) {
+            tc_fence_after();
+            const uint32_t v = kv0 + slot * C::SLOT, pp = p0 + pb * C::P_BYTES;
+            const uint32_t sfb = tmem + C::SFB_COL + 4 * pb;
+            tmem_cp_scales(sfb, sdesc_scales(f0 + (1 + pb) * C::SF_BYTES));
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              // a 64-wide head fills both halves of the 128 dims: the second repeats the first and is not read
+              mma_mxf8_ss(tmem + C::O_COL, sdesc_rows<HD>(v + kk * 32 * HD, 0),
+                          sdesc_rows<C::P_ROW>(pp + kk * 32 * C::P_ROW), idesc_o | ((uint32_t)kk << 4),
+                          tmem + C::SFA_COL, sfb, (np > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(&empty[slot]);
+            mma_commit(&pvdone[pb]);
+            ++np;
+            did = true;
+          }
+        }
+        if (ns < nt) {
+          const int u = 2 * ns, slot = u % C::SLOTS, sb = C::S_BUFS == 2 ? ns & 1 : 0;
+          const int use = C::S_BUFS == 2 ? ns >> 1 : ns;
+          if (mbar_test_wait(smem_u32(&full[slot]), (uint32_t)(u / C::SLOTS) & 1u) &&
+              (use == 0 || mbar_test_wait(smem_u32(&sfree[sb]), (uint32_t)(use - 1) & 1u))) {
+            tc_fence_after();
+            const uint32_t k = kv0 + slot * C::SLOT, d = tmem + C::S_COL + sb * N;
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int kk = 0; kk < HD / 32; ++kk)
+                mma_f8_ss(d, sdesc_rows<HD>(k + kk * 32), sdesc_rows<HD>(q0 + part * C::Q_BYTES + kk * 32), idesc_s,
+                          (part > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(&empty[slot]);
+            mma_commit(&sfull[sb]);
+            ++ns;
+            did = true;
+          }
+        }
+        if (did) {
+          idle_since = 0;
+          spins = 0;
+        } else if ((++spins & 63u) == 0) {
+          const unsigned long long now = globaltimer();
+          if (idle_since == 0) {
+            idle_since = now;
+          } else if (*abort_flag || now - idle_since > kWaitLimitNs) {
+            if (!*abort_flag) record_error(err, ERR_ATTN_FULL);
+            *abort_flag = 1;
+            break;
+          }
+        }
+      }
+      mma_commit(mdone);
+      mbar_wait(mdone, 0u, nullptr, err, ERR_ATTN_FULL);
+    }
+  } else {
+    const int q4 = warp & 3, key_l = q4 * 32 + lane;      // this thread's key in a tile, and its tensor-memory lane
+    const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
+    const int tid = (warp - 2) * 32 + lane;
+    // product t of P V is done
+    auto pv_wait = [&](int t) {
+      const int pb = C::P_BUFS == 2 ? t & 1 : 0;
+      return __all_sync(0xffffffffu, mbar_wait(&pvdone[pb], (uint32_t)(C::P_BUFS == 2 ? t >> 1 : t) & 1u, abort_flag, err,
+                                               ERR_ATTN_FULL)) != 0;
+    };
+    if (nt > 0) {
+      // ---------------------------------------------------- the query tile
+      constexpr int L = HD / 8;                           // lanes of a row
+      for (int n = tid / L; n < N; n += 128 / L) {
+        const int l = tid % L;
+        float x[8] = {};
+        if (n < n_rows) {
+          const int rn = rt * N + n, i = rn / p.group, h = g * p.group + rn % p.group;
+          ElemBf16::load8(reinterpret_cast<const __nv_bfloat16*>(p.q) + ((long long)seq * p.R + i) * p.q_rs +
+                              (long long)h * HD + l * 8,
+                          x);
+        }
+        uint32_t m = abs_bits8(x);
+#pragma unroll
+        for (int d = L / 2; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const int byte = scale_byte(m);
+        const float inv = byte == kScaleNan ? __uint_as_float(0x7fffffffu) : scale_inverse(byte);
+        float r[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[e] = x[e] * inv;    // a row that is not finite becomes NaN
+        const uint2 hi = encode8(r, 1.0f);
+        float b[8];
+        decode8(hi, 1.0f, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) b[e] = r[e] - b[e];
+        const uint2 lo = encode8(b, 1.0f);
+        const uint32_t off = swizzled<HD>(n, l >> 1) + (uint32_t)(l & 1) * 8;
+        *reinterpret_cast<uint2*>(sQ + off) = hi;
+        *reinterpret_cast<uint2*>(sQ + C::Q_BYTES + off) = lo;
+        if (l == 0) s_qf[n] = byte == kScaleNan ? 1.0f : p.scale_log2 * scale_value(byte);
+      }
+      reinterpret_cast<uint32_t*>(sSF)[tid] = 0x7f7f7f7fu;
+#pragma unroll
+      for (int b = 0; b < C::P_BUFS; ++b) reinterpret_cast<uint32_t*>(sSF + (1 + b) * C::SF_BYTES)[tid] = 0x7f7f7f7fu;
+      if (tid < N) s_m[tid] = 0.0f;
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qready);
+      named_bar_sync(2, 128);
+    }
+    // ------------------------------------------------------ the keys
+    float l_sum[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) l_sum[n] = 0.0f;
+    int vref = 0;
+    // After a wait that gave up (ok false) the loop goes on without waiting, so
+    // that every warp meets every barrier; the outputs are invalid and reported.
+    bool ok = true;
+    const uint8_t* ksc = p.c.k_scale + (long long)plane * p.c.T;
+    const uint8_t* vsc = p.c.v_scale + (long long)plane * p.c.T;
+    int kb_next = 127, vb_next = 127;
+    if (nt > 0 && t0 * KT + key_l < lim_max) {
+      kb_next = ksc[t0 * KT + key_l];
+      vb_next = vsc[t0 * KT + key_l];
+    }
+    for (int t = 0; t < nt; ++t) {
+      const int sb = C::S_BUFS == 2 ? t & 1 : 0, pb = C::P_BUFS == 2 ? t & 1 : 0;
+      const int key = (t0 + t) * KT + key_l;
+      int kb = kb_next, vb = vb_next;
+      if (t + 1 < nt && key + KT < lim_max) {
+        kb_next = ksc[key + KT];
+        vb_next = vsc[key + KT];
+      }
+      const bool seen = key < lim_max;                    // by some row
+      if (!seen) kb = vb = 127;
+      const bool bad = kb == kScaleNan || vb == kScaleNan;
+      const float kf = bad ? __uint_as_float(0x7fffffffu) : scale_value(kb);
+      const int ev = bad || !seen ? -1000 : vb - 127;     // -1000: no value scale to refer to
+      if (!__all_sync(0xffffffffu, mbar_wait(&sfull[sb], (uint32_t)(C::S_BUFS == 2 ? t >> 1 : t) & 1u, abort_flag, err,
+                                             ERR_ATTN_FULL))) {
+        ok = false;
+      }
+      tc_fence_after();
+      // scores in base 2, relative to their row's reference
+      float z[N];
+      float top = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < N; n += 16) {
+        tmem_ld16(trow + C::S_COL + sb * N + n, z + n);
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(s_qf + n + j);
+          const float4 m = *reinterpret_cast<const float4*>(s_m + n + j);
+          z[n + j] = fmaf(z[n + j], kf * f.x, -m.x);
+          z[n + j + 1] = fmaf(z[n + j + 1], kf * f.y, -m.y);
+          z[n + j + 2] = fmaf(z[n + j + 2], kf * f.z, -m.z);
+          z[n + j + 3] = fmaf(z[n + j + 3], kf * f.w, -m.w);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sfree[sb]);
+      if ((t0 + t + 1) * KT > lim_min) {                  // some row does not see all of the tile
+#pragma unroll
+        for (int n = 0; n < N; ++n) z[n] = key < s_lim[n] ? z[n] : -INFINITY;
+      }
+#pragma unroll
+      for (int n = 0; n < N; ++n) top = fmaxf(top, z[n]);
+      bool need = t == 0 || ev - vref > (int)kRefSlack || top > kRefSlack;
+      if (!ok) need = false;
+      if (named_bar_or(2, 128, need)) {
+        // new references: the first tile's, or a score far above the last ones
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          const int wt = __reduce_max_sync(0xffffffffu, float_order(z[n]));
+          if (lane == (n & 31)) s_wmax[q4 * N + n] = order_float(wt);
+        }
+        const int evw = __reduce_max_sync(0xffffffffu, ev);
+        if (lane == 0) s_wev[q4] = evw;
+        named_bar_sync(2, 128);
+        const int ev_top = max(max(s_wev[0], s_wev[1]), max(s_wev[2], s_wev[3]));
+        const int vref_new = t == 0 ? max(ev_top, -127) : max(vref, ev_top);
+        float up = 0.0f;                                  // row tid's reference rises by this
+        if (tid < N) {
+          int tr = float_order(s_wmax[tid]);
+#pragma unroll
+          for (int k = 1; k < 4; ++k) tr = max(tr, float_order(s_wmax[k * N + tid]));
+          up = order_float(tr);
+          if (up == -INFINITY || (t > 0 && up < 0.0f)) up = 0.0f;
+        }
+        named_bar_sync(2, 128);
+        if (tid < N) {
+          s_m[tid] += up;
+          s_wmax[tid] = up;
+        }
+        named_bar_sync(2, 128);
+#pragma unroll
+        for (int n = 0; n < N; ++n) z[n] -= s_wmax[n];
+        if (t > 0) {
+          ok = ok && pv_wait(t - 1);
+          tc_fence_after();
+          // exponents below -126 leave nothing of the old sums that counts
+          const float vcorr = vref - vref_new < -126 ? 0.0f : scale_value(127 + vref - vref_new);
+#pragma unroll
+          for (int n = 0; n < N; ++n) l_sum[n] *= exp2f(-s_wmax[n]);
+#pragma unroll 1
+          for (int c = 0; c < 2 * N; c += 16) {
+            float o[16];
+            tmem_ld16(trow + C::O_COL + c, o);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] *= exp2f(-s_wmax[(c + j) & (N - 1)]) * vcorr;
+            tmem_st16(trow + C::O_COL + c, o);
+          }
+          tc_fence_before();
+        }
+        vref = vref_new;
+      }
+      // the P buffer is free once the product that last read it is done
+      if (t >= C::P_BUFS && ok) ok = pv_wait(t - C::P_BUFS);
+      const int dv = max(ev - vref, -126);
+      const float vf = bad || !seen ? 0.0f : __uint_as_float((uint32_t)(127 + dv) << 23);
+      uint8_t* prow = sP + pb * C::P_BYTES;
+      uint8_t* sf = sSF + (1 + pb) * C::SF_BYTES;
+#pragma unroll
+      for (int n = 0; n < N; n += 16) {
+        uint32_t hi[4], lo[4];
+        int byte_me = 127;
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          float x[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float pr = ex2(z[n + j + e]);
+            l_sum[n + j + e] += pr;
+            const float pv = pr * vf;
+            // the block's scale puts its largest probability into [128, 256)
+            const int exp = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(pv)) >> 23);
+            const int byte = min(max(exp - 7, 4), 247);
+            if (lane == n + j + e - (n & 32)) byte_me = byte;
+            x[e] = pv * __uint_as_float((uint32_t)(254 - byte) << 23);
+          }
+          // hi: the nearest code; lo: what it leaves, at most a 16th of it, in a scale 2^4 smaller
+          const uint32_t ch = cvt_e4m3x2(x[0], x[1]);
+          const float2 h = f16x2_to_f32(cvt_f16x2_e4m3x2((uint16_t)ch));
+          const uint32_t cl = cvt_e4m3x2((x[0] - h.x) * 16.0f, (x[1] - h.y) * 16.0f);
+          if (j & 2) {
+            hi[j >> 2] |= ch << 16;
+            lo[j >> 2] |= cl << 16;
+          } else {
+            hi[j >> 2] = ch;
+            lo[j >> 2] = cl;
+          }
+        }
+        *reinterpret_cast<uint4*>(prow + swizzled<C::P_ROW>(key_l, n >> 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(prow + swizzled<C::P_ROW>(key_l, (N + n) >> 4)) =
+            make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        if ((lane & 16) == (n & 16)) {
+          // lane holds row n + (lane & 15): its scale byte for this warp's keys, once for hi and once for lo
+          const int r = n + (lane & 15);
+          sf[(r & 31) * 16 + (r >> 5) * 4 + q4] = (uint8_t)byte_me;
+          sf[((r + N) & 31) * 16 + ((r + N) >> 5) * 4 + q4] = (uint8_t)(byte_me - 4);
+        }
+      }
+      if ((t0 + t + 1) * KT > lim_max) {
+        // the last tile runs past every row's limit: whatever bytes lie there
+        // (codes of NaN among them) must not meet the zero probabilities
+        const int u = 2 * t + 1, slot = u % C::SLOTS;
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (uint32_t)(u / C::SLOTS) & 1u, abort_flag, err, ERR_ATTN_FULL));
+        if (!seen) {
+#pragma unroll
+          for (int c = 0; c < HD / 16; ++c)
+            *reinterpret_cast<uint4*>(sKV + slot * C::SLOT + key_l * HD + c * 16) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      fence_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pready[pb]);
+    }
+    // ------------------------------------------------------ sums and output
+    if (nt > 0) {
+      if (ok) ok = pv_wait(nt - 1);
+      tc_fence_after();
+#pragma unroll
+      for (int n = 0; n < N; n += 16) {
+        // sum 16 columns over the warp: lane c (and c + 16) ends with column n + (c & 15)
+#pragma unroll
+        for (int s = 8; s >= 1; s >>= 1) {
+          const bool up = (lane & s) != 0;
+#pragma unroll
+          for (int i = 0; i < s; ++i) {
+            const float send = up ? l_sum[n + i] : l_sum[n + i + s];
+            const float keep = up ? l_sum[n + i + s] : l_sum[n + i];
+            l_sum[n + i] = keep + __shfl_xor_sync(0xffffffffu, send, s);
+          }
+        }
+        l_sum[n] += __shfl_xor_sync(0xffffffffu, l_sum[n], 16);
+        if (lane < 16) s_wmax[q4 * N + n + lane] = l_sum[n];
+      }
+      named_bar_sync(2, 128);
+    }
+    const int dim = key_l;
+    const float vs = scale_value(127 + vref);
+    const long long slot = (long long)item * p.splits + split;
+#pragma unroll 1
+    for (int n = 0; n < N; n += 16) {
+      float a[16] = {}, b[16] = {};
+      if (nt > 0) {
+        tmem_ld16(trow + C::O_COL + n, a);
+        tmem_ld16(trow + C::O_COL + N + n, b);
+      }
+      if (dim < HD) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int r = n + j;
+          if (r >= n_rows) break;
+          float l = 0.0f;
+          if (nt > 0) l = (s_wmax[r] + s_wmax[N + r]) + (s_wmax[2 * N + r] + s_wmax[3 * N + r]);
+          const float v = l == 0.0f ? 0.0f : (a[j] + b[j]) / l * vs;
+          if (p.splits > 1) {
+            p.ws_o[(slot * N + r) * HD + dim] = v;
+            if (dim < 2) p.ws_ml[(slot * N + r) * 2 + dim] = dim ? l : (nt > 0 ? s_m[r] : 0.0f);
+          } else {
+            const int rn = rt * N + r, i = rn / p.group, h = g * p.group + rn % p.group;
+            p.out[((long long)seq * p.R + i) * p.o_rs + (long long)h * HD + dim] = f32_to_bf16_bits(v);
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Join the splits of every row: weights l_s 2^(m_s - M) over their sum.  A warp a row.
+template <int HD>
+__global__ void __launch_bounds__(128) attn_kv8_join_kernel(const __grid_constant__ AttnKv8Params p, int N) {
+  const int lane = threadIdx.x & 31;
+  const long long idx = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int h = (int)(idx % p.H);
+  const long long row = idx / p.H;
+  griddep_launch_dependents();
+  griddep_wait();
+  if (row >= (long long)p.c.b * p.R) return;
+  const int seq = (int)(row / p.R), i = (int)(row % p.R), rn = i * p.group + h % p.group;
+  const long long item = ((long long)seq * p.c.H_kv + h / p.group) * p.row_tiles + rn / N;
+  const long long first = item * p.splits * N + rn % N;   // then N apart
+  constexpr int D = HD / 32;
+  float M = -INFINITY;
+  for (int s = 0; s < p.splits; ++s) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + (first + (long long)s * N) * 2);
+    if (ml.y != 0.0f) M = ml.x > M || ml.x != ml.x ? ml.x : M;   // a NaN stays
+  }
+  float sum = 0.0f, o[D] = {};
+  for (int s = 0; s < p.splits; ++s) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + (first + (long long)s * N) * 2);
+    if (ml.y == 0.0f) continue;                            // a split that saw none of the row's keys
+    const float w = ml.y * exp2f(ml.x - M);
+    sum += w;
+    const float* src = p.ws_o + (first + (long long)s * N) * HD + lane * D;
+#pragma unroll
+    for (int d = 0; d < D; ++d) o[d] += w * src[d];
+  }
+  const float il = sum == 0.0f ? 0.0f : 1.0f / sum;
+  uint16_t* out = p.out + row * p.o_rs + (long long)h * HD + lane * D;
+#pragma unroll
+  for (int d = 0; d < D; ++d) out[d] = f32_to_bf16_bits(o[d] * il);
+}
+
+}  // namespace dllm

@@ -28,6 +28,7 @@ cudaError_t op_smem_once(const void* kernel, int bytes);
 
 // Error words of the kernels with bounded waits (device addresses).
 cudaError_t gemm8_err_word(int** p);
+cudaError_t attn_kv8_err_word(int** p);
 
 // Launch with programmatic dependent launch: the kernel's prologue overlaps the
 // end of the kernel before it in the stream, and griddepcontrol.wait in the

@@ -561,8 +561,10 @@ dllm_status dllm_op_kv8_load(const dllm_kv8* cache, void* k, void* v, int64_t k_
  * zeros.  What lies in the cache at or past every limit of its sequence is
  * never used, whatever its bytes; a key or value row with scale byte 255
  * turns the rows that see it into NaN and no others.  Scores, softmax
- * statistics and sums are float32; probabilities enter the value product as
- * bf16.  scale: finite, > 0.  workspace: device memory for the partial results of
+ * statistics and sums are float32; a probability enters the value product
+ * with 8 significant bits (an error of 2^-8 of itself, or of 2^-21 of the
+ * largest p * 2^ev of its row among 32 neighbouring keys where that is more).
+ * scale: finite, > 0.  workspace: device memory for the partial results of
  * split keys, 16-byte aligned, at least dllm_op_attention_kv8_workspace
  * bytes (0: may be NULL), contents irrelevant; calls that may run at the same
  * time need one each. */

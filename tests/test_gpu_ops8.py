@@ -258,6 +258,14 @@ def test_cache_slots_past_32_bits(torch):
     same(codes[0][0, :, T - 3:].cpu().numpy(), kc.transpose(1, 0, 2))
     same(scales[0][0, :, T - 3:].cpu().numpy(), ks.T)
     assert int(codes[0][0, :, :4096].max()) == 0 and int(codes[0][0, 1, T - 4].max()) == 0
+    # and attention reads them there: a query of zeros weighs all keys alike, and the earlier values are zeros
+    q = torch.zeros(1, h, hd, device="cuda", dtype=torch.bfloat16)
+    out = torch.zeros_like(q)
+    n = binding.attention_kv8_workspace(b, h, h, hd, 1, T)
+    ws = torch.empty(max(n, 16), device="cuda", dtype=torch.uint8)
+    binding.op_attention_kv8(q.data_ptr(), c, out.data_ptr(), h, 1, ws_ptr=ws.data_ptr(), ws_bytes=n)
+    want = ref.dequantise(*ref.quantise(f64(v))).sum(axis=0) / T
+    np.testing.assert_allclose(f64(out)[0], want, rtol=2.0 ** -7, atol=0)
 
 
 # --------------------------------------------------------------------------- attention
@@ -463,10 +471,16 @@ def test_attention_strided_rows_and_workspace(torch):
     qw[:, :H * hd] = q.view(b * R, -1)
     ow = torch.full((b * R, H * hd + 40), 5.0, device="cuda", dtype=torch.bfloat16)
     n = binding.attention_kv8_workspace(b, H, h, hd, R, T)
-    ws = torch.empty(max(n, 16), device="cuda", dtype=torch.uint8)
+    assert n > 0                                        # few rows, many keys: the keys are split
+    ws = torch.empty(n, device="cuda", dtype=torch.uint8)
     binding.op_attention_kv8(qw.data_ptr(), ca.c, ow.data_ptr(), H, R, ws_ptr=ws.data_ptr(), ws_bytes=n,
                              q_row_stride=H * hd + 24, out_row_stride=H * hd + 40)
     assert torch.equal(ow[:, :H * hd].reshape(b, R, H, hd), dense) and (ow[:, H * hd:] == 5.0).all()
+    for bad in [dict(ws_ptr=0, ws_bytes=n), dict(ws_ptr=ws.data_ptr(), ws_bytes=n - 1),
+                dict(ws_ptr=ws.data_ptr() + 8, ws_bytes=n)]:
+        with pytest.raises(binding.DllmError) as e:
+            binding.op_attention_kv8(q.data_ptr(), ca.c, ow.data_ptr(), H, R, **bad)
+        assert e.value.status == binding.EINVAL and "workspace" in str(e.value)
 
 
 # --------------------------------------------------------------------------- product
