@@ -2,12 +2,13 @@
 //   out[s, i, h] = sum_t p_t V[s, g, t],  p = softmax over t < limit[s, i] of
 //   scale * q[s, i, h] . K[s, g, t],      g = h / (H / H_kv)
 // K = k * 2^ek and V = v * 2^ev with one exponent a row.  A row whose limit is
-// 0 or less sees nothing and gives zeros.  The kernels are in attn_kv8_rows.cuh;
+// 0 or less sees nothing and gives zeros.  The kernels are in attn_kv8_rows.cuh
+// (up to 64 rows a cached head) and attn_kv8_tiles.cuh (more);
 // here is which runs, and on what.
 #include <algorithm>
 #include <cmath>
 
-#include "attn_kv8_rows.cuh"
+#include "attn_kv8_tiles.cuh"
 
 namespace dllm {
 
@@ -24,15 +25,15 @@ struct AttnKv8Plan {
 };
 
 // Rows of one cached head (R rows of H / H_kv heads) in tiles of N; the keys in
-// splits while the CTAs fit on the GPU at once, two an SM, each with at least
-// one tile of 128 keys.
+// splits while the CTAs fit on the GPU at once (two an SM, one with 64 rows), each with at least
+// one tile of keys.
 AttnKv8Plan plan_attn_kv8(long long b, long long H_kv, long long rows, int hd, int T) {
   AttnKv8Plan a;
-  a.N = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  a.N = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
   a.row_tiles = (int)((rows + a.N - 1) / a.N);
   a.items = b * H_kv * a.row_tiles;
-  const long long tiles = (T + 127LL) / 128;
-  a.splits = (int)std::max(1LL, std::min({tiles, 2LL * op_device_sms() / a.items, 64LL}));
+  const long long kt = a.N == 128 ? 64 : 128, tiles = (T + kt - 1) / kt, ctas = (a.N == 64 ? 1 : 2) * op_device_sms();
+  a.splits = (int)std::max(1LL, std::min({tiles, ctas / a.items, 64LL}));
   a.ws_bytes = a.splits > 1 ? (size_t)a.items * a.splits * a.N * (hd + 2) * 4 : 0;
   return a;
 }
@@ -43,16 +44,27 @@ cudaError_t launch_attn_rows(const CUtensorMap& tk, const CUtensorMap& tv, const
   using C = AttnRowsCfg<HD, N>;
   const cudaError_t e = op_smem_once(reinterpret_cast<const void*>(attn_kv8_rows_kernel<HD, N>), C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  return op_launch(attn_kv8_rows_kernel<HD, N>, dim3(grid), dim3(192), C::SMEM_BYTES, st, 1, tk, tv, p);
+  return op_launch(attn_kv8_rows_kernel<HD, N>, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, st, 1, tk, tv, p);
+}
+
+template <int HD>
+cudaError_t launch_attn_tiles(const CUtensorMap& tk, const CUtensorMap& tv, const AttnKv8Params& p, unsigned grid,
+                              cudaStream_t st) {
+  using C = AttnTilesCfg<HD>;
+  const cudaError_t e = op_smem_once(reinterpret_cast<const void*>(attn_kv8_tiles_kernel<HD>), C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  return op_launch(attn_kv8_tiles_kernel<HD>, dim3(grid), dim3(224), C::SMEM_BYTES, st, 1, tk, tv, p);
 }
 
 template <int HD>
 cudaError_t launch_attn(const CUtensorMap& tk, const CUtensorMap& tv, const AttnKv8Params& p, const AttnKv8Plan& a,
                         cudaStream_t st) {
   const unsigned grid = (unsigned)(a.items * a.splits);
-  cudaError_t e = a.N == 16   ? launch_attn_rows<HD, 16>(tk, tv, p, grid, st)
+  cudaError_t e = a.N == 8    ? launch_attn_rows<HD, 8>(tk, tv, p, grid, st)
+                  : a.N == 16 ? launch_attn_rows<HD, 16>(tk, tv, p, grid, st)
                   : a.N == 32 ? launch_attn_rows<HD, 32>(tk, tv, p, grid, st)
-                              : launch_attn_rows<HD, 64>(tk, tv, p, grid, st);
+                  : a.N == 64 ? launch_attn_rows<HD, 64>(tk, tv, p, grid, st)
+                              : launch_attn_tiles<HD>(tk, tv, p, grid, st);
   if (e != cudaSuccess || a.splits == 1) return e;
   const long long rows = (long long)p.c.b * p.R * p.H;
   return op_launch(attn_kv8_join_kernel<HD>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, 1, p, a.N);
@@ -114,11 +126,12 @@ extern "C" dllm_status dllm_op_attention_kv8(const uint16_t* q, int64_t q_row_st
   p.ws_o = static_cast<float*>(workspace);
   p.ws_ml = p.ws_o + (a.splits > 1 ? a.items * a.splits * a.N * cache->hd : 0);
   const uint64_t planes = (uint64_t)cache->b * cache->H_kv, plane = (uint64_t)cache->T * cache->hd;
+  const uint32_t keys = a.N == 128 ? 64 : 128;            // of a tile
   CUtensorMap tk, tv;
-  if (const dllm_status s = op_map_u8(&tk, cache->k, cache->hd, cache->T, planes, cache->hd, plane, cache->hd, 128);
+  if (const dllm_status s = op_map_u8(&tk, cache->k, cache->hd, cache->T, planes, cache->hd, plane, cache->hd, keys);
       s != DLLM_OK)
     return s;
-  if (const dllm_status s = op_map_u8(&tv, cache->v, cache->hd, cache->T, planes, cache->hd, plane, cache->hd, 128);
+  if (const dllm_status s = op_map_u8(&tv, cache->v, cache->hd, cache->T, planes, cache->hd, plane, cache->hd, keys);
       s != DLLM_OK)
     return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -19,15 +19,18 @@
 // and lo, 2^4 finer, is off by 2^-4 of that or by 2^-14.
 // The value scale 2^ev of a key is folded into its probability.
 //
-// Softmax runs with one key a thread and all rows in its registers: nothing is
+// Softmax runs with one key a thread and RW rows in its registers: nothing is
 // reduced across threads per tile but the 32-key maximum of each row (one
 // redux).  Rows share a reference maximum that moves only when a score exceeds
 // it by 2^40 (float32 sums and block scales have the range); sums l are kept
-// per key lane and joined once at the end.
+// per key lane and joined once at the end.  This is the longest of the
+// overlapped stages, so the rows of a tile are shared out over N / RW groups of
+// four warps: with one group of N rows a thread a tile of 128 keys took 1.8 us
+// (N = 16) to 2.8 us (N = 32), of which HBM needs 0.8 us.
 //
 //   warp 0     TMA: K and V tiles through a ring of 128-key slots
 //   warp 1     one thread issues scale copies and MMAs
-//   warps 2-5  softmax, one key a thread; the query tile before, the output after
+//   warps 2..  softmax, one key and RW rows a thread; the query tile before, the output after
 // Keys are split over CTAs when there are few (sequence, head) items; every
 // split leaves its normalised output and (m, l), and a second small kernel joins them.
 #pragma once
@@ -57,24 +60,30 @@ static __device__ int g_attn_kv8_err[1];
 template <int HD, int N>
 struct AttnRowsCfg {
   static constexpr int KT = 128;
+  static constexpr int RW = N <= 16 ? 8 : 16;           // rows of a softmax thread
+  static constexpr int WGS = N / RW;                    // groups of four softmax warps
+  static constexpr int SOFT = 128 * WGS;                // softmax threads
+  static constexpr int THREADS = 64 + SOFT;
+  static constexpr int CTAS = N == 64 ? 1 : 2;          // an SM
   static constexpr int SLOT = KT * HD;                  // one K or V tile
-  static constexpr int Q_BYTES = N * HD;                // hi or lo
-  static constexpr int P_ROW = 2 * N;                   // a key's hi codes, then its lo codes
+  static constexpr int NQ = N < 16 ? 16 : N;            // 8 rows: one operand of 8 hi and 8 lo rows
+  static constexpr int Q_BYTES = NQ * HD;               // hi or lo
+  static constexpr int Q_PARTS = N < 16 ? 1 : 2;
+  static constexpr int P_ROW = N < 16 ? 32 : 2 * N;     // a key's N hi codes, then its N lo codes
   static constexpr int P_BYTES = KT * P_ROW;
-  static constexpr int SLOTS = HD == 64 ? 8 : N == 16 ? 6 : N == 32 ? 5 : 4;
-  static constexpr int P_BUFS = N == 64 ? 1 : 2;
-  static constexpr int S_BUFS = N == 64 ? 1 : 2;
-  static constexpr int SF_BYTES = 512;
-  static constexpr int STAT_FLOATS = 4 * N + 4 + 3 * N;  // warp maxima, warp value exponents, m, qf, limits
-  static constexpr int SMEM_BYTES = 1024 + SLOTS * SLOT + 2 * Q_BYTES + P_BUFS * P_BYTES + (P_BUFS + 1) * SF_BYTES +
+  static constexpr int SLOTS = CTAS == 1 ? (HD == 64 ? 16 : 9) : HD == 64 ? 8 : N == 32 ? 5 : 6;
+  static constexpr int SF_BYTES = 512;                  // ones, query scales, two buffers of probability scales
+  static constexpr int STAT_FLOATS = 4 * N + 4 + 2 * N + 4 * N;  // warp maxima, warp value exponents, m, limits, scales
+  static constexpr int SMEM_BYTES = 1024 + SLOTS * SLOT + Q_PARTS * Q_BYTES + 2 * P_BYTES + 4 * SF_BYTES +
                                     STAT_FLOATS * 4 + (2 * SLOTS + 10) * 8 + 16;
-  static constexpr int S_COL = 0;
-  static constexpr int O_COL = S_BUFS * N;              // 2 N columns: hi and lo products
+  static constexpr int S_COL = 0;                       // two buffers
+  static constexpr int O_COL = 2 * NQ;                  // 2 N columns: hi and lo products
   static constexpr int SFA_COL = O_COL + 2 * N;
-  static constexpr int SFB_COL = SFA_COL + 4;
-  static constexpr int TMEM_COLS = SFB_COL + 4 * P_BUFS <= 128 ? 128 : 256;
-  static_assert(SFB_COL + 4 * P_BUFS <= TMEM_COLS, "tensor memory");
-  static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs an SM");
+  static constexpr int SFQ_COL = SFA_COL + 4;
+  static constexpr int SFB_COL = SFQ_COL + 4;
+  static constexpr int TMEM_COLS = SFB_COL + 8 <= 128 ? 128 : SFB_COL + 8 <= 256 ? 256 : 512;
+  static_assert(SFB_COL + 8 <= TMEM_COLS && CTAS * TMEM_COLS <= 512, "tensor memory");
+  static_assert(CTAS * (SMEM_BYTES + 1024) <= 228 * 1024, "shared memory");
 };
 
 // Order-preserving map of a float's bits to a signed integer (NaN above +inf).
@@ -94,28 +103,28 @@ __device__ __forceinline__ float ex2(float x) {
 constexpr float kRefSlack = 40.0f;   // log2 a score or a value scale may exceed its reference by
 
 template <int HD, int N>
-__global__ void __launch_bounds__(192, 2)
+__global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N>::CTAS)
     attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const __grid_constant__ AttnKv8Params p) {
   using C = AttnRowsCfg<HD, N>;
-  constexpr int KT = C::KT;
+  constexpr int KT = C::KT, RW = C::RW;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sKV = smem;
   uint8_t* sQ = sKV + C::SLOTS * C::SLOT;               // hi, lo
-  uint8_t* sP = sQ + 2 * C::Q_BYTES;
-  uint8_t* sSF = sP + C::P_BUFS * C::P_BYTES;           // ones, then a probability scale atom a P buffer
-  float* s_wmax = reinterpret_cast<float*>(sSF + (C::P_BUFS + 1) * C::SF_BYTES);   // [4][N]
-  int* s_wev = reinterpret_cast<int*>(s_wmax + 4 * N);                             // [4]
+  uint8_t* sP = sQ + C::Q_PARTS * C::Q_BYTES;
+  uint8_t* sSF = sP + 2 * C::P_BYTES;                   // scale atoms: ones, queries, a P buffer each
+  float* s_wmax = reinterpret_cast<float*>(sSF + 4 * C::SF_BYTES);   // [4][N]
+  int* s_wev = reinterpret_cast<int*>(s_wmax + 4 * N);  // [4]
   float* s_m = reinterpret_cast<float*>(s_wev + 4);     // [N] reference maxima
-  float* s_qf = s_m + N;                                // [N] scale * log2 e * 2^eq
-  int* s_lim = reinterpret_cast<int*>(s_qf + N);        // [N]
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_lim + N);
+  int* s_lim = reinterpret_cast<int*>(s_m + N);         // [N]
+  float* s_inv = reinterpret_cast<float*>(s_lim + N);   // [softmax warps][RW] inverse block scales
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_inv + 4 * N);
   uint64_t* empty = full + C::SLOTS;
   uint64_t* qready = empty + C::SLOTS;
   uint64_t* sfull = qready + 1;                         // [2]
   uint64_t* sfree = sfull + 2;                          // [2]
-  uint64_t* pready = sfree + 2;                         // [2]  (one is unused with single buffers)
+  uint64_t* pready = sfree + 2;                         // [2]
   uint64_t* pvdone = pready + 2;                        // [2]  the product that read a P buffer is done
   uint64_t* mdone = pvdone + 2;                         // every MMA is done (before tensor memory is freed)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdone + 1);
@@ -134,11 +143,11 @@ __global__ void __launch_bounds__(192, 2)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(qready, 4);
+    mbar_init(qready, C::SOFT / 32);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sfull[s], 1);
-      mbar_init(&sfree[s], 4);
-      mbar_init(&pready[s], 4);
+      mbar_init(&sfree[s], C::SOFT / 32);
+      mbar_init(&pready[s], C::SOFT / 32);
       mbar_init(&pvdone[s], 1);
     }
     mbar_init(mdone, 1);
@@ -166,7 +175,7 @@ __global__ void __launch_bounds__(192, 2)
   const uint32_t tmem = *tmem_slot;
   int lim_max, lim_min;
   {
-    int hi = s_lim[lane & (N - 1)], lo = hi;
+    int hi = s_lim[lane & (N < 32 ? N - 1 : 31)], lo = hi;
     if constexpr (N == 64) {
       hi = max(hi, s_lim[lane + 32]);
       lo = min(lo, s_lim[lane + 32]);
@@ -198,31 +207,32 @@ __global__ void __launch_bounds__(192, 2)
   } else if (warp == 1) {
     if (lane == 0 && nt > 0 && mbar_wait(qready, 0u, abort_flag, err, ERR_ATTN_FULL)) {
       tc_fence_after();
-      constexpr uint32_t idesc_s = idesc_f8(128, N);
+      constexpr uint32_t idesc_s = idesc_mxf8(128, C::NQ);
       // V and P MN-major; P's scale byte kk belongs to keys 32 kk .. 32 kk + 31
       constexpr uint32_t idesc_o = idesc_mxf8(128, 2 * N) | (1u << 15) | (1u << 16);
       const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV), p0 = smem_u32(sP), f0 = smem_u32(sSF);
-      tmem_cp_scales(tmem + C::SFA_COL, sdesc_scales(f0));
+      const uint32_t sfa = tmem + C::SFA_COL, sfq = tmem + C::SFQ_COL;
+      tmem_cp_scales(sfa, sdesc_scales(f0));
+      tmem_cp_scales(sfq, sdesc_scales(f0 + C::SF_BYTES));
       int ns = 0, np = 0;
       unsigned long long idle_since = 0;
       uint32_t spins = 0;
       while (np < nt) {
         bool did = false;
         if (np < ns) {
-          const int u = 2 * np + 1, slot = u % C::SLOTS, pb = C::P_BUFS == 2 ? np & 1 : 0;
-          const uint32_t pk = (uint32_t)(C::P_BUFS == 2 ? np >> 1 : np) & 1u;
-          if (mbar_test_wait(smem_u32(&pready[pb]), pk) &&
+          const int u = 2 * np + 1, slot = u % C::SLOTS, pb = np & 1;
+          if (mbar_test_wait(smem_u32(&pready[pb]), (uint32_t)(np >> 1) & 1u) &&
               mbar_test_wait(smem_u32(&full[slot]), (uint32_t)(u / C::SLOTS) & 1u)) {
             tc_fence_after();
             const uint32_t v = kv0 + slot * C::SLOT, pp = p0 + pb * C::P_BYTES;
             const uint32_t sfb = tmem + C::SFB_COL + 4 * pb;
-            tmem_cp_scales(sfb, sdesc_scales(f0 + (1 + pb) * C::SF_BYTES));
+            tmem_cp_scales(sfb, sdesc_scales(f0 + (2 + pb) * C::SF_BYTES));
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               // a 64-wide head fills both halves of the 128 dims: the second repeats the first and is not read
               mma_mxf8_ss(tmem + C::O_COL, sdesc_rows<HD>(v + kk * 32 * HD, 0),
-                          sdesc_rows<C::P_ROW>(pp + kk * 32 * C::P_ROW), idesc_o | ((uint32_t)kk << 4),
-                          tmem + C::SFA_COL, sfb, (np > 0 || kk > 0) ? 1u : 0u);
+                          sdesc_rows<C::P_ROW>(pp + kk * 32 * C::P_ROW), idesc_o | ((uint32_t)kk << 4), sfa, sfb,
+                          (np > 0 || kk > 0) ? 1u : 0u);
             mma_commit(&empty[slot]);
             mma_commit(&pvdone[pb]);
             ++np;
@@ -230,18 +240,17 @@ __global__ void __launch_bounds__(192, 2)
           }
         }
         if (ns < nt) {
-          const int u = 2 * ns, slot = u % C::SLOTS, sb = C::S_BUFS == 2 ? ns & 1 : 0;
-          const int use = C::S_BUFS == 2 ? ns >> 1 : ns;
+          const int u = 2 * ns, slot = u % C::SLOTS, sb = ns & 1;
           if (mbar_test_wait(smem_u32(&full[slot]), (uint32_t)(u / C::SLOTS) & 1u) &&
-              (use == 0 || mbar_test_wait(smem_u32(&sfree[sb]), (uint32_t)(use - 1) & 1u))) {
+              (ns < 2 || mbar_test_wait(smem_u32(&sfree[sb]), (uint32_t)((ns >> 1) - 1) & 1u))) {
             tc_fence_after();
-            const uint32_t k = kv0 + slot * C::SLOT, d = tmem + C::S_COL + sb * N;
+            const uint32_t k = kv0 + slot * C::SLOT, d = tmem + C::S_COL + sb * C::NQ;
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
+            for (int part = 0; part < C::Q_PARTS; ++part)
 #pragma unroll
               for (int kk = 0; kk < HD / 32; ++kk)
-                mma_f8_ss(d, sdesc_rows<HD>(k + kk * 32), sdesc_rows<HD>(q0 + part * C::Q_BYTES + kk * 32), idesc_s,
-                          (part > 0 || kk > 0) ? 1u : 0u);
+                mma_mxf8_ss(d, sdesc_rows<HD>(k + kk * 32), sdesc_rows<HD>(q0 + part * C::Q_BYTES + kk * 32), idesc_s,
+                            sfa, sfq, (part > 0 || kk > 0) ? 1u : 0u);
             mma_commit(&empty[slot]);
             mma_commit(&sfull[sb]);
             ++ns;
@@ -267,19 +276,42 @@ __global__ void __launch_bounds__(192, 2)
     }
   } else {
     const int q4 = warp & 3, key_l = q4 * 32 + lane;      // this thread's key in a tile, and its tensor-memory lane
+    const int row0 = ((warp - 2) >> 2) * RW;              // its first row
     const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
     const int tid = (warp - 2) * 32 + lane;
     // product t of P V is done
     auto pv_wait = [&](int t) {
-      const int pb = C::P_BUFS == 2 ? t & 1 : 0;
-      return __all_sync(0xffffffffu, mbar_wait(&pvdone[pb], (uint32_t)(C::P_BUFS == 2 ? t >> 1 : t) & 1u, abort_flag, err,
+      return __all_sync(0xffffffffu, mbar_wait(&pvdone[t & 1], (uint32_t)(t >> 1) & 1u, abort_flag, err,
                                                ERR_ATTN_FULL)) != 0;
     };
+    const uint8_t* ksc = p.c.k_scale + (long long)plane * p.c.T;
+    const uint8_t* vsc = p.c.v_scale + (long long)plane * p.c.T;
+    // scale bytes of this thread's key in four tiles, and of the next four in
+    // flight: fetched a tile ahead, their latency was the loop's (1.7 us a tile)
+    uint32_t kb4 = 0, vb4 = 0;
+    int kn[4], vn[4];
+    auto fetch = [&](int t) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int key = (t0 + t + e) * KT + key_l;
+        const bool in = t + e < nt && key < lim_max;
+        kn[e] = in ? __ldg(ksc + key) : 127;
+        vn[e] = in ? __ldg(vsc + key) : 127;
+      }
+    };
+    fetch(0);
     if (nt > 0) {
       // ---------------------------------------------------- the query tile
       constexpr int L = HD / 8;                           // lanes of a row
-      for (int n = tid / L; n < N; n += 128 / L) {
-        const int l = tid % L;
+      if (tid < 128) {
+#pragma unroll
+        for (int f = 0; f < 4; ++f) reinterpret_cast<uint32_t*>(sSF + f * C::SF_BYTES)[tid] = 0x7f7f7f7fu;
+      }
+      if (tid < N) s_m[tid] = 0.0f;
+      named_bar_sync(2, C::SOFT);
+#pragma unroll 1
+      for (int n0 = 0; n0 < N; n0 += C::SOFT / L) {
+        const int n = n0 + tid / L, l = tid % L;
         float x[8] = {};
         if (n < n_rows) {
           const int rn = rt * N + n, i = rn / p.group, h = g * p.group + rn % p.group;
@@ -290,101 +322,98 @@ __global__ void __launch_bounds__(192, 2)
         uint32_t m = abs_bits8(x);
 #pragma unroll
         for (int d = L / 2; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const int byte = scale_byte(m);
-        const float inv = byte == kScaleNan ? __uint_as_float(0x7fffffffu) : scale_inverse(byte);
-        float r[8];
+        if (n < N) {
+          const int byte = scale_byte(m);
+          const float inv = byte == kScaleNan ? __uint_as_float(0x7fffffffu) : scale_inverse(byte);
+          float r[8], b[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[e] = x[e] * inv;    // a row that is not finite becomes NaN
-        const uint2 hi = encode8(r, 1.0f);
-        float b[8];
-        decode8(hi, 1.0f, b);
+          for (int e = 0; e < 8; ++e) r[e] = x[e] * inv;  // a row that is not finite becomes NaN
+          const uint2 hi = encode8(r, 1.0f);
+          decode8(hi, 1.0f, b);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) b[e] = r[e] - b[e];
-        const uint2 lo = encode8(b, 1.0f);
-        const uint32_t off = swizzled<HD>(n, l >> 1) + (uint32_t)(l & 1) * 8;
-        *reinterpret_cast<uint2*>(sQ + off) = hi;
-        *reinterpret_cast<uint2*>(sQ + C::Q_BYTES + off) = lo;
-        if (l == 0) s_qf[n] = byte == kScaleNan ? 1.0f : p.scale_log2 * scale_value(byte);
+          for (int e = 0; e < 8; ++e) b[e] = r[e] - b[e];
+          const uint2 lo = encode8(b, 1.0f);
+          const int nl = C::Q_PARTS == 1 ? n + N : n;     // the lo row, in its own operand or behind the hi rows
+          *reinterpret_cast<uint2*>(sQ + swizzled<HD>(n, l >> 1) + (l & 1) * 8) = hi;
+          *reinterpret_cast<uint2*>(sQ + (C::Q_PARTS - 1) * C::Q_BYTES + swizzled<HD>(nl, l >> 1) + (l & 1) * 8) = lo;
+          if (l == 0 && byte != kScaleNan) {
+            uint32_t* sf = reinterpret_cast<uint32_t*>(sSF + C::SF_BYTES);
+            sf[(n & 31) * 4 + (n >> 5)] = (uint32_t)byte * 0x01010101u;
+            sf[(nl & 31) * 4 + (nl >> 5)] = (uint32_t)byte * 0x01010101u;
+          }
+        }
       }
-      reinterpret_cast<uint32_t*>(sSF)[tid] = 0x7f7f7f7fu;
-#pragma unroll
-      for (int b = 0; b < C::P_BUFS; ++b) reinterpret_cast<uint32_t*>(sSF + (1 + b) * C::SF_BYTES)[tid] = 0x7f7f7f7fu;
-      if (tid < N) s_m[tid] = 0.0f;
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(qready);
-      named_bar_sync(2, 128);
     }
     // ------------------------------------------------------ the keys
-    float l_sum[N];
+    float l_sum[RW];
 #pragma unroll
-    for (int n = 0; n < N; ++n) l_sum[n] = 0.0f;
+    for (int n = 0; n < RW; ++n) l_sum[n] = 0.0f;
     int vref = 0;
     // After a wait that gave up (ok false) the loop goes on without waiting, so
     // that every warp meets every barrier; the outputs are invalid and reported.
     bool ok = true;
-    const uint8_t* ksc = p.c.k_scale + (long long)plane * p.c.T;
-    const uint8_t* vsc = p.c.v_scale + (long long)plane * p.c.T;
-    int kb_next = 127, vb_next = 127;
-    if (nt > 0 && t0 * KT + key_l < lim_max) {
-      kb_next = ksc[t0 * KT + key_l];
-      vb_next = vsc[t0 * KT + key_l];
-    }
     for (int t = 0; t < nt; ++t) {
-      const int sb = C::S_BUFS == 2 ? t & 1 : 0, pb = C::P_BUFS == 2 ? t & 1 : 0;
+      const int b = t & 1;                                // S and P buffer
       const int key = (t0 + t) * KT + key_l;
-      int kb = kb_next, vb = vb_next;
-      if (t + 1 < nt && key + KT < lim_max) {
-        kb_next = ksc[key + KT];
-        vb_next = vsc[key + KT];
+      if ((t & 3) == 0) {
+        kb4 = (uint32_t)(kn[0] | kn[1] << 8 | kn[2] << 16 | kn[3] << 24);
+        vb4 = (uint32_t)(vn[0] | vn[1] << 8 | vn[2] << 16 | vn[3] << 24);
+        fetch(t + 4);
       }
+      const int kb = (int)(kb4 & 255u), vb = (int)(vb4 & 255u);
+      kb4 >>= 8;
+      vb4 >>= 8;
       const bool seen = key < lim_max;                    // by some row
-      if (!seen) kb = vb = 127;
       const bool bad = kb == kScaleNan || vb == kScaleNan;
-      const float kf = bad ? __uint_as_float(0x7fffffffu) : scale_value(kb);
+      const float kf = bad ? __uint_as_float(0x7fffffffu) : scale_value(kb) * p.scale_log2;
       const int ev = bad || !seen ? -1000 : vb - 127;     // -1000: no value scale to refer to
-      if (!__all_sync(0xffffffffu, mbar_wait(&sfull[sb], (uint32_t)(C::S_BUFS == 2 ? t >> 1 : t) & 1u, abort_flag, err,
-                                             ERR_ATTN_FULL))) {
-        ok = false;
-      }
+      ok = __all_sync(0xffffffffu, mbar_wait(&sfull[b], (uint32_t)(t >> 1) & 1u, abort_flag, err, ERR_ATTN_FULL)) && ok;
       tc_fence_after();
       // scores in base 2, relative to their row's reference
-      float z[N];
+      float z[RW];
       float top = -INFINITY;
+      if constexpr (C::Q_PARTS == 1) {
+        float s[16];
+        tmem_ld16(trow + C::S_COL + b * C::NQ, s);
 #pragma unroll
-      for (int n = 0; n < N; n += 16) {
-        tmem_ld16(trow + C::S_COL + sb * N + n, z + n);
-#pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(s_qf + n + j);
-          const float4 m = *reinterpret_cast<const float4*>(s_m + n + j);
-          z[n + j] = fmaf(z[n + j], kf * f.x, -m.x);
-          z[n + j + 1] = fmaf(z[n + j + 1], kf * f.y, -m.y);
-          z[n + j + 2] = fmaf(z[n + j + 2], kf * f.z, -m.z);
-          z[n + j + 3] = fmaf(z[n + j + 3], kf * f.w, -m.w);
-        }
+        for (int j = 0; j < RW; ++j) z[j] = s[j] + s[j + N];
+      } else if constexpr (RW == 8) {
+        tmem_ld8(trow + C::S_COL + b * C::NQ + row0, z);
+      } else {
+        tmem_ld16(trow + C::S_COL + b * C::NQ + row0, z);
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sfree[sb]);
+      if (lane == 0) mbar_arrive(&sfree[b]);
+#pragma unroll
+      for (int j = 0; j < RW; j += 4) {
+        const float4 m = *reinterpret_cast<const float4*>(s_m + row0 + j);
+        z[j] = fmaf(z[j], kf, -m.x);
+        z[j + 1] = fmaf(z[j + 1], kf, -m.y);
+        z[j + 2] = fmaf(z[j + 2], kf, -m.z);
+        z[j + 3] = fmaf(z[j + 3], kf, -m.w);
+      }
       if ((t0 + t + 1) * KT > lim_min) {                  // some row does not see all of the tile
 #pragma unroll
-        for (int n = 0; n < N; ++n) z[n] = key < s_lim[n] ? z[n] : -INFINITY;
+        for (int j = 0; j < RW; ++j) z[j] = key < s_lim[row0 + j] ? z[j] : -INFINITY;
       }
 #pragma unroll
-      for (int n = 0; n < N; ++n) top = fmaxf(top, z[n]);
+      for (int j = 0; j < RW; ++j) top = fmaxf(top, z[j]);
       bool need = t == 0 || ev - vref > (int)kRefSlack || top > kRefSlack;
       if (!ok) need = false;
-      if (named_bar_or(2, 128, need)) {
+      if (named_bar_or(2, C::SOFT, need)) {
         // new references: the first tile's, or a score far above the last ones
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          const int wt = __reduce_max_sync(0xffffffffu, float_order(z[n]));
-          if (lane == (n & 31)) s_wmax[q4 * N + n] = order_float(wt);
+        for (int j = 0; j < RW; ++j) {
+          const int wt = __reduce_max_sync(0xffffffffu, float_order(z[j]));
+          if (lane == j) s_wmax[q4 * N + row0 + j] = order_float(wt);
         }
         const int evw = __reduce_max_sync(0xffffffffu, ev);
-        if (lane == 0) s_wev[q4] = evw;
-        named_bar_sync(2, 128);
+        if (row0 == 0 && lane == 0) s_wev[q4] = evw;
+        named_bar_sync(2, C::SOFT);
         const int ev_top = max(max(s_wev[0], s_wev[1]), max(s_wev[2], s_wev[3]));
         const int vref_new = t == 0 ? max(ev_top, -127) : max(vref, ev_top);
         float up = 0.0f;                                  // row tid's reference rises by this
@@ -395,84 +424,90 @@ __global__ void __launch_bounds__(192, 2)
           up = order_float(tr);
           if (up == -INFINITY || (t > 0 && up < 0.0f)) up = 0.0f;
         }
-        named_bar_sync(2, 128);
+        named_bar_sync(2, C::SOFT);
         if (tid < N) {
           s_m[tid] += up;
           s_wmax[tid] = up;
         }
-        named_bar_sync(2, 128);
+        named_bar_sync(2, C::SOFT);
 #pragma unroll
-        for (int n = 0; n < N; ++n) z[n] -= s_wmax[n];
+        for (int j = 0; j < RW; ++j) z[j] -= s_wmax[row0 + j];
         if (t > 0) {
           ok = ok && pv_wait(t - 1);
           tc_fence_after();
           // exponents below -126 leave nothing of the old sums that counts
           const float vcorr = vref - vref_new < -126 ? 0.0f : scale_value(127 + vref - vref_new);
+          float corr[RW];
 #pragma unroll
-          for (int n = 0; n < N; ++n) l_sum[n] *= exp2f(-s_wmax[n]);
-#pragma unroll 1
-          for (int c = 0; c < 2 * N; c += 16) {
-            float o[16];
-            tmem_ld16(trow + C::O_COL + c, o);
+          for (int j = 0; j < RW; ++j) {
+            corr[j] = exp2f(-s_wmax[row0 + j]);
+            l_sum[j] *= corr[j];
+          }
 #pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] *= exp2f(-s_wmax[(c + j) & (N - 1)]) * vcorr;
-            tmem_st16(trow + C::O_COL + c, o);
+          for (int part = 0; part < 2; ++part) {
+            float o[RW];
+            tmem_ld<RW>(trow + C::O_COL + part * N + row0, o);
+#pragma unroll
+            for (int j = 0; j < RW; ++j) o[j] *= corr[j] * vcorr;
+            tmem_st<RW>(trow + C::O_COL + part * N + row0, o);
           }
           tc_fence_before();
         }
         vref = vref_new;
+        named_bar_sync(2, C::SOFT);                       // s_wmax is read: the next tile may rewrite it
       }
       // the P buffer is free once the product that last read it is done
-      if (t >= C::P_BUFS && ok) ok = pv_wait(t - C::P_BUFS);
+      if (t >= 2 && ok) ok = pv_wait(t - 2);
       const int dv = max(ev - vref, -126);
       const float vf = bad || !seen ? 0.0f : __uint_as_float((uint32_t)(127 + dv) << 23);
-      uint8_t* prow = sP + pb * C::P_BYTES;
-      uint8_t* sf = sSF + (1 + pb) * C::SF_BYTES;
+      uint8_t* prow = sP + b * C::P_BYTES;
+      uint8_t* sf = sSF + (2 + b) * C::SF_BYTES;
+      // probabilities, and each row's largest of the warp's 32 keys: lane j (modulo RW) keeps row j's
+      uint32_t top_me = 0;
 #pragma unroll
-      for (int n = 0; n < N; n += 16) {
-        uint32_t hi[4], lo[4];
-        int byte_me = 127;
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          float x[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float pr = ex2(z[n + j + e]);
-            l_sum[n + j + e] += pr;
-            const float pv = pr * vf;
-            // the block's scale puts its largest probability into [128, 256)
-            const int exp = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(pv)) >> 23);
-            const int byte = min(max(exp - 7, 4), 247);
-            if (lane == n + j + e - (n & 32)) byte_me = byte;
-            x[e] = pv * __uint_as_float((uint32_t)(254 - byte) << 23);
-          }
-          // hi: the nearest code; lo: what it leaves, at most a 16th of it, in a scale 2^4 smaller
-          const uint32_t ch = cvt_e4m3x2(x[0], x[1]);
-          const float2 h = f16x2_to_f32(cvt_f16x2_e4m3x2((uint16_t)ch));
-          const uint32_t cl = cvt_e4m3x2((x[0] - h.x) * 16.0f, (x[1] - h.y) * 16.0f);
-          if (j & 2) {
-            hi[j >> 2] |= ch << 16;
-            lo[j >> 2] |= cl << 16;
-          } else {
-            hi[j >> 2] = ch;
-            lo[j >> 2] = cl;
-          }
-        }
-        *reinterpret_cast<uint4*>(prow + swizzled<C::P_ROW>(key_l, n >> 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(prow + swizzled<C::P_ROW>(key_l, (N + n) >> 4)) =
-            make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        if ((lane & 16) == (n & 16)) {
-          // lane holds row n + (lane & 15): its scale byte for this warp's keys, once for hi and once for lo
-          const int r = n + (lane & 15);
-          sf[(r & 31) * 16 + (r >> 5) * 4 + q4] = (uint8_t)byte_me;
-          sf[((r + N) & 31) * 16 + ((r + N) >> 5) * 4 + q4] = (uint8_t)(byte_me - 4);
-        }
+      for (int j = 0; j < RW; ++j) {
+        const float pr = ex2(z[j]);
+        l_sum[j] += pr;
+        z[j] = pr * vf;
+        const uint32_t r = __reduce_max_sync(0xffffffffu, __float_as_uint(z[j]));
+        if ((lane & (RW - 1)) == j) top_me = r;
       }
-      if ((t0 + t + 1) * KT > lim_max) {
+      // the block's scale puts its largest probability into [128, 256); the lanes work out a row each
+      const int byte_me = min(max((int)(top_me >> 23) - 7, 4), 247);
+      float* inv = s_inv + (warp - 2) * RW;
+      if (lane < RW) inv[lane] = __uint_as_float((uint32_t)(254 - byte_me) << 23);
+      if (lane < 2 * RW) {
+        // lanes 0 .. RW-1: the scale bytes of the hi rows for this warp's keys, the next RW: of the lo rows
+        const int r = row0 + (lane & (RW - 1)) + (lane < RW ? 0 : N);
+        sf[(r & 31) * 16 + (r >> 5) * 4 + q4] = (uint8_t)(lane < RW ? byte_me : byte_me - 4);
+      }
+      __syncwarp();
+      uint32_t hi[RW / 4], lo[RW / 4];
+#pragma unroll
+      for (int j = 0; j < RW; j += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(inv + j);
+        // hi: the nearest code; lo: what it leaves, at most a 16th of it, in a scale 2^4 smaller
+        const uint32_t x0 = pack_f16x2(z[j] * f.x, z[j + 1] * f.y), x1 = pack_f16x2(z[j + 2] * f.z, z[j + 3] * f.w);
+        const uint32_t h0 = cvt_e4m3x2_f16x2(x0), h1 = cvt_e4m3x2_f16x2(x1);
+        hi[j >> 2] = h0 | (h1 << 16);
+        lo[j >> 2] = cvt_e4m3x2_f16x2(sub_mul16_f16x2(x0, cvt_f16x2_e4m3x2((uint16_t)h0))) |
+                     (cvt_e4m3x2_f16x2(sub_mul16_f16x2(x1, cvt_f16x2_e4m3x2((uint16_t)h1))) << 16);
+      }
+      uint8_t* ph = prow + swizzled<C::P_ROW>(key_l, row0 >> 4) + (row0 & 15);
+      uint8_t* pl = prow + swizzled<C::P_ROW>(key_l, (N + row0) >> 4) + ((N + row0) & 15);
+      if constexpr (RW == 8) {
+        *reinterpret_cast<uint2*>(ph) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(pl) = make_uint2(lo[0], lo[1]);
+      } else {
+        *reinterpret_cast<uint4*>(ph) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(pl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      if ((t0 + t + 1) * KT > lim_max && row0 == 0) {
         // the last tile runs past every row's limit: whatever bytes lie there
         // (codes of NaN among them) must not meet the zero probabilities
         const int u = 2 * t + 1, slot = u % C::SLOTS;
-        ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (uint32_t)(u / C::SLOTS) & 1u, abort_flag, err, ERR_ATTN_FULL));
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (uint32_t)(u / C::SLOTS) & 1u, abort_flag, err, ERR_ATTN_FULL)) &&
+             ok;
         if (!seen) {
 #pragma unroll
           for (int c = 0; c < HD / 16; ++c)
@@ -482,55 +517,50 @@ __global__ void __launch_bounds__(192, 2)
       fence_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&pready[pb]);
+      if (lane == 0) mbar_arrive(&pready[b]);
     }
     // ------------------------------------------------------ sums and output
     if (nt > 0) {
       if (ok) ok = pv_wait(nt - 1);
       tc_fence_after();
+      // sum RW columns over the warp: lane c (modulo RW) ends with column c
 #pragma unroll
-      for (int n = 0; n < N; n += 16) {
-        // sum 16 columns over the warp: lane c (and c + 16) ends with column n + (c & 15)
+      for (int s = RW / 2; s >= 1; s >>= 1) {
+        const bool upper = (lane & s) != 0;
 #pragma unroll
-        for (int s = 8; s >= 1; s >>= 1) {
-          const bool up = (lane & s) != 0;
-#pragma unroll
-          for (int i = 0; i < s; ++i) {
-            const float send = up ? l_sum[n + i] : l_sum[n + i + s];
-            const float keep = up ? l_sum[n + i + s] : l_sum[n + i];
-            l_sum[n + i] = keep + __shfl_xor_sync(0xffffffffu, send, s);
-          }
+        for (int i = 0; i < s; ++i) {
+          const float send = upper ? l_sum[i] : l_sum[i + s];
+          const float keep = upper ? l_sum[i + s] : l_sum[i];
+          l_sum[i] = keep + __shfl_xor_sync(0xffffffffu, send, s);
         }
-        l_sum[n] += __shfl_xor_sync(0xffffffffu, l_sum[n], 16);
-        if (lane < 16) s_wmax[q4 * N + n + lane] = l_sum[n];
       }
-      named_bar_sync(2, 128);
+#pragma unroll
+      for (int s = RW; s < 32; s <<= 1) l_sum[0] += __shfl_xor_sync(0xffffffffu, l_sum[0], s);
+      if (lane < RW) s_wmax[q4 * N + row0 + lane] = l_sum[0];
+      named_bar_sync(2, C::SOFT);
     }
     const int dim = key_l;
     const float vs = scale_value(127 + vref);
     const long long slot = (long long)item * p.splits + split;
-#pragma unroll 1
-    for (int n = 0; n < N; n += 16) {
-      float a[16] = {}, b[16] = {};
-      if (nt > 0) {
-        tmem_ld16(trow + C::O_COL + n, a);
-        tmem_ld16(trow + C::O_COL + N + n, b);
-      }
-      if (dim < HD) {
+    float a[RW] = {}, bl[RW] = {};
+    if (nt > 0) {
+      tmem_ld<RW>(trow + C::O_COL + row0, a);
+      tmem_ld<RW>(trow + C::O_COL + N + row0, bl);
+    }
+    if (dim < HD) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int r = n + j;
-          if (r >= n_rows) break;
-          float l = 0.0f;
-          if (nt > 0) l = (s_wmax[r] + s_wmax[N + r]) + (s_wmax[2 * N + r] + s_wmax[3 * N + r]);
-          const float v = l == 0.0f ? 0.0f : (a[j] + b[j]) / l * vs;
-          if (p.splits > 1) {
-            p.ws_o[(slot * N + r) * HD + dim] = v;
-            if (dim < 2) p.ws_ml[(slot * N + r) * 2 + dim] = dim ? l : (nt > 0 ? s_m[r] : 0.0f);
-          } else {
-            const int rn = rt * N + r, i = rn / p.group, h = g * p.group + rn % p.group;
-            p.out[((long long)seq * p.R + i) * p.o_rs + (long long)h * HD + dim] = f32_to_bf16_bits(v);
-          }
+      for (int j = 0; j < RW; ++j) {
+        const int r = row0 + j;
+        if (r >= n_rows) break;
+        float l = 0.0f;
+        if (nt > 0) l = (s_wmax[r] + s_wmax[N + r]) + (s_wmax[2 * N + r] + s_wmax[3 * N + r]);
+        const float v = l == 0.0f ? 0.0f : (a[j] + bl[j]) / l * vs;
+        if (p.splits > 1) {
+          p.ws_o[(slot * N + r) * HD + dim] = v;
+          if (dim < 2) p.ws_ml[(slot * N + r) * 2 + dim] = dim ? l : (nt > 0 ? s_m[r] : 0.0f);
+        } else {
+          const int rn = rt * N + r, i = rn / p.group, h = g * p.group + rn % p.group;
+          p.out[((long long)seq * p.R + i) * p.o_rs + (long long)h * HD + dim] = f32_to_bf16_bits(v);
         }
       }
     }

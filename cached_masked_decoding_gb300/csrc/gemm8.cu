@@ -11,37 +11,60 @@ namespace dllm {
 constexpr int kQBlock = 128;
 
 // ---------------------------------------------------------------- quantiser
-// A group of 16 lanes owns a block of 128 elements, 8 each.
+// Bound by HBM.  A group of 16 lanes owns a block of 128 elements, 8 each; a
+// thread group has kQAhead blocks in flight.
+constexpr int kQAhead = 4;
+
+struct Quantise8Params {
+  const void* x;
+  uint8_t *codes, *scales;
+  long long rs;
+  int rows, K;
+  uint32_t groups;     // rows * blocks of a row
+  FastDiv blocks;
+};
+
 template <typename E, bool VEC>
-__global__ void __launch_bounds__(256) quantise8_kernel(const void* x_, long long rs, int rows, int K, int kb,
-                                                        uint8_t* codes, uint8_t* scales) {
-  const long long tid = (long long)blockIdx.x * 256 + threadIdx.x;
-  const int l = (int)(tid & 15);
-  const long long g = tid >> 4;
-  const int B = (int)(g % kb);
-  const long long row = g / kb;
-  const int k0 = B * kQBlock + l * 8;
-  const bool on = row < rows && k0 < K;       // K % 16 == 0: a lane's 8 elements are all in or all out
-  float x[8] = {};
-  if (on) {
-    const typename E::T* px = static_cast<const typename E::T*>(x_) + row * rs + k0;
-    if constexpr (VEC) {
-      E::load8(px, x);
-    } else {
+__global__ void __launch_bounds__(256, 4) quantise8_kernel(const __grid_constant__ Quantise8Params p) {
+  const int l = threadIdx.x & 15;
+  griddep_launch_dependents();
+  griddep_wait();
+  const uint32_t g0 = blockIdx.x * (uint32_t)(16 * kQAhead) + (threadIdx.x >> 4);
+  Raw8<E> raw[kQAhead];
+  uint32_t row[kQAhead], B[kQAhead];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = E::get(px + i);
+  for (int j = 0; j < kQAhead; ++j) {
+    const uint32_t g = g0 + 16 * j;
+    row[j] = p.blocks.divmod(g, B[j]);
+    const int k0 = (int)B[j] * kQBlock + l * 8;
+    raw[j].zero();
+    if (g < p.groups && k0 < p.K) {            // K % 16 == 0: a lane's 8 elements are all in or all out
+      const typename E::T* px = static_cast<const typename E::T*>(p.x) + row[j] * p.rs + k0;
+      if constexpr (VEC) {
+        raw[j].load(px);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) reinterpret_cast<typename E::T*>(raw[j].w)[e] = px[e];
+      }
     }
   }
-  uint32_t m = abs_bits8(x);
 #pragma unroll
-  for (int d = 8; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-  const int byte = scale_byte(m);
-  if (on) {
-    uint2 c = make_uint2(0, 0);
-    if (byte != kScaleNan) c = encode8(x, scale_inverse(byte));
-    *reinterpret_cast<uint2*>(codes + row * K + k0) = c;
+  for (int j = 0; j < kQAhead; ++j) {
+    float x[8];
+    raw[j].floats(x);
+    uint32_t m = abs_bits8(x);
+#pragma unroll
+    for (int d = 8; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const int byte = scale_byte(m);
+    if (g0 + 16 * j >= p.groups) continue;
+    const int k0 = (int)B[j] * kQBlock + l * 8;
+    if (k0 < p.K) {
+      uint2 c = make_uint2(0, 0);
+      if (byte != kScaleNan) c = encode8(x, scale_inverse(byte));
+      *reinterpret_cast<uint2*>(p.codes + (long long)row[j] * p.K + k0) = c;
+    }
+    if (l == 0) p.scales[(long long)B[j] * p.rows + row[j]] = (uint8_t)byte;
   }
-  if (l == 0 && row < rows) scales[(long long)B * rows + row] = (uint8_t)byte;
 }
 
 // ---------------------------------------------------------------- product
@@ -171,31 +194,63 @@ __global__ void __launch_bounds__(224, 2)
       mma_commit(done);
     }
   } else if (warp == 6) {
+    // Four blocks' bytes in use, the next four's in flight: fetched one at a
+    // time, their latency was the block's time (0.7 us, where HBM needs 0.4).
+    constexpr int AHEAD = 4, WB = (BN + 31) / 32;
+    uint32_t wa[AHEAD][4], wb[AHEAD][WB];
+    auto fetch = [&](int i0) {
+#pragma unroll
+      for (int e = 0; e < AHEAD; ++e) {
+        const long long B = c0 + i0 + e;
+        const bool in = i0 + e < nc;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int m = m0 + lane + 32 * j;
+          wa[e][j] = in && m < p.M ? __ldg(p.ws + B * p.M + m) : 127u;
+        }
+#pragma unroll
+        for (int j = 0; j < WB; ++j) {
+          const int n = n0 + lane + 32 * j;
+          wb[e][j] = in && n < p.N ? __ldg(p.xs + B * p.N + n) : 127u;
+        }
+      }
+    };
     RingPos r{0, 0u};
-    for (int i = 0; i < nc; ++i) {
-      const long long B = c0 + i;
-      uint32_t wa[4], wb[4 * C::SFB_ATOMS];
+    fetch(0);
+    bool ok = true;
+    for (int i0 = 0; i0 < nc && ok; i0 += AHEAD) {
+      uint32_t ca[AHEAD][4], cb[AHEAD][WB];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int m = m0 + lane + 32 * j;
-        wa[j] = m < p.M ? __ldg(p.ws + B * p.M + m) : 127u;
+      for (int e = 0; e < AHEAD; ++e) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ca[e][j] = wa[e][j];
+#pragma unroll
+        for (int j = 0; j < WB; ++j) cb[e][j] = wb[e][j];
       }
+      fetch(i0 + AHEAD);
 #pragma unroll
-      for (int j = 0; j < 4 * C::SFB_ATOMS; ++j) {
-        const int n = n0 + lane + 32 * j;
-        wb[j] = 32 * j < BN && n < p.N ? __ldg(p.xs + B * p.N + n) : 127u;
+      for (int e = 0; e < AHEAD; ++e) {
+        if (i0 + e >= nc || !ok) break;
+        if (i0 + e >= S &&
+            !__all_sync(0xffffffffu, mbar_wait(&empty[r.s], r.par ^ 1u, abort_flag, err, ERR_GEMM_EMPTY))) {
+          ok = false;
+          break;
+        }
+        uint4* f = reinterpret_cast<uint4*>(sF + r.s * C::SF_BYTES) + lane;
+        constexpr uint32_t rep = 0x01010101u;
+        f[0] = make_uint4(ca[e][0] * rep, ca[e][1] * rep, ca[e][2] * rep, ca[e][3] * rep);
+#pragma unroll
+        for (int t = 0; t < C::SFB_ATOMS; ++t) {
+          uint32_t w4[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w4[j] = 4 * t + j < WB ? cb[e][4 * t + j < WB ? 4 * t + j : 0] * rep : 127u * rep;
+          f[32 * (t + 1)] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[r.s]);
+        r.next(S);
       }
-      if (i >= S && !__all_sync(0xffffffffu, mbar_wait(&empty[r.s], r.par ^ 1u, abort_flag, err, ERR_GEMM_EMPTY))) break;
-      uint4* f = reinterpret_cast<uint4*>(sF + r.s * C::SF_BYTES) + lane;
-      constexpr uint32_t rep = 0x01010101u;
-      f[0] = make_uint4(wa[0] * rep, wa[1] * rep, wa[2] * rep, wa[3] * rep);
-#pragma unroll
-      for (int t = 0; t < C::SFB_ATOMS; ++t)
-        f[32 * (t + 1)] = make_uint4(wb[4 * t] * rep, wb[4 * t + 1] * rep, wb[4 * t + 2] * rep, wb[4 * t + 3] * rep);
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&full[r.s]);
-      r.next(S);
     }
   }
   __syncwarp();
@@ -267,14 +322,10 @@ cudaError_t gemm8_err_word(int** p) { return cudaGetSymbolAddress(reinterpret_ca
 namespace {
 
 template <typename E>
-cudaError_t launch_quantise8(const void* x, long long rs, int rows, int K, uint8_t* codes, uint8_t* scales, bool vec,
-                             unsigned grid, cudaStream_t st) {
-  const int kb = (K + kQBlock - 1) / kQBlock;
-  if (vec)
-    quantise8_kernel<E, true><<<grid, 256, 0, st>>>(x, rs, rows, K, kb, codes, scales);
-  else
-    quantise8_kernel<E, false><<<grid, 256, 0, st>>>(x, rs, rows, K, kb, codes, scales);
-  return cudaGetLastError();
+cudaError_t launch_quantise8(const Quantise8Params& p, bool vec, cudaStream_t st) {
+  const dim3 grid((p.groups + 16 * kQAhead - 1) / (16 * kQAhead));
+  return vec ? op_launch(quantise8_kernel<E, true>, grid, dim3(256), 0, st, 1, p)
+             : op_launch(quantise8_kernel<E, false>, grid, dim3(256), 0, st, 1, p);
 }
 
 template <int BN>
@@ -299,15 +350,23 @@ extern "C" dllm_status dllm_op_quantise8(const void* x, int64_t row_stride, int3
                    rows, K, dtype);
   const long long rs = row_stride ? row_stride : K;
   if (rs < K || rs > (1LL << 40)) return op_fail(DLLM_EINVAL, "quantise8: row stride %lld (0, or at least K=%d)", rs, K);
-  const long long kb = (K + kQBlock - 1) / kQBlock;
-  const long long blocks = (rows * kb * 16 + 255) / 256;
-  if (blocks > 0x7fffffffLL) return op_fail(DLLM_EINVAL, "quantise8: rows=%d K=%d are too many blocks", rows, K);
+  const long long kb = ((long long)K + kQBlock - 1) / kQBlock;
+  if (rows * kb > 0x7fffff00LL) return op_fail(DLLM_EINVAL, "quantise8: rows=%d K=%d are too many blocks", rows, K);
   const bool vec = op_aligned(x, 16) && (rs * es) % 16 == 0;
+  Quantise8Params p = {};
+  p.x = x;
+  p.codes = codes;
+  p.scales = scales;
+  p.rs = rs;
+  p.rows = rows;
+  p.K = K;
+  p.groups = (uint32_t)(rows * kb);
+  p.blocks = FastDiv((uint32_t)kb);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (dtype) {
-    case DLLM_F32: OP_CK(launch_quantise8<ElemF32>(x, rs, rows, K, codes, scales, vec, (unsigned)blocks, st)); break;
-    case DLLM_BF16: OP_CK(launch_quantise8<ElemBf16>(x, rs, rows, K, codes, scales, vec, (unsigned)blocks, st)); break;
-    default: OP_CK(launch_quantise8<ElemF16>(x, rs, rows, K, codes, scales, vec, (unsigned)blocks, st)); break;
+    case DLLM_F32: OP_CK(launch_quantise8<ElemF32>(p, vec, st)); break;
+    case DLLM_BF16: OP_CK(launch_quantise8<ElemBf16>(p, vec, st)); break;
+    default: OP_CK(launch_quantise8<ElemF16>(p, vec, st)); break;
   }
   return DLLM_OK;
 }
@@ -328,7 +387,7 @@ extern "C" dllm_status dllm_op_gemm8(const uint8_t* W, const uint8_t* W_scale, c
   p.M = M;
   p.N = N;
   p.K = K;
-  p.kb = (K + kQBlock - 1) / kQBlock;
+  p.kb = (int)(((long long)K + kQBlock - 1) / kQBlock);
   p.out_bf16 = y_dtype == DLLM_BF16;
   const int bn = N <= 32 ? 32 : N <= 64 ? 64 : 128;
   p.n_tiles = (N + bn - 1) / bn;

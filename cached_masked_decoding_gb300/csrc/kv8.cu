@@ -7,6 +7,7 @@
 // is a shuffle reduction within the group, and a row's codes are one
 // contiguous write of hd bytes.  K and V go in one launch.
 #include "ops8.h"
+#include "ptx8.cuh"
 #include "q8.cuh"
 
 namespace dllm {
@@ -19,67 +20,96 @@ struct Kv8Params {
   const int32_t* starts; // [b] position of a sequence's first row, or null (0)
   const int32_t* counts; // [b] rows of a sequence that take part, or null (R)
   int R;
+  uint32_t groups;       // 2 * b * R * H_kv row-heads of K and V
+  FastDiv heads, rows;   // by H_kv and by R
 };
 
 // (sequence, row, head, K or V) of a thread group's item and its cache slot;
 // false where the row takes no part.
 struct Kv8Item {
-  int s, i, h, which;
-  long long slot;        // (s * H_kv + h) * T + position
-  __device__ __forceinline__ bool init(const Kv8Params& p, long long g) {
+  int which;
+  long long at;          // first element in the rows array
+  long long slot;        // (sequence * H_kv + head) * T + position
+  __device__ __forceinline__ bool init(const Kv8Params& p, uint32_t g) {
+    if (g >= p.groups) return false;
     which = (int)(g & 1);
-    g >>= 1;
-    h = (int)(g % p.c.H_kv);
-    g /= p.c.H_kv;
-    i = (int)(g % p.R);
-    g /= p.R;
-    if (g >= p.c.b) return false;
-    s = (int)g;
-    const int n = p.counts ? p.counts[s] : p.R;
-    if (i >= n) return false;
-    const long long pos = (long long)(p.starts ? p.starts[s] : 0) + i;
+    uint32_t h, i;
+    const uint32_t row = p.heads.divmod(g >> 1, h);
+    const uint32_t s = p.rows.divmod(row, i);
+    const int n = p.counts ? __ldg(p.counts + s) : p.R;
+    if ((int)i >= n) return false;
+    const long long pos = (long long)(p.starts ? __ldg(p.starts + s) : 0) + i;
     if (pos < 0 || pos >= p.c.T) return false;
     slot = ((long long)s * p.c.H_kv + h) * p.c.T + pos;
+    at = (long long)row * p.rs[which] + (long long)h * p.c.hd;
     return true;
   }
 };
 
-template <typename E, int HD>
-__global__ void __launch_bounds__(256) kv8_store_kernel(const __grid_constant__ Kv8Params p) {
-  constexpr int L = HD / 8;
-  const long long tid = (long long)blockIdx.x * 256 + threadIdx.x;
-  const int l = (int)(tid % L);
-  Kv8Item it;
-  const bool on = it.init(p, tid / L);
-  float x[8] = {};
-  if (on)
-    E::load8(static_cast<const typename E::T*>(p.in[it.which]) + ((long long)it.s * p.R + it.i) * p.rs[it.which] +
-                 (long long)it.h * HD + l * 8,
-             x);
-  uint32_t m = abs_bits8(x);
+// A block takes 256 / L * AHEAD consecutive row-heads, a thread group every
+// (256 / L)-th of them: all its loads are issued before the first is used.
+template <typename E, int HD, int AHEAD>
+__global__ void __launch_bounds__(256, 4) kv8_store_kernel(const __grid_constant__ Kv8Params p) {
+  constexpr int L = HD / 8, GROUPS = 256 / L;
+  const int l = threadIdx.x % L;
+  griddep_launch_dependents();
+  griddep_wait();
+  const uint32_t g0 = blockIdx.x * (uint32_t)(GROUPS * AHEAD) + threadIdx.x / L;
+  Kv8Item it[AHEAD];
+  bool on[AHEAD];
+  Raw8<E> raw[AHEAD];
 #pragma unroll
-  for (int d = L / 2; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-  if (!on) return;
-  const int byte = scale_byte(m);
-  uint2 codes = make_uint2(0, 0);
-  if (byte != kScaleNan) codes = encode8(x, scale_inverse(byte));
-  *reinterpret_cast<uint2*>((it.which ? p.c.v : p.c.k) + it.slot * HD + l * 8) = codes;
-  if (l == 0) (it.which ? p.c.v_scale : p.c.k_scale)[it.slot] = (uint8_t)byte;
+  for (int k = 0; k < AHEAD; ++k) on[k] = it[k].init(p, g0 + k * GROUPS);
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) {
+    raw[k].zero();
+    if (on[k]) raw[k].load(static_cast<const typename E::T*>(p.in[it[k].which]) + it[k].at + l * 8);
+  }
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) {
+    float x[8];
+    raw[k].floats(x);
+    uint32_t m = abs_bits8(x);
+#pragma unroll
+    for (int d = L / 2; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (!on[k]) continue;
+    const int byte = scale_byte(m);
+    uint2 codes = make_uint2(0, 0);
+    if (byte != kScaleNan) codes = encode8(x, scale_inverse(byte));
+    *reinterpret_cast<uint2*>((it[k].which ? p.c.v : p.c.k) + it[k].slot * HD + l * 8) = codes;
+    if (l == 0) (it[k].which ? p.c.v_scale : p.c.k_scale)[it[k].slot] = (uint8_t)byte;
+  }
 }
 
-template <typename E, int HD>
-__global__ void __launch_bounds__(256) kv8_load_kernel(const __grid_constant__ Kv8Params p) {
-  constexpr int L = HD / 8;
-  const long long tid = (long long)blockIdx.x * 256 + threadIdx.x;
-  const int l = (int)(tid % L);
-  Kv8Item it;
-  if (!it.init(p, tid / L)) return;
-  const uint2 codes = *reinterpret_cast<const uint2*>((it.which ? p.c.v : p.c.k) + it.slot * HD + l * 8);
-  float x[8];
-  decode8(codes, scale_value((it.which ? p.c.v_scale : p.c.k_scale)[it.slot]), x);
-  E::store8(static_cast<typename E::T*>(p.out[it.which]) + ((long long)it.s * p.R + it.i) * p.rs[it.which] +
-                (long long)it.h * HD + l * 8,
-            x);
+template <typename E, int HD, int AHEAD>
+__global__ void __launch_bounds__(256, 4) kv8_load_kernel(const __grid_constant__ Kv8Params p) {
+  constexpr int L = HD / 8, GROUPS = 256 / L;
+  const int l = threadIdx.x % L;
+  griddep_launch_dependents();
+  griddep_wait();
+  const uint32_t g0 = blockIdx.x * (uint32_t)(GROUPS * AHEAD) + threadIdx.x / L;
+  Kv8Item it[AHEAD];
+  bool on[AHEAD];
+  uint2 codes[AHEAD];
+  int byte[AHEAD];
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) on[k] = it[k].init(p, g0 + k * GROUPS);
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) {
+    codes[k] = make_uint2(0, 0);
+    byte[k] = 127;
+    if (on[k]) {
+      codes[k] = __ldg(reinterpret_cast<const uint2*>((it[k].which ? p.c.v : p.c.k) + it[k].slot * HD + l * 8));
+      byte[k] = __ldg((it[k].which ? p.c.v_scale : p.c.k_scale) + it[k].slot);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) {
+    if (!on[k]) continue;
+    float x[8];
+    decode8(codes[k], scale_value(byte[k]), x);
+    E::store8(static_cast<typename E::T*>(p.out[it[k].which]) + it[k].at + l * 8, x);
+  }
 }
 
 dllm_status kv8_check(const dllm_kv8* c, const char* who) {
@@ -94,20 +124,20 @@ dllm_status kv8_check(const dllm_kv8* c, const char* who) {
 
 namespace {
 
+template <typename E, int HD, int AHEAD>
+cudaError_t launch_kv8(const Kv8Params& p, bool store, cudaStream_t st) {
+  constexpr uint32_t per_block = 256 / (HD / 8) * AHEAD;
+  const dim3 grid((p.groups + per_block - 1) / per_block);
+  return store ? op_launch(kv8_store_kernel<E, HD, AHEAD>, grid, dim3(256), 0, st, 1, p)
+               : op_launch(kv8_load_kernel<E, HD, AHEAD>, grid, dim3(256), 0, st, 1, p);
+}
+
+// Four row-heads a thread group once that still leaves every SM two blocks.
 template <typename E>
-cudaError_t launch_kv8(const Kv8Params& p, bool store, unsigned grid, cudaStream_t st) {
-  if (store) {
-    if (p.c.hd == 64)
-      kv8_store_kernel<E, 64><<<grid, 256, 0, st>>>(p);
-    else
-      kv8_store_kernel<E, 128><<<grid, 256, 0, st>>>(p);
-  } else {
-    if (p.c.hd == 64)
-      kv8_load_kernel<E, 64><<<grid, 256, 0, st>>>(p);
-    else
-      kv8_load_kernel<E, 128><<<grid, 256, 0, st>>>(p);
-  }
-  return cudaGetLastError();
+cudaError_t launch_kv8(const Kv8Params& p, bool store, cudaStream_t st) {
+  const bool ahead = p.groups >= 2u * op_device_sms() * (256 / (p.c.hd / 8) * 4);
+  if (p.c.hd == 64) return ahead ? launch_kv8<E, 64, 4>(p, store, st) : launch_kv8<E, 64, 1>(p, store, st);
+  return ahead ? launch_kv8<E, 128, 4>(p, store, st) : launch_kv8<E, 128, 1>(p, store, st);
 }
 
 dllm_status kv8_rows(const dllm_kv8* cache, bool store, const void* k, const void* v, int64_t k_rs, int64_t v_rs,
@@ -135,14 +165,16 @@ dllm_status kv8_rows(const dllm_kv8* cache, bool store, const void* k, const voi
   p.counts = counts;
   p.R = R;
   const __int128 groups = (__int128)2 * cache->b * R * cache->H_kv;
-  const __int128 blocks = (groups * (cache->hd / 8) + 255) / 256;
-  if (blocks > 0x7fffffff)
+  if (groups > 0x7fffff00)
     return op_fail(DLLM_EINVAL, "%s: b=%d R=%d H_kv=%d are too many rows for one call", who, cache->b, R, cache->H_kv);
+  p.groups = (uint32_t)groups;
+  p.heads = FastDiv((uint32_t)cache->H_kv);
+  p.rows = FastDiv((uint32_t)R);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (dtype) {
-    case DLLM_F32: OP_CK(launch_kv8<ElemF32>(p, store, (unsigned)blocks, st)); break;
-    case DLLM_BF16: OP_CK(launch_kv8<ElemBf16>(p, store, (unsigned)blocks, st)); break;
-    default: OP_CK(launch_kv8<ElemF16>(p, store, (unsigned)blocks, st)); break;
+    case DLLM_F32: OP_CK(launch_kv8<ElemF32>(p, store, st)); break;
+    case DLLM_BF16: OP_CK(launch_kv8<ElemBf16>(p, store, st)); break;
+    default: OP_CK(launch_kv8<ElemF16>(p, store, st)); break;
   }
   return DLLM_OK;
 }

@@ -54,6 +54,26 @@ inline cudaError_t op_launch(Kern kernel, dim3 grid, dim3 block, size_t smem, cu
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Division of n < 2^31 by a launch constant d: a multiply and a shift in place of
+// the ~20 instructions of a 32-bit division (m = ceil(2^(31 + s) / d), 2^s >= d, is
+// exact for such n).
+struct FastDiv {
+  uint32_t d, m, s;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t div) : d(div), m(0), s(0) {
+    while ((1ull << s) < d) ++s;
+    m = (uint32_t)(((1ull << (31 + s)) + d - 1) / d);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return d == 1 ? n : __umulhi(n, m) >> (s - 1); }
+  __device__ __forceinline__ uint32_t divmod(uint32_t n, uint32_t& rem) const {
+    const uint32_t q = div(n);
+    rem = n - q * d;
+    return q;
+  }
+#endif
+};
+
 inline bool op_aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline int op_dtype_size(int32_t t) { return t == DLLM_F32 ? 4 : (t == DLLM_BF16 || t == DLLM_F16) ? 2 : 0; }
 

@@ -52,6 +52,22 @@ __device__ __forceinline__ float2 f16x2_to_f32(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// The same on packed halves: a in the low half.
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t cvt_e4m3x2_f16x2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_mul16_f16x2(uint32_t a, uint32_t b) {
+  const __half2 d = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b)),
+                            __floats2half2_rn(16.0f, 16.0f));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
 // Eight codes (one 8-byte word) of eight values times 2^-e.
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
   uint32_t p[4];
@@ -70,6 +86,23 @@ __device__ __forceinline__ void decode8(uint2 c, float scale, float (&x)[8]) {
 }
 
 // ------------------------------------------------------------ element types
+// Raw8<E>: the 16-byte words of 8 elements as loaded, so that several loads can
+// be in flight before the first is unpacked.
+template <typename E>
+struct Raw8 {
+  static constexpr int W = (int)sizeof(typename E::T) / 2;
+  uint4 w[W];
+  __device__ __forceinline__ void load(const typename E::T* p) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void floats(float (&x)[8]) const { E::load8(reinterpret_cast<const typename E::T*>(w), x); }
+};
+
 struct ElemF32 {
   using T = float;
   static __device__ __forceinline__ float get(const T* p) { return *p; }

@@ -10,11 +10,13 @@
 // floating point, whose rate is a 64th of 32-bit on this chip.
 //
 // Bound by HBM: one read and one write of x.  A thread owns 8 pairs of a row
-// (two 16-byte vectors of 16-bit elements) and walks kHeadRun heads with the
-// same cosines, so the trigonometry is paid once in kHeadRun heads.
+// (two 16-byte vectors of 16-bit elements) and walks up to 8 heads with the
+// same cosines, four heads' loads in flight.
+#include <algorithm>
 #include <cmath>
 
 #include "ops8.h"
+#include "ptx8.cuh"
 #include "q8.cuh"
 
 namespace dllm {
@@ -25,8 +27,10 @@ struct RopeParams {
   const void* x;
   void* out;
   const int32_t* pos;
-  long long rows, x_rs, x_hs, o_rs, o_hs;
-  int heads, hd, rot, interleaved, head_run;
+  long long x_rs, x_hs, o_rs, o_hs;
+  uint32_t items;
+  FastDiv units, runs;
+  int heads, rot, interleaved, head_run;
   float amp;
   uint64_t turns[kMaxPairs];   // turns per position * 2^64
 };
@@ -50,67 +54,89 @@ template <typename E, bool VEC>
 __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeParams p) {
   using T = typename E::T;
   constexpr int PAIRS = VEC ? 8 : 1;
-  const int units = p.hd / (2 * PAIRS);
-  const int runs = (p.heads + p.head_run - 1) / p.head_run;
-  const long long item = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (item >= p.rows * runs * units) return;
-  const int u = (int)(item % units);
-  const long long rr = item / units;
-  const int run = (int)(rr % runs);
-  const long long row = rr / runs;
-  const int h0 = run * p.head_run, h1 = min(p.heads, h0 + p.head_run);
+  constexpr int AHEAD = 4;                     // heads in flight
+  griddep_launch_dependents();
+  griddep_wait();
+  const uint32_t item = blockIdx.x * 256u + threadIdx.x;
+  if (item >= p.items) return;
+  uint32_t u, run;
+  const uint32_t row = p.runs.divmod(p.units.divmod(item, u), run);
+  const int h0 = (int)run * p.head_run, h1 = min(p.heads, h0 + p.head_run);
   const T* x = static_cast<const T*>(p.x) + row * p.x_rs;
   T* out = static_cast<T*>(p.out) + row * p.o_rs;
-  const int first = u * PAIRS;                 // pairs below rot / 2 turn, the rest is copied
+  const int first = (int)u * PAIRS;            // pairs below rot / 2 turn, the rest is copied
   const bool turns = first < p.rot / 2;
+  if (!turns && p.x == p.out) return;
   // elements a and b of the unit's first pair
   const int a = !turns || p.interleaved ? 2 * first : first;
   const int b = !turns || p.interleaved ? a + PAIRS : first + p.rot / 2;
+  float c[PAIRS], s[PAIRS];
+#pragma unroll
+  for (int i = 0; i < PAIRS; ++i) {
+    c[i] = 1.0f;
+    s[i] = 0.0f;
+  }
   if (turns) {
     const int pos = p.pos[row];
-    float c[PAIRS], s[PAIRS];
 #pragma unroll
     for (int i = 0; i < PAIRS; ++i) turn_cos_sin(p.turns[first + i], pos, p.amp, c[i], s[i]);
-    for (int h = h0; h < h1; ++h) {
-      const T* xh = x + h * p.x_hs;
-      T* oh = out + h * p.o_hs;
-      if constexpr (VEC) {
-        float v[2][8], w[2][8];
-        E::load8(xh + a, v[0]);
-        E::load8(xh + b, v[1]);
-        if (p.interleaved) {
+  }
+  for (int hb = h0; hb < h1; hb += AHEAD) {
+    if constexpr (VEC) {
+      constexpr int W = (int)sizeof(T) / 2;    // 16-byte words of 8 elements
+      uint4 raw[AHEAD][2][W];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float x0 = v[i >> 2][2 * (i & 3)], x1 = v[i >> 2][2 * (i & 3) + 1];
-            w[i >> 2][2 * (i & 3)] = x0 * c[i] - x1 * s[i];
-            w[i >> 2][2 * (i & 3) + 1] = x1 * c[i] + x0 * s[i];
-          }
-        } else {
+      for (int k = 0; k < AHEAD; ++k) {
+        if (hb + k >= h1) break;
+        const T* xh = x + (hb + k) * p.x_hs;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            w[0][i] = v[0][i] * c[i] - v[1][i] * s[i];
-            w[1][i] = v[1][i] * c[i] + v[0][i] * s[i];
-          }
+        for (int w = 0; w < W; ++w) {
+          raw[k][0][w] = reinterpret_cast<const uint4*>(xh + a)[w];
+          raw[k][1][w] = reinterpret_cast<const uint4*>(xh + b)[w];
         }
-        E::store8(oh + a, w[0]);
-        E::store8(oh + b, w[1]);
-      } else {
-        const float x0 = E::get(xh + a), x1 = E::get(xh + b);
-        E::put(oh + a, x0 * c[0] - x1 * s[0]);
-        E::put(oh + b, x1 * c[0] + x0 * s[0]);
       }
-    }
-  } else if (p.x != p.out) {
-    for (int h = h0; h < h1; ++h) {
-      const T* xh = x + h * p.x_hs;
-      T* oh = out + h * p.o_hs;
-      if constexpr (VEC) {
-        constexpr int N16 = 16 * (int)sizeof(T) / 16;
 #pragma unroll
-        for (int i = 0; i < N16; ++i) reinterpret_cast<uint4*>(oh + a)[i] = reinterpret_cast<const uint4*>(xh + a)[i];
-      } else {
-        oh[a] = xh[a];
-        oh[b] = xh[b];
+      for (int k = 0; k < AHEAD; ++k) {
+        if (hb + k >= h1) break;
+        T* oh = out + (hb + k) * p.o_hs;
+        if (turns) {
+          float v[2][8], r[2][8];
+          E::load8(reinterpret_cast<const T*>(raw[k][0]), v[0]);
+          E::load8(reinterpret_cast<const T*>(raw[k][1]), v[1]);
+          if (p.interleaved) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float x0 = v[i >> 2][2 * (i & 3)], x1 = v[i >> 2][2 * (i & 3) + 1];
+              r[i >> 2][2 * (i & 3)] = x0 * c[i] - x1 * s[i];
+              r[i >> 2][2 * (i & 3) + 1] = x1 * c[i] + x0 * s[i];
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              r[0][i] = v[0][i] * c[i] - v[1][i] * s[i];
+              r[1][i] = v[1][i] * c[i] + v[0][i] * s[i];
+            }
+          }
+          E::store8(reinterpret_cast<T*>(raw[k][0]), r[0]);
+          E::store8(reinterpret_cast<T*>(raw[k][1]), r[1]);
+        }
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          reinterpret_cast<uint4*>(oh + a)[w] = raw[k][0][w];
+          reinterpret_cast<uint4*>(oh + b)[w] = raw[k][1][w];
+        }
+      }
+    } else {
+      for (int h = hb; h < min(h1, hb + AHEAD); ++h) {
+        const T x0 = x[h * p.x_hs + a], x1 = x[h * p.x_hs + b];
+        T r0 = x0, r1 = x1;                    // the copied part keeps its bits
+        if (turns) {
+          const float f0 = E::get(&x0), f1 = E::get(&x1);
+          E::put(&r0, f0 * c[0] - f1 * s[0]);
+          E::put(&r1, f1 * c[0] + f0 * s[0]);
+        }
+        out[h * p.o_hs + a] = r0;
+        out[h * p.o_hs + b] = r1;
       }
     }
   }
@@ -125,13 +151,10 @@ bool strides_ok(long long rows, long long heads, long long hd, long long rs, lon
 }
 
 template <typename E>
-cudaError_t launch_rope(const RopeParams& p, bool vec, long long items, cudaStream_t st) {
-  const unsigned grid = (unsigned)((items + 255) / 256);
-  if (vec)
-    rope_kernel<E, true><<<grid, 256, 0, st>>>(p);
-  else
-    rope_kernel<E, false><<<grid, 256, 0, st>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_rope(const RopeParams& p, bool vec, cudaStream_t st) {
+  const dim3 grid((p.items + 255) / 256);
+  return vec ? op_launch(rope_kernel<E, true>, grid, dim3(256), 0, st, 1, p)
+             : op_launch(rope_kernel<E, false>, grid, dim3(256), 0, st, 1, p);
 }
 
 }  // namespace
@@ -173,9 +196,7 @@ extern "C" dllm_status dllm_op_rope(const void* x, void* out, const int32_t* pos
   p.x = x;
   p.out = out;
   p.pos = positions;
-  p.rows = rows;
   p.heads = heads;
-  p.hd = hd;
   p.rot = r->rot_dim;
   p.interleaved = r->layout == DLLM_ROPE_INTERLEAVED;
   p.x_hs = x_head_stride ? x_head_stride : hd;
@@ -199,14 +220,19 @@ extern "C" dllm_status dllm_op_rope(const void* x, void* out, const int32_t* pos
     amp = 0.1 * std::log(r->factor) + 1.0;
   }
   p.amp = (float)(r->amplitude > 0.0 ? r->amplitude : amp);
+  // theta^(-2i/rot) as the product of a power for i's upper and one for its lower
+  // three bits: 24 powers at most in place of 128 (each is most of the call's host time)
+  double lower[8], upper = 1.0;
+  for (int i = 0; i < std::min(pairs, 8); ++i) lower[i] = std::pow(theta, -2.0 * i / p.rot);
   for (int i = 0; i < pairs; ++i) {
-    double f = std::pow(theta, -2.0 * i / p.rot);
+    if (i % 8 == 0) upper = std::pow(theta, -2.0 * i / p.rot);
+    double f = upper * lower[i % 8];
     if (r->scaling == DLLM_ROPE_LINEAR) f /= r->factor;
     if (r->scaling == DLLM_ROPE_BY_PARTS) {
       const double ramp = std::fmin(1.0, std::fmax(0.0, (i - lo) / std::fmax(hi - lo, 0.001)));
       f = f / r->factor * ramp + f * (1.0 - ramp);
     }
-    // f <= 1, so the turns per position are at most 0.16: 2^64 of them fit
+    // f <= 1 (a rounding above it at most), so the turns per position stay under 0.16: 2^64 of them fit
     p.turns[i] = (uint64_t)(f * 0.15915494309189533577 * 0x1p64);
   }
 
@@ -215,15 +241,24 @@ extern "C" dllm_status dllm_op_rope(const void* x, void* out, const int32_t* pos
   const int v16 = 16 / es;
   const bool vec = hd % 16 == 0 && p.rot % 16 == 0 && op_aligned(x, 16) && op_aligned(out, 16) && p.x_rs % v16 == 0 &&
                    p.x_hs % v16 == 0 && p.o_rs % v16 == 0 && p.o_hs % v16 == 0;
-  p.head_run = 1;
+  // Heads a thread walks: as many, up to 8, as leave half the GPU's threads an
+  // item (8191 rows of 40 heads: 8 heads 34 us, 1 head 63 us; 32 rows of 64 heads
+  // take 1).
   const long long units = hd / (vec ? 16 : 2);
-  const long long items = (long long)rows * heads * units;
-  if ((items + 255) / 256 > 0x7fffffffLL) return op_fail(DLLM_EINVAL, "rope: %d rows of %d heads are too many", rows, heads);
+  p.head_run = 8;
+  while (p.head_run > 1 && (long long)rows * units * ((heads + p.head_run - 1) / p.head_run) < 1024LL * op_device_sms())
+    p.head_run /= 2;
+  const long long runs = (heads + p.head_run - 1) / p.head_run;
+  const __int128 items = (__int128)rows * units * runs;
+  if (items > 0x7fffff00) return op_fail(DLLM_EINVAL, "rope: %d rows of %d heads are too many for one call", rows, heads);
+  p.items = (uint32_t)items;
+  p.units = FastDiv((uint32_t)units);
+  p.runs = FastDiv((uint32_t)runs);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (dtype) {
-    case DLLM_F32: OP_CK(launch_rope<ElemF32>(p, vec, items, st)); break;
-    case DLLM_BF16: OP_CK(launch_rope<ElemBf16>(p, vec, items, st)); break;
-    default: OP_CK(launch_rope<ElemF16>(p, vec, items, st)); break;
+    case DLLM_F32: OP_CK(launch_rope<ElemF32>(p, vec, st)); break;
+    case DLLM_BF16: OP_CK(launch_rope<ElemBf16>(p, vec, st)); break;
+    default: OP_CK(launch_rope<ElemF16>(p, vec, st)); break;
   }
   return DLLM_OK;
 }
