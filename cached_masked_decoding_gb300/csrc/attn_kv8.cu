@@ -53,7 +53,7 @@ cudaError_t launch_attn_tiles(const CUtensorMap& tk, const CUtensorMap& tv, cons
   using C = AttnTilesCfg<HD>;
   const cudaError_t e = op_smem_once(reinterpret_cast<const void*>(attn_kv8_tiles_kernel<HD>), C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  return op_launch(attn_kv8_tiles_kernel<HD>, dim3(grid), dim3(224), C::SMEM_BYTES, st, 1, tk, tv, p);
+  return op_launch(attn_kv8_tiles_kernel<HD>, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, st, 1, tk, tv, p);
 }
 
 template <int HD>
@@ -111,6 +111,7 @@ extern "C" dllm_status dllm_op_attention_kv8(const uint16_t* q, int64_t q_row_st
   p.H = H;
   p.R = R;
   p.group = H / cache->H_kv;
+  p.by_group = FastDiv((uint32_t)p.group);
   p.scale_log2 = scale * 1.4426950408889634f;
   int64_t need = 0;
   if (const dllm_status s = dllm_op_attention_kv8_workspace(cache->b, H, cache->H_kv, cache->hd, R, cache->T, &need);

@@ -49,6 +49,7 @@ struct AttnKv8Params {
   const int32_t* limits;
   long long q_rs, o_rs;
   int H, R, group;        // group = H / H_kv query heads share a cached head
+  FastDiv by_group;
   int rows, row_tiles;    // R * group rows of an item, in tiles of N
   int splits;
   float scale_log2;
@@ -101,6 +102,60 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 constexpr float kRefSlack = 40.0f;   // log2 a score or a value scale may exceed its reference by
+
+// The query tile, rows rt * N .. of the item, by THREADS threads (a multiple of
+// 32): hi codes to q_hi, lo codes to q_lo from row lo0 on, and a word of the row's
+// scale byte to the 512-byte atom sf (prefilled with 1.0) for both.  Rows from
+// n_rows on are zeros.  BATCH rows a thread are loaded before the first is
+// used: one at a time, 128 rows took 13 us of load latency.
+template <int HD, int N, int THREADS>
+__device__ __forceinline__ void attn_query_tile(const AttnKv8Params& p, int seq, int g, int rt, int n_rows, int tid,
+                                                uint8_t* q_hi, uint8_t* q_lo, int lo0, uint32_t* sf) {
+  constexpr int L = HD / 8, PASS = THREADS / L;           // lanes of a row, rows a pass
+  constexpr int BATCH = (N + PASS - 1) / PASS < 8 ? (N + PASS - 1) / PASS : 8;
+  const int l = tid % L;
+#pragma unroll 1
+  for (int n0 = tid / L; n0 < N + tid / L; n0 += PASS * BATCH) {   // every thread makes the same trips
+    Raw8<ElemBf16> raw[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int n = n0 + k * PASS;
+      raw[k].zero();
+      if (n < n_rows) {
+        uint32_t j;
+        const uint32_t i = p.by_group.divmod((uint32_t)(rt * N + n), j);
+        raw[k].load(reinterpret_cast<const __nv_bfloat16*>(p.q) + ((long long)seq * p.R + i) * p.q_rs +
+                    (long long)(g * p.group + (int)j) * HD + l * 8);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int n = n0 + k * PASS;
+      float x[8], b[8];
+      raw[k].floats(x);
+      uint32_t m = abs_bits8(x);
+#pragma unroll
+      for (int d = L / 2; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+      if (n >= N) continue;
+      const int byte = scale_byte(m);
+      const float inv = byte == kScaleNan ? __uint_as_float(0x7fffffffu) : scale_inverse(byte);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] *= inv;            // a row that is not finite becomes NaN
+      const uint2 hi = encode8(x, 1.0f);
+      decode8(hi, 1.0f, b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) b[e] = x[e] - b[e];
+      const uint2 lo = encode8(b, 1.0f);
+      *reinterpret_cast<uint2*>(q_hi + swizzled<HD>(n, l >> 1) + (l & 1) * 8) = hi;
+      *reinterpret_cast<uint2*>(q_lo + swizzled<HD>(n + lo0, l >> 1) + (l & 1) * 8) = lo;
+      if (l == 0 && byte != kScaleNan) {
+        const uint32_t word = (uint32_t)byte * 0x01010101u;
+        sf[(n & 31) * 4 + (n >> 5)] = word;
+        if (lo0) sf[((n + lo0) & 31) * 4 + ((n + lo0) >> 5)] = word;
+      }
+    }
+  }
+}
 
 template <int HD, int N>
 __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N>::CTAS)
@@ -165,7 +220,7 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
   // limits of the tile's rows; rows past the last see what row 0 sees and are not stored
   if (threadIdx.x < N) {
     const int n = (int)threadIdx.x < n_rows ? (int)threadIdx.x : 0;
-    const int i = (rt * N + n) / p.group;
+    const int i = (int)p.by_group.div((uint32_t)(rt * N + n));
     const int lim = p.limits ? p.limits[(long long)seq * p.R + i] : p.c.T;
     s_lim[threadIdx.x] = min(max(lim, 0), p.c.T);
   }
@@ -302,47 +357,15 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
     fetch(0);
     if (nt > 0) {
       // ---------------------------------------------------- the query tile
-      constexpr int L = HD / 8;                           // lanes of a row
       if (tid < 128) {
 #pragma unroll
         for (int f = 0; f < 4; ++f) reinterpret_cast<uint32_t*>(sSF + f * C::SF_BYTES)[tid] = 0x7f7f7f7fu;
       }
       if (tid < N) s_m[tid] = 0.0f;
       named_bar_sync(2, C::SOFT);
-#pragma unroll 1
-      for (int n0 = 0; n0 < N; n0 += C::SOFT / L) {
-        const int n = n0 + tid / L, l = tid % L;
-        float x[8] = {};
-        if (n < n_rows) {
-          const int rn = rt * N + n, i = rn / p.group, h = g * p.group + rn % p.group;
-          ElemBf16::load8(reinterpret_cast<const __nv_bfloat16*>(p.q) + ((long long)seq * p.R + i) * p.q_rs +
-                              (long long)h * HD + l * 8,
-                          x);
-        }
-        uint32_t m = abs_bits8(x);
-#pragma unroll
-        for (int d = L / 2; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-        if (n < N) {
-          const int byte = scale_byte(m);
-          const float inv = byte == kScaleNan ? __uint_as_float(0x7fffffffu) : scale_inverse(byte);
-          float r[8], b[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) r[e] = x[e] * inv;  // a row that is not finite becomes NaN
-          const uint2 hi = encode8(r, 1.0f);
-          decode8(hi, 1.0f, b);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) b[e] = r[e] - b[e];
-          const uint2 lo = encode8(b, 1.0f);
-          const int nl = C::Q_PARTS == 1 ? n + N : n;     // the lo row, in its own operand or behind the hi rows
-          *reinterpret_cast<uint2*>(sQ + swizzled<HD>(n, l >> 1) + (l & 1) * 8) = hi;
-          *reinterpret_cast<uint2*>(sQ + (C::Q_PARTS - 1) * C::Q_BYTES + swizzled<HD>(nl, l >> 1) + (l & 1) * 8) = lo;
-          if (l == 0 && byte != kScaleNan) {
-            uint32_t* sf = reinterpret_cast<uint32_t*>(sSF + C::SF_BYTES);
-            sf[(n & 31) * 4 + (n >> 5)] = (uint32_t)byte * 0x01010101u;
-            sf[(nl & 31) * 4 + (nl >> 5)] = (uint32_t)byte * 0x01010101u;
-          }
-        }
-      }
+      // 8 rows: the lo rows lie behind the hi rows of one operand
+      attn_query_tile<HD, N, C::SOFT>(p, seq, g, rt, n_rows, tid, sQ, sQ + (C::Q_PARTS - 1) * C::Q_BYTES,
+                                      C::Q_PARTS == 1 ? N : 0, reinterpret_cast<uint32_t*>(sSF + C::SF_BYTES));
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(qready);

@@ -1,22 +1,32 @@
 // Attention over the 8-bit cache for many query rows a cached head (a prefill
 // over its own cache): 128 rows a CTA, one a softmax thread.
 //
-//   S[row][key] = Q K^T      kind::mxf8f6f4; q as hi + lo codes (two products), the
-//                            row's and the key's scales applied by the MMA
-//   O[row][dim] += P V       kind::mxf8f6f4; P as hi + lo codes in tensor memory, each
-//                            with a scale for a row's 32 keys; V MN-major from its TMA tile
-// The codes of K and V are used as they lie in the cache; precision of q and P as in
-// attn_kv8_rows.cuh.  Two e4m3 products cost what one bf16 product costs, so a
-// tile of 128 rows by 128 keys takes the tensor cores 1024 cycles; the softmax
-// needs about as many issue slots (10 a score over four schedulers), so two
-// CTAs share an SM and one's products run under the other's exponentials.
-// Tensor memory sets the tile: 64 keys make S 64 columns, P 32, O 128 and the
-// scales 20, just under half of it.
+//   S[row][key] = Q K^T      kind::mxf8f6f4 on the cache's codes; q as hi + lo codes (two
+//                            products, see attn_kv8_rows.cuh), the row's and the
+//                            key's scales applied by the MMA
+//   O[row][dim] += P V       kind::f16; P in tensor memory, V as halves
+// V's codes become halves in shared memory, code * 2^(ev - vref), exact down to
+// 2^-24 where the largest row of the tiles so far has values up to 448 (2^-33 of
+// it); vref follows the largest exponent.  P is a half too, 2^7 p: 11 bits down to
+// 2^-21 of the row's reference.  Where a tile's value exponents reach more than 2^10
+// below vref (a loud value may then count although its p is far below 2^-21), the
+// codes stay unscaled from there on, p takes the factor 2^(ev - vref) in 32 bits, and
+// the products get a reference of their own.  With P as two e4m3 codes and V untouched, as
+// for few rows, the softmax needed 16 instructions a score and a causal prefill
+// of 4096 rows 259 us; converting 64 V rows costs 1.5 a code, shared by 128
+// query rows, and leaves the softmax about 4.
 //
-//   warp 0     TMA: K and V tiles of 64 keys
+// A tile of 128 rows by 128 keys takes the tensor cores 1024 cycles (two e4m3
+// products cost what one product of halves costs); two CTAs share an SM, so that
+// one's products run under the other's exponentials.  Tensor memory sets the
+// tile: 64 keys make S 64 columns, P 32, O 128 and the scales 12, just under half.
+//
+//   warp 0     TMA: K and V tiles of 64 keys, a ring each
 //   warp 1     one thread issues scale copies and MMAs
-//   warp 2     scale bytes: K's for the MMA, V's as factors of P
-//   warps 3-6  softmax, one row a thread; the query tile before, the output after
+//   warp 2     scale bytes: K's for the MMA, V's as factors
+//   warps 4-7  softmax, one row a thread; the query tile before, the output after
+//   warps 8-11 V to halves, 16 keys each (two warps, the scales among their work,
+//              were the longest stage: 2600 cycles a tile against 1300 of softmax)
 #pragma once
 
 #include "attn_kv8_rows.cuh"
@@ -27,46 +37,60 @@ template <int HD>
 struct AttnTilesCfg {
   static constexpr int N = 128;                         // rows
   static constexpr int KT = 64;
+  static constexpr int THREADS = 384;
+  // registers: the launch's 80 a thread (3 warpgroups) shared out anew, 136 + 48 + 56 = 3 * 80
+  static constexpr int REGS_SOFT = 136, REGS_CONV = 48, REGS_REST = 56;
   static constexpr int SLOT = KT * HD;
-  static constexpr int SLOTS = 6;
+  static constexpr int KS = 3, VS = 2;                  // slots of the two rings
   static constexpr int Q_BYTES = N * HD;                // hi or lo
-  static constexpr int SF_BYTES = 512;                  // ones, query, two of K, P
-  static constexpr int STAT_FLOATS = 2 * KT + 4 + N;    // value factors and block exponents (two buffers), limits
+  static constexpr int V_BYTES = KT * HD * 2;           // V as halves: 64 dims a 128-byte row
+  static constexpr int SF_BYTES = 512;                  // query, two of K
   static constexpr int SMEM_BYTES =
-      1024 + SLOTS * SLOT + 2 * Q_BYTES + 5 * SF_BYTES + STAT_FLOATS * 4 + (2 * SLOTS + 10) * 8 + 16;
+      1024 + (KS + VS) * SLOT + 2 * Q_BYTES + 2 * V_BYTES + 3 * SF_BYTES + (4 + 4 * KT + N) * 4 + (2 * (KS + VS) + 12) * 8 + 16;
   static constexpr int S_COL = 0;
-  static constexpr int P_COL = KT;                      // 16 columns of hi codes, 16 of lo
-  static constexpr int O_COL = P_COL + 32;
-  static constexpr int SF_ONE = O_COL + HD, SF_Q = SF_ONE + 4, SF_K = SF_Q + 4, SF_P = SF_K + 8;
+  static constexpr int P_COL = KT;                      // two halves a column
+  static constexpr int O_COL = P_COL + KT / 2;
+  static constexpr int SF_Q = O_COL + HD, SF_K = SF_Q + 4;
   static constexpr int TMEM_COLS = 256;
-  static_assert(SF_P + 4 <= TMEM_COLS, "tensor memory");
+  static_assert(SF_K + 8 <= TMEM_COLS, "tensor memory");
   static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs an SM");
 };
 
+constexpr float kPShift = 7.0f;    // P is held as 2^7 p, p up to 2^kRowSlack: under a half's 65504
+constexpr float kRowSlack = 8.0f;  // log2 a score may exceed its row's reference by
+constexpr int kVSpread = 10;       // log2 of the value scales' spread that halves of V and P cover
+constexpr int kVSlack = 6;         // and a value exponent the common one: 448 * 2^6 is under 65504
+
 template <int HD>
-__global__ void __launch_bounds__(224, 2)
+__global__ void __launch_bounds__(384, 2)
     attn_kv8_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                           const __grid_constant__ AttnKv8Params p) {
   using C = AttnTilesCfg<HD>;
   constexpr int KT = C::KT, N = C::N;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sKV = smem;
-  uint8_t* sQ = sKV + C::SLOTS * C::SLOT;               // hi, lo
-  uint8_t* sSF = sQ + 2 * C::Q_BYTES;                   // scale atoms: ones, queries, K (two), P
-  float* s_vf = reinterpret_cast<float*>(sSF + 5 * C::SF_BYTES);   // [2][KT]
-  int* s_eb = reinterpret_cast<int*>(s_vf + 2 * KT);    // [2][2]
-  int* s_lim = s_eb + 4;                                // [N]
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_lim + N);
-  uint64_t* empty = full + C::SLOTS;
-  uint64_t* qready = empty + C::SLOTS;
+  uint8_t* sK = smem;
+  uint8_t* sV = sK + C::KS * C::SLOT;
+  uint8_t* sQ = sV + C::VS * C::SLOT;                   // hi, lo
+  uint8_t* sH = sQ + 2 * C::Q_BYTES;                    // [2] V as halves
+  uint8_t* sSF = sH + 2 * C::V_BYTES;                   // scale atoms: queries, K (two)
+  int* s_vref = reinterpret_cast<int*>(sSF + 3 * C::SF_BYTES);   // [2]
+  int* s_wide = s_vref + 2;                             // [2] value scales far apart
+  float* s_vf = reinterpret_cast<float*>(s_wide + 2);   // [2][KT] factors of P then
+  float* s_hf = s_vf + 2 * KT;                          // [2][KT] factors of V's halves
+  int* s_lim = reinterpret_cast<int*>(s_hf + 2 * KT);   // [N]
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(s_lim + N);
+  uint64_t* kempty = kfull + C::KS;
+  uint64_t* vfull = kempty + C::KS;
+  uint64_t* vempty = vfull + C::VS;
+  uint64_t* qready = vempty + C::VS;
   uint64_t* sfull = qready + 1;                         // S of a tile is there
   uint64_t* sfree = sfull + 1;                          // and has been read
   uint64_t* kready = sfree + 1;                         // [2] a tile's scales are there
-  uint64_t* pready = kready + 2;                        // [2] its P
-  uint64_t* pvdone = pready + 2;                        // its product
-  uint64_t* vfixed = pvdone + 1;                        // the last tile's values past every limit are cleared
-  uint64_t* mdone = vfixed + 1;
+  uint64_t* vready = kready + 2;                        // [2] its V as halves
+  uint64_t* pready = vready + 2;                        // [2] its P
+  uint64_t* pvdone = pready + 2;                        // [2] its product
+  uint64_t* mdone = pvdone + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdone + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* err = g_attn_kv8_err;
@@ -81,19 +105,23 @@ __global__ void __launch_bounds__(224, 2)
   const int n_rows = min(N, p.rows - rt * N);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::SLOTS; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+    for (int s = 0; s < C::KS; ++s) {
+      mbar_init(&kfull[s], 1);
+      mbar_init(&kempty[s], 1);
+    }
+    for (int s = 0; s < C::VS; ++s) {
+      mbar_init(&vfull[s], 1);
+      mbar_init(&vempty[s], 4);
     }
     mbar_init(qready, 4);
     mbar_init(sfull, 1);
     mbar_init(sfree, 4);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&kready[s], 1);
+      mbar_init(&vready[s], 4);
       mbar_init(&pready[s], 4);
+      mbar_init(&pvdone[s], 1);
     }
-    mbar_init(pvdone, 1);
-    mbar_init(vfixed, 1);
     mbar_init(mdone, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -108,11 +136,11 @@ __global__ void __launch_bounds__(224, 2)
   griddep_wait();
   if (threadIdx.x < N) {
     const int n = (int)threadIdx.x < n_rows ? (int)threadIdx.x : 0;
-    const int i = (rt * N + n) / p.group;
+    const int i = (int)p.by_group.div((uint32_t)(rt * N + n));
     const int lim = p.limits ? p.limits[(long long)seq * p.R + i] : p.c.T;
     s_lim[threadIdx.x] = min(max(lim, 0), p.c.T);
 #pragma unroll
-    for (int f = 0; f < 5; ++f) reinterpret_cast<uint32_t*>(sSF + f * C::SF_BYTES)[threadIdx.x] = 0x7f7f7f7fu;   // 1.0
+    for (int f = 0; f < 3; ++f) reinterpret_cast<uint32_t*>(sSF + f * C::SF_BYTES)[threadIdx.x] = 0x7f7f7f7fu;   // 1.0
   }
   tc_fence_before();
   __syncthreads();
@@ -133,198 +161,214 @@ __global__ void __launch_bounds__(224, 2)
   const int t0 = (int)((long long)tiles * split / p.splits), t1 = (int)((long long)tiles * (split + 1) / p.splits);
   const int nt = t1 - t0;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      const uint64_t pol = policy_evict_last();           // the other row tiles read the same keys
-      RingPos r{0, 0u};
-      int issued = 0;
-      for (int u = 0; u < 2 * nt; ++u) {
-        if (u >= C::SLOTS && !mbar_wait(&empty[r.s], r.par ^ 1u, abort_flag, err, ERR_ATTN_FULL)) break;
-        mbar_arrive_expect_tx(&full[r.s], C::SLOT);
-        tma_load_3d(sKV + r.s * C::SLOT, (u & 1) ? &tmV : &tmK, &full[r.s], 0, (t0 + (u >> 1)) * KT, plane, pol);
-        r.next(C::SLOTS);
-        issued = u + 1;
+  if (warp < 4) {
+    setmaxnreg_dec<C::REGS_REST>();   // takes a whole warpgroup: warp 3 has no other part
+    if (warp == 0) {
+      if (lane == 0) {
+        const uint64_t pol = policy_evict_last();           // the other row tiles read the same keys
+        RingPos rk{0, 0u}, rv{0, 0u};
+        int k_issued = 0, v_issued = 0;
+        for (int t = 0; t < nt; ++t) {
+          if (t >= C::KS && !mbar_wait(&kempty[rk.s], rk.par ^ 1u, abort_flag, err, ERR_ATTN_FULL)) break;
+          mbar_arrive_expect_tx(&kfull[rk.s], C::SLOT);
+          tma_load_3d(sK + rk.s * C::SLOT, &tmK, &kfull[rk.s], 0, (t0 + t) * KT, plane, pol);
+          rk.next(C::KS);
+          k_issued = t + 1;
+          if (t >= C::VS && !mbar_wait(&vempty[rv.s], rv.par ^ 1u, abort_flag, err, ERR_ATTN_FULL)) break;
+          mbar_arrive_expect_tx(&vfull[rv.s], C::SLOT);
+          tma_load_3d(sV + rv.s * C::SLOT, &tmV, &vfull[rv.s], 0, (t0 + t) * KT, plane, pol);
+          rv.next(C::VS);
+          v_issued = t + 1;
+        }
+        if (*abort_flag) {   // let copies in flight land before the CTA's shared memory goes away
+          for (int t = max(k_issued - C::KS, 0); t < k_issued; ++t)
+            mbar_wait(&kfull[t % C::KS], (uint32_t)(t / C::KS) & 1u, nullptr, err, ERR_ATTN_FULL);
+          for (int t = max(v_issued - C::VS, 0); t < v_issued; ++t)
+            mbar_wait(&vfull[t % C::VS], (uint32_t)(t / C::VS) & 1u, nullptr, err, ERR_ATTN_FULL);
+        }
       }
-      if (*abort_flag)   // let copies in flight land before the CTA's shared memory goes away
-        for (int u = issued > C::SLOTS ? issued - C::SLOTS : 0; u < issued; ++u)
-          mbar_wait(&full[u % C::SLOTS], (uint32_t)(u / C::SLOTS) & 1u, nullptr, err, ERR_ATTN_FULL);
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && nt > 0 && mbar_wait(qready, 0u, abort_flag, err, ERR_ATTN_FULL)) {
-      tc_fence_after();
-      constexpr uint32_t idesc_s = idesc_mxf8(128, KT);
-      constexpr uint32_t idesc_o = idesc_mxf8(128, HD) | (1u << 16);   // V MN-major
-      const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV), f0 = smem_u32(sSF);
-      tmem_cp_scales(tmem + C::SF_ONE, sdesc_scales(f0));
-      tmem_cp_scales(tmem + C::SF_Q, sdesc_scales(f0 + C::SF_BYTES));
-      auto wait = [&](uint64_t* bar, uint32_t par) { return mbar_wait(bar, par, abort_flag, err, ERR_ATTN_FULL); };
-      auto issue_s = [&](int t) {
-        const int u = 2 * t, slot = u % C::SLOTS, b = t & 1;
-        if ((t > 0 && !wait(sfree, (uint32_t)(t - 1) & 1u)) || !wait(&full[slot], (uint32_t)(u / C::SLOTS) & 1u) ||
-            !wait(&kready[b], (uint32_t)(t >> 1) & 1u))
-          return false;
+    } else if (warp == 1) {
+      if (lane == 0 && nt > 0 && mbar_wait(qready, 0u, abort_flag, err, ERR_ATTN_FULL)) {
         tc_fence_after();
-        const uint32_t k = kv0 + slot * C::SLOT, sfk = tmem + C::SF_K + 4 * b;
-        tmem_cp_scales(sfk, sdesc_scales(f0 + (2 + b) * C::SF_BYTES));
+        constexpr uint32_t idesc_s = idesc_mxf8(128, KT);
+        // f16 operands (type 0), f32 accumulator, V MN-major
+        constexpr uint32_t idesc_o = (1u << 4) | (1u << 16) | ((uint32_t)(HD >> 3) << 17) | (8u << 24);
+        const uint32_t q0 = smem_u32(sQ), k0 = smem_u32(sK), h0 = smem_u32(sH), f0 = smem_u32(sSF);
+        tmem_cp_scales(tmem + C::SF_Q, sdesc_scales(f0));
+        auto wait = [&](uint64_t* bar, int phase) {
+          return mbar_wait(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL);
+        };
+        auto issue_s = [&](int t) {
+          const int slot = t % C::KS, b = t & 1;
+          if ((t > 0 && !wait(sfree, t - 1)) || !wait(&kfull[slot], t / C::KS) || !wait(&kready[b], t >> 1)) return false;
+          tc_fence_after();
+          const uint32_t k = k0 + slot * C::SLOT, sfk = tmem + C::SF_K + 4 * b;
+          tmem_cp_scales(sfk, sdesc_scales(f0 + (1 + b) * C::SF_BYTES));
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+          for (int part = 0; part < 2; ++part)
 #pragma unroll
-          for (int kk = 0; kk < HD / 32; ++kk)
-            mma_mxf8_ss(tmem + C::S_COL, sdesc_rows<HD>(q0 + part * C::Q_BYTES + kk * 32), sdesc_rows<HD>(k + kk * 32),
-                        idesc_s, tmem + C::SF_Q, sfk, (part > 0 || kk > 0) ? 1u : 0u);
-        mma_commit(&empty[slot]);
-        mma_commit(sfull);
-        return true;
+            for (int kk = 0; kk < HD / 32; ++kk)
+              mma_mxf8_ss(tmem + C::S_COL, sdesc_rows<HD>(q0 + part * C::Q_BYTES + kk * 32), sdesc_rows<HD>(k + kk * 32),
+                          idesc_s, tmem + C::SF_Q, sfk, (part > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&kempty[slot]);
+          mma_commit(sfull);
+          return true;
+        };
+        bool ok = issue_s(0);
+        for (int t = 0; t < nt && ok; ++t) {
+          const int b = t & 1;
+          // the next tile's scores as soon as these have been read
+          if (t + 1 < nt && !(ok = issue_s(t + 1))) break;
+          if (!(ok = wait(&vready[b], t >> 1) && wait(&pready[b], t >> 1))) break;
+          tc_fence_after();
+          const uint32_t v = h0 + b * C::V_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < KT / 16; ++kk)
+            mma_bf16_ts(tmem + C::O_COL, tmem + C::P_COL + kk * 8, sdesc_rows<128>(v + kk * 2048, KT * 128), idesc_o,
+                        (t > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&pvdone[b]);
+        }
+        mma_commit(mdone);
+        mbar_wait(mdone, 0u, nullptr, err, ERR_ATTN_FULL);
+      }
+    } else if (warp == 2) {
+      // ------------------------------------------------------ scales, keys lane and lane + 32 of a tile
+      const uint8_t* ksc = p.c.k_scale + (long long)plane * p.c.T;
+      const uint8_t* vsc = p.c.v_scale + (long long)plane * p.c.T;
+      // bytes in four tiles, and of the next four in flight (256: past every limit)
+      uint64_t kb4[2] = {}, vb4[2] = {};
+      int kn[4][2], vn[4][2];
+      auto fetch = [&](int t) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int key = (t0 + t + e) * KT + 32 * j + lane;
+            const bool in = t + e < nt && key < lim_max;
+            kn[e][j] = in ? __ldg(ksc + key) : 127;
+            vn[e][j] = in ? __ldg(vsc + key) : 256;
+          }
       };
-      bool ok = issue_s(0);
-      for (int t = 0; t < nt && ok; ++t) {
-        // the next tile's scores as soon as these have been read
-        if (t + 1 < nt && !(ok = issue_s(t + 1))) break;
-        const int u = 2 * t + 1, slot = u % C::SLOTS;
-        if (!(ok = wait(&pready[t & 1], (uint32_t)(t >> 1) & 1u) && wait(&full[slot], (uint32_t)(u / C::SLOTS) & 1u)))
-          break;
-        if ((t0 + t + 1) * KT > lim_max && !(ok = wait(vfixed, 0u))) break;
-        tc_fence_after();
-        const uint32_t v = kv0 + slot * C::SLOT;
-        tmem_cp_scales(tmem + C::SF_P, sdesc_scales(f0 + 4 * C::SF_BYTES));
+      if (nt > 0) fetch(0);
+      bool ok = true;
+      int vref = -127;
+      bool wide = false;
+      auto wait = [&](uint64_t* bar, int phase) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
+      };
+#pragma unroll 1
+      for (int t = 0; t < nt; ++t) {
+        const int b = t & 1;
+        if ((t & 3) == 0) {
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int kk = 0; kk < KT / 32; ++kk)
-            // P's scale bytes of a row: hi of the first 32 keys, hi of the second, lo, lo
-            mma_mxf8_ts(tmem + C::O_COL, tmem + C::P_COL + part * 16 + kk * 8, sdesc_rows<HD>(v + kk * 32 * HD),
-                        idesc_o | ((uint32_t)(2 * part + kk) << 29), tmem + C::SF_P, tmem + C::SF_ONE,
-                        (t > 0 || part > 0 || kk > 0) ? 1u : 0u);
-        mma_commit(&empty[slot]);
-        mma_commit(pvdone);
-      }
-      mma_commit(mdone);
-      mbar_wait(mdone, 0u, nullptr, err, ERR_ATTN_FULL);
-    }
-  } else if (warp == 2) {
-    // ------------------------------------------------------ scale bytes, keys lane and lane + 32 of a tile
-    const uint8_t* ksc = p.c.k_scale + (long long)plane * p.c.T;
-    const uint8_t* vsc = p.c.v_scale + (long long)plane * p.c.T;
-    constexpr int AHEAD = 4;
-    int kn[AHEAD][2], vn[AHEAD][2];
-    auto fetch = [&](int t) {
-#pragma unroll
-      for (int e = 0; e < AHEAD; ++e)
+          for (int j = 0; j < 2; ++j) {
+            kb4[j] = (uint64_t)(kn[0][j] | kn[1][j] << 16) | (uint64_t)(kn[2][j] | kn[3][j] << 16) << 32;
+            vb4[j] = (uint64_t)(vn[0][j] | vn[1][j] << 16) | (uint64_t)(vn[2][j] | vn[3][j] << 16) << 32;
+          }
+          fetch(t + 4);
+        }
+        int kc[2], ev[2], top = -1000, low = 1000;          // -1000: no value to refer to
+        bool bad[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int key = (t0 + t + e) * KT + 32 * j + lane;
-          const bool in = t + e < nt && key < lim_max;
-          kn[e][j] = in ? __ldg(ksc + key) : 127;
-          vn[e][j] = in ? __ldg(vsc + key) : -1;          // past every limit
+          kc[j] = (int)(kb4[j] & 0xffffu);
+          const int vc = (int)(vb4[j] & 0xffffu);
+          kb4[j] >>= 16;
+          vb4[j] >>= 16;
+          bad[j] = kc[j] == kScaleNan || vc == kScaleNan;
+          ev[j] = vc > 255 || bad[j] ? -1000 : vc - 127;
+          top = max(top, ev[j]);
+          low = min(low, ev[j] == -1000 ? 1000 : ev[j]);
         }
-    };
-    if (nt > 0) fetch(0);
-    bool ok = true;
-    for (int tb = 0; tb < nt && ok; tb += AHEAD) {
-      int kc[AHEAD][2], vc[AHEAD][2];
-#pragma unroll
-      for (int e = 0; e < AHEAD; ++e)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          kc[e][j] = kn[e][j];
-          vc[e][j] = vn[e][j];
+        top = __reduce_max_sync(0xffffffffu, top);
+        low = __reduce_min_sync(0xffffffffu, low);
+        if (top - vref > (t == 0 ? 0 : kVSlack)) vref = top;
+        wide = wide || vref - low > kVSpread;
+        // tile t - 2's scores are computed and its references and factors read
+        if (t >= 2 && !(ok = wait(&pready[b], (t >> 1) - 1) && wait(&vready[b], (t >> 1) - 1))) break;
+        // a bad value makes the score NaN, so that only rows that see it are
+        *reinterpret_cast<uint2*>(sSF + (1 + b) * C::SF_BYTES + lane * 16) =
+            make_uint2((bad[0] ? 255u : (uint32_t)kc[0]) * 0x01010101u, (bad[1] ? 255u : (uint32_t)kc[1]) * 0x01010101u);
+        if (lane == 0) {
+          s_vref[b] = vref;
+          s_wide[b] = wide;
         }
-      fetch(tb + AHEAD);
-#pragma unroll
-      for (int e = 0; e < AHEAD; ++e) {
-        const int t = tb + e, b = t & 1;
-        if (t >= nt || !ok) break;
-        // tile t - 2's scores are computed and its factors read once its P is there
-        if (t >= 2 && !__all_sync(0xffffffffu, mbar_wait(&pready[b], (uint32_t)((t >> 1) - 1) & 1u, abort_flag, err,
-                                                         ERR_ATTN_FULL))) {
-          ok = false;
-          break;
-        }
-        uint32_t word[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const bool bad = kc[e][j] == kScaleNan || vc[e][j] == kScaleNan;
-          const int ev = vc[e][j] < 0 || bad ? -1000 : vc[e][j] - 127;
-          const int top = __reduce_max_sync(0xffffffffu, ev);   // of the 32 keys
-          // a bad value makes the score NaN, so that only rows that see it are
-          word[j] = (bad ? 255u : (uint32_t)kc[e][j]) * 0x01010101u;
-          s_vf[b * KT + 32 * j + lane] = ev == -1000 ? 0.0f : __uint_as_float((uint32_t)(127 + max(ev - top, -126)) << 23);
-          if (lane == 0) s_eb[b * 2 + j] = top;
+          const float f = ev[j] == -1000 ? 0.0f : exp2f((float)(ev[j] - vref));
+          s_vf[b * KT + 32 * j + lane] = f;
+          s_hf[b * KT + 32 * j + lane] = wide && f != 0.0f ? 1.0f : f;
         }
-        *reinterpret_cast<uint2*>(sSF + (2 + b) * C::SF_BYTES + lane * 16) = make_uint2(word[0], word[1]);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&kready[b]);
       }
     }
-    if (nt > 0 && ok && (t0 + nt) * KT > lim_max) {
-      // whatever bytes lie past every limit (codes of NaN among them) must not meet the zero probabilities
-      const int u = 2 * nt - 1, slot = u % C::SLOTS;
-      if (__all_sync(0xffffffffu, mbar_wait(&full[slot], (uint32_t)(u / C::SLOTS) & 1u, abort_flag, err, ERR_ATTN_FULL))) {
+  } else if (warp >= 8) {
+    setmaxnreg_dec<C::REGS_CONV>();
+    // ------------------------------------------------------ V to halves, keys 16 cw .. 16 cw + 15 of a tile
+    const int cw = warp - 8;
+    constexpr int CH = HD / 16;                           // 16-code chunks of a row
+    auto wait = [&](uint64_t* bar, int phase) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
+    };
+#pragma unroll 1
+    for (int t = 0; t < nt; ++t) {
+      const int b = t & 1, slot = t % C::VS;
+      if (!wait(&kready[b], t >> 1) || !wait(&vfull[slot], t / C::VS) || (t >= 2 && !wait(&pvdone[b], (t >> 1) - 1)))
+        break;
+      const uint8_t* src = sV + slot * C::SLOT;
+      uint8_t* dst = sH + b * C::V_BYTES;
+      // 32 / CH keys a step; 64 dims a 128-byte row of halves
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int key_l = 32 * j + lane;
-          if ((t0 + nt - 1) * KT + key_l >= lim_max) {
+      for (int i = 0; i < CH / 2; ++i) {
+        const int key_l = 16 * cw + i * (32 / CH) + lane / CH, c = lane % CH;
+        const float hf = s_hf[b * KT + key_l];
+        const uint32_t f = pack_f16x2(hf, hf);
+        uint4 w = *reinterpret_cast<const uint4*>(src + swizzled<HD>(key_l, c));
+        if (hf == 0.0f) w = make_uint4(0, 0, 0, 0);       // past every limit: whatever bytes lie there
+        uint32_t h[8];
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int c = 0; c < HD / 16; ++c)
-              *reinterpret_cast<uint4*>(sKV + slot * C::SLOT + key_l * HD + c * 16) = make_uint4(0, 0, 0, 0);
-          }
+        for (int k = 0; k < 4; ++k) {
+          h[2 * k] = mul_f16x2(cvt_f16x2_e4m3x2((uint16_t)(ww[k] & 0xffffu)), f);
+          h[2 * k + 1] = mul_f16x2(cvt_f16x2_e4m3x2((uint16_t)(ww[k] >> 16)), f);
         }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(vfixed);
+        uint8_t* d = dst + (c >> 2) * (KT * 128);
+        *reinterpret_cast<uint4*>(d + swizzled<128>(key_l, (2 * c) & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(d + swizzled<128>(key_l, (2 * c + 1) & 7)) = make_uint4(h[4], h[5], h[6], h[7]);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&vempty[slot]);
+        mbar_arrive(&vready[b]);
       }
     }
   } else {
-    const int q4 = warp & 3, row = q4 * 32 + lane, tid = (warp - 3) * 32 + lane;
+    setmaxnreg_inc<C::REGS_SOFT>();
+    const int q4 = warp & 3, row = q4 * 32 + lane, tid = (warp - 4) * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
     const int lim = s_lim[row];
     if (nt > 0) {
       // ---------------------------------------------------- the query tile
-      constexpr int L = HD / 8;                           // lanes of a row
-#pragma unroll 4
-      for (int n0 = 0; n0 < N; n0 += 128 / L) {
-        const int n = n0 + tid / L, l = tid % L;
-        float x[8] = {};
-        if (n < n_rows) {
-          const int rn = rt * N + n, i = rn / p.group, h = g * p.group + rn % p.group;
-          ElemBf16::load8(reinterpret_cast<const __nv_bfloat16*>(p.q) + ((long long)seq * p.R + i) * p.q_rs +
-                              (long long)h * HD + l * 8,
-                          x);
-        }
-        uint32_t m = abs_bits8(x);
-#pragma unroll
-        for (int d = L / 2; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const int byte = scale_byte(m);
-        const float inv = byte == kScaleNan ? __uint_as_float(0x7fffffffu) : scale_inverse(byte);
-        float r[8], b[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r[e] = x[e] * inv;    // a row that is not finite becomes NaN
-        const uint2 hi = encode8(r, 1.0f);
-        decode8(hi, 1.0f, b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) b[e] = r[e] - b[e];
-        const uint2 lo = encode8(b, 1.0f);
-        const uint32_t off = swizzled<HD>(n, l >> 1) + (uint32_t)(l & 1) * 8;
-        *reinterpret_cast<uint2*>(sQ + off) = hi;
-        *reinterpret_cast<uint2*>(sQ + C::Q_BYTES + off) = lo;
-        if (l == 0 && byte != kScaleNan)
-          reinterpret_cast<uint32_t*>(sSF + C::SF_BYTES)[(n & 31) * 4 + (n >> 5)] = (uint32_t)byte * 0x01010101u;
-      }
+      attn_query_tile<HD, N, 128>(p, seq, g, rt, n_rows, tid, sQ, sQ + C::Q_BYTES, 0, reinterpret_cast<uint32_t*>(sSF));
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(qready);
     }
     // ------------------------------------------------------ the keys
-    float m = 0.0f, l_sum = 0.0f;                         // reference (base 2) and sum of this row
-    int vref = 0;
+    float m = 0.0f;                                       // reference (base 2) of this row
+    uint64_t l2 = 0;                                      // its sum, times 2^7, in two parts
+    int vref = 0, r = 0;                                  // O is in units of 2^(vref + r)
     bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t par) {        // decided warp-wide: tensor-memory accesses are collective
-      return __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag, err, ERR_ATTN_FULL)) != 0;
+    auto wait = [&](uint64_t* bar, int phase) {           // decided warp-wide: tensor-memory accesses are collective
+      return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
     };
-    for (int t = 0; t < nt && ok; ++t) {
+    const uint64_t scale2 = f32x2(p.scale_log2, p.scale_log2);
+    for (int t = 0; t < nt; ++t) {
       const int b = t & 1, key0 = (t0 + t) * KT;
-      if (!(ok = wait(sfull, (uint32_t)t & 1u))) break;
+      if (!(ok = wait(sfull, t))) break;
       tc_fence_after();
       float s[KT];
       tmem_ld32(trow + C::S_COL, s);
@@ -332,90 +376,92 @@ __global__ void __launch_bounds__(224, 2)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(sfree);
-      if (key0 + KT > lim_min) {                          // some row does not see all of the tile
+      if (__builtin_expect(key0 + KT > lim_min, 0)) {     // some row does not see all of the tile
 #pragma unroll
         for (int c = 0; c < KT; ++c) s[c] = key0 + c < lim ? s[c] : -INFINITY;
       }
-      float mx = -INFINITY;
+      float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int c = 0; c < KT; ++c) mx = fmaxf(mx, s[c]);
-      mx *= p.scale_log2;
-      const int eb0 = s_eb[b * 2], eb1 = s_eb[b * 2 + 1];
-      // The row's reference rises when a score exceeds it by 2^8, and the common
-      // value reference when a key's exponent exceeds it by 40: float32 sums and
-      // the block scales have the range for what lies between.
-      const bool up = t == 0 ? mx > -INFINITY : mx > m + 8.0f;
-      const bool vup = t == 0 || max(eb0, eb1) - vref > 40;
-      if (__any_sync(0xffffffffu, up) || vup) {
-        const float mn = up ? mx : m;
-        const int vn = vup ? max(max(eb0, eb1), t == 0 ? -127 : vref) : vref;
-        if (t > 0) {
-          if (!(ok = wait(pvdone, (uint32_t)(t - 1) & 1u))) break;
-          tc_fence_after();
-          const float corr = exp2f(m - mn);
-          const float ocorr = vref - vn < -126 ? 0.0f : corr * scale_value(127 + vref - vn);
-          l_sum *= corr;
-#pragma unroll 1
-          for (int c = 0; c < HD; c += 32) {
-            float o[32];
-            tmem_ld32(trow + C::O_COL + c, o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= ocorr;
-            tmem_st32(trow + C::O_COL + c, o);
-          }
-          tc_fence_before();
-        }
+      for (int c = 4; c < KT; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+      const int vn = s_vref[b];
+      const bool wide = s_wide[b] != 0;
+      const bool up = t == 0 ? top > -INFINITY : top > m + kRowSlack;
+      const bool moved = __any_sync(0xffffffffu, up) || vn != vref;
+      float corr = 1.0f;                                  // of the row's old sums
+      if (moved) {
+        const float mn = up ? top : m;
+        if (t > 0) corr = exp2f(m - mn);
+        l2 = mul_f32x2(l2, f32x2(corr, corr));
         m = mn;
-        vref = vn;
       }
-      uint32_t hi[16], lo[16], word = 0;
+      // O times corr * 2^e; exponents below -126 leave nothing of the old sums that counts
+      auto rescale = [&](int e) {
+        ok = wait(&pvdone[b ^ 1], (t - 1) >> 1);
+        if (!ok) return;
+        tc_fence_after();
+        const float f = e < -126 ? 0.0f : corr * scale_value(127 + e);
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 32) {
+          float o[32];
+          tmem_ld32(trow + C::O_COL + c, o);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float4* vf = reinterpret_cast<const float4*>(s_vf + b * KT + 32 * j);
-        float top = 0.0f;
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 f = vf[c >> 2];
-          float* x = s + 32 * j + c;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float pr = ex2(fmaf(x[e], p.scale_log2, -m));
-            l_sum += pr;
-            x[e] = pr * (e == 0 ? f.x : e == 1 ? f.y : e == 2 ? f.z : f.w);
-            top = fmaxf(top, x[e]);
-          }
+          for (int i = 0; i < 32; ++i) o[i] *= f;
+          tmem_st32(trow + C::O_COL + c, o);
         }
-        // scaled so that the block's largest lies in [128, 256)
-        const int be = max((int)(__float_as_uint(top) >> 23) - 7, 1);
-        const float inv = __uint_as_float((uint32_t)(254 - be) << 23);
-        const int byte = min(max(be + (j ? eb1 : eb0) - vref, 4), 254);
-        word |= (uint32_t)byte << (8 * j) | (uint32_t)(byte - 4) << (16 + 8 * j);
+        tc_fence_before();
+      };
+      if (__builtin_expect(!wide && moved && t > 0, 0)) rescale(vref - vn);
+      const uint64_t off2 = f32x2(kPShift - m, kPShift - m);
+      uint32_t ph[KT / 2];
+      if (__builtin_expect(!wide, 1)) {
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float* x = s + 32 * j + c;
-          const uint32_t x0 = pack_f16x2(x[0] * inv, x[1] * inv), x1 = pack_f16x2(x[2] * inv, x[3] * inv);
-          const uint32_t h0 = cvt_e4m3x2_f16x2(x0), h1 = cvt_e4m3x2_f16x2(x1);
-          hi[8 * j + (c >> 2)] = h0 | (h1 << 16);
-          lo[8 * j + (c >> 2)] = cvt_e4m3x2_f16x2(sub_mul16_f16x2(x0, cvt_f16x2_e4m3x2((uint16_t)h0))) |
-                                 (cvt_e4m3x2_f16x2(sub_mul16_f16x2(x1, cvt_f16x2_e4m3x2((uint16_t)h1))) << 16);
+        for (int c = 0; c < KT; c += 2) {
+          const float2 z = f32x2_get(fma_f32x2(f32x2(s[c], s[c + 1]), scale2, off2));
+          const float p0 = ex2(z.x), p1 = ex2(z.y);
+          l2 = add_f32x2(l2, f32x2(p0, p1));
+          ph[c >> 1] = pack_f16x2(p0, p1);
         }
+      } else {
+        float most = 0.0f;
+#pragma unroll
+        for (int c = 0; c < KT; ++c) {
+          const float pr = ex2(fmaf(s[c], p.scale_log2, kPShift - m));
+          l2 = add_f32x2(l2, f32x2(pr, 0.0f));
+          s[c] = pr * s_vf[b * KT + c];
+          most = fmaxf(most, s[c]);
+        }
+        // The products' reference 2^r rises before a half would overflow, and falls to
+        // the new products' size when vref's rise has made room for the old sums.
+        const int e = (int)(__float_as_uint(most) >> 23) - 127 - 7;
+        int rn = r;
+        if (most > 0.0f && (t == 0 || e > r + 7)) rn = e;
+        if (most > 0.0f && t > 0 && vn > vref && e < r) rn = max(e, r - (vn - vref));
+        const int de = vref - vn + r - rn;
+        if (t > 0 && __any_sync(0xffffffffu, moved || de != 0)) rescale(de);
+        r = rn;
+        const float inv = exp2f((float)-r);
+#pragma unroll
+        for (int c = 0; c < KT; c += 2) ph[c >> 1] = pack_f16x2(s[c] * inv, s[c + 1] * inv);
       }
+      vref = vn;
+      if (!ok) break;
       // P is free once the last product is done
-      if (t > 0 && !(ok = wait(pvdone, (uint32_t)(t - 1) & 1u))) break;
+      if (t > 0 && !(ok = wait(&pvdone[b ^ 1], (t - 1) >> 1))) break;
       tc_fence_after();
-      tmem_st16(trow + C::P_COL, reinterpret_cast<const float*>(hi));
-      tmem_st16(trow + C::P_COL + 16, reinterpret_cast<const float*>(lo));
-      reinterpret_cast<uint32_t*>(sSF + 4 * C::SF_BYTES)[lane * 4 + q4] = word;
-      fence_async_smem();
+      tmem_st32(trow + C::P_COL, reinterpret_cast<const float*>(ph));
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&pready[b]);
     }
     // ------------------------------------------------------ output
-    if (nt > 0 && ok) ok = wait(pvdone, (uint32_t)(nt - 1) & 1u);
+    if (nt > 0 && ok) ok = wait(&pvdone[(nt - 1) & 1], (nt - 1) >> 1);
     tc_fence_after();
-    const float f = l_sum == 0.0f ? 0.0f : scale_value(127 + vref) / l_sum;
-    const int rn = rt * N + row, i = rn / p.group, h = g * p.group + rn % p.group;
+    const float2 lp = f32x2_get(l2);
+    const float l_sum = lp.x + lp.y;
+    const float f = l_sum == 0.0f ? 0.0f : ldexpf(1.0f / l_sum, vref + r);
+    uint32_t jh;
+    const int i = (int)p.by_group.divmod((uint32_t)(rt * N + row), jh), h = g * p.group + (int)jh;
     const bool valid = row < n_rows;
     const long long ws_row = ((long long)(plane * p.row_tiles + rt) * p.splits + split) * N + row;
 #pragma unroll 1
