@@ -29,7 +29,7 @@
 // (N = 16) to 2.8 us (N = 32), of which HBM needs 0.8 us.
 //
 //   warp 0     TMA: K and V tiles through a ring of 128-key slots
-//   warp 1     one thread issues scale copies and MMAs
+//   warp 1     scale copies and MMAs, issued by one lane
 //   warps 2..  softmax, one key and RW rows a thread; the query tile before, the output after
 // Keys are split over CTAs when there are few (sequence, head) items; every
 // split leaves its normalised output and (m, l), and a second small kernel joins them.
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* err = g_attn_kv8_err;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int split = (int)(blockIdx.x % (unsigned)p.splits);
   const int item = (int)(blockIdx.x / (unsigned)p.splits);
   const int rt = item % p.row_tiles, plane = item / p.row_tiles;      // plane = seq * H_kv + cached head
@@ -260,73 +260,54 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
           mbar_wait(&full[u % C::SLOTS], (uint32_t)(u / C::SLOTS) & 1u, nullptr, err, ERR_ATTN_FULL);
     }
   } else if (warp == 1) {
-    if (lane == 0 && nt > 0 && mbar_wait(qready, 0u, abort_flag, err, ERR_ATTN_FULL)) {
+    const uint32_t lead = elect_one();
+    auto wait = [&](uint64_t* bar, int phase) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
+    };
+    if (nt > 0 && wait(qready, 0)) {
       tc_fence_after();
       constexpr uint32_t idesc_s = idesc_mxf8(128, C::NQ);
       // V and P MN-major; P's scale byte kk belongs to keys 32 kk .. 32 kk + 31
       constexpr uint32_t idesc_o = idesc_mxf8(128, 2 * N) | (1u << 15) | (1u << 16);
       const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV), p0 = smem_u32(sP), f0 = smem_u32(sSF);
       const uint32_t sfa = tmem + C::SFA_COL, sfq = tmem + C::SFQ_COL;
-      tmem_cp_scales(sfa, sdesc_scales(f0));
-      tmem_cp_scales(sfq, sdesc_scales(f0 + C::SF_BYTES));
-      int ns = 0, np = 0;
-      unsigned long long idle_since = 0;
-      uint32_t spins = 0;
-      while (np < nt) {
-        bool did = false;
-        if (np < ns) {
-          const int u = 2 * np + 1, slot = u % C::SLOTS, pb = np & 1;
-          if (mbar_test_wait(smem_u32(&pready[pb]), (uint32_t)(np >> 1) & 1u) &&
-              mbar_test_wait(smem_u32(&full[slot]), (uint32_t)(u / C::SLOTS) & 1u)) {
-            tc_fence_after();
-            const uint32_t v = kv0 + slot * C::SLOT, pp = p0 + pb * C::P_BYTES;
-            const uint32_t sfb = tmem + C::SFB_COL + 4 * pb;
-            tmem_cp_scales(sfb, sdesc_scales(f0 + (2 + pb) * C::SF_BYTES));
+      tmem_cp_scales(lead, sfa, sdesc_scales(f0));
+      tmem_cp_scales(lead, sfq, sdesc_scales(f0 + C::SF_BYTES));
+      // Scores two tiles ahead of the products: the order K(t), V(t) of the ring keeps
+      // neither waiting on the other for long.
+      auto issue_s = [&](int t) {
+        const int u = 2 * t, slot = u % C::SLOTS, sb = t & 1;
+        if (!wait(&full[slot], u / C::SLOTS) || (t >= 2 && !wait(&sfree[sb], (t >> 1) - 1))) return false;
+        tc_fence_after();
+        const uint32_t k = kv0 + slot * C::SLOT, d = tmem + C::S_COL + sb * C::NQ;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              // a 64-wide head fills both halves of the 128 dims: the second repeats the first and is not read
-              mma_mxf8_ss(tmem + C::O_COL, sdesc_rows<HD>(v + kk * 32 * HD, 0),
-                          sdesc_rows<C::P_ROW>(pp + kk * 32 * C::P_ROW), idesc_o | ((uint32_t)kk << 4), sfa, sfb,
-                          (np > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(&empty[slot]);
-            mma_commit(&pvdone[pb]);
-            ++np;
-            did = true;
-          }
-        }
-        if (ns < nt) {
-          const int u = 2 * ns, slot = u % C::SLOTS, sb = ns & 1;
-          if (mbar_test_wait(smem_u32(&full[slot]), (uint32_t)(u / C::SLOTS) & 1u) &&
-              (ns < 2 || mbar_test_wait(smem_u32(&sfree[sb]), (uint32_t)((ns >> 1) - 1) & 1u))) {
-            tc_fence_after();
-            const uint32_t k = kv0 + slot * C::SLOT, d = tmem + C::S_COL + sb * C::NQ;
+        for (int part = 0; part < C::Q_PARTS; ++part)
 #pragma unroll
-            for (int part = 0; part < C::Q_PARTS; ++part)
+          for (int kk = 0; kk < HD / 32; ++kk)
+            mma_mxf8_ss(lead, d, sdesc_rows<HD>(k + kk * 32), sdesc_rows<HD>(q0 + part * C::Q_BYTES + kk * 32), idesc_s,
+                        sfa, sfq, (part > 0 || kk > 0) ? 1u : 0u);
+        mma_commit_lead(lead, &empty[slot]);
+        mma_commit_lead(lead, &sfull[sb]);
+        return true;
+      };
+      bool ok = issue_s(0) && (nt < 2 || issue_s(1));
+      for (int t = 0; t < nt && ok; ++t) {
+        const int u = 2 * t + 1, slot = u % C::SLOTS, pb = t & 1;
+        if (!(ok = wait(&pready[pb], t >> 1) && wait(&full[slot], u / C::SLOTS))) break;
+        tc_fence_after();
+        const uint32_t v = kv0 + slot * C::SLOT, pp = p0 + pb * C::P_BYTES, sfb = tmem + C::SFB_COL + 4 * pb;
+        tmem_cp_scales(lead, sfb, sdesc_scales(f0 + (2 + pb) * C::SF_BYTES));
 #pragma unroll
-              for (int kk = 0; kk < HD / 32; ++kk)
-                mma_mxf8_ss(d, sdesc_rows<HD>(k + kk * 32), sdesc_rows<HD>(q0 + part * C::Q_BYTES + kk * 32), idesc_s,
-                            sfa, sfq, (part > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(&empty[slot]);
-            mma_commit(&sfull[sb]);
-            ++ns;
-            did = true;
-          }
-        }
-        if (did) {
-          idle_since = 0;
-          spins = 0;
-        } else if ((++spins & 63u) == 0) {
-          const unsigned long long now = globaltimer();
-          if (idle_since == 0) {
-            idle_since = now;
-          } else if (*abort_flag || now - idle_since > kWaitLimitNs) {
-            if (!*abort_flag) record_error(err, ERR_ATTN_FULL);
-            *abort_flag = 1;
-            break;
-          }
-        }
+        for (int kk = 0; kk < 4; ++kk)
+          // a 64-wide head fills both halves of the 128 dims: the second repeats the first and is not read
+          mma_mxf8_ss(lead, tmem + C::O_COL, sdesc_rows<HD>(v + kk * 32 * HD, 0),
+                      sdesc_rows<C::P_ROW>(pp + kk * 32 * C::P_ROW), idesc_o | ((uint32_t)kk << 4), sfa, sfb,
+                      (t > 0 || kk > 0) ? 1u : 0u);
+        mma_commit_lead(lead, &empty[slot]);
+        mma_commit_lead(lead, &pvdone[pb]);
+        if (t + 2 < nt && !(ok = issue_s(t + 2))) break;
       }
-      mma_commit(mdone);
+      mma_commit_lead(lead, mdone);
       mbar_wait(mdone, 0u, nullptr, err, ERR_ATTN_FULL);
     }
   } else {

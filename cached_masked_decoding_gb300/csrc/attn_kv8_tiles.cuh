@@ -22,7 +22,7 @@
 // tile: 64 keys make S 64 columns, P 32, O 128 and the scales 12, just under half.
 //
 //   warp 0     TMA: K and V tiles of 64 keys, a ring each
-//   warp 1     one thread issues scale copies and MMAs
+//   warp 1     scale copies and MMAs, issued by one lane
 //   warp 2     scale bytes: K's for the MMA, V's as factors
 //   warps 4-7  softmax, one row a thread; the query tile before, the output after
 //   warps 8-11 V to halves, 16 keys each (two warps, the scales among their work,
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(384, 2)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* err = g_attn_kv8_err;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int split = (int)(blockIdx.x % (unsigned)p.splits);
   const int item = (int)(blockIdx.x / (unsigned)p.splits);
   // the last row tiles first: under a causal mask they see the most keys
@@ -188,33 +188,41 @@ __global__ void __launch_bounds__(384, 2)
         }
       }
     } else if (warp == 1) {
-      if (lane == 0 && nt > 0 && mbar_wait(qready, 0u, abort_flag, err, ERR_ATTN_FULL)) {
+      const uint32_t lead = elect_one();
+      auto wait = [&](uint64_t* bar, int phase) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
+      };
+      if (nt > 0 && wait(qready, 0)) {
         tc_fence_after();
         constexpr uint32_t idesc_s = idesc_mxf8(128, KT);
         // f16 operands (type 0), f32 accumulator, V MN-major
         constexpr uint32_t idesc_o = (1u << 4) | (1u << 16) | ((uint32_t)(HD >> 3) << 17) | (8u << 24);
         const uint32_t q0 = smem_u32(sQ), k0 = smem_u32(sK), h0 = smem_u32(sH), f0 = smem_u32(sSF);
-        tmem_cp_scales(tmem + C::SF_Q, sdesc_scales(f0));
-        auto wait = [&](uint64_t* bar, int phase) {
-          return mbar_wait(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL);
+        tmem_cp_scales(lead, tmem + C::SF_Q, sdesc_scales(f0));
+        // A tile's key scales go to tensor memory well before its scores' products: an
+        // MMA waits for the copy in front of it.
+        auto copy_scales = [&](int t) {
+          const int b = t & 1;
+          if (!wait(&kready[b], t >> 1)) return false;
+          tmem_cp_scales(lead, tmem + C::SF_K + 4 * b, sdesc_scales(f0 + (1 + b) * C::SF_BYTES));
+          return true;
         };
         auto issue_s = [&](int t) {
-          const int slot = t % C::KS, b = t & 1;
-          if ((t > 0 && !wait(sfree, t - 1)) || !wait(&kfull[slot], t / C::KS) || !wait(&kready[b], t >> 1)) return false;
+          const int slot = t % C::KS;
+          if ((t > 0 && !wait(sfree, t - 1)) || !wait(&kfull[slot], t / C::KS)) return false;
           tc_fence_after();
-          const uint32_t k = k0 + slot * C::SLOT, sfk = tmem + C::SF_K + 4 * b;
-          tmem_cp_scales(sfk, sdesc_scales(f0 + (1 + b) * C::SF_BYTES));
+          const uint32_t k = k0 + slot * C::SLOT, sfk = tmem + C::SF_K + 4 * (t & 1);
 #pragma unroll
           for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int kk = 0; kk < HD / 32; ++kk)
-              mma_mxf8_ss(tmem + C::S_COL, sdesc_rows<HD>(q0 + part * C::Q_BYTES + kk * 32), sdesc_rows<HD>(k + kk * 32),
-                          idesc_s, tmem + C::SF_Q, sfk, (part > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(&kempty[slot]);
-          mma_commit(sfull);
+              mma_mxf8_ss(lead, tmem + C::S_COL, sdesc_rows<HD>(q0 + part * C::Q_BYTES + kk * 32),
+                          sdesc_rows<HD>(k + kk * 32), idesc_s, tmem + C::SF_Q, sfk, (part > 0 || kk > 0) ? 1u : 0u);
+          mma_commit_lead(lead, &kempty[slot]);
+          mma_commit_lead(lead, sfull);
           return true;
         };
-        bool ok = issue_s(0);
+        bool ok = copy_scales(0) && issue_s(0) && (nt < 2 || copy_scales(1));
         for (int t = 0; t < nt && ok; ++t) {
           const int b = t & 1;
           // the next tile's scores as soon as these have been read
@@ -224,11 +232,12 @@ __global__ void __launch_bounds__(384, 2)
           const uint32_t v = h0 + b * C::V_BYTES;
 #pragma unroll
           for (int kk = 0; kk < KT / 16; ++kk)
-            mma_bf16_ts(tmem + C::O_COL, tmem + C::P_COL + kk * 8, sdesc_rows<128>(v + kk * 2048, KT * 128), idesc_o,
+            mma_f16_ts(lead, tmem + C::O_COL, tmem + C::P_COL + kk * 8, sdesc_rows<128>(v + kk * 2048, KT * 128), idesc_o,
                         (t > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(&pvdone[b]);
+          mma_commit_lead(lead, &pvdone[b]);
+          if (t + 2 < nt && !(ok = copy_scales(t + 2))) break;
         }
-        mma_commit(mdone);
+        mma_commit_lead(lead, mdone);
         mbar_wait(mdone, 0u, nullptr, err, ERR_ATTN_FULL);
       }
     } else if (warp == 2) {

@@ -102,7 +102,7 @@ struct Gemm8Cfg {
 // `split` CTAs of a cluster share a tile and join their partial tiles through
 // distributed shared memory in rank order.
 //   warp 0     TMA: weight and activation codes
-//   warp 1     one thread issues scale copies and MMAs
+//   warp 1     scale copies and MMAs, issued by one lane
 //   warps 2-5  epilogue
 //   warp 6     scale bytes: one row's byte replicated over a 32-bit word, in the
 //              512-byte layout tcgen05.cp wants (row r at (r % 32) * 16 + (r / 32) * 4)
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(224, 2)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* err = g_gemm8_err;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int split = p.split, rank = split > 1 ? (int)cluster_rank() : 0;
   const int tile = (int)(blockIdx.x / (unsigned)split);
   const int m0 = tile / p.n_tiles * 128, n0 = tile % p.n_tiles * BN;
@@ -171,28 +171,27 @@ __global__ void __launch_bounds__(224, 2)
           mbar_wait(&full[i % S], (uint32_t)(i / S) & 1u, nullptr, err, ERR_GEMM_DRAIN);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_mxf8(128, BN);
-      RingPos r{0, 0u};
-      for (int i = 0; i < nc; ++i) {
-        if (!mbar_wait(&full[r.s], r.par, abort_flag, err, ERR_GEMM_FULL)) break;
-        tc_fence_after();
-        const uint32_t a0 = smem_u32(sA + r.s * C::A_BYTES), b0 = smem_u32(sB + r.s * C::B_BYTES);
-        const uint32_t f0 = smem_u32(sF + r.s * C::SF_BYTES);
-        // a stage's scale columns are rewritten only once its MMAs are done (the empty barrier)
-        const uint32_t sfa = tmem + (uint32_t)(C::SF_COL + r.s * C::SF_COLS), sfb = sfa + 4;
-        tmem_cp_scales(sfa, sdesc_scales(f0));
+    const uint32_t lead = elect_one();
+    constexpr uint32_t idesc = idesc_mxf8(128, BN);
+    RingPos r{0, 0u};
+    for (int i = 0; i < nc; ++i) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[r.s], r.par, abort_flag, err, ERR_GEMM_FULL))) break;
+      tc_fence_after();
+      const uint32_t a0 = smem_u32(sA + r.s * C::A_BYTES), b0 = smem_u32(sB + r.s * C::B_BYTES);
+      const uint32_t f0 = smem_u32(sF + r.s * C::SF_BYTES);
+      // a stage's scale columns are rewritten only once its MMAs are done (the empty barrier)
+      const uint32_t sfa = tmem + (uint32_t)(C::SF_COL + r.s * C::SF_COLS), sfb = sfa + 4;
+      tmem_cp_scales(lead, sfa, sdesc_scales(f0));
 #pragma unroll
-        for (int t = 0; t < C::SFB_ATOMS; ++t) tmem_cp_scales(sfb + 4 * t, sdesc_scales(f0 + 512 * (t + 1)));
+      for (int t = 0; t < C::SFB_ATOMS; ++t) tmem_cp_scales(lead, sfb + 4 * t, sdesc_scales(f0 + 512 * (t + 1)));
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_mxf8_ss(tmem, sdesc_sw128(a0 + kk * 32), sdesc_sw128(b0 + kk * 32), idesc, sfa, sfb,
-                      (i > 0 || kk > 0) ? 1u : 0u);
-        mma_commit(&empty[r.s]);
-        r.next(S);
-      }
-      mma_commit(done);
+      for (int kk = 0; kk < 4; ++kk)
+        mma_mxf8_ss(lead, tmem, sdesc_sw128(a0 + kk * 32), sdesc_sw128(b0 + kk * 32), idesc, sfa, sfb,
+                    (i > 0 || kk > 0) ? 1u : 0u);
+      mma_commit_lead(lead, &empty[r.s]);
+      r.next(S);
     }
+    mma_commit_lead(lead, done);
   } else if (warp == 6) {
     // Four blocks' bytes in use, the next four's in flight: fetched one at a
     // time, their latency was the block's time (0.7 us, where HBM needs 0.4).

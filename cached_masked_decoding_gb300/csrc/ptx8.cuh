@@ -14,15 +14,52 @@ __host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N) {
   return ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 7) << 27);
 }
 
-// D[tmem] (+)= (A * 2^sa) (B * 2^sb)^T over 32 elements of K.
-__device__ __forceinline__ void mma_mxf8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate) {
+// Tensor-core instructions are issued by one thread of a warp whose lanes all walk
+// the same loop with `lead` set in one of them: in warp-uniform code descriptors and
+// addresses live in uniform registers, where a lone lane's cost about 12
+// instructions an MMA - more than the MMA itself takes for the smaller shapes.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r));
+  return r;
+}
+
+// D[tmem] (+)= (A * 2^sa) (B * 2^sb)^T over 32 elements of K.
+__device__ __forceinline__ void mma_mxf8_ss(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(
+      "setp.ne.b32 q, %7, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(
           d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] B^T over 16 halves of K (two a column of A).
+__device__ __forceinline__ void mma_f16_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+
+// Arrive once on bar when everything the leading thread has issued is done.
+__device__ __forceinline__ void mma_commit_lead(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(bar)),
+      "r"(lead)
       : "memory");
 }
 
@@ -38,8 +75,13 @@ __device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
 }
 
 // Copy 32 rows of 16 bytes to 4 tensor-memory columns, once into each 32-lane quarter.
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t s_desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
+__device__ __forceinline__ void tmem_cp_scales(uint32_t lead, uint32_t taddr, uint64_t s_desc) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}\n" ::"r"(taddr),
+      "l"(s_desc), "r"(lead)
+      : "memory");
 }
 
 // Order this thread's shared-memory stores before later asynchronous-proxy
