@@ -112,7 +112,7 @@ template <int HD, int N, int THREADS>
 __device__ __forceinline__ void attn_query_tile(const AttnKv8Params& p, int seq, int g, int rt, int n_rows, int tid,
                                                 uint8_t* q_hi, uint8_t* q_lo, int lo0, uint32_t* sf) {
   constexpr int L = HD / 8, PASS = THREADS / L;           // lanes of a row, rows a pass
-  constexpr int BATCH = (N + PASS - 1) / PASS < 8 ? (N + PASS - 1) / PASS : 8;
+  constexpr int BATCH = (N + PASS - 1) / PASS < 4 ? (N + PASS - 1) / PASS : 4;
   const int l = tid % L;
 #pragma unroll 1
   for (int n0 = tid / L; n0 < N + tid / L; n0 += PASS * BATCH) {   // every thread makes the same trips
@@ -131,21 +131,24 @@ __device__ __forceinline__ void attn_query_tile(const AttnKv8Params& p, int seq,
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
       const int n = n0 + k * PASS;
-      float x[8], b[8];
+      float x[8];
       raw[k].floats(x);
       uint32_t m = abs_bits8(x);
 #pragma unroll
       for (int d = L / 2; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
       if (n >= N) continue;
       const int byte = scale_byte(m);
+      // a row that is not finite becomes NaN
       const float inv = byte == kScaleNan ? __uint_as_float(0x7fffffffu) : scale_inverse(byte);
+      uint32_t h[4], w[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= inv;            // a row that is not finite becomes NaN
-      const uint2 hi = encode8(x, 1.0f);
-      decode8(hi, 1.0f, b);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) b[e] = x[e] - b[e];
-      const uint2 lo = encode8(b, 1.0f);
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t xh = pack_f16x2(x[2 * e] * inv, x[2 * e + 1] * inv);   // 8 bits: exact from 2^-14 on
+        h[e] = cvt_e4m3x2_f16x2(xh);
+        w[e] = cvt_e4m3x2_f16x2(sub_f16x2(xh, cvt_f16x2_e4m3x2((uint16_t)h[e])));
+      }
+      const uint2 hi = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+      const uint2 lo = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
       *reinterpret_cast<uint2*>(q_hi + swizzled<HD>(n, l >> 1) + (l & 1) * 8) = hi;
       *reinterpret_cast<uint2*>(q_lo + swizzled<HD>(n + lo0, l >> 1) + (l & 1) * 8) = lo;
       if (l == 0 && byte != kScaleNan) {

@@ -1,5 +1,5 @@
 // Attention over the 8-bit cache for many query rows a cached head (a prefill
-// over its own cache): 128 rows a CTA, one a softmax thread.
+// over its own cache): 128 rows a CTA, a row in two softmax threads.
 //
 //   S[row][key] = Q K^T      kind::mxf8f6f4 on the cache's codes; q as hi + lo codes (two
 //                            products, see attn_kv8_rows.cuh), the row's and the
@@ -24,9 +24,10 @@
 //   warp 0     TMA: K and V tiles of 64 keys, a ring each
 //   warp 1     scale copies and MMAs, issued by one lane
 //   warp 2     scale bytes: K's for the MMA, V's as factors
-//   warps 4-7  softmax, one row a thread; the query tile before, the output after
-//   warps 8-11 V to halves, 16 keys each (two warps, the scales among their work,
-//              were the longest stage: 2600 cycles a tile against 1300 of softmax)
+//   warps 4-11 softmax, a row in two threads of 32 keys each (with one thread a row the
+//              softmax was the longest stage, bound by its latencies: 2600 cycles a
+//              tile); the query tile before, the output after
+//   warps 12-15 V to halves, 16 keys each
 #pragma once
 
 #include "attn_kv8_rows.cuh"
@@ -37,16 +38,17 @@ template <int HD>
 struct AttnTilesCfg {
   static constexpr int N = 128;                         // rows
   static constexpr int KT = 64;
-  static constexpr int THREADS = 384;
-  // registers: the launch's 80 a thread (3 warpgroups) shared out anew, 136 + 48 + 56 = 3 * 80
-  static constexpr int REGS_SOFT = 136, REGS_CONV = 48, REGS_REST = 56;
+  static constexpr int THREADS = 512;
+  // registers: the launch's 64 a thread (4 warpgroups) shared out anew, 80 + 80 + 40 + 56 = 4 * 64
+  static constexpr int REGS_SOFT = 80, REGS_CONV = 40, REGS_REST = 56;
   static constexpr int SLOT = KT * HD;
   static constexpr int KS = 3, VS = 2;                  // slots of the two rings
   static constexpr int Q_BYTES = N * HD;                // hi or lo
   static constexpr int V_BYTES = KT * HD * 2;           // V as halves: 64 dims a 128-byte row
   static constexpr int SF_BYTES = 512;                  // query, two of K
   static constexpr int SMEM_BYTES =
-      1024 + (KS + VS) * SLOT + 2 * Q_BYTES + 2 * V_BYTES + 3 * SF_BYTES + (4 + 4 * KT + N) * 4 + (2 * (KS + VS) + 12) * 8 + 16;
+      1024 + (KS + VS) * SLOT + 2 * Q_BYTES + 2 * V_BYTES + 3 * SF_BYTES + (4 + 4 * KT + 5 * N) * 4 +
+      (2 * (KS + VS) + 12) * 8 + 16;
   static constexpr int S_COL = 0;
   static constexpr int P_COL = KT;                      // two halves a column
   static constexpr int O_COL = P_COL + KT / 2;
@@ -56,13 +58,13 @@ struct AttnTilesCfg {
   static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs an SM");
 };
 
-constexpr float kPShift = 7.0f;    // P is held as 2^7 p, p up to 2^kRowSlack: under a half's 65504
+constexpr float kPShift = 7.0f;    // P is held as 2^7 p, p up to 2^kRowSlack: a half has room to 65504
 constexpr float kRowSlack = 8.0f;  // log2 a score may exceed its row's reference by
 constexpr int kVSpread = 10;       // log2 of the value scales' spread that halves of V and P cover
 constexpr int kVSlack = 6;         // and a value exponent the common one: 448 * 2^6 is under 65504
 
 template <int HD>
-__global__ void __launch_bounds__(384, 2)
+__global__ void __launch_bounds__(512, 2)
     attn_kv8_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                           const __grid_constant__ AttnKv8Params p) {
   using C = AttnTilesCfg<HD>;
@@ -79,7 +81,9 @@ __global__ void __launch_bounds__(384, 2)
   float* s_vf = reinterpret_cast<float*>(s_wide + 2);   // [2][KT] factors of P then
   float* s_hf = s_vf + 2 * KT;                          // [2][KT] factors of V's halves
   int* s_lim = reinterpret_cast<int*>(s_hf + 2 * KT);   // [N]
-  uint64_t* kfull = reinterpret_cast<uint64_t*>(s_lim + N);
+  float* s_top = reinterpret_cast<float*>(s_lim + N);   // [2][N] a row's two halves: largest scores, sums
+  float* s_most = s_top + 2 * N;                        // [2][N] largest products
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(s_most + 2 * N);
   uint64_t* kempty = kfull + C::KS;
   uint64_t* vfull = kempty + C::KS;
   uint64_t* vempty = vfull + C::VS;
@@ -113,13 +117,13 @@ __global__ void __launch_bounds__(384, 2)
       mbar_init(&vfull[s], 1);
       mbar_init(&vempty[s], 4);
     }
-    mbar_init(qready, 4);
+    mbar_init(qready, 8);
     mbar_init(sfull, 1);
-    mbar_init(sfree, 4);
+    mbar_init(sfree, 8);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&kready[s], 1);
       mbar_init(&vready[s], 4);
-      mbar_init(&pready[s], 4);
+      mbar_init(&pready[s], 8);
       mbar_init(&pvdone[s], 1);
     }
     mbar_init(mdone, 1);
@@ -161,6 +165,14 @@ __global__ void __launch_bounds__(384, 2)
   const int t0 = (int)((long long)tiles * split / p.splits), t1 = (int)((long long)tiles * (split + 1) / p.splits);
   const int nt = t1 - t0;
 
+  // the query tile, by the softmax warps
+  auto query_tile = [&](int tid) {
+    attn_query_tile<HD, N, 256>(p, seq, g, rt, n_rows, tid, sQ, sQ + C::Q_BYTES, 0, reinterpret_cast<uint32_t*>(sSF));
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(qready);
+  };
+
   if (warp < 4) {
     setmaxnreg_dec<C::REGS_REST>();   // takes a whole warpgroup: warp 3 has no other part
     if (warp == 0) {
@@ -169,12 +181,12 @@ __global__ void __launch_bounds__(384, 2)
         RingPos rk{0, 0u}, rv{0, 0u};
         int k_issued = 0, v_issued = 0;
         for (int t = 0; t < nt; ++t) {
-          if (t >= C::KS && !mbar_wait(&kempty[rk.s], rk.par ^ 1u, abort_flag, err, ERR_ATTN_FULL)) break;
+          if (t >= C::KS && !mbar_wait_long(&kempty[rk.s], rk.par ^ 1u, abort_flag, err, ERR_ATTN_FULL)) break;
           mbar_arrive_expect_tx(&kfull[rk.s], C::SLOT);
           tma_load_3d(sK + rk.s * C::SLOT, &tmK, &kfull[rk.s], 0, (t0 + t) * KT, plane, pol);
           rk.next(C::KS);
           k_issued = t + 1;
-          if (t >= C::VS && !mbar_wait(&vempty[rv.s], rv.par ^ 1u, abort_flag, err, ERR_ATTN_FULL)) break;
+          if (t >= C::VS && !mbar_wait_long(&vempty[rv.s], rv.par ^ 1u, abort_flag, err, ERR_ATTN_FULL)) break;
           mbar_arrive_expect_tx(&vfull[rv.s], C::SLOT);
           tma_load_3d(sV + rv.s * C::SLOT, &tmV, &vfull[rv.s], 0, (t0 + t) * KT, plane, pol);
           rv.next(C::VS);
@@ -182,15 +194,15 @@ __global__ void __launch_bounds__(384, 2)
         }
         if (*abort_flag) {   // let copies in flight land before the CTA's shared memory goes away
           for (int t = max(k_issued - C::KS, 0); t < k_issued; ++t)
-            mbar_wait(&kfull[t % C::KS], (uint32_t)(t / C::KS) & 1u, nullptr, err, ERR_ATTN_FULL);
+            mbar_wait_long(&kfull[t % C::KS], (uint32_t)(t / C::KS) & 1u, nullptr, err, ERR_ATTN_FULL);
           for (int t = max(v_issued - C::VS, 0); t < v_issued; ++t)
-            mbar_wait(&vfull[t % C::VS], (uint32_t)(t / C::VS) & 1u, nullptr, err, ERR_ATTN_FULL);
+            mbar_wait_long(&vfull[t % C::VS], (uint32_t)(t / C::VS) & 1u, nullptr, err, ERR_ATTN_FULL);
         }
       }
     } else if (warp == 1) {
       const uint32_t lead = elect_one();
       auto wait = [&](uint64_t* bar, int phase) {
-        return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
+        return __all_sync(0xffffffffu, mbar_wait_long(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
       };
       if (nt > 0 && wait(qready, 0)) {
         tc_fence_after();
@@ -238,7 +250,7 @@ __global__ void __launch_bounds__(384, 2)
           if (t + 2 < nt && !(ok = copy_scales(t + 2))) break;
         }
         mma_commit_lead(lead, mdone);
-        mbar_wait(mdone, 0u, nullptr, err, ERR_ATTN_FULL);
+        mbar_wait_long(mdone, 0u, nullptr, err, ERR_ATTN_FULL);
       }
     } else if (warp == 2) {
       // ------------------------------------------------------ scales, keys lane and lane + 32 of a tile
@@ -263,7 +275,7 @@ __global__ void __launch_bounds__(384, 2)
       int vref = -127;
       bool wide = false;
       auto wait = [&](uint64_t* bar, int phase) {
-        return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
+        return __all_sync(0xffffffffu, mbar_wait_long(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
       };
 #pragma unroll 1
       for (int t = 0; t < nt; ++t) {
@@ -313,13 +325,13 @@ __global__ void __launch_bounds__(384, 2)
         if (lane == 0) mbar_arrive(&kready[b]);
       }
     }
-  } else if (warp >= 8) {
+  } else if (warp >= 12) {
     setmaxnreg_dec<C::REGS_CONV>();
     // ------------------------------------------------------ V to halves, keys 16 cw .. 16 cw + 15 of a tile
-    const int cw = warp - 8;
+    const int cw = warp - 12;
     constexpr int CH = HD / 16;                           // 16-code chunks of a row
     auto wait = [&](uint64_t* bar, int phase) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
+      return __all_sync(0xffffffffu, mbar_wait_long(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
     };
 #pragma unroll 1
     for (int t = 0; t < nt; ++t) {
@@ -356,147 +368,170 @@ __global__ void __launch_bounds__(384, 2)
     }
   } else {
     setmaxnreg_inc<C::REGS_SOFT>();
-    const int q4 = warp & 3, row = q4 * 32 + lane, tid = (warp - 4) * 32 + lane;
+    const int q4 = warp & 3, row = q4 * 32 + lane, hf = (warp - 4) >> 2;   // keys 32 hf .. of a tile, dims HD / 2 * hf ..
     const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
     const int lim = s_lim[row];
-    if (nt > 0) {
-      // ---------------------------------------------------- the query tile
-      attn_query_tile<HD, N, 128>(p, seq, g, rt, n_rows, tid, sQ, sQ + C::Q_BYTES, 0, reinterpret_cast<uint32_t*>(sSF));
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(qready);
-    }
+    if (nt > 0) query_tile((warp - 4) * 32 + lane);
     // ------------------------------------------------------ the keys
     float m = 0.0f;                                       // reference (base 2) of this row
     uint64_t l2 = 0;                                      // its sum, times 2^7, in two parts
     int vref = 0, r = 0;                                  // O is in units of 2^(vref + r)
+    // After a wait that gave up (ok false) the loop goes on, so that every warp meets
+    // every barrier; the outputs are invalid and reported.
     bool ok = true;
     auto wait = [&](uint64_t* bar, int phase) {           // decided warp-wide: tensor-memory accesses are collective
-      return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
+      return __all_sync(0xffffffffu, mbar_wait_long(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
     };
     const uint64_t scale2 = f32x2(p.scale_log2, p.scale_log2);
     for (int t = 0; t < nt; ++t) {
       const int b = t & 1, key0 = (t0 + t) * KT;
-      if (!(ok = wait(sfull, t))) break;
+      ok = wait(sfull, t) && ok;
       tc_fence_after();
-      float s[KT];
-      tmem_ld32(trow + C::S_COL, s);
-      tmem_ld32(trow + C::S_COL + 32, s + 32);
+      constexpr int KH = KT / 2;
+      float s[KH];
+      tmem_ld32(trow + C::S_COL + hf * KH, s);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(sfree);
       if (__builtin_expect(key0 + KT > lim_min, 0)) {     // some row does not see all of the tile
 #pragma unroll
-        for (int c = 0; c < KT; ++c) s[c] = key0 + c < lim ? s[c] : -INFINITY;
+        for (int c = 0; c < KH; ++c) s[c] = key0 + hf * KH + c < lim ? s[c] : -INFINITY;
       }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-      for (int c = 4; c < KT; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
       const int vn = s_vref[b];
       const bool wide = s_wide[b] != 0;
-      const bool up = t == 0 ? top > -INFINITY : top > m + kRowSlack;
-      const bool moved = __any_sync(0xffffffffu, up) || vn != vref;
-      float corr = 1.0f;                                  // of the row's old sums
-      if (moved) {
-        const float mn = up ? top : m;
-        if (t > 0) corr = exp2f(m - mn);
-        l2 = mul_f32x2(l2, f32x2(corr, corr));
-        m = mn;
-      }
-      // O times corr * 2^e; exponents below -126 leave nothing of the old sums that counts
-      auto rescale = [&](int e) {
-        ok = wait(&pvdone[b ^ 1], (t - 1) >> 1);
-        if (!ok) return;
-        tc_fence_after();
-        const float f = e < -126 ? 0.0f : corr * scale_value(127 + e);
-#pragma unroll 1
-        for (int c = 0; c < HD; c += 32) {
-          float o[32];
-          tmem_ld32(trow + C::O_COL + c, o);
+      uint32_t ph[KH / 2];
+      // Most tiles: the references stand.  A sum under 2^14 in either half means that no
+      // score is over its row's reference by 2^kRowSlack (P holds 2^7 p), so no
+      // maximum is taken.
+      bool redo = t == 0 || wide || vn != vref;
+      uint64_t tile2 = 0;
+      if (!redo) {
+        const uint64_t off2 = f32x2(kPShift - m, kPShift - m);
+        uint64_t sum[4] = {};
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= f;
-          tmem_st32(trow + C::O_COL + c, o);
-        }
-        tc_fence_before();
-      };
-      if (__builtin_expect(!wide && moved && t > 0, 0)) rescale(vref - vn);
-      const uint64_t off2 = f32x2(kPShift - m, kPShift - m);
-      uint32_t ph[KT / 2];
-      if (__builtin_expect(!wide, 1)) {
-#pragma unroll
-        for (int c = 0; c < KT; c += 2) {
+        for (int c = 0; c < KH; c += 2) {
           const float2 z = f32x2_get(fma_f32x2(f32x2(s[c], s[c + 1]), scale2, off2));
           const float p0 = ex2(z.x), p1 = ex2(z.y);
-          l2 = add_f32x2(l2, f32x2(p0, p1));
+          sum[(c >> 1) & 3] = add_f32x2(sum[(c >> 1) & 3], f32x2(p0, p1));
           ph[c >> 1] = pack_f16x2(p0, p1);
         }
-      } else {
-        float most = 0.0f;
-#pragma unroll
-        for (int c = 0; c < KT; ++c) {
-          const float pr = ex2(fmaf(s[c], p.scale_log2, kPShift - m));
-          l2 = add_f32x2(l2, f32x2(pr, 0.0f));
-          s[c] = pr * s_vf[b * KT + c];
-          most = fmaxf(most, s[c]);
-        }
-        // The products' reference 2^r rises before a half would overflow, and falls to
-        // the new products' size when vref's rise has made room for the old sums.
-        const int e = (int)(__float_as_uint(most) >> 23) - 127 - 7;
-        int rn = r;
-        if (most > 0.0f && (t == 0 || e > r + 7)) rn = e;
-        if (most > 0.0f && t > 0 && vn > vref && e < r) rn = max(e, r - (vn - vref));
-        const int de = vref - vn + r - rn;
-        if (t > 0 && __any_sync(0xffffffffu, moved || de != 0)) rescale(de);
-        r = rn;
-        const float inv = exp2f((float)-r);
-#pragma unroll
-        for (int c = 0; c < KT; c += 2) ph[c >> 1] = pack_f16x2(s[c] * inv, s[c + 1] * inv);
+        tile2 = add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3]));
+        const float2 both = f32x2_get(tile2);
+        redo = both.x + both.y >= 32768.0f;
       }
-      vref = vn;
-      if (!ok) break;
+      if (__builtin_expect(named_bar_or(3 + q4, 64, redo), 0)) {
+        float top = s[0];
+#pragma unroll
+        for (int c = 1; c < KH; ++c) top = fmaxf(top, s[c]);
+        s_top[hf * N + row] = top;
+        named_bar_sync(3 + q4, 64);
+        top = fmaxf(top, s_top[(hf ^ 1) * N + row]) * p.scale_log2;
+        const bool up = t == 0 ? top > -INFINITY : top > m + kRowSlack;
+        const bool moved = __any_sync(0xffffffffu, up) || vn != vref;
+        float corr = 1.0f;                                // of the row's old sums
+        if (moved) {
+          const float mn = up ? top : m;
+          if (t > 0) corr = exp2f(m - mn);
+          l2 = mul_f32x2(l2, f32x2(corr, corr));
+          m = mn;
+        }
+        // this half's dims of O times corr * 2^e; exponents below -126 leave nothing of the old
+        // sums that counts
+        auto rescale = [&](int e) {
+          if (!wait(&pvdone[b ^ 1], (t - 1) >> 1)) {
+            ok = false;
+            return;
+          }
+          tc_fence_after();
+          const float f = e < -126 ? 0.0f : corr * scale_value(127 + e);
+#pragma unroll 1
+          for (int c = hf * (HD / 2); c < (hf + 1) * (HD / 2); c += 16) {
+            float o[16];
+            tmem_ld16(trow + C::O_COL + c, o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] *= f;
+            tmem_st16(trow + C::O_COL + c, o);
+          }
+          tc_fence_before();
+        };
+        tile2 = 0;
+        if (!wide) {
+          if (moved && t > 0) rescale(vref - vn);
+#pragma unroll
+          for (int c = 0; c < KH; c += 2) {
+            const float p0 = ex2(fmaf(s[c], p.scale_log2, kPShift - m));
+            const float p1 = ex2(fmaf(s[c + 1], p.scale_log2, kPShift - m));
+            tile2 = add_f32x2(tile2, f32x2(p0, p1));
+            ph[c >> 1] = pack_f16x2(p0, p1);
+          }
+        } else {
+          float most = 0.0f;
+#pragma unroll
+          for (int c = 0; c < KH; ++c) {
+            const float pr = ex2(fmaf(s[c], p.scale_log2, kPShift - m));
+            tile2 = add_f32x2(tile2, f32x2(pr, 0.0f));
+            s[c] = pr * s_vf[b * KT + hf * KH + c];
+            most = fmaxf(most, s[c]);
+          }
+          s_most[hf * N + row] = most;
+          named_bar_sync(3 + q4, 64);
+          most = fmaxf(most, s_most[(hf ^ 1) * N + row]);
+          // The products' reference 2^r rises before a half would overflow, and falls to
+          // the new products' size when vref's rise has made room for the old sums.
+          const int e = (int)(__float_as_uint(most) >> 23) - 127 - 7;
+          int rn = r;
+          if (most > 0.0f && (t == 0 || e > r + 7)) rn = e;
+          if (most > 0.0f && t > 0 && vn > vref && e < r) rn = max(e, r - (vn - vref));
+          const int de = vref - vn + r - rn;
+          if (t > 0 && __any_sync(0xffffffffu, moved || de != 0)) rescale(de);
+          r = rn;
+          const float inv = exp2f((float)-r);
+#pragma unroll
+          for (int c = 0; c < KH; c += 2) ph[c >> 1] = pack_f16x2(s[c] * inv, s[c + 1] * inv);
+        }
+        vref = vn;
+      }
+      l2 = add_f32x2(l2, tile2);
       // P is free once the last product is done
-      if (t > 0 && !(ok = wait(&pvdone[b ^ 1], (t - 1) >> 1))) break;
+      if (t > 0) ok = wait(&pvdone[b ^ 1], (t - 1) >> 1) && ok;
       tc_fence_after();
-      tmem_st32(trow + C::P_COL, reinterpret_cast<const float*>(ph));
+      tmem_st16(trow + C::P_COL + hf * (KH / 2), reinterpret_cast<const float*>(ph));
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&pready[b]);
     }
     // ------------------------------------------------------ output
-    if (nt > 0 && ok) ok = wait(&pvdone[(nt - 1) & 1], (nt - 1) >> 1);
+    if (nt > 0) ok = wait(&pvdone[(nt - 1) & 1], (nt - 1) >> 1) && ok;
     tc_fence_after();
     const float2 lp = f32x2_get(l2);
-    const float l_sum = lp.x + lp.y;
+    named_bar_sync(3 + q4, 64);
+    s_top[hf * N + row] = lp.x + lp.y;
+    named_bar_sync(3 + q4, 64);
+    const float l_sum = s_top[row] + s_top[N + row];
     const float f = l_sum == 0.0f ? 0.0f : ldexpf(1.0f / l_sum, vref + r);
     uint32_t jh;
     const int i = (int)p.by_group.divmod((uint32_t)(rt * N + row), jh), h = g * p.group + (int)jh;
     const bool valid = row < n_rows;
     const long long ws_row = ((long long)(plane * p.row_tiles + rt) * p.splits + split) * N + row;
 #pragma unroll 1
-    for (int c = 0; c < HD; c += 32) {
-      float o[32];
-      if (nt > 0) {
-        tmem_ld32(trow + C::O_COL + c, o);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0.0f;
-      }
+    for (int c = hf * (HD / 2); c < (hf + 1) * (HD / 2); c += 16) {
+      float o[16] = {};
+      if (nt > 0) tmem_ld16(trow + C::O_COL + c, o);
       if (l_sum == 0.0f) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0.0f;         // a row that sees nothing
+        for (int e = 0; e < 16; ++e) o[e] = 0.0f;         // a row that sees nothing
       }
       if (!valid) {
         // nothing to store; the loads above are the whole warp's
       } else if (p.splits > 1) {
         float4* dst = reinterpret_cast<float4*>(p.ws_o + ws_row * HD + c);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < 4; ++e)
           dst[e] = make_float4(o[4 * e] * f, o[4 * e + 1] * f, o[4 * e + 2] * f, o[4 * e + 3] * f);
       } else {
         uint4* dst = reinterpret_cast<uint4*>(p.out + ((long long)seq * p.R + i) * p.o_rs + (long long)h * HD + c);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 2; ++e) {
           uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -507,7 +542,7 @@ __global__ void __launch_bounds__(384, 2)
         }
       }
     }
-    if (valid && p.splits > 1) *reinterpret_cast<float2*>(p.ws_ml + ws_row * 2) = make_float2(m, l_sum);
+    if (valid && hf == 0 && p.splits > 1) *reinterpret_cast<float2*>(p.ws_ml + ws_row * 2) = make_float2(m, l_sum);
   }
   // lanes that skipped their role arrive here first: reconverge before the CTA-wide barrier
   __syncwarp();

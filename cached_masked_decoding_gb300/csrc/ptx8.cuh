@@ -190,6 +190,34 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const float* v) {
     tmem_st16(taddr, v);
 }
 
+// mbar_wait of ptx.cuh with a suspend hint: a waiting warp sleeps in the barrier for
+// up to 20 us a try instead of polling issue slots away from the others.
+__device__ __forceinline__ bool mbar_try_wait_long(uint32_t addr, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(addr), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, int site) {
+  const uint32_t a = smem_u32(bar);
+  if (mbar_try_wait_long(a, parity)) return true;
+  const unsigned long long t0 = globaltimer();
+  while (!mbar_try_wait_long(a, parity)) {
+    if (abort && *abort) return false;
+    if (globaltimer() - t0 > kWaitLimitNs) {
+      if (abort) *abort = 1;
+      record_error(err, site);
+      return false;
+    }
+  }
+  return true;
+}
+
 // ----------------------------------------------------------------- register shares
 // By every warp of a warpgroup (four warps); the shares of a CTA's warpgroups
 // must not add up to more than its threads were launched with.
