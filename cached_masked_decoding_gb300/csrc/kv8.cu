@@ -20,34 +20,32 @@ struct Kv8Params {
   const int32_t* starts; // [b] position of a sequence's first row, or null (0)
   const int32_t* counts; // [b] rows of a sequence that take part, or null (R)
   int R;
-  uint32_t groups;       // 2 * b * R * H_kv row-heads of K and V
+  uint32_t groups;       // b * R * H_kv row-heads
   FastDiv heads, rows;   // by H_kv and by R
 };
 
-// (sequence, row, head, K or V) of a thread group's item and its cache slot;
-// false where the row takes no part.
+// (sequence, row, head) of a thread group's item and its cache slot; false
+// where the row takes no part.
 struct Kv8Item {
-  int which;
-  long long at;          // first element in the rows array
+  uint32_t row, h;
   long long slot;        // (sequence * H_kv + head) * T + position
   __device__ __forceinline__ bool init(const Kv8Params& p, uint32_t g) {
     if (g >= p.groups) return false;
-    which = (int)(g & 1);
-    uint32_t h, i;
-    const uint32_t row = p.heads.divmod(g >> 1, h);
+    uint32_t i;
+    row = p.heads.divmod(g, h);
     const uint32_t s = p.rows.divmod(row, i);
     const int n = p.counts ? __ldg(p.counts + s) : p.R;
     if ((int)i >= n) return false;
     const long long pos = (long long)(p.starts ? __ldg(p.starts + s) : 0) + i;
     if (pos < 0 || pos >= p.c.T) return false;
     slot = ((long long)s * p.c.H_kv + h) * p.c.T + pos;
-    at = (long long)row * p.rs[which] + (long long)h * p.c.hd;
     return true;
   }
 };
 
 // A block takes 256 / L * AHEAD consecutive row-heads, a thread group every
-// (256 / L)-th of them: all its loads are issued before the first is used.
+// (256 / L)-th of them, K and V of each (the slot's arithmetic, a third of
+// the kernel's instructions, serves both): all loads are issued before the first is used.
 template <typename E, int HD, int AHEAD>
 __global__ void __launch_bounds__(256, 4) kv8_store_kernel(const __grid_constant__ Kv8Params p) {
   constexpr int L = HD / 8, GROUPS = 256 / L;
@@ -57,28 +55,33 @@ __global__ void __launch_bounds__(256, 4) kv8_store_kernel(const __grid_constant
   const uint32_t g0 = blockIdx.x * (uint32_t)(GROUPS * AHEAD) + threadIdx.x / L;
   Kv8Item it[AHEAD];
   bool on[AHEAD];
-  Raw8<E> raw[AHEAD];
+  Raw8<E> raw[AHEAD][2];
 #pragma unroll
   for (int k = 0; k < AHEAD; ++k) on[k] = it[k].init(p, g0 + k * GROUPS);
 #pragma unroll
-  for (int k = 0; k < AHEAD; ++k) {
-    raw[k].zero();
-    if (on[k]) raw[k].load(static_cast<const typename E::T*>(p.in[it[k].which]) + it[k].at + l * 8);
-  }
+  for (int k = 0; k < AHEAD; ++k)
 #pragma unroll
-  for (int k = 0; k < AHEAD; ++k) {
-    float x[8];
-    raw[k].floats(x);
-    uint32_t m = abs_bits8(x);
+    for (int w = 0; w < 2; ++w) {
+      raw[k][w].zero();
+      if (on[k])
+        raw[k][w].template load<L>(static_cast<const typename E::T*>(p.in[w]) + it[k].row * p.rs[w] + it[k].h * HD, l);
+    }
 #pragma unroll
-    for (int d = L / 2; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (!on[k]) continue;
-    const int byte = scale_byte(m);
-    uint2 codes = make_uint2(0, 0);
-    if (byte != kScaleNan) codes = encode8(x, scale_inverse(byte));
-    *reinterpret_cast<uint2*>((it[k].which ? p.c.v : p.c.k) + it[k].slot * HD + l * 8) = codes;
-    if (l == 0) (it[k].which ? p.c.v_scale : p.c.k_scale)[it[k].slot] = (uint8_t)byte;
-  }
+  for (int k = 0; k < AHEAD; ++k)
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      float x[8];
+      raw[k][w].floats(x);
+      uint32_t m = abs_bits8(x);
+#pragma unroll
+      for (int d = L / 2; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+      if (!on[k]) continue;
+      const int byte = scale_byte(m);
+      uint2 codes = make_uint2(0, 0);
+      if (byte != kScaleNan) codes = encode8(x, scale_inverse(byte));
+      Raw8<E>::template store_codes<L>((w ? p.c.v : p.c.k) + it[k].slot * HD, l, codes);
+      if (l == 0) (w ? p.c.v_scale : p.c.k_scale)[it[k].slot] = (uint8_t)byte;
+    }
 }
 
 template <typename E, int HD, int AHEAD>
@@ -90,26 +93,32 @@ __global__ void __launch_bounds__(256, 4) kv8_load_kernel(const __grid_constant_
   const uint32_t g0 = blockIdx.x * (uint32_t)(GROUPS * AHEAD) + threadIdx.x / L;
   Kv8Item it[AHEAD];
   bool on[AHEAD];
-  uint2 codes[AHEAD];
-  int byte[AHEAD];
+  uint2 codes[AHEAD][2];
+  int byte[AHEAD][2];
 #pragma unroll
   for (int k = 0; k < AHEAD; ++k) on[k] = it[k].init(p, g0 + k * GROUPS);
 #pragma unroll
-  for (int k = 0; k < AHEAD; ++k) {
-    codes[k] = make_uint2(0, 0);
-    byte[k] = 127;
-    if (on[k]) {
-      codes[k] = __ldg(reinterpret_cast<const uint2*>((it[k].which ? p.c.v : p.c.k) + it[k].slot * HD + l * 8));
-      byte[k] = __ldg((it[k].which ? p.c.v_scale : p.c.k_scale) + it[k].slot);
-    }
-  }
+  for (int k = 0; k < AHEAD; ++k)
 #pragma unroll
-  for (int k = 0; k < AHEAD; ++k) {
-    if (!on[k]) continue;
-    float x[8];
-    decode8(codes[k], scale_value(byte[k]), x);
-    E::store8(static_cast<typename E::T*>(p.out[it[k].which]) + it[k].at + l * 8, x);
-  }
+    for (int w = 0; w < 2; ++w) {
+      codes[k][w] = make_uint2(0, 0);
+      byte[k][w] = 127;
+      if (on[k]) {
+        codes[k][w] = Raw8<E>::template load_codes<L>((w ? p.c.v : p.c.k) + it[k].slot * HD, l);
+        byte[k][w] = __ldg((w ? p.c.v_scale : p.c.k_scale) + it[k].slot);
+      }
+    }
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k)
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      if (!on[k]) continue;
+      float x[8];
+      decode8(codes[k][w], scale_value(byte[k][w]), x);
+      Raw8<E> out;
+      out.from(x);
+      out.template store<L>(static_cast<typename E::T*>(p.out[w]) + it[k].row * p.rs[w] + it[k].h * HD, l);
+    }
 }
 
 dllm_status kv8_check(const dllm_kv8* c, const char* who) {
@@ -132,12 +141,12 @@ cudaError_t launch_kv8(const Kv8Params& p, bool store, cudaStream_t st) {
                : op_launch(kv8_load_kernel<E, HD, AHEAD>, grid, dim3(256), 0, st, 1, p);
 }
 
-// Four row-heads a thread group once that still leaves every SM two blocks.
+// Two row-heads a thread group once that still leaves every SM two blocks.
 template <typename E>
 cudaError_t launch_kv8(const Kv8Params& p, bool store, cudaStream_t st) {
-  const bool ahead = p.groups >= 2u * op_device_sms() * (256 / (p.c.hd / 8) * 4);
-  if (p.c.hd == 64) return ahead ? launch_kv8<E, 64, 4>(p, store, st) : launch_kv8<E, 64, 1>(p, store, st);
-  return ahead ? launch_kv8<E, 128, 4>(p, store, st) : launch_kv8<E, 128, 1>(p, store, st);
+  const bool ahead = p.groups >= 2u * op_device_sms() * (256 / (p.c.hd / 8) * 2);
+  if (p.c.hd == 64) return ahead ? launch_kv8<E, 64, 2>(p, store, st) : launch_kv8<E, 64, 1>(p, store, st);
+  return ahead ? launch_kv8<E, 128, 2>(p, store, st) : launch_kv8<E, 128, 1>(p, store, st);
 }
 
 dllm_status kv8_rows(const dllm_kv8* cache, bool store, const void* k, const void* v, int64_t k_rs, int64_t v_rs,
@@ -164,7 +173,7 @@ dllm_status kv8_rows(const dllm_kv8* cache, bool store, const void* k, const voi
   p.starts = starts;
   p.counts = counts;
   p.R = R;
-  const __int128 groups = (__int128)2 * cache->b * R * cache->H_kv;
+  const __int128 groups = (__int128)cache->b * R * cache->H_kv;
   if (groups > 0x7fffff00)
     return op_fail(DLLM_EINVAL, "%s: b=%d R=%d H_kv=%d are too many rows for one call", who, cache->b, R, cache->H_kv);
   p.groups = (uint32_t)groups;

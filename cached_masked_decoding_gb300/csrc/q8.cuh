@@ -110,6 +110,36 @@ struct Raw8 {
     for (int i = 0; i < W; ++i) w[i] = make_uint4(0, 0, 0, 0);
   }
   __device__ __forceinline__ void floats(float (&x)[8]) const { E::load8(reinterpret_cast<const typename E::T*>(w), x); }
+  __device__ __forceinline__ void from(const float (&x)[8]) { E::store8(reinterpret_cast<typename E::T*>(w), x); }
+
+  // The same shared out over the L lanes of a row of 8 L elements: lane l's word i is
+  // the row's word i L + l, so that a warp's access is contiguous (two words a
+  // lane side by side made every access of float32 rows use half its sectors).
+  // The 8 / W elements of a word keep their codes together.
+  template <int L>
+  __device__ __forceinline__ void load(const typename E::T* row, int l) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(row) + i * L + l);
+  }
+  template <int L>
+  __device__ __forceinline__ void store(typename E::T* row, int l) const {
+#pragma unroll
+    for (int i = 0; i < W; ++i) reinterpret_cast<uint4*>(row)[i * L + l] = w[i];
+  }
+  template <int L>
+  static __device__ __forceinline__ void store_codes(uint8_t* row, int l, uint2 c) {
+    if constexpr (W == 1) {
+      reinterpret_cast<uint2*>(row)[l] = c;
+    } else {
+      reinterpret_cast<uint32_t*>(row)[l] = c.x;
+      reinterpret_cast<uint32_t*>(row)[L + l] = c.y;
+    }
+  }
+  template <int L>
+  static __device__ __forceinline__ uint2 load_codes(const uint8_t* row, int l) {
+    if constexpr (W == 1) return __ldg(reinterpret_cast<const uint2*>(row) + l);
+    return make_uint2(__ldg(reinterpret_cast<const uint32_t*>(row) + l), __ldg(reinterpret_cast<const uint32_t*>(row) + L + l));
+  }
 };
 
 struct ElemF32 {
