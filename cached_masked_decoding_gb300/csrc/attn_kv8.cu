@@ -24,16 +24,27 @@ struct AttnKv8Plan {
   size_t ws_bytes;
 };
 
-// Rows of one cached head (R rows of H / H_kv heads) in tiles of N; the keys in
-// splits while the CTAs fit on the GPU at once (two an SM, one with 64 rows), each with at least
-// one tile of keys.
+// Rows of one cached head (R rows of H / H_kv heads) in tiles of N, the keys in
+// splits.  A CTA's time is taken as the tiles of keys that it walks, and a split's
+// partial results with the kernel that joins them as four tiles' (measured: 8B
+// block, 32 heads of 6 tiles: 15.7 us in six splits, 9.5 us in one); a round of
+// CTAs is two an SM, one with 64 rows.
 AttnKv8Plan plan_attn_kv8(long long b, long long H_kv, long long rows, int hd, int T) {
   AttnKv8Plan a;
   a.N = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
   a.row_tiles = (int)((rows + a.N - 1) / a.N);
   a.items = b * H_kv * a.row_tiles;
-  const long long kt = a.N == 128 ? 64 : 128, tiles = (T + kt - 1) / kt, ctas = (a.N == 64 ? 1 : 2) * op_device_sms();
-  a.splits = (int)std::max(1LL, std::min({tiles, ctas / a.items, 64LL}));
+  const long long kt = a.N == 128 ? 64 : 128, tiles = (T + kt - 1) / kt;
+  const long long ctas = (a.N == 64 ? 1 : 2) * op_device_sms(), join = a.N == 128 ? 8 : 4;
+  long long best = (a.items + ctas - 1) / ctas * tiles;
+  a.splits = 1;
+  for (long long s = 2; s <= std::min(tiles, 64LL) && s * a.items <= ctas; ++s) {
+    const long long t = (tiles + s - 1) / s + join;
+    if (t < best) {
+      best = t;
+      a.splits = (int)s;
+    }
+  }
   a.ws_bytes = a.splits > 1 ? (size_t)a.items * a.splits * a.N * (hd + 2) * 4 : 0;
   return a;
 }

@@ -21,9 +21,12 @@
 //
 // Softmax runs with one key a thread and RW rows in its registers: nothing is
 // reduced across threads per tile but the 32-key maximum of each row (one
-// redux).  Rows share a reference maximum that moves only when a score exceeds
-// it by 2^40 (float32 sums and block scales have the range); sums l are kept
-// per key lane and joined once at the end.  This is the longest of the
+// redux).  A row's reference is its maximum over the CTA's first tile, and stays:
+// float32 sums and block scales hold what exceeds it by up to 2^110, so the
+// warps meet at no barrier after the first tile.  A CTA that met more, or
+// value scales over 2^60 apart, walks its keys again with references that follow the
+// scores, and others that follow the products (score plus value exponent).  Sums l
+// are kept per key lane and joined once at the end.  This is the longest of the
 // overlapped stages, so the rows of a tile are shared out over N / RW groups of
 // four warps: with one group of N rows a thread a tile of 128 keys took 1.8 us
 // (N = 16) to 2.8 us (N = 32), of which HBM needs 0.8 us.
@@ -74,9 +77,9 @@ struct AttnRowsCfg {
   static constexpr int P_BYTES = KT * P_ROW;
   static constexpr int SLOTS = CTAS == 1 ? (HD == 64 ? 16 : 9) : HD == 64 ? 8 : N == 32 ? 5 : 6;
   static constexpr int SF_BYTES = 512;                  // ones, query scales, two buffers of probability scales
-  static constexpr int STAT_FLOATS = 4 * N + 4 + 2 * N + 4 * N;  // warp maxima, warp value exponents, m, limits, scales
+  static constexpr int STAT_FLOATS = 8 * N + 4 + 3 * N + 4 * N;  // warp maxima (two), warp value exponents, m, d, limits, scales
   static constexpr int SMEM_BYTES = 1024 + SLOTS * SLOT + Q_PARTS * Q_BYTES + 2 * P_BYTES + 4 * SF_BYTES +
-                                    STAT_FLOATS * 4 + (2 * SLOTS + 10) * 8 + 16;
+                                    STAT_FLOATS * 4 + (2 * SLOTS + 10) * 8 + 24;
   static constexpr int S_COL = 0;                       // two buffers
   static constexpr int O_COL = 2 * NQ;                  // 2 N columns: hi and lo products
   static constexpr int SFA_COL = O_COL + 2 * N;
@@ -101,7 +104,9 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-constexpr float kRefSlack = 40.0f;   // log2 a score or a value scale may exceed its reference by
+constexpr float kRefSlack = 40.0f;   // log2 a score or a product may exceed a reference by that follows them
+constexpr int kRefFixed = 110;       // and a product or sum one that does not
+constexpr int kVRange = 60;          // value exponents' distance from the first tile's that such references allow
 
 // The query tile, rows rt * N .. of the item, by THREADS threads (a multiple of
 // 32): hi codes to q_hi, lo codes to q_lo from row lo0 on, and a word of the row's
@@ -173,9 +178,11 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
   uint8_t* sP = sQ + C::Q_PARTS * C::Q_BYTES;
   uint8_t* sSF = sP + 2 * C::P_BYTES;                   // scale atoms: ones, queries, a P buffer each
   float* s_wmax = reinterpret_cast<float*>(sSF + 4 * C::SF_BYTES);   // [4][N]
-  int* s_wev = reinterpret_cast<int*>(s_wmax + 4 * N);  // [4]
+  float* s_nmax = s_wmax + 4 * N;                       // [4][N]
+  int* s_wev = reinterpret_cast<int*>(s_nmax + 4 * N);  // [4]
   float* s_m = reinterpret_cast<float*>(s_wev + 4);     // [N] reference maxima
-  int* s_lim = reinterpret_cast<int*>(s_m + N);         // [N]
+  float* s_d = s_m + N;                                 // [N] O is in units of 2^(m + d)
+  int* s_lim = reinterpret_cast<int*>(s_d + N);         // [N]
   float* s_inv = reinterpret_cast<float*>(s_lim + N);   // [softmax warps][RW] inverse block scales
   uint64_t* full = reinterpret_cast<uint64_t*>(s_inv + 4 * N);
   uint64_t* empty = full + C::SLOTS;
@@ -187,6 +194,7 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
   uint64_t* mdone = pvdone + 2;                         // every MMA is done (before tensor memory is freed)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdone + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* again = abort_flag + 1;                 // the keys have to be walked once more
   int* err = g_attn_kv8_err;
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -210,6 +218,7 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
     }
     mbar_init(mdone, 1);
     *abort_flag = 0;
+    *again = 0;
     fence_mbar_init();
     prefetch_tensormap(&tmK);
     prefetch_tensormap(&tmV);
@@ -246,289 +255,351 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
   const int t0 = (int)((long long)tiles * split / p.splits), t1 = (int)((long long)tiles * (split + 1) / p.splits);
   const int nt = t1 - t0;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      const uint64_t pol = p.row_tiles > 1 ? policy_evict_last() : policy_evict_first();
-      RingPos r{0, 0u};
-      int issued = 0;
-      for (int u = 0; u < 2 * nt; ++u) {
-        if (u >= C::SLOTS && !mbar_wait(&empty[r.s], r.par ^ 1u, abort_flag, err, ERR_ATTN_FULL)) break;
-        mbar_arrive_expect_tx(&full[r.s], C::SLOT);
-        tma_load_3d(sKV + r.s * C::SLOT, (u & 1) ? &tmV : &tmK, &full[r.s], 0, (t0 + (u >> 1)) * KT, plane, pol);
-        r.next(C::SLOTS);
-        issued = u + 1;
+  // softmax: a row's sums, the reference of the value scales
+  float l_sum[RW];
+  int vref = 0;
+  // tiles count on through the second walk: T of a tile is pass * nt + t
+  for (int pass = 0;; ++pass) {
+    const int base = pass * nt;
+    if (warp == 0) {
+      if (lane == 0) {
+        const uint64_t pol = p.row_tiles > 1 ? policy_evict_last() : policy_evict_first();
+        int issued = 2 * base;
+        for (int u = 2 * base; u < 2 * (base + nt); ++u) {
+          const int slot = u % C::SLOTS;
+          if (u >= C::SLOTS &&
+              !mbar_wait_long(&empty[slot], (uint32_t)(u / C::SLOTS - 1) & 1u, abort_flag, err, ERR_ATTN_FULL))
+            break;
+          mbar_arrive_expect_tx(&full[slot], C::SLOT);
+          tma_load_3d(sKV + slot * C::SLOT, (u & 1) ? &tmV : &tmK, &full[slot], 0, (t0 + (u >> 1) - base) * KT, plane, pol);
+          issued = u + 1;
+        }
+        if (*abort_flag)   // let copies in flight land before the CTA's shared memory goes away
+          for (int u = max(issued - C::SLOTS, 2 * base); u < issued; ++u)
+            mbar_wait_long(&full[u % C::SLOTS], (uint32_t)(u / C::SLOTS) & 1u, nullptr, err, ERR_ATTN_FULL);
       }
-      if (*abort_flag)   // let copies in flight land before the CTA's shared memory goes away
-        for (int u = issued > C::SLOTS ? issued - C::SLOTS : 0; u < issued; ++u)
-          mbar_wait(&full[u % C::SLOTS], (uint32_t)(u / C::SLOTS) & 1u, nullptr, err, ERR_ATTN_FULL);
-    }
-  } else if (warp == 1) {
-    const uint32_t lead = elect_one();
-    auto wait = [&](uint64_t* bar, int phase) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
-    };
-    if (nt > 0 && wait(qready, 0)) {
-      tc_fence_after();
-      constexpr uint32_t idesc_s = idesc_mxf8(128, C::NQ);
-      // V and P MN-major; P's scale byte kk belongs to keys 32 kk .. 32 kk + 31
-      constexpr uint32_t idesc_o = idesc_mxf8(128, 2 * N) | (1u << 15) | (1u << 16);
-      const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV), p0 = smem_u32(sP), f0 = smem_u32(sSF);
-      const uint32_t sfa = tmem + C::SFA_COL, sfq = tmem + C::SFQ_COL;
-      tmem_cp_scales(lead, sfa, sdesc_scales(f0));
-      tmem_cp_scales(lead, sfq, sdesc_scales(f0 + C::SF_BYTES));
-      // Scores two tiles ahead of the products: the order K(t), V(t) of the ring keeps
-      // neither waiting on the other for long.
-      auto issue_s = [&](int t) {
-        const int u = 2 * t, slot = u % C::SLOTS, sb = t & 1;
-        if (!wait(&full[slot], u / C::SLOTS) || (t >= 2 && !wait(&sfree[sb], (t >> 1) - 1))) return false;
-        tc_fence_after();
-        const uint32_t k = kv0 + slot * C::SLOT, d = tmem + C::S_COL + sb * C::NQ;
-#pragma unroll
-        for (int part = 0; part < C::Q_PARTS; ++part)
-#pragma unroll
-          for (int kk = 0; kk < HD / 32; ++kk)
-            mma_mxf8_ss(lead, d, sdesc_rows<HD>(k + kk * 32), sdesc_rows<HD>(q0 + part * C::Q_BYTES + kk * 32), idesc_s,
-                        sfa, sfq, (part > 0 || kk > 0) ? 1u : 0u);
-        mma_commit_lead(lead, &empty[slot]);
-        mma_commit_lead(lead, &sfull[sb]);
-        return true;
+    } else if (warp == 1) {
+      const uint32_t lead = elect_one();
+      auto wait = [&](uint64_t* bar, int phase) {
+        return __all_sync(0xffffffffu, mbar_wait_long(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
       };
-      bool ok = issue_s(0) && (nt < 2 || issue_s(1));
-      for (int t = 0; t < nt && ok; ++t) {
-        const int u = 2 * t + 1, slot = u % C::SLOTS, pb = t & 1;
-        if (!(ok = wait(&pready[pb], t >> 1) && wait(&full[slot], u / C::SLOTS))) break;
+      if (nt > 0 && (pass > 0 || wait(qready, 0))) {
         tc_fence_after();
-        const uint32_t v = kv0 + slot * C::SLOT, pp = p0 + pb * C::P_BYTES, sfb = tmem + C::SFB_COL + 4 * pb;
-        tmem_cp_scales(lead, sfb, sdesc_scales(f0 + (2 + pb) * C::SF_BYTES));
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          // a 64-wide head fills both halves of the 128 dims: the second repeats the first and is not read
-          mma_mxf8_ss(lead, tmem + C::O_COL, sdesc_rows<HD>(v + kk * 32 * HD, 0),
-                      sdesc_rows<C::P_ROW>(pp + kk * 32 * C::P_ROW), idesc_o | ((uint32_t)kk << 4), sfa, sfb,
-                      (t > 0 || kk > 0) ? 1u : 0u);
-        mma_commit_lead(lead, &empty[slot]);
-        mma_commit_lead(lead, &pvdone[pb]);
-        if (t + 2 < nt && !(ok = issue_s(t + 2))) break;
-      }
-      mma_commit_lead(lead, mdone);
-      mbar_wait(mdone, 0u, nullptr, err, ERR_ATTN_FULL);
-    }
-  } else {
-    const int q4 = warp & 3, key_l = q4 * 32 + lane;      // this thread's key in a tile, and its tensor-memory lane
-    const int row0 = ((warp - 2) >> 2) * RW;              // its first row
-    const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
-    const int tid = (warp - 2) * 32 + lane;
-    // product t of P V is done
-    auto pv_wait = [&](int t) {
-      return __all_sync(0xffffffffu, mbar_wait(&pvdone[t & 1], (uint32_t)(t >> 1) & 1u, abort_flag, err,
-                                               ERR_ATTN_FULL)) != 0;
-    };
-    const uint8_t* ksc = p.c.k_scale + (long long)plane * p.c.T;
-    const uint8_t* vsc = p.c.v_scale + (long long)plane * p.c.T;
-    // scale bytes of this thread's key in four tiles, and of the next four in
-    // flight: fetched a tile ahead, their latency was the loop's (1.7 us a tile)
-    uint32_t kb4 = 0, vb4 = 0;
-    int kn[4], vn[4];
-    auto fetch = [&](int t) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int key = (t0 + t + e) * KT + key_l;
-        const bool in = t + e < nt && key < lim_max;
-        kn[e] = in ? __ldg(ksc + key) : 127;
-        vn[e] = in ? __ldg(vsc + key) : 127;
-      }
-    };
-    fetch(0);
-    if (nt > 0) {
-      // ---------------------------------------------------- the query tile
-      if (tid < 128) {
-#pragma unroll
-        for (int f = 0; f < 4; ++f) reinterpret_cast<uint32_t*>(sSF + f * C::SF_BYTES)[tid] = 0x7f7f7f7fu;
-      }
-      if (tid < N) s_m[tid] = 0.0f;
-      named_bar_sync(2, C::SOFT);
-      // 8 rows: the lo rows lie behind the hi rows of one operand
-      attn_query_tile<HD, N, C::SOFT>(p, seq, g, rt, n_rows, tid, sQ, sQ + (C::Q_PARTS - 1) * C::Q_BYTES,
-                                      C::Q_PARTS == 1 ? N : 0, reinterpret_cast<uint32_t*>(sSF + C::SF_BYTES));
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(qready);
-    }
-    // ------------------------------------------------------ the keys
-    float l_sum[RW];
-#pragma unroll
-    for (int n = 0; n < RW; ++n) l_sum[n] = 0.0f;
-    int vref = 0;
-    // After a wait that gave up (ok false) the loop goes on without waiting, so
-    // that every warp meets every barrier; the outputs are invalid and reported.
-    bool ok = true;
-    for (int t = 0; t < nt; ++t) {
-      const int b = t & 1;                                // S and P buffer
-      const int key = (t0 + t) * KT + key_l;
-      if ((t & 3) == 0) {
-        kb4 = (uint32_t)(kn[0] | kn[1] << 8 | kn[2] << 16 | kn[3] << 24);
-        vb4 = (uint32_t)(vn[0] | vn[1] << 8 | vn[2] << 16 | vn[3] << 24);
-        fetch(t + 4);
-      }
-      const int kb = (int)(kb4 & 255u), vb = (int)(vb4 & 255u);
-      kb4 >>= 8;
-      vb4 >>= 8;
-      const bool seen = key < lim_max;                    // by some row
-      const bool bad = kb == kScaleNan || vb == kScaleNan;
-      const float kf = bad ? __uint_as_float(0x7fffffffu) : scale_value(kb) * p.scale_log2;
-      const int ev = bad || !seen ? -1000 : vb - 127;     // -1000: no value scale to refer to
-      ok = __all_sync(0xffffffffu, mbar_wait(&sfull[b], (uint32_t)(t >> 1) & 1u, abort_flag, err, ERR_ATTN_FULL)) && ok;
-      tc_fence_after();
-      // scores in base 2, relative to their row's reference
-      float z[RW];
-      float top = -INFINITY;
-      if constexpr (C::Q_PARTS == 1) {
-        float s[16];
-        tmem_ld16(trow + C::S_COL + b * C::NQ, s);
-#pragma unroll
-        for (int j = 0; j < RW; ++j) z[j] = s[j] + s[j + N];
-      } else if constexpr (RW == 8) {
-        tmem_ld8(trow + C::S_COL + b * C::NQ + row0, z);
-      } else {
-        tmem_ld16(trow + C::S_COL + b * C::NQ + row0, z);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sfree[b]);
-#pragma unroll
-      for (int j = 0; j < RW; j += 4) {
-        const float4 m = *reinterpret_cast<const float4*>(s_m + row0 + j);
-        z[j] = fmaf(z[j], kf, -m.x);
-        z[j + 1] = fmaf(z[j + 1], kf, -m.y);
-        z[j + 2] = fmaf(z[j + 2], kf, -m.z);
-        z[j + 3] = fmaf(z[j + 3], kf, -m.w);
-      }
-      if ((t0 + t + 1) * KT > lim_min) {                  // some row does not see all of the tile
-#pragma unroll
-        for (int j = 0; j < RW; ++j) z[j] = key < s_lim[row0 + j] ? z[j] : -INFINITY;
-      }
-#pragma unroll
-      for (int j = 0; j < RW; ++j) top = fmaxf(top, z[j]);
-      bool need = t == 0 || ev - vref > (int)kRefSlack || top > kRefSlack;
-      if (!ok) need = false;
-      if (named_bar_or(2, C::SOFT, need)) {
-        // new references: the first tile's, or a score far above the last ones
-#pragma unroll
-        for (int j = 0; j < RW; ++j) {
-          const int wt = __reduce_max_sync(0xffffffffu, float_order(z[j]));
-          if (lane == j) s_wmax[q4 * N + row0 + j] = order_float(wt);
+        constexpr uint32_t idesc_s = idesc_mxf8(128, C::NQ);
+        // V and P MN-major; P's scale byte kk belongs to keys 32 kk .. 32 kk + 31
+        constexpr uint32_t idesc_o = idesc_mxf8(128, 2 * N) | (1u << 15) | (1u << 16);
+        const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV), p0 = smem_u32(sP), f0 = smem_u32(sSF);
+        const uint32_t sfa = tmem + C::SFA_COL, sfq = tmem + C::SFQ_COL;
+        if (pass == 0) {
+          tmem_cp_scales(lead, sfa, sdesc_scales(f0));
+          tmem_cp_scales(lead, sfq, sdesc_scales(f0 + C::SF_BYTES));
         }
-        const int evw = __reduce_max_sync(0xffffffffu, ev);
-        if (row0 == 0 && lane == 0) s_wev[q4] = evw;
-        named_bar_sync(2, C::SOFT);
-        const int ev_top = max(max(s_wev[0], s_wev[1]), max(s_wev[2], s_wev[3]));
-        const int vref_new = t == 0 ? max(ev_top, -127) : max(vref, ev_top);
-        float up = 0.0f;                                  // row tid's reference rises by this
-        if (tid < N) {
-          int tr = float_order(s_wmax[tid]);
-#pragma unroll
-          for (int k = 1; k < 4; ++k) tr = max(tr, float_order(s_wmax[k * N + tid]));
-          up = order_float(tr);
-          if (up == -INFINITY || (t > 0 && up < 0.0f)) up = 0.0f;
-        }
-        named_bar_sync(2, C::SOFT);
-        if (tid < N) {
-          s_m[tid] += up;
-          s_wmax[tid] = up;
-        }
-        named_bar_sync(2, C::SOFT);
-#pragma unroll
-        for (int j = 0; j < RW; ++j) z[j] -= s_wmax[row0 + j];
-        if (t > 0) {
-          ok = ok && pv_wait(t - 1);
+        // Scores two tiles ahead of the products: the order K(t), V(t) of the ring keeps
+        // neither waiting on the other for long.
+        auto issue_s = [&](int t) {
+          const int T = base + t, u = 2 * T, slot = u % C::SLOTS, sb = T & 1;
+          if (!wait(&full[slot], u / C::SLOTS) || (T >= 2 && !wait(&sfree[sb], (T >> 1) - 1))) return false;
           tc_fence_after();
-          // exponents below -126 leave nothing of the old sums that counts
-          const float vcorr = vref - vref_new < -126 ? 0.0f : scale_value(127 + vref - vref_new);
-          float corr[RW];
+          const uint32_t k = kv0 + slot * C::SLOT, d = tmem + C::S_COL + sb * C::NQ;
 #pragma unroll
-          for (int j = 0; j < RW; ++j) {
-            corr[j] = exp2f(-s_wmax[row0 + j]);
-            l_sum[j] *= corr[j];
-          }
+          for (int part = 0; part < C::Q_PARTS; ++part)
 #pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            float o[RW];
-            tmem_ld<RW>(trow + C::O_COL + part * N + row0, o);
+            for (int kk = 0; kk < HD / 32; ++kk)
+              mma_mxf8_ss(lead, d, sdesc_rows<HD>(k + kk * 32), sdesc_rows<HD>(q0 + part * C::Q_BYTES + kk * 32), idesc_s,
+                          sfa, sfq, (part > 0 || kk > 0) ? 1u : 0u);
+          mma_commit_lead(lead, &empty[slot]);
+          mma_commit_lead(lead, &sfull[sb]);
+          return true;
+        };
+        bool ok = issue_s(0) && (nt < 2 || issue_s(1));
+        for (int t = 0; t < nt && ok; ++t) {
+          const int T = base + t, u = 2 * T + 1, slot = u % C::SLOTS, pb = T & 1;
+          if (!(ok = wait(&pready[pb], T >> 1) && wait(&full[slot], u / C::SLOTS))) break;
+          tc_fence_after();
+          const uint32_t v = kv0 + slot * C::SLOT, pp = p0 + pb * C::P_BYTES, sfb = tmem + C::SFB_COL + 4 * pb;
+          tmem_cp_scales(lead, sfb, sdesc_scales(f0 + (2 + pb) * C::SF_BYTES));
 #pragma unroll
-            for (int j = 0; j < RW; ++j) o[j] *= corr[j] * vcorr;
-            tmem_st<RW>(trow + C::O_COL + part * N + row0, o);
-          }
-          tc_fence_before();
+          for (int kk = 0; kk < 4; ++kk)
+            // a 64-wide head fills both halves of the 128 dims: the second repeats the first and is not read
+            mma_mxf8_ss(lead, tmem + C::O_COL, sdesc_rows<HD>(v + kk * 32 * HD, 0),
+                        sdesc_rows<C::P_ROW>(pp + kk * 32 * C::P_ROW), idesc_o | ((uint32_t)kk << 4), sfa, sfb,
+                        (t > 0 || kk > 0) ? 1u : 0u);
+          mma_commit_lead(lead, &empty[slot]);
+          mma_commit_lead(lead, &pvdone[pb]);
+          if (t + 2 < nt && !(ok = issue_s(t + 2))) break;
         }
-        vref = vref_new;
-        named_bar_sync(2, C::SOFT);                       // s_wmax is read: the next tile may rewrite it
+        mma_commit_lead(lead, mdone);
+        mbar_wait_long(mdone, (uint32_t)pass & 1u, nullptr, err, ERR_ATTN_FULL);
       }
-      // the P buffer is free once the product that last read it is done
-      if (t >= 2 && ok) ok = pv_wait(t - 2);
-      const int dv = max(ev - vref, -126);
-      const float vf = bad || !seen ? 0.0f : __uint_as_float((uint32_t)(127 + dv) << 23);
-      uint8_t* prow = sP + b * C::P_BYTES;
-      uint8_t* sf = sSF + (2 + b) * C::SF_BYTES;
-      // probabilities, and each row's largest of the warp's 32 keys: lane j (modulo RW) keeps row j's
-      uint32_t top_me = 0;
+    } else {
+      const int q4 = warp & 3, key_l = q4 * 32 + lane;      // this thread's key in a tile, and its tensor-memory lane
+      const int row0 = ((warp - 2) >> 2) * RW;              // its first row
+      const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
+      const int tid = (warp - 2) * 32 + lane;
+      // product t of P V is done
+      auto pv_wait = [&](int t) {
+        const int T = base + t;
+        return __all_sync(0xffffffffu, mbar_wait_long(&pvdone[T & 1], (uint32_t)(T >> 1) & 1u, abort_flag, err,
+                                                      ERR_ATTN_FULL)) != 0;
+      };
+      const uint8_t* ksc = p.c.k_scale + (long long)plane * p.c.T;
+      const uint8_t* vsc = p.c.v_scale + (long long)plane * p.c.T;
+      // scale bytes of this thread's key in four tiles, and of the next four in
+      // flight: fetched a tile ahead, their latency was the loop's (1.7 us a tile)
+      uint32_t kb4 = 0, vb4 = 0;
+      int kn[4], vn[4];
+      auto fetch = [&](int t) {
 #pragma unroll
-      for (int j = 0; j < RW; ++j) {
-        const float pr = ex2(z[j]);
-        l_sum[j] += pr;
-        z[j] = pr * vf;
-        const uint32_t r = __reduce_max_sync(0xffffffffu, __float_as_uint(z[j]));
-        if ((lane & (RW - 1)) == j) top_me = r;
-      }
-      // the block's scale puts its largest probability into [128, 256); the lanes work out a row each
-      const int byte_me = min(max((int)(top_me >> 23) - 7, 4), 247);
-      float* inv = s_inv + (warp - 2) * RW;
-      if (lane < RW) inv[lane] = __uint_as_float((uint32_t)(254 - byte_me) << 23);
-      if (lane < 2 * RW) {
-        // lanes 0 .. RW-1: the scale bytes of the hi rows for this warp's keys, the next RW: of the lo rows
-        const int r = row0 + (lane & (RW - 1)) + (lane < RW ? 0 : N);
-        sf[(r & 31) * 16 + (r >> 5) * 4 + q4] = (uint8_t)(lane < RW ? byte_me : byte_me - 4);
-      }
-      __syncwarp();
-      uint32_t hi[RW / 4], lo[RW / 4];
+        for (int e = 0; e < 4; ++e) {
+          const int key = (t0 + t + e) * KT + key_l;
+          const bool in = t + e < nt && key < lim_max;
+          kn[e] = in ? __ldg(ksc + key) : 127;
+          vn[e] = in ? __ldg(vsc + key) : 127;
+        }
+      };
+      fetch(0);
+      if (pass > 0) {
+        if (tid < N) s_m[tid] = s_d[tid] = 0.0f;
+        named_bar_sync(2, C::SOFT);
+      } else if (nt > 0) {
+        // ---------------------------------------------------- the query tile
+        if (tid < 128) {
 #pragma unroll
-      for (int j = 0; j < RW; j += 4) {
-        const float4 f = *reinterpret_cast<const float4*>(inv + j);
-        // hi: the nearest code; lo: what it leaves, at most a 16th of it, in a scale 2^4 smaller
-        const uint32_t x0 = pack_f16x2(z[j] * f.x, z[j + 1] * f.y), x1 = pack_f16x2(z[j + 2] * f.z, z[j + 3] * f.w);
-        const uint32_t h0 = cvt_e4m3x2_f16x2(x0), h1 = cvt_e4m3x2_f16x2(x1);
-        hi[j >> 2] = h0 | (h1 << 16);
-        lo[j >> 2] = cvt_e4m3x2_f16x2(sub_mul16_f16x2(x0, cvt_f16x2_e4m3x2((uint16_t)h0))) |
-                     (cvt_e4m3x2_f16x2(sub_mul16_f16x2(x1, cvt_f16x2_e4m3x2((uint16_t)h1))) << 16);
+          for (int f = 0; f < 4; ++f) reinterpret_cast<uint32_t*>(sSF + f * C::SF_BYTES)[tid] = 0x7f7f7f7fu;
+        }
+        if (tid < N) s_m[tid] = s_d[tid] = 0.0f;
+        named_bar_sync(2, C::SOFT);
+        // 8 rows: the lo rows lie behind the hi rows of one operand
+        attn_query_tile<HD, N, C::SOFT>(p, seq, g, rt, n_rows, tid, sQ, sQ + (C::Q_PARTS - 1) * C::Q_BYTES,
+                                        C::Q_PARTS == 1 ? N : 0, reinterpret_cast<uint32_t*>(sSF + C::SF_BYTES));
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qready);
       }
-      uint8_t* ph = prow + swizzled<C::P_ROW>(key_l, row0 >> 4) + (row0 & 15);
-      uint8_t* pl = prow + swizzled<C::P_ROW>(key_l, (N + row0) >> 4) + ((N + row0) & 15);
-      if constexpr (RW == 8) {
-        *reinterpret_cast<uint2*>(ph) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(pl) = make_uint2(lo[0], lo[1]);
-      } else {
-        *reinterpret_cast<uint4*>(ph) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(pl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      }
-      if ((t0 + t + 1) * KT > lim_max && row0 == 0) {
-        // the last tile runs past every row's limit: whatever bytes lie there
-        // (codes of NaN among them) must not meet the zero probabilities
-        const int u = 2 * t + 1, slot = u % C::SLOTS;
-        ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], (uint32_t)(u / C::SLOTS) & 1u, abort_flag, err, ERR_ATTN_FULL)) &&
+      // ------------------------------------------------------ the keys
+#pragma unroll
+      for (int n = 0; n < RW; ++n) l_sum[n] = 0.0f;
+      vref = 0;
+      uint32_t most = 0;                                    // largest block maximum of this lane's row
+      bool far = false;                                     // a value scale far from the first tile's
+      // After a wait that gave up (ok false) the loop goes on without waiting, so
+      // that every warp meets every barrier; the outputs are invalid and reported.
+      bool ok = true;
+      for (int t = 0; t < nt; ++t) {
+        const int T = base + t, b = T & 1;                  // S and P buffer
+        const int key = (t0 + t) * KT + key_l;
+        if ((t & 3) == 0) {
+          kb4 = (uint32_t)(kn[0] | kn[1] << 8 | kn[2] << 16 | kn[3] << 24);
+          vb4 = (uint32_t)(vn[0] | vn[1] << 8 | vn[2] << 16 | vn[3] << 24);
+          fetch(t + 4);
+        }
+        const int kb = (int)(kb4 & 255u), vb = (int)(vb4 & 255u);
+        kb4 >>= 8;
+        vb4 >>= 8;
+        const bool seen = key < lim_max;                    // by some row
+        const bool bad = kb == kScaleNan || vb == kScaleNan;
+        const float kf = bad ? __uint_as_float(0x7fffffffu) : scale_value(kb) * p.scale_log2;
+        const int ev = bad || !seen ? -1000 : vb - 127;     // -1000: no value scale to refer to
+        ok = __all_sync(0xffffffffu, mbar_wait_long(&sfull[b], (uint32_t)(T >> 1) & 1u, abort_flag, err, ERR_ATTN_FULL)) &&
              ok;
-        if (!seen) {
+        tc_fence_after();
+        // scores in base 2, relative to their row's reference
+        float z[RW];
+        if constexpr (C::Q_PARTS == 1) {
+          float s[16];
+          tmem_ld16(trow + C::S_COL + b * C::NQ, s);
 #pragma unroll
-          for (int c = 0; c < HD / 16; ++c)
-            *reinterpret_cast<uint4*>(sKV + slot * C::SLOT + key_l * HD + c * 16) = make_uint4(0, 0, 0, 0);
+          for (int j = 0; j < RW; ++j) z[j] = s[j] + s[j + N];
+        } else {
+          tmem_ld<RW>(trow + C::S_COL + b * C::NQ + row0, z);
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sfree[b]);
+        const uint64_t kf2 = f32x2(kf, kf);
+#pragma unroll
+        for (int j = 0; j < RW; j += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(s_m + row0 + j);
+          const float2 za = f32x2_get(fma_f32x2(f32x2(z[j], z[j + 1]), kf2, f32x2(-m.x, -m.y)));
+          const float2 zb = f32x2_get(fma_f32x2(f32x2(z[j + 2], z[j + 3]), kf2, f32x2(-m.z, -m.w)));
+          z[j] = za.x;
+          z[j + 1] = za.y;
+          z[j + 2] = zb.x;
+          z[j + 3] = zb.y;
+        }
+        if ((t0 + t + 1) * KT > lim_min) {                  // some row does not see all of the tile
+#pragma unroll
+          for (int j = 0; j < RW; ++j) z[j] = key < s_lim[row0 + j] ? z[j] : -INFINITY;
+        }
+        if (t == 0 || pass > 0) {
+          bool need = t == 0;
+          const float evf = (float)ev;                    // of no account where the score is -inf or NaN
+          if (pass > 0) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < RW; ++j) top = fmaxf(top, fmaxf(z[j], z[j] + evf - s_d[row0 + j]));
+            need = need || top > kRefSlack;
+          }
+          if (!ok) need = false;
+          if (named_bar_or(2, C::SOFT, need)) {
+            // new references: the first tile's, or scores or products far above the last ones
+#pragma unroll
+            for (int j = 0; j < RW; ++j) {
+              const int wt = __reduce_max_sync(0xffffffffu, float_order(z[j]));
+              const int nm = __reduce_max_sync(0xffffffffu, float_order(z[j] + evf - s_d[row0 + j]));
+              if (lane == j) {
+                s_wmax[q4 * N + row0 + j] = order_float(wt);
+                s_nmax[q4 * N + row0 + j] = order_float(nm);
+              }
+            }
+            const int evw = __reduce_max_sync(0xffffffffu, ev);
+            if (row0 == 0 && lane == 0) s_wev[q4] = evw;
+            named_bar_sync(2, C::SOFT);
+            const int ev_top = max(max(s_wev[0], s_wev[1]), max(s_wev[2], s_wev[3]));
+            if (pass == 0) vref = max(ev_top, -127);
+            float up = 0.0f, un = 0.0f;                   // row tid's references rise by these
+            if (tid < N) {
+              int a = float_order(s_wmax[tid]), c = float_order(s_nmax[tid]);
+#pragma unroll
+              for (int k = 1; k < 4; ++k) {
+                a = max(a, float_order(s_wmax[k * N + tid]));
+                c = max(c, float_order(s_nmax[k * N + tid]));
+              }
+              up = order_float(a);
+              un = order_float(c);
+              if (up == -INFINITY || (t > 0 && up < 0.0f)) up = 0.0f;
+              if (un == -INFINITY || (t > 0 && un < 0.0f)) un = 0.0f;
+            }
+            named_bar_sync(2, C::SOFT);
+            if (tid < N) {
+              s_m[tid] += up;
+              s_d[tid] = pass == 0 ? (float)vref : s_d[tid] + (un - up);
+              s_wmax[tid] = up;
+              s_nmax[tid] = un;
+            }
+            named_bar_sync(2, C::SOFT);
+#pragma unroll
+            for (int j = 0; j < RW; ++j) z[j] -= s_wmax[row0 + j];
+            if (t > 0) {
+              ok = ok && pv_wait(t - 1);
+              tc_fence_after();
+#pragma unroll
+              for (int j = 0; j < RW; ++j) l_sum[j] *= exp2f(-s_wmax[row0 + j]);
+#pragma unroll
+              for (int part = 0; part < 2; ++part) {
+                float o[RW];
+                tmem_ld<RW>(trow + C::O_COL + part * N + row0, o);
+#pragma unroll
+                for (int j = 0; j < RW; ++j) o[j] *= exp2f(-s_nmax[row0 + j]);
+                tmem_st<RW>(trow + C::O_COL + part * N + row0, o);
+              }
+              tc_fence_before();
+            }
+            named_bar_sync(2, C::SOFT);                   // the maxima are read: the next tile may rewrite them
+          }
+        }
+        // The P buffer is free: S(t) was issued behind the product of tile t - 2, and its
+        // commit stands for everything issued before it.
+        const int dv = ev - vref;
+        far = far || (ev != -1000 && (dv > kVRange || dv < -kVRange));
+        const float vf = bad || !seen ? 0.0f : __uint_as_float((uint32_t)(127 + min(max(dv, -kVRange), kVRange)) << 23);
+        uint8_t* prow = sP + b * C::P_BYTES;
+        uint8_t* sf = sSF + (2 + b) * C::SF_BYTES;
+        // probabilities, and each row's largest of the warp's 32 keys: lane j (modulo RW) keeps row j's
+        uint32_t top_me = 0;
+        const uint64_t vf2 = f32x2(vf, vf);
+#pragma unroll
+        for (int j = 0; j < RW; j += 2) {
+          const uint64_t pr = f32x2(ex2(z[j]), ex2(z[j + 1]));
+          const float2 l = f32x2_get(add_f32x2(f32x2(l_sum[j], l_sum[j + 1]), pr));
+          l_sum[j] = l.x;
+          l_sum[j + 1] = l.y;
+          if (__builtin_expect(pass == 0, 1)) {
+            const float2 pv = f32x2_get(mul_f32x2(pr, vf2));
+            z[j] = pv.x;
+            z[j + 1] = pv.y;
+          } else {
+            z[j] = ex2(z[j] + (float)ev - s_d[row0 + j]);
+            z[j + 1] = ex2(z[j + 1] + (float)ev - s_d[row0 + j + 1]);
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t r = __reduce_max_sync(0xffffffffu, __float_as_uint(z[j + e]));
+            if ((lane & (RW - 1)) == j + e) top_me = r;
+          }
+        }
+        most = max(most, top_me);
+        // the block's scale puts its largest probability into [128, 256); the lanes work out a row each
+        const int byte_me = min(max((int)(top_me >> 23) - 7, 4), 247);
+        float* inv = s_inv + (warp - 2) * RW;
+        if (lane < RW) inv[lane] = __uint_as_float((uint32_t)(254 - byte_me) << 23);
+        if (lane < 2 * RW) {
+          // lanes 0 .. RW-1: the scale bytes of the hi rows for this warp's keys, the next RW: of the lo rows
+          const int r = row0 + (lane & (RW - 1)) + (lane < RW ? 0 : N);
+          sf[(r & 31) * 16 + (r >> 5) * 4 + q4] = (uint8_t)(lane < RW ? byte_me : byte_me - 4);
+        }
+        __syncwarp();
+        uint32_t hi[RW / 4], lo[RW / 4];
+#pragma unroll
+        for (int j = 0; j < RW; j += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(inv + j);
+          // hi: the nearest code; lo: what it leaves, at most a 16th of it, in a scale 2^4 smaller
+          const float2 a = f32x2_get(mul_f32x2(f32x2(z[j], z[j + 1]), f32x2(f.x, f.y)));
+          const float2 c = f32x2_get(mul_f32x2(f32x2(z[j + 2], z[j + 3]), f32x2(f.z, f.w)));
+          const uint32_t x0 = pack_f16x2(a.x, a.y), x1 = pack_f16x2(c.x, c.y);
+          const uint32_t h0 = cvt_e4m3x2_f16x2(x0), h1 = cvt_e4m3x2_f16x2(x1);
+          hi[j >> 2] = h0 | (h1 << 16);
+          lo[j >> 2] = cvt_e4m3x2_f16x2(sub_mul16_f16x2(x0, cvt_f16x2_e4m3x2((uint16_t)h0))) |
+                       (cvt_e4m3x2_f16x2(sub_mul16_f16x2(x1, cvt_f16x2_e4m3x2((uint16_t)h1))) << 16);
+        }
+        uint8_t* ph = prow + swizzled<C::P_ROW>(key_l, row0 >> 4) + (row0 & 15);
+        uint8_t* pl = prow + swizzled<C::P_ROW>(key_l, (N + row0) >> 4) + ((N + row0) & 15);
+        if constexpr (RW == 8) {
+          *reinterpret_cast<uint2*>(ph) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(pl) = make_uint2(lo[0], lo[1]);
+        } else {
+          *reinterpret_cast<uint4*>(ph) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(pl) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        if ((t0 + t + 1) * KT > lim_max && row0 == 0) {
+          // the last tile runs past every row's limit: whatever bytes lie there
+          // (codes of NaN among them) must not meet the zero probabilities
+          const int u = 2 * T + 1, slot = u % C::SLOTS;
+          ok = __all_sync(0xffffffffu, mbar_wait_long(&full[slot], (uint32_t)(u / C::SLOTS) & 1u, abort_flag, err, ERR_ATTN_FULL)) &&
+               ok;
+          if (!seen) {
+#pragma unroll
+            for (int c = 0; c < HD / 16; ++c)
+              *reinterpret_cast<uint4*>(sKV + slot * C::SLOT + key_l * HD + c * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pready[b]);
       }
-      fence_async_smem();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pready[b]);
+      if (nt > 0) {
+        if (ok) ok = pv_wait(nt - 1);
+        tc_fence_after();
+      }
+      // a product or a sum over what float32 and the block scales hold (a NaN is no reason)
+      constexpr uint32_t kOver = (uint32_t)(127 + kRefFixed) << 23;
+      bool over = far || (most >= kOver && most <= 0x7f800000u);
+#pragma unroll
+      for (int j = 0; j < RW; ++j) over = over || l_sum[j] >= __uint_as_float(kOver);
+      if (pass == 0 && over) *again = 1;
     }
+    // lanes that skipped their role arrive here first: reconverge before the CTA-wide barrier
+    __syncwarp();
+    __syncthreads();
+    if (pass > 0 || *again == 0) break;
+  }
+
+  if (warp >= 2) {
     // ------------------------------------------------------ sums and output
+    const int q4 = warp & 3, key_l = q4 * 32 + lane, row0 = ((warp - 2) >> 2) * RW;
+    const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
     if (nt > 0) {
-      if (ok) ok = pv_wait(nt - 1);
       tc_fence_after();
       // sum RW columns over the warp: lane c (modulo RW) ends with column c
 #pragma unroll
@@ -547,7 +618,6 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
       named_bar_sync(2, C::SOFT);
     }
     const int dim = key_l;
-    const float vs = scale_value(127 + vref);
     const long long slot = (long long)item * p.splits + split;
     float a[RW] = {}, bl[RW] = {};
     if (nt > 0) {
@@ -561,7 +631,9 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
         if (r >= n_rows) break;
         float l = 0.0f;
         if (nt > 0) l = (s_wmax[r] + s_wmax[N + r]) + (s_wmax[2 * N + r] + s_wmax[3 * N + r]);
-        const float v = l == 0.0f ? 0.0f : (a[j] + bl[j]) / l * vs;
+        // 2^d in two steps: it alone may leave the range that the result is in
+        const float vs = exp2f(0.5f * s_d[r]);
+        const float v = l == 0.0f ? 0.0f : (a[j] + bl[j]) / l * vs * vs;
         if (p.splits > 1) {
           p.ws_o[(slot * N + r) * HD + dim] = v;
           if (dim < 2) p.ws_ml[(slot * N + r) * 2 + dim] = dim ? l : (nt > 0 ? s_m[r] : 0.0f);

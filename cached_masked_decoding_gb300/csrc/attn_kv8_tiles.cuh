@@ -10,8 +10,8 @@
 // it); vref follows the largest exponent.  P is a half too, 2^7 p: 11 bits down to
 // 2^-21 of the row's reference.  Where a tile's value exponents reach more than 2^10
 // below vref (a loud value may then count although its p is far below 2^-21), the
-// codes stay unscaled from there on, p takes the factor 2^(ev - vref) in 32 bits, and
-// the products get a reference of their own.  With P as two e4m3 codes and V untouched, as
+// codes stay unscaled from there on, P is formed from the score plus the value's
+// exponent, and the products get a reference of their own.  With P as two e4m3 codes and V untouched, as
 // for few rows, the softmax needed 16 instructions a score and a causal prefill
 // of 4096 rows 259 us; converting 64 V rows costs 1.5 a code, shared by 128
 // query rows, and leaves the softmax about 4.
@@ -78,8 +78,8 @@ __global__ void __launch_bounds__(512, 2)
   uint8_t* sSF = sH + 2 * C::V_BYTES;                   // scale atoms: queries, K (two)
   int* s_vref = reinterpret_cast<int*>(sSF + 3 * C::SF_BYTES);   // [2]
   int* s_wide = s_vref + 2;                             // [2] value scales far apart
-  float* s_vf = reinterpret_cast<float*>(s_wide + 2);   // [2][KT] factors of P then
-  float* s_hf = s_vf + 2 * KT;                          // [2][KT] factors of V's halves
+  float* s_ev = reinterpret_cast<float*>(s_wide + 2);   // [2][KT] their exponents then
+  float* s_hf = s_ev + 2 * KT;                          // [2][KT] factors of V's halves
   int* s_lim = reinterpret_cast<int*>(s_hf + 2 * KT);   // [N]
   float* s_top = reinterpret_cast<float*>(s_lim + N);   // [2][N] a row's two halves: largest scores, sums
   float* s_most = s_top + 2 * N;                        // [2][N] largest products
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(512, 2)
       };
       if (nt > 0) fetch(0);
       bool ok = true;
-      int vref = -127;
+      int vref = -127, low = 1000;
       bool wide = false;
       auto wait = [&](uint64_t* bar, int phase) {
         return __all_sync(0xffffffffu, mbar_wait_long(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(512, 2)
           }
           fetch(t + 4);
         }
-        int kc[2], ev[2], top = -1000, low = 1000;          // -1000: no value to refer to
+        int kc[2], ev[2], top = -1000;                      // -1000: no value to refer to
         bool bad[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(512, 2)
           low = min(low, ev[j] == -1000 ? 1000 : ev[j]);
         }
         top = __reduce_max_sync(0xffffffffu, top);
-        low = __reduce_min_sync(0xffffffffu, low);
+        low = __reduce_min_sync(0xffffffffu, low);          // of the tiles so far
         if (top - vref > (t == 0 ? 0 : kVSlack)) vref = top;
         wide = wide || vref - low > kVSpread;
         // tile t - 2's scores are computed and its references and factors read
@@ -316,9 +316,9 @@ __global__ void __launch_bounds__(512, 2)
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float f = ev[j] == -1000 ? 0.0f : exp2f((float)(ev[j] - vref));
-          s_vf[b * KT + 32 * j + lane] = f;
-          s_hf[b * KT + 32 * j + lane] = wide && f != 0.0f ? 1.0f : f;
+          const bool none = ev[j] == -1000;
+          s_ev[b * KT + 32 * j + lane] = none ? 0.0f : (float)ev[j];
+          s_hf[b * KT + 32 * j + lane] = none ? 0.0f : wide ? 1.0f : exp2f((float)(ev[j] - vref));
         }
         fence_async_smem();
         __syncwarp();
@@ -375,7 +375,8 @@ __global__ void __launch_bounds__(512, 2)
     // ------------------------------------------------------ the keys
     float m = 0.0f;                                       // reference (base 2) of this row
     uint64_t l2 = 0;                                      // its sum, times 2^7, in two parts
-    int vref = 0, r = 0;                                  // O is in units of 2^(vref + r)
+    int vref = 0;
+    float d = 0.0f;                                       // O is in units of 2^(m + d): d = vref until scales lie far apart
     // After a wait that gave up (ok false) the loop goes on, so that every warp meets
     // every barrier; the outputs are invalid and reported.
     bool ok = true;
@@ -427,23 +428,17 @@ __global__ void __launch_bounds__(512, 2)
         named_bar_sync(3 + q4, 64);
         top = fmaxf(top, s_top[(hf ^ 1) * N + row]) * p.scale_log2;
         const bool up = t == 0 ? top > -INFINITY : top > m + kRowSlack;
-        const bool moved = __any_sync(0xffffffffu, up) || vn != vref;
-        float corr = 1.0f;                                // of the row's old sums
-        if (moved) {
-          const float mn = up ? top : m;
-          if (t > 0) corr = exp2f(m - mn);
-          l2 = mul_f32x2(l2, f32x2(corr, corr));
-          m = mn;
-        }
-        // this half's dims of O times corr * 2^e; exponents below -126 leave nothing of the old
-        // sums that counts
-        auto rescale = [&](int e) {
+        const bool moved = __any_sync(0xffffffffu, up) || (!wide && vn != vref);
+        const float mn = up ? top : m;
+        const float corr = t > 0 ? exp2f(m - mn) : 1.0f;  // of the row's old sums
+        if (moved) l2 = mul_f32x2(l2, f32x2(corr, corr));
+        // this half's dims of O times f
+        auto rescale = [&](float f) {
           if (!wait(&pvdone[b ^ 1], (t - 1) >> 1)) {
             ok = false;
             return;
           }
           tc_fence_after();
-          const float f = e < -126 ? 0.0f : corr * scale_value(127 + e);
 #pragma unroll 1
           for (int c = hf * (HD / 2); c < (hf + 1) * (HD / 2); c += 16) {
             float o[16];
@@ -456,7 +451,11 @@ __global__ void __launch_bounds__(512, 2)
         };
         tile2 = 0;
         if (!wide) {
-          if (moved && t > 0) rescale(vref - vn);
+          m = mn;
+          // exponents below -126 leave nothing of the old sums that counts
+          if (moved && t > 0) rescale(vref - vn < -126 ? 0.0f : corr * scale_value(127 + vref - vn));
+          vref = vn;
+          d = (float)vn;
 #pragma unroll
           for (int c = 0; c < KH; c += 2) {
             const float p0 = ex2(fmaf(s[c], p.scale_log2, kPShift - m));
@@ -465,31 +464,26 @@ __global__ void __launch_bounds__(512, 2)
             ph[c >> 1] = pack_f16x2(p0, p1);
           }
         } else {
-          float most = 0.0f;
+          if (t > 0) d -= mn - m;                         // the products keep their reference m + d
+          m = mn;
+          float most = -INFINITY;
 #pragma unroll
           for (int c = 0; c < KH; ++c) {
-            const float pr = ex2(fmaf(s[c], p.scale_log2, kPShift - m));
-            tile2 = add_f32x2(tile2, f32x2(pr, 0.0f));
-            s[c] = pr * s_vf[b * KT + hf * KH + c];
+            const float z = fmaf(s[c], p.scale_log2, -m);
+            tile2 = add_f32x2(tile2, f32x2(ex2(z + kPShift), 0.0f));
+            s[c] = z + (s_ev[b * KT + hf * KH + c] - d);
             most = fmaxf(most, s[c]);
           }
           s_most[hf * N + row] = most;
           named_bar_sync(3 + q4, 64);
           most = fmaxf(most, s_most[(hf ^ 1) * N + row]);
-          // The products' reference 2^r rises before a half would overflow, and falls to
-          // the new products' size when vref's rise has made room for the old sums.
-          const int e = (int)(__float_as_uint(most) >> 23) - 127 - 7;
-          int rn = r;
-          if (most > 0.0f && (t == 0 || e > r + 7)) rn = e;
-          if (most > 0.0f && t > 0 && vn > vref && e < r) rn = max(e, r - (vn - vref));
-          const int de = vref - vn + r - rn;
-          if (t > 0 && __any_sync(0xffffffffu, moved || de != 0)) rescale(de);
-          r = rn;
-          const float inv = exp2f((float)-r);
+          const float un = most > -INFINITY && (t == 0 || most > kRowSlack) ? most : 0.0f;
+          d += un;
+          if (t > 0 && __any_sync(0xffffffffu, un != 0.0f)) rescale(exp2f(-un));
 #pragma unroll
-          for (int c = 0; c < KH; c += 2) ph[c >> 1] = pack_f16x2(s[c] * inv, s[c + 1] * inv);
+          for (int c = 0; c < KH; c += 2)
+            ph[c >> 1] = pack_f16x2(ex2(s[c] - un + kPShift), ex2(s[c + 1] - un + kPShift));
         }
-        vref = vn;
       }
       l2 = add_f32x2(l2, tile2);
       // P is free once the last product is done
@@ -508,7 +502,8 @@ __global__ void __launch_bounds__(512, 2)
     s_top[hf * N + row] = lp.x + lp.y;
     named_bar_sync(3 + q4, 64);
     const float l_sum = s_top[row] + s_top[N + row];
-    const float f = l_sum == 0.0f ? 0.0f : ldexpf(1.0f / l_sum, vref + r);
+    // 2^d in two steps: it alone may leave the range that the result is in
+    const float f = l_sum == 0.0f ? 0.0f : exp2f(0.5f * d) / l_sum, f2 = exp2f(0.5f * d);
     uint32_t jh;
     const int i = (int)p.by_group.divmod((uint32_t)(rt * N + row), jh), h = g * p.group + (int)jh;
     const bool valid = row < n_rows;
@@ -527,7 +522,7 @@ __global__ void __launch_bounds__(512, 2)
         float4* dst = reinterpret_cast<float4*>(p.ws_o + ws_row * HD + c);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          dst[e] = make_float4(o[4 * e] * f, o[4 * e + 1] * f, o[4 * e + 2] * f, o[4 * e + 3] * f);
+          dst[e] = make_float4(o[4 * e] * f * f2, o[4 * e + 1] * f * f2, o[4 * e + 2] * f * f2, o[4 * e + 3] * f * f2);
       } else {
         uint4* dst = reinterpret_cast<uint4*>(p.out + ((long long)seq * p.R + i) * p.o_rs + (long long)h * HD + c);
 #pragma unroll
@@ -535,7 +530,7 @@ __global__ void __launch_bounds__(512, 2)
           uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(o[8 * e + 2 * k] * f, o[8 * e + 2 * k + 1] * f);
+            const __nv_bfloat162 v = __floats2bfloat162_rn(o[8 * e + 2 * k] * f * f2, o[8 * e + 2 * k + 1] * f * f2);
             w[k] = *reinterpret_cast<const uint32_t*>(&v);
           }
           dst[e] = make_uint4(w[0], w[1], w[2], w[3]);

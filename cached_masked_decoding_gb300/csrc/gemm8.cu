@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(224, 2)
       RingPos r{0, 0u};
       int issued = 0;
       for (int i = 0; i < nc; ++i) {
-        if (i >= S && !mbar_wait(&empty[r.s], r.par ^ 1u, abort_flag, err, ERR_GEMM_EMPTY)) break;
+        if (i >= S && !mbar_wait_long(&empty[r.s], r.par ^ 1u, abort_flag, err, ERR_GEMM_EMPTY)) break;
         mbar_arrive_expect_tx(&full[r.s], C::A_BYTES + C::B_BYTES);
         tma_load_3d(sA + r.s * C::A_BYTES, &tmW, &full[r.s], (c0 + i) * kQBlock, m0, 0, pol_w);
         tma_load_3d(sB + r.s * C::B_BYTES, &tmX, &full[r.s], (c0 + i) * kQBlock, n0, 0, pol_x);
@@ -168,14 +168,14 @@ __global__ void __launch_bounds__(224, 2)
       }
       if (*abort_flag)   // let copies in flight land before the CTA's shared memory goes away
         for (int i = issued > S ? issued - S : 0; i < issued; ++i)
-          mbar_wait(&full[i % S], (uint32_t)(i / S) & 1u, nullptr, err, ERR_GEMM_DRAIN);
+          mbar_wait_long(&full[i % S], (uint32_t)(i / S) & 1u, nullptr, err, ERR_GEMM_DRAIN);
     }
   } else if (warp == 1) {
     const uint32_t lead = elect_one();
     constexpr uint32_t idesc = idesc_mxf8(128, BN);
     RingPos r{0, 0u};
     for (int i = 0; i < nc; ++i) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&full[r.s], r.par, abort_flag, err, ERR_GEMM_FULL))) break;
+      if (!__all_sync(0xffffffffu, mbar_wait_long(&full[r.s], r.par, abort_flag, err, ERR_GEMM_FULL))) break;
       tc_fence_after();
       const uint32_t a0 = smem_u32(sA + r.s * C::A_BYTES), b0 = smem_u32(sB + r.s * C::B_BYTES);
       const uint32_t f0 = smem_u32(sF + r.s * C::SF_BYTES);
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(224, 2)
       for (int e = 0; e < AHEAD; ++e) {
         if (i0 + e >= nc || !ok) break;
         if (i0 + e >= S &&
-            !__all_sync(0xffffffffu, mbar_wait(&empty[r.s], r.par ^ 1u, abort_flag, err, ERR_GEMM_EMPTY))) {
+            !__all_sync(0xffffffffu, mbar_wait_long(&empty[r.s], r.par ^ 1u, abort_flag, err, ERR_GEMM_EMPTY))) {
           ok = false;
           break;
         }
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(224, 2)
       static_cast<float*>(p.y)[o] = v;
   };
   if (epi) {
-    const bool ok = __all_sync(0xffffffffu, mbar_wait(done, 0u, abort_flag, err, ERR_GEMM_TFULL));
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_long(done, 0u, abort_flag, err, ERR_GEMM_TFULL));
     (void)ok;   // after a wait that gave up the outputs are invalid and reported as such
     tc_fence_after();
   }

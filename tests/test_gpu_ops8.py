@@ -294,7 +294,7 @@ def _attend(torch, q, ca, lim, H, R, scale=None, stream=0):
     return out
 
 
-def _attention_check(got, q, ca, limits, scale):
+def _attention_check(got, q, ca, limits, scale, lost=0.0):
     b, R, H, hd = got.shape
     k, v = ca.values(0), ca.values(1)
     for s in range(b):
@@ -302,7 +302,7 @@ def _attention_check(got, q, ca, limits, scale):
         want, pv, sk = ref.attention(q[s], k[s], v[s], lim, scale)
         # a score: hd products summed in float32, under hd * 2^-24 of sum |q||k|, moves p by as much, the sum
         # too; exp2 and the sums 2^-20; P rounded to bf16: 2^-8 of sum p|v|; the output: 2^-8 of itself
-        tol = (2.0 ** -8 + 2.0 ** -20 + 2 * hd * 2.0 ** -24 * sk) * pv + 2.0 ** -8 * np.abs(want)
+        tol = (2.0 ** -8 + 2.0 ** -20 + 2 * hd * 2.0 ** -24 * sk) * pv + 2.0 ** -8 * np.abs(want) + lost
         err = np.abs(got[s] - want)
         assert (err <= tol).all(), f"seq {s}: {(err / (tol + 1e-300)).max():.2f} of the tolerance"
 
@@ -396,6 +396,25 @@ def test_attention_value_scales_of_any_size(torch, hd, R, H, h):
     ca.scales[1].copy_(dev(torch, np.where(e > 100, 27, 20).astype(np.uint8)))
     got = f64(_attend(torch, q, ca, None, H, R))
     _attention_check(got, f64(q), ca, None, hd ** -0.5)
+
+
+@pytest.mark.parametrize("R,H,h", [(1, 8, 2), (1, 16, 1), (32, 4, 4), (64, 1, 1), (130, 2, 1)])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attention_values_that_grow_or_vanish(torch, hd, R, H, h):
+    """Value scales far below 1 in the first tiles of keys and far above it in the
+    last, and the other way round; scores that grow with them."""
+    rng = np.random.default_rng(13)
+    T = 600
+    for lo, hi in ((20, 230), (230, 20), (27, 227)):
+        q, ca, _ = _attention_case(torch, rng, 1, R, H, h, T, hd, None, loud=8.0)
+        e = np.full((1, h, T), lo, dtype=np.uint8)
+        e[:, :, 400:] = hi
+        e[:, :, 500] = 127
+        ca.scales[1].copy_(dev(torch, e))
+        got = f64(_attend(torch, q, ca, None, H, R))
+        # the sums are float32 in units of the largest value scale: each of T products loses at most
+        # 2^-126 of it to underflow, T * 448 * 2^-126 < 2^-100
+        _attention_check(got, f64(q), ca, None, hd ** -0.5, lost=2.0 ** (max(lo, hi) - 127 - 100))
 
 
 @pytest.mark.parametrize("R,H,h", [(1, 8, 2), (16, 4, 4), (140, 2, 1)])
