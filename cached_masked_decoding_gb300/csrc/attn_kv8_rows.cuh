@@ -21,10 +21,10 @@
 //
 // Softmax runs with one key a thread and RW rows in its registers: nothing is
 // reduced across threads per tile but the 32-key maximum of each row (one
-// redux).  A row's reference is its maximum over the CTA's first tile, and stays:
+// redux).  A row's reference is its maximum over the CTA's first 32 keys, and stays:
 // float32 sums and block scales hold what exceeds it by up to 2^110, so the
 // warps meet at no barrier after the first tile.  A CTA that met more, or
-// value scales over 2^60 apart, walks its keys again with references that follow the
+// value scales over 2^60 from the first keys', walks its keys again with references that follow the
 // scores, and others that follow the products (score plus value exponent).  Sums l
 // are kept per key lane and joined once at the end.  This is the longest of the
 // overlapped stages, so the rows of a tile are shared out over N / RW groups of
@@ -77,7 +77,7 @@ struct AttnRowsCfg {
   static constexpr int P_BYTES = KT * P_ROW;
   static constexpr int SLOTS = CTAS == 1 ? (HD == 64 ? 16 : 9) : HD == 64 ? 8 : N == 32 ? 5 : 6;
   static constexpr int SF_BYTES = 512;                  // ones, query scales, two buffers of probability scales
-  static constexpr int STAT_FLOATS = 8 * N + 4 + 3 * N + 4 * N;  // warp maxima (two), warp value exponents, m, d, limits, scales
+  static constexpr int STAT_FLOATS = 8 * N + 3 * N + 4 * N;  // warp maxima (two), m, d, limits, scales
   static constexpr int SMEM_BYTES = 1024 + SLOTS * SLOT + Q_PARTS * Q_BYTES + 2 * P_BYTES + 4 * SF_BYTES +
                                     STAT_FLOATS * 4 + (2 * SLOTS + 10) * 8 + 24;
   static constexpr int S_COL = 0;                       // two buffers
@@ -179,8 +179,7 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
   uint8_t* sSF = sP + 2 * C::P_BYTES;                   // scale atoms: ones, queries, a P buffer each
   float* s_wmax = reinterpret_cast<float*>(sSF + 4 * C::SF_BYTES);   // [4][N]
   float* s_nmax = s_wmax + 4 * N;                       // [4][N]
-  int* s_wev = reinterpret_cast<int*>(s_nmax + 4 * N);  // [4]
-  float* s_m = reinterpret_cast<float*>(s_wev + 4);     // [N] reference maxima
+  float* s_m = s_nmax + 4 * N;                          // [N] reference maxima
   float* s_d = s_m + N;                                 // [N] O is in units of 2^(m + d)
   int* s_lim = reinterpret_cast<int*>(s_d + N);         // [N]
   float* s_inv = reinterpret_cast<float*>(s_lim + N);   // [softmax warps][RW] inverse block scales
@@ -255,9 +254,7 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
   const int t0 = (int)((long long)tiles * split / p.splits), t1 = (int)((long long)tiles * (split + 1) / p.splits);
   const int nt = t1 - t0;
 
-  // softmax: a row's sums, the reference of the value scales
-  float l_sum[RW];
-  int vref = 0;
+  float l_sum[RW];                                        // softmax: this key lane's sums of its rows
   // tiles count on through the second walk: T of a tile is pass * nt + t
   for (int pass = 0;; ++pass) {
     const int base = pass * nt;
@@ -271,7 +268,8 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
               !mbar_wait_long(&empty[slot], (uint32_t)(u / C::SLOTS - 1) & 1u, abort_flag, err, ERR_ATTN_FULL))
             break;
           mbar_arrive_expect_tx(&full[slot], C::SLOT);
-          tma_load_3d(sKV + slot * C::SLOT, (u & 1) ? &tmV : &tmK, &full[slot], 0, (t0 + (u >> 1) - base) * KT, plane, pol);
+          tma_load_3d(sKV + slot * C::SLOT, (u & 1) ? &tmV : &tmK, &full[slot], 0, (t0 + (u >> 1) - base) * KT, plane,
+                      pol);
           issued = u + 1;
         }
         if (*abort_flag)   // let copies in flight land before the CTA's shared memory goes away
@@ -332,8 +330,8 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
         mbar_wait_long(mdone, (uint32_t)pass & 1u, nullptr, err, ERR_ATTN_FULL);
       }
     } else {
-      const int q4 = warp & 3, key_l = q4 * 32 + lane;      // this thread's key in a tile, and its tensor-memory lane
-      const int row0 = ((warp - 2) >> 2) * RW;              // its first row
+      const int q4 = warp & 3, key_l = q4 * 32 + lane;    // this thread's key in a tile, and its tensor-memory lane
+      const int row0 = ((warp - 2) >> 2) * RW;            // its first row
       const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
       const int tid = (warp - 2) * 32 + lane;
       // product t of P V is done
@@ -342,22 +340,22 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
         return __all_sync(0xffffffffu, mbar_wait_long(&pvdone[T & 1], (uint32_t)(T >> 1) & 1u, abort_flag, err,
                                                       ERR_ATTN_FULL)) != 0;
       };
+      // Scale bytes of this thread's key in four tiles, and of the next four in
+      // flight (their latency under load is over a tile's time).  Positions past every
+      // limit read the last key's and are of no account.
       const uint8_t* ksc = p.c.k_scale + (long long)plane * p.c.T;
       const uint8_t* vsc = p.c.v_scale + (long long)plane * p.c.T;
-      // scale bytes of this thread's key in four tiles, and of the next four in
-      // flight: fetched a tile ahead, their latency was the loop's (1.7 us a tile)
       uint32_t kb4 = 0, vb4 = 0;
       int kn[4], vn[4];
       auto fetch = [&](int t) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int key = (t0 + t + e) * KT + key_l;
-          const bool in = t + e < nt && key < lim_max;
-          kn[e] = in ? __ldg(ksc + key) : 127;
-          vn[e] = in ? __ldg(vsc + key) : 127;
+          const int key = min((t0 + t + e) * KT + key_l, lim_max - 1);
+          kn[e] = __ldg(ksc + key);
+          vn[e] = __ldg(vsc + key);
         }
       };
-      fetch(0);
+      if (nt > 0) fetch(0);
       if (pass > 0) {
         if (tid < N) s_m[tid] = s_d[tid] = 0.0f;
         named_bar_sync(2, C::SOFT);
@@ -367,7 +365,7 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
 #pragma unroll
           for (int f = 0; f < 4; ++f) reinterpret_cast<uint32_t*>(sSF + f * C::SF_BYTES)[tid] = 0x7f7f7f7fu;
         }
-        if (tid < N) s_m[tid] = s_d[tid] = 0.0f;
+        if (tid < N) s_m[tid] = 0.0f;
         named_bar_sync(2, C::SOFT);
         // 8 rows: the lo rows lie behind the hi rows of one operand
         attn_query_tile<HD, N, C::SOFT>(p, seq, g, rt, n_rows, tid, sQ, sQ + (C::Q_PARTS - 1) * C::Q_BYTES,
@@ -379,9 +377,9 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
       // ------------------------------------------------------ the keys
 #pragma unroll
       for (int n = 0; n < RW; ++n) l_sum[n] = 0.0f;
-      vref = 0;
-      uint32_t most = 0;                                    // largest block maximum of this lane's row
-      bool far = false;                                     // a value scale far from the first tile's
+      int vref = 0;                                       // the value scales' reference
+      uint32_t most = 0;                                  // largest block maximum of this lane's row
+      bool far = false;                                   // a value scale far from the first ones
       // After a wait that gave up (ok false) the loop goes on without waiting, so
       // that every warp meets every barrier; the outputs are invalid and reported.
       bool ok = true;
@@ -389,6 +387,11 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
         const int T = base + t, b = T & 1;                  // S and P buffer
         const int key = (t0 + t) * KT + key_l;
         if ((t & 3) == 0) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            due(kn[e]);
+            due(vn[e]);
+          }
           kb4 = (uint32_t)(kn[0] | kn[1] << 8 | kn[2] << 16 | kn[3] << 24);
           vb4 = (uint32_t)(vn[0] | vn[1] << 8 | vn[2] << 16 | vn[3] << 24);
           fetch(t + 4);
@@ -396,10 +399,10 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
         const int kb = (int)(kb4 & 255u), vb = (int)(vb4 & 255u);
         kb4 >>= 8;
         vb4 >>= 8;
-        const bool seen = key < lim_max;                    // by some row
+        const bool seen = key < lim_max;                  // by some row
         const bool bad = kb == kScaleNan || vb == kScaleNan;
         const float kf = bad ? __uint_as_float(0x7fffffffu) : scale_value(kb) * p.scale_log2;
-        const int ev = bad || !seen ? -1000 : vb - 127;     // -1000: no value scale to refer to
+        const int ev = bad || !seen ? -1000 : vb - 127;   // -1000: no value scale to refer to
         ok = __all_sync(0xffffffffu, mbar_wait_long(&sfull[b], (uint32_t)(T >> 1) & 1u, abort_flag, err, ERR_ATTN_FULL)) &&
              ok;
         tc_fence_after();
@@ -417,9 +420,11 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
         __syncwarp();
         if (lane == 0) mbar_arrive(&sfree[b]);
         const uint64_t kf2 = f32x2(kf, kf);
+        const bool first = t == 0 && pass == 0;           // no references yet: other warps may be writing them
 #pragma unroll
         for (int j = 0; j < RW; j += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(s_m + row0 + j);
+          const float4 m =
+              first ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4*>(s_m + row0 + j);
           const float2 za = f32x2_get(fma_f32x2(f32x2(z[j], z[j + 1]), kf2, f32x2(-m.x, -m.y)));
           const float2 zb = f32x2_get(fma_f32x2(f32x2(z[j + 2], z[j + 3]), kf2, f32x2(-m.z, -m.w)));
           z[j] = za.x;
@@ -431,32 +436,44 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
 #pragma unroll
           for (int j = 0; j < RW; ++j) z[j] = key < s_lim[row0 + j] ? z[j] : -INFINITY;
         }
-        if (t == 0 || pass > 0) {
-          bool need = t == 0;
-          const float evf = (float)ev;                    // of no account where the score is -inf or NaN
-          if (pass > 0) {
-            float top = -INFINITY;
+        if (first) {
+          // the references: over the first quarter's keys (key 0 is seen wherever any is)
+          if (q4 == 0) {
+            float mine = 0.0f;
 #pragma unroll
-            for (int j = 0; j < RW; ++j) top = fmaxf(top, fmaxf(z[j], z[j] + evf - s_d[row0 + j]));
-            need = need || top > kRefSlack;
+            for (int j = 0; j < RW; ++j) {
+              const float top = order_float(__reduce_max_sync(0xffffffffu, float_order(z[j])));
+              if (lane == j) mine = top;
+            }
+            const int top_ev = max(__reduce_max_sync(0xffffffffu, ev), -127);
+            if (lane < RW) {
+              s_m[row0 + lane] = mine == -INFINITY ? 0.0f : mine;
+              s_d[row0 + lane] = (float)top_ev;
+            }
           }
+          named_bar_sync(2, C::SOFT);
+          vref = (int)s_d[0];
+#pragma unroll
+          for (int j = 0; j < RW; ++j) z[j] -= s_m[row0 + j];
+        } else if (__builtin_expect(pass > 0, 0)) {
+          bool need = t == 0;
+          float top = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < RW; ++j) top = fmaxf(top, fmaxf(z[j], z[j] + (float)ev - s_d[row0 + j]));
+          need = need || top > kRefSlack;
           if (!ok) need = false;
           if (named_bar_or(2, C::SOFT, need)) {
-            // new references: the first tile's, or scores or products far above the last ones
+            // new references: the first tile's, or where scores or products lie far above the last ones
 #pragma unroll
             for (int j = 0; j < RW; ++j) {
               const int wt = __reduce_max_sync(0xffffffffu, float_order(z[j]));
-              const int nm = __reduce_max_sync(0xffffffffu, float_order(z[j] + evf - s_d[row0 + j]));
+              const int nm = __reduce_max_sync(0xffffffffu, float_order(z[j] + (float)ev - s_d[row0 + j]));
               if (lane == j) {
                 s_wmax[q4 * N + row0 + j] = order_float(wt);
                 s_nmax[q4 * N + row0 + j] = order_float(nm);
               }
             }
-            const int evw = __reduce_max_sync(0xffffffffu, ev);
-            if (row0 == 0 && lane == 0) s_wev[q4] = evw;
             named_bar_sync(2, C::SOFT);
-            const int ev_top = max(max(s_wev[0], s_wev[1]), max(s_wev[2], s_wev[3]));
-            if (pass == 0) vref = max(ev_top, -127);
             float up = 0.0f, un = 0.0f;                   // row tid's references rise by these
             if (tid < N) {
               int a = float_order(s_wmax[tid]), c = float_order(s_nmax[tid]);
@@ -473,7 +490,7 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
             named_bar_sync(2, C::SOFT);
             if (tid < N) {
               s_m[tid] += up;
-              s_d[tid] = pass == 0 ? (float)vref : s_d[tid] + (un - up);
+              s_d[tid] += un - up;
               s_wmax[tid] = up;
               s_nmax[tid] = un;
             }
@@ -502,7 +519,7 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
         // commit stands for everything issued before it.
         const int dv = ev - vref;
         far = far || (ev != -1000 && (dv > kVRange || dv < -kVRange));
-        const float vf = bad || !seen ? 0.0f : __uint_as_float((uint32_t)(127 + min(max(dv, -kVRange), kVRange)) << 23);
+        const float vf = ev == -1000 ? 0.0f : __uint_as_float((uint32_t)(127 + min(max(dv, -kVRange), kVRange)) << 23);
         uint8_t* prow = sP + b * C::P_BYTES;
         uint8_t* sf = sSF + (2 + b) * C::SF_BYTES;
         // probabilities, and each row's largest of the warp's 32 keys: lane j (modulo RW) keeps row j's
@@ -615,31 +632,49 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
 #pragma unroll
       for (int s = RW; s < 32; s <<= 1) l_sum[0] += __shfl_xor_sync(0xffffffffu, l_sum[0], s);
       if (lane < RW) s_wmax[q4 * N + row0 + lane] = l_sum[0];
-      named_bar_sync(2, C::SOFT);
     }
-    const int dim = key_l;
+    named_bar_sync(2, C::SOFT);
+    // per row: 2^d / l in two factors, and where its output goes
+    const int tid = (warp - 2) * 32 + lane;
     const long long slot = (long long)item * p.splits + split;
-    float a[RW] = {}, bl[RW] = {};
-    if (nt > 0) {
-      tmem_ld<RW>(trow + C::O_COL + row0, a);
-      tmem_ld<RW>(trow + C::O_COL + N + row0, bl);
+    float2* s_f = reinterpret_cast<float2*>(s_nmax);      // [N]
+    long long* s_to = reinterpret_cast<long long*>(s_nmax + 2 * N);   // [N]
+    if (tid < N) {
+      float l = 0.0f;
+      if (nt > 0) l = (s_wmax[tid] + s_wmax[N + tid]) + (s_wmax[2 * N + tid] + s_wmax[3 * N + tid]);
+      // 2^d in two steps: it alone may leave the range that the result is in
+      const float vs = exp2f(0.5f * s_d[tid]);
+      s_f[tid] = l == 0.0f ? make_float2(0.0f, 0.0f) : make_float2(vs / l, vs);
+      if (p.splits > 1) {
+        s_to[tid] = (slot * N + tid) * HD;
+        if (tid < n_rows)
+          *reinterpret_cast<float2*>(p.ws_ml + (slot * N + tid) * 2) = make_float2(nt > 0 ? s_m[tid] : 0.0f, l);
+      } else {
+        uint32_t j;
+        const uint32_t i = p.by_group.divmod((uint32_t)(rt * N + tid), j);
+        s_to[tid] = ((long long)seq * p.R + i) * p.o_rs + (long long)(g * p.group + (int)j) * HD;
+      }
     }
-    if (dim < HD) {
+    named_bar_sync(2, C::SOFT);
+    // (rolled: code that runs once a CTA costs its instruction fetches)
+    const int dim = key_l;
+#pragma unroll 1
+    for (int n = row0; n < row0 + RW; n += 4) {
+      float a[4] = {}, c[4] = {};
+      if (nt > 0) {
+        tmem_ld4(trow + C::O_COL + n, a);
+        tmem_ld4(trow + C::O_COL + N + n, c);
+      }
 #pragma unroll
-      for (int j = 0; j < RW; ++j) {
-        const int r = row0 + j;
-        if (r >= n_rows) break;
-        float l = 0.0f;
-        if (nt > 0) l = (s_wmax[r] + s_wmax[N + r]) + (s_wmax[2 * N + r] + s_wmax[3 * N + r]);
-        // 2^d in two steps: it alone may leave the range that the result is in
-        const float vs = exp2f(0.5f * s_d[r]);
-        const float v = l == 0.0f ? 0.0f : (a[j] + bl[j]) / l * vs * vs;
-        if (p.splits > 1) {
-          p.ws_o[(slot * N + r) * HD + dim] = v;
-          if (dim < 2) p.ws_ml[(slot * N + r) * 2 + dim] = dim ? l : (nt > 0 ? s_m[r] : 0.0f);
-        } else {
-          const int rn = rt * N + r, i = rn / p.group, h = g * p.group + rn % p.group;
-          p.out[((long long)seq * p.R + i) * p.o_rs + (long long)h * HD + dim] = f32_to_bf16_bits(v);
+      for (int j = 0; j < 4; ++j) {
+        const int r = n + j;
+        if (dim < HD && r < n_rows) {
+          const float2 f = s_f[r];
+          const float v = f.x == 0.0f ? 0.0f : (a[j] + c[j]) * f.x * f.y;
+          if (p.splits > 1)
+            p.ws_o[s_to[r] + dim] = v;
+          else
+            p.out[s_to[r] + dim] = f32_to_bf16_bits(v);
         }
       }
     }

@@ -283,6 +283,11 @@ __global__ void __launch_bounds__(512, 2)
         if ((t & 3) == 0) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              due(kn[e][j]);
+              due(vn[e][j]);
+            }
             kb4[j] = (uint64_t)(kn[0][j] | kn[1][j] << 16) | (uint64_t)(kn[2][j] | kn[3][j] << 16) << 32;
             vb4[j] = (uint64_t)(vn[0][j] | vn[1][j] << 16) | (uint64_t)(vn[2][j] | vn[3][j] << 16) << 32;
           }

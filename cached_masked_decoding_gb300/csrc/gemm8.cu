@@ -222,9 +222,15 @@ __global__ void __launch_bounds__(224, 2)
 #pragma unroll
       for (int e = 0; e < AHEAD; ++e) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) ca[e][j] = wa[e][j];
+        for (int j = 0; j < 4; ++j) {
+          due(wa[e][j]);
+          ca[e][j] = wa[e][j];
+        }
 #pragma unroll
-        for (int j = 0; j < WB; ++j) cb[e][j] = wb[e][j];
+        for (int j = 0; j < WB; ++j) {
+          due(wb[e][j]);
+          cb[e][j] = wb[e][j];
+        }
       }
       fetch(i0 + AHEAD);
 #pragma unroll

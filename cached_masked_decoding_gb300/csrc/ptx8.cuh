@@ -122,6 +122,15 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, float* v) {
+  uint32_t r[4];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
@@ -205,7 +214,7 @@ __device__ __forceinline__ bool mbar_try_wait_long(uint32_t addr, uint32_t parit
 }
 __device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort, int* err, int site) {
   const uint32_t a = smem_u32(bar);
-  if (mbar_try_wait_long(a, parity)) return true;
+  if (mbar_test_wait(a, parity) || mbar_try_wait_long(a, parity)) return true;
   const unsigned long long t0 = globaltimer();
   while (!mbar_try_wait_long(a, parity)) {
     if (abort && *abort) return false;
@@ -229,6 +238,12 @@ template <int N>
 __device__ __forceinline__ void setmaxnreg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
+
+// The value as of here: nothing computed from it moves in front of this point.  Kept on a
+// load's result until it is due - the compiler otherwise packs prefetched bytes at once
+// (fewer registers) and with that waits for the load where it is issued.
+__device__ __forceinline__ void due(int& v) { asm volatile("" : "+r"(v)); }
+__device__ __forceinline__ void due(uint32_t& v) { asm volatile("" : "+r"(v)); }
 
 // ----------------------------------------------------------------- pairs of floats
 __device__ __forceinline__ uint64_t f32x2(float a, float b) {
