@@ -18,34 +18,36 @@ cudaError_t attn_kv8_err_word(int** p) { return cudaGetSymbolAddress(reinterpret
 
 namespace {
 
+constexpr int kMaxCluster = 8;   // portable cluster size
+
 struct AttnKv8Plan {
-  int N, row_tiles, splits;
+  int N, row_tiles, splits, cluster;
   long long items;
   size_t ws_bytes;
 };
 
 // Rows of one cached head (R rows of H / H_kv heads) in tiles of N, the keys in
-// splits.  A CTA's time is taken as the tiles of keys that it walks, and a split's
-// partial results with the kernel that joins them as four tiles' (measured: 8B
-// block, 32 heads of 6 tiles: 15.7 us in six splits, 9.5 us in one); a round of
-// CTAs is two an SM, one with 64 rows.
+// splits.  A CTA's time is taken as the tiles of keys that it walks; the join of up
+// to 8 splits in a cluster as one tile's, that of more (or of 128-row tiles) through the
+// workspace as four of 128 keys.  A round of CTAs is two an SM, one with 64 rows.
 AttnKv8Plan plan_attn_kv8(long long b, long long H_kv, long long rows, int hd, int T) {
   AttnKv8Plan a;
   a.N = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
   a.row_tiles = (int)((rows + a.N - 1) / a.N);
   a.items = b * H_kv * a.row_tiles;
   const long long kt = a.N == 128 ? 64 : 128, tiles = (T + kt - 1) / kt;
-  const long long ctas = (a.N == 64 ? 1 : 2) * op_device_sms(), join = a.N == 128 ? 8 : 4;
+  const long long ctas = (a.N == 64 ? 1 : 2) * op_device_sms();
   long long best = (a.items + ctas - 1) / ctas * tiles;
   a.splits = 1;
   for (long long s = 2; s <= std::min(tiles, 64LL) && s * a.items <= ctas; ++s) {
-    const long long t = (tiles + s - 1) / s + join;
+    const long long t = (tiles + s - 1) / s + (a.N == 128 ? 8 : s <= kMaxCluster ? 1 : 4);
     if (t < best) {
       best = t;
       a.splits = (int)s;
     }
   }
-  a.ws_bytes = a.splits > 1 ? (size_t)a.items * a.splits * a.N * (hd + 2) * 4 : 0;
+  a.cluster = a.N < 128 && a.splits > 1 && a.splits <= kMaxCluster;
+  a.ws_bytes = a.splits > 1 && !a.cluster ? (size_t)a.items * a.splits * a.N * (hd + 2) * 4 : 0;
   return a;
 }
 
@@ -55,7 +57,8 @@ cudaError_t launch_attn_rows(const CUtensorMap& tk, const CUtensorMap& tv, const
   using C = AttnRowsCfg<HD, N>;
   const cudaError_t e = op_smem_once(reinterpret_cast<const void*>(attn_kv8_rows_kernel<HD, N>), C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  return op_launch(attn_kv8_rows_kernel<HD, N>, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, st, 1, tk, tv, p);
+  return op_launch(attn_kv8_rows_kernel<HD, N>, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, st, p.cluster ? p.splits : 1, tk, tv,
+                   p);
 }
 
 template <int HD>
@@ -76,7 +79,7 @@ cudaError_t launch_attn(const CUtensorMap& tk, const CUtensorMap& tv, const Attn
                   : a.N == 32 ? launch_attn_rows<HD, 32>(tk, tv, p, grid, st)
                   : a.N == 64 ? launch_attn_rows<HD, 64>(tk, tv, p, grid, st)
                               : launch_attn_tiles<HD>(tk, tv, p, grid, st);
-  if (e != cudaSuccess || a.splits == 1) return e;
+  if (e != cudaSuccess || a.splits == 1 || a.cluster) return e;
   const long long rows = (long long)p.c.b * p.R * p.H;
   return op_launch(attn_kv8_join_kernel<HD>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, 1, p, a.N);
 }
@@ -135,8 +138,9 @@ extern "C" dllm_status dllm_op_attention_kv8(const uint16_t* q, int64_t q_row_st
   const AttnKv8Plan a = plan_attn_kv8(cache->b, cache->H_kv, p.rows, cache->hd, cache->T);
   p.row_tiles = a.row_tiles;
   p.splits = a.splits;
+  p.cluster = a.cluster;
   p.ws_o = static_cast<float*>(workspace);
-  p.ws_ml = p.ws_o + (a.splits > 1 ? a.items * a.splits * a.N * cache->hd : 0);
+  p.ws_ml = p.ws_o + (a.ws_bytes ? a.items * a.splits * a.N * cache->hd : 0);
   const uint64_t planes = (uint64_t)cache->b * cache->H_kv, plane = (uint64_t)cache->T * cache->hd;
   const uint32_t keys = a.N == 128 ? 64 : 128;            // of a tile
   CUtensorMap tk, tv;

@@ -34,8 +34,10 @@
 //   warp 0     TMA: K and V tiles through a ring of 128-key slots
 //   warp 1     scale copies and MMAs, issued by one lane
 //   warps 2..  softmax, one key and RW rows a thread; the query tile before, the output after
-// Keys are split over CTAs when there are few (sequence, head) items; every
-// split leaves its normalised output and (m, l), and a second small kernel joins them.
+// Keys are split over CTAs when there are few (sequence, head) items.  Up to 8
+// splits form a cluster and join through distributed shared memory; more
+// leave their normalised outputs and (m, l) in the workspace, and a second small
+// kernel joins them.
 #pragma once
 
 #include "gemm.cuh"
@@ -54,7 +56,7 @@ struct AttnKv8Params {
   int H, R, group;        // group = H / H_kv query heads share a cached head
   FastDiv by_group;
   int rows, row_tiles;    // R * group rows of an item, in tiles of N
-  int splits;
+  int splits, cluster;    // cluster: the splits of an item are one
   float scale_log2;
   float *ws_o, *ws_ml;    // [item][split][N][hd] and [item][split][N][2]
 };
@@ -75,9 +77,9 @@ struct AttnRowsCfg {
   static constexpr int Q_PARTS = N < 16 ? 1 : 2;
   static constexpr int P_ROW = N < 16 ? 32 : 2 * N;     // a key's N hi codes, then its N lo codes
   static constexpr int P_BYTES = KT * P_ROW;
-  static constexpr int SLOTS = CTAS == 1 ? (HD == 64 ? 16 : 9) : HD == 64 ? 8 : N == 32 ? 5 : 6;
+  static constexpr int SLOTS = CTAS == 1 ? (HD == 64 ? 16 : 9) : HD == 64 ? 8 : N == 8 ? 6 : 5;
   static constexpr int SF_BYTES = 512;                  // ones, query scales, two buffers of probability scales
-  static constexpr int STAT_FLOATS = 8 * N + 3 * N + 4 * N;  // warp maxima (two), m, d, limits, scales
+  static constexpr int STAT_FLOATS = 8 * N + 3 * N + 4 * N + 16 * N;  // warp maxima (two), m, d, limits, scales, (m, l) of 8 splits
   static constexpr int SMEM_BYTES = 1024 + SLOTS * SLOT + Q_PARTS * Q_BYTES + 2 * P_BYTES + 4 * SF_BYTES +
                                     STAT_FLOATS * 4 + (2 * SLOTS + 10) * 8 + 24;
   static constexpr int S_COL = 0;                       // two buffers
@@ -183,7 +185,9 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
   float* s_d = s_m + N;                                 // [N] O is in units of 2^(m + d)
   int* s_lim = reinterpret_cast<int*>(s_d + N);         // [N]
   float* s_inv = reinterpret_cast<float*>(s_lim + N);   // [softmax warps][RW] inverse block scales
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_inv + 4 * N);
+  float* s_cm = s_inv + 4 * N;                          // [8][N] reference maxima of the cluster's splits
+  float* s_cl = s_cm + 8 * N;                           // [8][N] and sums
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_cl + 8 * N);
   uint64_t* empty = full + C::SLOTS;
   uint64_t* qready = empty + C::SLOTS;
   uint64_t* sfull = qready + 1;                         // [2]
@@ -235,6 +239,7 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
     const int lim = p.limits ? p.limits[(long long)seq * p.R + i] : p.c.T;
     s_lim[threadIdx.x] = min(max(lim, 0), p.c.T);
   }
+  if (p.cluster) cluster_arrive();                      // waited for before the first access of another CTA's memory
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -612,72 +617,111 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
     if (pass > 0 || *again == 0) break;
   }
 
-  if (warp >= 2) {
-    // ------------------------------------------------------ sums and output
-    const int q4 = warp & 3, key_l = q4 * 32 + lane, row0 = ((warp - 2) >> 2) * RW;
-    const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
-    if (nt > 0) {
-      tc_fence_after();
-      // sum RW columns over the warp: lane c (modulo RW) ends with column c
+  // ------------------------------------------------------ sums and output
+  const int q4 = warp & 3, dim = q4 * 32 + lane, row0 = ((warp - 2) >> 2) * RW, tid = (warp - 2) * 32 + lane;
+  const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
+  const bool soft = warp >= 2;
+  const long long slot = (long long)item * p.splits + split;
+  float l = 0.0f;                                         // of row tid
+  if (soft && nt > 0) {
+    tc_fence_after();
+    // sum RW columns over the warp: lane c (modulo RW) ends with column c
 #pragma unroll
-      for (int s = RW / 2; s >= 1; s >>= 1) {
-        const bool upper = (lane & s) != 0;
+    for (int s = RW / 2; s >= 1; s >>= 1) {
+      const bool upper = (lane & s) != 0;
 #pragma unroll
-        for (int i = 0; i < s; ++i) {
-          const float send = upper ? l_sum[i] : l_sum[i + s];
-          const float keep = upper ? l_sum[i + s] : l_sum[i];
-          l_sum[i] = keep + __shfl_xor_sync(0xffffffffu, send, s);
-        }
+      for (int i = 0; i < s; ++i) {
+        const float send = upper ? l_sum[i] : l_sum[i + s];
+        const float keep = upper ? l_sum[i + s] : l_sum[i];
+        l_sum[i] = keep + __shfl_xor_sync(0xffffffffu, send, s);
       }
-#pragma unroll
-      for (int s = RW; s < 32; s <<= 1) l_sum[0] += __shfl_xor_sync(0xffffffffu, l_sum[0], s);
-      if (lane < RW) s_wmax[q4 * N + row0 + lane] = l_sum[0];
     }
+#pragma unroll
+    for (int s = RW; s < 32; s <<= 1) l_sum[0] += __shfl_xor_sync(0xffffffffu, l_sum[0], s);
+    if (lane < RW) s_wmax[q4 * N + row0 + lane] = l_sum[0];
     named_bar_sync(2, C::SOFT);
-    // per row: 2^d / l in two factors, and where its output goes
-    const int tid = (warp - 2) * 32 + lane;
-    const long long slot = (long long)item * p.splits + split;
-    float2* s_f = reinterpret_cast<float2*>(s_nmax);      // [N]
-    long long* s_to = reinterpret_cast<long long*>(s_nmax + 2 * N);   // [N]
-    if (tid < N) {
-      float l = 0.0f;
-      if (nt > 0) l = (s_wmax[tid] + s_wmax[N + tid]) + (s_wmax[2 * N + tid] + s_wmax[3 * N + tid]);
-      // 2^d in two steps: it alone may leave the range that the result is in
-      const float vs = exp2f(0.5f * s_d[tid]);
-      s_f[tid] = l == 0.0f ? make_float2(0.0f, 0.0f) : make_float2(vs / l, vs);
-      if (p.splits > 1) {
-        s_to[tid] = (slot * N + tid) * HD;
-        if (tid < n_rows)
-          *reinterpret_cast<float2*>(p.ws_ml + (slot * N + tid) * 2) = make_float2(nt > 0 ? s_m[tid] : 0.0f, l);
-      } else {
-        uint32_t j;
-        const uint32_t i = p.by_group.divmod((uint32_t)(rt * N + tid), j);
-        s_to[tid] = ((long long)seq * p.R + i) * p.o_rs + (long long)(g * p.group + (int)j) * HD;
+    if (tid < N) l = (s_wmax[tid] + s_wmax[N + tid]) + (s_wmax[2 * N + tid] + s_wmax[3 * N + tid]);
+  }
+  // per row: the factors of O (2^d in two steps: it alone may leave the range that the
+  // result is in), and where the row goes
+  float2* s_f = reinterpret_cast<float2*>(s_nmax);        // [N]
+  long long* s_to = reinterpret_cast<long long*>(s_nmax + 2 * N);   // [N]
+  uint32_t* s_dst = reinterpret_cast<uint32_t*>(s_wmax);  // [N] its place in the cluster
+  const int own = (N + p.splits - 1) / p.splits;          // rows of a split in a cluster: split, split + splits, ...
+  float* s_part = reinterpret_cast<float*>(sKV);          // [split][own][HD]
+  if (p.cluster) {
+    // every split learns the others' (m, l) of its rows
+    cluster_wait();
+    if (soft && tid < N)
+      for (int r = 0; r < p.splits; ++r) {
+        cluster_store(cluster_addr(smem_u32(s_cm + split * N + tid), (uint32_t)r), nt > 0 ? s_m[tid] : 0.0f);
+        cluster_store(cluster_addr(smem_u32(s_cl + split * N + tid), (uint32_t)r), l);
       }
+    cluster_sync();   // and every CTA's MMAs and copies are done: the rings are free
+  }
+  if (soft) named_bar_sync(2, C::SOFT);                   // s_wmax is read
+  if (soft && tid < N) {
+    uint32_t j;
+    const uint32_t i = p.by_group.divmod((uint32_t)(rt * N + tid), j);
+    s_to[tid] = ((long long)seq * p.R + i) * p.o_rs + (long long)(g * p.group + (int)j) * HD;
+    float w = l == 0.0f ? 0.0f : 1.0f / l;
+    if (p.cluster) {
+      float M = -INFINITY, sum = 0.0f;
+      for (int r = 0; r < p.splits; ++r) {
+        const float mr = s_cm[r * N + tid];
+        if (s_cl[r * N + tid] != 0.0f) M = mr > M || mr != mr ? mr : M;   // a NaN stays
+      }
+      for (int r = 0; r < p.splits; ++r) {
+        const float lr = s_cl[r * N + tid];
+        if (lr != 0.0f) sum += lr * exp2f(s_cm[r * N + tid] - M);
+      }
+      w = l == 0.0f ? 0.0f : exp2f(s_m[tid] - M) / sum;
+      s_dst[tid] = cluster_addr(smem_u32(s_part + (split * own + tid / p.splits) * HD), (uint32_t)(tid % p.splits));
+    } else if (p.splits > 1) {
+      s_to[tid] = (slot * N + tid) * HD;
+      if (tid < n_rows)
+        *reinterpret_cast<float2*>(p.ws_ml + (slot * N + tid) * 2) = make_float2(nt > 0 ? s_m[tid] : 0.0f, l);
     }
+    const float vs = nt > 0 ? exp2f(0.5f * s_d[tid]) : 0.0f;
+    s_f[tid] = w == 0.0f ? make_float2(0.0f, 0.0f) : make_float2(vs * w, vs);
+  }
+  if (soft) {
     named_bar_sync(2, C::SOFT);
     // (rolled: code that runs once a CTA costs its instruction fetches)
-    const int dim = key_l;
 #pragma unroll 1
-    for (int n = row0; n < row0 + RW; n += 4) {
-      float a[4] = {}, c[4] = {};
-      if (nt > 0) {
-        tmem_ld4(trow + C::O_COL + n, a);
-        tmem_ld4(trow + C::O_COL + N + n, c);
-      }
+    for (int n = row0; n < row0 + RW && nt > 0; n += 4) {
+      float a[4], c[4];
+      tmem_ld4(trow + C::O_COL + n, a);
+      tmem_ld4(trow + C::O_COL + N + n, c);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int r = n + j;
         if (dim < HD && r < n_rows) {
           const float2 f = s_f[r];
           const float v = f.x == 0.0f ? 0.0f : (a[j] + c[j]) * f.x * f.y;
-          if (p.splits > 1)
+          if (p.cluster)
+            cluster_store(s_dst[r] + 4u * (uint32_t)dim, v);
+          else if (p.splits > 1)
             p.ws_o[s_to[r] + dim] = v;
           else
             p.out[s_to[r] + dim] = f32_to_bf16_bits(v);
         }
       }
     }
+    if (nt == 0 && p.splits == 1 && dim < HD)             // no row of the item sees a key
+      for (int r = row0; r < min(row0 + RW, n_rows); ++r) p.out[s_to[r] + dim] = 0;
+  }
+  if (p.cluster) {
+    cluster_sync();
+    if (soft)
+      for (int e = tid; e < own * HD; e += C::SOFT) {
+        const int i = e / HD, r = split + i * p.splits, d = e % HD;
+        if (r >= n_rows) continue;
+        float v = 0.0f;
+        for (int k = 0; k < p.splits; ++k)
+          if (s_cl[k * N + r] != 0.0f) v += s_part[(k * own + i) * HD + d];   // a split that saw none sent nothing
+        p.out[s_to[r] + d] = f32_to_bf16_bits(v);
+      }
   }
   __syncwarp();
   tc_fence_before();
@@ -702,25 +746,61 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const __grid_constan
   const long long item = ((long long)seq * p.c.H_kv + h / p.group) * p.row_tiles + rn / N;
   const long long first = item * p.splits * N + rn % N;   // then N apart
   constexpr int D = HD / 32;
-  float M = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) {
-    const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + (first + (long long)s * N) * 2);
-    if (ml.y != 0.0f) M = ml.x > M || ml.x != ml.x ? ml.x : M;   // a NaN stays
-  }
-  float sum = 0.0f, o[D] = {};
-  for (int s = 0; s < p.splits; ++s) {
-    const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + (first + (long long)s * N) * 2);
-    if (ml.y == 0.0f) continue;                            // a split that saw none of the row's keys
-    const float w = ml.y * exp2f(ml.x - M);
-    sum += w;
-    const float* src = p.ws_o + (first + (long long)s * N) * HD + lane * D;
+  // Eight splits' loads at once (a dependent one each was a round trip of L2 each);
+  // a running maximum joins the eights.
+  float M = -INFINITY, sum = 0.0f, o[D] = {};
+  for (int s0 = 0; s0 < p.splits; s0 += 8) {
+    float2 ml[8];
+    float v[8][D];
 #pragma unroll
-    for (int d = 0; d < D; ++d) o[d] += w * src[d];
+    for (int k = 0; k < 8; ++k) {
+      const bool in = s0 + k < p.splits;
+      const long long at = first + (long long)(in ? s0 + k : 0) * N;
+      ml[k] = *reinterpret_cast<const float2*>(p.ws_ml + at * 2);
+      if (!in) ml[k].y = 0.0f;
+      const float* src = p.ws_o + at * HD + lane * D;
+      if constexpr (D == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(src);
+        v[k][0] = f.x;
+        v[k][1] = f.y;
+        v[k][2] = f.z;
+        v[k][3] = f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(src);
+        v[k][0] = f.x;
+        v[k][1] = f.y;
+      }
+    }
+    float Mn = M;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (ml[k].y != 0.0f) Mn = ml[k].x > Mn || ml[k].x != ml[k].x ? ml[k].x : Mn;   // a NaN stays
+    const float c = M == -INFINITY ? 0.0f : exp2f(M - Mn);
+    sum *= c;
+#pragma unroll
+    for (int d = 0; d < D; ++d) o[d] *= c;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (ml[k].y == 0.0f) continue;                       // a split that saw none of the row's keys
+      const float w = ml[k].y * exp2f(ml[k].x - Mn);
+      sum += w;
+#pragma unroll
+      for (int d = 0; d < D; ++d) o[d] += w * v[k][d];
+    }
+    M = Mn;
   }
   const float il = sum == 0.0f ? 0.0f : 1.0f / sum;
-  uint16_t* out = p.out + row * p.o_rs + (long long)h * HD + lane * D;
+  uint32_t w[D / 2];
 #pragma unroll
-  for (int d = 0; d < D; ++d) out[d] = f32_to_bf16_bits(o[d] * il);
+  for (int d = 0; d < D; d += 2) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(o[d] * il, o[d + 1] * il);
+    w[d / 2] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  uint16_t* out = p.out + row * p.o_rs + (long long)h * HD + lane * D;
+  if constexpr (D == 4)
+    *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint32_t*>(out) = w[0];
 }
 
 }  // namespace dllm
