@@ -1,6 +1,8 @@
 // 8-bit matrix product with a scale for each block of 128 along K, and the
 // quantiser of its operands (see q8.cuh):
 //   Y[n][m] = sum_B 2^(ex[B][n] + ew[B][m]) * sum_{k in block B} X[n][k] W[m][k]
+#include <atomic>
+
 #include "gemm.cuh"
 #include "ops8.h"
 #include "ptx8.cuh"
@@ -322,6 +324,229 @@ __global__ void __launch_bounds__(224, 2)
   }
 }
 
+// ---------------------------------------------------------------- many rows
+// The same product for activations of hundreds of rows, bound by the tensor cores
+// and by what L2 delivers to them: at the MMA's full rate a tile of 128 x 128 asks
+// for 128 bytes a cycle and SM (measured: about 50 were delivered, 38% of the rate).  Here a
+// pair of CTAs (a cluster) takes 256 x 192 outputs, its activation rows fetched
+// once and multicast to both, 75 bytes a cycle; and a CTA is persistent, one an SM, with two
+// accumulators, so that storing one tile overlaps the next one's products.
+//   warp 0     TMA: weight codes, and half the activation codes for both CTAs
+//   warp 1     scale copies and MMAs, issued by one lane
+//   warps 2-5  epilogue
+//   warp 6     weight scale bytes, warp 7 activation scale bytes
+struct Gemm8BigCfg {
+  static constexpr int BN = 192;
+  static constexpr int A_BYTES = 128 * kQBlock;
+  static constexpr int B_BYTES = BN * kQBlock;
+  static constexpr int SF_BYTES = 3 * 512;
+  static constexpr int STAGES = 5;
+  static constexpr int SMEM_BYTES = 1024 + STAGES * (A_BYTES + B_BYTES + SF_BYTES) + (2 * STAGES + 4) * 8 + 16;
+  static constexpr int SF_COL = 2 * BN, SF_COLS = 12;
+  static_assert(SF_COL + STAGES * SF_COLS <= 512, "tensor memory");
+  static_assert(SMEM_BYTES <= 232448, "shared memory");
+};
+
+__global__ void __launch_bounds__(256, 1)
+    gemm8_big_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                     const __grid_constant__ Gemm8Params p) {
+  using C = Gemm8BigCfg;
+  constexpr int S = C::STAGES, BN = C::BN;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + S * C::A_BYTES;
+  uint8_t* sF = sB + S * C::B_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sF + S * C::SF_BYTES);
+  uint64_t* empty = full + S;
+  uint64_t* tfull = empty + S;    // [2] an accumulator is complete
+  uint64_t* tempty = tfull + 2;   // [2] and has been read
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* err = g_gemm8_err;
+
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const int pairs = (int)(gridDim.x >> 1), pair = (int)(blockIdx.x >> 1);
+  const int total = (p.M + 255) / 256 * p.n_tiles;        // tiles of 256 x BN
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 3);
+      mbar_init(&empty[s], 2);    // both CTAs' MMAs: the activations land in both
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 4);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&tmW);
+    prefetch_tensormap(&tmX);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                 // the other CTA's barriers are initialised
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
+    return __all_sync(0xffffffffu, mbar_wait_long(bar, parity, abort_flag, err, site)) != 0;
+  };
+  if (warp == 0) {
+    const uint32_t lead = elect_one();
+    const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
+    RingPos r{0, 0u};
+    int issued = 0;
+    bool ok = true;
+    for (int t = pair; t < total && ok; t += pairs) {
+      const int m0 = (t / p.n_tiles * 2 + rank) * 128, n0 = t % p.n_tiles * BN;
+      for (int i = 0; i < p.kb; ++i) {
+        if (issued >= S && !(ok = wait(&empty[r.s], r.par ^ 1u, ERR_GEMM_EMPTY))) break;
+        if (lead) {
+          mbar_arrive_expect_tx(&full[r.s], C::A_BYTES + C::B_BYTES);
+          tma_load_3d(sA + r.s * C::A_BYTES, &tmW, &full[r.s], i * kQBlock, m0, 0, pol_w);
+          tma_load_3d_multicast(sB + r.s * C::B_BYTES + rank * (C::B_BYTES / 2), &tmX, &full[r.s], i * kQBlock,
+                                n0 + rank * (BN / 2), 0, (uint16_t)3, pol_x);
+        }
+        r.next(S);
+        ++issued;
+      }
+    }
+    // Every copy into this CTA has landed and both CTAs' releases have arrived before
+    // its shared memory goes away.
+    for (int i = max(issued - S, 0); i < issued; ++i) {
+      if (*abort_flag) mbar_wait_long(&full[i % S], (uint32_t)(i / S) & 1u, nullptr, err, ERR_GEMM_DRAIN);
+      mbar_wait_long(&empty[i % S], (uint32_t)(i / S) & 1u, abort_flag, err, ERR_GEMM_EMPTY);
+    }
+  } else if (warp == 1) {
+    const uint32_t lead = elect_one();
+    constexpr uint32_t idesc = idesc_mxf8(128, BN);
+    RingPos r{0, 0u};
+    bool ok = true;
+    int n = 0;
+    for (int t = pair; t < total && ok; t += pairs, ++n) {
+      const uint32_t d = tmem + (uint32_t)((n & 1) * BN);
+      if (n >= 2 && !(ok = wait(&tempty[n & 1], (uint32_t)((n >> 1) - 1) & 1u, ERR_GEMM_TEMPTY))) break;
+      tc_fence_after();
+      for (int i = 0; i < p.kb; ++i) {
+        if (!(ok = wait(&full[r.s], r.par, ERR_GEMM_FULL))) break;
+        tc_fence_after();
+        const uint32_t a0 = smem_u32(sA + r.s * C::A_BYTES), b0 = smem_u32(sB + r.s * C::B_BYTES);
+        const uint32_t f0 = smem_u32(sF + r.s * C::SF_BYTES);
+        // a stage's scale columns are rewritten only once its MMAs are done (the empty barrier)
+        const uint32_t sfa = tmem + (uint32_t)(C::SF_COL + r.s * C::SF_COLS), sfb = sfa + 4;
+        tmem_cp_scales(lead, sfa, sdesc_scales(f0));
+        tmem_cp_scales(lead, sfb, sdesc_scales(f0 + 512));
+        tmem_cp_scales(lead, sfb + 4, sdesc_scales(f0 + 1024));
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_mxf8_ss(lead, d, sdesc_sw128(a0 + kk * 32), sdesc_sw128(b0 + kk * 32), idesc, sfa, sfb,
+                      (i > 0 || kk > 0) ? 1u : 0u);
+        mma_commit_multicast(lead, &empty[r.s], (uint16_t)3);
+        r.next(S);
+      }
+      if (ok) mma_commit_lead(lead, &tfull[n & 1]);
+    }
+  } else if (warp >= 6) {
+    // four blocks' bytes in use, the next four's in flight
+    constexpr int AHEAD = 4, W = 6;
+    const bool is_a = warp == 6;
+    const uint8_t* src = is_a ? p.ws : p.xs;
+    const int limit = is_a ? p.M : p.N, words = is_a ? 4 : W;
+    uint32_t nx[AHEAD][W];
+    RingPos r{0, 0u};
+    int done = 0;
+    bool ok = true;
+    for (int t = pair; t < total && ok; t += pairs) {
+      const int row0 = is_a ? (t / p.n_tiles * 2 + rank) * 128 : t % p.n_tiles * BN;
+      auto fetch = [&](int i0) {
+#pragma unroll
+        for (int e = 0; e < AHEAD; ++e)
+#pragma unroll
+          for (int j = 0; j < W; ++j) {
+            const int row = row0 + lane + 32 * j;
+            nx[e][j] = i0 + e < p.kb && j < words && row < limit ? __ldg(src + (long long)(i0 + e) * limit + row) : 127u;
+          }
+      };
+      fetch(0);
+      for (int i0 = 0; i0 < p.kb && ok; i0 += AHEAD) {
+        uint32_t cur[AHEAD][W];
+#pragma unroll
+        for (int e = 0; e < AHEAD; ++e)
+#pragma unroll
+          for (int j = 0; j < W; ++j) {
+            due(nx[e][j]);
+            cur[e][j] = nx[e][j];
+          }
+        fetch(i0 + AHEAD);
+#pragma unroll
+        for (int e = 0; e < AHEAD; ++e) {
+          if (i0 + e >= p.kb || !ok) break;
+          if (done >= S && !(ok = wait(&empty[r.s], r.par ^ 1u, ERR_GEMM_EMPTY))) break;
+          constexpr uint32_t rep = 0x01010101u;
+          uint4* f = reinterpret_cast<uint4*>(sF + r.s * C::SF_BYTES + (is_a ? 0 : 512)) + lane;
+          f[0] = make_uint4(cur[e][0] * rep, cur[e][1] * rep, cur[e][2] * rep, cur[e][3] * rep);
+          if (!is_a) f[32] = make_uint4(cur[e][4] * rep, cur[e][5] * rep, 127u * rep, 127u * rep);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[r.s]);
+          r.next(S);
+          ++done;
+        }
+      }
+    }
+  } else {
+    // epilogue: thread = weight row, columns = activation rows
+    const int q = warp & 3, l128 = q * 32 + lane;
+    int n = 0;
+    for (int t = pair; t < total; t += pairs, ++n) {
+      const int m = (t / p.n_tiles * 2 + rank) * 128 + l128, n0 = t % p.n_tiles * BN;
+      const int cols = min(BN, p.N - n0);
+      if (!wait(&tfull[n & 1], (uint32_t)(n >> 1) & 1u, ERR_GEMM_TFULL)) break;
+      tc_fence_after();
+      const uint32_t d = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)((n & 1) * BN);
+#pragma unroll 1
+      for (int c = 0; c < cols; c += 32) {
+        float v[32];
+        tmem_ld32(d + (uint32_t)c, v);
+        if (m < p.M) {
+          long long o = (long long)(n0 + c) * p.M + m;
+          if (p.out_bf16) {
+            __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y);
+#pragma unroll
+            for (int j = 0; j < 32; ++j, o += p.M)
+              if (c + j < cols) y[o] = __float2bfloat16_rn(v[j]);
+          } else {
+            float* y = static_cast<float*>(p.y);
+#pragma unroll
+            for (int j = 0; j < 32; ++j, o += p.M)
+              if (c + j < cols) y[o] = v[j];
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[n & 1]);
+    }
+  }
+  // no CTA leaves while the other may still write to it
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
 cudaError_t gemm8_err_word(int** p) { return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_gemm8_err); }
 
 namespace {
@@ -340,6 +565,34 @@ cudaError_t launch_gemm8(const CUtensorMap& tw, const CUtensorMap& tx, const Gem
   const cudaError_t e = op_smem_once(reinterpret_cast<const void*>(gemm8_kernel<BN>), C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   return op_launch(gemm8_kernel<BN>, dim3(grid), dim3(224), C::SMEM_BYTES, st, p.split, tw, tx, p);
+}
+
+// CTA pairs of gemm8_big_kernel that the current device holds at once.
+cudaError_t big_pairs(int* pairs) {
+  const void* k = reinterpret_cast<const void*>(gemm8_big_kernel);
+  const cudaError_t e = op_smem_once(k, Gemm8BigCfg::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  static std::atomic<int> known[64];                      // by device; 0: not asked yet
+  int dev = 0;
+  const cudaError_t d = cudaGetDevice(&dev);
+  if (d != cudaSuccess) return d;
+  const bool slot = dev >= 0 && dev < 64;
+  if (slot && (*pairs = known[dev].load()) > 0) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)op_device_sms() & ~1u);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = Gemm8BigCfg::SMEM_BYTES;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t o = cudaOccupancyMaxActiveClusters(pairs, k, &cfg);
+  if (o != cudaSuccess) return o;
+  if (*pairs < 1) *pairs = 1;
+  if (slot) known[dev].store(*pairs);
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -394,6 +647,22 @@ extern "C" dllm_status dllm_op_gemm8(const uint8_t* W, const uint8_t* W_scale, c
   p.K = K;
   p.kb = (int)(((long long)K + kQBlock - 1) / kQBlock);
   p.out_bf16 = y_dtype == DLLM_BF16;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  CUtensorMap tw, tx;
+  if (const dllm_status s = op_map_u8(&tw, W, K, M, 1, K, (uint64_t)K * M, 128, 128); s != DLLM_OK) return s;
+  // Tiles of 256 x 192 once they fill the GPU's CTA pairs.
+  const long long big = (M + 255LL) / 256 * ((N + Gemm8BigCfg::BN - 1LL) / Gemm8BigCfg::BN);
+  if (N > 128 && 2 * big >= op_device_sms()) {
+    int pairs = 0;
+    OP_CK(big_pairs(&pairs));
+    if (big >= pairs && big <= 0x3fffffffLL) {
+      p.n_tiles = (N + Gemm8BigCfg::BN - 1) / Gemm8BigCfg::BN;
+      if (const dllm_status s = op_map_u8(&tx, X, K, N, 1, K, (uint64_t)K * N, 128, Gemm8BigCfg::BN / 2); s != DLLM_OK)
+        return s;
+      OP_CK(op_launch(gemm8_big_kernel, dim3(2u * (unsigned)pairs), dim3(256), Gemm8BigCfg::SMEM_BYTES, st, 2, tw, tx, p));
+      return DLLM_OK;
+    }
+  }
   const int bn = N <= 32 ? 32 : N <= 64 ? 64 : 128;
   p.n_tiles = (N + bn - 1) / bn;
   const long long tiles = (long long)((M + 127LL) / 128) * p.n_tiles;
@@ -403,10 +672,7 @@ extern "C" dllm_status dllm_op_gemm8(const uint8_t* W, const uint8_t* W_scale, c
   p.split = 1;
   while (p.split < 8 && tiles * p.split * 2 <= 2LL * op_device_sms() && p.kb >= 4 * p.split) p.split *= 2;
   if (tiles * p.split > 0x7fffffffLL) return op_fail(DLLM_EINVAL, "gemm8: M=%d N=%d are too large", M, N);
-  CUtensorMap tw, tx;
-  if (const dllm_status s = op_map_u8(&tw, W, K, M, 1, K, (uint64_t)K * M, 128, 128); s != DLLM_OK) return s;
   if (const dllm_status s = op_map_u8(&tx, X, K, N, 1, K, (uint64_t)K * N, 128, bn); s != DLLM_OK) return s;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   const unsigned grid = (unsigned)(tiles * p.split);
   switch (bn) {
     case 32: OP_CK(launch_gemm8<32>(tw, tx, p, grid, st)); break;

@@ -508,6 +508,7 @@ PRODUCTS = [
     # M, N, K
     (1, 1, 16), (5, 3, 48), (128, 32, 128), (130, 33, 144), (256, 1, 4096), (2048, 16, 2048), (688, 40, 256),
     (256, 7, 688), (300, 129, 1040), (512, 200, 512), (1024, 300, 384), (97, 513, 4096), (4096, 32, 5504),
+    (3000, 1201, 272), (12300, 400, 144), (2049, 2000, 656),     # tiles of CTA pairs, ragged in every direction
 ]
 
 
