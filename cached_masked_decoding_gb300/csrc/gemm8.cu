@@ -1,6 +1,7 @@
 // 8-bit matrix product with a scale for each block of 128 along K, and the
 // quantiser of its operands (see q8.cuh):
 //   Y[n][m] = sum_B 2^(ex[B][n] + ew[B][m]) * sum_{k in block B} X[n][k] W[m][k]
+#include <algorithm>
 #include <atomic>
 
 #include "gemm.cuh"
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(256, 4) quantise8_kernel(const __grid_constant
 struct Gemm8Params {
   const uint8_t *ws, *xs;
   void* y;
-  int M, N, K, kb, n_tiles, split, out_bf16;
+  int M, N, K, kb, n_tiles, split_log, out_bf16;
 };
 
 // Set by a kernel that gave up a bounded wait; read by dllm_op_check.
@@ -127,10 +128,10 @@ __global__ void __launch_bounds__(224, 2)
   int* err = g_gemm8_err;
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int split = p.split, rank = split > 1 ? (int)cluster_rank() : 0;
-  const int tile = (int)(blockIdx.x / (unsigned)split);
+  const int sl = p.split_log, split = 1 << sl, rank = sl ? (int)cluster_rank() : 0;
+  const int tile = (int)(blockIdx.x >> sl);
   const int m0 = tile / p.n_tiles * 128, n0 = tile % p.n_tiles * BN;
-  const int c0 = (int)((long long)p.kb * rank / split), c1 = (int)((long long)p.kb * (rank + 1) / split);
+  const int c0 = (int)((long long)p.kb * rank >> sl), c1 = (int)((long long)p.kb * (rank + 1) >> sl);
   const int nc = c1 - c0;
 
   if (threadIdx.x == 0) {
@@ -294,25 +295,29 @@ __global__ void __launch_bounds__(224, 2)
     // every CTA's MMAs and copies are done: the rings hold partial tiles now.
     // Rank r owns the columns r, r + split, ... and gets each from every rank.
     float* part = reinterpret_cast<float*>(smem);        // [source rank][owned column][128]
-    const int own = (BN + split - 1) / split;
-    const uint32_t base = smem_u32(part) + 4u * (uint32_t)(rank * own * 128 + l128);
+    const int own = (BN + split - 1) >> sl;
+    uint32_t to[8];                                      // this thread's place in every rank
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      to[k] = cluster_addr(smem_u32(part) + 4u * (uint32_t)(rank * own * 128 + l128), (uint32_t)(k & (split - 1)));
     cluster_sync();
     if (epi) {
-      for (int n = 0; n < cols; n += 32) {
-        float v[32];
-        tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + n, v);
+#pragma unroll 1
+      for (int n = 0; n < cols; n += 8) {
+        float v[8];
+        tmem_ld8(tmem + ((uint32_t)(q * 32) << 16) + n, v);
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (n + j < cols)
-            cluster_store(cluster_addr(base + 4u * (uint32_t)((n + j) / split * 128), (uint32_t)((n + j) % split)), v[j]);
+        for (int j = 0; j < 8; ++j)                      // column n + j: rank (n + j) % split = j % split
+          if (n + j < cols) cluster_store(to[j] + 512u * (uint32_t)((n + j) >> sl), v[j]);
       }
     }
     cluster_sync();
     if (epi && m < p.M) {
-      for (int i = 0; i * split + rank < cols; ++i) {
+#pragma unroll 1
+      for (int i = 0; (i << sl) + rank < cols; ++i) {
         float v = 0.0f;
         for (int s = 0; s < split; ++s) v += part[(s * own + i) * 128 + l128];
-        put(i * split + rank, v);
+        put((i << sl) + rank, v);
       }
     }
   }
@@ -564,7 +569,7 @@ cudaError_t launch_gemm8(const CUtensorMap& tw, const CUtensorMap& tx, const Gem
   using C = Gemm8Cfg<BN>;
   const cudaError_t e = op_smem_once(reinterpret_cast<const void*>(gemm8_kernel<BN>), C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  return op_launch(gemm8_kernel<BN>, dim3(grid), dim3(224), C::SMEM_BYTES, st, p.split, tw, tx, p);
+  return op_launch(gemm8_kernel<BN>, dim3(grid), dim3(224), C::SMEM_BYTES, st, 1 << p.split_log, tw, tx, p);
 }
 
 // CTA pairs of gemm8_big_kernel that the current device holds at once.
@@ -650,30 +655,36 @@ extern "C" dllm_status dllm_op_gemm8(const uint8_t* W, const uint8_t* W_scale, c
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   CUtensorMap tw, tx;
   if (const dllm_status s = op_map_u8(&tw, W, K, M, 1, K, (uint64_t)K * M, 128, 128); s != DLLM_OK) return s;
-  // Tiles of 256 x 192 once they fill the GPU's CTA pairs.
-  const long long big = (M + 255LL) / 256 * ((N + Gemm8BigCfg::BN - 1LL) / Gemm8BigCfg::BN);
-  if (N > 128 && 2 * big >= op_device_sms()) {
-    int pairs = 0;
-    OP_CK(big_pairs(&pairs));
-    if (big >= pairs && big <= 0x3fffffffLL) {
-      p.n_tiles = (N + Gemm8BigCfg::BN - 1) / Gemm8BigCfg::BN;
-      if (const dllm_status s = op_map_u8(&tx, X, K, N, 1, K, (uint64_t)K * N, 128, Gemm8BigCfg::BN / 2); s != DLLM_OK)
-        return s;
-      OP_CK(op_launch(gemm8_big_kernel, dim3(2u * (unsigned)pairs), dim3(256), Gemm8BigCfg::SMEM_BYTES, st, 2, tw, tx, p));
-      return DLLM_OK;
-    }
-  }
   const int bn = N <= 32 ? 32 : N <= 64 ? 64 : 128;
   p.n_tiles = (N + bn - 1) / bn;
-  const long long tiles = (long long)((M + 127LL) / 128) * p.n_tiles;
+  const long long tiles = (long long)((M + 127LL) / 128) * p.n_tiles, slots = 2LL * op_device_sms();
   // Split a tile's K over a cluster while all CTAs fit on the GPU at once, two
   // an SM: bound by HBM they then share its bandwidth evenly and finish
   // together.  Each keeps at least two blocks of K.
-  p.split = 1;
-  while (p.split < 8 && tiles * p.split * 2 <= 2LL * op_device_sms() && p.kb >= 4 * p.split) p.split *= 2;
-  if (tiles * p.split > 0x7fffffffLL) return op_fail(DLLM_EINVAL, "gemm8: M=%d N=%d are too large", M, N);
+  while (p.split_log < 3 && (tiles << p.split_log) * 2 <= slots && p.kb >= 4 << p.split_log) ++p.split_log;
+  if (N > 64) {
+    // Or tiles of 256 x 192 by CTA pairs.  A block of K takes a round of those 0.31 us and a
+    // round of 128-row CTAs 0.56 us, the join of a split about six blocks (measured, us, with
+    // the quantiser, pairs / CTAs: 4096 x 4096 weights, 400 rows 16 / 24, 768 rows 18 / 22, 1024 rows 27 / 22;
+    // 12288 x 4096, 160 rows 17 / 22, 256 rows 26 / 22, 512 rows 27 / 38).
+    const long long big = (M + 255LL) / 256 * ((N + Gemm8BigCfg::BN - 1LL) / Gemm8BigCfg::BN);
+    int pairs = 0;
+    OP_CK(big_pairs(&pairs));
+    const __int128 big_cost = (__int128)5 * ((big + pairs - 1) / pairs) * p.kb;
+    const __int128 cta_cost = (__int128)9 * (((tiles << p.split_log) + slots - 1) / slots) *
+                              (((p.kb + (1 << p.split_log) - 1) >> p.split_log) + (p.split_log ? 6 : 0));
+    if (big_cost <= cta_cost && big <= 0x3fffffffLL) {
+      p.n_tiles = (N + Gemm8BigCfg::BN - 1) / Gemm8BigCfg::BN;
+      if (const dllm_status s = op_map_u8(&tx, X, K, N, 1, K, (uint64_t)K * N, 128, Gemm8BigCfg::BN / 2); s != DLLM_OK)
+        return s;
+      const unsigned grid = 2u * (unsigned)std::min<long long>(pairs, big);
+      OP_CK(op_launch(gemm8_big_kernel, dim3(grid), dim3(256), Gemm8BigCfg::SMEM_BYTES, st, 2, tw, tx, p));
+      return DLLM_OK;
+    }
+  }
+  if ((tiles << p.split_log) > 0x7fffffffLL) return op_fail(DLLM_EINVAL, "gemm8: M=%d N=%d are too large", M, N);
   if (const dllm_status s = op_map_u8(&tx, X, K, N, 1, K, (uint64_t)K * N, 128, bn); s != DLLM_OK) return s;
-  const unsigned grid = (unsigned)(tiles * p.split);
+  const unsigned grid = (unsigned)(tiles << p.split_log);
   switch (bn) {
     case 32: OP_CK(launch_gemm8<32>(tw, tx, p, grid, st)); break;
     case 64: OP_CK(launch_gemm8<64>(tw, tx, p, grid, st)); break;
