@@ -28,19 +28,19 @@ struct AttnKv8Plan {
 
 // Rows of one cached head (R rows of H / H_kv heads) in tiles of N, the keys in
 // splits.  A CTA's time is taken as the tiles of keys that it walks; the join of up
-// to 8 splits in a cluster as one tile's, that of more (or of 128-row tiles) through the
-// workspace as four of 128 keys.  A round of CTAs is two an SM, one with 64 rows.
+// to 8 splits in a cluster as one tile's, that of more (or of 128 rows and up) through the
+// workspace as four of 128 keys.  A round of CTAs is two an SM, one with 64 or 256 rows.
 AttnKv8Plan plan_attn_kv8(long long b, long long H_kv, long long rows, int hd, int T) {
   AttnKv8Plan a;
-  a.N = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  a.N = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
   a.row_tiles = (int)((rows + a.N - 1) / a.N);
   a.items = b * H_kv * a.row_tiles;
-  const long long kt = a.N == 128 ? 64 : 128, tiles = (T + kt - 1) / kt;
-  const long long ctas = (a.N == 64 ? 1 : 2) * op_device_sms();
+  const long long kt = a.N >= 128 ? 64 : 128, tiles = (T + kt - 1) / kt;
+  const long long ctas = (a.N == 64 || a.N == 256 ? 1 : 2) * op_device_sms();
   long long best = (a.items + ctas - 1) / ctas * tiles;
   a.splits = 1;
   for (long long s = 2; s <= std::min(tiles, 64LL) && s * a.items <= ctas; ++s) {
-    const long long t = (tiles + s - 1) / s + (a.N == 128 ? 8 : s <= kMaxCluster ? 1 : 4);
+    const long long t = (tiles + s - 1) / s + (a.N >= 128 ? 8 : s <= kMaxCluster ? 1 : 4);
     if (t < best) {
       best = t;
       a.splits = (int)s;
@@ -57,17 +57,17 @@ cudaError_t launch_attn_rows(const CUtensorMap& tk, const CUtensorMap& tv, const
   using C = AttnRowsCfg<HD, N>;
   const cudaError_t e = op_smem_once(reinterpret_cast<const void*>(attn_kv8_rows_kernel<HD, N>), C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  return op_launch(attn_kv8_rows_kernel<HD, N>, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, st, p.cluster ? p.splits : 1, tk, tv,
-                   p);
+  return op_launch(attn_kv8_rows_kernel<HD, N>, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, st,
+                   p.cluster ? p.splits : 1, tk, tv, p);
 }
 
-template <int HD>
+template <int HD, int SUBS>
 cudaError_t launch_attn_tiles(const CUtensorMap& tk, const CUtensorMap& tv, const AttnKv8Params& p, unsigned grid,
                               cudaStream_t st) {
-  using C = AttnTilesCfg<HD>;
-  const cudaError_t e = op_smem_once(reinterpret_cast<const void*>(attn_kv8_tiles_kernel<HD>), C::SMEM_BYTES);
+  using C = AttnTilesCfg<HD, SUBS>;
+  const cudaError_t e = op_smem_once(reinterpret_cast<const void*>(attn_kv8_tiles_kernel<HD, SUBS>), C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  return op_launch(attn_kv8_tiles_kernel<HD>, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, st, 1, tk, tv, p);
+  return op_launch(attn_kv8_tiles_kernel<HD, SUBS>, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, st, 1, tk, tv, p);
 }
 
 template <int HD>
@@ -78,7 +78,8 @@ cudaError_t launch_attn(const CUtensorMap& tk, const CUtensorMap& tv, const Attn
                   : a.N == 16 ? launch_attn_rows<HD, 16>(tk, tv, p, grid, st)
                   : a.N == 32 ? launch_attn_rows<HD, 32>(tk, tv, p, grid, st)
                   : a.N == 64 ? launch_attn_rows<HD, 64>(tk, tv, p, grid, st)
-                              : launch_attn_tiles<HD>(tk, tv, p, grid, st);
+                  : a.N == 128 ? launch_attn_tiles<HD, 1>(tk, tv, p, grid, st)
+                               : launch_attn_tiles<HD, 2>(tk, tv, p, grid, st);
   if (e != cudaSuccess || a.splits == 1 || a.cluster) return e;
   const long long rows = (long long)p.c.b * p.R * p.H;
   return op_launch(attn_kv8_join_kernel<HD>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, 1, p, a.N);
@@ -142,7 +143,7 @@ extern "C" dllm_status dllm_op_attention_kv8(const uint16_t* q, int64_t q_row_st
   p.ws_o = static_cast<float*>(workspace);
   p.ws_ml = p.ws_o + (a.ws_bytes ? a.items * a.splits * a.N * cache->hd : 0);
   const uint64_t planes = (uint64_t)cache->b * cache->H_kv, plane = (uint64_t)cache->T * cache->hd;
-  const uint32_t keys = a.N == 128 ? 64 : 128;            // of a tile
+  const uint32_t keys = a.N >= 128 ? 64 : 128;            // of a tile
   CUtensorMap tk, tv;
   if (const dllm_status s = op_map_u8(&tk, cache->k, cache->hd, cache->T, planes, cache->hd, plane, cache->hd, keys);
       s != DLLM_OK)

@@ -79,7 +79,8 @@ struct AttnRowsCfg {
   static constexpr int P_BYTES = KT * P_ROW;
   static constexpr int SLOTS = CTAS == 1 ? (HD == 64 ? 16 : 9) : HD == 64 ? 8 : N == 8 ? 6 : 5;
   static constexpr int SF_BYTES = 512;                  // ones, query scales, two buffers of probability scales
-  static constexpr int STAT_FLOATS = 8 * N + 3 * N + 4 * N + 16 * N;  // warp maxima (two), m, d, limits, scales, (m, l) of 8 splits
+  // warp maxima (two), m, d, limits, scales, (m, l) of 8 splits
+  static constexpr int STAT_FLOATS = 8 * N + 3 * N + 4 * N + 16 * N;
   static constexpr int SMEM_BYTES = 1024 + SLOTS * SLOT + Q_PARTS * Q_BYTES + 2 * P_BYTES + 4 * SF_BYTES +
                                     STAT_FLOATS * 4 + (2 * SLOTS + 10) * 8 + 24;
   static constexpr int S_COL = 0;                       // two buffers
@@ -110,34 +111,33 @@ constexpr float kRefSlack = 40.0f;   // log2 a score or a product may exceed a r
 constexpr int kRefFixed = 110;       // and a product or sum one that does not
 constexpr int kVRange = 60;          // value exponents' distance from the first tile's that such references allow
 
-// The query tile, rows rt * N .. of the item, by THREADS threads (a multiple of
-// 32): hi codes to q_hi, lo codes to q_lo from row lo0 on, and a word of the row's
-// scale byte to the 512-byte atom sf (prefilled with 1.0) for both.  Rows from
-// n_rows on are zeros.  BATCH rows a thread are loaded before the first is
-// used: one at a time, 128 rows took 13 us of load latency.
+// The query tile, rows rt * N .. of the item, by THREADS threads (a multiple of 32):
+// load() asks for them, store() puts hi codes to q_hi, lo codes to q_lo from row lo0 on, and a
+// word of the row's scale byte to the 512-byte atom sf (prefilled with 1.0) for both.
+// Rows from n_rows on are zeros.  All rows are in flight at once, 16 bytes of a row a thread:
+// one at a time, 128 rows took 13 us of load latency.
 template <int HD, int N, int THREADS>
-__device__ __forceinline__ void attn_query_tile(const AttnKv8Params& p, int seq, int g, int rt, int n_rows, int tid,
-                                                uint8_t* q_hi, uint8_t* q_lo, int lo0, uint32_t* sf) {
-  constexpr int L = HD / 8, PASS = THREADS / L;           // lanes of a row, rows a pass
-  constexpr int BATCH = (N + PASS - 1) / PASS < 4 ? (N + PASS - 1) / PASS : 4;
-  const int l = tid % L;
-#pragma unroll 1
-  for (int n0 = tid / L; n0 < N + tid / L; n0 += PASS * BATCH) {   // every thread makes the same trips
-    Raw8<ElemBf16> raw[BATCH];
+struct AttnQueryTile {
+  static constexpr int L = HD / 8, PASS = THREADS / L;    // lanes of a row, rows a pass
+  static constexpr int ROWS = (N + PASS - 1) / PASS;
+  Raw8<ElemBf16> raw[ROWS];
+
+  __device__ __forceinline__ void load(const AttnKv8Params& p, int seq, int g, int rt, int n_rows, int tid) {
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      const int n = n0 + k * PASS;
-      raw[k].zero();
-      if (n < n_rows) {
-        uint32_t j;
-        const uint32_t i = p.by_group.divmod((uint32_t)(rt * N + n), j);
-        raw[k].load(reinterpret_cast<const __nv_bfloat16*>(p.q) + ((long long)seq * p.R + i) * p.q_rs +
-                    (long long)(g * p.group + (int)j) * HD + l * 8);
-      }
+    for (int k = 0; k < ROWS; ++k) {
+      const int n = tid / L + k * PASS;
+      uint32_t j;                                         // a row that there is: a branch would wait for each load
+      const uint32_t i = p.by_group.divmod((uint32_t)(rt * N + (n < n_rows ? n : 0)), j);
+      raw[k].load(reinterpret_cast<const __nv_bfloat16*>(p.q) + ((long long)seq * p.R + i) * p.q_rs +
+                  (long long)(g * p.group + (int)j) * HD + tid % L * 8);
     }
+  }
+  __device__ __forceinline__ void store(int n_rows, int tid, uint8_t* q_hi, uint8_t* q_lo, int lo0, uint32_t* sf) {
+    const int l = tid % L;
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      const int n = n0 + k * PASS;
+    for (int k = 0; k < ROWS; ++k) {
+      const int n = tid / L + k * PASS;
+      if (n >= n_rows) raw[k].zero();
       float x[8];
       raw[k].floats(x);
       uint32_t m = abs_bits8(x);
@@ -165,7 +165,7 @@ __device__ __forceinline__ void attn_query_tile(const AttnKv8Params& p, int seq,
       }
     }
   }
-}
+};
 
 template <int HD, int N>
 __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N>::CTAS)
@@ -308,7 +308,8 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
           for (int part = 0; part < C::Q_PARTS; ++part)
 #pragma unroll
             for (int kk = 0; kk < HD / 32; ++kk)
-              mma_mxf8_ss(lead, d, sdesc_rows<HD>(k + kk * 32), sdesc_rows<HD>(q0 + part * C::Q_BYTES + kk * 32), idesc_s,
+              mma_mxf8_ss(lead, d, sdesc_rows<HD>(k + kk * 32), sdesc_rows<HD>(q0 + part * C::Q_BYTES + kk * 32),
+                          idesc_s,
                           sfa, sfq, (part > 0 || kk > 0) ? 1u : 0u);
           mma_commit_lead(lead, &empty[slot]);
           mma_commit_lead(lead, &sfull[sb]);
@@ -373,8 +374,10 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
         if (tid < N) s_m[tid] = 0.0f;
         named_bar_sync(2, C::SOFT);
         // 8 rows: the lo rows lie behind the hi rows of one operand
-        attn_query_tile<HD, N, C::SOFT>(p, seq, g, rt, n_rows, tid, sQ, sQ + (C::Q_PARTS - 1) * C::Q_BYTES,
-                                        C::Q_PARTS == 1 ? N : 0, reinterpret_cast<uint32_t*>(sSF + C::SF_BYTES));
+        AttnQueryTile<HD, N, C::SOFT> query;
+        query.load(p, seq, g, rt, n_rows, tid);
+        query.store(n_rows, tid, sQ, sQ + (C::Q_PARTS - 1) * C::Q_BYTES, C::Q_PARTS == 1 ? N : 0,
+                    reinterpret_cast<uint32_t*>(sSF + C::SF_BYTES));
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(qready);

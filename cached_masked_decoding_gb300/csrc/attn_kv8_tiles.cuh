@@ -1,102 +1,123 @@
 // Attention over the 8-bit cache for many query rows a cached head (a prefill
-// over its own cache): 128 rows a CTA, a row in two softmax threads.
+// over its own cache, a block of grouped heads): SUBS times 128 rows a CTA, a row in two
+// softmax threads.
 //
-//   S[row][key] = Q K^T      kind::mxf8f6f4 on the cache's codes; q as hi + lo codes (two
-//                            products, see attn_kv8_rows.cuh), the row's and the
-//                            key's scales applied by the MMA
-//   O[row][dim] += P V       kind::f16; P in tensor memory, V as halves
-// V's codes become halves in shared memory, code * 2^(ev - vref), exact down to
-// 2^-24 where the largest row of the tiles so far has values up to 448 (2^-33 of
-// it); vref follows the largest exponent.  P is a half too, 2^7 p: 11 bits down to
-// 2^-21 of the row's reference.  Where a tile's value exponents reach more than 2^10
-// below vref (a loud value may then count although its p is far below 2^-21), the
-// codes stay unscaled from there on, P is formed from the score plus the value's
-// exponent, and the products get a reference of their own.  With P as two e4m3 codes and V untouched, as
-// for few rows, the softmax needed 16 instructions a score and a causal prefill
-// of 4096 rows 259 us; converting 64 V rows costs 1.5 a code, shared by 128
-// query rows, and leaves the softmax about 4.
+//   S[row][key] = Q K^T      kind::f8f6f4 on the cache's codes; q as hi + lo codes (two
+//                            products, see attn_kv8_rows.cuh), the row's and the key's
+//                            scales applied by the softmax
+//   O[row][dim] += P V       kind::f16 with bf16; P in tensor memory, V made bf16
+// V's codes become bf16 in shared memory with their scale, code * 2^(ev - vsh): four
+// significant bits lose nothing.  P is rounded to bf16 (2^-9 of itself; its sum is not).  Both
+// have float32's range, so nothing has to follow the scores: a row's reference is its
+// maximum over the CTA's first tile of keys and stays, and vsh is the largest value
+// exponent there.  A CTA that meets a row whose sum reaches 2^kRowFixed, or value
+// exponents more than kVRange above vsh, walks its keys again, with the largest exponent
+// it met and references that rise with the scores.
 //
-// A tile of 128 rows by 128 keys takes the tensor cores 1024 cycles (two e4m3
-// products cost what one product of halves costs); two CTAs share an SM, so that
-// one's products run under the other's exponentials.  Tensor memory sets the
-// tile: 64 keys make S 64 columns, P 32, O 128 and the scales 12, just under half.
+// 256 rows (SUBS 2) fill an SM: K and V are fetched, and V converted, once for both
+// halves, whose products run under one another's exponentials.  Tensor memory sets the tile:
+// 64 keys make the scores of two tiles 128 columns, of which the second tile's are there
+// when the first's are used up; P takes the place of its scores; O is 128 more.
+// 128 rows are for CTAs that would be half empty, two an SM.
 //
-//   warp 0     TMA: K and V tiles of 64 keys, a ring each
-//   warp 1     scale copies and MMAs, issued by one lane
-//   warp 2     scale bytes: K's for the MMA, V's as factors
-//   warps 4-11 softmax, a row in two threads of 32 keys each (with one thread a row the
-//              softmax was the longest stage, bound by its latencies: 2600 cycles a
-//              tile); the query tile before, the output after
-//   warps 12-15 V to halves, 16 keys each
+// 4096 causal rows of 32 heads on 8, hd 128 (137 GFLOP): 156 us, 0.88 PFLOP/s, 46 % of the
+// measured bf16 rate; hd 64: 117 us.  A tile of 256 rows takes 2070 cycles of which the products
+// need 1024: shared memory's port is taken by operands (1024 cycles), the walk of scores and
+// probabilities through registers (about 770), V's conversion (190) and the key factors
+// (256), and what waits for it waits longer.  Tried: 128 keys a tile with one tile's scores
+// only, 186 us; 128 rows a CTA throughout, 187; halves in place of bf16 with references that
+// follow the scores, 190; e4m3 for P as well, 259.  A CTA's start and end, 19,000 cycles (the
+// query tile's conversion 5,000), are the next largest part: nothing else runs on the SM.
+//
+//   warp 0         TMA: K and V tiles of 64 keys, a ring each
+//   warps 1, 3     MMAs of a half, issued by one lane
+//   warp 2         scale bytes as factors, fetched four tiles ahead
+//   8 SUBS warps   softmax, 32 keys of a row a thread; the query tile before, the output after
+//   4 SUBS warps   V to bf16
 #pragma once
 
 #include "attn_kv8_rows.cuh"
 
 namespace dllm {
 
-template <int HD>
+template <int HD, int SUBS>
 struct AttnTilesCfg {
-  static constexpr int N = 128;                         // rows
-  static constexpr int KT = 64;
-  static constexpr int THREADS = 512;
-  // registers: the launch's 64 a thread (4 warpgroups) shared out anew, 80 + 80 + 40 + 56 = 4 * 64
-  static constexpr int REGS_SOFT = 80, REGS_CONV = 40, REGS_REST = 56;
+  static constexpr int N = 128 * SUBS;                  // rows
+  static constexpr int KT = 64;                         // keys of a tile
+  static constexpr int SB = 2;                          // buffers of scores
+  static constexpr int SOFT_WARPS = 8 * SUBS, CONV_WARPS = 4 * SUBS;
+  static constexpr int THREADS = 32 * (4 + SOFT_WARPS + CONV_WARPS);
+  static constexpr int CTAS = SUBS == 1 ? 2 : 1;        // an SM
+  // registers, from the launch's 64 a thread (SUBS 1) or 72 (SUBS 2) shared out anew by
+  // warpgroups: 2 * 80 + 40 + 56 = 4 * 64, 4 * 88 + 2 * 40 + 72 = 7 * 72
+  static constexpr int REGS_SOFT = SUBS == 1 ? 80 : 88, REGS_CONV = 40, REGS_REST = SUBS == 1 ? 56 : 72;
   static constexpr int SLOT = KT * HD;
-  static constexpr int KS = 3, VS = 2;                  // slots of the two rings
+  static constexpr int VS = SUBS == 1 ? 2 : 3;          // V slots (K has 3)
+  static constexpr int VB = SUBS == 1 ? 2 : 3;          // V tiles as bf16
   static constexpr int Q_BYTES = N * HD;                // hi or lo
-  static constexpr int V_BYTES = KT * HD * 2;           // V as halves: 64 dims a 128-byte row
-  static constexpr int SF_BYTES = 512;                  // query, two of K
+  static constexpr int V_BYTES = KT * HD * 2;           // V as bf16: 64 dims a 128-byte row
+  static constexpr int BARS = 3 + 3 + 2 * VS + SUBS * (1 + SB + 3 + 2) + 3;
   static constexpr int SMEM_BYTES =
-      1024 + (KS + VS) * SLOT + 2 * Q_BYTES + 2 * V_BYTES + 3 * SF_BYTES + (4 + 4 * KT + 5 * N) * 4 +
-      (2 * (KS + VS) + 12) * 8 + 16;
-  static constexpr int S_COL = 0;
-  static constexpr int P_COL = KT;                      // two halves a column
-  static constexpr int O_COL = P_COL + KT / 2;
-  static constexpr int SF_Q = O_COL + HD, SF_K = SF_Q + 4;
-  static constexpr int TMEM_COLS = 256;
-  static_assert(SF_K + 8 <= TMEM_COLS, "tensor memory");
-  static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs an SM");
+      1024 + (3 + VS) * SLOT + 2 * Q_BYTES + VB * V_BYTES + (N + 15 * KT / 2 + N + 2 * N) * 4 + BARS * 8 + 32;
+  static constexpr int SUB_COLS = 256;                  // of 128 rows: scores of two tiles, then the output
+  static constexpr int O_COL = SB * KT;
+  static_assert(O_COL + HD <= SUB_COLS && CTAS * SUBS * SUB_COLS <= 512, "tensor memory");
+  static_assert(CTAS * (SMEM_BYTES + 1024) <= 228 * 1024, "shared memory");
 };
 
-constexpr float kPShift = 7.0f;    // P is held as 2^7 p, p up to 2^kRowSlack: a half has room to 65504
-constexpr float kRowSlack = 8.0f;  // log2 a score may exceed its row's reference by
-constexpr int kVSpread = 10;       // log2 of the value scales' spread that halves of V and P cover
-constexpr int kVSlack = 6;         // and a value exponent the common one: 448 * 2^6 is under 65504
+constexpr float kRowSlack = 8.0f;    // log2 a score may exceed a reference by that rises with the scores
+constexpr float kRowFixed = 40.0f;   // and a row's sum one that does not
 
-template <int HD>
-__global__ void __launch_bounds__(512, 2)
+// A word of four codes to two pairs of bf16, code * 2^-120: the code's exponent and
+// mantissa bits in bf16's places.
+__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t& a, uint32_t& b) {
+  const uint32_t x = __byte_perm(w, 0, 0x1404), y = __byte_perm(w, 0, 0x3424);
+  a = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+  b = ((y >> 4) & 0x07f007f0u) | (y & 0x80008000u);
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 d =
+      __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+// 2^e as a pair of bf16, 0 below the normal range.
+__device__ __forceinline__ uint32_t pow2_bf16x2(int e) {
+  return e < -126 ? 0u : (uint32_t)(127 + min(e, 127)) * 0x00800080u;
+}
+
+template <int HD, int SUBS>
+__global__ void __launch_bounds__(AttnTilesCfg<HD, SUBS>::THREADS, AttnTilesCfg<HD, SUBS>::CTAS)
     attn_kv8_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                           const __grid_constant__ AttnKv8Params p) {
-  using C = AttnTilesCfg<HD>;
-  constexpr int KT = C::KT, N = C::N;
+  using C = AttnTilesCfg<HD, SUBS>;
+  constexpr int KT = C::KT, N = C::N, KH = KT / 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sK = smem;
-  uint8_t* sV = sK + C::KS * C::SLOT;
-  uint8_t* sQ = sV + C::VS * C::SLOT;                   // hi, lo
-  uint8_t* sH = sQ + 2 * C::Q_BYTES;                    // [2] V as halves
-  uint8_t* sSF = sH + 2 * C::V_BYTES;                   // scale atoms: queries, K (two)
-  int* s_vref = reinterpret_cast<int*>(sSF + 3 * C::SF_BYTES);   // [2]
-  int* s_wide = s_vref + 2;                             // [2] value scales far apart
-  float* s_ev = reinterpret_cast<float*>(s_wide + 2);   // [2][KT] their exponents then
-  float* s_hf = s_ev + 2 * KT;                          // [2][KT] factors of V's halves
-  int* s_lim = reinterpret_cast<int*>(s_hf + 2 * KT);   // [N]
+  uint8_t* sV = sK + 3 * C::SLOT;
+  uint8_t* sQ = sV + C::VS * C::SLOT;                   // [SUBS] hi, lo of 128 rows
+  uint8_t* sH = sQ + 2 * C::Q_BYTES;                    // [VB] V as bf16
+  uint32_t* s_q = reinterpret_cast<uint32_t*>(sH + C::VB * C::V_BYTES);   // [SUBS] the rows' scale bytes, an atom
+  __nv_bfloat16* s_kf = reinterpret_cast<__nv_bfloat16*>(s_q + N);   // [3][KT] 2^(ek - 9)
+  uint32_t* s_vf = reinterpret_cast<uint32_t*>(s_kf + 3 * KT);   // [3][KT] 2^(120 + ev - vsh), bf16 pairs
+  uint32_t* s_vg = s_vf + 3 * KT;                       // [3][KT] what of it is over 2^127
+  int* s_lim = reinterpret_cast<int*>(s_vg + 3 * KT);   // [N]
   float* s_top = reinterpret_cast<float*>(s_lim + N);   // [2][N] a row's two halves: largest scores, sums
-  float* s_most = s_top + 2 * N;                        // [2][N] largest products
-  uint64_t* kfull = reinterpret_cast<uint64_t*>(s_most + 2 * N);
-  uint64_t* kempty = kfull + C::KS;
-  uint64_t* vfull = kempty + C::KS;
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(s_top + 2 * N);   // [3] a tile's K and factors are there
+  uint64_t* kempty = kfull + 3;
+  uint64_t* vfull = kempty + 3;
   uint64_t* vempty = vfull + C::VS;
-  uint64_t* qready = vempty + C::VS;
-  uint64_t* sfull = qready + 1;                         // S of a tile is there
-  uint64_t* sfree = sfull + 1;                          // and has been read
-  uint64_t* kready = sfree + 1;                         // [2] a tile's scales are there
-  uint64_t* vready = kready + 2;                        // [2] its V as halves
-  uint64_t* pready = vready + 2;                        // [2] its P
-  uint64_t* pvdone = pready + 2;                        // [2] its product
-  uint64_t* mdone = pvdone + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdone + 1);
+  uint64_t* pvdone = vempty + C::VS;                    // [3] a tile's products with V
+  uint64_t* qready = pvdone + 3;                        // [SUBS]
+  uint64_t* sfull = qready + SUBS;                      // [SUBS][SB] scores
+  uint64_t* pready = sfull + C::SB * SUBS;                  // [SUBS][3] probabilities, and V as bf16
+  uint64_t* mdone = pready + 3 * SUBS;                  // [SUBS]
+  uint64_t* pread = mdone + SUBS;                       // [SUBS] a product has read its probabilities
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pread + SUBS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* again = abort_flag + 1;                 // the keys have to be walked once more
+  volatile int* s_vsh = abort_flag + 2;                 // the value exponents' reference
+  volatile int* s_vbig = abort_flag + 3;                // [3] a tile has factors in s_vg
   int* err = g_attn_kv8_err;
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -107,439 +128,447 @@ __global__ void __launch_bounds__(512, 2)
   const int rt = p.row_tiles - 1 - item / planes, plane = item % planes;
   const int seq = plane / p.c.H_kv, g = plane % p.c.H_kv;
   const int n_rows = min(N, p.rows - rt * N);
+  const int subs = SUBS == 1 ? 1 : (n_rows + 127) / 128;   // the last row tile may lack its second half
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::KS; ++s) {
-      mbar_init(&kfull[s], 1);
-      mbar_init(&kempty[s], 1);
+    for (int s = 0; s < 3; ++s) {
+      mbar_init(&kfull[s], 2);
+      mbar_init(&kempty[s], subs);
+      mbar_init(&pvdone[s], subs);
     }
     for (int s = 0; s < C::VS; ++s) {
       mbar_init(&vfull[s], 1);
-      mbar_init(&vempty[s], 4);
+      mbar_init(&vempty[s], C::CONV_WARPS);
     }
-    mbar_init(qready, 8);
-    mbar_init(sfull, 1);
-    mbar_init(sfree, 8);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&kready[s], 1);
-      mbar_init(&vready[s], 4);
-      mbar_init(&pready[s], 8);
-      mbar_init(&pvdone[s], 1);
+    for (int s = 0; s < SUBS; ++s) {
+      mbar_init(&qready[s], 8);
+      for (int k = 0; k < C::SB; ++k) mbar_init(&sfull[C::SB * s + k], 1);
+      for (int k = 0; k < 3; ++k) mbar_init(&pready[3 * s + k], 8 + C::CONV_WARPS);
+      mbar_init(&mdone[s], 1);
+      mbar_init(&pread[s], 1);
     }
-    mbar_init(mdone, 1);
     *abort_flag = 0;
+    *again = 0;
     fence_mbar_init();
     prefetch_tensormap(&tmK);
     prefetch_tensormap(&tmV);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_alloc(tmem_slot, SUBS * C::SUB_COLS);
     tmem_relinquish();
   }
   griddep_launch_dependents();
   griddep_wait();
-  if (threadIdx.x < N) {
-    const int n = (int)threadIdx.x < n_rows ? (int)threadIdx.x : 0;
+  // the softmax warps: 128 rows' eight, of which w and w + 4 share 32 rows
+  const int sub_w = (warp - 4) >> 3, tid = ((warp - 4) & 7) * 32 + lane;
+  AttnQueryTile<HD, 128, 256> query;
+  if (warp >= 4 && sub_w < subs) query.load(p, seq, g, rt * SUBS + sub_w, n_rows - sub_w * 128, tid);
+  // the limits by the last N threads: loads return in order, and the query's are slow
+  if (const int k = (int)threadIdx.x - (C::THREADS - N); k >= 0) {
+    const int n = k < n_rows ? k : 0;
     const int i = (int)p.by_group.div((uint32_t)(rt * N + n));
     const int lim = p.limits ? p.limits[(long long)seq * p.R + i] : p.c.T;
-    s_lim[threadIdx.x] = min(max(lim, 0), p.c.T);
-#pragma unroll
-    for (int f = 0; f < 3; ++f) reinterpret_cast<uint32_t*>(sSF + f * C::SF_BYTES)[threadIdx.x] = 0x7f7f7f7fu;   // 1.0
+    s_lim[k] = min(max(lim, 0), p.c.T);
+    s_q[k] = 0x7f7f7f7fu;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  int lim_max, lim_min;
-  {
-    int hi = s_lim[lane], lo = hi;
+  int lim_max = 0;
 #pragma unroll
-    for (int k = 1; k < 4; ++k) {
-      hi = max(hi, s_lim[lane + 32 * k]);
-      lo = min(lo, s_lim[lane + 32 * k]);
-    }
-    lim_max = __reduce_max_sync(0xffffffffu, hi);
-    lim_min = __reduce_min_sync(0xffffffffu, lo);
-  }
+  for (int k = 0; k < N / 32; ++k) lim_max = max(lim_max, s_lim[lane + 32 * k]);
+  lim_max = __reduce_max_sync(0xffffffffu, lim_max);
   const int tiles = (lim_max + KT - 1) / KT;
   const int t0 = (int)((long long)tiles * split / p.splits), t1 = (int)((long long)tiles * (split + 1) / p.splits);
   const int nt = t1 - t0;
 
-  // the query tile, by the softmax warps
-  auto query_tile = [&](int tid) {
-    attn_query_tile<HD, N, 256>(p, seq, g, rt, n_rows, tid, sQ, sQ + C::Q_BYTES, 0, reinterpret_cast<uint32_t*>(sSF));
-    fence_async_smem();
+  auto wait = [&](uint64_t* bar, int phase) {           // decided warp-wide: tensor-memory accesses are collective
+    return __all_sync(0xffffffffu, mbar_wait_long(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
+  };
+  // Tiles count on through the second walk (T = pass * nt + t); each role walks twice in
+  // its own branch, which a register share needs, and meets the others in between.
+  auto once_more = [&](int pass) {
     __syncwarp();
-    if (lane == 0) mbar_arrive(qready);
+    named_bar_sync(1, C::THREADS);
+    const bool more = pass == 0 && *again != 0;
+    named_bar_sync(1, C::THREADS);
+    return more;
   };
 
   if (warp < 4) {
-    setmaxnreg_dec<C::REGS_REST>();   // takes a whole warpgroup: warp 3 has no other part
-    if (warp == 0) {
-      if (lane == 0) {
-        const uint64_t pol = policy_evict_last();           // the other row tiles read the same keys
-        RingPos rk{0, 0u}, rv{0, 0u};
-        int k_issued = 0, v_issued = 0;
-        for (int t = 0; t < nt; ++t) {
-          if (t >= C::KS && !mbar_wait_long(&kempty[rk.s], rk.par ^ 1u, abort_flag, err, ERR_ATTN_FULL)) break;
-          mbar_arrive_expect_tx(&kfull[rk.s], C::SLOT);
-          tma_load_3d(sK + rk.s * C::SLOT, &tmK, &kfull[rk.s], 0, (t0 + t) * KT, plane, pol);
-          rk.next(C::KS);
-          k_issued = t + 1;
-          if (t >= C::VS && !mbar_wait_long(&vempty[rv.s], rv.par ^ 1u, abort_flag, err, ERR_ATTN_FULL)) break;
-          mbar_arrive_expect_tx(&vfull[rv.s], C::SLOT);
-          tma_load_3d(sV + rv.s * C::SLOT, &tmV, &vfull[rv.s], 0, (t0 + t) * KT, plane, pol);
-          rv.next(C::VS);
-          v_issued = t + 1;
-        }
-        if (*abort_flag) {   // let copies in flight land before the CTA's shared memory goes away
-          for (int t = max(k_issued - C::KS, 0); t < k_issued; ++t)
-            mbar_wait_long(&kfull[t % C::KS], (uint32_t)(t / C::KS) & 1u, nullptr, err, ERR_ATTN_FULL);
-          for (int t = max(v_issued - C::VS, 0); t < v_issued; ++t)
-            mbar_wait_long(&vfull[t % C::VS], (uint32_t)(t / C::VS) & 1u, nullptr, err, ERR_ATTN_FULL);
-        }
-      }
-    } else if (warp == 1) {
-      const uint32_t lead = elect_one();
-      auto wait = [&](uint64_t* bar, int phase) {
-        return __all_sync(0xffffffffu, mbar_wait_long(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
-      };
-      if (nt > 0 && wait(qready, 0)) {
-        tc_fence_after();
-        constexpr uint32_t idesc_s = idesc_mxf8(128, KT);
-        // f16 operands (type 0), f32 accumulator, V MN-major
-        constexpr uint32_t idesc_o = (1u << 4) | (1u << 16) | ((uint32_t)(HD >> 3) << 17) | (8u << 24);
-        const uint32_t q0 = smem_u32(sQ), k0 = smem_u32(sK), h0 = smem_u32(sH), f0 = smem_u32(sSF);
-        tmem_cp_scales(lead, tmem + C::SF_Q, sdesc_scales(f0));
-        // A tile's key scales go to tensor memory well before its scores' products: an
-        // MMA waits for the copy in front of it.
-        auto copy_scales = [&](int t) {
-          const int b = t & 1;
-          if (!wait(&kready[b], t >> 1)) return false;
-          tmem_cp_scales(lead, tmem + C::SF_K + 4 * b, sdesc_scales(f0 + (1 + b) * C::SF_BYTES));
-          return true;
-        };
-        auto issue_s = [&](int t) {
-          const int slot = t % C::KS;
-          if ((t > 0 && !wait(sfree, t - 1)) || !wait(&kfull[slot], t / C::KS)) return false;
-          tc_fence_after();
-          const uint32_t k = k0 + slot * C::SLOT, sfk = tmem + C::SF_K + 4 * (t & 1);
-#pragma unroll
-          for (int part = 0; part < 2; ++part)
-#pragma unroll
-            for (int kk = 0; kk < HD / 32; ++kk)
-              mma_mxf8_ss(lead, tmem + C::S_COL, sdesc_rows<HD>(q0 + part * C::Q_BYTES + kk * 32),
-                          sdesc_rows<HD>(k + kk * 32), idesc_s, tmem + C::SF_Q, sfk, (part > 0 || kk > 0) ? 1u : 0u);
-          mma_commit_lead(lead, &kempty[slot]);
-          mma_commit_lead(lead, sfull);
-          return true;
-        };
-        bool ok = copy_scales(0) && issue_s(0) && (nt < 2 || copy_scales(1));
-        for (int t = 0; t < nt && ok; ++t) {
-          const int b = t & 1;
-          // the next tile's scores as soon as these have been read
-          if (t + 1 < nt && !(ok = issue_s(t + 1))) break;
-          if (!(ok = wait(&vready[b], t >> 1) && wait(&pready[b], t >> 1))) break;
-          tc_fence_after();
-          const uint32_t v = h0 + b * C::V_BYTES;
-#pragma unroll
-          for (int kk = 0; kk < KT / 16; ++kk)
-            mma_f16_ts(lead, tmem + C::O_COL, tmem + C::P_COL + kk * 8, sdesc_rows<128>(v + kk * 2048, KT * 128), idesc_o,
-                        (t > 0 || kk > 0) ? 1u : 0u);
-          mma_commit_lead(lead, &pvdone[b]);
-          if (t + 2 < nt && !(ok = copy_scales(t + 2))) break;
-        }
-        mma_commit_lead(lead, mdone);
-        mbar_wait_long(mdone, 0u, nullptr, err, ERR_ATTN_FULL);
-      }
-    } else if (warp == 2) {
-      // ------------------------------------------------------ scales, keys lane and lane + 32 of a tile
-      const uint8_t* ksc = p.c.k_scale + (long long)plane * p.c.T;
-      const uint8_t* vsc = p.c.v_scale + (long long)plane * p.c.T;
-      // bytes in four tiles, and of the next four in flight (256: past every limit)
-      uint64_t kb4[2] = {}, vb4[2] = {};
-      int kn[4][2], vn[4][2];
-      auto fetch = [&](int t) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int key = (t0 + t + e) * KT + 32 * j + lane;
-            const bool in = t + e < nt && key < lim_max;
-            kn[e][j] = in ? __ldg(ksc + key) : 127;
-            vn[e][j] = in ? __ldg(vsc + key) : 256;
-          }
-      };
-      if (nt > 0) fetch(0);
-      bool ok = true;
-      int vref = -127, low = 1000;
-      bool wide = false;
-      auto wait = [&](uint64_t* bar, int phase) {
-        return __all_sync(0xffffffffu, mbar_wait_long(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
-      };
-#pragma unroll 1
-      for (int t = 0; t < nt; ++t) {
-        const int b = t & 1;
-        if ((t & 3) == 0) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              due(kn[e][j]);
-              due(vn[e][j]);
-            }
-            kb4[j] = (uint64_t)(kn[0][j] | kn[1][j] << 16) | (uint64_t)(kn[2][j] | kn[3][j] << 16) << 32;
-            vb4[j] = (uint64_t)(vn[0][j] | vn[1][j] << 16) | (uint64_t)(vn[2][j] | vn[3][j] << 16) << 32;
-          }
-          fetch(t + 4);
-        }
-        int kc[2], ev[2], top = -1000;                      // -1000: no value to refer to
-        bool bad[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          kc[j] = (int)(kb4[j] & 0xffffu);
-          const int vc = (int)(vb4[j] & 0xffffu);
-          kb4[j] >>= 16;
-          vb4[j] >>= 16;
-          bad[j] = kc[j] == kScaleNan || vc == kScaleNan;
-          ev[j] = vc > 255 || bad[j] ? -1000 : vc - 127;
-          top = max(top, ev[j]);
-          low = min(low, ev[j] == -1000 ? 1000 : ev[j]);
-        }
-        top = __reduce_max_sync(0xffffffffu, top);
-        low = __reduce_min_sync(0xffffffffu, low);          // of the tiles so far
-        if (top - vref > (t == 0 ? 0 : kVSlack)) vref = top;
-        wide = wide || vref - low > kVSpread;
-        // tile t - 2's scores are computed and its references and factors read
-        if (t >= 2 && !(ok = wait(&pready[b], (t >> 1) - 1) && wait(&vready[b], (t >> 1) - 1))) break;
-        // a bad value makes the score NaN, so that only rows that see it are
-        *reinterpret_cast<uint2*>(sSF + (1 + b) * C::SF_BYTES + lane * 16) =
-            make_uint2((bad[0] ? 255u : (uint32_t)kc[0]) * 0x01010101u, (bad[1] ? 255u : (uint32_t)kc[1]) * 0x01010101u);
+    setmaxnreg_dec<C::REGS_REST>();   // takes a whole warpgroup
+    for (int pass = 0;; ++pass) {
+      const int base = pass * nt;
+      if (warp == 0) {
         if (lane == 0) {
-          s_vref[b] = vref;
-          s_wide[b] = wide;
+          const uint64_t pol = policy_evict_last();       // the other row tiles read the same keys
+          int k_issued = base, v_issued = base;
+          for (int T = base; T < base + nt; ++T) {
+            const int ks = T % 3, vs = T % C::VS, row = (t0 + T - base) * KT;
+            if (T >= 3 && !mbar_wait_long(&kempty[ks], (uint32_t)(T / 3 - 1) & 1u, abort_flag, err, ERR_ATTN_FULL))
+              break;
+            mbar_arrive_expect_tx(&kfull[ks], C::SLOT);
+            tma_load_3d(sK + ks * C::SLOT, &tmK, &kfull[ks], 0, row, plane, pol);
+            k_issued = T + 1;
+            if (T >= C::VS &&
+                !mbar_wait_long(&vempty[vs], (uint32_t)(T / C::VS - 1) & 1u, abort_flag, err, ERR_ATTN_FULL))
+              break;
+            mbar_arrive_expect_tx(&vfull[vs], C::SLOT);
+            tma_load_3d(sV + vs * C::SLOT, &tmV, &vfull[vs], 0, row, plane, pol);
+            v_issued = T + 1;
+          }
+          if (*abort_flag) {   // let copies in flight land before the CTA's shared memory goes away
+            for (int T = max(k_issued - 3, base); T < k_issued; ++T)
+              mbar_wait_long(&kfull[T % 3], (uint32_t)(T / 3) & 1u, nullptr, err, ERR_ATTN_FULL);
+            for (int T = max(v_issued - C::VS, base); T < v_issued; ++T)
+              mbar_wait_long(&vfull[T % C::VS], (uint32_t)(T / C::VS) & 1u, nullptr, err, ERR_ATTN_FULL);
+          }
         }
+      } else if ((warp & 1) && warp >> 1 < subs) {
+        const int sub = warp >> 1;
+        const uint32_t lead = elect_one();
+        if (nt > 0 && (pass > 0 || wait(&qready[sub], 0))) {
+          tc_fence_after();
+          constexpr uint32_t idesc_s = idesc_f8(128, KT);
+          // bf16 operands (type 1), f32 accumulator, V MN-major
+          constexpr uint32_t idesc_o =
+              (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(HD >> 3) << 17) | (8u << 24);
+          const uint32_t q0 = smem_u32(sQ) + sub * (256 * HD), k0 = smem_u32(sK), h0 = smem_u32(sH);
+          const uint32_t ts = tmem + sub * C::SUB_COLS, to = ts + C::O_COL;
+          auto issue_s = [&](int t) {
+            const int T = base + t, b = T % C::SB, slot = T % 3;
+            if (!wait(&kfull[slot], T / 3)) return false;
+            // Scores come over the probabilities that tile t - SB's product reads: nothing but its
+            // completion orders the two.  (Waited for before the keys, 162 us in place of 156.)
+            if (t >= C::SB && !wait(&pread[sub], T - C::SB)) return false;
+            tc_fence_after();
+            const uint32_t k = k0 + slot * C::SLOT;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const bool none = ev[j] == -1000;
-          s_ev[b * KT + 32 * j + lane] = none ? 0.0f : (float)ev[j];
-          s_hf[b * KT + 32 * j + lane] = none ? 0.0f : wide ? 1.0f : exp2f((float)(ev[j] - vref));
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int kk = 0; kk < HD / 32; ++kk)
+                mma_f8_ss(lead, ts + b * KT, sdesc_rows<HD>(q0 + part * (128 * HD) + kk * 32),
+                          sdesc_rows<HD>(k + kk * 32), idesc_s, (part > 0 || kk > 0) ? 1u : 0u);
+            mma_commit_lead(lead, &sfull[C::SB * sub + b]);
+            mma_commit_lead(lead, &kempty[slot]);
+            return true;
+          };
+          bool ok = issue_s(0) && (C::SB == 1 || nt < 2 || issue_s(1));
+          for (int t = 0; t < nt && ok; ++t) {
+            const int T = base + t, r = T % 3;
+            if (!wait(&pready[3 * sub + r], T / 3)) break;
+            tc_fence_after();
+            const uint32_t v = h0 + T % C::VB * C::V_BYTES, pb = ts + T % C::SB * KT;
+#pragma unroll
+            for (int kk = 0; kk < KT / 16; ++kk)
+              mma_f16_ts(lead, to, pb + kk / (KT / 32) * KH + kk % (KT / 32) * 8,
+                         sdesc_rows<128>(v + kk * 2048, KT * 128), idesc_o, (t > 0 || kk > 0) ? 1u : 0u);
+            mma_commit_lead(lead, &pvdone[r]);
+            mma_commit_lead(lead, &pread[sub]);
+            if (t + C::SB < nt) ok = issue_s(t + C::SB);
+          }
+          mma_commit_lead(lead, &mdone[sub]);
+          mbar_wait_long(&mdone[sub], (uint32_t)pass & 1u, nullptr, err, ERR_ATTN_FULL);
+        }
+      } else if (warp == 2) {
+        // -------------------------------------------------- factors of keys lane + 32 j of a tile
+        constexpr int J = KT / 32, AHEAD = 256 / KT;
+        const uint8_t* ksc = p.c.k_scale + (long long)plane * p.c.T;
+        const uint8_t* vsc = p.c.v_scale + (long long)plane * p.c.T;
+        // bytes of AHEAD tiles, and of the next AHEAD in flight; positions past every limit
+        // read the last key's and are of no account
+        uint32_t kb4[J] = {}, vb4[J] = {};
+        int kn[AHEAD][J], vn[AHEAD][J];
+        auto fetch = [&](int t) {
+#pragma unroll
+          for (int e = 0; e < AHEAD; ++e)
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+              const int key = min((t0 + t + e) * KT + 32 * j + lane, lim_max - 1);
+              kn[e][j] = __ldg(ksc + key);
+              vn[e][j] = __ldg(vsc + key);
+            }
+        };
+        if (nt > 0) fetch(0);
+        int vsh = pass == 0 ? -127 : *s_vsh, most = -127;
+        bool far = false;
+#pragma unroll 1
+        for (int t = 0; t < nt; ++t) {
+          const int T = base + t, r = T % 3;
+          if (t % AHEAD == 0) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+              kb4[j] = vb4[j] = 0;
+#pragma unroll
+              for (int e = 0; e < AHEAD; ++e) {
+                due(kn[e][j]);
+                due(vn[e][j]);
+                kb4[j] |= (uint32_t)kn[e][j] << 8 * e;
+                vb4[j] |= (uint32_t)vn[e][j] << 8 * e;
+              }
+            }
+            fetch(t + AHEAD);
+          }
+          int kb[J], ev[J], top = -1000;                  // -1000: no value counts
+          bool bad[J];
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            kb[j] = (int)(kb4[j] & 255u);
+            const int vb = (int)(vb4[j] & 255u);
+            kb4[j] >>= 8;
+            vb4[j] >>= 8;
+            bad[j] = kb[j] == kScaleNan || vb == kScaleNan;
+            ev[j] = bad[j] || (t0 + t) * KT + 32 * j + lane >= lim_max ? -1000 : vb - 127;
+            top = max(top, ev[j]);
+          }
+          top = __reduce_max_sync(0xffffffffu, top);
+          if (t == 0 && pass == 0) vsh = max(top, -127);
+          most = max(most, top);
+          far = far || top - vsh > kVRange;
+          if (T >= 3 && !wait(&pvdone[r], T / 3 - 1)) break;   // tile T - 3's factors have been read
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            const int e = ev[j] == -1000 ? -1000 : min(ev[j] - vsh, 100), at = r * KT + 32 * j + lane;
+            // a bad row makes its scores NaN, so that only rows that see it are
+            s_kf[at] = __float2bfloat16_rn(scale_value(bad[j] ? kScaleNan : kb[j]) * 0x1p-9f);
+            s_vf[at] = pow2_bf16x2(min(120 + e, 127));
+            s_vg[at] = pow2_bf16x2(max(e - 7, 0));
+          }
+          if (lane == 0) s_vbig[r] = top - vsh > 7;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&kfull[r]);
+        }
+        if (lane == 0 && pass == 0 && far) {
+          *s_vsh = most;
+          *again = 1;
+        } else if (lane == 0 && pass == 0) {
+          *s_vsh = vsh;
+        }
+      }
+      if (!once_more(pass)) break;
+    }
+  } else if (warp >= 4 + C::SOFT_WARPS) {
+    setmaxnreg_dec<C::REGS_CONV>();
+    // ------------------------------------------------------ V to bf16, KEYS keys of a tile
+    constexpr int KEYS = KT / C::CONV_WARPS, ROWS = 512 / HD;   // a warp's keys, of a step
+    const int key0 = (warp - 4 - C::SOFT_WARPS) * KEYS;
+    for (int pass = 0;; ++pass) {
+      const int base = pass * nt;
+#pragma unroll 1
+      for (int T = base; T < base + nt; ++T) {
+        const int r = T % 3, vs = T % C::VS, vb = T % C::VB;
+        if (!wait(&kfull[r], T / 3) || !wait(&vfull[vs], T / C::VS) ||
+            (T >= C::VB && !wait(&pvdone[(T - C::VB) % 3], (T - C::VB) / 3)))
+          break;
+        const uint8_t* src = sV + vs * C::SLOT;
+        uint8_t* dst = sH + vb * C::V_BYTES;
+        const bool big = s_vbig[r] != 0;
+#pragma unroll
+        for (int i = 0; i < KEYS / ROWS; ++i) {
+          // A lane takes 16 codes of a key, into two chunks of 64 dims' 128-byte row.  Eight
+          // lanes that access shared memory together touch all banks, loading and storing: two
+          // keys of 64 dims one after the other, or half of two keys of 128 dims whose
+          // numbers differ in bits 0 and 2, which the swizzles turn into the other banks.
+          int key, c;
+          if constexpr (HD == 64) {
+            key = key0 + i * ROWS + (lane >> 2);
+            c = lane & 3;
+          } else {
+            const int pair = (lane >> 4) + 2 * (i & 1);
+            key = key0 + 8 * (i >> 1) + ((lane & 4) ? pair ^ 5 : pair);
+            c = (lane & 3) + ((lane >> 1) & 4);
+          }
+          const uint32_t f = s_vf[r * KT + key];
+          const uint4 w = *reinterpret_cast<const uint4*>(src + swizzled<HD>(key, c));
+          uint32_t h[8];
+          codes_to_bf16(w.x, h[0], h[1]);
+          codes_to_bf16(w.y, h[2], h[3]);
+          codes_to_bf16(w.z, h[4], h[5]);
+          codes_to_bf16(w.w, h[6], h[7]);
+          // (past every limit the factor is 0: any code's bits are a finite bf16)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) h[k] = mul_bf16x2(h[k], f);
+          if (__builtin_expect(big, 0)) {
+            const uint32_t f2 = s_vg[r * KT + key];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) h[k] = mul_bf16x2(h[k], f2);
+          }
+          uint8_t* d = dst + (c >> 2) * (KT * 128);
+          *reinterpret_cast<uint4*>(d + swizzled<128>(key, (2 * c) & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(d + swizzled<128>(key, (2 * c + 1) & 7)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&kready[b]);
+        if (lane < subs) mbar_arrive(&pready[3 * lane + r]);
+        if (lane == 0) mbar_arrive(&vempty[vs]);
       }
-    }
-  } else if (warp >= 12) {
-    setmaxnreg_dec<C::REGS_CONV>();
-    // ------------------------------------------------------ V to halves, keys 16 cw .. 16 cw + 15 of a tile
-    const int cw = warp - 12;
-    constexpr int CH = HD / 16;                           // 16-code chunks of a row
-    auto wait = [&](uint64_t* bar, int phase) {
-      return __all_sync(0xffffffffu, mbar_wait_long(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
-    };
-#pragma unroll 1
-    for (int t = 0; t < nt; ++t) {
-      const int b = t & 1, slot = t % C::VS;
-      if (!wait(&kready[b], t >> 1) || !wait(&vfull[slot], t / C::VS) || (t >= 2 && !wait(&pvdone[b], (t >> 1) - 1)))
-        break;
-      const uint8_t* src = sV + slot * C::SLOT;
-      uint8_t* dst = sH + b * C::V_BYTES;
-      // 32 / CH keys a step; 64 dims a 128-byte row of halves
-#pragma unroll
-      for (int i = 0; i < CH / 2; ++i) {
-        const int key_l = 16 * cw + i * (32 / CH) + lane / CH, c = lane % CH;
-        const float hf = s_hf[b * KT + key_l];
-        const uint32_t f = pack_f16x2(hf, hf);
-        uint4 w = *reinterpret_cast<const uint4*>(src + swizzled<HD>(key_l, c));
-        if (hf == 0.0f) w = make_uint4(0, 0, 0, 0);       // past every limit: whatever bytes lie there
-        uint32_t h[8];
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          h[2 * k] = mul_f16x2(cvt_f16x2_e4m3x2((uint16_t)(ww[k] & 0xffffu)), f);
-          h[2 * k + 1] = mul_f16x2(cvt_f16x2_e4m3x2((uint16_t)(ww[k] >> 16)), f);
-        }
-        uint8_t* d = dst + (c >> 2) * (KT * 128);
-        *reinterpret_cast<uint4*>(d + swizzled<128>(key_l, (2 * c) & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(d + swizzled<128>(key_l, (2 * c + 1) & 7)) = make_uint4(h[4], h[5], h[6], h[7]);
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&vempty[slot]);
-        mbar_arrive(&vready[b]);
-      }
+      if (!once_more(pass)) break;
     }
   } else {
     setmaxnreg_inc<C::REGS_SOFT>();
-    const int q4 = warp & 3, row = q4 * 32 + lane, hf = (warp - 4) >> 2;   // keys 32 hf .. of a tile, dims HD / 2 * hf ..
-    const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
-    const int lim = s_lim[row];
-    if (nt > 0) query_tile((warp - 4) * 32 + lane);
-    // ------------------------------------------------------ the keys
+    // keys 32 hf .. of a tile, dims HD / 2 * hf ..
+    const int sub = sub_w, q4 = warp & 3, hf = ((warp - 4) >> 2) & 1, row = sub * 128 + q4 * 32 + lane;
+    const int pair_bar = 4 + sub * 4 + q4;
+    const bool part = nt > 0 && sub < subs;
+    const uint32_t trow = tmem + sub * C::SUB_COLS + ((uint32_t)(q4 * 32) << 16);
+    const int lim_row = s_lim[row], lim = lim_row - hf * KH, lim_min = __reduce_min_sync(0xffffffffu, lim_row);
+    if (part) {
+      query.store(n_rows - sub * 128, tid, sQ + sub * (256 * HD), sQ + sub * (256 * HD) + 128 * HD, 0, s_q + sub * 128);
+      fence_async_smem();
+      named_bar_sync(2 + sub, 256);                       // and the rows' scales are there
+      if (lane == 0) mbar_arrive(&qready[sub]);
+    }
+    // scores to base 2: the row's scale and the softmax's.  The 2^9 comes off the keys'
+    // factors, so that neither a query nor a key in bf16 takes its factor out of range (keys
+    // under 2^-90 lose bits: they matter to queries over 2^60).
+    const float rc = fminf(scale_value((int)(s_q[sub * 128 + lane * 4 + q4] & 255u)) * p.scale_log2 * 0x1p9f, 3e38f);
+    const uint64_t rc2 = f32x2(rc, rc);
     float m = 0.0f;                                       // reference (base 2) of this row
-    uint64_t l2 = 0;                                      // its sum, times 2^7, in two parts
-    int vref = 0;
-    float d = 0.0f;                                       // O is in units of 2^(m + d): d = vref until scales lie far apart
-    // After a wait that gave up (ok false) the loop goes on, so that every warp meets
-    // every barrier; the outputs are invalid and reported.
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, int phase) {           // decided warp-wide: tensor-memory accesses are collective
-      return __all_sync(0xffffffffu, mbar_wait_long(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
-    };
-    const uint64_t scale2 = f32x2(p.scale_log2, p.scale_log2);
-    for (int t = 0; t < nt; ++t) {
-      const int b = t & 1, key0 = (t0 + t) * KT;
-      ok = wait(sfull, t) && ok;
-      tc_fence_after();
-      constexpr int KH = KT / 2;
-      float s[KH];
-      tmem_ld32(trow + C::S_COL + hf * KH, s);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(sfree);
-      if (__builtin_expect(key0 + KT > lim_min, 0)) {     // some row does not see all of the tile
+    uint64_t l2 = 0;                                      // its sum, in two parts
+    for (int pass = 0;; ++pass) {
+      const int base = pass * nt;
+      m = 0.0f;
+      l2 = 0;
+      // After a wait that gave up the loop goes on, so that every warp meets every barrier;
+      // the outputs are invalid and reported.
+      for (int t = 0; t < nt && part; ++t) {
+        const int T = base + t, b = T % C::SB, r = T % 3, key0 = (t0 + t) * KT;
+        const uint32_t ts = trow + b * KT + hf * KH;
+        wait(&sfull[C::SB * sub + b], T / C::SB);
+        tc_fence_after();
+        // 32 scores, times their keys' factors
+        auto scores = [&](int k0, float (&s)[32]) {
+          tmem_ld32(ts + k0, s);
+          const uint4* kf = reinterpret_cast<const uint4*>(s_kf + r * KT + hf * KH + k0);
 #pragma unroll
-        for (int c = 0; c < KH; ++c) s[c] = key0 + hf * KH + c < lim ? s[c] : -INFINITY;
-      }
-      const int vn = s_vref[b];
-      const bool wide = s_wide[b] != 0;
-      uint32_t ph[KH / 2];
-      // Most tiles: the references stand.  A sum under 2^14 in either half means that no
-      // score is over its row's reference by 2^kRowSlack (P holds 2^7 p), so no
-      // maximum is taken.
-      bool redo = t == 0 || wide || vn != vref;
-      uint64_t tile2 = 0;
-      if (!redo) {
-        const uint64_t off2 = f32x2(kPShift - m, kPShift - m);
-        uint64_t sum[4] = {};
+          for (int c = 0; c < 32; c += 8) {
+            const uint4 f = kf[c >> 3];
+            const uint32_t w[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-        for (int c = 0; c < KH; c += 2) {
-          const float2 z = f32x2_get(fma_f32x2(f32x2(s[c], s[c + 1]), scale2, off2));
-          const float p0 = ex2(z.x), p1 = ex2(z.y);
-          sum[(c >> 1) & 3] = add_f32x2(sum[(c >> 1) & 3], f32x2(p0, p1));
-          ph[c >> 1] = pack_f16x2(p0, p1);
-        }
-        tile2 = add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3]));
-        const float2 both = f32x2_get(tile2);
-        redo = both.x + both.y >= 32768.0f;
-      }
-      if (__builtin_expect(named_bar_or(3 + q4, 64, redo), 0)) {
-        float top = s[0];
-#pragma unroll
-        for (int c = 1; c < KH; ++c) top = fmaxf(top, s[c]);
-        s_top[hf * N + row] = top;
-        named_bar_sync(3 + q4, 64);
-        top = fmaxf(top, s_top[(hf ^ 1) * N + row]) * p.scale_log2;
-        const bool up = t == 0 ? top > -INFINITY : top > m + kRowSlack;
-        const bool moved = __any_sync(0xffffffffu, up) || (!wide && vn != vref);
-        const float mn = up ? top : m;
-        const float corr = t > 0 ? exp2f(m - mn) : 1.0f;  // of the row's old sums
-        if (moved) l2 = mul_f32x2(l2, f32x2(corr, corr));
-        // this half's dims of O times f
-        auto rescale = [&](float f) {
-          if (!wait(&pvdone[b ^ 1], (t - 1) >> 1)) {
-            ok = false;
-            return;
+            for (int e = 0; e < 4; ++e) {
+              const uint64_t f2 = f32x2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+              const float2 a = f32x2_get(mul_f32x2(f32x2(s[c + 2 * e], s[c + 2 * e + 1]), f2));
+              s[c + 2 * e] = a.x;
+              s[c + 2 * e + 1] = a.y;
+            }
           }
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = hf * (HD / 2); c < (hf + 1) * (HD / 2); c += 16) {
-            float o[16];
-            tmem_ld16(trow + C::O_COL + c, o);
+          if (__builtin_expect(key0 + KT > lim_min, 0)) {   // some row does not see all of the tile
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] *= f;
-            tmem_st16(trow + C::O_COL + c, o);
+            for (int c = 0; c < 32; ++c) s[c] = key0 + k0 + c < lim ? s[c] : -INFINITY;
           }
-          tc_fence_before();
         };
-        tile2 = 0;
-        if (!wide) {
-          m = mn;
-          // exponents below -126 leave nothing of the old sums that counts
-          if (moved && t > 0) rescale(vref - vn < -126 ? 0.0f : corr * scale_value(127 + vref - vn));
-          vref = vn;
-          d = (float)vn;
+        if (__builtin_expect(t == 0 || pass > 0, 0)) {
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int k0 = 0; k0 < KH; k0 += 32) {
+            float s[32];
+            scores(k0, s);
 #pragma unroll
-          for (int c = 0; c < KH; c += 2) {
-            const float p0 = ex2(fmaf(s[c], p.scale_log2, kPShift - m));
-            const float p1 = ex2(fmaf(s[c + 1], p.scale_log2, kPShift - m));
-            tile2 = add_f32x2(tile2, f32x2(p0, p1));
-            ph[c >> 1] = pack_f16x2(p0, p1);
+            for (int c = 0; c < 32; ++c) top = fmaxf(top, s[c]);
           }
-        } else {
-          if (t > 0) d -= mn - m;                         // the products keep their reference m + d
-          m = mn;
-          float most = -INFINITY;
+          s_top[hf * N + row] = top;
+          named_bar_sync(pair_bar, 64);
+          top = fmaxf(top, s_top[(hf ^ 1) * N + row]) * rc;
+          named_bar_sync(pair_bar, 64);                   // both are read
+          const bool up = t == 0 ? top > -INFINITY : top > m + kRowSlack;
+          const float corr = t > 0 && up ? exp2f(m - top) : 1.0f;
+          if (up) m = top;
+          if (t > 0 && __any_sync(0xffffffffu, up)) {
+            l2 = mul_f32x2(l2, f32x2(corr, corr));
+            wait(&pvdone[(T - 1) % 3], (T - 1) / 3);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = hf * (HD / 2); c < (hf + 1) * (HD / 2); c += 16) {
+              float o[16];
+              tmem_ld16(trow + C::O_COL + c, o);
 #pragma unroll
-          for (int c = 0; c < KH; ++c) {
-            const float z = fmaf(s[c], p.scale_log2, -m);
-            tile2 = add_f32x2(tile2, f32x2(ex2(z + kPShift), 0.0f));
-            s[c] = z + (s_ev[b * KT + hf * KH + c] - d);
-            most = fmaxf(most, s[c]);
+              for (int i = 0; i < 16; ++i) o[i] *= corr;
+              tmem_st16(trow + C::O_COL + c, o);
+            }
           }
-          s_most[hf * N + row] = most;
-          named_bar_sync(3 + q4, 64);
-          most = fmaxf(most, s_most[(hf ^ 1) * N + row]);
-          const float un = most > -INFINITY && (t == 0 || most > kRowSlack) ? most : 0.0f;
-          d += un;
-          if (t > 0 && __any_sync(0xffffffffu, un != 0.0f)) rescale(exp2f(-un));
-#pragma unroll
-          for (int c = 0; c < KH; c += 2)
-            ph[c >> 1] = pack_f16x2(ex2(s[c] - un + kPShift), ex2(s[c + 1] - un + kPShift));
         }
+        const uint64_t m2 = f32x2(-m, -m);
+#pragma unroll 1
+        for (int k0 = 0; k0 < KH; k0 += 32) {
+          float s[32];
+          scores(k0, s);
+          uint32_t ph[16];
+          uint64_t sum[2] = {};
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float2 z = f32x2_get(fma_f32x2(f32x2(s[c], s[c + 1]), rc2, m2));
+            const float p0 = ex2(z.x), p1 = ex2(z.y);
+            sum[(c >> 1) & 1] = add_f32x2(sum[(c >> 1) & 1], f32x2(p0, p1));
+            const __nv_bfloat162 v = __floats2bfloat162_rn(p0, p1);
+            ph[c >> 1] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+          l2 = add_f32x2(l2, add_f32x2(sum[0], sum[1]));
+          tmem_st16(ts + k0 / 2, reinterpret_cast<const float*>(ph));   // over scores that have been read
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pready[3 * sub + r]);
       }
-      l2 = add_f32x2(l2, tile2);
-      // P is free once the last product is done
-      if (t > 0) ok = wait(&pvdone[b ^ 1], (t - 1) >> 1) && ok;
-      tc_fence_after();
-      tmem_st16(trow + C::P_COL + hf * (KH / 2), reinterpret_cast<const float*>(ph));
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pready[b]);
+      if (part) {
+        wait(&pvdone[(base + nt - 1) % 3], (base + nt - 1) / 3);
+        tc_fence_after();
+      }
+      const float2 l = f32x2_get(l2);
+      if (pass == 0 && l.x + l.y >= exp2f(kRowFixed)) *again = 1;   // (a NaN is no reason)
+      if (!once_more(pass)) break;
     }
     // ------------------------------------------------------ output
-    if (nt > 0) ok = wait(&pvdone[(nt - 1) & 1], (nt - 1) >> 1) && ok;
-    tc_fence_after();
     const float2 lp = f32x2_get(l2);
-    named_bar_sync(3 + q4, 64);
     s_top[hf * N + row] = lp.x + lp.y;
-    named_bar_sync(3 + q4, 64);
+    named_bar_sync(pair_bar, 64);
     const float l_sum = s_top[row] + s_top[N + row];
-    // 2^d in two steps: it alone may leave the range that the result is in
-    const float f = l_sum == 0.0f ? 0.0f : exp2f(0.5f * d) / l_sum, f2 = exp2f(0.5f * d);
-    uint32_t jh;
-    const int i = (int)p.by_group.divmod((uint32_t)(rt * N + row), jh), h = g * p.group + (int)jh;
+    // 2^vsh in two steps: it alone may leave the range that the result is in
+    const int vsh = nt > 0 ? *s_vsh : 0;
+    const float f2 = scale_value(127 + vsh / 2);
+    const float f = l_sum == 0.0f ? 0.0f : __fdividef(scale_value(127 + vsh - vsh / 2), l_sum);
     const bool valid = row < n_rows;
     const long long ws_row = ((long long)(plane * p.row_tiles + rt) * p.splits + split) * N + row;
+    // Rows leave through the query tile's place, 16 lanes (8) a row's 256 (128) bytes: a row
+    // a lane took 4 us of the stores' address cycles.
+    uint8_t* stage = sQ + row * (2 * HD);
+    constexpr int CHUNKS = HD / 8;
 #pragma unroll 1
-    for (int c = hf * (HD / 2); c < (hf + 1) * (HD / 2); c += 16) {
-      float o[16] = {};
-      if (nt > 0) tmem_ld16(trow + C::O_COL + c, o);
-      if (l_sum == 0.0f) {
+    for (int c = hf * (HD / 2); c < (hf + 1) * (HD / 2); c += 32) {
+      float o[32] = {};
+      if (part) tmem_ld32(trow + C::O_COL + c, o);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = 0.0f;         // a row that sees nothing
-      }
-      if (!valid) {
-        // nothing to store; the loads above are the whole warp's
-      } else if (p.splits > 1) {
+      for (int e = 0; e < 32; ++e) o[e] = l_sum == 0.0f ? 0.0f : o[e] * f * f2;   // a row that sees nothing: 0
+      if (p.splits > 1) {
         float4* dst = reinterpret_cast<float4*>(p.ws_o + ws_row * HD + c);
+        if (valid) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          dst[e] = make_float4(o[4 * e] * f * f2, o[4 * e + 1] * f * f2, o[4 * e + 2] * f * f2, o[4 * e + 3] * f * f2);
+          for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
       } else {
-        uint4* dst = reinterpret_cast<uint4*>(p.out + ((long long)seq * p.R + i) * p.o_rs + (long long)h * HD + c);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < 4; ++e) {
           uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(o[8 * e + 2 * k] * f * f2, o[8 * e + 2 * k + 1] * f * f2);
+            const __nv_bfloat162 v = __floats2bfloat162_rn(o[8 * e + 2 * k], o[8 * e + 2 * k + 1]);
             w[k] = *reinterpret_cast<const uint32_t*>(&v);
           }
-          dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(stage + ((((c >> 3) + e) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+      }
+    }
+    if (p.splits == 1) {
+      named_bar_sync(pair_bar, 64);
+      const int l = lane % CHUNKS;
+#pragma unroll 4
+      for (int k = 0; k < 16; k += 32 / CHUNKS) {
+        const int n = sub * 128 + q4 * 32 + hf * 16 + k + lane / CHUNKS;   // of the pair's 32 rows, 16 a warp
+        uint32_t jh;
+        const int i = (int)p.by_group.divmod((uint32_t)(rt * N + n), jh), h = g * p.group + (int)jh;
+        uint16_t* dst = p.out + ((long long)seq * p.R + i) * p.o_rs + (long long)h * HD + l * 8;
+        const uint4 w = *reinterpret_cast<const uint4*>(sQ + n * (2 * HD) + ((l ^ (n & 7)) << 4));
+        if (n < n_rows) *reinterpret_cast<uint4*>(dst) = w;
       }
     }
     if (valid && hf == 0 && p.splits > 1) *reinterpret_cast<float2*>(p.ws_ml + ws_row * 2) = make_float2(m, l_sum);
@@ -550,7 +579,7 @@ __global__ void __launch_bounds__(512, 2)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::TMEM_COLS);
+    tmem_dealloc(tmem, SUBS * C::SUB_COLS);
   }
 }
 

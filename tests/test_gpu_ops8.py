@@ -417,6 +417,26 @@ def test_attention_values_that_grow_or_vanish(torch, hd, R, H, h):
         _attention_check(got, f64(q), ca, None, hd ** -0.5, lost=2.0 ** (max(lo, hi) - 127 - 100))
 
 
+@pytest.mark.parametrize("b,R,h,hd", [(4, 100, 80, 64), (2, 200, 80, 128)])
+def test_attention_many_heads_leave_the_keys_whole(torch, b, R, h, hd):
+    """So many rows that one walk has all keys of a head: once, and (scores and value
+    scales that grow) a second time."""
+    rng = np.random.default_rng(15)
+    T = 450
+    limits = _causal(b, R, T, [T - 60 * s for s in range(b)])
+    for loud, hi in ((1.0, 127), (64.0, 230)):
+        q, ca, lim = _attention_case(torch, rng, b, R, h, h, T, hd, limits, loud=loud)
+        assert binding.attention_kv8_workspace(b, h, h, hd, R, T) == 0
+        e = np.full((b, h, T), 127, dtype=np.uint8)
+        e[:, ::2, 300:] = hi
+        ca.scales[1].copy_(dev(torch, e))
+        out = _attend(torch, q, ca, lim, h, R)
+        # products under 2^-126 of the largest value scale are lost in float32 (a probability of 2^-400
+        # in float64 is nothing here), T * 448 * 2^-126 < 2^-100
+        _attention_check(f64(out), f64(q), ca, limits, hd ** -0.5, lost=2.0 ** (hi - 127 - 100))
+        assert torch.equal(out, _attend(torch, q, ca, lim, h, R))
+
+
 @pytest.mark.parametrize("R,H,h", [(1, 8, 2), (16, 4, 4), (140, 2, 1)])
 @pytest.mark.parametrize("hd", [64, 128])
 def test_attention_ignores_what_lies_behind_the_limits(torch, hd, R, H, h):
