@@ -92,10 +92,11 @@ using namespace dllm;
 
 extern "C" dllm_status dllm_op_attention_kv8_workspace(int32_t b, int32_t H, int32_t H_kv, int32_t hd, int32_t R,
                                                        int32_t T, int64_t* bytes) {
-  if (!bytes || b < 1 || H < 1 || H_kv < 1 || H % H_kv || (hd != 64 && hd != 128) || R < 1 || T < 1)
+  if (!bytes || b < 1 || H < 1 || H_kv < 1 || H % H_kv || (hd != 64 && hd != 128) || R < 1 || T < 1 ||
+      T > kMostRows)
     return op_fail(DLLM_EINVAL, "bad attention shape: b=%d H=%d H_kv=%d hd=%d R=%d T=%d", b, H, H_kv, hd, R, T);
   const long long rows = (long long)R * (H / H_kv);
-  if (rows > (1LL << 30) || (__int128)b * R * H > (1LL << 31))
+  if (rows > (1LL << 30) || (__int128)b * R * H > 0x7fffffff)
     return op_fail(DLLM_EINVAL, "attention_kv8: b=%d R=%d H=%d are too many rows", b, R, H);
   *bytes = (int64_t)plan_attn_kv8(b, H_kv, rows, hd, T).ws_bytes;
   return DLLM_OK;
@@ -106,10 +107,11 @@ extern "C" dllm_status dllm_op_attention_kv8(const uint16_t* q, int64_t q_row_st
                                              int64_t out_row_stride, int32_t H, int32_t R, void* workspace,
                                              int64_t workspace_bytes, void* stream) {
   if (const dllm_status s = kv8_check(cache, "attention_kv8"); s != DLLM_OK) return s;
-  if (!q || !out || H < 1 || H % cache->H_kv || R < 1 || !(scale > 0.0f) || !std::isfinite(scale) ||
+  if (!q || !out || H < 1 || H % cache->H_kv || R < 1 || !(scale > 0.0f) || !(scale <= 1e30f) ||
       !op_aligned(q, 16) || !op_aligned(out, 16) || !op_aligned(limits, 4))
     return op_fail(DLLM_EINVAL,
-                   "bad attention_kv8 arguments: H=%d (a multiple of H_kv=%d) R=%d scale=%g, q and out 16-byte aligned",
+                   "bad attention_kv8 arguments: H=%d (a multiple of H_kv=%d) R=%d scale=%g (over 0, to 1e30), q and out 16-byte "
+                   "aligned",
                    H, cache->H_kv, R, scale);
   const long long width = (long long)H * cache->hd;
   AttnKv8Params p = {};

@@ -638,7 +638,7 @@ extern "C" dllm_status dllm_op_gemm8(const uint8_t* W, const uint8_t* W_scale, c
                                      const uint8_t* X_scale, void* Y, int32_t y_dtype, int32_t M, int32_t N, int32_t K,
                                      void* stream) {
   if (!W || !W_scale || !X || !X_scale || !Y || (y_dtype != DLLM_F32 && y_dtype != DLLM_BF16) || M < 1 || N < 1 ||
-      K < 16 || K % 16 || !op_aligned(W, 16) || !op_aligned(X, 16) || !op_aligned(Y, 16))
+      M > kMostRows || N > kMostRows || K < 16 || K % 16 || !op_aligned(W, 16) || !op_aligned(X, 16) || !op_aligned(Y, 16))
     return op_fail(DLLM_EINVAL,
                    "bad gemm8 arguments: M=%d N=%d K=%d (K %% 16 == 0) y_dtype=%d (float32 or bf16), W, X and Y "
                    "16-byte aligned",

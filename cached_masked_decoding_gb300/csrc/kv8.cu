@@ -122,10 +122,10 @@ __global__ void __launch_bounds__(256, 4) kv8_load_kernel(const __grid_constant_
 }
 
 dllm_status kv8_check(const dllm_kv8* c, const char* who) {
-  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || c->b < 1 || c->H_kv < 1 || c->T < 1 ||
+  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || c->b < 1 || c->H_kv < 1 || c->T < 1 || c->T > kMostRows ||
       (c->hd != 64 && c->hd != 128) || !op_aligned(c->k, 16) || !op_aligned(c->v, 16))
-    return op_fail(DLLM_EINVAL, "%s: bad cache (b, H_kv, T >= 1, hd 64 or 128, codes 16-byte aligned)%s", who,
-                   c ? "" : ": null");
+    return op_fail(DLLM_EINVAL, "%s: bad cache (b, H_kv >= 1, T 1..%d, hd 64 or 128, codes 16-byte aligned)%s", who,
+                   kMostRows, c ? "" : ": null");
   if ((__int128)c->b * c->H_kv * c->T > ((__int128)1 << 48))
     return op_fail(DLLM_EINVAL, "%s: a cache of b=%d H_kv=%d T=%d is too large", who, c->b, c->H_kv, c->T);
   return DLLM_OK;

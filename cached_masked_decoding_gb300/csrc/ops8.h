@@ -74,6 +74,10 @@ struct FastDiv {
 #endif
 };
 
+// Most rows of a tiled axis (a cache's positions, a product's sides): tiles past the end and
+// the prefetches ahead of them stay in 31 bits.
+constexpr int32_t kMostRows = 0x7fffffff - 4095;
+
 inline bool op_aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline int op_dtype_size(int32_t t) { return t == DLLM_F32 ? 4 : (t == DLLM_BF16 || t == DLLM_F16) ? 2 : 0; }
 

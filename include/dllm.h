@@ -526,7 +526,9 @@ dllm_status dllm_op_rope(const void* x, void* out, const int32_t* positions, int
 
 /* An 8-bit K/V cache in the caller's device memory: codes [b][H_kv][T][hd]
  * (16-byte aligned) and scale bytes [b][H_kv][T], one scale for each row of hd
- * (a token's head).  hd in {64, 128}.  The struct is read during the call. */
+ * (a token's head).  hd in {64, 128}, T at most 2^31 - 4096.  The codes 0x7f and 0xff (NaN in
+ * e4m3) are never stored; what a caller's own cache makes of them is not defined.  The struct is
+ * read during the call. */
 typedef struct dllm_kv8 {
     uint8_t *k, *v, *k_scale, *v_scale;
     int32_t b, H_kv, T, hd;
@@ -564,7 +566,7 @@ dllm_status dllm_op_kv8_load(const dllm_kv8* cache, void* k, void* v, int64_t k_
  * statistics and sums are float32; a probability enters the value product
  * with 8 significant bits (an error of 2^-8 of itself, or of 2^-21 of the
  * largest p * 2^ev of its row among 32 neighbouring keys where that is more).
- * scale: finite, > 0.  workspace: device memory for the partial results of
+ * scale: > 0, at most 1e30.  workspace: device memory for the partial results of
  * split keys, 16-byte aligned, at least dllm_op_attention_kv8_workspace
  * bytes (0: may be NULL), contents irrelevant; calls that may run at the same
  * time need one each. */

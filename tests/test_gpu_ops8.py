@@ -739,3 +739,68 @@ def test_two_graphs_and_two_streams(torch):
         for g, (y, att) in zip(layers, want):
             assert torch.equal(g["y"], y) and torch.equal(g["att"], att)
     assert binding.op_check() == 0
+
+
+FIRST_CALLS = """
+import numpy as np
+import torch
+from cached_masked_decoding_gb300 import binding
+
+def forward(s):
+    rope = binding.make_rope(hd)
+    binding.op_quantise8(x.data_ptr(), "bf16", N, K, xc.data_ptr(), xs.data_ptr(), stream=s)
+    for n, y in ys.items():
+        binding.op_gemm8(wc.data_ptr(), ws.data_ptr(), xc.data_ptr(), xs.data_ptr(), y.data_ptr(), "bf16", M, n, K, stream=s)
+    binding.op_rope(q.data_ptr(), q.data_ptr(), pos.data_ptr(), T, H, hd, "bf16", rope, stream=s)
+    binding.op_kv8_store(cache, kv[0].data_ptr(), kv[1].data_ptr(), "bf16", T, stream=s)
+    binding.op_kv8_load(cache, back[0].data_ptr(), back[1].data_ptr(), "bf16", T, stream=s)
+    for r, (o, w) in outs.items():
+        binding.op_attention_kv8(q.data_ptr(), cache, o.data_ptr(), H, r, ws_ptr=w.data_ptr(), ws_bytes=w.numel(), stream=s)
+
+torch.manual_seed(0)
+M, N, K, H, T, hd = 4096, 800, 512, 2, 600, 128
+z = lambda *s, t=torch.uint8: torch.zeros(*s, device="cuda", dtype=t)
+x = torch.randn(N, K, device="cuda").to(torch.bfloat16)
+wc = torch.randint(0, 0x7e, (M, K), device="cuda", dtype=torch.uint8)
+ws = torch.full((K // 128, M), 120, device="cuda", dtype=torch.uint8)
+xc, xs = z(N, K), z(K // 128, N)
+ys = {n: z(n, M, t=torch.bfloat16) for n in (1, 50, 100, N)}
+pos = torch.arange(T, device="cuda", dtype=torch.int32)
+q0 = torch.randn(T, H, hd, device="cuda").to(torch.bfloat16)
+q = q0.clone()
+kv = torch.randn(2, T, 1, hd, device="cuda").to(torch.bfloat16)
+back = torch.zeros_like(kv)
+kc, ks = z(2, 1, 1, T, hd), z(2, 1, 1, T)
+cache = binding.make_kv8(kc[0].data_ptr(), kc[1].data_ptr(), ks[0].data_ptr(), ks[1].data_ptr(), 1, 1, T, hd)
+outs = {r: (z(r, H, hd, t=torch.bfloat16), z(max(binding.attention_kv8_workspace(1, H, 1, hd, r, T), 16)))
+        for r in (1, 8, 16, 32, 64, 300)}
+torch.cuda.synchronize()
+s = torch.cuda.Stream()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g, stream=s):
+    forward(s.cuda_stream)
+g.replay()
+torch.cuda.synchronize()
+tensors = [xc, xs, *ys.values(), q, kc, ks, back, *[o for o, _ in outs.values()]]
+got = [t.clone() for t in tensors]
+assert all(t.float().abs().sum() > 0 for t in got)
+for t in tensors:
+    t.zero_()
+q.copy_(q0)
+forward(0)
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, tensors))
+assert binding.op_check() == 0
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_can_be_captured(torch):
+    """Every kernel's first launch inside a capture, in a process of its own: the same bits
+    as launched directly."""
+    import subprocess
+    import sys
+    from pathlib import Path
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=Path(__file__).resolve().parent.parent,
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stdout[-500:] + r.stderr[-2000:]

@@ -121,6 +121,18 @@ def test_attention_refuses_bad_arguments():
     assert binding.lib().dllm_op_attention_kv8_workspace(1, 8, 4, 128, 1, 8, None) == binding.EINVAL
 
 
+def test_sizes_whose_tiles_leave_31_bits_are_refused():
+    far = 2 ** 31 - 4095
+    for T in (far, 2 ** 31 - 1):
+        refused(binding.op_kv8_store, cache(b=1, h=1, t=T), A, A, "bf16", 1)
+        refused(binding.op_attention_kv8, A, cache(b=1, h=1, t=T), A, 1, 1)
+        refused(binding.attention_kv8_workspace, 1, 1, 1, 64, 1, T)
+    assert binding.attention_kv8_workspace(1, 1, 1, 64, 1, far - 1) >= 0
+    refused(binding.op_attention_kv8, A, cache(), A, 8, 1, scale=2e38)
+    for M, N in ((far, 8), (8, far)):
+        refused(binding.op_gemm8, A, A, A, A, A, "bf16", M, N, 16)
+
+
 def test_product_refuses_bad_arguments():
     for args in [(0, "bf16", 4, 64, A, A), (A, "bf16", 0, 64, A, A), (A, "bf16", 4, 8, A, A), (A, "bf16", 4, 72, A, A),
                  (A, "bf16", 4, 64, 0, A), (A, "bf16", 4, 64, A, 0), (A, "bf16", 4, 64, A + 8, A),
