@@ -2,10 +2,16 @@
 // back.  One scale for each row of hd elements (a token's head), see q8.cuh.
 //
 // Both directions are bound by HBM (store reads 2 hd elements and writes
-// 2 hd + 2 bytes a token and head).  A group of hd / 8 lanes owns a row: each
-// lane takes one 16-byte vector of 16-bit elements, the row's largest value
+// 2 hd + 2 bytes a token and head).  A group of hd / 8 lanes owns a row of K and that of V
+// (the slot's arithmetic, a third of the instructions, serves both): each lane
+// takes one 16-byte vector of 16-bit elements, the row's largest value
 // is a shuffle reduction within the group, and a row's codes are one
-// contiguous write of hd bytes.  K and V go in one launch.
+// contiguous write of hd bytes.  Consecutive groups take consecutive tokens of a head,
+// whose codes and scale bytes lie side by side in the cache (5 % faster than
+// consecutive heads of a token, whose elements do: 49 against 51 us for 3 x 5000
+// tokens of 16 heads of 64 in float32).  A second row in flight in every thread made it slower
+// (64 x 32 tokens of 32 heads of 128 in bf16, store and load, 21.5 us against 20.3, 4.1 TB/s; 4 x 1000
+// tokens of 8 heads of 64, 8.9 against 6.9).
 #include "ops8.h"
 #include "ptx8.cuh"
 #include "q8.cuh"
@@ -32,8 +38,8 @@ struct Kv8Item {
   __device__ __forceinline__ bool init(const Kv8Params& p, uint32_t g) {
     if (g >= p.groups) return false;
     uint32_t i;
-    row = p.heads.divmod(g, h);
-    const uint32_t s = p.rows.divmod(row, i);
+    const uint32_t s = p.heads.divmod(p.rows.divmod(g, i), h);
+    row = s * (uint32_t)p.R + i;
     const int n = p.counts ? __ldg(p.counts + s) : p.R;
     if ((int)i >= n) return false;
     const long long pos = (long long)(p.starts ? __ldg(p.starts + s) : 0) + i;
@@ -43,82 +49,59 @@ struct Kv8Item {
   }
 };
 
-// A block takes 256 / L * AHEAD consecutive row-heads, a thread group every
-// (256 / L)-th of them, K and V of each (the slot's arithmetic, a third of
-// the kernel's instructions, serves both): all loads are issued before the first is used.
-template <typename E, int HD, int AHEAD>
+template <typename E, int HD>
 __global__ void __launch_bounds__(256, 4) kv8_store_kernel(const __grid_constant__ Kv8Params p) {
-  constexpr int L = HD / 8, GROUPS = 256 / L;
+  constexpr int L = HD / 8;
   const int l = threadIdx.x % L;
   griddep_launch_dependents();
   griddep_wait();
-  const uint32_t g0 = blockIdx.x * (uint32_t)(GROUPS * AHEAD) + threadIdx.x / L;
-  Kv8Item it[AHEAD];
-  bool on[AHEAD];
-  Raw8<E> raw[AHEAD][2];
+  Kv8Item it;
+  const bool on = it.init(p, blockIdx.x * (uint32_t)(256 / L) + threadIdx.x / L);
+  Raw8<E> raw[2];
 #pragma unroll
-  for (int k = 0; k < AHEAD; ++k) on[k] = it[k].init(p, g0 + k * GROUPS);
+  for (int w = 0; w < 2; ++w) {
+    raw[w].zero();
+    if (on) raw[w].template load<L>(static_cast<const typename E::T*>(p.in[w]) + it.row * p.rs[w] + it.h * HD, l);
+  }
 #pragma unroll
-  for (int k = 0; k < AHEAD; ++k)
+  for (int w = 0; w < 2; ++w) {
+    float x[8];
+    raw[w].floats(x);
+    uint32_t m = abs_bits8(x);
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      raw[k][w].zero();
-      if (on[k])
-        raw[k][w].template load<L>(static_cast<const typename E::T*>(p.in[w]) + it[k].row * p.rs[w] + it[k].h * HD, l);
-    }
-#pragma unroll
-  for (int k = 0; k < AHEAD; ++k)
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      float x[8];
-      raw[k][w].floats(x);
-      uint32_t m = abs_bits8(x);
-#pragma unroll
-      for (int d = L / 2; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-      if (!on[k]) continue;
-      const int byte = scale_byte(m);
-      uint2 codes = make_uint2(0, 0);
-      if (byte != kScaleNan) codes = encode8(x, scale_inverse(byte));
-      Raw8<E>::template store_codes<L>((w ? p.c.v : p.c.k) + it[k].slot * HD, l, codes);
-      if (l == 0) (w ? p.c.v_scale : p.c.k_scale)[it[k].slot] = (uint8_t)byte;
-    }
+    for (int d = L / 2; d >= 1; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (!on) continue;
+    const int byte = scale_byte(m);
+    uint2 codes = make_uint2(0, 0);
+    if (byte != kScaleNan) codes = encode8(x, scale_inverse(byte));
+    Raw8<E>::template store_codes<L>((w ? p.c.v : p.c.k) + it.slot * HD, l, codes);
+    if (l == 0) (w ? p.c.v_scale : p.c.k_scale)[it.slot] = (uint8_t)byte;
+  }
 }
 
-template <typename E, int HD, int AHEAD>
+template <typename E, int HD>
 __global__ void __launch_bounds__(256, 4) kv8_load_kernel(const __grid_constant__ Kv8Params p) {
-  constexpr int L = HD / 8, GROUPS = 256 / L;
+  constexpr int L = HD / 8;
   const int l = threadIdx.x % L;
   griddep_launch_dependents();
   griddep_wait();
-  const uint32_t g0 = blockIdx.x * (uint32_t)(GROUPS * AHEAD) + threadIdx.x / L;
-  Kv8Item it[AHEAD];
-  bool on[AHEAD];
-  uint2 codes[AHEAD][2];
-  int byte[AHEAD][2];
+  Kv8Item it;
+  if (!it.init(p, blockIdx.x * (uint32_t)(256 / L) + threadIdx.x / L)) return;
+  uint2 codes[2];
+  int byte[2];
 #pragma unroll
-  for (int k = 0; k < AHEAD; ++k) on[k] = it[k].init(p, g0 + k * GROUPS);
+  for (int w = 0; w < 2; ++w) {
+    codes[w] = Raw8<E>::template load_codes<L>((w ? p.c.v : p.c.k) + it.slot * HD, l);
+    byte[w] = __ldg((w ? p.c.v_scale : p.c.k_scale) + it.slot);
+  }
 #pragma unroll
-  for (int k = 0; k < AHEAD; ++k)
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      codes[k][w] = make_uint2(0, 0);
-      byte[k][w] = 127;
-      if (on[k]) {
-        codes[k][w] = Raw8<E>::template load_codes<L>((w ? p.c.v : p.c.k) + it[k].slot * HD, l);
-        byte[k][w] = __ldg((w ? p.c.v_scale : p.c.k_scale) + it[k].slot);
-      }
-    }
-#pragma unroll
-  for (int k = 0; k < AHEAD; ++k)
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      if (!on[k]) continue;
-      float x[8];
-      decode8(codes[k][w], scale_value(byte[k][w]), x);
-      Raw8<E> out;
-      out.from(x);
-      out.template store<L>(static_cast<typename E::T*>(p.out[w]) + it[k].row * p.rs[w] + it[k].h * HD, l);
-    }
+  for (int w = 0; w < 2; ++w) {
+    float x[8];
+    decode8(codes[w], scale_value(byte[w]), x);
+    Raw8<E> out;
+    out.from(x);
+    out.template store<L>(static_cast<typename E::T*>(p.out[w]) + it.row * p.rs[w] + it.h * HD, l);
+  }
 }
 
 dllm_status kv8_check(const dllm_kv8* c, const char* who) {
@@ -133,20 +116,17 @@ dllm_status kv8_check(const dllm_kv8* c, const char* who) {
 
 namespace {
 
-template <typename E, int HD, int AHEAD>
+template <typename E, int HD>
 cudaError_t launch_kv8(const Kv8Params& p, bool store, cudaStream_t st) {
-  constexpr uint32_t per_block = 256 / (HD / 8) * AHEAD;
+  constexpr uint32_t per_block = 256 / (HD / 8);
   const dim3 grid((p.groups + per_block - 1) / per_block);
-  return store ? op_launch(kv8_store_kernel<E, HD, AHEAD>, grid, dim3(256), 0, st, 1, p)
-               : op_launch(kv8_load_kernel<E, HD, AHEAD>, grid, dim3(256), 0, st, 1, p);
+  return store ? op_launch(kv8_store_kernel<E, HD>, grid, dim3(256), 0, st, 1, p)
+               : op_launch(kv8_load_kernel<E, HD>, grid, dim3(256), 0, st, 1, p);
 }
 
-// Two row-heads a thread group once that still leaves every SM two blocks.
 template <typename E>
 cudaError_t launch_kv8(const Kv8Params& p, bool store, cudaStream_t st) {
-  const bool ahead = p.groups >= 2u * op_device_sms() * (256 / (p.c.hd / 8) * 2);
-  if (p.c.hd == 64) return ahead ? launch_kv8<E, 64, 2>(p, store, st) : launch_kv8<E, 64, 1>(p, store, st);
-  return ahead ? launch_kv8<E, 128, 2>(p, store, st) : launch_kv8<E, 128, 1>(p, store, st);
+  return p.c.hd == 64 ? launch_kv8<E, 64>(p, store, st) : launch_kv8<E, 128>(p, store, st);
 }
 
 dllm_status kv8_rows(const dllm_kv8* cache, bool store, const void* k, const void* v, int64_t k_rs, int64_t v_rs,

@@ -11,7 +11,8 @@
 //
 // Bound by HBM: one read and one write of x.  A thread owns 8 pairs of a row
 // (two 16-byte vectors of 16-bit elements) and walks up to 8 heads with the
-// same cosines, four heads' loads in flight.
+// same cosines, four heads' loads in flight.  8191 rows of 40 heads of 128, bf16, half
+// of them turned: 28.7 us, 5.8 TB/s; 32 rows of 64 heads: 2.6 us, a launch's latency.
 #include <algorithm>
 #include <cmath>
 
@@ -221,7 +222,7 @@ extern "C" dllm_status dllm_op_rope(const void* x, void* out, const int32_t* pos
   }
   p.amp = (float)(r->amplitude > 0.0 ? r->amplitude : amp);
   // theta^(-2i/rot) as the product of a power for i's upper and one for its lower
-  // three bits: 24 powers at most in place of 128 (each is most of the call's host time)
+  // three bits: 24 powers at most in place of 128 on the calling thread
   double lower[8], upper = 1.0;
   for (int i = 0; i < std::min(pairs, 8); ++i) lower[i] = std::pow(theta, -2.0 * i / p.rot);
   for (int i = 0; i < pairs; ++i) {
@@ -242,7 +243,7 @@ extern "C" dllm_status dllm_op_rope(const void* x, void* out, const int32_t* pos
   const bool vec = hd % 16 == 0 && p.rot % 16 == 0 && op_aligned(x, 16) && op_aligned(out, 16) && p.x_rs % v16 == 0 &&
                    p.x_hs % v16 == 0 && p.o_rs % v16 == 0 && p.o_hs % v16 == 0;
   // Heads a thread walks: as many, up to 8, as leave half the GPU's threads an
-  // item (8191 rows of 40 heads: 8 heads 34 us, 1 head 63 us; 32 rows of 64 heads
+  // item (8191 rows of 40 heads: 8 heads 29 us, 1 head 68 us; 32 rows of 64 heads
   // take 1).
   const long long units = hd / (vec ? 16 : 2);
   p.head_run = 8;
