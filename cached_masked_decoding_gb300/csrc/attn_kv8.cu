@@ -129,6 +129,7 @@ extern "C" dllm_status dllm_op_attention_kv8(const uint16_t* q, int64_t q_row_st
   p.R = R;
   p.group = H / cache->H_kv;
   p.by_group = FastDiv((uint32_t)p.group);
+  p.by_heads = FastDiv((uint32_t)cache->H_kv);
   p.scale_log2 = scale * 1.4426950408889634f;
   int64_t need = 0;
   if (const dllm_status s = dllm_op_attention_kv8_workspace(cache->b, H, cache->H_kv, cache->hd, R, cache->T, &need);
@@ -141,6 +142,8 @@ extern "C" dllm_status dllm_op_attention_kv8(const uint16_t* q, int64_t q_row_st
   const AttnKv8Plan a = plan_attn_kv8(cache->b, cache->H_kv, p.rows, cache->hd, cache->T);
   p.row_tiles = a.row_tiles;
   p.splits = a.splits;
+  p.by_splits = FastDiv((uint32_t)a.splits);
+  p.by_tiles = FastDiv((uint32_t)(a.N < 128 ? a.row_tiles : cache->b * cache->H_kv));
   p.cluster = a.cluster;
   p.ws_o = static_cast<float*>(workspace);
   p.ws_ml = p.ws_o + (a.ws_bytes ? a.items * a.splits * a.N * cache->hd : 0);

@@ -54,9 +54,10 @@ struct AttnKv8Params {
   const int32_t* limits;
   long long q_rs, o_rs;
   int H, R, group;        // group = H / H_kv query heads share a cached head
-  FastDiv by_group;
   int rows, row_tiles;    // R * group rows of an item, in tiles of N
   int splits, cluster;    // cluster: the splits of an item are one
+  FastDiv by_group, by_splits, by_heads;
+  FastDiv by_tiles;       // by row_tiles (few rows) or by b * H_kv
   float scale_log2;
   float *ws_o, *ws_ml;    // [item][split][N][hd] and [item][split][N][2]
 };
@@ -79,8 +80,8 @@ struct AttnRowsCfg {
   static constexpr int P_BYTES = KT * P_ROW;
   static constexpr int SLOTS = CTAS == 1 ? (HD == 64 ? 16 : 9) : HD == 64 ? 8 : N == 8 ? 6 : 5;
   static constexpr int SF_BYTES = 512;                  // ones, query scales, two buffers of probability scales
-  // warp maxima (two), m, d, limits, scales, (m, l) of 8 splits
-  static constexpr int STAT_FLOATS = 8 * N + 3 * N + 4 * N + 16 * N;
+  // warp maxima (two), m, d, limits, scales, (m, l) of 8 splits, warps' sums
+  static constexpr int STAT_FLOATS = 8 * N + 3 * N + 4 * N + 16 * N + 4 * N;
   static constexpr int SMEM_BYTES = 1024 + SLOTS * SLOT + Q_PARTS * Q_BYTES + 2 * P_BYTES + 4 * SF_BYTES +
                                     STAT_FLOATS * 4 + (2 * SLOTS + 10) * 8 + 24;
   static constexpr int S_COL = 0;                       // two buffers
@@ -187,7 +188,8 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
   float* s_inv = reinterpret_cast<float*>(s_lim + N);   // [softmax warps][RW] inverse block scales
   float* s_cm = s_inv + 4 * N;                          // [8][N] reference maxima of the cluster's splits
   float* s_cl = s_cm + 8 * N;                           // [8][N] and sums
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_cl + 8 * N);
+  float* s_ls = s_cl + 8 * N;                           // [4][N] the warps' sums
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_ls + 4 * N);
   uint64_t* empty = full + C::SLOTS;
   uint64_t* qready = empty + C::SLOTS;
   uint64_t* sfull = qready + 1;                         // [2]
@@ -201,10 +203,11 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
   int* err = g_attn_kv8_err;
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int split = (int)(blockIdx.x % (unsigned)p.splits);
-  const int item = (int)(blockIdx.x / (unsigned)p.splits);
-  const int rt = item % p.row_tiles, plane = item / p.row_tiles;      // plane = seq * H_kv + cached head
-  const int seq = plane / p.c.H_kv, g = plane % p.c.H_kv;
+  uint32_t split_u, rt_u, g_u;
+  const int item = (int)p.by_splits.divmod(blockIdx.x, split_u);
+  const int plane = (int)p.by_tiles.divmod((uint32_t)item, rt_u);     // seq * H_kv + cached head
+  const int seq = (int)p.by_heads.divmod((uint32_t)plane, g_u);
+  const int split = (int)split_u, rt = (int)rt_u, g = (int)g_u;
   const int n_rows = min(N, p.rows - rt * N);
 
   if (threadIdx.x == 0) {
@@ -232,6 +235,17 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
   }
   griddep_launch_dependents();
   griddep_wait();
+  // the softmax warps ask for the query tile at once
+  const int tid = (warp - 2) * 32 + lane;
+  AttnQueryTile<HD, N, C::SOFT> query;
+  if (warp >= 2) {
+    query.load(p, seq, g, rt, n_rows, tid);
+    if (tid < 128) {
+#pragma unroll
+      for (int f = 0; f < 4; ++f) reinterpret_cast<uint32_t*>(sSF + f * C::SF_BYTES)[tid] = 0x7f7f7f7fu;
+    }
+    if (tid < N) s_m[tid] = 0.0f;
+  }
   // limits of the tile's rows; rows past the last see what row 0 sees and are not stored
   if (threadIdx.x < N) {
     const int n = (int)threadIdx.x < n_rows ? (int)threadIdx.x : 0;
@@ -256,8 +270,8 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
   }
   // this split's keys: whole tiles, shared out evenly over the keys some row sees
   const int tiles = (lim_max + KT - 1) / KT;
-  const int t0 = (int)((long long)tiles * split / p.splits), t1 = (int)((long long)tiles * (split + 1) / p.splits);
-  const int nt = t1 - t0;
+  const int t0 = (int)p.by_splits.div((uint32_t)(tiles * split));
+  const int nt = (int)p.by_splits.div((uint32_t)(tiles * (split + 1))) - t0;
 
   float l_sum[RW];                                        // softmax: this key lane's sums of its rows
   // tiles count on through the second walk: T of a tile is pass * nt + t
@@ -339,7 +353,6 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
       const int q4 = warp & 3, key_l = q4 * 32 + lane;    // this thread's key in a tile, and its tensor-memory lane
       const int row0 = ((warp - 2) >> 2) * RW;            // its first row
       const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
-      const int tid = (warp - 2) * 32 + lane;
       // product t of P V is done
       auto pv_wait = [&](int t) {
         const int T = base + t;
@@ -366,16 +379,7 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
         if (tid < N) s_m[tid] = s_d[tid] = 0.0f;
         named_bar_sync(2, C::SOFT);
       } else if (nt > 0) {
-        // ---------------------------------------------------- the query tile
-        if (tid < 128) {
-#pragma unroll
-          for (int f = 0; f < 4; ++f) reinterpret_cast<uint32_t*>(sSF + f * C::SF_BYTES)[tid] = 0x7f7f7f7fu;
-        }
-        if (tid < N) s_m[tid] = 0.0f;
-        named_bar_sync(2, C::SOFT);
         // 8 rows: the lo rows lie behind the hi rows of one operand
-        AttnQueryTile<HD, N, C::SOFT> query;
-        query.load(p, seq, g, rt, n_rows, tid);
         query.store(n_rows, tid, sQ, sQ + (C::Q_PARTS - 1) * C::Q_BYTES, C::Q_PARTS == 1 ? N : 0,
                     reinterpret_cast<uint32_t*>(sSF + C::SF_BYTES));
         fence_async_smem();
@@ -603,16 +607,30 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
         __syncwarp();
         if (lane == 0) mbar_arrive(&pready[b]);
       }
-      if (nt > 0) {
-        if (ok) ok = pv_wait(nt - 1);
-        tc_fence_after();
-      }
       // a product or a sum over what float32 and the block scales hold (a NaN is no reason)
       constexpr uint32_t kOver = (uint32_t)(127 + kRefFixed) << 23;
       bool over = far || (most >= kOver && most <= 0x7f800000u);
 #pragma unroll
       for (int j = 0; j < RW; ++j) over = over || l_sum[j] >= __uint_as_float(kOver);
       if (pass == 0 && over) *again = 1;
+      // sum RW columns over the warp, lane c (modulo RW) ending with column c, while the last product runs
+#pragma unroll
+      for (int s = RW / 2; s >= 1; s >>= 1) {
+        const bool upper = (lane & s) != 0;
+#pragma unroll
+        for (int i = 0; i < s; ++i) {
+          const float send = upper ? l_sum[i] : l_sum[i + s];
+          const float keep = upper ? l_sum[i + s] : l_sum[i];
+          l_sum[i] = keep + __shfl_xor_sync(0xffffffffu, send, s);
+        }
+      }
+#pragma unroll
+      for (int s = RW; s < 32; s <<= 1) l_sum[0] += __shfl_xor_sync(0xffffffffu, l_sum[0], s);
+      if (lane < RW) s_ls[q4 * N + row0 + lane] = l_sum[0];
+      if (nt > 0) {
+        if (ok) ok = pv_wait(nt - 1);
+        tc_fence_after();
+      }
     }
     // lanes that skipped their role arrive here first: reconverge before the CTA-wide barrier
     __syncwarp();
@@ -621,29 +639,14 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
   }
 
   // ------------------------------------------------------ sums and output
-  const int q4 = warp & 3, dim = q4 * 32 + lane, row0 = ((warp - 2) >> 2) * RW, tid = (warp - 2) * 32 + lane;
+  const int q4 = warp & 3, dim = q4 * 32 + lane, row0 = ((warp - 2) >> 2) * RW;
   const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
   const bool soft = warp >= 2;
   const long long slot = (long long)item * p.splits + split;
   float l = 0.0f;                                         // of row tid
   if (soft && nt > 0) {
     tc_fence_after();
-    // sum RW columns over the warp: lane c (modulo RW) ends with column c
-#pragma unroll
-    for (int s = RW / 2; s >= 1; s >>= 1) {
-      const bool upper = (lane & s) != 0;
-#pragma unroll
-      for (int i = 0; i < s; ++i) {
-        const float send = upper ? l_sum[i] : l_sum[i + s];
-        const float keep = upper ? l_sum[i + s] : l_sum[i];
-        l_sum[i] = keep + __shfl_xor_sync(0xffffffffu, send, s);
-      }
-    }
-#pragma unroll
-    for (int s = RW; s < 32; s <<= 1) l_sum[0] += __shfl_xor_sync(0xffffffffu, l_sum[0], s);
-    if (lane < RW) s_wmax[q4 * N + row0 + lane] = l_sum[0];
-    named_bar_sync(2, C::SOFT);
-    if (tid < N) l = (s_wmax[tid] + s_wmax[N + tid]) + (s_wmax[2 * N + tid] + s_wmax[3 * N + tid]);
+    if (tid < N) l = (s_ls[tid] + s_ls[N + tid]) + (s_ls[2 * N + tid] + s_ls[3 * N + tid]);
   }
   // per row: the factors of O (2^d in two steps: it alone may leave the range that the
   // result is in), and where the row goes
@@ -662,7 +665,6 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
       }
     cluster_sync();   // and every CTA's MMAs and copies are done: the rings are free
   }
-  if (soft) named_bar_sync(2, C::SOFT);                   // s_wmax is read
   if (soft && tid < N) {
     uint32_t j;
     const uint32_t i = p.by_group.divmod((uint32_t)(rt * N + tid), j);
@@ -692,12 +694,11 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
     named_bar_sync(2, C::SOFT);
     // (rolled: code that runs once a CTA costs its instruction fetches)
 #pragma unroll 1
-    for (int n = row0; n < row0 + RW && nt > 0; n += 4) {
-      float a[4], c[4];
-      tmem_ld4(trow + C::O_COL + n, a);
-      tmem_ld4(trow + C::O_COL + N + n, c);
+    for (int n = row0; n < row0 + RW && nt > 0; n += 8) {
+      float a[8], c[8];
+      tmem_ld8x2(trow + C::O_COL + n, trow + C::O_COL + N + n, a, c);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 8; ++j) {
         const int r = n + j;
         if (dim < HD && r < n_rows) {
           const float2 f = s_f[r];

@@ -121,12 +121,12 @@ __global__ void __launch_bounds__(AttnTilesCfg<HD, SUBS>::THREADS, AttnTilesCfg<
   int* err = g_attn_kv8_err;
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int split = (int)(blockIdx.x % (unsigned)p.splits);
-  const int item = (int)(blockIdx.x / (unsigned)p.splits);
+  uint32_t split_u, plane_u, g_u;
+  const int item = (int)p.by_splits.divmod(blockIdx.x, split_u);
   // the last row tiles first: under a causal mask they see the most keys
-  const int planes = p.c.b * p.c.H_kv;
-  const int rt = p.row_tiles - 1 - item / planes, plane = item % planes;
-  const int seq = plane / p.c.H_kv, g = plane % p.c.H_kv;
+  const int rt = p.row_tiles - 1 - (int)p.by_tiles.divmod((uint32_t)item, plane_u);
+  const int seq = (int)p.by_heads.divmod(plane_u, g_u);
+  const int split = (int)split_u, plane = (int)plane_u, g = (int)g_u;
   const int n_rows = min(N, p.rows - rt * N);
   const int subs = SUBS == 1 ? 1 : (n_rows + 127) / 128;   // the last row tile may lack its second half
 
@@ -180,8 +180,8 @@ __global__ void __launch_bounds__(AttnTilesCfg<HD, SUBS>::THREADS, AttnTilesCfg<
   for (int k = 0; k < N / 32; ++k) lim_max = max(lim_max, s_lim[lane + 32 * k]);
   lim_max = __reduce_max_sync(0xffffffffu, lim_max);
   const int tiles = (lim_max + KT - 1) / KT;
-  const int t0 = (int)((long long)tiles * split / p.splits), t1 = (int)((long long)tiles * (split + 1) / p.splits);
-  const int nt = t1 - t0;
+  const int t0 = (int)p.by_splits.div((uint32_t)(tiles * split));
+  const int nt = (int)p.by_splits.div((uint32_t)(tiles * (split + 1))) - t0;
 
   auto wait = [&](uint64_t* bar, int phase) {           // decided warp-wide: tensor-memory accesses are collective
     return __all_sync(0xffffffffu, mbar_wait_long(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
