@@ -692,26 +692,27 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
   }
   if (soft) {
     named_bar_sync(2, C::SOFT);
-    // (rolled: code that runs once a CTA costs its instruction fetches)
+    // (rolled: code that runs once a CTA costs its instruction fetches; the kinds of output apart, or
+    // every row's store would branch)
+    auto put = [&](auto store) {
 #pragma unroll 1
-    for (int n = row0; n < row0 + RW && nt > 0; n += 8) {
-      float a[8], c[8];
-      tmem_ld8x2(trow + C::O_COL + n, trow + C::O_COL + N + n, a, c);
+      for (int n = row0; n < row0 + RW && nt > 0; n += 8) {
+        float a[8], c[8];
+        tmem_ld8x2(trow + C::O_COL + n, trow + C::O_COL + N + n, a, c);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int r = n + j;
-        if (dim < HD && r < n_rows) {
-          const float2 f = s_f[r];
+        for (int j = 0; j < 8; ++j) {
+          const float2 f = s_f[n + j];
           const float v = f.x == 0.0f ? 0.0f : (a[j] + c[j]) * f.x * f.y;
-          if (p.cluster)
-            cluster_store(s_dst[r] + 4u * (uint32_t)dim, v);
-          else if (p.splits > 1)
-            p.ws_o[s_to[r] + dim] = v;
-          else
-            p.out[s_to[r] + dim] = f32_to_bf16_bits(v);
+          if (dim < HD && n + j < n_rows) store(n + j, v);
         }
       }
-    }
+    };
+    if (p.cluster)
+      put([&](int r, float v) { cluster_store(s_dst[r] + 4u * (uint32_t)dim, v); });
+    else if (p.splits > 1)
+      put([&](int r, float v) { p.ws_o[s_to[r] + dim] = v; });
+    else
+      put([&](int r, float v) { p.out[s_to[r] + dim] = f32_to_bf16_bits(v); });
     if (nt == 0 && p.splits == 1 && dim < HD)             // no row of the item sees a key
       for (int r = row0; r < min(row0 + RW, n_rows); ++r) p.out[s_to[r] + dim] = 0;
   }
