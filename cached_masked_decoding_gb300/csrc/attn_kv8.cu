@@ -27,7 +27,9 @@ struct AttnKv8Plan {
 };
 
 // Rows of one cached head (R rows of H / H_kv heads) in tiles of N, the keys in
-// splits.  A CTA's time is taken as the tiles of keys that it walks; the join of up
+// splits.  256 rows in place of 128 once they are more (192 rows of 64 items, 4096 keys: 54
+// us against 66; 8192 causal rows of 8 items, 2048 keys: 50 against 64).  A CTA's time
+// is taken as the tiles of keys that it walks; the join of up
 // to 8 splits in a cluster as one tile's, that of more (or of 128 rows and up) through the
 // workspace as four of 128 keys.  A round of CTAs is two an SM, one with 64 or 256 rows.
 AttnKv8Plan plan_attn_kv8(long long b, long long H_kv, long long rows, int hd, int T) {
@@ -110,8 +112,8 @@ extern "C" dllm_status dllm_op_attention_kv8(const uint16_t* q, int64_t q_row_st
   if (!q || !out || H < 1 || H % cache->H_kv || R < 1 || !(scale > 0.0f) || !(scale <= 1e30f) ||
       !op_aligned(q, 16) || !op_aligned(out, 16) || !op_aligned(limits, 4))
     return op_fail(DLLM_EINVAL,
-                   "bad attention_kv8 arguments: H=%d (a multiple of H_kv=%d) R=%d scale=%g (over 0, to 1e30), q and out 16-byte "
-                   "aligned",
+                   "bad attention_kv8 arguments: H=%d (a multiple of H_kv=%d) R=%d scale=%g (over 0, to 1e30), "
+                   "q and out 16-byte aligned",
                    H, cache->H_kv, R, scale);
   const long long width = (long long)H * cache->hd;
   AttnKv8Params p = {};

@@ -28,8 +28,11 @@
 // scores, and others that follow the products (score plus value exponent).  Sums l
 // are kept per key lane and joined once at the end.  This is the longest of the
 // overlapped stages, so the rows of a tile are shared out over N / RW groups of
-// four warps: with one group of N rows a thread a tile of 128 keys took 1.8 us
-// (N = 16) to 2.8 us (N = 32), of which HBM needs 0.8 us.
+// four warps (one group of N rows a thread: 1.8 us a tile of 128 keys for N = 16, 2.8 us for
+// N = 32).  Now two CTAs of an SM take 1.5 us a tile each for N = 32, about HBM's rate, one
+// alone 1.1 us; what a batch loses is starts, ends and the last CTAs alone.  hd 128: one token of 32 sequences,
+// 4096 keys, 32 heads on 8: 38 us, 5.5 TB/s; of 8 sequences, 8193 keys: 25 us, 4.3 TB/s;
+// 32 rows of 16 sequences of 32 heads, up to 2048 keys: 53 us, 4.0 TB/s.
 //
 //   warp 0     TMA: K and V tiles through a ring of 128-key slots
 //   warp 1     scale copies and MMAs, issued by one lane
@@ -415,7 +418,8 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
         const bool bad = kb == kScaleNan || vb == kScaleNan;
         const float kf = bad ? __uint_as_float(0x7fffffffu) : scale_value(kb) * p.scale_log2;
         const int ev = bad || !seen ? -1000 : vb - 127;   // -1000: no value scale to refer to
-        ok = __all_sync(0xffffffffu, mbar_wait_long(&sfull[b], (uint32_t)(T >> 1) & 1u, abort_flag, err, ERR_ATTN_FULL)) &&
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait_long(&sfull[b], (uint32_t)(T >> 1) & 1u, abort_flag, err, ERR_ATTN_FULL)) &&
              ok;
         tc_fence_after();
         // scores in base 2, relative to their row's reference
@@ -594,7 +598,8 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
           // the last tile runs past every row's limit: whatever bytes lie there
           // (codes of NaN among them) must not meet the zero probabilities
           const int u = 2 * T + 1, slot = u % C::SLOTS;
-          ok = __all_sync(0xffffffffu, mbar_wait_long(&full[slot], (uint32_t)(u / C::SLOTS) & 1u, abort_flag, err, ERR_ATTN_FULL)) &&
+          ok = __all_sync(0xffffffffu, mbar_wait_long(&full[slot], (uint32_t)(u / C::SLOTS) & 1u, abort_flag, err,
+                                                      ERR_ATTN_FULL)) &&
                ok;
           if (!seen) {
 #pragma unroll

@@ -20,12 +20,12 @@
 // when the first's are used up; P takes the place of its scores; O is 128 more.
 // 128 rows are for CTAs that would be half empty, two an SM.
 //
-// 4096 causal rows of 32 heads on 8, hd 128 (137 GFLOP): 156 us, 0.88 PFLOP/s, 46 % of the
-// measured bf16 rate; hd 64: 117 us.  A tile of 256 rows takes 2070 cycles of which the products
+// 4096 causal rows of 32 heads on 8, hd 128 (137 GFLOP): 153 us, 0.90 PFLOP/s, 47 % of the
+// measured bf16 rate; hd 64: 116 us.  A tile of 256 rows takes 2070 cycles of which the products
 // need 1024: shared memory's port is taken by operands (1024 cycles), the walk of scores and
 // probabilities through registers (about 770), V's conversion (190) and the key factors
 // (256), and what waits for it waits longer.  Tried: 128 keys a tile with one tile's scores
-// only, 186 us; 128 rows a CTA throughout, 187; halves in place of bf16 with references that
+// only, 186 us; 128 rows a CTA throughout, 193; halves in place of bf16 with references that
 // follow the scores, 190; e4m3 for P as well, 259.  A CTA's start and end, 19,000 cycles (the
 // query tile's conversion 5,000), are the next largest part: nothing else runs on the SM.
 //

@@ -103,7 +103,8 @@ struct Gemm8Cfg {
 // memory and the block-scaled tcgen05.mma applies them, so blocks accumulate
 // in one float32 accumulator.  A CTA computes a share of one tile's K; the
 // `split` CTAs of a cluster share a tile and join their partial tiles through
-// distributed shared memory in rank order.
+// distributed shared memory in rank order.  Bound by HBM: 24576 x 4096 weights, 32 rows, 20 us
+// with the quantiser's launch, 5.3 TB/s; 4096 x 4096, one row, 6.3 us.
 //   warp 0     TMA: weight and activation codes
 //   warp 1     scale copies and MMAs, issued by one lane
 //   warps 2-5  epilogue
@@ -335,7 +336,9 @@ __global__ void __launch_bounds__(224, 2)
 // for 128 bytes a cycle and SM (measured: about 50 were delivered, 38% of the rate).  Here a
 // pair of CTAs (a cluster) takes 256 x 192 outputs, its activation rows fetched
 // once and multicast to both, 75 bytes a cycle; and a CTA is persistent, one an SM, with two
-// accumulators, so that storing one tile overlaps the next one's products.
+// accumulators, so that storing one tile overlaps the next one's products.  12288 x 4096
+// weights, 2048 rows: 79 us with the quantiser, 2.6 PFLOP/s; a block of K takes 640 cycles, in which an SM takes in
+// its 40 KB of operands, for 384 cycles of products.
 //   warp 0     TMA: weight codes, and half the activation codes for both CTAs
 //   warp 1     scale copies and MMAs, issued by one lane
 //   warps 2-5  epilogue
@@ -638,7 +641,8 @@ extern "C" dllm_status dllm_op_gemm8(const uint8_t* W, const uint8_t* W_scale, c
                                      const uint8_t* X_scale, void* Y, int32_t y_dtype, int32_t M, int32_t N, int32_t K,
                                      void* stream) {
   if (!W || !W_scale || !X || !X_scale || !Y || (y_dtype != DLLM_F32 && y_dtype != DLLM_BF16) || M < 1 || N < 1 ||
-      M > kMostRows || N > kMostRows || K < 16 || K % 16 || !op_aligned(W, 16) || !op_aligned(X, 16) || !op_aligned(Y, 16))
+      M > kMostRows || N > kMostRows || K < 16 || K % 16 || !op_aligned(W, 16) || !op_aligned(X, 16) ||
+      !op_aligned(Y, 16))
     return op_fail(DLLM_EINVAL,
                    "bad gemm8 arguments: M=%d N=%d K=%d (K %% 16 == 0) y_dtype=%d (float32 or bf16), W, X and Y "
                    "16-byte aligned",
