@@ -30,9 +30,10 @@
 // overlapped stages, so the rows of a tile are shared out over N / RW groups of
 // four warps (one group of N rows a thread: 1.8 us a tile of 128 keys for N = 16, 2.8 us for
 // N = 32).  Now two CTAs of an SM take 1.5 us a tile each for N = 32, about HBM's rate, one
-// alone 1.1 us; what a batch loses is starts, ends and the last CTAs alone.  hd 128: one token of 32 sequences,
-// 4096 keys, 32 heads on 8: 38 us, 5.5 TB/s; of 8 sequences, 8193 keys: 25 us, 4.3 TB/s;
-// 32 rows of 16 sequences of 32 heads, up to 2048 keys: 53 us, 4.0 TB/s.
+// alone 1.1 us; what a batch loses is starts, ends and the last CTAs alone.  hd 128: one
+// token of 32 sequences, 4096 keys, 32 heads on 8: 37 us, 5.5 TB/s; of 8 sequences, up to
+// 8193 keys: 24 us, 4.4 TB/s; 32 rows of 16 sequences of 32 heads, up to 2048 keys: 52 us,
+// 4.1 TB/s; 32 rows of one sequence, 768 keys: 9.7 us.
 //
 //   warp 0     TMA: K and V tiles through a ring of 128-key slots
 //   warp 1     scale copies and MMAs, issued by one lane
@@ -83,8 +84,8 @@ struct AttnRowsCfg {
   static constexpr int P_BYTES = KT * P_ROW;
   static constexpr int SLOTS = CTAS == 1 ? (HD == 64 ? 16 : 9) : HD == 64 ? 8 : N == 8 ? 6 : 5;
   static constexpr int SF_BYTES = 512;                  // ones, query scales, two buffers of probability scales
-  // warp maxima (two), m, d, limits, scales, (m, l) of 8 splits, warps' sums
-  static constexpr int STAT_FLOATS = 8 * N + 3 * N + 4 * N + 16 * N + 4 * N;
+  // warp maxima (two), m, d, limits, scales, (m, l) of 8 splits, warps' sums, places (64 and 32 bits)
+  static constexpr int STAT_FLOATS = 8 * N + 3 * N + 4 * N + 16 * N + 4 * N + 3 * N;
   static constexpr int SMEM_BYTES = 1024 + SLOTS * SLOT + Q_PARTS * Q_BYTES + 2 * P_BYTES + 4 * SF_BYTES +
                                     STAT_FLOATS * 4 + (2 * SLOTS + 10) * 8 + 24;
   static constexpr int S_COL = 0;                       // two buffers
@@ -192,7 +193,10 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
   float* s_cm = s_inv + 4 * N;                          // [8][N] reference maxima of the cluster's splits
   float* s_cl = s_cm + 8 * N;                           // [8][N] and sums
   float* s_ls = s_cl + 8 * N;                           // [4][N] the warps' sums
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_ls + 4 * N);
+  long long* s_to = reinterpret_cast<long long*>(s_ls + 4 * N);   // [N] where a row goes
+  uint32_t* s_dst = reinterpret_cast<uint32_t*>(s_to + N);        // [N] its place in the cluster
+  float* s_part = reinterpret_cast<float*>(sKV);        // [split][own][HD] rows that the cluster joins here
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_dst + N);
   uint64_t* empty = full + C::SLOTS;
   uint64_t* qready = empty + C::SLOTS;
   uint64_t* sfull = qready + 1;                         // [2]
@@ -238,6 +242,8 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
   }
   griddep_launch_dependents();
   griddep_wait();
+  // rows of a split in a cluster: split, split + splits, ...
+  const int own = (int)p.by_splits.div((uint32_t)(N + p.splits - 1));
   // the softmax warps ask for the query tile at once
   const int tid = (warp - 2) * 32 + lane;
   AttnQueryTile<HD, N, C::SOFT> query;
@@ -247,7 +253,19 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
 #pragma unroll
       for (int f = 0; f < 4; ++f) reinterpret_cast<uint32_t*>(sSF + f * C::SF_BYTES)[tid] = 0x7f7f7f7fu;
     }
-    if (tid < N) s_m[tid] = 0.0f;
+    if (tid < N) {
+      s_m[tid] = 0.0f;
+      uint32_t j;
+      const uint32_t i = p.by_group.divmod((uint32_t)(rt * N + tid), j);
+      s_to[tid] = p.splits > 1 && !p.cluster
+                      ? (((long long)item * p.splits + split) * N + tid) * HD
+                      : ((long long)seq * p.R + i) * p.o_rs + (long long)(g * p.group + (int)j) * HD;
+      if (p.cluster) {
+        uint32_t rank;
+        const uint32_t at = p.by_splits.divmod((uint32_t)tid, rank);
+        s_dst[tid] = cluster_addr(smem_u32(s_part + (split * own + (int)at) * HD), rank);
+      }
+    }
   }
   // limits of the tile's rows; rows past the last see what row 0 sees and are not stored
   if (threadIdx.x < N) {
@@ -647,50 +665,41 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
   const int q4 = warp & 3, dim = q4 * 32 + lane, row0 = ((warp - 2) >> 2) * RW;
   const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
   const bool soft = warp >= 2;
-  const long long slot = (long long)item * p.splits + split;
-  float l = 0.0f;                                         // of row tid
-  if (soft && nt > 0) {
-    tc_fence_after();
-    if (tid < N) l = (s_ls[tid] + s_ls[N + tid]) + (s_ls[2 * N + tid] + s_ls[3 * N + tid]);
-  }
-  // per row: the factors of O (2^d in two steps: it alone may leave the range that the
-  // result is in), and where the row goes
+  tc_fence_after();
+  auto sum_of = [&](int n) { return (s_ls[n] + s_ls[N + n]) + (s_ls[2 * N + n] + s_ls[3 * N + n]); };   // 0 if nt is
+  // per row the factors of O (2^d in two steps: it alone may leave the range that the result is in)
   float2* s_f = reinterpret_cast<float2*>(s_nmax);        // [N]
-  long long* s_to = reinterpret_cast<long long*>(s_nmax + 2 * N);   // [N]
-  uint32_t* s_dst = reinterpret_cast<uint32_t*>(s_wmax);  // [N] its place in the cluster
-  const int own = (N + p.splits - 1) / p.splits;          // rows of a split in a cluster: split, split + splits, ...
-  float* s_part = reinterpret_cast<float*>(sKV);          // [split][own][HD]
   if (p.cluster) {
     // every split learns the others' (m, l) of its rows
     cluster_wait();
-    if (soft && tid < N)
-      for (int r = 0; r < p.splits; ++r) {
-        cluster_store(cluster_addr(smem_u32(s_cm + split * N + tid), (uint32_t)r), nt > 0 ? s_m[tid] : 0.0f);
-        cluster_store(cluster_addr(smem_u32(s_cl + split * N + tid), (uint32_t)r), l);
+    if (soft)
+      for (int e = tid; e < N * p.splits; e += C::SOFT) {
+        const int n = e % N;
+        const uint32_t r = (uint32_t)(e / N);
+        cluster_store(cluster_addr(smem_u32(s_cm + split * N + n), r), s_m[n]);
+        cluster_store(cluster_addr(smem_u32(s_cl + split * N + n), r), sum_of(n));
       }
     cluster_sync();   // and every CTA's MMAs and copies are done: the rings are free
   }
   if (soft && tid < N) {
-    uint32_t j;
-    const uint32_t i = p.by_group.divmod((uint32_t)(rt * N + tid), j);
-    s_to[tid] = ((long long)seq * p.R + i) * p.o_rs + (long long)(g * p.group + (int)j) * HD;
-    float w = l == 0.0f ? 0.0f : 1.0f / l;
+    const float l = sum_of(tid);
+    float w = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
     if (p.cluster) {
-      float M = -INFINITY, sum = 0.0f;
-      for (int r = 0; r < p.splits; ++r) {
-        const float mr = s_cm[r * N + tid];
-        if (s_cl[r * N + tid] != 0.0f) M = mr > M || mr != mr ? mr : M;   // a NaN stays
+      float mr[8], lr[8], M = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        lr[r] = r < p.splits ? s_cl[r * N + tid] : 0.0f;
+        mr[r] = r < p.splits ? s_cm[r * N + tid] : 0.0f;
       }
-      for (int r = 0; r < p.splits; ++r) {
-        const float lr = s_cl[r * N + tid];
-        if (lr != 0.0f) sum += lr * exp2f(s_cm[r * N + tid] - M);
-      }
-      w = l == 0.0f ? 0.0f : exp2f(s_m[tid] - M) / sum;
-      s_dst[tid] = cluster_addr(smem_u32(s_part + (split * own + tid / p.splits) * HD), (uint32_t)(tid % p.splits));
-    } else if (p.splits > 1) {
-      s_to[tid] = (slot * N + tid) * HD;
-      if (tid < n_rows)
-        *reinterpret_cast<float2*>(p.ws_ml + (slot * N + tid) * 2) = make_float2(nt > 0 ? s_m[tid] : 0.0f, l);
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (lr[r] != 0.0f) M = mr[r] > M || mr[r] != mr[r] ? mr[r] : M;   // a NaN stays
+#pragma unroll
+      for (int r = 0; r < 8; ++r) sum += lr[r] != 0.0f ? lr[r] * ex2(mr[r] - M) : 0.0f;
+      w = l == 0.0f ? 0.0f : __fdividef(ex2(s_m[tid] - M), sum);
+    } else if (p.splits > 1 && tid < n_rows) {
+      const long long slot = (long long)item * p.splits + split;
+      *reinterpret_cast<float2*>(p.ws_ml + (slot * N + tid) * 2) = make_float2(s_m[tid], l);
     }
     const float vs = nt > 0 ? exp2f(0.5f * s_d[tid]) : 0.0f;
     s_f[tid] = w == 0.0f ? make_float2(0.0f, 0.0f) : make_float2(vs * w, vs);
@@ -701,9 +710,9 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
     // every row's store would branch)
     auto put = [&](auto store) {
 #pragma unroll 1
-      for (int n = row0; n < row0 + RW && nt > 0; n += 8) {
-        float a[8], c[8];
-        tmem_ld8x2(trow + C::O_COL + n, trow + C::O_COL + N + n, a, c);
+      for (int n = row0; n < row0 + RW; n += 8) {
+        float a[8] = {}, c[8] = {};
+        if (nt > 0) tmem_ld8x2(trow + C::O_COL + n, trow + C::O_COL + N + n, a, c);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float2 f = s_f[n + j];
@@ -712,25 +721,32 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
         }
       }
     };
-    if (p.cluster)
+    if (p.cluster)                                        // zeros from a split that saw no key
       put([&](int r, float v) { cluster_store(s_dst[r] + 4u * (uint32_t)dim, v); });
     else if (p.splits > 1)
       put([&](int r, float v) { p.ws_o[s_to[r] + dim] = v; });
     else
       put([&](int r, float v) { p.out[s_to[r] + dim] = f32_to_bf16_bits(v); });
-    if (nt == 0 && p.splits == 1 && dim < HD)             // no row of the item sees a key
-      for (int r = row0; r < min(row0 + RW, n_rows); ++r) p.out[s_to[r] + dim] = 0;
   }
   if (p.cluster) {
     cluster_sync();
     if (soft)
-      for (int e = tid; e < own * HD; e += C::SOFT) {
-        const int i = e / HD, r = split + i * p.splits, d = e % HD;
+      for (int e = tid; e < own * (HD / 4); e += C::SOFT) {
+        const int i = e / (HD / 4), r = split + i * p.splits, d = e % (HD / 4) * 4;
         if (r >= n_rows) continue;
-        float v = 0.0f;
-        for (int k = 0; k < p.splits; ++k)
-          if (s_cl[k * N + r] != 0.0f) v += s_part[(k * own + i) * HD + d];   // a split that saw none sent nothing
-        p.out[s_to[r] + d] = f32_to_bf16_bits(v);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k < p.splits) {
+            const float4 o = *reinterpret_cast<const float4*>(s_part + (k * own + i) * HD + d);
+            v.x += o.x;
+            v.y += o.y;
+            v.z += o.z;
+            v.w += o.w;
+          }
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), c = __floats2bfloat162_rn(v.z, v.w);
+        *reinterpret_cast<uint2*>(p.out + s_to[r] + d) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
       }
   }
   __syncwarp();
