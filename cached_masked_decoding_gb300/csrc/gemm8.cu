@@ -268,13 +268,6 @@ __global__ void __launch_bounds__(224, 2)
   const int q = warp & 3, l128 = q * 32 + lane, m = m0 + l128;
   const bool epi = warp >= 2 && warp < 6;
   const int cols = min(BN, p.N - n0);
-  auto put = [&](int n, float v) {
-    const long long o = (long long)(n0 + n) * p.M + m;
-    if (p.out_bf16)
-      static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(v);
-    else
-      static_cast<float*>(p.y)[o] = v;
-  };
   if (epi) {
     const bool ok = __all_sync(0xffffffffu, mbar_wait_long(done, 0u, abort_flag, err, ERR_GEMM_TFULL));
     (void)ok;   // after a wait that gave up the outputs are invalid and reported as such
@@ -286,9 +279,18 @@ __global__ void __launch_bounds__(224, 2)
         float v[32];
         tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + n, v);
         if (m < p.M) {
+          long long o = (long long)(n0 + n) * p.M + m;
+          if (p.out_bf16) {
+            __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y);
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (n + j < cols) put(n + j, v[j]);
+            for (int j = 0; j < 32; ++j, o += p.M)
+              if (n + j < cols) y[o] = __float2bfloat16_rn(v[j]);
+          } else {
+            float* y = static_cast<float*>(p.y);
+#pragma unroll
+            for (int j = 0; j < 32; ++j, o += p.M)
+              if (n + j < cols) y[o] = v[j];
+          }
         }
       }
     }
@@ -317,8 +319,14 @@ __global__ void __launch_bounds__(224, 2)
 #pragma unroll 1
       for (int i = 0; (i << sl) + rank < cols; ++i) {
         float v = 0.0f;
-        for (int s = 0; s < split; ++s) v += part[(s * own + i) * 128 + l128];
-        put((i << sl) + rank, v);
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          if (s < split) v += part[(s * own + i) * 128 + l128];
+        const long long o = (long long)(n0 + (i << sl) + rank) * p.M + m;
+        if (p.out_bf16)
+          static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(v);
+        else
+          static_cast<float*>(p.y)[o] = v;
       }
     }
   }
