@@ -758,7 +758,9 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
   }
 }
 
-// Join the splits of every row: weights l_s 2^(m_s - M) over their sum.  A warp a row.
+// Join the splits of every row (64 at most): weights l_s 2^(m_s - M) over their sum.  A warp
+// a row, a lane two splits' weights: they are whole before the first output meets one, since
+// a sum times an output may leave float32's range where the row does not.
 template <int HD>
 __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const __grid_constant__ AttnKv8Params p, int N) {
   const int lane = threadIdx.x & 31;
@@ -772,19 +774,37 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const __grid_constan
   const long long item = ((long long)seq * p.c.H_kv + h / p.group) * p.row_tiles + rn / N;
   const long long first = item * p.splits * N + rn % N;   // then N apart
   constexpr int D = HD / 32;
-  // Eight splits' loads at once (a dependent one each was a round trip of L2 each);
-  // a running maximum joins the eights.
-  float M = -INFINITY, sum = 0.0f, o[D] = {};
+  float2 ml[2];
+  float M = -INFINITY;
+  bool nan = false;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int s = lane + 32 * e;
+    ml[e] = s < p.splits ? *reinterpret_cast<const float2*>(p.ws_ml + (first + (long long)s * N) * 2)
+                         : make_float2(-INFINITY, 0.0f);
+    if (ml[e].y != 0.0f) {                                // 0: the split saw none of the row's keys
+      M = fmaxf(M, ml[e].x);
+      nan = nan || ml[e].x != ml[e].x;
+    }
+  }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  if (__any_sync(0xffffffffu, nan)) M = __uint_as_float(0x7fffffffu);
+  float w[2], sum;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) w[e] = ml[e].y == 0.0f ? 0.0f : ml[e].y * exp2f(ml[e].x - M);
+  sum = w[0] + w[1];
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) w[e] = w[e] == 0.0f ? 0.0f : w[e] / sum;
+  float o[D] = {};
+  // eight splits' loads at once (a dependent one each was a round trip of L2 each)
   for (int s0 = 0; s0 < p.splits; s0 += 8) {
-    float2 ml[8];
     float v[8][D];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const bool in = s0 + k < p.splits;
-      const long long at = first + (long long)(in ? s0 + k : 0) * N;
-      ml[k] = *reinterpret_cast<const float2*>(p.ws_ml + at * 2);
-      if (!in) ml[k].y = 0.0f;
-      const float* src = p.ws_o + at * HD + lane * D;
+      const float* src = p.ws_o + (first + (long long)min(s0 + k, p.splits - 1) * N) * HD + lane * D;
       if constexpr (D == 4) {
         const float4 f = *reinterpret_cast<const float4*>(src);
         v[k][0] = f.x;
@@ -797,36 +817,25 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const __grid_constan
         v[k][1] = f.y;
       }
     }
-    float Mn = M;
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (ml[k].y != 0.0f) Mn = ml[k].x > Mn || ml[k].x != ml[k].x ? ml[k].x : Mn;   // a NaN stays
-    const float c = M == -INFINITY ? 0.0f : exp2f(M - Mn);
-    sum *= c;
-#pragma unroll
-    for (int d = 0; d < D; ++d) o[d] *= c;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      if (ml[k].y == 0.0f) continue;                       // a split that saw none of the row's keys
-      const float w = ml[k].y * exp2f(ml[k].x - Mn);
-      sum += w;
+      const float wk = __shfl_sync(0xffffffffu, s0 < 32 ? w[0] : w[1], (s0 + k) & 31);   // 0 past the last split
+      if (wk == 0.0f) continue;
 #pragma unroll
-      for (int d = 0; d < D; ++d) o[d] += w * v[k][d];
+      for (int d = 0; d < D; ++d) o[d] += wk * v[k][d];
     }
-    M = Mn;
   }
-  const float il = sum == 0.0f ? 0.0f : 1.0f / sum;
-  uint32_t w[D / 2];
+  uint32_t word[D / 2];
 #pragma unroll
   for (int d = 0; d < D; d += 2) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(o[d] * il, o[d + 1] * il);
-    w[d / 2] = *reinterpret_cast<const uint32_t*>(&b);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(o[d], o[d + 1]);
+    word[d / 2] = *reinterpret_cast<const uint32_t*>(&b);
   }
   uint16_t* out = p.out + row * p.o_rs + (long long)h * HD + lane * D;
   if constexpr (D == 4)
-    *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(out) = make_uint2(word[0], word[1]);
   else
-    *reinterpret_cast<uint32_t*>(out) = w[0];
+    *reinterpret_cast<uint32_t*>(out) = word[0];
 }
 
 }  // namespace dllm

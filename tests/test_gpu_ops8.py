@@ -417,6 +417,22 @@ def test_attention_values_that_grow_or_vanish(torch, hd, R, H, h):
         _attention_check(got, f64(q), ca, None, hd ** -0.5, lost=2.0 ** (max(lo, hi) - 127 - 100))
 
 
+@pytest.mark.parametrize("R,H,h,T,loud", [(200, 20, 5, 700, 1.0), (257, 12, 3, 1025, 1.0), (1, 2, 2, 16384, 8.0),
+                                          (16, 1, 1, 16384, 8.0)])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attention_splits_of_large_values_and_sums(torch, hd, R, H, h, T, loud):
+    """Values up to 2^111 and scores far above the first keys' in every split: a split's sum times
+    its output is out of float32's range, the joined row is not."""
+    rng = np.random.default_rng(16)
+    q, ca, _ = _attention_case(torch, rng, 1, R, H, h, T, hd, None, loud=loud)
+    assert binding.attention_kv8_workspace(1, H, h, hd, R, T) > 0
+    ca.scales[1].copy_(dev(torch, rng.integers(20, 231, (1, h, T)).astype(np.uint8)))
+    got = f64(_attend(torch, q, ca, None, H, R, scale=0.3))
+    # the sums are float32 in units of the largest value scale: T * 448 * 2^-126 of it < 2^-100 underflows; in the
+    # few-row kernel a probability is off by 2^-21 of the largest p 2^ev near it, times a code
+    _attention_check(got, f64(q), ca, None, 0.3, lost=2.0 ** 3 + (2.0 ** -21 * 2.0 ** 103 * 448 if R * H // h <= 64 else 0))
+
+
 @pytest.mark.parametrize("b,R,h,hd", [(4, 100, 80, 64), (2, 200, 80, 128)])
 def test_attention_many_heads_leave_the_keys_whole(torch, b, R, h, hd):
     """So many rows that one walk has all keys of a head: once, and (scores and value
