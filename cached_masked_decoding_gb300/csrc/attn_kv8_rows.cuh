@@ -774,6 +774,27 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const __grid_constan
   const long long item = ((long long)seq * p.c.H_kv + h / p.group) * p.row_tiles + rn / N;
   const long long first = item * p.splits * N + rn % N;   // then N apart
   constexpr int D = HD / 32;
+  // eight splits' outputs at once (a dependent load each was a round trip of L2 each), the first
+  // eight beside the weights
+  float v[8][D];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float* src = p.ws_o + (first + (long long)min(s0 + k, p.splits - 1) * N) * HD + lane * D;
+      if constexpr (D == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(src);
+        v[k][0] = f.x;
+        v[k][1] = f.y;
+        v[k][2] = f.z;
+        v[k][3] = f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(src);
+        v[k][0] = f.x;
+        v[k][1] = f.y;
+      }
+    }
+  };
+  load(0);
   float2 ml[2];
   float M = -INFINITY;
   bool nan = false;
@@ -799,24 +820,7 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const __grid_constan
 #pragma unroll
   for (int e = 0; e < 2; ++e) w[e] = w[e] == 0.0f ? 0.0f : w[e] / sum;
   float o[D] = {};
-  // eight splits' loads at once (a dependent one each was a round trip of L2 each)
   for (int s0 = 0; s0 < p.splits; s0 += 8) {
-    float v[8][D];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float* src = p.ws_o + (first + (long long)min(s0 + k, p.splits - 1) * N) * HD + lane * D;
-      if constexpr (D == 4) {
-        const float4 f = *reinterpret_cast<const float4*>(src);
-        v[k][0] = f.x;
-        v[k][1] = f.y;
-        v[k][2] = f.z;
-        v[k][3] = f.w;
-      } else {
-        const float2 f = *reinterpret_cast<const float2*>(src);
-        v[k][0] = f.x;
-        v[k][1] = f.y;
-      }
-    }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float wk = __shfl_sync(0xffffffffu, s0 < 32 ? w[0] : w[1], (s0 + k) & 31);   // 0 past the last split
@@ -824,6 +828,7 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const __grid_constan
 #pragma unroll
       for (int d = 0; d < D; ++d) o[d] += wk * v[k][d];
     }
+    if (s0 + 8 < p.splits) load(s0 + 8);
   }
   uint32_t word[D / 2];
 #pragma unroll

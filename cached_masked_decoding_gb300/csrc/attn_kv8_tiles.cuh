@@ -1,5 +1,5 @@
 // Attention over the 8-bit cache for many query rows a cached head (a prefill
-// over its own cache, a block of grouped heads): SUBS times 128 rows a CTA, a row in two
+// over its own cache, a block of grouped heads): SUBS times 128 rows a CTA, a row in HF
 // softmax threads.
 //
 //   S[row][key] = Q K^T      kind::f8f6f4 on the cache's codes; q as hi + lo codes (two
@@ -20,20 +20,20 @@
 // when the first's are used up; P takes the place of its scores; O is 128 more.
 // 128 rows are for CTAs that would be half empty, two an SM.
 //
-// 4096 causal rows of 32 heads on 8, hd 128 (137 GFLOP): 153 us, 0.90 PFLOP/s, 47 % of the
-// measured bf16 rate; hd 64: 116 us.  A tile of 256 rows takes 2070 cycles of which the products
-// need 1024: shared memory's port is taken by operands (1024 cycles), the walk of scores and
+// 4096 causal rows of 32 heads on 8, hd 128 (137 GFLOP): 146 us, 0.94 PFLOP/s, 49 % of the
+// measured bf16 rate; hd 64: 114 us.  With HF 2 a tile of 256 rows took 2070 cycles, of which the
+// products need 1024: shared memory's port is taken by operands (1024 cycles), the walk of scores and
 // probabilities through registers (about 770), V's conversion (190) and the key factors
 // (256), and what waits for it waits longer.  Tried: 128 keys a tile with one tile's scores
 // only, 186 us; 128 rows a CTA throughout, 193; halves in place of bf16 with references that
 // follow the scores, 190; e4m3 for P as well, 259.  A CTA's start and end, 19,000 cycles (the
 // query tile's conversion 5,000), are the next largest part: nothing else runs on the SM.
 //
-//   warp 0         TMA: K and V tiles of 64 keys, a ring each
-//   warps 1, 3     MMAs of a half, issued by one lane
-//   warp 2         scale bytes as factors, fetched four tiles ahead
-//   8 SUBS warps   softmax, 32 keys of a row a thread; the query tile before, the output after
-//   4 SUBS warps   V to bf16
+//   warp 0           TMA: K and V tiles of 64 keys, a ring each
+//   warps 1, 3       MMAs of a half, issued by one lane
+//   warp 2           scale bytes as factors, fetched four tiles ahead
+//   4 HF SUBS warps  softmax, 64 / HF keys of a row a thread; the query tile before, the output after
+//   4 SUBS warps     V to bf16; before (HF 1) the query tile with the softmax warps
 #pragma once
 
 #include "attn_kv8_rows.cuh"
@@ -45,12 +45,18 @@ struct AttnTilesCfg {
   static constexpr int N = 128 * SUBS;                  // rows
   static constexpr int KT = 64;                         // keys of a tile
   static constexpr int SB = 2;                          // buffers of scores
-  static constexpr int SOFT_WARPS = 8 * SUBS, CONV_WARPS = 4 * SUBS;
+  // Softmax threads of a row: one issues less (hd 128: 146 us against 153 for the rows above),
+  // two wait less (256 rows of hd 64: 114 against 127; at 128 rows, two CTAs an SM, one is the faster:
+  // 64 sequences of 32 x 4 rows, 2048 keys, 76 us against 83).
+  static constexpr int HF = HD == 64 && SUBS == 2 ? 2 : 1;
+  static constexpr int SOFT_WARPS = 4 * HF * SUBS, CONV_WARPS = 4 * SUBS;
   static constexpr int THREADS = 32 * (4 + SOFT_WARPS + CONV_WARPS);
   static constexpr int CTAS = SUBS == 1 ? 2 : 1;        // an SM
-  // registers, from the launch's 64 a thread (SUBS 1) or 72 (SUBS 2) shared out anew by
-  // warpgroups: 2 * 80 + 40 + 56 = 4 * 64, 4 * 88 + 2 * 40 + 72 = 7 * 72
-  static constexpr int REGS_SOFT = SUBS == 1 ? 80 : 88, REGS_CONV = 40, REGS_REST = SUBS == 1 ? 56 : 72;
+  // registers, from the launch's a thread shared out anew by warpgroups: 128 + 48 + 56 <= 3 * 80,
+  // 2 * 144 + 2 * 56 + 72 <= 5 * 96, 4 * 88 + 2 * 40 + 72 = 7 * 72 (HF 2)
+  static constexpr int REGS_SOFT = HF == 2 ? 88 : SUBS == 1 ? 128 : 144;
+  static constexpr int REGS_CONV = HF == 2 ? 40 : SUBS == 1 ? 48 : 56;
+  static constexpr int REGS_REST = SUBS == 1 ? 56 : 72;
   static constexpr int SLOT = KT * HD;
   static constexpr int VS = SUBS == 1 ? 2 : 3;          // V slots (K has 3)
   static constexpr int VB = SUBS == 1 ? 2 : 3;          // V tiles as bf16
@@ -90,7 +96,7 @@ __global__ void __launch_bounds__(AttnTilesCfg<HD, SUBS>::THREADS, AttnTilesCfg<
     attn_kv8_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                           const __grid_constant__ AttnKv8Params p) {
   using C = AttnTilesCfg<HD, SUBS>;
-  constexpr int KT = C::KT, N = C::N, KH = KT / 2;
+  constexpr int KT = C::KT, N = C::N, HF = C::HF, KH = KT / HF;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sK = smem;
@@ -143,7 +149,7 @@ __global__ void __launch_bounds__(AttnTilesCfg<HD, SUBS>::THREADS, AttnTilesCfg<
     for (int s = 0; s < SUBS; ++s) {
       mbar_init(&qready[s], 8);
       for (int k = 0; k < C::SB; ++k) mbar_init(&sfull[C::SB * s + k], 1);
-      for (int k = 0; k < 3; ++k) mbar_init(&pready[3 * s + k], 8 + C::CONV_WARPS);
+      for (int k = 0; k < 3; ++k) mbar_init(&pready[3 * s + k], 4 * HF + C::CONV_WARPS);
       mbar_init(&mdone[s], 1);
       mbar_init(&pread[s], 1);
     }
@@ -159,17 +165,22 @@ __global__ void __launch_bounds__(AttnTilesCfg<HD, SUBS>::THREADS, AttnTilesCfg<
   }
   griddep_launch_dependents();
   griddep_wait();
-  // the softmax warps: 128 rows' eight, of which w and w + 4 share 32 rows
-  const int sub_w = (warp - 4) >> 3, tid = ((warp - 4) & 7) * 32 + lane;
+  // The query tile: 128 rows by eight warps, their softmax warps and (HF 1) four that convert V later.
+  const bool soft = warp >= 4 && warp < 4 + C::SOFT_WARPS;
+  const int sub_w = soft ? (warp - 4) / (4 * HF) : (warp - 4 - C::SOFT_WARPS) / 4;   // of the converting warps, too
+  const int tid = (soft ? (warp - 4) % (4 * HF) : 4 + (warp & 3)) * 32 + lane;
+  const bool asks = (soft || (HF == 1 && warp >= 4)) && sub_w < subs;
   AttnQueryTile<HD, 128, 256> query;
-  if (warp >= 4 && sub_w < subs) query.load(p, seq, g, rt * SUBS + sub_w, n_rows - sub_w * 128, tid);
-  // the limits by the last N threads: loads return in order, and the query's are slow
-  if (const int k = (int)threadIdx.x - (C::THREADS - N); k >= 0) {
-    const int n = k < n_rows ? k : 0;
-    const int i = (int)p.by_group.div((uint32_t)(rt * N + n));
-    const int lim = p.limits ? p.limits[(long long)seq * p.R + i] : p.c.T;
-    s_lim[k] = min(max(lim, 0), p.c.T);
-    s_q[k] = 0x7f7f7f7fu;
+  if (asks) query.load(p, seq, g, rt * SUBS + sub_w, n_rows - sub_w * 128, tid);
+  // the limits by other threads: loads return in order, and the query's are slow
+  if (warp < 4) {
+#pragma unroll
+    for (int k = (int)threadIdx.x; k < N; k += 128) {
+      const int i = (int)p.by_group.div((uint32_t)(rt * N + (k < n_rows ? k : 0)));
+      const int lim = p.limits ? p.limits[(long long)seq * p.R + i] : p.c.T;
+      s_lim[k] = min(max(lim, 0), p.c.T);
+      s_q[k] = 0x7f7f7f7fu;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -185,6 +196,14 @@ __global__ void __launch_bounds__(AttnTilesCfg<HD, SUBS>::THREADS, AttnTilesCfg<
 
   auto wait = [&](uint64_t* bar, int phase) {           // decided warp-wide: tensor-memory accesses are collective
     return __all_sync(0xffffffffu, mbar_wait_long(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
+  };
+  auto query_tile = [&]() {
+    if (!asks || nt == 0) return;
+    uint8_t* q = sQ + sub_w * (256 * HD);
+    query.store(n_rows - sub_w * 128, tid, q, q + 128 * HD, 0, s_q + sub_w * 128);
+    fence_async_smem();
+    named_bar_sync(2 + sub_w, 256);                       // and the rows' scales are there
+    if (lane == 0) mbar_arrive(&qready[sub_w]);
   };
   // Tiles count on through the second walk (T = pass * nt + t); each role walks twice in
   // its own branch, which a register share needs, and meets the others in between.
@@ -262,7 +281,7 @@ __global__ void __launch_bounds__(AttnTilesCfg<HD, SUBS>::THREADS, AttnTilesCfg<
             const uint32_t v = h0 + T % C::VB * C::V_BYTES, pb = ts + T % C::SB * KT;
 #pragma unroll
             for (int kk = 0; kk < KT / 16; ++kk)
-              mma_f16_ts(lead, to, pb + kk / (KT / 32) * KH + kk % (KT / 32) * 8,
+              mma_f16_ts(lead, to, pb + kk / (KH / 16) * KH + kk % (KH / 16) * 8,
                          sdesc_rows<128>(v + kk * 2048, KT * 128), idesc_o, (t > 0 || kk > 0) ? 1u : 0u);
             mma_commit_lead(lead, &pvdone[r]);
             mma_commit_lead(lead, &pread[sub]);
@@ -349,6 +368,7 @@ __global__ void __launch_bounds__(AttnTilesCfg<HD, SUBS>::THREADS, AttnTilesCfg<
       if (!once_more(pass)) break;
     }
   } else if (warp >= 4 + C::SOFT_WARPS) {
+    query_tile();                                         // before registers move: its barrier is for both sides
     setmaxnreg_dec<C::REGS_CONV>();
     // ------------------------------------------------------ V to bf16, KEYS keys of a tile
     constexpr int KEYS = KT / C::CONV_WARPS, ROWS = 512 / HD;   // a warp's keys, of a step
@@ -406,19 +426,14 @@ __global__ void __launch_bounds__(AttnTilesCfg<HD, SUBS>::THREADS, AttnTilesCfg<
       if (!once_more(pass)) break;
     }
   } else {
+    query_tile();
     setmaxnreg_inc<C::REGS_SOFT>();
     // keys 32 hf .. of a tile, dims HD / 2 * hf ..
-    const int sub = sub_w, q4 = warp & 3, hf = ((warp - 4) >> 2) & 1, row = sub * 128 + q4 * 32 + lane;
+    const int sub = sub_w, q4 = warp & 3, hf = ((warp - 4) >> 2) % HF, row = sub * 128 + q4 * 32 + lane;
     const int pair_bar = 4 + sub * 4 + q4;
     const bool part = nt > 0 && sub < subs;
     const uint32_t trow = tmem + sub * C::SUB_COLS + ((uint32_t)(q4 * 32) << 16);
     const int lim_row = s_lim[row], lim = lim_row - hf * KH, lim_min = __reduce_min_sync(0xffffffffu, lim_row);
-    if (part) {
-      query.store(n_rows - sub * 128, tid, sQ + sub * (256 * HD), sQ + sub * (256 * HD) + 128 * HD, 0, s_q + sub * 128);
-      fence_async_smem();
-      named_bar_sync(2 + sub, 256);                       // and the rows' scales are there
-      if (lane == 0) mbar_arrive(&qready[sub]);
-    }
     // scores to base 2: the row's scale and the softmax's.  The 2^9 comes off the keys'
     // factors, so that neither a query nor a key in bf16 takes its factor out of range (keys
     // under 2^-90 lose bits: they matter to queries over 2^60).
@@ -467,10 +482,13 @@ __global__ void __launch_bounds__(AttnTilesCfg<HD, SUBS>::THREADS, AttnTilesCfg<
 #pragma unroll
             for (int c = 0; c < 32; ++c) top = fmaxf(top, s[c]);
           }
-          s_top[hf * N + row] = top;
-          named_bar_sync(pair_bar, 64);
-          top = fmaxf(top, s_top[(hf ^ 1) * N + row]) * rc;
-          named_bar_sync(pair_bar, 64);                   // both are read
+          if constexpr (HF == 2) {
+            s_top[hf * N + row] = top;
+            named_bar_sync(pair_bar, 64);
+            top = fmaxf(top, s_top[(hf ^ 1) * N + row]);
+            named_bar_sync(pair_bar, 64);                 // both are read
+          }
+          top *= rc;
           const bool up = t == 0 ? top > -INFINITY : top > m + kRowSlack;
           const float corr = t > 0 && up ? exp2f(m - top) : 1.0f;
           if (up) m = top;
@@ -479,7 +497,7 @@ __global__ void __launch_bounds__(AttnTilesCfg<HD, SUBS>::THREADS, AttnTilesCfg<
             wait(&pvdone[(T - 1) % 3], (T - 1) / 3);
             tc_fence_after();
 #pragma unroll 1
-            for (int c = hf * (HD / 2); c < (hf + 1) * (HD / 2); c += 16) {
+            for (int c = hf * (HD / HF); c < (hf + 1) * (HD / HF); c += 16) {
               float o[16];
               tmem_ld16(trow + C::O_COL + c, o);
 #pragma unroll
@@ -520,9 +538,12 @@ __global__ void __launch_bounds__(AttnTilesCfg<HD, SUBS>::THREADS, AttnTilesCfg<
     }
     // ------------------------------------------------------ output
     const float2 lp = f32x2_get(l2);
-    s_top[hf * N + row] = lp.x + lp.y;
-    named_bar_sync(pair_bar, 64);
-    const float l_sum = s_top[row] + s_top[N + row];
+    float l_sum = lp.x + lp.y;
+    if constexpr (HF == 2) {
+      s_top[hf * N + row] = l_sum;
+      named_bar_sync(pair_bar, 64);
+      l_sum = s_top[row] + s_top[N + row];
+    }
     // 2^vsh in two steps: it alone may leave the range that the result is in
     const int vsh = nt > 0 ? *s_vsh : 0;
     const float f2 = scale_value(127 + vsh / 2);
@@ -534,7 +555,7 @@ __global__ void __launch_bounds__(AttnTilesCfg<HD, SUBS>::THREADS, AttnTilesCfg<
     uint8_t* stage = sQ + row * (2 * HD);
     constexpr int CHUNKS = HD / 8;
 #pragma unroll 1
-    for (int c = hf * (HD / 2); c < (hf + 1) * (HD / 2); c += 32) {
+    for (int c = hf * (HD / HF); c < (hf + 1) * (HD / HF); c += 32) {
       float o[32] = {};
       if (part) tmem_ld32(trow + C::O_COL + c, o);
 #pragma unroll
@@ -559,11 +580,12 @@ __global__ void __launch_bounds__(AttnTilesCfg<HD, SUBS>::THREADS, AttnTilesCfg<
       }
     }
     if (p.splits == 1) {
-      named_bar_sync(pair_bar, 64);
+      if constexpr (HF == 2) named_bar_sync(pair_bar, 64);
+      __syncwarp();
       const int l = lane % CHUNKS;
 #pragma unroll 4
-      for (int k = 0; k < 16; k += 32 / CHUNKS) {
-        const int n = sub * 128 + q4 * 32 + hf * 16 + k + lane / CHUNKS;   // of the pair's 32 rows, 16 a warp
+      for (int k = 0; k < 32 / HF; k += 32 / CHUNKS) {
+        const int n = sub * 128 + q4 * 32 + hf * 16 + k + lane / CHUNKS;
         uint32_t jh;
         const int i = (int)p.by_group.divmod((uint32_t)(rt * N + n), jh), h = g * p.group + (int)jh;
         uint16_t* dst = p.out + ((long long)seq * p.R + i) * p.o_rs + (long long)h * HD + l * 8;
