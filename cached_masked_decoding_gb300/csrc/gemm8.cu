@@ -2,7 +2,6 @@
 // quantiser of its operands (see q8.cuh):
 //   Y[n][m] = sum_B 2^(ex[B][n] + ew[B][m]) * sum_{k in block B} X[n][k] W[m][k]
 #include <algorithm>
-#include <atomic>
 
 #include "gemm.cuh"
 #include "ops8.h"
@@ -341,23 +340,23 @@ __global__ void __launch_bounds__(224, 2)
 // ---------------------------------------------------------------- many rows
 // The same product for activations of hundreds of rows, bound by the tensor cores
 // and by what L2 delivers to them: at the MMA's full rate a tile of 128 x 128 asks
-// for 128 bytes a cycle and SM (measured: about 50 were delivered, 38% of the rate).  Here a
-// pair of CTAs (a cluster) takes 256 x 192 outputs, its activation rows fetched
-// once and multicast to both, 75 bytes a cycle; and a CTA is persistent, one an SM, with two
-// accumulators, so that storing one tile overlaps the next one's products.  12288 x 4096
-// weights, 2048 rows: 79 us with the quantiser, 2.6 PFLOP/s; a block of K takes 640 cycles, in which an SM takes in
-// its 40 KB of operands, for 384 cycles of products.
-//   warp 0     TMA: weight codes, and half the activation codes for both CTAs
+// for 128 bytes a cycle and SM (measured: about 50 were delivered, 38% of the rate), one of 128 x 192 for
+// 107.  A CTA is persistent, one an SM, with two accumulators, so that storing one tile overlaps the next
+// one's products.  12288 x 4096 weights, 2048 rows, on the GPU: 80 us with the quantiser, 2.6 PFLOP/s; a block of
+// K takes about 650 cycles, in which an SM takes in its 40 KB of operands, for 384 cycles of products.  Tiles of 256 x 192
+// (28 KB for the same products, but no accumulator left to store from): 85 us there, 144 against 156 for 24576 x 4096,
+// and 22-27 against 15-19 where one round of the smaller tiles is enough.
+//   warp 0     TMA: weight and activation codes
 //   warp 1     scale copies and MMAs, issued by one lane
-//   warps 2-5  epilogue
-//   warp 6     weight scale bytes, warp 7 activation scale bytes
+//   warp 2     weight scale bytes, warp 3 activation scale bytes
+//   warps 4-7  epilogue
 struct Gemm8BigCfg {
   static constexpr int BN = 192;
   static constexpr int A_BYTES = 128 * kQBlock;
   static constexpr int B_BYTES = BN * kQBlock;
   static constexpr int SF_BYTES = 3 * 512;
   static constexpr int STAGES = 5;
-  static constexpr int SMEM_BYTES = 1024 + STAGES * (A_BYTES + B_BYTES + SF_BYTES) + (2 * STAGES + 4) * 8 + 16;
+  static constexpr int SMEM_BYTES = 1024 + STAGES * (A_BYTES + B_BYTES + SF_BYTES) + (2 * STAGES + 5) * 8 + 16;
   static constexpr int SF_COL = 2 * BN, SF_COLS = 12;
   static_assert(SF_COL + STAGES * SF_COLS <= 512, "tensor memory");
   static_assert(SMEM_BYTES <= 232448, "shared memory");
@@ -377,24 +376,24 @@ __global__ void __launch_bounds__(256, 1)
   uint64_t* empty = full + S;
   uint64_t* tfull = empty + S;    // [2] an accumulator is complete
   uint64_t* tempty = tfull + 2;   // [2] and has been read
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  uint64_t* mdone = tempty + 2;   // every MMA is done (before tensor memory is freed)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mdone + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* err = g_gemm8_err;
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int rank = (int)cluster_rank();
-  const int pairs = (int)(gridDim.x >> 1), pair = (int)(blockIdx.x >> 1);
-  const int total = (p.M + 255) / 256 * p.n_tiles;        // tiles of 256 x BN
+  const int total = (p.M + 127) / 128 * p.n_tiles;   // tiles of 128 x BN
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 3);
-      mbar_init(&empty[s], 2);    // both CTAs' MMAs: the activations land in both
+      mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], 4);
     }
+    mbar_init(mdone, 1);
     *abort_flag = 0;
     fence_mbar_init();
     prefetch_tensormap(&tmW);
@@ -406,7 +405,6 @@ __global__ void __launch_bounds__(256, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();                 // the other CTA's barriers are initialised
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_launch_dependents();
@@ -421,33 +419,29 @@ __global__ void __launch_bounds__(256, 1)
     RingPos r{0, 0u};
     int issued = 0;
     bool ok = true;
-    for (int t = pair; t < total && ok; t += pairs) {
-      const int m0 = (t / p.n_tiles * 2 + rank) * 128, n0 = t % p.n_tiles * BN;
+    for (int t = (int)blockIdx.x; t < total && ok; t += (int)gridDim.x) {
+      const int m0 = t / p.n_tiles * 128, n0 = t % p.n_tiles * BN;
       for (int i = 0; i < p.kb; ++i) {
         if (issued >= S && !(ok = wait(&empty[r.s], r.par ^ 1u, ERR_GEMM_EMPTY))) break;
         if (lead) {
           mbar_arrive_expect_tx(&full[r.s], C::A_BYTES + C::B_BYTES);
           tma_load_3d(sA + r.s * C::A_BYTES, &tmW, &full[r.s], i * kQBlock, m0, 0, pol_w);
-          tma_load_3d_multicast(sB + r.s * C::B_BYTES + rank * (C::B_BYTES / 2), &tmX, &full[r.s], i * kQBlock,
-                                n0 + rank * (BN / 2), 0, (uint16_t)3, pol_x);
+          tma_load_3d(sB + r.s * C::B_BYTES, &tmX, &full[r.s], i * kQBlock, n0, 0, pol_x);
         }
         r.next(S);
         ++issued;
       }
     }
-    // Every copy into this CTA has landed and both CTAs' releases have arrived before
-    // its shared memory goes away.
-    for (int i = max(issued - S, 0); i < issued; ++i) {
-      if (*abort_flag) mbar_wait_long(&full[i % S], (uint32_t)(i / S) & 1u, nullptr, err, ERR_GEMM_DRAIN);
-      mbar_wait_long(&empty[i % S], (uint32_t)(i / S) & 1u, abort_flag, err, ERR_GEMM_EMPTY);
-    }
+    if (*abort_flag)   // let copies in flight land before the CTA's shared memory goes away
+      for (int i = max(issued - S, 0); i < issued; ++i)
+        mbar_wait_long(&full[i % S], (uint32_t)(i / S) & 1u, nullptr, err, ERR_GEMM_DRAIN);
   } else if (warp == 1) {
     const uint32_t lead = elect_one();
     constexpr uint32_t idesc = idesc_mxf8(128, BN);
     RingPos r{0, 0u};
     bool ok = true;
     int n = 0;
-    for (int t = pair; t < total && ok; t += pairs, ++n) {
+    for (int t = (int)blockIdx.x; t < total && ok; t += (int)gridDim.x, ++n) {
       const uint32_t d = tmem + (uint32_t)((n & 1) * BN);
       if (n >= 2 && !(ok = wait(&tempty[n & 1], (uint32_t)((n >> 1) - 1) & 1u, ERR_GEMM_TEMPTY))) break;
       tc_fence_after();
@@ -465,23 +459,25 @@ __global__ void __launch_bounds__(256, 1)
         for (int kk = 0; kk < 4; ++kk)
           mma_mxf8_ss(lead, d, sdesc_sw128(a0 + kk * 32), sdesc_sw128(b0 + kk * 32), idesc, sfa, sfb,
                       (i > 0 || kk > 0) ? 1u : 0u);
-        mma_commit_multicast(lead, &empty[r.s], (uint16_t)3);
+        mma_commit_lead(lead, &empty[r.s]);
         r.next(S);
       }
       if (ok) mma_commit_lead(lead, &tfull[n & 1]);
     }
-  } else if (warp >= 6) {
+    mma_commit_lead(lead, mdone);
+    mbar_wait_long(mdone, 0u, nullptr, err, ERR_GEMM_TFULL);
+  } else if (warp < 4) {
     // four blocks' bytes in use, the next four's in flight
     constexpr int AHEAD = 4, W = 6;
-    const bool is_a = warp == 6;
+    const bool is_a = warp == 2;
     const uint8_t* src = is_a ? p.ws : p.xs;
     const int limit = is_a ? p.M : p.N, words = is_a ? 4 : W;
     uint32_t nx[AHEAD][W];
     RingPos r{0, 0u};
     int done = 0;
     bool ok = true;
-    for (int t = pair; t < total && ok; t += pairs) {
-      const int row0 = is_a ? (t / p.n_tiles * 2 + rank) * 128 : t % p.n_tiles * BN;
+    for (int t = (int)blockIdx.x; t < total && ok; t += (int)gridDim.x) {
+      const int row0 = is_a ? t / p.n_tiles * 128 : t % p.n_tiles * BN;
       auto fetch = [&](int i0) {
 #pragma unroll
         for (int e = 0; e < AHEAD; ++e)
@@ -522,8 +518,8 @@ __global__ void __launch_bounds__(256, 1)
     // epilogue: thread = weight row, columns = activation rows
     const int q = warp & 3, l128 = q * 32 + lane;
     int n = 0;
-    for (int t = pair; t < total; t += pairs, ++n) {
-      const int m = (t / p.n_tiles * 2 + rank) * 128 + l128, n0 = t % p.n_tiles * BN;
+    for (int t = (int)blockIdx.x; t < total; t += (int)gridDim.x, ++n) {
+      const int m = t / p.n_tiles * 128 + l128, n0 = t % p.n_tiles * BN;
       const int cols = min(BN, p.N - n0);
       if (!wait(&tfull[n & 1], (uint32_t)(n >> 1) & 1u, ERR_GEMM_TFULL)) break;
       tc_fence_after();
@@ -552,11 +548,9 @@ __global__ void __launch_bounds__(256, 1)
       if (lane == 0) mbar_arrive(&tempty[n & 1]);
     }
   }
-  // no CTA leaves while the other may still write to it
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  cluster_sync();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -583,32 +577,11 @@ cudaError_t launch_gemm8(const CUtensorMap& tw, const CUtensorMap& tx, const Gem
   return op_launch(gemm8_kernel<BN>, dim3(grid), dim3(224), C::SMEM_BYTES, st, 1 << p.split_log, tw, tx, p);
 }
 
-// CTA pairs of gemm8_big_kernel that the current device holds at once.
-cudaError_t big_pairs(int* pairs) {
-  const void* k = reinterpret_cast<const void*>(gemm8_big_kernel);
-  const cudaError_t e = op_smem_once(k, Gemm8BigCfg::SMEM_BYTES);
+cudaError_t launch_gemm8_big(const CUtensorMap& tw, const CUtensorMap& tx, const Gemm8Params& p, unsigned grid,
+                             cudaStream_t st) {
+  const cudaError_t e = op_smem_once(reinterpret_cast<const void*>(gemm8_big_kernel), Gemm8BigCfg::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  static std::atomic<int> known[64];                      // by device; 0: not asked yet
-  int dev = 0;
-  const cudaError_t d = cudaGetDevice(&dev);
-  if (d != cudaSuccess) return d;
-  const bool slot = dev >= 0 && dev < 64;
-  if (slot && (*pairs = known[dev].load()) > 0) return cudaSuccess;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)op_device_sms() & ~1u);
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = Gemm8BigCfg::SMEM_BYTES;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t o = cudaOccupancyMaxActiveClusters(pairs, k, &cfg);
-  if (o != cudaSuccess) return o;
-  if (*pairs < 1) *pairs = 1;
-  if (slot) known[dev].store(*pairs);
-  return cudaSuccess;
+  return op_launch(gemm8_big_kernel, dim3(grid), dim3(256), Gemm8BigCfg::SMEM_BYTES, st, 1, tw, tx, p);
 }
 
 }  // namespace
@@ -675,22 +648,20 @@ extern "C" dllm_status dllm_op_gemm8(const uint8_t* W, const uint8_t* W_scale, c
   // together.  Each keeps at least two blocks of K.
   while (p.split_log < 3 && (tiles << p.split_log) * 2 <= slots && p.kb >= 4 << p.split_log) ++p.split_log;
   if (N > 64) {
-    // Or tiles of 256 x 192 by CTA pairs.  A block of K takes a round of those 0.31 us and a
-    // round of 128-row CTAs 0.56 us, the join of a split about six blocks (measured, us, with
-    // the quantiser, pairs / CTAs: 4096 x 4096 weights, 400 rows 16 / 24, 768 rows 18 / 22, 1024 rows 27 / 22;
-    // 12288 x 4096, 160 rows 17 / 22, 256 rows 26 / 22, 512 rows 27 / 38).
-    const long long big = (M + 255LL) / 256 * ((N + Gemm8BigCfg::BN - 1LL) / Gemm8BigCfg::BN);
-    int pairs = 0;
-    OP_CK(big_pairs(&pairs));
-    const __int128 big_cost = (__int128)5 * ((big + pairs - 1) / pairs) * p.kb;
-    const __int128 cta_cost = (__int128)9 * (((tiles << p.split_log) + slots - 1) / slots) *
-                              (((p.kb + (1 << p.split_log) - 1) >> p.split_log) + (p.split_log ? 6 : 0));
+    // Or tiles of 128 x 192 by persistent CTAs.  A block of K takes a round of those 0.36 us and a
+    // round of the two CTAs an SM 0.52 us, the join of a split about 15 blocks (measured, us, with
+    // the quantiser, persistent / two CTAs: 4096 x 4096 weights, 128 rows 15.0 / 14.4, 400 rows 16.7 / 22.5, 768 rows
+    // 18.9 / 21.1, 1024 rows 28.6 / 21.7; 12288 x 4096, 160 rows 17.1 / 20.0, 256 rows 26.9 / 21.7, 512 rows 27.9 / 35.4,
+    // 2048 rows 82 / 99; 4096 x 12288, 100 rows 34 / 19, 2048 rows 107 / 99; 688 x 256, 300 rows 6.5 / 5.8).
+    const long long sms = op_device_sms(), big = (M + 127LL) / 128 * ((N + Gemm8BigCfg::BN - 1LL) / Gemm8BigCfg::BN);
+    const __int128 big_cost = 9 * ((__int128)((big + sms - 1) / sms) * p.kb + 1);
+    const __int128 cta_cost = (__int128)13 * (((tiles << p.split_log) + slots - 1) / slots) *
+                              (((p.kb + (1 << p.split_log) - 1) >> p.split_log) + (p.split_log ? 15 : 0));
     if (big_cost <= cta_cost && big <= 0x3fffffffLL) {
       p.n_tiles = (N + Gemm8BigCfg::BN - 1) / Gemm8BigCfg::BN;
-      if (const dllm_status s = op_map_u8(&tx, X, K, N, 1, K, (uint64_t)K * N, 128, Gemm8BigCfg::BN / 2); s != DLLM_OK)
+      if (const dllm_status s = op_map_u8(&tx, X, K, N, 1, K, (uint64_t)K * N, 128, Gemm8BigCfg::BN); s != DLLM_OK)
         return s;
-      const unsigned grid = 2u * (unsigned)std::min<long long>(pairs, big);
-      OP_CK(op_launch(gemm8_big_kernel, dim3(grid), dim3(256), Gemm8BigCfg::SMEM_BYTES, st, 2, tw, tx, p));
+      OP_CK(launch_gemm8_big(tw, tx, p, (unsigned)std::min(sms, big), st));
       return DLLM_OK;
     }
   }

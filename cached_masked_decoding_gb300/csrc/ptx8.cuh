@@ -80,28 +80,6 @@ __device__ __forceinline__ void mma_commit_lead(uint32_t lead, uint64_t* bar) {
       : "memory");
 }
 
-// The same in every CTA of the cluster whose bit is set in mask.
-__device__ __forceinline__ void mma_commit_multicast(uint32_t lead, uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}\n" ::"r"(
-          smem_u32(bar)),
-      "r"(lead), "h"(mask)
-      : "memory");
-}
-
-// tma_load_3d into the same place of every CTA of the cluster whose bit is set in
-// mask, each one's mbarrier counting its bytes.
-__device__ __forceinline__ void tma_load_3d_multicast(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y,
-                                                      int z, uint16_t mask, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.L2::cache_hint"
-      " [%0], [%1, {%3, %4, %5}], [%2], %6, %7;" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "h"(mask), "l"(policy)
-      : "memory");
-}
-
 // Shared-memory descriptor of 512 contiguous bytes, 32 rows of 16: four
 // unswizzled 8-row cores 128 bytes apart.
 __device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
