@@ -22,7 +22,9 @@
 // Softmax runs with one key a thread and RW rows in its registers: nothing is
 // reduced across threads per tile but the 32-key maximum of each row (one
 // redux).  A row's reference is its maximum over the CTA's first 32 keys, and stays:
-// float32 sums and block scales hold what exceeds it by up to 2^110, so the
+// float32 sums and block scales hold what exceeds it by up to 2^110 (a probability
+// times its value scale by 2^118 over the CTA's number of keys, so that all of them times the
+// largest code, 448, add up to less than 2^127), so the
 // warps meet at no barrier after the first tile.  A CTA that met more, or
 // value scales over 2^60 from the first keys', walks its keys again with references that follow the
 // scores, and others that follow the products (score plus value exponent).  Sums l
@@ -113,7 +115,8 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 constexpr float kRefSlack = 40.0f;   // log2 a score or a product may exceed a reference by that follows them
-constexpr int kRefFixed = 110;       // and a product or sum one that does not
+constexpr int kRefFixed = 110;       // and a sum one that does not
+constexpr int kSumFixed = 118;       // and a product one, plus log2 of the keys that are added up
 constexpr int kVRange = 60;          // value exponents' distance from the first tile's that such references allow
 
 // The query tile, rows rt * N .. of the item, by THREADS threads (a multiple of 32):
@@ -632,7 +635,9 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
       }
       // a product or a sum over what float32 and the block scales hold (a NaN is no reason)
       constexpr uint32_t kOver = (uint32_t)(127 + kRefFixed) << 23;
-      bool over = far || (most >= kOver && most <= 0x7f800000u);
+      const int keys_log = 32 - __clz(max(nt * KT - 1, 1));   // 31 at most
+      const uint32_t over_product = (uint32_t)(127 + min(kRefFixed, kSumFixed - keys_log)) << 23;
+      bool over = far || (most >= over_product && most <= 0x7f800000u);
 #pragma unroll
       for (int j = 0; j < RW; ++j) over = over || l_sum[j] >= __uint_as_float(kOver);
       if (pass == 0 && over) *again = 1;

@@ -1,0 +1,82 @@
+"""The 8-bit operators at the ends of their ranges.
+
+Tolerances count roundings: half a step is 2^-8 of the value in bf16.
+"""
+import math
+
+import numpy as np
+import pytest
+
+import ops8_ref as ref
+from cached_masked_decoding_gb300 import binding
+from gpu_util import torch_cuda
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    t = torch_cuda()
+    binding.lib()
+    return t
+
+
+def dev(torch, a):
+    return torch.from_numpy(np.array(a, order="C")).cuda()
+
+
+# --------------------------------------------------------------------------- attention
+
+def attend(torch, q, k, ks, v, vs, scale):
+    """q [b][R][H][hd] bf16 over codes [b][H_kv][T][hd], bytes [b][H_kv][T] (device tensors)."""
+    b, R, H, hd = q.shape
+    h, T = k.shape[1:3]
+    cache = binding.make_kv8(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), b, h, T, hd)
+    n = binding.attention_kv8_workspace(b, H, h, hd, R, T)
+    ws = torch.full((max(n, 16),), 0xff, device="cuda", dtype=torch.uint8)
+    out = torch.full_like(q, 9.0)
+    binding.op_attention_kv8(q.data_ptr(), cache, out.data_ptr(), H, R, scale=scale, ws_ptr=ws.data_ptr(), ws_bytes=n)
+    assert binding.op_check() == 0
+    return out
+
+
+def along_first_dim(torch, h, R, hd, score2, values, byte):
+    """A cache whose key t scores score2[t] (to base 2, with scale ln 2) for queries of (1, 0, ..), and whose
+    value rows are codes of +-values[t] with scale byte byte[t]."""
+    T = len(score2)
+    rows = np.zeros((T, hd))
+    rows[:, 0] = score2
+    kc, ks = ref.quantise(rows)
+    assert (ref.dequantise(kc, ks) == rows).all()
+    sign = np.where(np.arange(hd) % 3 == 0, -1.0, 1.0)
+    vc = ref.encode(values[:, None] * sign)
+    q = torch.zeros(1, R, h, hd, device="cuda", dtype=torch.bfloat16)
+    q[..., 0] = 1.0
+    every = [dev(torch, np.broadcast_to(a, (1, h) + a.shape)) for a in (kc, ks, vc, byte)]
+    v = ref.dequantise(vc, byte)
+    p = np.exp2(score2 - score2.max())
+    return q, every, (p @ v) / p.sum()
+
+
+def check(got, want):
+    """Every row and head alike: bf16 probabilities and output, 2^-8 of sum p|v| each (|v| the same for all that
+    counts), and scores to base 2 up to 2^8 in float32: 2^-16 of a probability."""
+    np.testing.assert_allclose(got, np.broadcast_to(want, got.shape), rtol=2.0 ** -7 + 2.0 ** -15, atol=0)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("R", [1, 16, 32, 64, 100, 200])
+@pytest.mark.parametrize("score2,above,T", [(104.0, 5, 2048), (60.0, 49, 1600), (96.0, 13, 4096), (104.0, 4, 4096)])
+def test_many_large_products_of_one_sign(torch, R, hd, score2, above, T):
+    """Scores far above the first 32 keys', value scales 2^above over theirs and codes near the largest, so that each
+    product and each key lane's sum is under 2^110 but what they add up to is over 2^128: so many heads
+    that one walk has all keys."""
+    h = 160
+    if R <= 64:
+        assert binding.attention_kv8_workspace(1, h, h, hd, R, T) == 0
+    late = np.arange(T) >= 32
+    q, c, want = along_first_dim(torch, h, R, hd, np.where(late, score2, 0.0), np.where(late, 448.0, 1.0),
+                                 np.where(late, 127 + above, 127).astype(np.uint8))
+    got = attend(torch, q, *c, math.log(2.0)).double().cpu().numpy()
+    assert abs(want).min() > 447 * 2.0 ** above
+    check(got, want)
