@@ -114,6 +114,12 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// A split's sum l of probabilities is up to 2^117 (its reference stays), so that splits weigh by
+// l 2^m together: l as a factor in [1, 2) times 2^sum_log, whose exponents join those of m, both less
+// the heaviest split's.  (l times 2^(m - M) lost splits of low references to underflow.)
+__device__ __forceinline__ int sum_log(float l) { return min((int)(__float_as_uint(l) >> 23), 250) - 127; }
+__device__ __forceinline__ float pow2_f32(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
 constexpr float kRefSlack = 40.0f;   // log2 a score or a product may exceed a reference by that follows them
 constexpr int kRefFixed = 110;       // and a sum one that does not
 constexpr int kSumFixed = 118;       // and a product one, plus log2 of the keys that are added up
@@ -688,26 +694,32 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
   }
   if (soft && tid < N) {
     const float l = sum_of(tid);
-    float w = l == 0.0f ? 0.0f : __fdividef(1.0f, l);
+    float w = l == 0.0f ? 0.0f : __fdividef(1.0f, l), w2 = 1.0f;
     if (p.cluster) {
-      float mr[8], lr[8], M = -INFINITY, sum = 0.0f;
+      float mr[8], lr[8], M = -INFINITY, top = -INFINITY, sum = 0.0f;
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
         lr[r] = r < p.splits ? s_cl[r * N + tid] : 0.0f;
         mr[r] = r < p.splits ? s_cm[r * N + tid] : 0.0f;
       }
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        if (lr[r] != 0.0f) M = mr[r] > M || mr[r] != mr[r] ? mr[r] : M;   // a NaN stays
+      for (int r = 0; r < 8; ++r) {
+        M = fmaxf(M, lr[r] != 0.0f ? mr[r] : -INFINITY);  // (a NaN comes through the sum)
+        top = fmaxf(top, lr[r] != 0.0f ? mr[r] + (float)sum_log(lr[r]) : -INFINITY);
+      }
+      const int E = (int)(top - M);
+      auto weight = [&](float m, float ll) { return ex2((m - M) + (float)(sum_log(ll) - E)); };
 #pragma unroll
-      for (int r = 0; r < 8; ++r) sum += lr[r] != 0.0f ? lr[r] * ex2(mr[r] - M) : 0.0f;
-      w = l == 0.0f ? 0.0f : __fdividef(ex2(s_m[tid] - M), sum);
+      for (int r = 0; r < 8; ++r)
+        sum += lr[r] != 0.0f ? lr[r] * pow2_f32(-sum_log(lr[r])) * weight(mr[r], lr[r]) : 0.0f;
+      w = l == 0.0f ? 0.0f : pow2_f32(-sum_log(l));
+      w2 = __fdividef(weight(s_m[tid], l), sum);
     } else if (p.splits > 1 && tid < n_rows) {
       const long long slot = (long long)item * p.splits + split;
       *reinterpret_cast<float2*>(p.ws_ml + (slot * N + tid) * 2) = make_float2(s_m[tid], l);
     }
     const float vs = nt > 0 ? exp2f(0.5f * s_d[tid]) : 0.0f;
-    s_f[tid] = w == 0.0f ? make_float2(0.0f, 0.0f) : make_float2(vs * w, vs);
+    s_f[tid] = w == 0.0f || w2 == 0.0f ? make_float2(0.0f, 0.0f) : make_float2(vs * w, vs * w2);
   }
   if (soft) {
     named_bar_sync(2, C::SOFT);
@@ -763,7 +775,7 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
   }
 }
 
-// Join the splits of every row (64 at most): weights l_s 2^(m_s - M) over their sum.  A warp
+// Join the splits of every row (64 at most): weights l_s 2^m_s over their sum.  A warp
 // a row, a lane two splits' weights: they are whole before the first output meets one, since
 // a sum times an output may leave float32's range where the row does not.
 template <int HD>
@@ -801,24 +813,29 @@ __global__ void __launch_bounds__(128) attn_kv8_join_kernel(const __grid_constan
   };
   load(0);
   float2 ml[2];
-  float M = -INFINITY;
-  bool nan = false;
+  float M = -INFINITY, top = -INFINITY;                   // (a NaN comes through the sum)
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int s = lane + 32 * e;
     ml[e] = s < p.splits ? *reinterpret_cast<const float2*>(p.ws_ml + (first + (long long)s * N) * 2)
-                         : make_float2(-INFINITY, 0.0f);
+                         : make_float2(0.0f, 0.0f);
     if (ml[e].y != 0.0f) {                                // 0: the split saw none of the row's keys
       M = fmaxf(M, ml[e].x);
-      nan = nan || ml[e].x != ml[e].x;
+      top = fmaxf(top, ml[e].x + (float)sum_log(ml[e].y));
     }
   }
 #pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  if (__any_sync(0xffffffffu, nan)) M = __uint_as_float(0x7fffffffu);
+  for (int d = 16; d >= 1; d >>= 1) {
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  }
+  const int E = (int)(top - M);
   float w[2], sum;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) w[e] = ml[e].y == 0.0f ? 0.0f : ml[e].y * exp2f(ml[e].x - M);
+  for (int e = 0; e < 2; ++e) {
+    const int le = sum_log(ml[e].y);
+    w[e] = ml[e].y == 0.0f ? 0.0f : ml[e].y * pow2_f32(-le) * exp2f((ml[e].x - M) + (float)(le - E));
+  }
   sum = w[0] + w[1];
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);

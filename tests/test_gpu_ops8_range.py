@@ -80,3 +80,20 @@ def test_many_large_products_of_one_sign(torch, R, hd, score2, above, T):
     got = attend(torch, q, *c, math.log(2.0)).double().cpu().numpy()
     assert abs(want).min() > 447 * 2.0 ** above
     check(got, want)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("R,T,keys", [(1, 1024, 128), (32, 1024, 128), (64, 640, 128), (1, 16384, 256), (8, 16384, 256),
+                                      (64, 16384, 256), (100, 4096, 64)])
+@pytest.mark.parametrize("order", [1, -1])
+def test_splits_whose_references_lie_far_apart(torch, R, T, keys, hd, order):
+    """A split whose first keys score 0 and the rest 104 beside splits that score 160 throughout (base 2): the first
+    has 2^-56 of the weight for values 2^70 as large, so it is what the row is made of."""
+    rest = np.arange(T) >= keys
+    score2 = np.where(rest, 160.0, np.where(np.arange(T) < 32, 0.0, 104.0))
+    byte = np.where(rest, 120, 190)
+    if order < 0:
+        score2, byte = np.roll(score2, -keys), np.roll(byte, -keys)
+    q, c, want = along_first_dim(torch, 1, R, hd, score2, np.full(T, 256.0), byte.astype(np.uint8))
+    assert abs(want).min() > 100                     # 256 * 2^-7 = 2 without that split
+    check(attend(torch, q, *c, math.log(2.0)).double().cpu().numpy(), want)
