@@ -400,8 +400,8 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int key = min((t0 + t + e) * KT + key_l, lim_max - 1);
-          kn[e] = __ldg(ksc + key);
-          vn[e] = __ldg(vsc + key);
+          kn[e] = ksc[key];
+          vn[e] = vsc[key];
         }
       };
       if (nt > 0) fetch(0);

@@ -305,8 +305,8 @@ __global__ void __launch_bounds__(AttnTilesCfg<HD, SUBS>::THREADS, AttnTilesCfg<
 #pragma unroll
             for (int j = 0; j < J; ++j) {
               const int key = min((t0 + t + e) * KT + 32 * j + lane, lim_max - 1);
-              kn[e][j] = __ldg(ksc + key);
-              vn[e][j] = __ldg(vsc + key);
+              kn[e][j] = ksc[key];
+              vn[e][j] = vsc[key];
             }
         };
         if (nt > 0) fetch(0);

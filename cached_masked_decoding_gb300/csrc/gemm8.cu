@@ -208,12 +208,12 @@ __global__ void __launch_bounds__(224, 2)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int m = m0 + lane + 32 * j;
-          wa[e][j] = in && m < p.M ? __ldg(p.ws + B * p.M + m) : 127u;
+          wa[e][j] = in && m < p.M ? p.ws[B * p.M + m] : 127u;
         }
 #pragma unroll
         for (int j = 0; j < WB; ++j) {
           const int n = n0 + lane + 32 * j;
-          wb[e][j] = in && n < p.N ? __ldg(p.xs + B * p.N + n) : 127u;
+          wb[e][j] = in && n < p.N ? p.xs[B * p.N + n] : 127u;
         }
       }
     };
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
           for (int j = 0; j < W; ++j) {
             const int row = row0 + lane + 32 * j;
-            nx[e][j] = i0 + e < p.kb && j < words && row < limit ? __ldg(src + (long long)(i0 + e) * limit + row) : 127u;
+            nx[e][j] = i0 + e < p.kb && j < words && row < limit ? src[(long long)(i0 + e) * limit + row] : 127u;
           }
       };
       fetch(0);

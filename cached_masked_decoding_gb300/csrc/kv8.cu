@@ -40,9 +40,9 @@ struct Kv8Item {
     uint32_t i;
     const uint32_t s = p.heads.divmod(p.rows.divmod(g, i), h);
     row = s * (uint32_t)p.R + i;
-    const int n = p.counts ? __ldg(p.counts + s) : p.R;
+    const int n = p.counts ? p.counts[s] : p.R;
     if ((int)i >= n) return false;
-    const long long pos = (long long)(p.starts ? __ldg(p.starts + s) : 0) + i;
+    const long long pos = (long long)(p.starts ? p.starts[s] : 0) + i;
     if (pos < 0 || pos >= p.c.T) return false;
     slot = ((long long)s * p.c.H_kv + h) * p.c.T + pos;
     return true;
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(256, 4) kv8_load_kernel(const __grid_constant_
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     codes[w] = Raw8<E>::template load_codes<L>((w ? p.c.v : p.c.k) + it.slot * HD, l);
-    byte[w] = __ldg((w ? p.c.v_scale : p.c.k_scale) + it.slot);
+    byte[w] = (w ? p.c.v_scale : p.c.k_scale)[it.slot];
   }
 #pragma unroll
   for (int w = 0; w < 2; ++w) {

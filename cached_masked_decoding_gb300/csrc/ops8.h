@@ -33,6 +33,8 @@ cudaError_t attn_kv8_err_word(int** p);
 // Launch with programmatic dependent launch: the kernel's prologue overlaps the
 // end of the kernel before it in the stream, and griddepcontrol.wait in the
 // kernel orders everything that touches global memory behind that kernel.
+// A kernel launched so is resident while the ones before it still write, so its loads are ordinary
+// ones: the non-coherent path is for data that nothing writes during the kernel's whole life.
 // cluster > 1: that many consecutive CTAs form a cluster.
 template <typename Kern, typename... Args>
 inline cudaError_t op_launch(Kern kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t st, int cluster,

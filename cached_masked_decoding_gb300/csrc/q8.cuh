@@ -99,7 +99,7 @@ struct Raw8 {
   uint4 w[W];
   __device__ __forceinline__ void load(const typename E::T* p) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    for (int i = 0; i < W; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -115,7 +115,7 @@ struct Raw8 {
   template <int L>
   __device__ __forceinline__ void load(const typename E::T* row, int l) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(row) + i * L + l);
+    for (int i = 0; i < W; ++i) w[i] = reinterpret_cast<const uint4*>(row)[i * L + l];
   }
   template <int L>
   __device__ __forceinline__ void store(typename E::T* row, int l) const {
@@ -133,8 +133,8 @@ struct Raw8 {
   }
   template <int L>
   static __device__ __forceinline__ uint2 load_codes(const uint8_t* row, int l) {
-    if constexpr (W == 1) return __ldg(reinterpret_cast<const uint2*>(row) + l);
-    return make_uint2(__ldg(reinterpret_cast<const uint32_t*>(row) + l), __ldg(reinterpret_cast<const uint32_t*>(row) + L + l));
+    if constexpr (W == 1) return reinterpret_cast<const uint2*>(row)[l];
+    return make_uint2(reinterpret_cast<const uint32_t*>(row)[l], reinterpret_cast<const uint32_t*>(row)[L + l]);
   }
 };
 

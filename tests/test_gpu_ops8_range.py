@@ -97,3 +97,62 @@ def test_splits_whose_references_lie_far_apart(torch, R, T, keys, hd, order):
     q, c, want = along_first_dim(torch, 1, R, hd, score2, np.full(T, 256.0), byte.astype(np.uint8))
     assert abs(want).min() > 100                     # 256 * 2^-7 = 2 without that split
     check(attend(torch, q, *c, math.log(2.0)).double().cpu().numpy(), want)
+
+
+# --------------------------------------------------------------------------- calls in turn
+
+def test_calls_in_turn_see_what_the_one_before_wrote(torch):
+    """Quantise and product, store and attention, again and again over the same buffers with changing
+    inputs and no synchronisation: the same bits as step by step."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    steps, N, M, K, h, hd, T = 12, 4, 1024, 512, 8, 64, 300
+    w = torch.randint(0, 0x7f, (M, K), generator=g, device="cuda", dtype=torch.uint8)
+    ws = torch.full((K // 128, M), 119, device="cuda", dtype=torch.uint8)
+    x = (torch.randn(steps, N, K, generator=g, device="cuda") *
+         torch.exp2(torch.arange(steps, device="cuda") - 6.0)[:, None, None]).bfloat16()
+    kv = x[..., :h * hd].contiguous()
+    spec = binding.make_rope(hd)
+    pos = torch.arange(N, device="cuda", dtype=torch.int32)
+    starts = torch.full((1,), T - N, device="cuda", dtype=torch.int32)
+    n = binding.attention_kv8_workspace(1, h, h, hd, N, T)
+    atts = torch.empty(max(n, 16), device="cuda", dtype=torch.uint8)
+
+    def run(sync):
+        xc = torch.zeros(N, K, device="cuda", dtype=torch.uint8)
+        xs = torch.zeros(K // 128, N, device="cuda", dtype=torch.uint8)
+        codes = torch.zeros(2, 1, h, T, hd, device="cuda", dtype=torch.uint8)
+        scales = torch.full((2, 1, h, T), 127, device="cuda", dtype=torch.uint8)
+        cache = binding.make_kv8(codes[0].data_ptr(), codes[1].data_ptr(), scales[0].data_ptr(), scales[1].data_ptr(), 1, h,
+                                 T, hd)
+        turned = torch.zeros(N, h, hd, device="cuda", dtype=torch.bfloat16)
+        y = torch.zeros(steps, N, M, device="cuda")
+        out = torch.zeros(steps, N, h, hd, device="cuda", dtype=torch.bfloat16)
+        back = torch.zeros(2, steps, N, h, hd, device="cuda", dtype=torch.bfloat16)
+        torch.cuda.synchronize()
+        for i in range(steps):
+            calls = [
+                lambda: binding.op_quantise8(x[i].data_ptr(), "bf16", N, K, xc.data_ptr(), xs.data_ptr()),
+                lambda: binding.op_gemm8(w.data_ptr(), ws.data_ptr(), xc.data_ptr(), xs.data_ptr(), y[i].data_ptr(), "f32", M,
+                                         N, K),
+                lambda: binding.op_rope(kv[i].data_ptr(), turned.data_ptr(), pos.data_ptr(), N, h, hd, "bf16", spec),
+                lambda: binding.op_kv8_store(cache, turned.data_ptr(), kv[i].data_ptr(), "bf16", N,
+                                             starts_ptr=starts.data_ptr()),
+                lambda: binding.op_kv8_load(cache, back[0, i].data_ptr(), back[1, i].data_ptr(), "bf16", N,
+                                            starts_ptr=starts.data_ptr()),
+                lambda: binding.op_attention_kv8(turned.data_ptr(), cache, out[i].data_ptr(), h, N, ws_ptr=atts.data_ptr(),
+                                                 ws_bytes=n),
+            ]
+            for call in calls:
+                call()
+                if sync:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert binding.op_check() == 0
+        return y, out, back
+
+    want = run(True)
+    assert all(t.float().abs().amax(dim=tuple(range(1, t.dim()))).min() > 0 for t in want)
+    for _ in range(20):
+        for a, b in zip(want, run(False)):
+            assert torch.equal(a, b)

@@ -19,3 +19,14 @@ def test_every_copy_lands_in_one_cta_only(path):
     """The library also runs on several GPUs, where a copy to many CTAs may not be used; no operand
     of the 8-bit product is known to lie on this GPU."""
     assert "multi" + "cast" not in path.read_text()
+
+
+OPS8 = [p for p in ALL if p.name in ("gemm8.cu", "kv8.cu", "rope.cu", "attn_kv8.cu", "attn_kv8_rows.cuh", "attn_kv8_tiles.cuh",
+                                     "q8.cuh", "ptx8.cuh", "ops8.h")]
+
+
+@pytest.mark.parametrize("path", OPS8, ids=lambda p: p.name)
+def test_loads_are_coherent(path):
+    """The operators' kernels are resident while the one before writes what they read: the non-coherent
+    path is not defined for such data."""
+    assert not re.search(r"__ldg|ld\.global(\.\w+)*\.nc|__restrict__", code(path))
