@@ -249,7 +249,6 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
     tmem_alloc(tmem_slot, C::TMEM_COLS);
     tmem_relinquish();
   }
-  griddep_launch_dependents();
   griddep_wait();
   // rows of a split in a cluster: split, split + splits, ...
   const int own = (int)p.by_splits.div((uint32_t)(N + p.splits - 1));
@@ -288,6 +287,7 @@ __global__ void __launch_bounds__(AttnRowsCfg<HD, N>::THREADS, AttnRowsCfg<HD, N
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  griddep_launch_dependents();                          // not before: a dependent could take the columns awaited
   int lim_max, lim_min;
   {
     int hi = s_lim[lane & (N < 32 ? N - 1 : 31)], lo = hi;

@@ -163,7 +163,6 @@ __global__ void __launch_bounds__(AttnTilesCfg<HD, SUBS>::THREADS, AttnTilesCfg<
     tmem_alloc(tmem_slot, SUBS * C::SUB_COLS);
     tmem_relinquish();
   }
-  griddep_launch_dependents();
   griddep_wait();
   // The query tile: 128 rows by eight warps, their softmax warps and (HF 1) four that convert V later.
   const bool soft = warp >= 4 && warp < 4 + C::SOFT_WARPS;
@@ -186,6 +185,7 @@ __global__ void __launch_bounds__(AttnTilesCfg<HD, SUBS>::THREADS, AttnTilesCfg<
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  griddep_launch_dependents();                          // not before: a dependent could take the columns awaited
   int lim_max = 0;
 #pragma unroll
   for (int k = 0; k < N / 32; ++k) lim_max = max(lim_max, s_lim[lane + 32 * k]);

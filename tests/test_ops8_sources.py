@@ -30,3 +30,16 @@ def test_loads_are_coherent(path):
     """The operators' kernels are resident while the one before writes what they read: the non-coherent
     path is not defined for such data."""
     assert not re.search(r"__ldg|ld\.global(\.\w+)*\.nc|__restrict__", code(path))
+
+
+KERNELS = [(p, i, body) for p in ALL for i, body in enumerate(code(p).split("__global__")[1:]) if "tmem_alloc(" in body]
+
+
+@pytest.mark.parametrize("path,i,body", KERNELS, ids=lambda v: v.name if isinstance(v, Path) else str(v)[:3])
+def test_dependents_start_once_tensor_memory_is_held(path, i, body):
+    """The first thread that triggers the dependents does so for its CTA.  A dependent that took the columns
+    for which this CTA still waits would wait for this grid in turn: a barrier lies between the two."""
+    if "griddep_launch_dependents()" not in body:
+        return
+    alloc, trigger = body.index("tmem_alloc("), body.index("griddep_launch_dependents()")
+    assert alloc < body.find("__syncthreads()", alloc) < trigger
