@@ -34,6 +34,7 @@ struct Kv8Params {
 // where the row takes no part.
 struct Kv8Item {
   uint32_t row, h;
+  long long elem;        // the head's first element within a row (over 2^32 where heads are many)
   long long slot;        // (sequence * H_kv + head) * T + position
   __device__ __forceinline__ bool init(const Kv8Params& p, uint32_t g) {
     if (g >= p.groups) return false;
@@ -44,6 +45,7 @@ struct Kv8Item {
     if ((int)i >= n) return false;
     const long long pos = (long long)(p.starts ? p.starts[s] : 0) + i;
     if (pos < 0 || pos >= p.c.T) return false;
+    elem = (long long)h * p.c.hd;
     slot = ((long long)s * p.c.H_kv + h) * p.c.T + pos;
     return true;
   }
@@ -61,7 +63,7 @@ __global__ void __launch_bounds__(256, 4) kv8_store_kernel(const __grid_constant
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     raw[w].zero();
-    if (on) raw[w].template load<L>(static_cast<const typename E::T*>(p.in[w]) + it.row * p.rs[w] + it.h * HD, l);
+    if (on) raw[w].template load<L>(static_cast<const typename E::T*>(p.in[w]) + it.row * p.rs[w] + it.elem, l);
   }
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
@@ -100,7 +102,7 @@ __global__ void __launch_bounds__(256, 4) kv8_load_kernel(const __grid_constant_
     decode8(codes[w], scale_value(byte[w]), x);
     Raw8<E> out;
     out.from(x);
-    out.template store<L>(static_cast<typename E::T*>(p.out[w]) + it.row * p.rs[w] + it.h * HD, l);
+    out.template store<L>(static_cast<typename E::T*>(p.out[w]) + it.row * p.rs[w] + it.elem, l);
   }
 }
 

@@ -156,3 +156,26 @@ def test_calls_in_turn_see_what_the_one_before_wrote(torch):
     for _ in range(20):
         for a, b in zip(want, run(False)):
             assert torch.equal(a, b)
+
+
+# --------------------------------------------------------------------------- cache
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_cache_rows_past_32_bits_of_elements(torch, hd):
+    """A row of 2^32 elements and one head: the last head is its own, not the first one again."""
+    h = 2 ** 32 // hd + 1
+    rows = [torch.zeros(1, h, hd, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    for w, r in enumerate(rows):
+        r[0, 0], r[0, -1] = 1.0 + w, 5.0 + w
+    codes = [torch.zeros(h, hd, device="cuda", dtype=torch.uint8) for _ in range(2)]
+    scales = [torch.zeros(h, device="cuda", dtype=torch.uint8) for _ in range(2)]
+    cache = binding.make_kv8(codes[0].data_ptr(), codes[1].data_ptr(), scales[0].data_ptr(), scales[1].data_ptr(), 1, h, 1, hd)
+    binding.op_kv8_store(cache, rows[0].data_ptr(), rows[1].data_ptr(), "bf16", 1)
+    for w in range(2):
+        for at, value in ((0, 1.0 + w), (-1, 5.0 + w), (1, 0.0), (-2, 0.0)):
+            got = ref.dequantise(codes[w][at].cpu().numpy()[None], scales[w][at].cpu().numpy()[None])
+            assert (got == value).all()
+        rows[w].fill_(9.0)
+    binding.op_kv8_load(cache, rows[0].data_ptr(), rows[1].data_ptr(), "bf16", 1)
+    for w, r in enumerate(rows):
+        assert (r[0, 0] == 1.0 + w).all() and (r[0, -1] == 5.0 + w).all() and (r[0, 1:-1] == 0).all()
