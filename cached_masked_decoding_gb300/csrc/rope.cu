@@ -216,8 +216,9 @@ extern "C" dllm_status dllm_op_rope(const void* x, void* out, const int32_t* pos
   if (r->scaling == DLLM_ROPE_BASE) theta *= std::pow(r->factor, p.rot / (p.rot - 2.0));
   if (r->scaling == DLLM_ROPE_BY_PARTS) {
     const double k = p.rot / (2.0 * std::log(theta)), turn = 2.0 * 3.14159265358979323846;
+    // (the ramp may end past the last pair, for long original contexts)
     lo = std::fmax(0.0, std::floor(k * std::log(r->orig_len / (r->beta_fast * turn))));
-    hi = std::fmin(pairs - 1.0, std::ceil(k * std::log(r->orig_len / (r->beta_slow * turn))));
+    hi = std::fmin(p.rot - 1.0, std::ceil(k * std::log(r->orig_len / (r->beta_slow * turn))));
     amp = 0.1 * std::log(r->factor) + 1.0;
   }
   p.amp = (float)(r->amplitude > 0.0 ? r->amplitude : amp);

@@ -500,7 +500,7 @@ typedef enum dllm_rope_scaling {
                                   positions, f_i / factor where fewer than beta_slow, a linear ramp over
                                   the pair index between: from floor to ceil of
                                   rot_dim ln(orig_len / (2 pi beta)) / (2 ln theta), kept within
-                                  0..rot_dim/2 - 1 */
+                                  0..rot_dim - 1 (so the ramp may end past the last pair) */
 } dllm_rope_scaling;
 
 typedef struct dllm_rope {

@@ -179,3 +179,40 @@ def test_cache_rows_past_32_bits_of_elements(torch, hd):
     binding.op_kv8_load(cache, rows[0].data_ptr(), rows[1].data_ptr(), "bf16", 1)
     for w, r in enumerate(rows):
         assert (r[0, 0] == 1.0 + w).all() and (r[0, -1] == 5.0 + w).all() and (r[0, 1:-1] == 0).all()
+
+
+# --------------------------------------------------------------------------- rotary positions
+
+def turn(torch, spec, rot, pos, layout="half"):
+    """(cosine, sine) of every pair at positions pos, in float64."""
+    x = torch.zeros(len(pos), 1, rot, device="cuda")
+    x[..., :rot // 2] = 1.0
+    out = torch.empty_like(x)
+    p = dev(torch, np.asarray(pos, dtype=np.int32))
+    binding.op_rope(x.data_ptr(), out.data_ptr(), p.data_ptr(), len(pos), 1, rot, "f32", spec)
+    o = out.double().cpu().numpy()[:, 0]
+    return o[:, :rot // 2], o[:, rot // 2:]
+
+
+def yarn_rates(rot, theta, factor, orig_len, fast=32.0, slow=1.0):
+    """The published ramp: its edges kept within 0 and rot - 1, so that it may end past the last pair."""
+    def edge(turns):
+        return rot * math.log(orig_len / (turns * 2 * math.pi)) / (2 * math.log(theta))
+    lo, hi = max(math.floor(edge(fast)), 0), min(math.ceil(edge(slow)), rot - 1)
+    i = np.arange(rot // 2)
+    ramp = np.clip((i - lo) / (hi - lo if hi > lo else 0.001), 0, 1)
+    f = theta ** (-2.0 * i / rot)
+    return f / factor * ramp + f * (1 - ramp)
+
+
+@pytest.mark.parametrize("rot,theta,orig_len", [(64, 1e4, 65536), (128, 1e4, 65536), (128, 1e4, 1 << 20), (32, 1e4, 131072),
+                                                (16, 100.0, 4096), (64, 5e5, 8192), (64, 1e4, 4096)])
+@pytest.mark.parametrize("factor", [4.0, 40.0])
+def test_ramps_that_end_past_the_last_pair(torch, rot, theta, orig_len, factor):
+    pos = np.array([1, 2, 3, 1000, orig_len, 4 * orig_len - 1])
+    spec = binding.make_rope(rot, theta=theta, scaling="by_parts", factor=factor, orig_len=orig_len, amplitude=1.0)
+    c, s = turn(torch, spec, rot, pos)
+    a = pos[:, None] * yarn_rates(rot, theta, factor, orig_len)
+    # cosines to 8 float32 roundings; angles of up to 2^22 to some 2^-51 of themselves on both sides
+    np.testing.assert_allclose(c, np.cos(a), rtol=0, atol=2.0 ** -20)
+    np.testing.assert_allclose(s, np.sin(a), rtol=0, atol=2.0 ** -20)
