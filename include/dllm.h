@@ -516,8 +516,9 @@ typedef struct dllm_rope {
  * even, 2..1024, with strides in elements between rows and heads (0: dense);
  * a head's elements are contiguous; a fused [rows][q|k|v] buffer or a
  * head-major one is covered by strides.  out may be x with the same strides.
- * positions: device int32 [rows], any value.  Angles are reduced exactly
- * (64-bit fixed-point turns), so far positions lose nothing; the products
+ * positions: device int32 [rows], any value.  A rate is computed in 64-bit
+ * floating point and its angle reduced by whole turns in fixed point, so that an angle is
+ * off by at most |position| * f_i * 2^-49 radians for theta to 1e8 (2^-28 at position 2^21); the products
  * are float32, rounded once.  The rates reach the device with the launch:
  * *rope may be reused at once. */
 dllm_status dllm_op_rope(const void* x, void* out, const int32_t* positions, int32_t rows, int32_t heads, int32_t hd,

@@ -3,6 +3,7 @@
 Tolerances count roundings: half a step is 2^-8 of the value in bf16.
 """
 import math
+from decimal import Decimal, getcontext
 
 import numpy as np
 import pytest
@@ -216,3 +217,19 @@ def test_ramps_that_end_past_the_last_pair(torch, rot, theta, orig_len, factor):
     # cosines to 8 float32 roundings; angles of up to 2^22 to some 2^-51 of themselves on both sides
     np.testing.assert_allclose(c, np.cos(a), rtol=0, atol=2.0 ** -20)
     np.testing.assert_allclose(s, np.sin(a), rtol=0, atol=2.0 ** -20)
+
+
+@pytest.mark.parametrize("rot", [128, 96])
+@pytest.mark.parametrize("theta", [1e4, 5e5, 1e8])
+def test_far_angles_are_off_by_what_the_header_says(torch, theta, rot):
+    """|position| * rate * 2^-49 radians, and the cosine's float32 roundings."""
+    getcontext().prec = 60
+    pos = [1, -7, 99999, 2 ** 24 + 1, 123456789, 2 ** 31 - 1, -2 ** 31]
+    c, s = turn(torch, binding.make_rope(rot, theta=theta), rot, pos)
+    two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+    for i in range(rot // 2):
+        f = (Decimal(theta).ln() * Decimal(-2 * i) / rot).exp()
+        for j, n in enumerate(pos):
+            a = float((Decimal(n) * f) % two_pi)
+            tol = abs(n) * float(f) * 2.0 ** -49 + 4 * 2.0 ** -24
+            assert abs(c[j, i] - math.cos(a)) <= tol and abs(s[j, i] - math.sin(a)) <= tol
