@@ -567,7 +567,8 @@ dllm_status dllm_op_kv8_load(const dllm_kv8* cache, void* k, void* v, int64_t k_
  * statistics and sums are float32; a probability enters the value product
  * with 8 significant bits (an error of 2^-8 of itself, or of 2^-21 of the
  * largest p * 2^ev of its row among 32 neighbouring keys where that is more).
- * scale: > 0, at most 1e30.  workspace: device memory for the partial results of
+ * scale: > 0, at most 1e30.  Scores are formed in float32 from the codes and their
+ * scales apart: elements of q and of K, and scale times either, stay within 2^100.  workspace: device memory for the partial results of
  * split keys, 16-byte aligned, at least dllm_op_attention_kv8_workspace
  * bytes (0: may be NULL), contents irrelevant; calls that may run at the same
  * time need one each. */

@@ -182,6 +182,28 @@ def test_cache_rows_past_32_bits_of_elements(torch, hd):
         assert (r[0, 0] == 1.0 + w).all() and (r[0, -1] == 5.0 + w).all() and (r[0, 1:-1] == 0).all()
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("R", [1, 32, 64, 100, 200])
+@pytest.mark.parametrize("e,scale_e", [(96, 0), (-96, 0), (0, 96), (-48, 90), (20, -60)])
+def test_scores_of_large_and_small_factors(torch, R, hd, e, scale_e):
+    """Queries times 2^e, keys by 2^(-e - scale_e), the scale times 2^scale_e: the same scores, to the ends of the
+    ranges in the header."""
+    rng = np.random.default_rng(21)
+    T, h = 300, 2
+    q = rng.standard_normal((1, R, h, hd))
+    kc, ks = ref.quantise(rng.standard_normal((1, h, T, hd)))
+    vc, vs = ref.quantise(rng.standard_normal((1, h, T, hd)))
+    scale = float(np.float32(hd ** -0.5))
+    qt = dev(torch, q).bfloat16()
+    out = attend(torch, (qt.double() * 2.0 ** e).bfloat16(), *[dev(torch, a) for a in
+                 (kc, (ks.astype(int) - e - scale_e).astype(np.uint8), vc, vs)], scale * 2.0 ** scale_e)
+    want, pv, sk = ref.attention(qt.double().cpu().numpy()[0], ref.dequantise(kc, ks)[0], ref.dequantise(vc, vs)[0], [T] * R,
+                                 scale)
+    # a score's float32 sum of hd products, exp2 and the sums 2^-20; bf16 probabilities and output, 2^-8 each
+    tol = (2.0 ** -8 + 2.0 ** -20 + 2 * hd * 2.0 ** -24 * sk) * pv + 2.0 ** -8 * np.abs(want)
+    assert (np.abs(out.double().cpu().numpy()[0] - want) <= tol).all()
+
+
 # --------------------------------------------------------------------------- rotary positions
 
 def turn(torch, spec, rot, pos, layout="half"):
