@@ -2,10 +2,10 @@
 // block, grouped heads): the codes go from HBM to the tensor cores untouched.
 //
 // Keys are the 128-row operand.  A tile of 128 keys gives
-//   S^T[key][row] = K Q^T          (kind::f8f6f4, e4m3 x e4m3)
+//   S^T[key][row] = K Q^T          (kind::mxf8f6f4, the rows' scales as block scales)
 //   O^T[dim][row] += V^T P^T       (kind::mxf8f6f4, V read MN-major from its TMA tile)
-// with N = 16, 32 or 64 rows as the narrow operand, so the products cost N / 128
-// of a 128-row tile's and the kernel is bound by the codes it reads: 2 (hd + 1)
+// with N = 8, 16, 32 or 64 rows as the narrow operand (8: hi and lo codes side by side in
+// one of 16), so the products cost N / 128 of a 128-row tile's and the kernel is bound by the codes it reads: 2 (hd + 1)
 // bytes a key and cached head.
 //
 // 8 bits lose nothing on the query side: a bf16 q scaled by a power of two to at

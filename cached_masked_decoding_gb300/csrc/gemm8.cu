@@ -102,8 +102,8 @@ struct Gemm8Cfg {
 // memory and the block-scaled tcgen05.mma applies them, so blocks accumulate
 // in one float32 accumulator.  A CTA computes a share of one tile's K; the
 // `split` CTAs of a cluster share a tile and join their partial tiles through
-// distributed shared memory in rank order.  Bound by HBM: 24576 x 4096 weights, 32 rows, 20 us
-// with the quantiser's launch, 5.3 TB/s; 4096 x 4096, one row, 6.3 us.
+// distributed shared memory in rank order.  Bound by HBM, on the GPU with the quantiser's launch:
+// 24576 x 4096 weights, 32 rows, 20 us, 5.3 TB/s; 4096 x 4096, one row, 6.3 us.
 //   warp 0     TMA: weight and activation codes
 //   warp 1     scale copies and MMAs, issued by one lane
 //   warps 2-5  epilogue
