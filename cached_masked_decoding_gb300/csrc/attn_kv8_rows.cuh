@@ -35,7 +35,7 @@
 // alone 1.1 us; what a batch loses is starts, ends and the last CTAs alone.  hd 128: one
 // token of 32 sequences, 4096 keys, 32 heads on 8: 37 us, 5.5 TB/s; of 8 sequences, up to
 // 8193 keys: 24 us, 4.4 TB/s; 32 rows of 16 sequences of 32 heads, up to 2048 keys: 52 us,
-// 4.1 TB/s; 32 rows of one sequence, 768 keys: 9.7 us.
+// 4.1 TB/s; 32 rows of one sequence, 768 keys: 9.9 us.
 //
 //   warp 0     TMA: K and V tiles through a ring of 128-key slots
 //   warp 1     scale copies and MMAs, issued by one lane
