@@ -77,6 +77,13 @@ class Kv8(ctypes.Structure):
                 ("T", ctypes.c_int32), ("hd", ctypes.c_int32)]
 
 
+class KvPaged(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p), ("b", ctypes.c_int32),
+                ("H_kv", ctypes.c_int32), ("hd", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 # int32 (*)(void* user, int32 event, int32 block_idx, int32 step_in_block)
@@ -129,6 +136,16 @@ SIGNATURES = {
     "dllm_op_kv8_store": (_I32, [ctypes.POINTER(Kv8), _P, _P, _I64, _I64, _I32, _I32, _P, _P, _P]),
     "dllm_op_kv8_load": (_I32, [ctypes.POINTER(Kv8), _P, _P, _I64, _I64, _I32, _I32, _P, _P, _P]),
     "dllm_op_attention_kv8": (_I32, [_P, _I64, ctypes.POINTER(Kv8), _P, _F, _P, _I64, _I32, _I32, _P, _I64, _P]),
+    "dllm_op_qk_norm_rope": (_I32, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I32, _I32, _I32, _I32, _I32, _I32, _P,
+                                    _P, _F, ctypes.POINTER(Rope), _P]),
+    "dllm_op_qk_norm_rope_paged": (_I32, [ctypes.POINTER(KvPaged), _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _I32,
+                                          _I32, _P, _P, _P, _P, _P, _F, ctypes.POINTER(Rope), _P]),
+    "dllm_op_attention_paged": (_I32, [_P, _I64, ctypes.POINTER(KvPaged), _P, _F, _P, _I64, _I32, _I32, _P, _I64, _P,
+                                       _I64, _P]),
+    "dllm_op_attention_paged_workspace": (_I32, [_I32, _I32, _I32, _I32, _I32, _I32, _I32, ctypes.POINTER(_I64)]),
+    "dllm_op_kv_paged_evict": (_I32, [ctypes.POINTER(KvPaged), ctypes.POINTER(KvPaged), _P, _I64, _P, _I32, _I32,
+                                      _I32, _P, _P, _P, _I64, _P]),
+    "dllm_op_token_logprobs": (_I32, [_P, _I64, _I32, _I32, _I32, _F, _P, _P, _P, _I32, _P, _P, _P]),
     "dllm_op_attention_kv8_workspace": (_I32, [_I32, _I32, _I32, _I32, _I32, _I32, ctypes.POINTER(_I64)]),
     "dllm_op_quantise8": (_I32, [_P, _I64, _I32, _I32, _I32, _P, _P, _P]),
     "dllm_op_gemm8": (_I32, [_P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _P]),
@@ -510,3 +527,66 @@ def op_quantise8(x_ptr: int, dtype: str, rows: int, K: int, codes_ptr: int, scal
 def op_gemm8(W_ptr: int, W_scale_ptr: int, X_ptr: int, X_scale_ptr: int, Y_ptr: int, y_dtype: str, M: int, N: int,
              K: int, stream: int = 0):
     check(lib().dllm_op_gemm8(W_ptr, W_scale_ptr, X_ptr, X_scale_ptr, Y_ptr, DTYPES[y_dtype], M, N, K, stream))
+
+
+# ------------------------------------------------------------------ paged decoding
+
+def make_kv_paged(k_ptr: int, v_ptr: int, table_ptr: int, b: int, H_kv: int, hd: int, dtype: str, pages: int,
+                  page_size: int, max_pages: int) -> KvPaged:
+    """A paged cache over the caller's device memory: K and V [pages][H_kv][page_size][hd],
+    table int32 [b][max_pages]."""
+    return KvPaged(k_ptr, v_ptr, table_ptr, b, H_kv, hd, DTYPES[dtype], pages, page_size, max_pages, 0)
+
+
+def op_qk_norm_rope(q_ptr: int, k_ptr: int, q_out_ptr: int, k_out_ptr: int, positions_ptr: int, rows: int, H: int,
+                    H_kv: int, hd: int, dtype: str, out_dtype: str | None = None, q_weight_ptr: int = 0,
+                    k_weight_ptr: int = 0, eps: float = 1e-6, rope: Rope | None = None, q_row_stride: int = 0,
+                    k_row_stride: int = 0, q_out_row_stride: int = 0, k_out_row_stride: int = 0, stream: int = 0):
+    """out_dtype None takes dtype; eps < 0: no norm; rope None: nothing turns."""
+    check(lib().dllm_op_qk_norm_rope(q_ptr, q_row_stride, k_ptr, k_row_stride, q_out_ptr, q_out_row_stride, k_out_ptr,
+                                     k_out_row_stride, positions_ptr, rows, H, H_kv, hd, DTYPES[dtype],
+                                     DTYPES[out_dtype or dtype], q_weight_ptr, k_weight_ptr, eps, rope, stream))
+
+
+def op_qk_norm_rope_paged(cache: KvPaged, q_ptr: int, k_ptr: int, v_ptr: int, q_out_ptr: int, H: int, R: int,
+                          dtype: str, starts_ptr: int = 0, counts_ptr: int = 0, positions_ptr: int = 0,
+                          q_weight_ptr: int = 0, k_weight_ptr: int = 0, eps: float = 1e-6, rope: Rope | None = None,
+                          q_row_stride: int = 0, k_row_stride: int = 0, v_row_stride: int = 0,
+                          q_out_row_stride: int = 0, stream: int = 0):
+    """eps < 0: no norm; rope None: nothing turns."""
+    check(lib().dllm_op_qk_norm_rope_paged(cache, q_ptr, q_row_stride, k_ptr, k_row_stride, v_ptr, v_row_stride,
+                                           q_out_ptr, q_out_row_stride, H, R, DTYPES[dtype], starts_ptr, counts_ptr,
+                                           positions_ptr, q_weight_ptr, k_weight_ptr, eps, rope, stream))
+
+
+def attention_paged_workspace(b: int, H: int, H_kv: int, hd: int, R: int, T: int, mass: bool = False) -> int:
+    """Bytes of device workspace op_attention_paged needs for this shape on the current device; T: the positions that
+    a sequence's table row holds."""
+    n = ctypes.c_int64()
+    check(lib().dllm_op_attention_paged_workspace(b, H, H_kv, hd, R, T, 1 if mass else 0, ctypes.byref(n)))
+    return n.value
+
+
+def op_attention_paged(q_ptr: int, cache: KvPaged, out_ptr: int, H: int, R: int, lens_ptr: int = 0,
+                       scale: float | None = None, mass_ptr: int = 0, mass_stride: int = 0, ws_ptr: int = 0,
+                       ws_bytes: int = 0, q_row_stride: int = 0, out_row_stride: int = 0, stream: int = 0):
+    """scale None takes 1/sqrt(hd); mass_stride 0 takes what the table holds."""
+    check(lib().dllm_op_attention_paged(q_ptr, q_row_stride, cache, lens_ptr,
+                                        cache.hd ** -0.5 if scale is None else scale, out_ptr, out_row_stride, H, R,
+                                        mass_ptr, mass_stride, ws_ptr, ws_bytes, stream))
+
+
+def op_kv_paged_evict(src: KvPaged, dst: KvPaged, mass_ptr: int, keep: int, kept_ptr: int, new_lens_ptr: int,
+                      lens_ptr: int = 0, sinks: int = 0, recent: int = 0, mass_stride: int = 0,
+                      mass_out_ptr: int = 0, mass_out_stride: int = 0, stream: int = 0):
+    """mass_stride 0 takes what src's table holds, mass_out_stride 0 takes keep."""
+    check(lib().dllm_op_kv_paged_evict(src, dst, mass_ptr, mass_stride, lens_ptr, keep, sinks, recent, kept_ptr,
+                                       new_lens_ptr, mass_out_ptr, mass_out_stride, stream))
+
+
+def op_token_logprobs(logits_ptr: int, dtype: str, rows: int, vocab: int, targets_ptr: int = 0,
+                      logprobs_ptr: int = 0, entropy_ptr: int = 0, top: int = 0, top_ids_ptr: int = 0,
+                      top_logprobs_ptr: int = 0, inv_temperature: float = 1.0, row_stride: int = 0, stream: int = 0):
+    check(lib().dllm_op_token_logprobs(logits_ptr, row_stride, DTYPES[dtype], rows, vocab, inv_temperature,
+                                       targets_ptr, logprobs_ptr, entropy_ptr, top, top_ids_ptr, top_logprobs_ptr,
+                                       stream))

@@ -19,10 +19,9 @@
 #include "ops8.h"
 #include "ptx8.cuh"
 #include "q8.cuh"
+#include "rope.cuh"
 
 namespace dllm {
-
-constexpr int kMaxPairs = 128;
 
 struct RopeParams {
   const void* x;
@@ -35,20 +34,6 @@ struct RopeParams {
   float amp;
   uint64_t turns[kMaxPairs];   // turns per position * 2^64
 };
-
-__device__ __forceinline__ void turn_cos_sin(uint64_t turns, int pos, float amp, float& c, float& s) {
-  const uint64_t t = turns * (uint64_t)(int64_t)pos;          // fraction of a turn, exact modulo 1
-  const uint32_t quarter = (uint32_t)((t + (1ull << 61)) >> 62);
-  const int64_t r = (int64_t)(t - ((uint64_t)quarter << 62));  // within an eighth of a turn of the quarter
-  float cr, sr;
-  sincospif((float)r * 0x1p-63f, &sr, &cr);
-  c = (quarter & 1) ? sr : cr;
-  s = (quarter & 1) ? cr : sr;
-  if (quarter == 1 || quarter == 2) c = -c;
-  if (quarter >= 2) s = -s;
-  c *= amp;
-  s *= amp;
-}
 
 // VEC: 8 pairs (16 elements) a thread in 16-byte accesses; else one pair.
 template <typename E, bool VEC>
@@ -143,6 +128,52 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeP
   }
 }
 
+dllm_status rope_turns(const dllm_rope* r, int hd, uint64_t* turns, float* amp_out) {
+  if (r->rot_dim < 2 || r->rot_dim % 2 || r->rot_dim > hd || r->rot_dim > 2 * kMaxPairs || r->layout < 0 ||
+      r->layout > 1 || r->scaling < 0 || r->scaling > 3 || !(r->theta >= 1.0) || !std::isfinite(r->theta) ||
+      !std::isfinite(r->amplitude) || r->amplitude < 0.0)
+    return op_fail(DLLM_EINVAL,
+                   "bad rope: rot_dim=%d (even, 2..min(hd, 256)) layout=%d scaling=%d theta=%g (>= 1) amplitude=%g",
+                   r->rot_dim, r->layout, r->scaling, r->theta, r->amplitude);
+  if (r->scaling != DLLM_ROPE_UNSCALED && (!(r->factor >= 1.0) || !std::isfinite(r->factor)))
+    return op_fail(DLLM_EINVAL, "bad rope factor %g (>= 1)", r->factor);
+  if (r->scaling == DLLM_ROPE_BASE && r->rot_dim < 4)
+    return op_fail(DLLM_EINVAL, "rope base scaling needs rot_dim >= 4, got %d", r->rot_dim);
+  if (r->scaling == DLLM_ROPE_BY_PARTS &&
+      (!(r->orig_len >= 1.0) || !std::isfinite(r->orig_len) || !(r->beta_slow > 0.0) ||
+       !(r->beta_fast >= r->beta_slow) || !std::isfinite(r->beta_fast) || !(r->theta > 1.0)))
+    return op_fail(DLLM_EINVAL, "bad rope by parts: orig_len=%g beta_fast=%g beta_slow=%g theta=%g", r->orig_len,
+                   r->beta_fast, r->beta_slow, r->theta);
+  // turning rates in 64 bits
+  const int rot = r->rot_dim, pairs = rot / 2;
+  double theta = r->theta, amp = 1.0, lo = 0.0, hi = 0.0;
+  if (r->scaling == DLLM_ROPE_BASE) theta *= std::pow(r->factor, rot / (rot - 2.0));
+  if (r->scaling == DLLM_ROPE_BY_PARTS) {
+    const double k = rot / (2.0 * std::log(theta)), turn = 2.0 * 3.14159265358979323846;
+    // (the ramp may end past the last pair, for long original contexts)
+    lo = std::fmax(0.0, std::floor(k * std::log(r->orig_len / (r->beta_fast * turn))));
+    hi = std::fmin(rot - 1.0, std::ceil(k * std::log(r->orig_len / (r->beta_slow * turn))));
+    amp = 0.1 * std::log(r->factor) + 1.0;
+  }
+  *amp_out = (float)(r->amplitude > 0.0 ? r->amplitude : amp);
+  // theta^(-2i/rot) as the product of a power for i's upper and one for its lower
+  // three bits: 24 powers at most in place of 128 on the calling thread
+  double lower[8], upper = 1.0;
+  for (int i = 0; i < std::min(pairs, 8); ++i) lower[i] = std::pow(theta, -2.0 * i / rot);
+  for (int i = 0; i < pairs; ++i) {
+    if (i % 8 == 0) upper = std::pow(theta, -2.0 * i / rot);
+    double f = upper * lower[i % 8];
+    if (r->scaling == DLLM_ROPE_LINEAR) f /= r->factor;
+    if (r->scaling == DLLM_ROPE_BY_PARTS) {
+      const double ramp = std::fmin(1.0, std::fmax(0.0, (i - lo) / std::fmax(hi - lo, 0.001)));
+      f = f / r->factor * ramp + f * (1.0 - ramp);
+    }
+    // f <= 1 (a rounding above it at most), so the turns per position stay under 0.16: 2^64 of them fit
+    turns[i] = (uint64_t)(f * 0.15915494309189533577 * 0x1p64);
+  }
+  return DLLM_OK;
+}
+
 namespace {
 
 // Rows and heads of a strided [rows][heads][hd] array do not overlap: heads
@@ -172,21 +203,6 @@ extern "C" dllm_status dllm_op_rope(const void* x, void* out, const int32_t* pos
                    dtype);
   if (!op_aligned(x, es) || !op_aligned(out, es) || !op_aligned(positions, 4))
     return op_fail(DLLM_EINVAL, "rope: x, out and positions must be aligned to their elements");
-  if (r->rot_dim < 2 || r->rot_dim % 2 || r->rot_dim > hd || r->rot_dim > 2 * kMaxPairs || r->layout < 0 ||
-      r->layout > 1 || r->scaling < 0 || r->scaling > 3 || !(r->theta >= 1.0) || !std::isfinite(r->theta) ||
-      !std::isfinite(r->amplitude) || r->amplitude < 0.0)
-    return op_fail(DLLM_EINVAL,
-                   "bad rope: rot_dim=%d (even, 2..min(hd, 256)) layout=%d scaling=%d theta=%g (>= 1) amplitude=%g",
-                   r->rot_dim, r->layout, r->scaling, r->theta, r->amplitude);
-  if (r->scaling != DLLM_ROPE_UNSCALED && (!(r->factor >= 1.0) || !std::isfinite(r->factor)))
-    return op_fail(DLLM_EINVAL, "bad rope factor %g (>= 1)", r->factor);
-  if (r->scaling == DLLM_ROPE_BASE && r->rot_dim < 4)
-    return op_fail(DLLM_EINVAL, "rope base scaling needs rot_dim >= 4, got %d", r->rot_dim);
-  if (r->scaling == DLLM_ROPE_BY_PARTS &&
-      (!(r->orig_len >= 1.0) || !std::isfinite(r->orig_len) || !(r->beta_slow > 0.0) ||
-       !(r->beta_fast >= r->beta_slow) || !std::isfinite(r->beta_fast) || !(r->theta > 1.0)))
-    return op_fail(DLLM_EINVAL, "bad rope by parts: orig_len=%g beta_fast=%g beta_slow=%g theta=%g", r->orig_len,
-                   r->beta_fast, r->beta_slow, r->theta);
   const int64_t most = int64_t(1) << 31;   // rows, heads and strides of 31 bits: offsets stay in 64
   if (x_row_stride < 0 || x_row_stride > most || x_head_stride < 0 || x_head_stride > most || out_row_stride < 0 ||
       out_row_stride > most || out_head_stride < 0 || out_head_stride > most)
@@ -197,6 +213,7 @@ extern "C" dllm_status dllm_op_rope(const void* x, void* out, const int32_t* pos
   p.x = x;
   p.out = out;
   p.pos = positions;
+  if (const dllm_status st = rope_turns(r, hd, p.turns, &p.amp); st != DLLM_OK) return st;
   p.heads = heads;
   p.rot = r->rot_dim;
   p.interleaved = r->layout == DLLM_ROPE_INTERLEAVED;
@@ -209,34 +226,6 @@ extern "C" dllm_status dllm_op_rope(const void* x, void* out, const int32_t* pos
                    p.o_rs, p.o_hs);
   if (x == out && (p.x_rs != p.o_rs || p.x_hs != p.o_hs))
     return op_fail(DLLM_EINVAL, "rope in place needs the same strides on both sides");
-
-  // turning rates in 64 bits
-  const int pairs = p.rot / 2;
-  double theta = r->theta, amp = 1.0, lo = 0.0, hi = 0.0;
-  if (r->scaling == DLLM_ROPE_BASE) theta *= std::pow(r->factor, p.rot / (p.rot - 2.0));
-  if (r->scaling == DLLM_ROPE_BY_PARTS) {
-    const double k = p.rot / (2.0 * std::log(theta)), turn = 2.0 * 3.14159265358979323846;
-    // (the ramp may end past the last pair, for long original contexts)
-    lo = std::fmax(0.0, std::floor(k * std::log(r->orig_len / (r->beta_fast * turn))));
-    hi = std::fmin(p.rot - 1.0, std::ceil(k * std::log(r->orig_len / (r->beta_slow * turn))));
-    amp = 0.1 * std::log(r->factor) + 1.0;
-  }
-  p.amp = (float)(r->amplitude > 0.0 ? r->amplitude : amp);
-  // theta^(-2i/rot) as the product of a power for i's upper and one for its lower
-  // three bits: 24 powers at most in place of 128 on the calling thread
-  double lower[8], upper = 1.0;
-  for (int i = 0; i < std::min(pairs, 8); ++i) lower[i] = std::pow(theta, -2.0 * i / p.rot);
-  for (int i = 0; i < pairs; ++i) {
-    if (i % 8 == 0) upper = std::pow(theta, -2.0 * i / p.rot);
-    double f = upper * lower[i % 8];
-    if (r->scaling == DLLM_ROPE_LINEAR) f /= r->factor;
-    if (r->scaling == DLLM_ROPE_BY_PARTS) {
-      const double ramp = std::fmin(1.0, std::fmax(0.0, (i - lo) / std::fmax(hi - lo, 0.001)));
-      f = f / r->factor * ramp + f * (1.0 - ramp);
-    }
-    // f <= 1 (a rounding above it at most), so the turns per position stay under 0.16: 2^64 of them fit
-    p.turns[i] = (uint64_t)(f * 0.15915494309189533577 * 0x1p64);
-  }
 
   // 16-byte accesses: units of 8 pairs that do not straddle the turned part,
   // and vectors that start on 16 bytes in every row and head

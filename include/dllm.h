@@ -594,6 +594,142 @@ dllm_status dllm_op_quantise8(const void* x, int64_t row_stride, int32_t dtype, 
 dllm_status dllm_op_gemm8(const uint8_t* W, const uint8_t* W_scale, const uint8_t* X, const uint8_t* X_scale, void* Y,
                           int32_t y_dtype, int32_t M, int32_t N, int32_t K, void* cuda_stream);
 
+/* ------------------------------------------------------------ paged decoding
+ *
+ * What a decode step over sequences of different lengths does around its
+ * products, on a cache whose pages lie anywhere in a pool:
+ * dllm_op_qk_norm_rope_paged (head norms, positions, the cache's new rows),
+ * dllm_op_attention_paged (attention over the pages, and the weight that each
+ * key received), dllm_op_kv_paged_evict (the heaviest keys to new pages) and
+ * dllm_op_token_logprobs (what the logits say).  As the 8-bit forms they
+ * allocate nothing, keep nothing between calls and can be captured into a CUDA
+ * graph; calls on different streams do not disturb one another as long as
+ * their outputs and workspaces differ.  Device pointers belong to the current
+ * device, and so does the stream.  Outputs do not overlap inputs unless the
+ * text says so.  The pages this library follows have no counterpart: their
+ * cache is one canvas. */
+
+/* A paged K/V cache in the caller's device memory.  A page holds page_size
+ * positions of every cached head: k, v [pages][H_kv][page_size][hd] of dtype
+ * (bf16 or f16), 16-byte aligned, hd in {64, 128}, page_size a power of two,
+ * 16..256.  table: device int32 [b][max_pages]; position t of sequence s lies
+ * on page table[s][t / page_size], slot t % page_size.  Entries past a
+ * sequence's last page are never read.  An entry outside [0, pages) is no page:
+ * nothing is written there, and its positions hold no key.  A sequence has at
+ * most max_pages * page_size positions (at most 2^31 - 4096 in all).  Sequences
+ * may share pages that are only read.  The struct is read during the call. */
+typedef struct dllm_kv_paged {
+    void *k, *v;
+    const int32_t* table;
+    int32_t b, H_kv, hd, dtype;
+    int32_t pages, page_size, max_pages, reserved;
+} dllm_kv_paged;
+
+/* Head norms and rotary positions in one pass: for every row and head x of q
+ * (H heads) and k (H_kv heads)
+ *   y = x / sqrt(mean(x^2) + eps) * weight,  then y's pairs turned as in
+ * dllm_op_rope; float32, rounded once (the angle's error as there).
+ * q: [rows][H][hd], k: [rows][H_kv][hd] of dtype, outputs of out_dtype: dtype,
+ * or bf16 / f16 from float32.  Rows are *_row_stride elements apart (0: dense;
+ * else at least the row and a multiple of 16 bytes): one [rows][q|k|v] buffer
+ * is covered.  Everything 16-byte aligned.  hd a multiple of 16, 16..256.
+ * q_weight, k_weight: [hd] of dtype, NULL: ones; eps >= 0; eps < 0: no norm
+ * (both weights NULL).  rope: NULL: nothing turns (positions may be NULL);
+ * rot_dim a multiple of 16.  positions: device int32 [rows].  An output may be
+ * its input with the same strides and type. */
+dllm_status dllm_op_qk_norm_rope(const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride, void* q_out,
+                                 int64_t q_out_row_stride, void* k_out, int64_t k_out_row_stride,
+                                 const int32_t* positions, int32_t rows, int32_t H, int32_t H_kv, int32_t hd,
+                                 int32_t dtype, int32_t out_dtype, const void* q_weight, const void* k_weight,
+                                 float eps, const dllm_rope* rope, void* cuda_stream);
+
+/* The same with k, and v as it is, going to their places in the cache: q, k, v
+ * [b*R] rows of H, H_kv and H_kv heads, of dtype (the cache's, or float32);
+ * q_out of the cache's type.  Row i of sequence s goes to position
+ * starts[s] + i for i < counts[s] (device int32 [b]; NULL starts: 0, NULL
+ * counts: R).  positions: device int32 [b*R], what q and k turn by, or NULL:
+ * starts[s] + i.  Rows from counts[s] on, and rows whose position in the cache
+ * lies outside the table or on no page, take no part: their q_out and every
+ * other slot stay as they were.  With rope NULL and eps < 0 it stores rows as
+ * they are.  No two rows of a call may go to one slot. */
+dllm_status dllm_op_qk_norm_rope_paged(const dllm_kv_paged* cache, const void* q, int64_t q_row_stride, const void* k,
+                                       int64_t k_row_stride, const void* v, int64_t v_row_stride, void* q_out,
+                                       int64_t q_out_row_stride, int32_t H, int32_t R, int32_t dtype,
+                                       const int32_t* starts, const int32_t* counts, const int32_t* positions,
+                                       const void* q_weight, const void* k_weight, float eps, const dllm_rope* rope,
+                                       void* cuda_stream);
+
+/* Attention over the pages: for sequence s, row i, head h
+ *   out[s*R+i][h] = sum_t p_t V[s][g][t],  p = softmax_t(scale * q . K[s][g][t]),
+ * over t < lens[s] (device int32 [b]; NULL, or more than the table holds: all
+ * it holds), g = h / (H / H_kv) (grouped heads; H a multiple of H_kv).  R = 1
+ * is single-token decoding; the R rows of a block see the same keys, each
+ * other's among them once these are stored.  (Rows that see different keys are
+ * sequences of their own, whose table rows name the same pages.)  A sequence of
+ * lens <= 0 gives zeros.  What lies at or past lens[s], or on no page, is not
+ * used, whatever its bytes.  q, out: of the cache's type, [b*R][H][hd], 16-byte
+ * aligned, rows q_row_stride / out_row_stride elements apart (0: dense; else a
+ * multiple of 8).  scale: > 0, finite.  Scores, statistics and sums are float32; a probability
+ * enters the value product as the sum of two halves of the cache's type (16
+ * bits of it in bf16).  K, V and q are finite, and so are the scores.
+ *   mass (nullable): device float32 [b][H_kv][mass_stride], mass_stride at
+ * least max_pages * page_size or the largest of lens;
+ * mass[s][g][t] += the sum of p_t over the R rows and the heads of g, for
+ * t < lens[s]; the rest stays as it was.  In a fixed order: the same inputs
+ * give the same bits.
+ *   workspace: device memory, 16-byte aligned, of at least
+ * dllm_op_attention_paged_workspace bytes for the same shape on the current
+ * device (T = max_pages * page_size, with_mass: whether mass is given; 0: may
+ * be NULL), contents irrelevant; calls that may run at the same time need one
+ * each. */
+dllm_status dllm_op_attention_paged(const void* q, int64_t q_row_stride, const dllm_kv_paged* cache,
+                                    const int32_t* lens, float scale, void* out, int64_t out_row_stride, int32_t H,
+                                    int32_t R, float* mass, int64_t mass_stride, void* workspace,
+                                    int64_t workspace_bytes, void* cuda_stream);
+dllm_status dllm_op_attention_paged_workspace(int32_t b, int32_t H, int32_t H_kv, int32_t hd, int32_t R, int32_t T,
+                                              int32_t with_mass, int64_t* bytes);
+
+/* Eviction by accumulated weight: of the n = lens[s] positions of every
+ * sequence s and cached head g, keep m = min(n, keep) and copy their K and V rows,
+ * in the order of their positions, to positions 0..m-1 of dst.  All n are kept
+ * when n <= keep; else the first `sinks`, the last `recent`, and of the others
+ * the keep - sinks - recent of largest mass[s][g][t] (ties: the lowest
+ * position; a NaN counts as less than every number).  src and dst: of the same b, H_kv, hd and
+ * dtype, page sizes of their own; dst's pages are not among src's (they may lie
+ * in the same pool), and its table holds at least keep positions.
+ *   lens: device int32 [b]; NULL, or more than src's table holds: all it holds.
+ *   mass: device float32 [b][H_kv][mass_stride], mass_stride >= the largest of lens.
+ *   kept: device int32 [b][H_kv][keep], the positions kept, ascending, -1 from m on.
+ *   new_lens: device int32 [b], m.
+ *   mass_out (nullable): device float32 [b][H_kv][mass_out_stride],
+ *   mass_out_stride >= keep: the weights of the kept, its other elements stay as they were.
+ * A kept position that lies on no page gives a row of zeros.
+ * keep >= 1, sinks, recent >= 0, sinks + recent <= keep. */
+dllm_status dllm_op_kv_paged_evict(const dllm_kv_paged* src, const dllm_kv_paged* dst, const float* mass,
+                                   int64_t mass_stride, const int32_t* lens, int32_t keep, int32_t sinks,
+                                   int32_t recent, int32_t* kept, int32_t* new_lens, float* mass_out,
+                                   int64_t mass_out_stride, void* cuda_stream);
+
+/* What rows of logits say: with z = inv_temperature * logits[r] and
+ * log p_i = z_i - log sum_j exp z_j,
+ *   logprobs[r] = log p at targets[r] (NaN for a target outside [0, vocab)),
+ *   entropy[r]  = -sum_i p_i log p_i (in nats),
+ *   top_ids[r][0..top), top_logprobs[r][0..top): the largest logits, ties the
+ *   lowest id first, and their log p.
+ * logits: device [rows][vocab] of dtype, rows row_stride elements apart (0:
+ * vocab; else >= vocab), aligned to their elements.  targets: device int32
+ * [rows], goes with logprobs; every output may be NULL, top_ids and
+ * top_logprobs are given together when top > 0; top <= 64 and <= vocab.
+ * inv_temperature: > 0, finite.  Sums are float32, taken apart from the largest
+ * term, so that log p and entropy of a nearly certain row keep their relative
+ * accuracy.  A logit of -inf is a token that cannot come: p = 0, and an
+ * alternative only after all others.  A row with a NaN or +inf, or of nothing
+ * but -inf, has NaN for every log p and entropy; a NaN is no alternative (id -1 where there are
+ * too few others). */
+dllm_status dllm_op_token_logprobs(const void* logits, int64_t row_stride, int32_t dtype, int32_t rows, int32_t vocab,
+                                   float inv_temperature, const int32_t* targets, float* logprobs, float* entropy,
+                                   int32_t top, int32_t* top_ids, float* top_logprobs, void* cuda_stream);
+
 /* Cache staleness diagnostics for block block_idx of the current canvas (the
  * Fast-dLLM notes, section 14, Algorithm 4 steps 4-5: compare fresh and
  * cached representations and predictions at the positions about to be
