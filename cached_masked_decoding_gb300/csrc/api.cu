@@ -2591,9 +2591,10 @@ extern "C" dllm_status dllm_op_check(int32_t* site, void* stream) {
   int dev = 0;
   CK(cudaGetDevice(&dev));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // error words: the library's workspace, the no-alloc scratch, the 8-bit kernels
-  int* word[4] = {};
-  int code_of[4] = {};
+  // error words: the library's workspace, the no-alloc scratch, the 8-bit kernels, the paged attention
+  constexpr int kWords = 5;
+  int* word[kWords] = {};
+  int code_of[kWords] = {};
   {
     std::lock_guard<std::mutex> lk(g_op_mu);
     auto it = g_op_ws.find(dev);
@@ -2604,7 +2605,8 @@ extern "C" dllm_status dllm_op_check(int32_t* site, void* stream) {
   word[1] = sc.err;
   CK(gemm8_err_word(&word[2]));
   CK(attn_kv8_err_word(&word[3]));
-  for (int i = 0; i < 4; ++i)
+  CK(attn_paged_err_word(&word[4]));
+  for (int i = 0; i < kWords; ++i)
     if (word[i]) CK(cudaMemcpyAsync(&code_of[i], word[i], 4, cudaMemcpyDeviceToHost, st));
   CK(cudaStreamSynchronize(st));
   for (int* w : word)

@@ -1,124 +1,80 @@
 // Attention over a paged K/V cache:
 //   out[s, i, h] = sum_t p_t V[s, g, t],  p = softmax over t < len[s] of scale * q[s, i, h] . K[s, g, t],
-// g = h / (H / H_kv), and the weight that every key received, summed over the rows and heads of g.
-//
-// One CTA a (sequence, cached head); its rows eight at a time over tiles of 128 keys, a key a thread for the
-// scores and a dimension a thread for the values.
+// g = h / (H / H_kv), and the weight that every key received, summed over the rows and heads of g.  The kernels are
+// in attn_paged.cuh; here is what runs, and on what.
 #include <algorithm>
 #include <cmath>
 
-#include "kv_paged.h"
-#include "ptx8.cuh"
-#include "q8.cuh"
+#include "attn_paged.cuh"
 
 namespace dllm {
 
-struct AttnPagedParams {
-  PagedKv c;
-  const uint16_t* q;
-  uint16_t* out;
-  const int32_t* lens;
-  long long q_rs, o_rs, mass_rs;
-  float* mass;
-  int H, R, group, rows;     // rows: R * group of a cached head
-  float scale_log2;
+cudaError_t attn_paged_err_word(int** p) { return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_attn_paged_err); }
+
+namespace {
+
+struct AttnPagedPlan {
+  int N, row_tiles, whole, ctas, nz;
+  long long items, tiles;     // tiles: of an item, at most
+  size_t o, ml, plan, lse, z, bytes;
 };
 
-template <typename E, int HD>
-__global__ void __launch_bounds__(128) attn_paged_simple_kernel(const __grid_constant__ AttnPagedParams p) {
-  constexpr int N = 8, KT = 128;
-  __shared__ float s_q[N][HD], s_p[N][KT], s_red[N][4], s_m[N], s_l[N], s_up[N];
-  const int s = blockIdx.x / p.c.H_kv, g = blockIdx.x % p.c.H_kv, tid = threadIdx.x;
-  griddep_wait();
-  const int n = p.c.len(p.lens, s);
-  using T = typename E::T;
-  for (int r0 = 0; r0 < p.rows; r0 += N) {
-    const int nr = min(N, p.rows - r0);
-    __syncthreads();
-    for (int e = tid; e < N * HD; e += 128) {
-      const int r = r0 + e / HD;
-      s_q[e / HD][e % HD] =
-          r < p.rows ? E::get(reinterpret_cast<const T*>(p.q) + ((long long)s * p.R + r / p.group) * p.q_rs +
-                              (long long)(g * p.group + r % p.group) * HD + e % HD) : 0.0f;
-    }
-    if (tid < N) {
-      s_m[tid] = -INFINITY;
-      s_l[tid] = 0.0f;
-    }
-    float o[N] = {};
-    __syncthreads();
-    auto scores = [&](int key, float (&z)[N]) {
-      const long long at = key < n ? p.c.row(s, g, key) : -1;
-#pragma unroll
-      for (int j = 0; j < N; ++j) z[j] = at < 0 ? -INFINITY : 0.0f;
-      if (at < 0) return;
-      for (int d = 0; d < HD; d += 8) {
-        float x[8];
-        E::load8(reinterpret_cast<const T*>(p.c.k) + at + d, x);
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) z[j] += x[e] * s_q[j][d + e];
-      }
-#pragma unroll
-      for (int j = 0; j < N; ++j) z[j] *= p.scale_log2;
-    };
-    for (int t0 = 0; t0 < n; t0 += KT) {
-      float z[N];
-      scores(t0 + tid, z);
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        float m = z[j];
-        for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        if (tid % 32 == 0) s_red[j][tid / 32] = m;
-      }
-      __syncthreads();
-      if (tid < N) {
-        const float m = fmaxf(fmaxf(s_red[tid][0], s_red[tid][1]), fmaxf(s_red[tid][2], s_red[tid][3]));
-        const float top = fmaxf(m, s_m[tid]);
-        s_up[tid] = top == -INFINITY ? 1.0f : exp2f(s_m[tid] - top);
-        s_m[tid] = top;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const float e = z[j] == -INFINITY ? 0.0f : exp2f(z[j] - s_m[j]);
-        s_p[j][tid] = e;
-        float sum = e;
-        for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (tid % 32 == 0) s_red[j][tid / 32] = sum;
-        o[j] *= s_up[j];
-      }
-      __syncthreads();
-      if (tid < N) s_l[tid] = s_l[tid] * s_up[tid] + (s_red[tid][0] + s_red[tid][1]) + (s_red[tid][2] + s_red[tid][3]);
-      if (tid < HD)
-        for (int k = 0; k < min(KT, n - t0); ++k) {
-          const long long at = p.c.row(s, g, t0 + k);
-          if (at < 0) continue;
-          const float v = E::get(reinterpret_cast<const T*>(p.c.v) + at + tid);
-#pragma unroll
-          for (int j = 0; j < N; ++j) o[j] += s_p[j][k] * v;
-        }
-      __syncthreads();
-    }
-    if (tid < HD)
-      for (int j = 0; j < nr; ++j) {
-        const int r = r0 + j;
-        E::put(reinterpret_cast<T*>(p.out) + ((long long)s * p.R + r / p.group) * p.o_rs +
-                   (long long)(g * p.group + r % p.group) * HD + tid,
-               s_l[j] == 0.0f ? 0.0f : o[j] / s_l[j]);
-      }
-    if (p.mass)
-      for (int t = tid; t < n; t += KT) {
-        float z[N], sum = 0.0f;
-        scores(t, z);
-        for (int j = 0; j < nr; ++j)
-          if (z[j] != -INFINITY) sum += exp2f(z[j] - s_m[j]) / s_l[j];
-        if (t < p.mass_rs) p.mass[((long long)s * p.c.H_kv + g) * p.mass_rs + t] += sum;
-      }
+AttnPagedPlan plan_attn_paged(long long b, long long H_kv, long long rows, int hd, long long T, bool mass) {
+  AttnPagedPlan a = {};
+  a.N = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  a.row_tiles = (int)((rows + a.N - 1) / a.N);
+  a.items = b * H_kv * a.row_tiles;
+  a.tiles = std::max(1LL, (T + kPagedKeys - 1) / kPagedKeys);
+  a.ctas = op_device_sms();
+  a.whole = a.tiles <= 2;
+  a.nz = (int)std::min<long long>((rows + 3) / 4 * 4, a.N);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t from = at;
+    at += (bytes + 15) / 16 * 16;
+    return from;
+  };
+  a.o = take(a.whole ? 0 : (size_t)2 * a.ctas * a.N * hd * 4);
+  a.ml = take(a.whole ? 0 : (size_t)2 * a.ctas * a.N * 8);
+  a.plan = take(a.whole ? 0 : (size_t)a.items * 8);
+  a.lse = take(mass ? (size_t)a.items * a.N * 4 : 0);
+  a.z = take(mass ? (size_t)a.items * a.tiles * kPagedKeys * a.nz * 4 : 0);
+  a.bytes = at;
+  return a;
+}
+
+template <typename F, int HD, int N>
+cudaError_t launch_attn_paged(const CUtensorMap& tk, const CUtensorMap& tv, const AttnPagedParams& p,
+                              const AttnPagedPlan& a, cudaStream_t st) {
+  using C = AttnPagedCfg<HD, N>;
+  cudaError_t e = op_smem_once(reinterpret_cast<const void*>(attn_paged_kernel<F, HD, N>), C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  const long long units = a.whole ? a.items : a.items * a.tiles;
+  const unsigned grid = (unsigned)std::min<long long>(a.ctas, (units + p.min_share - 1) / p.min_share);
+  e = op_launch(attn_paged_kernel<F, HD, N>, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, st, 1, tk, tv, p);
+  if (e != cudaSuccess) return e;
+  if (!a.whole) {
+    e = op_launch(attn_paged_join_kernel<F, HD>, dim3((unsigned)a.items, (unsigned)std::min(N, p.rows)), dim3(128), 0, st,
+                  1, p, N);
+    if (e != cudaSuccess) return e;
+  }
+  if (!p.mass) return cudaSuccess;
+  return op_launch(attn_paged_mass_kernel, dim3((unsigned)((long long)p.c.b * p.c.H_kv * p.by_chunks.d)), dim3(256), 0, st,
+                   1, p, N);
+}
+
+template <typename F, int HD>
+cudaError_t launch_attn_paged(const CUtensorMap& tk, const CUtensorMap& tv, const AttnPagedParams& p,
+                              const AttnPagedPlan& a, cudaStream_t st) {
+  switch (a.N) {
+    case 8: return launch_attn_paged<F, HD, 8>(tk, tv, p, a, st);
+    case 16: return launch_attn_paged<F, HD, 16>(tk, tv, p, a, st);
+    case 32: return launch_attn_paged<F, HD, 32>(tk, tv, p, a, st);
+    default: return launch_attn_paged<F, HD, 64>(tk, tv, p, a, st);
   }
 }
 
+}  // namespace
 }  // namespace dllm
 
 using namespace dllm;
@@ -129,8 +85,10 @@ extern "C" dllm_status dllm_op_attention_paged_workspace(int32_t b, int32_t H, i
     return op_fail(DLLM_EINVAL, "bad attention shape: b=%d H=%d H_kv=%d hd=%d R=%d T=%d", b, H, H_kv, hd, R, T);
   if ((__int128)b * R * H > 0x7fffffff)
     return op_fail(DLLM_EINVAL, "attention_paged: b=%d R=%d H=%d are too many rows", b, R, H);
-  (void)with_mass;
-  *bytes = 0;
+  const AttnPagedPlan a = plan_attn_paged(b, H_kv, (long long)R * (H / H_kv), hd, T, with_mass != 0);
+  if (a.items > 0x7fffffff || (double)a.items * (double)a.tiles > 1e11)
+    return op_fail(DLLM_EINVAL, "attention_paged: b=%d R=%d H=%d T=%d are too many keys for one call", b, R, H, T);
+  *bytes = (int64_t)a.bytes;
   return DLLM_OK;
 }
 
@@ -174,14 +132,40 @@ extern "C" dllm_status dllm_op_attention_paged(const void* q, int64_t q_row_stri
     return op_fail(DLLM_EINVAL, "attention_paged: a 16-byte aligned workspace of %lld bytes is needed, got %lld",
                    (long long)need, workspace ? (long long)workspace_bytes : 0LL);
   p.rows = R * p.group;
-  const dim3 grid((unsigned)(cache->b * cache->H_kv));
+  const AttnPagedPlan a = plan_attn_paged(cache->b, cache->H_kv, p.rows, cache->hd, p.c.positions, mass != nullptr);
+  p.row_tiles = a.row_tiles;
+  p.per_seq = cache->H_kv * a.row_tiles;
+  p.whole = a.whole;
+  p.min_share = a.whole ? 1 : 2;
+  p.by_group = FastDiv((uint32_t)p.group);
+  p.by_tiles = FastDiv((uint32_t)a.row_tiles);
+  p.by_chunks = FastDiv((uint32_t)((p.c.positions + 255) / 256));
+  p.nz = a.nz;
+  p.z_tiles = (int)a.tiles;
+  if (mass && (double)cache->b * cache->H_kv * p.by_chunks.d > 0x7fffffff)
+    return op_fail(DLLM_EINVAL, "attention_paged: b=%d H_kv=%d of %lld positions are too many weights for one call", cache->b,
+                   cache->H_kv, p.c.positions);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.ws_o = reinterpret_cast<float*>(ws + a.o);
+  p.ws_ml = reinterpret_cast<float*>(ws + a.ml);
+  p.ws_plan = reinterpret_cast<int2*>(ws + a.plan);
+  p.ws_lse = reinterpret_cast<float*>(ws + a.lse);
+  p.ws_z = reinterpret_cast<float*>(ws + a.z);
+  // bytes of a page's cached head: rows of hd * 2, in boxes of 128
+  const uint64_t row = (uint64_t)cache->hd * 2, plane = row * cache->page_size;
+  const uint32_t box = (uint32_t)std::min(cache->page_size, kPagedKeys);
+  CUtensorMap tk, tv;
+  for (int i = 0; i < 2; ++i)
+    if (const dllm_status s = op_map_u8(i ? &tv : &tk, i ? cache->v : cache->k, row, cache->page_size,
+                                        (uint64_t)cache->pages * cache->H_kv, row, plane, 128, box);
+        s != DLLM_OK)
+      return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool bf = cache->dtype == DLLM_BF16;
-  if (cache->hd == 64)
-    OP_CK(bf ? op_launch(attn_paged_simple_kernel<ElemBf16, 64>, grid, dim3(128), 0, st, 1, p)
-             : op_launch(attn_paged_simple_kernel<ElemF16, 64>, grid, dim3(128), 0, st, 1, p));
+  if (cache->dtype == DLLM_BF16)
+    OP_CK((cache->hd == 64 ? launch_attn_paged<PairBf16, 64>(tk, tv, p, a, st)
+                           : launch_attn_paged<PairBf16, 128>(tk, tv, p, a, st)));
   else
-    OP_CK(bf ? op_launch(attn_paged_simple_kernel<ElemBf16, 128>, grid, dim3(128), 0, st, 1, p)
-             : op_launch(attn_paged_simple_kernel<ElemF16, 128>, grid, dim3(128), 0, st, 1, p));
+    OP_CK((cache->hd == 64 ? launch_attn_paged<PairF16, 64>(tk, tv, p, a, st)
+                           : launch_attn_paged<PairF16, 128>(tk, tv, p, a, st)));
   return DLLM_OK;
 }

@@ -1,0 +1,730 @@
+// Attention over a paged cache for few query rows a cached head (a token, a block, grouped heads).
+//
+// Keys are the 128-row operand, so K and V go from HBM to the tensor cores as they are.  A tile of 128 keys gives
+//   S^T[key][row] = K Q^T,      O^T[dim][row] += V^T P^T        (tcgen05, kind::f16)
+// with N = 8, 16, 32 or 64 rows as the narrow operand (8: in products of 16 columns).  V is read MN-major from its
+// TMA tile.  A probability is the sum of two values of the cache's type, hi and lo, each a product of its own into
+// one sum (8 rows: the two side by side in 16 columns): one rounding of P to bf16 alone is as large an error as the
+// output's own rounding.
+//
+// Bound by HBM: 4 hd bytes a key and cached head.  So the work is shared out evenly whatever the lengths: one CTA an
+// SM takes an equal run of tiles of the (sequence, cached head, row tile) items laid end to end, and its ring of TMA
+// tiles runs on across the items' borders.  An item that lies in several CTAs leaves its parts - normalised outputs
+// with their reference m and sum l - in the workspace, and a second small kernel joins them.
+//
+// Softmax runs with one key a thread and RW rows in its registers.  A row's reference is the maximum over the first
+// tile of the CTA's part; it follows when a score exceeds it by 2^20 (2^12 in f16, whose probabilities end at 65504),
+// which one vote a tile finds out; else the warps meet at no barrier.  Sums l are kept per key lane and joined once a
+// part.
+//
+//   warp 0     TMA: the pages of a tile, a lane each, K and V through a ring of 128-key slots
+//   warp 1     MMAs, issued by one lane: scores two tiles ahead of the products, across items too
+//   warps 2..  softmax, one key and RW rows a thread; the next item's query tile; the output
+//
+// Positions at or past a sequence's length, or on no page, are not loaded (or come with a page's other rows): their
+// scores are taken as -inf and their V rows zeroed in shared memory, so that whatever bytes lie there meet no product.
+#pragma once
+
+#include "gemm.cuh"
+#include "kv_paged.h"
+#include "ptx8.cuh"
+#include "q8.cuh"
+
+namespace dllm {
+
+struct AttnPagedParams {
+  PagedKv c;
+  const uint16_t* q;
+  uint16_t* out;
+  const int32_t* lens;
+  long long q_rs, o_rs, mass_rs;
+  float* mass;
+  int H, R, group, rows;      // rows: R * group of a cached head, in row_tiles tiles of N
+  int row_tiles, per_seq;     // per_seq: items of a sequence, H_kv * row_tiles
+  int min_share, whole;       // tiles a CTA takes at least; whole: items are not split
+  FastDiv by_group, by_tiles; // by_tiles: by row_tiles
+  FastDiv by_chunks;          // by the 256-key chunks of a table
+  float scale_log2;
+  int nz, z_tiles;            // scores kept for the weights: [item][z_tiles][128][nz]
+  float *ws_o, *ws_ml, *ws_lse, *ws_z;   // [2 * CTAs][N][hd], [2 * CTAs][N][2], [item][N]
+  int2* ws_plan;              // [item] first and last CTA's slot of a split item, or -1
+};
+
+static __device__ int g_attn_paged_err[1];
+
+constexpr int kPagedKeys = 128;
+
+struct PairBf16 {
+  using E = ElemBf16;
+  static constexpr uint32_t kFormat = 1;
+  static constexpr float kSlack = 20.0f;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+};
+struct PairF16 {
+  using E = ElemF16;
+  static constexpr uint32_t kFormat = 0;
+  static constexpr float kSlack = 12.0f;
+  static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack_f16x2(a, b); }
+  static __device__ __forceinline__ float2 unpack(uint32_t w) { return f16x2_to_f32(w); }
+};
+
+template <int HD, int N>
+struct AttnPagedCfg {
+  static constexpr int KT = kPagedKeys;
+  static constexpr int RW = N <= 16 ? 8 : 16;           // rows of a softmax thread
+  static constexpr int WGS = N / RW;                    // groups of four softmax warps
+  static constexpr int SOFT = 128 * WGS;                // softmax threads
+  static constexpr int THREADS = 64 + SOFT;
+  static constexpr int SLOT = KT * HD * 2;              // one K or V tile: HD / 64 parts of 128 keys x 128 bytes
+  static constexpr int NP = N < 16 ? 16 : N;            // columns of a product
+  static constexpr int Q_BYTES = NP * HD * 2;           // HD / 64 parts of NP rows x 128 bytes
+  static constexpr int P_ROW = 2 * NP;                  // a key's probabilities (8 rows: hi, then lo)
+  static constexpr int P_PARTS = N < 16 ? 1 : 2;
+  static constexpr int P_BYTES = KT * P_ROW;            // one part
+  static constexpr int P_BUFS = N == 64 ? 1 : 2;
+  // warp maxima (4), m, rise, sums of the warps (4), places (2 buffers of 64 bits)
+  static constexpr int STAT_FLOATS = 4 * N + 2 * N + 4 * N + 4 * N;
+  static constexpr int FIXED = 1024 + 2 * Q_BYTES + P_BUFS * P_PARTS * P_BYTES + STAT_FLOATS * 4 + 512;
+  static constexpr int MOST = (232448 - FIXED) / SLOT;
+  static constexpr int SLOTS = MOST > 12 ? 12 : MOST;
+  static constexpr int SMEM_BYTES = FIXED + SLOTS * SLOT;
+  static constexpr int S_COL = 0;                       // two buffers of NP
+  static constexpr int O_COL = 2 * NP;                  // NP (8 rows: hi and lo products)
+  static constexpr int TMEM_COLS = 3 * NP <= 64 ? 64 : 3 * NP <= 128 ? 128 : 256;
+  static_assert(SLOTS >= 4 && SMEM_BYTES <= 232448 && 3 * NP <= TMEM_COLS, "shared and tensor memory");
+};
+
+// 2^x; results below the normal range are 0
+__device__ __forceinline__ float pow2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Order-preserving map of a float's bits to a signed integer, and back.
+__device__ __forceinline__ int order_of(float x) {
+  const int b = __float_as_int(x);
+  return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float of_order(int o) { return __int_as_float(o ^ ((o >> 31) & 0x7fffffff)); }
+
+// A sequence's tiles: one at least, so that every item is somebody's.
+__device__ __forceinline__ int paged_tiles(int n) { return max(1, (n + kPagedKeys - 1) / kPagedKeys); }
+
+// The parts of a CTA's run of tiles, one item after the other; every role walks them by itself.
+struct PagedWalk {
+  int s, item, t0, nt, n, left, next_n, part;   // part: counts up
+  __device__ __forceinline__ PagedWalk(const AttnPagedParams& p, int s_, int item_, int t0_, int total)
+      : s(s_), item(item_), t0(t0_), nt(0), left(total), part(0) {
+    n = p.c.len(p.lens, s);
+    next_n = s + 1 < p.c.b ? p.c.len(p.lens, s + 1) : 0;
+    take();
+  }
+  __device__ __forceinline__ void take() {
+    nt = min(paged_tiles(n) - t0, left);
+    left -= nt;
+  }
+  // false: that was the last one
+  __device__ __forceinline__ bool next(const AttnPagedParams& p) {
+    if (left <= 0) return false;
+    ++part;
+    if (++item == p.per_seq) {
+      item = 0;
+      ++s;
+      n = next_n;
+      next_n = s + 1 < p.c.b ? p.c.len(p.lens, s + 1) : 0;
+    }
+    t0 = 0;
+    take();
+    return true;
+  }
+  __device__ __forceinline__ bool complete() const { return t0 == 0 && nt == paged_tiles(n); }
+};
+
+template <typename F, int HD, int N>
+__global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, 1)
+    attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const __grid_constant__ AttnPagedParams p) {
+  using C = AttnPagedCfg<HD, N>;
+  using T = typename F::E::T;
+  constexpr int KT = C::KT, RW = C::RW, PARTS = HD / 64;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sKV = smem;
+  uint8_t* sQ = sKV + C::SLOTS * C::SLOT;               // two buffers
+  uint8_t* sP = sQ + 2 * C::Q_BYTES;                    // buffers of hi, lo
+  long long* s_to = reinterpret_cast<long long*>(sP + C::P_BUFS * C::P_PARTS * C::P_BYTES);   // [2][N] where a row goes
+  float* s_wmax = reinterpret_cast<float*>(s_to + 2 * N);   // [4][N]
+  float* s_m = s_wmax + 4 * N;                          // [N] references
+  float* s_up = s_m + N;                                // [N] their rise
+  float* s_ls = s_up + N;                               // [4][N] the warps' sums
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_ls + 4 * N);
+  uint64_t* empty = full + C::SLOTS;
+  uint64_t* qready = empty + C::SLOTS;                  // [2]
+  uint64_t* sfull = qready + 2;                         // [2]
+  uint64_t* sfree = sfull + 2;                          // [2]
+  uint64_t* pready = sfree + 2;                         // [2]
+  uint64_t* pvdone = pready + 2;                        // [2]
+  uint64_t* mdone = pvdone + 2;                         // every MMA is done
+  int* s_plan = reinterpret_cast<int*>(mdone + 1);      // first sequence, item, tile, and how many tiles
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_plan + 5);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* err = g_attn_paged_err;
+
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::SLOTS; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&qready[s], C::SOFT / 32);
+      mbar_init(&sfull[s], 1);
+      mbar_init(&sfree[s], C::SOFT / 32);
+      mbar_init(&pready[s], C::SOFT / 32);
+      mbar_init(&pvdone[s], 1);
+    }
+    mbar_init(mdone, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  if constexpr (N < 16) {   // the columns past the rows: queries of zero
+    for (int e = threadIdx.x; e < 2 * C::Q_BYTES / 16; e += C::THREADS) reinterpret_cast<uint4*>(sQ)[e] = make_uint4(0, 0, 0, 0);
+  }
+  griddep_wait();
+  // this CTA's run of tiles
+  if (warp == 0) {
+    long long sum = 0;
+    for (int s0 = 0; s0 < p.c.b; s0 += 32) {
+      int t = s0 + lane < p.c.b ? (p.whole ? 1 : paged_tiles(p.c.len(p.lens, s0 + lane))) : 0;
+      sum += __reduce_add_sync(0xffffffffu, t);
+    }
+    // (whole: the units are items)
+    const long long units = sum * p.per_seq;
+    const long long share = max((units + gridDim.x - 1) / gridDim.x, (long long)p.min_share);
+    const long long first = min(units, share * blockIdx.x), last = min(units, first + share);
+    long long base = 0;
+    int s_at = 0, item = 0, t0 = 0;
+    long long total = last - first;
+    for (int s0 = 0; s0 < p.c.b && total > 0; s0 += 32) {
+      const int t = s0 + lane < p.c.b ? (p.whole ? 1 : paged_tiles(p.c.len(p.lens, s0 + lane))) : 0;
+      int upto = t;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += v;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, base + (long long)upto * p.per_seq > first);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        const int before = __shfl_sync(0xffffffffu, upto - t, l), tl = __shfl_sync(0xffffffffu, t, l);
+        const long long in = first - base - (long long)before * p.per_seq;
+        s_at = s0 + l;
+        item = (int)(in / tl);
+        t0 = (int)(in - (long long)item * tl);
+        break;
+      }
+      base += (long long)__shfl_sync(0xffffffffu, upto, 31) * p.per_seq;
+    }
+    if (p.whole && total > 0) {   // items to tiles
+      long long tiles = 0;
+      int s = s_at, it = item;
+      for (long long left = total; left > 0;) {
+        const int here = (int)min((long long)(p.per_seq - it), left);
+        tiles += (long long)here * paged_tiles(p.c.len(p.lens, s));
+        left -= here;
+        it = 0;
+        ++s;
+      }
+      total = tiles;
+    }
+    if (lane == 0) {
+      s_plan[0] = s_at;
+      s_plan[1] = item;
+      s_plan[2] = t0;
+      s_plan[3] = (int)total;
+      s_plan[4] = (int)min(share, 0x7fffffffLL);
+    }
+  }
+  fence_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_launch_dependents();                          // not before: a dependent could take the columns awaited
+  const int total = s_plan[3];
+
+  if (total > 0) {
+    PagedWalk w(p, s_plan[0], s_plan[1], s_plan[2], total);
+    if (warp == 0) {
+      // ------------------------------------------------------ pages to the ring
+      const uint64_t pol = p.row_tiles > 1 ? policy_evict_last() : policy_evict_first();
+      const int box = min(1 << p.c.page_shift, KT), boxes = KT / box;
+      int u = 0;                                          // ring position
+      bool ok = true;
+      do {
+        const int g = (int)p.by_tiles.div((uint32_t)w.item);
+        const int32_t* table = p.c.table + (long long)w.s * p.c.max_pages;
+        auto page_of = [&](int t) {
+          const int at = t * KT + lane * box;
+          return lane < boxes && t < w.t0 + w.nt && at < w.n ? table[at >> p.c.page_shift] : -1;
+        };
+        int page = page_of(w.t0);
+        for (int t = w.t0; t < w.t0 + w.nt && ok; ++t) {
+          const int next = page_of(t + 1);
+          const bool there = (unsigned)page < (unsigned)p.c.pages;
+          const int y = (t * KT + lane * box) & ((1 << p.c.page_shift) - 1), z = page * p.c.H_kv + g;
+          const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, there)) * box) * (HD * 2);
+#pragma unroll
+          for (int v = 0; v < 2; ++v, ++u) {
+            const int slot = u % C::SLOTS;
+            if (u >= C::SLOTS &&
+                !__all_sync(0xffffffffu, mbar_wait_long(&empty[slot], (uint32_t)(u / C::SLOTS - 1) & 1u, abort_flag, err,
+                                                        ERR_ATTN_FULL))) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
+            __syncwarp();
+            if (there) {
+#pragma unroll
+              for (int h = 0; h < PARTS; ++h)
+                tma_load_3d(sKV + slot * C::SLOT + h * (KT * 128) + lane * box * 128, v ? &tmV : &tmK, &full[slot], h * 128,
+                            y, z, pol);
+            }
+          }
+          page = next;
+        }
+      } while (ok && w.next(p));
+      if (*abort_flag)   // let copies in flight land before the CTA's shared memory goes away
+        for (int k = max(u - C::SLOTS, 0); k < u; ++k)
+          mbar_wait_long(&full[k % C::SLOTS], (uint32_t)(k / C::SLOTS) & 1u, nullptr, err, ERR_ATTN_FULL);
+    } else if (warp == 1) {
+      // ------------------------------------------------------ products
+      const uint32_t lead = elect_one();
+      auto wait = [&](uint64_t* bar, int phase) {
+        return __all_sync(0xffffffffu, mbar_wait_long(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
+      };
+      constexpr uint32_t idesc = (1u << 4) | (F::kFormat << 7) | (F::kFormat << 10) | ((uint32_t)(C::NP >> 3) << 17) |
+                                 ((128u >> 4) << 24);
+      constexpr uint32_t idesc_o = idesc | (1u << 15) | (1u << 16);     // V and P MN-major
+      const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV), p0 = smem_u32(sP);
+      PagedWalk ws = w;                                   // the scores' part, two tiles ahead
+      int s_left = ws.nt, o_left = w.nt;
+      bool s_new = true, o_new = true;
+      auto issue_s = [&](int t) {
+        if (s_left == 0) {
+          ws.next(p);
+          s_left = ws.nt;
+          s_new = true;
+        }
+        --s_left;
+        const int u = 2 * t, slot = u % C::SLOTS, sb = t & 1;
+        if (s_new && !wait(&qready[ws.part & 1], ws.part >> 1)) return false;
+        s_new = false;
+        if (!wait(&full[slot], u / C::SLOTS) || (t >= 2 && !wait(&sfree[sb], (t >> 1) - 1))) return false;
+        tc_fence_after();
+        const uint32_t k = kv0 + slot * C::SLOT, q = q0 + (ws.part & 1) * C::Q_BYTES, d = tmem + C::S_COL + sb * C::NP;
+#pragma unroll
+        for (int h = 0; h < PARTS; ++h)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_ss(lead, d, sdesc_rows<128>(k + h * (KT * 128) + kk * 32),
+                       sdesc_rows<128>(q + h * (C::NP * 128) + kk * 32), idesc, (h > 0 || kk > 0) ? 1u : 0u);
+        mma_commit_lead(lead, &empty[slot]);
+        mma_commit_lead(lead, &sfull[sb]);
+        return true;
+      };
+      bool ok = issue_s(0) && (total < 2 || issue_s(1));
+      for (int t = 0; t < total && ok; ++t) {
+        if (o_left == 0) {
+          w.next(p);
+          o_left = w.nt;
+          o_new = true;
+        }
+        --o_left;
+        const int u = 2 * t + 1, slot = u % C::SLOTS, pb = C::P_BUFS == 2 ? t & 1 : 0;
+        if (!(ok = wait(&pready[t & 1], t >> 1) && wait(&full[slot], u / C::SLOTS))) break;
+        tc_fence_after();
+        const uint32_t v = kv0 + slot * C::SLOT, pp = p0 + pb * (C::P_PARTS * C::P_BYTES);
+#pragma unroll
+        for (int part = 0; part < C::P_PARTS; ++part)
+#pragma unroll
+          for (int kk = 0; kk < KT / 16; ++kk)
+            // a 64-wide head fills both halves of the 128 dims: the second repeats the first and is not read
+            mma_f16_ss(lead, tmem + C::O_COL, sdesc_rows<128>(v + kk * 2048, HD == 64 ? 0 : KT * 128),
+                       sdesc_rows<C::P_ROW>(pp + part * C::P_BYTES + kk * 16 * C::P_ROW), idesc_o,
+                       (!o_new || part > 0 || kk > 0) ? 1u : 0u);
+        o_new = false;
+        mma_commit_lead(lead, &empty[slot]);
+        mma_commit_lead(lead, &pvdone[t & 1]);
+        if (t + 2 < total && !(ok = issue_s(t + 2))) break;
+      }
+      mma_commit_lead(lead, mdone);
+      mbar_wait_long(mdone, 0u, nullptr, err, ERR_ATTN_FULL);
+    } else {
+      // ------------------------------------------------------ softmax
+      const int tid = (warp - 2) * 32 + lane, q4 = warp & 3, key_l = q4 * 32 + lane;   // this thread's key of a tile
+      const int row0 = ((warp - 2) >> 2) * RW;            // its first row
+      const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
+      constexpr int L = HD / 8, QV = N * L / C::SOFT > 0 ? N * L / C::SOFT : 1;   // lanes of a row; vectors of a thread
+      uint4 qv[QV];
+      // the query tile of a part: its rows' elements on their way, then in place
+      auto q_load = [&](const PagedWalk& x) {
+        uint32_t rt;
+        const int g = (int)p.by_tiles.divmod((uint32_t)x.item, rt);
+#pragma unroll
+        for (int k = 0; k < QV; ++k) {
+          const int e = tid + k * C::SOFT, row = e / L;
+          uint32_t j;
+          const int at = (int)rt * N + row;
+          const uint32_t i = p.by_group.divmod((uint32_t)min(at, p.rows - 1), j);
+          qv[k] = make_uint4(0, 0, 0, 0);
+          if (row < N && at < p.rows)
+            qv[k] = *reinterpret_cast<const uint4*>(p.q + ((long long)x.s * p.R + i) * p.q_rs +
+                                                    (long long)(g * p.group + (int)j) * HD + e % L * 8);
+        }
+      };
+      auto q_store = [&](const PagedWalk& x) {
+        uint32_t rt;
+        const int g = (int)p.by_tiles.divmod((uint32_t)x.item, rt), buf = x.part & 1;
+#pragma unroll
+        for (int k = 0; k < QV; ++k) {
+          const int e = tid + k * C::SOFT, row = e / L, c = e % L;
+          if (row < N)
+            *reinterpret_cast<uint4*>(sQ + buf * C::Q_BYTES + (c >> 3) * (C::NP * 128) + swizzled<128>(row, c & 7)) = qv[k];
+        }
+        if (tid < N) {
+          uint32_t j;
+          const int at = (int)rt * N + tid;
+          const uint32_t i = p.by_group.divmod((uint32_t)min(at, p.rows - 1), j);
+          s_to[buf * N + tid] = ((long long)x.s * p.R + i) * p.o_rs + (long long)(g * p.group + (int)j) * HD;
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&qready[buf]);
+      };
+      q_load(w);
+      q_store(w);
+      bool ok = true, more = true;
+      // after a wait that gave up (ok false) the loop goes on without waiting, so that every warp meets every
+      // barrier; the outputs are invalid and reported
+      auto wait = [&](uint64_t* bar, int phase) {
+        ok = __all_sync(0xffffffffu, mbar_wait_long(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) && ok;
+      };
+      int tt = 0;                                         // tiles so far
+      while (more) {
+        float l_sum[RW];
+#pragma unroll
+        for (int j = 0; j < RW; ++j) l_sum[j] = 0.0f;
+        const int32_t* table = p.c.table + (long long)w.s * p.c.max_pages;
+        const long long item = (long long)w.s * p.per_seq + w.item;
+        auto page_of = [&](int t) {
+          const int key = t * KT + key_l;
+          return t < w.t0 + w.nt && key < w.n ? table[key >> p.c.page_shift] : -1;
+        };
+        int page = page_of(w.t0);
+        PagedWalk wn = w;
+        more = wn.next(p);
+        if (more) q_load(wn);
+        for (int t = 0; t < w.nt; ++t, ++tt) {
+          const int b = tt & 1, pb = C::P_BUFS == 2 ? b : 0;
+          const bool seen = (unsigned)page < (unsigned)p.c.pages;
+          page = page_of(w.t0 + t + 1);
+          wait(&sfull[b], tt >> 1);
+          tc_fence_after();
+          float z[RW];
+          tmem_ld<RW>(trow + C::S_COL + b * C::NP + row0, z);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sfree[b]);
+#pragma unroll
+          for (int j = 0; j < RW; ++j) z[j] = seen ? z[j] * p.scale_log2 : -INFINITY;
+          if (p.mass) {
+            float* zs = p.ws_z + ((item * p.z_tiles + w.t0 + t) * KT + key_l) * p.nz + row0;
+#pragma unroll
+            for (int j = 0; j < RW; j += 4)
+              if (row0 + j < p.nz) *reinterpret_cast<float4*>(zs + j) = make_float4(z[j], z[j + 1], z[j + 2], z[j + 3]);
+          }
+          float top = -INFINITY;
+          if (t > 0) {
+#pragma unroll
+            for (int j = 0; j < RW; j += 4) {
+              const float4 m = *reinterpret_cast<const float4*>(s_m + row0 + j);
+              z[j] -= m.x;
+              z[j + 1] -= m.y;
+              z[j + 2] -= m.z;
+              z[j + 3] -= m.w;
+            }
+#pragma unroll
+            for (int j = 0; j < RW; ++j) top = fmaxf(top, z[j]);
+          }
+          if (named_bar_or(2, C::SOFT, t == 0 || top > F::kSlack)) {
+            // references: the first tile's, or higher ones
+#pragma unroll
+            for (int j = 0; j < RW; ++j) {
+              const int r = __reduce_max_sync(0xffffffffu, order_of(z[j]));
+              if (lane == j) s_wmax[q4 * N + row0 + j] = of_order(r);
+            }
+            named_bar_sync(2, C::SOFT);
+            if (tid < N) {
+              float up = fmaxf(fmaxf(s_wmax[tid], s_wmax[N + tid]), fmaxf(s_wmax[2 * N + tid], s_wmax[3 * N + tid]));
+              if (!(up > -INFINITY) || (t > 0 && up < 0.0f)) up = 0.0f;
+              s_up[tid] = up;
+              s_m[tid] = t == 0 ? up : s_m[tid] + up;
+            }
+            named_bar_sync(2, C::SOFT);
+#pragma unroll
+            for (int j = 0; j < RW; ++j) z[j] -= s_up[row0 + j];
+            if (t > 0) {
+              wait(&pvdone[(tt - 1) & 1], (tt - 1) >> 1);
+              tc_fence_after();
+              float f[RW], o[RW];
+#pragma unroll
+              for (int j = 0; j < RW; ++j) {
+                f[j] = pow2_approx(-s_up[row0 + j]);
+                l_sum[j] *= f[j];
+              }
+#pragma unroll
+              for (int part = 0; part < (N < 16 ? 2 : 1); ++part) {
+                tmem_ld<RW>(trow + C::O_COL + part * N + row0, o);
+#pragma unroll
+                for (int j = 0; j < RW; ++j) o[j] *= f[j];
+                tmem_st<RW>(trow + C::O_COL + part * N + row0, o);
+              }
+            }
+            // (the maxima are read again only behind the next vote)
+          }
+          if (C::P_BUFS == 1 && tt > 0) wait(&pvdone[(tt - 1) & 1], (tt - 1) >> 1);
+          // With two buffers this one is free: S of this tile was issued behind the product of the tile before the
+          // last, and its commit stands for everything issued before it.
+          uint32_t hi[RW / 2], lo[RW / 2];
+#pragma unroll
+          for (int j = 0; j < RW; j += 2) {
+            const float a = pow2_approx(z[j]), c = pow2_approx(z[j + 1]);
+            l_sum[j] += a;
+            l_sum[j + 1] += c;
+            hi[j >> 1] = F::pack(a, c);
+            const float2 h = F::unpack(hi[j >> 1]);
+            lo[j >> 1] = F::pack(a - h.x, c - h.y);
+          }
+          uint8_t* pp = sP + pb * (C::P_PARTS * C::P_BYTES);
+#pragma unroll
+          for (int j = 0; j < RW; j += 8) {
+            const uint4 h = make_uint4(hi[j / 2], hi[j / 2 + 1], hi[j / 2 + 2], hi[j / 2 + 3]);
+            const uint4 l = make_uint4(lo[j / 2], lo[j / 2 + 1], lo[j / 2 + 2], lo[j / 2 + 3]);
+            *reinterpret_cast<uint4*>(pp + swizzled<C::P_ROW>(key_l, (row0 + j) >> 3)) = h;
+            if constexpr (N < 16)
+              *reinterpret_cast<uint4*>(pp + swizzled<C::P_ROW>(key_l, 1)) = l;
+            else
+              *reinterpret_cast<uint4*>(pp + C::P_BYTES + swizzled<C::P_ROW>(key_l, (row0 + j) >> 3)) = l;
+          }
+          if (row0 == 0 && !__all_sync(0xffffffffu, seen)) {
+            const int u = 2 * tt + 1, slot = u % C::SLOTS;
+            wait(&full[slot], u / C::SLOTS);
+            if (!seen) {
+#pragma unroll
+              for (int h = 0; h < PARTS; ++h)
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                  *reinterpret_cast<uint4*>(sKV + slot * C::SLOT + h * (KT * 128) + key_l * 128 + c * 16) =
+                      make_uint4(0, 0, 0, 0);
+            }
+          }
+          fence_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&pready[b]);
+        }
+        if (more) q_store(wn);
+        // sum RW columns over the warp, lane c (modulo RW) ending with column c, while the last product runs
+#pragma unroll
+        for (int s = RW / 2; s >= 1; s >>= 1) {
+          const bool upper = (lane & s) != 0;
+#pragma unroll
+          for (int i = 0; i < s; ++i) {
+            const float send = upper ? l_sum[i] : l_sum[i + s];
+            const float keep = upper ? l_sum[i + s] : l_sum[i];
+            l_sum[i] = keep + __shfl_xor_sync(0xffffffffu, send, s);
+          }
+        }
+#pragma unroll
+        for (int s = RW; s < 32; s <<= 1) l_sum[0] += __shfl_xor_sync(0xffffffffu, l_sum[0], s);
+        if (lane < RW) s_ls[q4 * N + row0 + lane] = l_sum[0];
+        named_bar_sync(2, C::SOFT);
+        // ------------------------------------------------------ the part's output
+        const bool complete = w.complete();
+        const int n_rows = min(N, p.rows - (w.item - (int)p.by_tiles.div((uint32_t)w.item) * p.row_tiles) * N);
+        const int slot = 2 * blockIdx.x + (w.part > 0 ? 1 : 0);
+        if (tid < N) {
+          const float l = (s_ls[tid] + s_ls[N + tid]) + (s_ls[2 * N + tid] + s_ls[3 * N + tid]);
+          if (!complete)
+            *reinterpret_cast<float2*>(p.ws_ml + ((long long)slot * N + tid) * 2) = make_float2(s_m[tid], l);
+          else if (p.mass)
+            p.ws_lse[item * N + tid] = l == 0.0f ? INFINITY : s_m[tid] + log2f(l);
+          s_up[tid] = l == 0.0f ? 0.0f : 1.0f / l;
+        }
+        if (tid == 0 && w.t0 == 0 && !p.whole) {
+          // where the item's other parts lie: CTAs that follow, each with `share` tiles
+          int2 plan = make_int2(-1, -1);
+          if (!complete) {
+            const int rest = paged_tiles(w.n) - w.nt, share = s_plan[4];
+            plan = make_int2(slot, 2 * ((int)blockIdx.x + (rest + share - 1) / share));
+          }
+          p.ws_plan[item] = plan;
+        }
+        named_bar_sync(2, C::SOFT);
+        wait(&pvdone[(tt - 1) & 1], (tt - 1) >> 1);
+        tc_fence_after();
+        const int dim = q4 * 32 + lane;
+        const long long* to = s_to + (w.part & 1) * N;
+#pragma unroll
+        for (int n = 0; n < RW; n += 8) {
+          float o[8];
+          if constexpr (N < 16) {
+            float o2[8];
+            tmem_ld8x2(trow + C::O_COL, trow + C::O_COL + N, o, o2);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] += o2[j];
+          } else {
+            tmem_ld8(trow + C::O_COL + row0 + n, o);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int r = row0 + n + j;
+            const float f = s_up[r], v = f == 0.0f ? 0.0f : o[j] * f;
+            if (dim < HD && r < n_rows) {
+              if (complete)
+                F::E::put(reinterpret_cast<T*>(p.out) + to[r] + dim, v);
+              else
+                p.ws_o[((long long)slot * N + r) * HD + dim] = v;
+            }
+          }
+        }
+        tc_fence_before();
+        if (more) w = wn;
+      }
+    }
+  }
+  // lanes that skipped their role arrive here first: reconverge before the CTA-wide barrier
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Joins the parts of split items: weights l 2^m over their sum (l is 1 at least, 2^51 at most, and m the part's
+// reference: what a weight loses to underflow is nothing beside the largest).  A CTA a row; its warps share the parts.
+template <typename F, int HD>
+__global__ void __launch_bounds__(128) attn_paged_join_kernel(const __grid_constant__ AttnPagedParams p, int N) {
+  __shared__ float s_o[4][HD], s_w[4];
+  const long long item = blockIdx.x;
+  const int r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int2 plan = p.ws_plan[item];
+  const int s = (int)(item / p.per_seq);
+  uint32_t rt, j;
+  const int g = (int)p.by_tiles.divmod((uint32_t)(item - (long long)s * p.per_seq), rt);
+  if (plan.x < 0 || (int)rt * N + r >= p.rows) return;
+  // slots: the first CTA's, then every following one's first
+  const int parts = (plan.y >> 1) - (plan.x >> 1) + 1;
+  auto slot_of = [&](int k) { return k == 0 ? plan.x : ((plan.x >> 1) + k) * 2; };
+  float M = -INFINITY;
+  for (int k = lane; k < parts; k += 32) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + ((long long)slot_of(k) * N + r) * 2);
+    if (ml.y != 0.0f) M = fmaxf(M, ml.x);
+  }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  constexpr int D = HD / 32;
+  float o[D] = {}, sum = 0.0f;
+  for (int k0 = warp; k0 < parts; k0 += 16) {
+    // four parts' outputs at once
+    float2 ml[4];
+    float v[4][D];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const long long at = (long long)slot_of(min(k0 + 4 * e, parts - 1)) * N + r;
+      ml[e] = *reinterpret_cast<const float2*>(p.ws_ml + at * 2);
+      const float* src = p.ws_o + at * HD + lane * D;
+      if constexpr (D == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(src);
+        v[e][0] = f.x;
+        v[e][1] = f.y;
+        v[e][2] = f.z;
+        v[e][3] = f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(src);
+        v[e][0] = f.x;
+        v[e][1] = f.y;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (k0 + 4 * e >= parts || ml[e].y == 0.0f) continue;
+      const float wk = ml[e].y * exp2f(ml[e].x - M);
+      sum += wk;
+#pragma unroll
+      for (int d = 0; d < D; ++d) o[d] += wk * v[e][d];
+    }
+  }
+#pragma unroll
+  for (int d = 0; d < D; ++d) s_o[warp][lane * D + d] = o[d];
+  if (lane == 0) s_w[warp] = sum;
+  __syncthreads();
+  sum = (s_w[0] + s_w[1]) + (s_w[2] + s_w[3]);
+  if (threadIdx.x == 0 && p.mass) p.ws_lse[item * N + r] = sum == 0.0f ? INFINITY : M + log2f(sum);
+  if (threadIdx.x >= HD) return;
+  const float v = (s_o[0][threadIdx.x] + s_o[1][threadIdx.x]) + (s_o[2][threadIdx.x] + s_o[3][threadIdx.x]);
+  const uint32_t i = p.by_group.divmod(rt * (uint32_t)N + (uint32_t)r, j);
+  F::E::put(reinterpret_cast<typename F::E::T*>(p.out) + ((long long)s * p.R + i) * p.o_rs +
+                (long long)(g * p.group + (int)j) * HD + threadIdx.x,
+            sum == 0.0f ? 0.0f : v / sum);
+}
+
+// Adds what every key received: the rows' probabilities from their scores (base 2) and log sums.  A thread a key.
+static __global__ void __launch_bounds__(256) attn_paged_mass_kernel(const __grid_constant__ AttnPagedParams p, int N) {
+  __shared__ float s_lse[64];
+  griddep_launch_dependents();
+  griddep_wait();
+  uint32_t chunk;
+  const int plane = (int)p.by_chunks.divmod(blockIdx.x, chunk), s = plane / p.c.H_kv, g = plane % p.c.H_kv;
+  const int n = (int)min((long long)p.c.len(p.lens, s), p.mass_rs);
+  const int t = (int)(chunk * 256 + threadIdx.x);
+  if ((int)(chunk * 256) >= n) return;
+  const long long item0 = (long long)s * p.per_seq + (long long)g * p.row_tiles;
+  float sum = 0.0f;
+  for (int rt = 0; rt < p.row_tiles; ++rt) {
+    const int n_rows = min(N, p.rows - rt * N);
+    __syncthreads();
+    if ((int)threadIdx.x < N) s_lse[threadIdx.x] = p.ws_lse[(item0 + rt) * N + threadIdx.x];
+    __syncthreads();
+    if (t >= n) continue;
+    const float* z = p.ws_z + (((item0 + rt) * p.z_tiles + t / kPagedKeys) * kPagedKeys + t % kPagedKeys) * p.nz;
+    for (int r = 0; r < n_rows; r += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(z + r);
+      sum += pow2_approx(v.x - s_lse[r]);
+      if (r + 1 < n_rows) sum += pow2_approx(v.y - s_lse[r + 1]);
+      if (r + 2 < n_rows) sum += pow2_approx(v.z - s_lse[r + 2]);
+      if (r + 3 < n_rows) sum += pow2_approx(v.w - s_lse[r + 3]);
+    }
+  }
+  if (t < n) p.mass[plane * p.mass_rs + t] += sum;
+}
+
+}  // namespace dllm

@@ -70,6 +70,18 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t lead, uint32_t d_tmem, uint3
       : "memory");
 }
 
+// D[tmem] (+)= A B^T over 16 bf16 (or halves, by idesc) of K, both operands in shared memory.
+__device__ __forceinline__ void mma_f16_ss(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+
 // Arrive once on bar when everything the leading thread has issued is done.
 __device__ __forceinline__ void mma_commit_lead(uint32_t lead, uint64_t* bar) {
   asm volatile(
