@@ -25,7 +25,7 @@ AttnPagedPlan plan_attn_paged(long long b, long long H_kv, long long rows, int h
   a.row_tiles = (int)((rows + a.N - 1) / a.N);
   a.items = b * H_kv * a.row_tiles;
   a.tiles = std::max(1LL, (T + kPagedKeys - 1) / kPagedKeys);
-  a.ctas = op_device_sms();
+  a.ctas = (a.N <= 16 ? 2 : 1) * op_device_sms();
   a.whole = a.tiles <= 2;
   a.nz = (int)std::min<long long>((rows + 3) / 4 * 4, a.N);
   size_t at = 0;
@@ -49,7 +49,7 @@ cudaError_t launch_attn_paged(const CUtensorMap& tk, const CUtensorMap& tv, cons
   using C = AttnPagedCfg<HD, N>;
   cudaError_t e = op_smem_once(reinterpret_cast<const void*>(attn_paged_kernel<F, HD, N>), C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const long long units = a.whole ? a.items : a.items * a.tiles;
+  const long long units = a.whole ? a.items : a.items * (a.tiles + 1);
   const unsigned grid = (unsigned)std::min<long long>(a.ctas, (units + p.min_share - 1) / p.min_share);
   e = op_launch(attn_paged_kernel<F, HD, N>, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, st, 1, tk, tv, p);
   if (e != cudaSuccess) return e;

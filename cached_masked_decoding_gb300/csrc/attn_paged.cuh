@@ -41,7 +41,7 @@ struct AttnPagedParams {
   float* mass;
   int H, R, group, rows;      // rows: R * group of a cached head, in row_tiles tiles of N
   int row_tiles, per_seq;     // per_seq: items of a sequence, H_kv * row_tiles
-  int min_share, whole;       // tiles a CTA takes at least; whole: items are not split
+  int min_share, whole;       // units a CTA takes at least; whole: items are not split
   FastDiv by_group, by_tiles; // by_tiles: by row_tiles
   FastDiv by_chunks;          // by the 256-key chunks of a table
   float scale_log2;
@@ -87,17 +87,18 @@ struct AttnPagedCfg {
   static constexpr int P_ROW = 2 * NP;                  // a key's probabilities (8 rows: hi, then lo)
   static constexpr int P_PARTS = N < 16 ? 1 : 2;
   static constexpr int P_BYTES = KT * P_ROW;            // one part
-  static constexpr int P_BUFS = N == 64 ? 1 : 2;
+  static constexpr int CTAS = N <= 16 ? 2 : 1;          // an SM
+  static constexpr int P_BUFS = N == 64 || (N == 16 && HD == 128) ? 1 : 2;
   // warp maxima (4), m, rise, sums of the warps (4), places (2 buffers of 64 bits)
   static constexpr int STAT_FLOATS = 4 * N + 2 * N + 4 * N + 4 * N;
-  static constexpr int FIXED = 1024 + 2 * Q_BYTES + P_BUFS * P_PARTS * P_BYTES + STAT_FLOATS * 4 + 512;
-  static constexpr int MOST = (232448 - FIXED) / SLOT;
+  static constexpr int FIXED = 1024 + Q_BYTES + P_BUFS * P_PARTS * P_BYTES + STAT_FLOATS * 4 + 384;
+  static constexpr int MOST = (228 * 1024 / CTAS - 1024 - FIXED) / SLOT;
   static constexpr int SLOTS = MOST > 12 ? 12 : MOST;
   static constexpr int SMEM_BYTES = FIXED + SLOTS * SLOT;
   static constexpr int S_COL = 0;                       // two buffers of NP
   static constexpr int O_COL = 2 * NP;                  // NP (8 rows: hi and lo products)
   static constexpr int TMEM_COLS = 3 * NP <= 64 ? 64 : 3 * NP <= 128 ? 128 : 256;
-  static_assert(SLOTS >= 4 && SMEM_BYTES <= 232448 && 3 * NP <= TMEM_COLS, "shared and tensor memory");
+  static_assert(SLOTS >= 3 && SMEM_BYTES <= 232448 && 3 * NP <= TMEM_COLS && (2 * SLOTS + 10) * 8 + 28 <= 384, "shared and tensor memory");
 };
 
 // 2^x; results below the normal range are 0
@@ -113,21 +114,35 @@ __device__ __forceinline__ int order_of(float x) {
 }
 __device__ __forceinline__ float of_order(int o) { return __int_as_float(o ^ ((o >> 31) & 0x7fffffff)); }
 
-// A sequence's tiles: one at least, so that every item is somebody's.
-__device__ __forceinline__ int paged_tiles(int n) { return max(1, (n + kPagedKeys - 1) / kPagedKeys); }
+__device__ __forceinline__ int paged_tiles(int n) { return (n + kPagedKeys - 1) / kPagedKeys; }
 
-// The parts of a CTA's run of tiles, one item after the other; every role walks them by itself.
+// What an item costs, in the units that are shared out: its tiles, and one for its start and end (about a tile's
+// time: two batches of equal keys, one with 8 items of nothing more, took 29 us and 45 us in units of tiles alone).
+// whole: items are the units.
+__device__ __forceinline__ int paged_units(const AttnPagedParams& p, int n) {
+  return p.whole ? 1 : n > 0 ? paged_tiles(n) + 1 : 0;
+}
+
+// The parts of a CTA's run of units, one item after the other; every role walks them by itself.
 struct PagedWalk {
-  int s, item, t0, nt, n, left, next_n, part;   // part: counts up
-  __device__ __forceinline__ PagedWalk(const AttnPagedParams& p, int s_, int item_, int t0_, int total)
-      : s(s_), item(item_), t0(t0_), nt(0), left(total), part(0) {
+  int s, item, t0, nt, n, left, next_n, part;   // nt: the part's tiles; part: counts up
+  // from unit u0 of an item on, `units` of them
+  __device__ __forceinline__ PagedWalk(const AttnPagedParams& p, int s_, int item_, int u0, int units)
+      : s(s_), item(item_), left(units), part(0) {
     n = p.c.len(p.lens, s);
     next_n = s + 1 < p.c.b ? p.c.len(p.lens, s + 1) : 0;
-    take();
+    take(p, u0);
   }
-  __device__ __forceinline__ void take() {
-    nt = min(paged_tiles(n) - t0, left);
-    left -= nt;
+  __device__ __forceinline__ void take(const AttnPagedParams& p, int u0) {
+    t0 = max(u0 - 1, 0);
+    if (p.whole) {
+      nt = max(paged_tiles(n), 1);                // (an empty one too: it writes its zeros)
+      --left;
+    } else {
+      const int start = u0 == 0 ? 1 : 0;
+      nt = min(paged_tiles(n) - t0, left - start);
+      left -= nt + start;
+    }
   }
   // false: that was the last one
   __device__ __forceinline__ bool next(const AttnPagedParams& p) {
@@ -135,19 +150,20 @@ struct PagedWalk {
     ++part;
     if (++item == p.per_seq) {
       item = 0;
-      ++s;
-      n = next_n;
-      next_n = s + 1 < p.c.b ? p.c.len(p.lens, s + 1) : 0;
+      do {
+        ++s;
+        n = next_n;
+        next_n = s + 1 < p.c.b ? p.c.len(p.lens, s + 1) : 0;
+      } while (!p.whole && n == 0 && s + 1 < p.c.b);
     }
-    t0 = 0;
-    take();
-    return true;
+    take(p, 0);
+    return nt > 0;                                // (no tile: the run ends behind an item's first unit)
   }
-  __device__ __forceinline__ bool complete() const { return t0 == 0 && nt == paged_tiles(n); }
+  __device__ __forceinline__ bool complete() const { return t0 == 0 && nt >= paged_tiles(n); }
 };
 
 template <typename F, int HD, int N>
-__global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, 1)
+__global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD, N>::CTAS)
     attn_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ AttnPagedParams p) {
   using C = AttnPagedCfg<HD, N>;
@@ -156,8 +172,8 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sKV = smem;
-  uint8_t* sQ = sKV + C::SLOTS * C::SLOT;               // two buffers
-  uint8_t* sP = sQ + 2 * C::Q_BYTES;                    // buffers of hi, lo
+  uint8_t* sQ = sKV + C::SLOTS * C::SLOT;
+  uint8_t* sP = sQ + C::Q_BYTES;                        // buffers of hi, lo
   long long* s_to = reinterpret_cast<long long*>(sP + C::P_BUFS * C::P_PARTS * C::P_BYTES);   // [2][N] where a row goes
   float* s_wmax = reinterpret_cast<float*>(s_to + 2 * N);   // [4][N]
   float* s_m = s_wmax + 4 * N;                          // [N] references
@@ -165,13 +181,13 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, 1)
   float* s_ls = s_up + N;                               // [4][N] the warps' sums
   uint64_t* full = reinterpret_cast<uint64_t*>(s_ls + 4 * N);
   uint64_t* empty = full + C::SLOTS;
-  uint64_t* qready = empty + C::SLOTS;                  // [2]
-  uint64_t* sfull = qready + 2;                         // [2]
+  uint64_t* qready = empty + C::SLOTS;
+  uint64_t* sfull = qready + 1;                         // [2]
   uint64_t* sfree = sfull + 2;                          // [2]
   uint64_t* pready = sfree + 2;                         // [2]
   uint64_t* pvdone = pready + 2;                        // [2]
   uint64_t* mdone = pvdone + 2;                         // every MMA is done
-  int* s_plan = reinterpret_cast<int*>(mdone + 1);      // first sequence, item, tile, and how many tiles
+  int* s_plan = reinterpret_cast<int*>(mdone + 1);      // first sequence, item, unit; how many units; a CTA's share
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_plan + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* err = g_attn_paged_err;
@@ -182,8 +198,8 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
+    mbar_init(qready, C::SOFT / 32);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&qready[s], C::SOFT / 32);
       mbar_init(&sfull[s], 1);
       mbar_init(&sfree[s], C::SOFT / 32);
       mbar_init(&pready[s], C::SOFT / 32);
@@ -200,25 +216,21 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, 1)
     tmem_relinquish();
   }
   if constexpr (N < 16) {   // the columns past the rows: queries of zero
-    for (int e = threadIdx.x; e < 2 * C::Q_BYTES / 16; e += C::THREADS) reinterpret_cast<uint4*>(sQ)[e] = make_uint4(0, 0, 0, 0);
+    for (int e = threadIdx.x; e < C::Q_BYTES / 16; e += C::THREADS) reinterpret_cast<uint4*>(sQ)[e] = make_uint4(0, 0, 0, 0);
   }
   griddep_wait();
-  // this CTA's run of tiles
+  // this CTA's run of units
   if (warp == 0) {
     long long sum = 0;
-    for (int s0 = 0; s0 < p.c.b; s0 += 32) {
-      int t = s0 + lane < p.c.b ? (p.whole ? 1 : paged_tiles(p.c.len(p.lens, s0 + lane))) : 0;
-      sum += __reduce_add_sync(0xffffffffu, t);
-    }
-    // (whole: the units are items)
+    for (int s0 = 0; s0 < p.c.b; s0 += 32)
+      sum += __reduce_add_sync(0xffffffffu, s0 + lane < p.c.b ? paged_units(p, p.c.len(p.lens, s0 + lane)) : 0);
     const long long units = sum * p.per_seq;
     const long long share = max((units + gridDim.x - 1) / gridDim.x, (long long)p.min_share);
     const long long first = min(units, share * blockIdx.x), last = min(units, first + share);
     long long base = 0;
-    int s_at = 0, item = 0, t0 = 0;
-    long long total = last - first;
-    for (int s0 = 0; s0 < p.c.b && total > 0; s0 += 32) {
-      const int t = s0 + lane < p.c.b ? (p.whole ? 1 : paged_tiles(p.c.len(p.lens, s0 + lane))) : 0;
+    int s_at = 0, item = 0, u0 = 0;
+    for (int s0 = 0; s0 < p.c.b && first < last; s0 += 32) {
+      const int t = s0 + lane < p.c.b ? paged_units(p, p.c.len(p.lens, s0 + lane)) : 0;
       int upto = t;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -232,28 +244,16 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, 1)
         const long long in = first - base - (long long)before * p.per_seq;
         s_at = s0 + l;
         item = (int)(in / tl);
-        t0 = (int)(in - (long long)item * tl);
+        u0 = (int)(in - (long long)item * tl);
         break;
       }
       base += (long long)__shfl_sync(0xffffffffu, upto, 31) * p.per_seq;
     }
-    if (p.whole && total > 0) {   // items to tiles
-      long long tiles = 0;
-      int s = s_at, it = item;
-      for (long long left = total; left > 0;) {
-        const int here = (int)min((long long)(p.per_seq - it), left);
-        tiles += (long long)here * paged_tiles(p.c.len(p.lens, s));
-        left -= here;
-        it = 0;
-        ++s;
-      }
-      total = tiles;
-    }
     if (lane == 0) {
       s_plan[0] = s_at;
       s_plan[1] = item;
-      s_plan[2] = t0;
-      s_plan[3] = (int)total;
+      s_plan[2] = u0;
+      s_plan[3] = (int)(last - first);
       s_plan[4] = (int)min(share, 0x7fffffffLL);
     }
   }
@@ -263,10 +263,9 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_launch_dependents();                          // not before: a dependent could take the columns awaited
-  const int total = s_plan[3];
 
-  if (total > 0) {
-    PagedWalk w(p, s_plan[0], s_plan[1], s_plan[2], total);
+  PagedWalk w(p, s_plan[0], s_plan[1], s_plan[2], s_plan[3]);
+  if (s_plan[3] > 0 && w.nt > 0) {
     if (warp == 0) {
       // ------------------------------------------------------ pages to the ring
       const uint64_t pol = p.row_tiles > 1 ? policy_evict_last() : policy_evict_first();
@@ -322,34 +321,35 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, 1)
       const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV), p0 = smem_u32(sP);
       PagedWalk ws = w;                                   // the scores' part, two tiles ahead
       int s_left = ws.nt, o_left = w.nt;
-      bool s_new = true, o_new = true;
-      auto issue_s = [&](int t) {
-        if (s_left == 0) {
-          ws.next(p);
+      bool s_new = true, o_new = true, s_done = false;
+      auto issue_s = [&](int t) {                         // nothing behind the last tile
+        if (!s_done && s_left == 0) {
+          s_done = !ws.next(p);
           s_left = ws.nt;
           s_new = true;
         }
+        if (s_done) return true;
         --s_left;
         const int u = 2 * t, slot = u % C::SLOTS, sb = t & 1;
-        if (s_new && !wait(&qready[ws.part & 1], ws.part >> 1)) return false;
+        if (s_new && !wait(qready, ws.part)) return false;
         s_new = false;
         if (!wait(&full[slot], u / C::SLOTS) || (t >= 2 && !wait(&sfree[sb], (t >> 1) - 1))) return false;
         tc_fence_after();
-        const uint32_t k = kv0 + slot * C::SLOT, q = q0 + (ws.part & 1) * C::Q_BYTES, d = tmem + C::S_COL + sb * C::NP;
+        const uint32_t k = kv0 + slot * C::SLOT, d = tmem + C::S_COL + sb * C::NP;
 #pragma unroll
         for (int h = 0; h < PARTS; ++h)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_f16_ss(lead, d, sdesc_rows<128>(k + h * (KT * 128) + kk * 32),
-                       sdesc_rows<128>(q + h * (C::NP * 128) + kk * 32), idesc, (h > 0 || kk > 0) ? 1u : 0u);
+                       sdesc_rows<128>(q0 + h * (C::NP * 128) + kk * 32), idesc, (h > 0 || kk > 0) ? 1u : 0u);
         mma_commit_lead(lead, &empty[slot]);
         mma_commit_lead(lead, &sfull[sb]);
         return true;
       };
-      bool ok = issue_s(0) && (total < 2 || issue_s(1));
-      for (int t = 0; t < total && ok; ++t) {
+      bool ok = issue_s(0) && issue_s(1);
+      for (int t = 0; ok; ++t) {
         if (o_left == 0) {
-          w.next(p);
+          if (!w.next(p)) break;
           o_left = w.nt;
           o_new = true;
         }
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, 1)
         o_new = false;
         mma_commit_lead(lead, &empty[slot]);
         mma_commit_lead(lead, &pvdone[t & 1]);
-        if (t + 2 < total && !(ok = issue_s(t + 2))) break;
+        ok = issue_s(t + 2);
       }
       mma_commit_lead(lead, mdone);
       mbar_wait_long(mdone, 0u, nullptr, err, ERR_ATTN_FULL);
@@ -380,7 +380,8 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, 1)
       const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
       constexpr int L = HD / 8, QV = N * L / C::SOFT > 0 ? N * L / C::SOFT : 1;   // lanes of a row; vectors of a thread
       uint4 qv[QV];
-      // the query tile of a part: its rows' elements on their way, then in place
+      // The query tile of a part: its rows' elements on their way, then in place.  One buffer does: the tile is
+      // stored when the scores of the part before are all there.
       auto q_load = [&](const PagedWalk& x) {
         uint32_t rt;
         const int g = (int)p.by_tiles.divmod((uint32_t)x.item, rt);
@@ -403,7 +404,7 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, 1)
         for (int k = 0; k < QV; ++k) {
           const int e = tid + k * C::SOFT, row = e / L, c = e % L;
           if (row < N)
-            *reinterpret_cast<uint4*>(sQ + buf * C::Q_BYTES + (c >> 3) * (C::NP * 128) + swizzled<128>(row, c & 7)) = qv[k];
+            *reinterpret_cast<uint4*>(sQ + (c >> 3) * (C::NP * 128) + swizzled<128>(row, c & 7)) = qv[k];
         }
         if (tid < N) {
           uint32_t j;
@@ -413,7 +414,7 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, 1)
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&qready[buf]);
+        if (lane == 0) mbar_arrive(qready);
       };
       q_load(w);
       q_store(w);
@@ -636,11 +637,19 @@ __global__ void __launch_bounds__(128) attn_paged_join_kernel(const __grid_const
   const int r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_launch_dependents();
   griddep_wait();
-  const int2 plan = p.ws_plan[item];
   const int s = (int)(item / p.per_seq);
   uint32_t rt, j;
   const int g = (int)p.by_tiles.divmod((uint32_t)(item - (long long)s * p.per_seq), rt);
-  if (plan.x < 0 || (int)rt * N + r >= p.rows) return;
+  if ((int)rt * N + r >= p.rows) return;
+  const uint32_t i = p.by_group.divmod(rt * (uint32_t)N + (uint32_t)r, j);
+  typename F::E::T* out = reinterpret_cast<typename F::E::T*>(p.out) + ((long long)s * p.R + i) * p.o_rs +
+                          (long long)(g * p.group + (int)j) * HD + threadIdx.x;
+  if (p.c.len(p.lens, s) == 0) {   // nobody's item
+    if (threadIdx.x < HD) F::E::put(out, 0.0f);
+    return;
+  }
+  const int2 plan = p.ws_plan[item];
+  if (plan.x < 0) return;
   // slots: the first CTA's, then every following one's first
   const int parts = (plan.y >> 1) - (plan.x >> 1) + 1;
   auto slot_of = [&](int k) { return k == 0 ? plan.x : ((plan.x >> 1) + k) * 2; };
@@ -691,10 +700,7 @@ __global__ void __launch_bounds__(128) attn_paged_join_kernel(const __grid_const
   if (threadIdx.x == 0 && p.mass) p.ws_lse[item * N + r] = sum == 0.0f ? INFINITY : M + log2f(sum);
   if (threadIdx.x >= HD) return;
   const float v = (s_o[0][threadIdx.x] + s_o[1][threadIdx.x]) + (s_o[2][threadIdx.x] + s_o[3][threadIdx.x]);
-  const uint32_t i = p.by_group.divmod(rt * (uint32_t)N + (uint32_t)r, j);
-  F::E::put(reinterpret_cast<typename F::E::T*>(p.out) + ((long long)s * p.R + i) * p.o_rs +
-                (long long)(g * p.group + (int)j) * HD + threadIdx.x,
-            sum == 0.0f ? 0.0f : v / sum);
+  F::E::put(out, sum == 0.0f ? 0.0f : v / sum);
 }
 
 // Adds what every key received: the rows' probabilities from their scores (base 2) and log sums.  A thread a key.
