@@ -6,7 +6,15 @@
 // The largest term is left out of the sums, so a nearly certain row's S keeps its relative accuracy, and both
 // parts of the entropy are of one sign.
 //
-// One CTA a row: its maximum, its sums, and one pass for each alternative (the largest that comes after the last).
+// Bound by HBM: the logits are read once.  A CTA (or a cluster of up to 8, where rows are few) takes a row and streams
+// it; every thread keeps the largest of its elements m and, relative to it, S and W of them all.  What needs the
+// elements again is a few threads' worth, which lies in L2 or L1 still:
+//   - the thread that holds the row's largest takes its S and W again without it;
+//   - the alternatives are among the elements of threads whose m is no less than the top-th largest of 128 group
+//     maxima (a lower bound of the top-th largest element): for 20 of 126464 about 22 threads of 512.  Elements above
+//     the bound are ranked by counting; its equals join in the order of their ids.
+// Rows that would give more than 1024 elements above the bound (one thread's elements are the largest by far) take a
+// pass of the row an alternative.
 #include <cmath>
 
 #include "ops8.h"
@@ -21,11 +29,14 @@ struct LogprobsParams {
   float *logp, *entropy, *top_logp;
   int32_t* top_ids;
   long long rs;
-  int vocab, top;
+  int vocab, top, cluster;
   float scale;
 };
 
-constexpr int kLogThreads = 512;
+constexpr int kMostTop = 64;
+constexpr int kMostAbove = 1024;     // elements above the bound that are ranked
+constexpr int kMostEqual = 256;      // and equals that are, before the row is walked for them in order
+constexpr int kLogCluster = 8;
 
 struct Best {
   float x;
@@ -36,84 +47,450 @@ __device__ __forceinline__ bool before(const Best& a, const Best& b) {
   return a.i >= 0 && (b.i < 0 || a.x > b.x || (a.x == b.x && a.i < b.i));
 }
 
-__device__ Best block_best(Best b, Best* s) {
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) {
-    const Best o = {__shfl_xor_sync(0xffffffffu, b.x, d), __shfl_xor_sync(0xffffffffu, b.i, d)};
-    if (before(o, b)) b = o;
-  }
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = b;
-  __syncthreads();
-  b = s[0];
-  for (int w = 1; w < kLogThreads / 32; ++w)
-    if (before(s[w], b)) b = s[w];
-  return b;
+// 2^x; results below the normal range are 0
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// The larger, a NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
-template <typename E>
-__global__ void __launch_bounds__(kLogThreads) logprobs_kernel(const __grid_constant__ LogprobsParams p) {
-  __shared__ Best s_best[kLogThreads / 32];
-  __shared__ float s_sum[2][kLogThreads / 32];
-  const int tid = threadIdx.x;
-  const long long row = blockIdx.x;
+// Largest element m (-inf: none yet), and S and W of all elements so far relative to it; W in base 2.
+struct LogSums {
+  float m = -INFINITY, S = 0.0f, W = 0.0f;
+
+  __device__ __forceinline__ void raise(float to, float c2) {
+    if (m > -INFINITY) {
+      const float d = max_nan((m - to) * c2, -200.0f), f = exp2_fast(d);
+      W = (W + S * d) * f;
+      S *= f;
+    }
+    m = to;
+  }
+  // n elements (a multiple of 2)
+  template <int n>
+  __device__ __forceinline__ void add(const float (&x)[n], float c2) {
+    float top = x[0];
+#pragma unroll
+    for (int i = 1; i < n; ++i) top = fmaxf(top, x[i]);
+    if (top > m) raise(top, c2);
+    const float ref = m == -INFINITY ? 0.0f : m;
+    const uint64_t r2 = f32x2(-ref, -ref), s2 = f32x2(c2, c2);
+    uint64_t Sp = f32x2(S, 0.0f), Wp = f32x2(W, 0.0f);
+#pragma unroll
+    for (int i = 0; i < n; i += 2) {
+      const float2 d = f32x2_get(mul_f32x2(add_f32x2(f32x2(x[i], x[i + 1]), r2), s2));
+      // (2^-200 is 0: a term of -inf has to leave W alone)
+      const float a = max_nan(d.x, -200.0f), b = max_nan(d.y, -200.0f);
+      const uint64_t e = f32x2(exp2_fast(a), exp2_fast(b));
+      Sp = add_f32x2(Sp, e);
+      Wp = fma_f32x2(f32x2(a, b), e, Wp);
+    }
+    const float2 s = f32x2_get(Sp), w = f32x2_get(Wp);
+    S = s.x + s.y;
+    W = w.x + w.y;
+  }
+};
+
+// Row sums with the largest element m left out: o's joined to t's.
+__device__ __forceinline__ void join_sums(LogSums& t, LogSums o, float c2) {
+  if (o.m > t.m) {
+    const LogSums x = t;
+    t = o;
+    o = x;
+  }
+  if (o.m == -INFINITY) {
+    t.S += o.S;                        // 0, or a NaN
+    return;
+  }
+  const float d = max_nan((o.m - t.m) * c2, -200.0f), f = exp2_fast(d);
+  t.S += (1.0f + o.S) * f;
+  t.W += (o.W + (1.0f + o.S) * d) * f;
+}
+
+template <int THREADS>
+struct LogShared {
+  float warp_S[THREADS / 32], warp_W[THREADS / 32];
+  int warp_n[THREADS / 32 + 1];
+  float group[128];                    // group maxima
+  float bound;
+  int owner, n_above, n_equal, n_hot;
+  int hot[THREADS];
+  Best above[kMostAbove];
+  int equal[kMostEqual];
+  Best top[kLogCluster][kMostTop];     // lists of the cluster's CTAs, in order
+  float sums[kLogCluster][3];          // m, S, W
+  Best best[THREADS / 32];
+};
+
+template <typename E, int THREADS>
+struct LogRow {
+  using T = typename E::T;
+  static constexpr int VE = 16 / (int)sizeof(T);
+  const T* x;
+  int vocab, head, extra;              // extra: elements before and after the vectors, a thread each
+  int nvec, v0, v1;                    // the CTA's vectors
+  __device__ __forceinline__ LogRow(const LogprobsParams& p, long long row, int rank, int ranks) {
+    x = static_cast<const T*>(p.logits) + row * p.rs;
+    vocab = p.vocab;
+    head = min(vocab, (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int)sizeof(T));
+    nvec = (vocab - head) / VE;
+    v0 = (int)((long long)nvec * rank / ranks);
+    v1 = (int)((long long)nvec * (rank + 1) / ranks);
+    extra = rank == 0 ? vocab - nvec * VE : 0;
+  }
+  __device__ __forceinline__ int extra_index(int e) const { return e < head ? e : e + nvec * VE; }
+  __device__ __forceinline__ int index(int v, int e) const { return head + v * VE + e; }
+  __device__ __forceinline__ uint4 load(int v) const { return reinterpret_cast<const uint4*>(x + head)[v]; }
+  static __device__ __forceinline__ void floats(const uint4& r, float (&f)[VE]) {
+    if constexpr (VE == 8) {
+      E::load8(reinterpret_cast<const T*>(&r), f);
+    } else {
+      f[0] = __uint_as_float(r.x);
+      f[1] = __uint_as_float(r.y);
+      f[2] = __uint_as_float(r.z);
+      f[3] = __uint_as_float(r.w);
+    }
+  }
+  // f(x, index) of every element of thread t, by the lanes of a warp
+  template <typename Fn>
+  __device__ __forceinline__ void each(int t, int lane, Fn f) const {
+    for (int v = v0 + t + lane * THREADS; v < v1; v += 32 * THREADS) {
+      float e[VE];
+      floats(load(v), e);
+#pragma unroll
+      for (int i = 0; i < VE; ++i) f(e[i], index(v, i));
+    }
+    if (lane == 0 && t < extra) f(E::get(x + extra_index(t)), extra_index(t));
+  }
+};
+
+// The `top` best of the CTA's elements, in order, one pass each.
+template <typename E, int THREADS>
+__device__ void top_by_passes(const LogRow<E, THREADS>& row, LogShared<THREADS>& sh, int top, Best* out) {
+  Best last = {INFINITY, -1};
+  for (int k = 0; k < top; ++k) {
+    Best b = {0.0f, -1};
+    auto look = [&](float x, int i) {
+      const Best c = {x, i};
+      if (x == x && (k == 0 || before(last, c)) && before(c, b)) b = c;
+    };
+    for (int v = row.v0 + (int)threadIdx.x; v < row.v1; v += THREADS) {
+      float e[LogRow<E, THREADS>::VE];
+      row.floats(row.load(v), e);
+#pragma unroll
+      for (int i = 0; i < LogRow<E, THREADS>::VE; ++i) look(e[i], row.index(v, i));
+    }
+    if ((int)threadIdx.x < row.extra) look(E::get(row.x + row.extra_index(threadIdx.x)), row.extra_index(threadIdx.x));
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) {
+      const Best o = {__shfl_xor_sync(0xffffffffu, b.x, d), __shfl_xor_sync(0xffffffffu, b.i, d)};
+      if (before(o, b)) b = o;
+    }
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) sh.best[threadIdx.x / 32] = b;
+    __syncthreads();
+    b = sh.best[0];
+    for (int w = 1; w < THREADS / 32; ++w)
+      if (before(sh.best[w], b)) b = sh.best[w];
+    if (threadIdx.x == 0) out[k] = b;
+    last = b;
+    if (b.i < 0) {                     // none left, here and in every further pass
+      for (int j = k + 1 + (int)threadIdx.x; j < top; j += THREADS) out[j] = b;
+      break;
+    }
+  }
+}
+
+// The first `need` elements equal to `bound` in the order of their ids, and how many there are; the CTA's elements
+// lie in the order head, vectors, tail.
+template <typename E, int THREADS>
+__device__ int equals_in_order(const LogRow<E, THREADS>& row, LogShared<THREADS>& sh, float bound, int need, Best* out) {
+  constexpr int VE = LogRow<E, THREADS>::VE;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, heads = row.extra ? row.head : 0;
+  int found = 0;
+  for (int at = row.v0 - THREADS; at < row.v1 + THREADS && found < need; at += THREADS) {
+    // one step for the head, one of THREADS vectors each, one for the tail
+    float e[VE];
+    int n = 0, first = 0;
+    if (at < row.v0) {
+      if (tid < heads) {
+        e[0] = E::get(row.x + tid);
+        n = 1;
+        first = tid;
+      }
+    } else if (at < row.v1) {
+      if (at + tid < row.v1) {
+        row.floats(row.load(at + tid), e);
+        n = VE;
+        first = row.index(at + tid, 0);
+      }
+    } else if (tid < row.extra - heads) {
+      first = row.extra_index(heads + tid);
+      e[0] = E::get(row.x + first);
+      n = 1;
+    }
+    uint32_t mask = 0;
+#pragma unroll
+    for (int i = 0; i < VE; ++i)
+      if (i < n && e[i] == bound) mask |= 1u << i;
+    int upto = __popc(mask);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += v;
+    }
+    if (lane == 31) sh.warp_n[warp] = upto;
+    __syncthreads();
+    int pos = found + upto - __popc(mask);
+    int total = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) pos += sh.warp_n[w];
+      total += sh.warp_n[w];
+    }
+    for (; mask && pos < need; mask &= mask - 1, ++pos) out[pos] = {bound, first + __ffs(mask) - 1};
+    found += total;
+    __syncthreads();
+  }
+  return min(found, need);
+}
+
+template <typename E, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1536 / THREADS) logprobs_kernel(const __grid_constant__ LogprobsParams p) {
+  constexpr int VE = LogRow<E, THREADS>::VE, QUAD = THREADS / 128, AHEAD = 4;
+  __shared__ LogShared<THREADS> sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ranks = p.cluster, rank = ranks > 1 ? (int)cluster_rank() : 0;
+  const long long r = ranks > 1 ? blockIdx.x / (unsigned)ranks : blockIdx.x;
+  const float c2 = p.scale * 1.4426950408889634f;
+  if (tid == 0) {
+    sh.owner = THREADS;
+    sh.n_above = sh.n_equal = sh.n_hot = 0;
+    sh.bound = INFINITY;
+  }
+  if (ranks > 1) cluster_arrive();     // waited for before the first access of another CTA's memory
   griddep_launch_dependents();
   griddep_wait();
-  const typename E::T* x = static_cast<const typename E::T*>(p.logits) + row * p.rs;
-  Best b = {0.0f, -1};
-  for (int i = tid; i < p.vocab; i += kLogThreads) {
-    const Best c = {E::get(x + i), i};
-    if (c.x == c.x && before(c, b)) b = c;
+  const LogRow<E, THREADS> row(p, r, rank, ranks);
+
+  // ------------------------------------------------------ one pass
+  LogSums mine;
+  int v = row.v0 + tid;
+  for (; v + (AHEAD - 1) * THREADS < row.v1; v += AHEAD * THREADS) {
+    uint4 raw[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) raw[k] = row.load(v + k * THREADS);
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      float f[VE];
+      row.floats(raw[k], f);
+      mine.add(f, c2);
+    }
   }
-  const Best first = block_best(b, s_best);
+  for (; v < row.v1; v += THREADS) {
+    float f[VE];
+    row.floats(row.load(v), f);
+    mine.add(f, c2);
+  }
+  if (tid < row.extra) {
+    const float f[2] = {E::get(row.x + row.extra_index(tid)), -INFINITY};
+    mine.add(f, c2);
+  }
+
+  // ------------------------------------------------------ the largest, and a bound of the alternatives
+  float M = mine.m;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    if (2 * d == QUAD && lane % QUAD == 0) sh.group[tid / QUAD] = M;
+  }
+  if (QUAD == 1) sh.group[tid] = mine.m;
+  if (lane == 0) sh.warp_S[warp] = M;
+  __syncthreads();
+  for (int w = 0; w < THREADS / 32; ++w) M = fmaxf(M, sh.warp_S[w]);
+  if (mine.m == M && M > -INFINITY) atomicMin(&sh.owner, tid);
+  if (p.top > 0) {
+    // rank of this thread's group among all, a share of the comparisons each
+    const int g = tid / QUAD;
+    const float x = sh.group[g];
+    int n = 0;
+#pragma unroll 8
+    for (int j = tid % QUAD; j < 128; j += QUAD) {
+      const float y = sh.group[j];
+      n += y > x || (y == x && j < g) ? 1 : 0;
+    }
+#pragma unroll
+    for (int d = 1; d < QUAD; d <<= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
+    if (n == p.top - 1) sh.bound = x;
+  }
+  __syncthreads();
+  const float bound = sh.bound;
+  const int owner = sh.owner;
+  // (elements of -inf that are alternatives all the same come by the walk in order)
+  if (tid == owner || (p.top > 0 && mine.m >= bound && mine.m > -INFINITY))
+    sh.hot[atomicAdd(&sh.n_hot, 1)] = tid;
+  // everyone's sums relative to M; the owner's come again without the largest
   float S = 0.0f, W = 0.0f;
-  for (int i = tid; i < p.vocab; i += kLogThreads) {
-    if (i == first.i) continue;
-    const float v = E::get(x + i), d = (v - first.x) * p.scale;
-    const float e = expf(d);
-    S += e;
-    if (e > 0.0f) W += d * e;      // (a term of 0 may have an infinite d)
+  if (tid != owner) {
+    if (mine.m > -INFINITY) mine.raise(M, c2);
+    S = mine.S;
+    W = mine.W;
+  }
+  __syncthreads();
+  const int n_hot = sh.n_hot;
+  for (int h = warp; h < n_hot; h += THREADS / 32) {
+    const int t = sh.hot[h];
+    int top_count = 0;
+    row.each(t, lane, [&](float x, int i) {
+      if (p.top > 0 && x >= bound) {
+        // (no more than tells that there are too many)
+        if (x > bound) {
+          if (*(volatile int*)&sh.n_above <= kMostAbove) {
+            const int at = atomicAdd(&sh.n_above, 1);
+            if (at < kMostAbove) sh.above[at] = {x, i};
+          }
+        } else if (bound > -INFINITY && *(volatile int*)&sh.n_equal <= kMostEqual) {
+          const int at = atomicAdd(&sh.n_equal, 1);
+          if (at < kMostEqual) sh.equal[at] = i;
+        }
+      }
+      if (t == owner) {
+        if (x == M) {
+          ++top_count;
+        } else {
+          const float d = max_nan((x - M) * c2, -200.0f), e = exp2_fast(d);
+          S += e;
+          W += d * e;
+        }
+      }
+    });
+    if (t == owner) {
+      top_count = __reduce_add_sync(0xffffffffu, top_count);
+      if (lane == 0) S += (float)(top_count - 1);
+    }
   }
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) {
     S += __shfl_xor_sync(0xffffffffu, S, d);
     W += __shfl_xor_sync(0xffffffffu, W, d);
   }
-  if (tid % 32 == 0) {
-    s_sum[0][tid / 32] = S;
-    s_sum[1][tid / 32] = W;
+  if (lane == 0) {
+    sh.warp_S[warp] = S;
+    sh.warp_W[warp] = W;
   }
   __syncthreads();
-  S = W = 0.0f;
-  for (int w = 0; w < kLogThreads / 32; ++w) {
-    S += s_sum[0][w];
-    W += s_sum[1][w];
+
+  // ------------------------------------------------------ this CTA's alternatives, in order
+  Best* list = sh.top[rank];
+  if (p.top > 0) {
+    const int na = sh.n_above, ne = sh.n_equal;
+    if (na > kMostAbove) {
+      top_by_passes(row, sh, p.top, list);
+    } else {
+      for (int i = tid; i < na; i += THREADS) {
+        const Best b = sh.above[i];
+        int n = 0;
+        for (int j = 0; j < na; ++j) n += before(sh.above[j], b) ? 1 : 0;
+        if (n < p.top) list[n] = b;
+      }
+      const int need = p.top - na;
+      if (need > 0) {
+        int found = min(need, ne);
+        if (bound == -INFINITY || ne > kMostEqual) {
+          found = equals_in_order(row, sh, bound, need, list + na);
+        } else {
+          for (int t = tid; t < ne; t += THREADS) {
+            const int b = sh.equal[t];
+            int n = 0;
+            for (int j = 0; j < ne; ++j) n += sh.equal[j] < b ? 1 : 0;
+            if (n < need) list[na + n] = {bound, b};
+          }
+        }
+        for (int k = na + found + tid; k < p.top; k += THREADS) list[k] = {-INFINITY, -1};
+      }
+    }
   }
-  const bool finite = first.i >= 0 && fabsf(first.x) != INFINITY && S == S;
-  const float nan = __uint_as_float(0x7fffffffu), log_sum = finite ? log1pf(S) : nan;
+  LogSums sum;
+  sum.m = M;
+  sum.S = sum.W = 0.0f;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    sum.S += sh.warp_S[w];
+    sum.W += sh.warp_W[w];
+  }
+  __syncthreads();
+
+  // ------------------------------------------------------ the cluster's
+  if (ranks > 1) {
+    cluster_wait();
+    if (rank != 0) {
+      for (int i = tid; i < 2 * p.top; i += THREADS)
+        cluster_store(cluster_addr(smem_u32(reinterpret_cast<float*>(sh.top[rank]) + i), 0),
+                      reinterpret_cast<const float*>(list)[i]);
+      if (tid < 3)
+        cluster_store(cluster_addr(smem_u32(&sh.sums[rank][tid]), 0),
+                      tid == 0 ? sum.m : tid == 1 ? sum.S : sum.W);
+    }
+    cluster_sync();
+    if (rank != 0) return;
+    for (int k = 1; k < ranks; ++k) {
+      LogSums o;
+      o.m = sh.sums[k][0];
+      o.S = sh.sums[k][1];
+      o.W = sh.sums[k][2];
+      join_sums(sum, o, c2);
+    }
+  }
+  const bool finite = fabsf(sum.m) != INFINITY && sum.S == sum.S;
+  const float nan = __uint_as_float(0x7fffffffu), log_sum = finite ? log1pf(sum.S) : nan;
   if (tid == 0) {
     if (p.logp) {
-      const int t = p.targets[row];
-      p.logp[row] = t >= 0 && t < p.vocab ? (E::get(x + t) - first.x) * p.scale - log_sum : nan;
+      const int t = p.targets[r];
+      p.logp[r] = t >= 0 && t < p.vocab ? (E::get(row.x + t) - sum.m) * p.scale - log_sum : nan;
     }
-    if (p.entropy) p.entropy[row] = log_sum - W / (1.0f + S);
+    if (p.entropy) p.entropy[r] = log_sum - sum.W * 0.6931471805599453f / (1.0f + sum.S);
   }
-  Best last = first;
-  for (int k = 0; k < p.top; ++k) {
-    if (tid == 0) {
-      p.top_ids[row * p.top + k] = last.i;
-      p.top_logp[row * p.top + k] = last.i < 0 ? nan : (last.x - first.x) * p.scale - log_sum;
+  for (int i = tid; i < ranks * p.top; i += THREADS) {
+    // an alternative's place: its own in its list, and how many of each other list come before it
+    const int k = i / p.top, at = i - k * p.top;
+    const Best b = sh.top[k][at];
+    int n = at;
+    for (int o = 0; o < ranks; ++o) {
+      if (o == k) continue;
+      int lo = 0, hi = p.top;
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        // those that are none come last, in the order of the lists
+        const Best c = sh.top[o][mid];
+        const bool first = b.i < 0 && c.i < 0 ? o < k : before(c, b);
+        if (first)
+          lo = mid + 1;
+        else
+          hi = mid;
+      }
+      n += lo;
     }
-    if (k + 1 == p.top || last.i < 0) continue;
-    b = {0.0f, -1};
-    for (int i = tid; i < p.vocab; i += kLogThreads) {
-      const Best c = {E::get(x + i), i};
-      if (c.x == c.x && before(last, c) && before(c, b)) b = c;
+    if (n < p.top) {
+      p.top_ids[r * p.top + n] = b.i;
+      p.top_logp[r * p.top + n] = b.i < 0 ? nan : (b.x - sum.m) * p.scale - log_sum;
     }
-    last = block_best(b, s_best);
   }
 }
 
+namespace {
+
+template <typename E>
+cudaError_t launch_logprobs(const LogprobsParams& p, int rows, int threads, cudaStream_t st) {
+  const dim3 grid((unsigned)rows * (unsigned)p.cluster);
+  return threads == 128 ? op_launch(logprobs_kernel<E, 128>, grid, dim3(128), 0, st, p.cluster, p)
+                        : op_launch(logprobs_kernel<E, 512>, grid, dim3(512), 0, st, p.cluster, p);
+}
+
+}  // namespace
 }  // namespace dllm
 
 using namespace dllm;
@@ -149,12 +526,18 @@ extern "C" dllm_status dllm_op_token_logprobs(const void* logits, int64_t row_st
   p.top_logp = top_logprobs;
   p.vocab = vocab;
   p.scale = inv_temperature;
-  const dim3 grid((unsigned)rows), block(kLogThreads);
+  // Threads of a row, and CTAs: as many as fill the GPU, each with 8192 elements at least.
+  const int threads = vocab <= 8192 ? 128 : 512;
+  p.cluster = 1;
+  while (p.cluster < kLogCluster && (long long)rows * p.cluster * 2 <= 3LL * op_device_sms() &&
+         vocab / (p.cluster * 2) >= 8192)
+    p.cluster *= 2;
+  if ((long long)rows * p.cluster > 0x7fffffff) p.cluster = 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (dtype) {
-    case DLLM_F32: OP_CK(op_launch(logprobs_kernel<ElemF32>, grid, block, 0, st, 1, p)); break;
-    case DLLM_BF16: OP_CK(op_launch(logprobs_kernel<ElemBf16>, grid, block, 0, st, 1, p)); break;
-    default: OP_CK(op_launch(logprobs_kernel<ElemF16>, grid, block, 0, st, 1, p)); break;
+    case DLLM_F32: OP_CK(launch_logprobs<ElemF32>(p, rows, threads, st)); break;
+    case DLLM_BF16: OP_CK(launch_logprobs<ElemBf16>(p, rows, threads, st)); break;
+    default: OP_CK(launch_logprobs<ElemF16>(p, rows, threads, st)); break;
   }
   return DLLM_OK;
 }
