@@ -37,53 +37,50 @@ constexpr int kHeadsRows = 64;         // and most rows
 
 // E, O: element types in and out; L: lanes of a head (8 pairs each, some idle where hd / 16 is no power of two).
 template <typename E, typename O, int L, bool PAGED>
-__global__ void __launch_bounds__(512) heads_kernel(const __grid_constant__ HeadsParams p) {
+__global__ void __launch_bounds__(512, sizeof(typename E::T) == 2 ? 2 : 1)
+    heads_kernel(const __grid_constant__ HeadsParams p) {
+  using T = typename E::T;
+  using TO = typename O::T;
+  constexpr int ITEMS = 2;                         // heads of a thread in flight
   __shared__ float2 s_cs[kHeadsAngles];            // [row][pair] cosine and sine
-  __shared__ int s_slot[kHeadsRows];               // position in the cache, or -1: the row takes no part
+  __shared__ long long s_slot[kHeadsRows];         // row of the cache's head 0, or -1: the row takes no part
   const int row0 = blockIdx.x * p.row_run, n_rows = min(p.row_run, p.rows - row0), pairs = p.rot / 2;
   const int l = threadIdx.x % L, group = threadIdx.x / L, groups = blockDim.x / L;
-  const int items = n_rows * p.heads;
+  const int items = n_rows * p.heads, first = 8 * l;   // first: the lane's first pair
   griddep_launch_dependents();
   griddep_wait();
 
-  for (int r = threadIdx.x; PAGED && r < n_rows; r += blockDim.x) {
-    uint32_t i;
-    const int s = (int)p.by_R.divmod((uint32_t)(row0 + r), i);
-    const int n = p.counts ? p.counts[s] : p.R;
-    const long long at = (long long)(p.starts ? p.starts[s] : 0) + i;
-    s_slot[r] = (int)i < n && at >= 0 && at < p.c.positions && p.c.row(s, 0, (int)at) >= 0 ? (int)at : -1;
-  }
-  if (PAGED) __syncthreads();
-  for (int a = threadIdx.x; a < n_rows * pairs; a += blockDim.x) {
-    const int r = a / pairs, i = a - r * pairs;
-    float c, s;
-    turn_cos_sin(p.turns[i], p.pos ? p.pos[row0 + r] : PAGED ? s_slot[r] : 0, p.amp, c, s);
-    s_cs[a] = make_float2(c, s);
-  }
-  __syncthreads();
-
-  for (int base = 0; base < items; base += groups) {
-    const int it = base + group;
-    bool on = it < items && l * 16 < p.hd;
+  struct Item {
+    Raw8<E> a, b;
+    int r, kind, g;                                // row of the CTA; q, k, v; head
+    bool on;
+    __device__ __forceinline__ bool turns(int first, int pairs) const { return kind < 2 && first < pairs; }
+  };
+  // elements a and b: the pairs' members, or 16 in a row
+  auto at_a = [&](bool turns) { return turns && !p.interleaved ? first : 2 * first; };
+  auto at_b = [&](bool turns) { return turns && !p.interleaved ? first + pairs : 2 * first + 8; };
+  auto load = [&](Item& x, int it) {
+    x.on = it < items && l * 16 < p.hd;
     uint32_t h = 0;
-    const int r = on ? (int)p.by_heads.divmod((uint32_t)it, h) : 0;
-    if (PAGED && on) on = s_slot[r] >= 0;
-    const int kind = (int)h < p.H ? 0 : (int)h < p.H + p.H_kv ? 1 : 2;      // q, k, v
-    const int g = (int)h - (kind == 0 ? 0 : kind == 1 ? p.H : p.H + p.H_kv);
-    const long long row = row0 + r;
-    using T = typename E::T;
-    const T* x = (kind == 0   ? static_cast<const T*>(p.q) + row * p.q_rs
-                  : kind == 1 ? static_cast<const T*>(p.k) + row * p.k_rs
-                              : static_cast<const T*>(p.v) + row * p.v_rs) +
-                 (long long)g * p.hd;
-    const int first = 8 * l;                        // the lane's first pair
-    const bool turns = kind < 2 && first < pairs;
-    const int a = turns && !p.interleaved ? first : 2 * first;
-    const int b = turns && !p.interleaved ? first + pairs : a + 8;
+    x.r = x.on ? (int)p.by_heads.divmod((uint32_t)it, h) : 0;
+    x.kind = (int)h < p.H ? 0 : (int)h < p.H + p.H_kv ? 1 : 2;
+    x.g = (int)h - (x.kind == 0 ? 0 : x.kind == 1 ? p.H : p.H + p.H_kv);
+    if (!x.on) return;
+    const long long row = row0 + x.r;
+    const T* src = (x.kind == 0   ? static_cast<const T*>(p.q) + row * p.q_rs
+                    : x.kind == 1 ? static_cast<const T*>(p.k) + row * p.k_rs
+                                  : static_cast<const T*>(p.v) + row * p.v_rs) +
+                   (long long)x.g * p.hd;
+    const bool t = x.turns(first, pairs);
+    x.a.load(src + at_a(t));
+    x.b.load(src + at_b(t));
+  };
+  auto finish = [&](const Item& x) {
     float va[8], vb[8];
+    const bool on = x.on && (!PAGED || s_slot[x.r] >= 0), turns = x.turns(first, pairs);
     if (on) {
-      E::load8(x + a, va);
-      E::load8(x + b, vb);
+      x.a.floats(va);
+      x.b.floats(vb);
     }
     if (p.norm) {
       float sum = 0.0f;
@@ -93,15 +90,15 @@ __global__ void __launch_bounds__(512) heads_kernel(const __grid_constant__ Head
       }
 #pragma unroll
       for (int d = L / 2; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      if (on && kind < 2) {
+      if (on && x.kind < 2) {
         const float inv = 1.0f / sqrtf(sum * p.inv_hd + p.eps);
-        const T* w = static_cast<const T*>(kind == 0 ? p.q_w : p.k_w);
+        const T* w = static_cast<const T*>(x.kind == 0 ? p.q_w : p.k_w);
         float wa[8], wb[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) wa[e] = wb[e] = 1.0f;
         if (w) {
-          E::load8(w + a, wa);
-          E::load8(w + b, wb);
+          E::load8(w + at_a(turns), wa);
+          E::load8(w + at_b(turns), wb);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -110,9 +107,9 @@ __global__ void __launch_bounds__(512) heads_kernel(const __grid_constant__ Head
         }
       }
     }
-    if (!on) continue;
+    if (!on) return;
     if (turns) {
-      const float2* cs = s_cs + r * pairs + first;
+      const float2* cs = s_cs + x.r * pairs + first;
       if (p.interleaved) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -131,17 +128,57 @@ __global__ void __launch_bounds__(512) heads_kernel(const __grid_constant__ Head
         }
       }
     }
-    using TO = typename O::T;
+    const long long row = row0 + x.r;
     TO* out;
-    if (kind == 0)
-      out = static_cast<TO*>(p.q_out) + row * p.q_out_rs + (long long)g * p.hd;
+    if (x.kind == 0)
+      out = static_cast<TO*>(p.q_out) + row * p.q_out_rs + (long long)x.g * p.hd;
     else if constexpr (PAGED)
-      out = reinterpret_cast<TO*>(kind == 1 ? p.c.k : p.c.v) +
-            p.c.row((int)p.by_R.div((uint32_t)row), g, s_slot[r]);
+      out = reinterpret_cast<TO*>(x.kind == 1 ? p.c.k : p.c.v) + (s_slot[x.r] + ((long long)x.g << p.c.page_shift)) * p.hd;
     else
-      out = static_cast<TO*>(p.k_out) + row * p.k_out_rs + (long long)g * p.hd;
-    O::store8(out + a, va);
-    O::store8(out + b, vb);
+      out = static_cast<TO*>(p.k_out) + row * p.k_out_rs + (long long)x.g * p.hd;
+    O::store8(out + at_a(turns), va);
+    O::store8(out + at_b(turns), vb);
+  };
+
+  // the first heads on their way while the rows' places and angles are worked out
+  Item x[ITEMS];
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) load(x[k], group + k * groups);
+  for (int r = threadIdx.x; PAGED && r < n_rows; r += blockDim.x) {
+    uint32_t i;
+    const int s = (int)p.by_R.divmod((uint32_t)(row0 + r), i);
+    const int n = p.counts ? p.counts[s] : p.R;
+    const long long at = (long long)(p.starts ? p.starts[s] : 0) + i;
+    long long slot = -1;
+    if ((int)i < n && at >= 0 && at < p.c.positions) {
+      const int page = p.c.table[(long long)s * p.c.max_pages + (at >> p.c.page_shift)];
+      if ((unsigned)page < (unsigned)p.c.pages)
+        slot = (((long long)page * p.H_kv) << p.c.page_shift) + (at & ((1 << p.c.page_shift) - 1));
+    }
+    s_slot[r] = slot;
+  }
+  for (int a = threadIdx.x; a < n_rows * pairs; a += blockDim.x) {
+    const int r = a / pairs, i = a - r * pairs;
+    int pos = 0;
+    if (p.pos) {
+      pos = p.pos[row0 + r];
+    } else if (PAGED) {                             // its place in the cache
+      uint32_t k;
+      const int s = (int)p.by_R.divmod((uint32_t)(row0 + r), k);
+      pos = (int)((p.starts ? p.starts[s] : 0) + (long long)k);
+    }
+    float c, s;
+    turn_cos_sin(p.turns[i], pos, p.amp, c, s);
+    s_cs[a] = make_float2(c, s);
+  }
+  __syncthreads();
+  for (int base = 0; base < items; base += ITEMS * groups) {
+    if (base > 0) {
+#pragma unroll
+      for (int k = 0; k < ITEMS; ++k) load(x[k], base + group + k * groups);
+    }
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) finish(x[k]);
   }
 }
 
@@ -226,11 +263,13 @@ dllm_status heads(HeadsParams& p, const char* who, bool paged, int dtype, int ou
   if (heads > (1 << 24)) return op_fail(DLLM_EINVAL, "%s: H=%d H_kv=%d are too many heads", who, p.H, p.H_kv);
   p.heads = (int)heads;
   p.by_heads = FastDiv((uint32_t)heads);
-  // rows of a CTA: as many as fill 256 threads
+  // rows of a CTA: as many as give 256 threads two heads each, where that leaves the GPU's SMs a CTA each
   p.row_run = 1;
-  while (p.row_run < kHeadsRows && 2 * p.row_run * heads * lanes <= 256 && 2 * p.row_run * (p.rot / 2) <= kHeadsAngles)
+  while (p.row_run < kHeadsRows && 2 * p.row_run * heads * lanes <= 512 && 2 * p.row_run * (p.rot / 2) <= kHeadsAngles &&
+         p.rows / (2 * p.row_run) >= op_device_sms())
     p.row_run *= 2;
-  const long long threads = std::min(512LL, (p.row_run * heads * lanes + 31) / 32 * 32);
+  const bool few = p.rows <= 2 * op_device_sms();       // a head a thread: its latency counts
+  const long long threads = std::min(512LL, (p.row_run * heads * lanes / (few ? 1 : 2) + 31) / 32 * 32);
   const dim3 grid((unsigned)((p.rows + p.row_run - 1) / p.row_run)), block((unsigned)threads);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == DLLM_BF16)

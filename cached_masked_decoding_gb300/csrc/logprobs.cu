@@ -16,6 +16,7 @@
 // Rows that would give more than 1024 elements above the bound (one thread's elements are the largest by far) take a
 // pass of the row an alternative.
 #include <cmath>
+#include <type_traits>
 
 #include "ops8.h"
 #include "ptx8.cuh"
@@ -60,47 +61,128 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// Largest element m (-inf: none yet), and S and W of all elements so far relative to it; W in base 2.
-struct LogSums {
-  float m = -INFINITY, S = 0.0f, W = 0.0f;
-
-  __device__ __forceinline__ void raise(float to, float c2) {
-    if (m > -INFINITY) {
-      const float d = max_nan((m - to) * c2, -200.0f), f = exp2_fast(d);
-      W = (W + S * d) * f;
-      S *= f;
-    }
-    m = to;
-  }
-  // n elements (a multiple of 2)
+// Words of 16 bytes as the element types have them: their largest (a NaN is none), and their pairs.
+template <typename E>
+struct LogWords {
   template <int n>
-  __device__ __forceinline__ void add(const float (&x)[n], float c2) {
-    float top = x[0];
+  static __device__ __forceinline__ float largest(const uint4 (&r)[n]) {
+    using T2 = typename std::conditional<std::is_same<E, ElemBf16>::value, __nv_bfloat162, __half2>::type;
+    auto two = [](uint32_t w) { return *reinterpret_cast<const T2*>(&w); };
+    T2 m = two(r[0].x);
 #pragma unroll
-    for (int i = 1; i < n; ++i) top = fmaxf(top, x[i]);
-    if (top > m) raise(top, c2);
-    const float ref = m == -INFINITY ? 0.0f : m;
-    const uint64_t r2 = f32x2(-ref, -ref), s2 = f32x2(c2, c2);
-    uint64_t Sp = f32x2(S, 0.0f), Wp = f32x2(W, 0.0f);
-#pragma unroll
-    for (int i = 0; i < n; i += 2) {
-      const float2 d = f32x2_get(mul_f32x2(add_f32x2(f32x2(x[i], x[i + 1]), r2), s2));
-      // (2^-200 is 0: a term of -inf has to leave W alone)
-      const float a = max_nan(d.x, -200.0f), b = max_nan(d.y, -200.0f);
-      const uint64_t e = f32x2(exp2_fast(a), exp2_fast(b));
-      Sp = add_f32x2(Sp, e);
-      Wp = fma_f32x2(f32x2(a, b), e, Wp);
+    for (int k = 0; k < n; ++k) {
+      if (k) m = __hmax2(m, two(r[k].x));
+      m = __hmax2(__hmax2(m, two(r[k].y)), __hmax2(two(r[k].z), two(r[k].w)));
     }
-    const float2 s = f32x2_get(Sp), w = f32x2_get(Wp);
-    S = s.x + s.y;
-    W = w.x + w.y;
+    const float2 f = pair(*reinterpret_cast<const uint32_t*>(&m));
+    return fmaxf(f.x, f.y);
+  }
+  static __device__ __forceinline__ float2 pair(uint32_t w) {
+    if constexpr (std::is_same<E, ElemBf16>::value)
+      return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    else
+      return f16x2_to_f32(w);
+  }
+  template <typename Fn>
+  static __device__ __forceinline__ void pairs(const uint4& r, Fn f) {
+    f(pair(r.x));
+    f(pair(r.y));
+    f(pair(r.z));
+    f(pair(r.w));
+  }
+};
+template <>
+struct LogWords<ElemF32> {
+  template <int n>
+  static __device__ __forceinline__ float largest(const uint4 (&r)[n]) {
+    float m = __uint_as_float(r[0].x);
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+      m = fmaxf(fmaxf(m, __uint_as_float(r[k].x)), __uint_as_float(r[k].y));
+      m = fmaxf(fmaxf(m, __uint_as_float(r[k].z)), __uint_as_float(r[k].w));
+    }
+    return m;
+  }
+  template <typename Fn>
+  static __device__ __forceinline__ void pairs(const uint4& r, Fn f) {
+    f(make_float2(__uint_as_float(r.x), __uint_as_float(r.y)));
+    f(make_float2(__uint_as_float(r.z), __uint_as_float(r.w)));
   }
 };
 
-// Row sums with the largest element m left out: o's joined to t's.
-__device__ __forceinline__ void join_sums(LogSums& t, LogSums o, float c2) {
+// The largest element m so far (-inf: none yet), and S and W of all elements so far relative to it, W in base 2; kept in
+// pairs.  Where m c2 is of ordinary size the reference is m c2 rounded, ref, and a term's exponent x c2 - ref one fused
+// rounding (an eighth of the instructions less than (x - m) c2, which rows of the type's lowest value need).
+struct LogSums {
+  float m = -INFINITY, ref = 0.0f;
+  bool plain = false;                  // the reference is ref, not m c2
+  uint64_t S = 0, W = 0;
+
+  // the exponent that takes sums from this reference to to_m c2, or to to_ref
+  __device__ __forceinline__ float rise(float to_m, float to_ref, bool to_plain, float c2) const {
+    return to_plain ? (plain ? ref - to_ref : fmaf(m, c2, -to_ref)) : (plain ? -fmaf(to_m, c2, -ref) : (m - to_m) * c2);
+  }
+  __device__ __forceinline__ void scale(float d) {
+    d = max_nan(d, -200.0f);
+    const float f = exp2_fast(d);
+    const uint64_t f2 = f32x2(f, f);
+    W = mul_f32x2(fma_f32x2(S, f32x2(d, d), W), f2);
+    S = mul_f32x2(S, f2);
+  }
+  __device__ __forceinline__ void raise(float to, float c2) {
+    const float to_ref = to * c2;
+    const bool to_plain = fabsf(to_ref) <= 32768.0f;
+    if (m > -INFINITY) scale(rise(to, to_ref, to_plain, c2));
+    m = to;
+    ref = to_ref;
+    plain = to_plain;
+  }
+  template <typename E, int n>
+  __device__ __forceinline__ void add(const uint4 (&r)[n], float c2) {
+    const float top = LogWords<E>::largest(r);
+    if (top > m) raise(top, c2);
+    const uint64_t S0 = S, W0 = W;
+    if (plain) {
+      const uint64_t r2 = f32x2(-ref, -ref), s2 = f32x2(c2, c2);
+#pragma unroll
+      for (int k = 0; k < n; ++k)
+        LogWords<E>::pairs(r[k], [&](float2 x) {
+          const uint64_t d = fma_f32x2(f32x2(x.x, x.y), s2, r2);
+          const float2 v = f32x2_get(d);
+          const uint64_t e = f32x2(exp2_fast(v.x), exp2_fast(v.y));
+          S = add_f32x2(S, e);
+          W = fma_f32x2(d, e, W);
+        });
+    }
+    const float2 w = f32x2_get(W);
+    if (!plain || !(w.x + w.y == w.x + w.y)) {
+      // an exponent of -inf has to leave W alone (2^-200 is 0)
+      S = S0;
+      W = W0;
+#pragma unroll 1
+      for (int k = 0; k < n; ++k) {
+        const uint4 x4 = k == 0 ? r[0] : k == 1 ? r[n > 1 ? 1 : 0] : k == 2 ? r[n > 2 ? 2 : 0] : r[n - 1];
+        LogWords<E>::pairs(x4, [&](float2 x) { one(x.x, c2), one(x.y, c2); });
+      }
+    }
+  }
+  __device__ __forceinline__ void one(float x, float c2) {
+    const float d = max_nan(plain ? fmaf(x, c2, -ref) : (x - (m == -INFINITY ? 0.0f : m)) * c2, -200.0f);
+    const float e = exp2_fast(d);
+    S = add_f32x2(S, f32x2(e, 0.0f));
+    W = add_f32x2(W, f32x2(d * e, 0.0f));
+  }
+};
+
+// A row's (or a part's) largest element, and S and W of the others relative to it.
+struct LogRest {
+  float m, S, W;
+};
+
+// o's joined to t's.
+__device__ __forceinline__ void join_sums(LogRest& t, LogRest o, float c2) {
   if (o.m > t.m) {
-    const LogSums x = t;
+    const LogRest x = t;
     t = o;
     o = x;
   }
@@ -261,8 +343,8 @@ __device__ int equals_in_order(const LogRow<E, THREADS>& row, LogShared<THREADS>
 }
 
 template <typename E, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1536 / THREADS) logprobs_kernel(const __grid_constant__ LogprobsParams p) {
-  constexpr int VE = LogRow<E, THREADS>::VE, QUAD = THREADS / 128, AHEAD = 4;
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const __grid_constant__ LogprobsParams p) {
+  constexpr int QUAD = THREADS / 128, AHEAD = 6;
   __shared__ LogShared<THREADS> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ranks = p.cluster, rank = ranks > 1 ? (int)cluster_rank() : 0;
@@ -281,25 +363,29 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logprobs_kernel(const
   // ------------------------------------------------------ one pass
   LogSums mine;
   int v = row.v0 + tid;
-  for (; v + (AHEAD - 1) * THREADS < row.v1; v += AHEAD * THREADS) {
+  if (v + (AHEAD - 1) * THREADS < row.v1) {
+    // a batch in the sums, the next one on its way
     uint4 raw[AHEAD];
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) raw[k] = row.load(v + k * THREADS);
+    for (v += AHEAD * THREADS; v + (AHEAD - 1) * THREADS < row.v1; v += AHEAD * THREADS) {
+      uint4 next[AHEAD];
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) {
-      float f[VE];
-      row.floats(raw[k], f);
-      mine.add(f, c2);
+      for (int k = 0; k < AHEAD; ++k) next[k] = row.load(v + k * THREADS);
+      mine.template add<E>(raw, c2);
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) raw[k] = next[k];
     }
+    mine.template add<E>(raw, c2);
   }
   for (; v < row.v1; v += THREADS) {
-    float f[VE];
-    row.floats(row.load(v), f);
-    mine.add(f, c2);
+    const uint4 raw[1] = {row.load(v)};
+    mine.template add<E>(raw, c2);
   }
   if (tid < row.extra) {
-    const float f[2] = {E::get(row.x + row.extra_index(tid)), -INFINITY};
-    mine.add(f, c2);
+    const float x = E::get(row.x + row.extra_index(tid));
+    if (x > mine.m) mine.raise(x, c2);
+    mine.one(x, c2);
   }
 
   // ------------------------------------------------------ the largest, and a bound of the alternatives
@@ -337,9 +423,10 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logprobs_kernel(const
   // everyone's sums relative to M; the owner's come again without the largest
   float S = 0.0f, W = 0.0f;
   if (tid != owner) {
-    if (mine.m > -INFINITY) mine.raise(M, c2);
-    S = mine.S;
-    W = mine.W;
+    if (mine.m > -INFINITY) mine.scale(mine.rise(M, 0.0f, false, c2));
+    const float2 s = f32x2_get(mine.S), w = f32x2_get(mine.W);
+    S = s.x + s.y;
+    W = w.x + w.y;
   }
   __syncthreads();
   const int n_hot = sh.n_hot;
@@ -415,9 +502,7 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logprobs_kernel(const
       }
     }
   }
-  LogSums sum;
-  sum.m = M;
-  sum.S = sum.W = 0.0f;
+  LogRest sum = {M, 0.0f, 0.0f};
   for (int w = 0; w < THREADS / 32; ++w) {
     sum.S += sh.warp_S[w];
     sum.W += sh.warp_W[w];
@@ -437,13 +522,7 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logprobs_kernel(const
     }
     cluster_sync();
     if (rank != 0) return;
-    for (int k = 1; k < ranks; ++k) {
-      LogSums o;
-      o.m = sh.sums[k][0];
-      o.S = sh.sums[k][1];
-      o.W = sh.sums[k][2];
-      join_sums(sum, o, c2);
-    }
+    for (int k = 1; k < ranks; ++k) join_sums(sum, LogRest{sh.sums[k][0], sh.sums[k][1], sh.sums[k][2]}, c2);
   }
   const bool finite = fabsf(sum.m) != INFINITY && sum.S == sum.S;
   const float nan = __uint_as_float(0x7fffffffu), log_sum = finite ? log1pf(sum.S) : nan;
