@@ -1,10 +1,13 @@
 // Eviction by accumulated weight: which keys of a (sequence, cached head) stay, and their rows' copy.
 //
-// Weights map to 32-bit whole numbers of the same order.  A cluster takes the positions of a (sequence, head) between
-// its CTAs, each reads its share once into shared memory; the weight of the last key that stays is found by three
-// histograms of 11, 11 and 10 bits from the top, of the keys that agree in the bits above, added up over the cluster.
-// Then every CTA knows how many keys stay, and how many equals, before its share, and writes its part of the kept
-// positions in their order.
+// Weights map to 32-bit whole numbers of the same order.  One CTA takes a (sequence, head) and reads its weights once,
+// into shared memory as far as they fit.  The weight of the last key that stays is found from the top: a histogram of
+// 12 bits over all keys that compete, then two of 10 bits over those that agree so far, which are few and kept in a
+// list.  A last walk writes the positions that stay in their order.
+//
+// Latency bounds the selection (a chain of scans), HBM the copy: 8 sequences of 16 to 32 thousand keys of 8 heads of
+// 128 in bf16 to 8192 keys: EVICT_TIMES.  Clusters of four CTAs a head, with histograms added up over distributed
+// shared memory, took 40 us for the selection alone.
 #include <algorithm>
 
 #include "kv_paged.h"
@@ -20,7 +23,7 @@ struct EvictParams {
   int32_t *kept, *new_lens;
   long long mass_rs, mass_out_rs;
   int keep, sinks, recent;
-  int cluster, cached;                 // CTAs of a (sequence, head); weights a CTA holds in shared memory
+  int cached;                          // weights held in shared memory
   FastDiv by_chunks;                   // by the CTAs that copy one's rows
 };
 
@@ -35,15 +38,16 @@ __device__ __forceinline__ int evict_len(const EvictParams& p, int s) {
   return (int)min((long long)p.src.len(p.lens, s), p.mass_rs);
 }
 
-constexpr int kEvictThreads = 512, kEvictWarps = kEvictThreads / 32;
-constexpr int kEvictMost = 40960;      // positions of a CTA whose weights stay in shared memory
-constexpr int kEvictCluster = 8;
+constexpr int kEvictThreads = 1024, kEvictWarps = kEvictThreads / 32;
+constexpr int kEvictMost = 49152;      // positions whose weights stay in shared memory
+constexpr int kEvictList = 2048;       // keys that agree with the threshold's first bits, where they are no more
+constexpr int kEvictBins = 4096;
 
 struct EvictShared {
-  int hist[2048];
+  int hist[kEvictBins];
+  uint32_t list[kEvictList];
   int warp[kEvictWarps];
-  int digit, left;                     // of the threshold's digit; how many of its equals stay
-  int counts[kEvictCluster][2];        // of every CTA: keys that stay, and equals of the threshold
+  int digit, left, n_list;             // of the threshold's digit; how many of its equals stay
 };
 
 // Sum over the CTA's threads before this one, and the total.
@@ -58,154 +62,132 @@ __device__ __forceinline__ int evict_scan(int v, int* s_warp, int& total) {
   __syncthreads();                     // (the last scan's sums are read)
   if (lane == 31) s_warp[warp] = upto;
   __syncthreads();
-  int base = 0;
-  total = 0;
+  int sums = s_warp[lane];             // every warp scans the warps' sums
 #pragma unroll
-  for (int w = 0; w < kEvictWarps; ++w) {
-    const int o = s_warp[w];
-    base += w < warp ? o : 0;
-    total += o;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, sums, d);
+    if (lane >= d) sums += o;
   }
-  return base + upto - v;
+  total = __shfl_sync(0xffffffffu, sums, 31);
+  const int base = __shfl_sync(0xffffffffu, sums, (warp + 31) & 31);
+  return (warp ? base : 0) + upto - v;
+}
+
+// From a histogram of SIZE bins: the bin from the top in which `left` of its and higher ones' keys are reached (into
+// sh.digit), and how many of its own that takes (sh.left).  The bins are zeros afterwards.
+template <int SIZE>
+__device__ __forceinline__ void evict_digit(EvictShared& sh, int left) {
+  constexpr int B = SIZE / kEvictThreads;
+  __syncthreads();
+  int c[B], sum = 0;
+#pragma unroll
+  for (int k = 0; k < B; ++k) sum += c[k] = sh.hist[SIZE - 1 - ((int)threadIdx.x * B + k)];
+  int total;
+  int above = evict_scan(sum, sh.warp, total);
+#pragma unroll
+  for (int k = 0; k < B; ++k) {
+    const int b = SIZE - 1 - ((int)threadIdx.x * B + k);
+    if (above < left && above + c[k] >= left) {
+      sh.digit = b;
+      sh.left = left - above;
+    }
+    above += c[k];
+    sh.hist[b] = 0;
+  }
+  __syncthreads();
 }
 
 __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
-  extern __shared__ uint32_t s_w[];    // the share's weights, as far as they fit
+  extern __shared__ __align__(16) uint32_t s_w[];   // weights by position, as far as they fit
   __shared__ EvictShared sh;
-  const int ranks = p.cluster, rank = ranks > 1 ? (int)cluster_rank() : 0, tid = threadIdx.x;
-  const int plane = (int)(blockIdx.x / (unsigned)ranks), s = plane / p.src.H_kv;
+  const int tid = threadIdx.x, plane = blockIdx.x, s = plane / p.src.H_kv;
+#pragma unroll
+  for (int i = tid; i < kEvictBins; i += kEvictThreads) sh.hist[i] = 0;
+  if (tid == 0) sh.n_list = 0;
   griddep_launch_dependents();
   griddep_wait();
   const int n = evict_len(p, s), m = min(n, p.keep);
   const float* mass = p.mass + plane * p.mass_rs;
   int32_t* kept = p.kept + (long long)plane * p.keep;
-  if (rank == 0 && tid == 0 && plane % p.src.H_kv == 0) p.new_lens[s] = m;
-  for (int i = m + rank * kEvictThreads + tid; i < p.keep; i += ranks * kEvictThreads) kept[i] = -1;
+  if (tid == 0 && plane % p.src.H_kv == 0) p.new_lens[s] = m;
+  for (int i = m + tid; i < p.keep; i += kEvictThreads) kept[i] = -1;
   if (n <= p.keep) {
-    for (int i = rank * kEvictThreads + tid; i < n; i += ranks * kEvictThreads) kept[i] = i;
-    return;                            // (all of the cluster)
+    for (int i = tid; i < n; i += kEvictThreads) kept[i] = i;
+    return;
   }
-  for (int i = tid; i < 2048; i += kEvictThreads) sh.hist[i] = 0;
-  if (ranks > 1) cluster_arrive();     // waited for before the first access of another CTA's memory
-  // the positions that compete, and this CTA's share of all
-  const int lo = p.sinks, hi = n - p.recent;
-  int left = p.keep - p.sinks - p.recent;
-  const int t0 = (int)((long long)n * rank / ranks), t1 = (int)((long long)n * (rank + 1) / ranks);
-  const int c0 = min(max(t0, lo), t1), c1 = max(min(t1, hi), c0);
-  auto weight = [&](int t) {
-    const int at = t - c0;
-    return at < p.cached ? s_w[at] : weight_order(mass[t]);
-  };
-  uint32_t bits = 0;                   // the last kept one's weight
-  bool waited = ranks == 1;
+  const int lo = p.sinks, hi = n - p.recent;        // the positions that compete
+  int left = p.keep - p.sinks - p.recent;           // how many of them stay
+  const bool some = left > 0;
+  uint32_t bits = 0;                                // the last kept one's weight
+  auto weight = [&](int t) { return t < p.cached ? s_w[t] : weight_order(mass[t]); };
   __syncthreads();
-  if (left > 0) {
+  if (some) {
+    for (int t = tid; t < n; t += 8 * kEvictThreads) {
+      float x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = t + k * kEvictThreads < n ? mass[t + k * kEvictThreads] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int at = t + k * kEvictThreads;
+        const uint32_t w = weight_order(x[k]);
+        if (at < min(n, p.cached)) s_w[at] = w;
+        if (at >= lo && at < hi) atomicAdd(&sh.hist[w >> 20], 1);
+      }
+    }
+    evict_digit<4096>(sh, left);
+    bits = (uint32_t)sh.digit << 20;
+    left = sh.left;
+    // those that agree: how many they are, the histogram knew; the list holds the first of them at least
+    for (int t = lo + tid; t < hi; t += kEvictThreads) {
+      const uint32_t w = weight(t);
+      if ((w >> 20) == (bits >> 20)) {
+        const int at = *(volatile int*)&sh.n_list <= kEvictList ? atomicAdd(&sh.n_list, 1) : kEvictList;
+        if (at < kEvictList) sh.list[at] = w;
+      }
+    }
+    __syncthreads();
+    const int n_list = sh.n_list;
+    const bool listed = n_list <= kEvictList;
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, size = pass == 2 ? 1024 : 2048;
-      if (pass == 0) {
-        // the share, four loads in flight
-        for (int t = c0 + tid; t < c1; t += 4 * kEvictThreads) {
-          float x[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = t + k * kEvictThreads < c1 ? mass[t + k * kEvictThreads] : 0.0f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int at = t + k * kEvictThreads - c0;
-            if (at >= c1 - c0) break;
-            const uint32_t w = weight_order(x[k]);
-            if (at < p.cached) s_w[at] = w;
-            atomicAdd(&sh.hist[w >> 21], 1);
-          }
-        }
+    for (int pass = 0; pass < 2; ++pass) {
+      const int shift = pass == 0 ? 10 : 0, up = shift + 10;
+      if (listed) {
+        for (int i = tid; i < n_list; i += kEvictThreads)
+          if ((sh.list[i] >> up) == (bits >> up)) atomicAdd(&sh.hist[(sh.list[i] >> shift) & 1023], 1);
       } else {
-        const int up = pass == 1 ? 21 : 10;
-        for (int t = c0 + tid; t < c1; t += kEvictThreads) {
+        for (int t = lo + tid; t < hi; t += kEvictThreads) {
           const uint32_t w = weight(t);
-          if ((w >> up) == (bits >> up)) atomicAdd(&sh.hist[(w >> shift) & (size - 1)], 1);
+          if ((w >> up) == (bits >> up)) atomicAdd(&sh.hist[(w >> shift) & 1023], 1);
         }
       }
-      __syncthreads();
-      constexpr int B = 2048 / kEvictThreads;            // bins of a thread, from the top
-      int c[B], sum = 0;
-      if (ranks > 1) {
-        if (!waited) cluster_wait();
-        if (!waited) waited = true;
-        cluster_sync();                                  // every CTA's histogram is whole
-        for (int k = 0; k < B; ++k) c[k] = 0;
-        for (int r = 0; r < ranks; ++r)
-#pragma unroll
-          for (int k = 0; k < B; ++k) {
-            const int b = size - 1 - (tid * B + k);
-            if (b >= 0) c[k] += cluster_load(cluster_addr(smem_u32(&sh.hist[b]), (uint32_t)r));
-          }
-      } else {
-#pragma unroll
-        for (int k = 0; k < B; ++k) {
-          const int b = size - 1 - (tid * B + k);
-          c[k] = b >= 0 ? sh.hist[b] : 0;
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < B; ++k) sum += c[k];
-      int total;
-      int above = evict_scan(sum, sh.warp, total);       // keys in higher bins
-#pragma unroll
-      for (int k = 0; k < B; ++k) {
-        if (above < left && above + c[k] >= left) {
-          sh.digit = size - 1 - (tid * B + k);
-          sh.left = left - above;
-        }
-        above += c[k];
-      }
-      if (ranks > 1) cluster_sync();                     // the histograms are read
-      __syncthreads();
+      evict_digit<1024>(sh, left);
       bits |= (uint32_t)sh.digit << shift;
       left = sh.left;
-      for (int i = tid; i < 2048; i += kEvictThreads) sh.hist[i] = 0;
-      __syncthreads();
     }
   }
-  const bool some = p.keep > p.sinks + p.recent;         // some of those that compete stay
-  auto kind = [&](int t) {             // 2: stays, 1: an equal of the last one that does
-    if (t < lo || t >= hi) return 2;
-    const uint32_t w = some ? weight(t) : 0;
-    return !some ? 0 : w > bits ? 2 : w == bits ? 1 : 0;
-  };
-  // what the CTAs before this one keep
-  int stay = 0, equal = 0, stays_before = 0, equals_before = 0;
-  if (ranks > 1) {
-    for (int t = t0 + tid; t < t1; t += kEvictThreads) {
-      const int k = kind(t);
-      stay += k >> 1;
-      equal += k & 1;
-    }
-    int stay_all, equal_all;
-    evict_scan(stay, sh.warp, stay_all);
-    evict_scan(equal, sh.warp, equal_all);
-    if (!waited) cluster_wait();
-    if (tid < ranks) {
-      cluster_store_int(cluster_addr(smem_u32(&sh.counts[rank][0]), (uint32_t)tid), stay_all);
-      cluster_store_int(cluster_addr(smem_u32(&sh.counts[rank][1]), (uint32_t)tid), equal_all);
-    }
-    cluster_sync();
-    for (int r = 0; r < rank; ++r) {
-      stays_before += sh.counts[r][0];
-      equals_before += sh.counts[r][1];
-    }
-  }
-  // the kept positions, in order: every thread takes a run
+  // the kept positions, in order: every thread takes a run of 8
   constexpr int RUN = 8;
-  for (int b0 = t0; b0 < t1; b0 += RUN * kEvictThreads) {
+  int stays_before = 0, equals_before = 0;
+  for (int b0 = 0; b0 < n; b0 += RUN * kEvictThreads) {
     const int f = b0 + tid * RUN;
-    uint32_t two = 0, one = 0;
+    uint32_t w[RUN];
+    if (some && f + RUN <= p.cached) {
+      const uint4 a = reinterpret_cast<const uint4*>(s_w + f)[0], c = reinterpret_cast<const uint4*>(s_w + f)[1];
+      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+      w[4] = c.x; w[5] = c.y; w[6] = c.z; w[7] = c.w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < RUN; ++k) w[k] = some && f + k < n ? weight(f + k) : 0;
+    }
+    uint32_t two = 0, one = 0;         // stays whatever comes; an equal of the last one that stays
 #pragma unroll
     for (int k = 0; k < RUN; ++k) {
-      const int x = f + k < t1 ? kind(f + k) : 0;
-      two |= (uint32_t)(x >> 1) << k;
-      one |= (uint32_t)(x & 1) << k;
+      const int t = f + k;
+      const bool fixed = t < n && (t < lo || t >= hi), competes = some && t >= lo && t < hi;
+      two |= (uint32_t)(fixed || (competes && w[k] > bits)) << k;
+      one |= (uint32_t)(competes && w[k] == bits) << k;
     }
-    // equals stay while there is room: both counts in one scan (16 bits each hold RUN * threads)
+    // both counts in one scan (16 bits each hold RUN * threads)
     int total;
     const int base = evict_scan(__popc(two) | __popc(one) << 16, sh.warp, total);
     int eq = equals_before + (base >> 16);
@@ -301,7 +283,7 @@ extern "C" dllm_status dllm_op_kv_paged_evict(const dllm_kv_paged* src, const dl
                    p.mass_out_rs, keep);
   if ((const void*)mass == mass_out) return op_fail(DLLM_EINVAL, "kv_paged_evict: mass_out is mass");
   const long long planes = (long long)src->b * src->H_kv;
-  if (planes > 0x7fffffff / kEvictCluster || (double)planes * ((keep + 63) / 64) > 0x7fffffff)
+  if (planes > 0x7fffffff || (double)planes * ((keep + 63) / 64) > 0x7fffffff)
     return op_fail(DLLM_EINVAL, "kv_paged_evict: b=%d H_kv=%d keep=%d are too many for one call", src->b, src->H_kv, keep);
   p.mass = mass;
   p.mass_out = mass_out;
@@ -312,18 +294,9 @@ extern "C" dllm_status dllm_op_kv_paged_evict(const dllm_kv_paged* src, const dl
   p.sinks = sinks;
   p.recent = recent;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // CTAs of a (sequence, head): 4096 positions each, as far as that fills the GPU; more where they do not fit in shared memory
-  const long long most = std::min(p.src.positions, p.mass_rs);
-  p.cluster = 1;
-  while (p.cluster < kEvictCluster && most > 4096LL * p.cluster &&
-         (planes * p.cluster * 2 <= 2LL * op_device_sms() || most > (long long)kEvictMost * p.cluster))
-    p.cluster *= 2;
-  const long long share = (most + p.cluster - 1) / p.cluster;
-  p.cached = (int)std::min<long long>(share, kEvictMost);
-  const int smem = (p.cached + 3) / 4 * 16;
+  p.cached = (int)std::min<long long>((std::min(p.src.positions, p.mass_rs) + 7) / 8 * 8, kEvictMost);
   OP_CK(op_smem_once(reinterpret_cast<const void*>(evict_select_kernel), kEvictMost * 4));
-  OP_CK(op_launch(evict_select_kernel, dim3((unsigned)(planes * p.cluster)), dim3(kEvictThreads), (size_t)smem, st,
-                  p.cluster, p));
+  OP_CK(op_launch(evict_select_kernel, dim3((unsigned)planes), dim3(kEvictThreads), (size_t)p.cached * 4, st, 1, p));
   OP_CK(src->hd == 64 ? launch_evict_copy<64>(p, planes, st) : launch_evict_copy<128>(p, planes, st));
   return DLLM_OK;
 }

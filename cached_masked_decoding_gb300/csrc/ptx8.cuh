@@ -311,13 +311,4 @@ __device__ __forceinline__ void cluster_store(uint32_t caddr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(caddr), "f"(v) : "memory");
 }
 
-__device__ __forceinline__ void cluster_store_int(uint32_t caddr, int v) {
-  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(caddr), "r"(v) : "memory");
-}
-__device__ __forceinline__ int cluster_load(uint32_t caddr) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(caddr) : "memory");
-  return v;
-}
-
 }  // namespace dllm
