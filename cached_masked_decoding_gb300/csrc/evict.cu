@@ -42,6 +42,7 @@ constexpr int kEvictThreads = 1024, kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictMost = 49152;      // positions whose weights stay in shared memory
 constexpr int kEvictList = 2048;       // keys that agree with the threshold's first bits, where they are no more
 constexpr int kEvictBins = 4096;
+constexpr uint32_t kEvictFixed = 0xffffffffu;   // the weight of what stays in any case
 
 struct EvictShared {
   int hist[kEvictBins];
@@ -115,89 +116,94 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
     for (int i = tid; i < n; i += kEvictThreads) kept[i] = i;
     return;
   }
-  const int lo = p.sinks, hi = n - p.recent;        // the positions that compete
-  int left = p.keep - p.sinks - p.recent;           // how many of them stay
-  const bool some = left > 0;
-  uint32_t bits = 0;                                // the last kept one's weight
-  auto weight = [&](int t) { return t < p.cached ? s_w[t] : weight_order(mass[t]); };
+  // Those that stay whatever their weight count as heavier than all others; then keep of n stay.
+  const int lo = p.sinks, hi = n - p.recent, held = min(n, p.cached);
+  auto weight = [&](int t) {
+    return t < p.cached ? s_w[t] : t < lo || t >= hi ? kEvictFixed : weight_order(mass[t]);
+  };
+  for (int i = tid; i < lo + n - hi; i += kEvictThreads) {
+    const int t = i < lo ? i : hi + i - lo;
+    if (t < held) s_w[t] = kEvictFixed;
+  }
   __syncthreads();
-  if (some) {
-    for (int t = tid; t < n; t += 8 * kEvictThreads) {
-      float x[8];
+  if (tid == 0) atomicAdd(&sh.hist[kEvictBins - 1], lo + n - hi);
+  auto count = [&](int t, float x) {
+    const uint32_t w = weight_order(x);
+    if (t < held) s_w[t] = w;
+    atomicAdd(&sh.hist[w >> 20], 1);
+  };
+  int t = lo + tid;
+  for (; t + 7 * kEvictThreads < hi; t += 8 * kEvictThreads) {
+    float x[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = t + k * kEvictThreads < n ? mass[t + k * kEvictThreads] : 0.0f;
+    for (int k = 0; k < 8; ++k) x[k] = mass[t + k * kEvictThreads];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int at = t + k * kEvictThreads;
-        const uint32_t w = weight_order(x[k]);
-        if (at < min(n, p.cached)) s_w[at] = w;
-        if (at >= lo && at < hi) atomicAdd(&sh.hist[w >> 20], 1);
-      }
+    for (int k = 0; k < 8; ++k) count(t + k * kEvictThreads, x[k]);
+  }
+  for (; t < hi; t += kEvictThreads) count(t, mass[t]);
+  int left = p.keep;
+  evict_digit<4096>(sh, left);
+  uint32_t bits = (uint32_t)sh.digit << 20;         // the last kept one's weight
+  left = sh.left;                                   // how many of those that agree stay
+  // Those that agree; a list holds them where they are few.
+  auto agree = [&](uint32_t w) {
+    if ((w >> 20) == (bits >> 20) && *(volatile int*)&sh.n_list <= kEvictList) {
+      const int at = atomicAdd(&sh.n_list, 1);
+      if (at < kEvictList) sh.list[at] = w;
     }
-    evict_digit<4096>(sh, left);
-    bits = (uint32_t)sh.digit << 20;
-    left = sh.left;
-    // those that agree: how many they are, the histogram knew; the list holds the first of them at least
-    for (int t = lo + tid; t < hi; t += kEvictThreads) {
-      const uint32_t w = weight(t);
-      if ((w >> 20) == (bits >> 20)) {
-        const int at = *(volatile int*)&sh.n_list <= kEvictList ? atomicAdd(&sh.n_list, 1) : kEvictList;
-        if (at < kEvictList) sh.list[at] = w;
-      }
-    }
-    __syncthreads();
-    const int n_list = sh.n_list;
-    const bool listed = n_list <= kEvictList;
+  };
+  for (int f = 4 * tid; f < held; f += 4 * kEvictThreads) {
+    const uint4 w = *reinterpret_cast<const uint4*>(s_w + f);   // (past held: of no account)
+    agree(w.x);
+    if (f + 1 < held) agree(w.y);
+    if (f + 2 < held) agree(w.z);
+    if (f + 3 < held) agree(w.w);
+  }
+  for (int f = held + tid; f < n; f += kEvictThreads) agree(weight(f));
+  __syncthreads();
+  const int n_list = sh.n_list;
+  const bool listed = n_list <= kEvictList;
 #pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-      const int shift = pass == 0 ? 10 : 0, up = shift + 10;
-      if (listed) {
-        for (int i = tid; i < n_list; i += kEvictThreads)
-          if ((sh.list[i] >> up) == (bits >> up)) atomicAdd(&sh.hist[(sh.list[i] >> shift) & 1023], 1);
-      } else {
-        for (int t = lo + tid; t < hi; t += kEvictThreads) {
-          const uint32_t w = weight(t);
-          if ((w >> up) == (bits >> up)) atomicAdd(&sh.hist[(w >> shift) & 1023], 1);
-        }
-      }
-      evict_digit<1024>(sh, left);
-      bits |= (uint32_t)sh.digit << shift;
-      left = sh.left;
+  for (int pass = 0; pass < 2; ++pass) {
+    const int shift = pass == 0 ? 10 : 0, up = shift + 10;
+    for (int i = tid; i < (listed ? n_list : n); i += kEvictThreads) {
+      const uint32_t w = listed ? sh.list[i] : weight(i);
+      if ((w >> up) == (bits >> up)) atomicAdd(&sh.hist[(w >> shift) & 1023], 1);
     }
+    evict_digit<1024>(sh, left);
+    bits |= (uint32_t)sh.digit << shift;
+    left = sh.left;
   }
   // the kept positions, in order: every thread takes a run of 8
   constexpr int RUN = 8;
   int stays_before = 0, equals_before = 0;
   for (int b0 = 0; b0 < n; b0 += RUN * kEvictThreads) {
     const int f = b0 + tid * RUN;
-    uint32_t w[RUN];
-    if (some && f + RUN <= p.cached) {
+    uint32_t above = 0, equal = 0;
+    if (f + RUN <= held) {
       const uint4 a = reinterpret_cast<const uint4*>(s_w + f)[0], c = reinterpret_cast<const uint4*>(s_w + f)[1];
-      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-      w[4] = c.x; w[5] = c.y; w[6] = c.z; w[7] = c.w;
+      const uint32_t w[RUN] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int k = 0; k < RUN; ++k) {
+        above |= w[k] > bits ? 1u << k : 0;
+        equal |= w[k] == bits ? 1u << k : 0;
+      }
     } else {
-#pragma unroll
-      for (int k = 0; k < RUN; ++k) w[k] = some && f + k < n ? weight(f + k) : 0;
-    }
-    uint32_t two = 0, one = 0;         // stays whatever comes; an equal of the last one that stays
-#pragma unroll
-    for (int k = 0; k < RUN; ++k) {
-      const int t = f + k;
-      const bool fixed = t < n && (t < lo || t >= hi), competes = some && t >= lo && t < hi;
-      two |= (uint32_t)(fixed || (competes && w[k] > bits)) << k;
-      one |= (uint32_t)(competes && w[k] == bits) << k;
+      for (int k = 0; k < RUN && f + k < n; ++k) {
+        const uint32_t w = weight(f + k);
+        above |= w > bits ? 1u << k : 0;
+        equal |= w == bits ? 1u << k : 0;
+      }
     }
     // both counts in one scan (16 bits each hold RUN * threads)
     int total;
-    const int base = evict_scan(__popc(two) | __popc(one) << 16, sh.warp, total);
-    int eq = equals_before + (base >> 16);
+    const int base = evict_scan(__popc(above) | __popc(equal) << 16, sh.warp, total);
+    const int eq = equals_before + (base >> 16);
     int at = stays_before + (base & 0xffff) + min(eq, left);
-#pragma unroll
-    for (int k = 0; k < RUN; ++k) {
-      const bool e = (one >> k) & 1;
-      if ((two >> k) & 1 || (e && eq < left)) kept[at++] = f + k;
-      eq += e ? 1 : 0;
-    }
+    // of the run's equals, those that there is room for
+    uint32_t room = equal;
+    for (int over = __popc(equal) - max(left - eq, 0); over > 0 && room; --over) room &= ~(1u << (31 - __clz(room)));
+    for (uint32_t stay = above | room; stay; stay &= stay - 1) kept[at++] = f + __ffs(stay) - 1;
     stays_before += total & 0xffff;
     equals_before += total >> 16;
   }
