@@ -4,9 +4,11 @@
 //
 // Bound by HBM: every element is read once and written once.  A lane owns 8
 // pairs of a head - two 16-byte vectors of 16-bit elements, the members of a pair
-// in one thread - so a head of 128 is 8 lanes and its mean three shuffles.  A CTA
-// takes whole rows: their cosines and sines are worked out once, by one thread a
-// pair, while the first elements are on their way.
+// in one thread - so a head of 128 is 8 lanes and its mean three shuffles.  A thread
+// keeps its head (its weights and addresses) over a run of rows, which come into a ring in shared memory
+// by bulk copies, up to 64 KB ahead; the cosines and sines of up to 1024 pairs of rows to come
+// are worked out at once, one a thread.
+// HEADS_TIMES
 #include <algorithm>
 
 #include "kv_paged.h"
@@ -25,161 +27,240 @@ struct HeadsParams {
   float eps, amp, inv_hd;
   int norm, rot, interleaved;
   int rows, H, H_kv, hd, heads;        // heads: of a row, over q, k and (paged) v
-  int row_run;                         // rows of a CTA
-  FastDiv by_heads, by_R;
+  int step, batch, run;                // rows of a CTA at once, with angles at hand, in all
+  int chunk;                           // heads of a CTA
+  int stages, row_bytes;               // of the ring, each `step` rows of a chunk's heads
+  FastDiv by_chunk, by_R;
   int R;
   PagedKv c;
   uint64_t turns[kMaxPairs];           // turns per position * 2^64
 };
 
-constexpr int kHeadsAngles = 1024;     // pairs of a CTA's rows
+constexpr int kHeadsAngles = 1024;     // pairs of a batch of rows
 constexpr int kHeadsRows = 64;         // and most rows
+constexpr int kHeadsStages = 8;
+constexpr int kHeadsRing = 64 * 1024;
+
+static __device__ int g_heads_err[1];
 
 // E, O: element types in and out; L: lanes of a head (8 pairs each, some idle where hd / 16 is no power of two).
 template <typename E, typename O, int L, bool PAGED>
-__global__ void __launch_bounds__(512, sizeof(typename E::T) == 2 ? 2 : 1)
-    heads_kernel(const __grid_constant__ HeadsParams p) {
+__global__ void __launch_bounds__(512, 2) heads_kernel(const __grid_constant__ HeadsParams p) {
   using T = typename E::T;
   using TO = typename O::T;
-  constexpr int ITEMS = 2;                         // heads of a thread in flight
-  __shared__ float2 s_cs[kHeadsAngles];            // [row][pair] cosine and sine
+  extern __shared__ __align__(16) uint8_t s_ring[];
+  // [row][4][lanes]: cosines of a lane's first and last four pairs, then the sines
+  __shared__ float4 s_cs[kHeadsAngles / 2];
   __shared__ long long s_slot[kHeadsRows];         // row of the cache's head 0, or -1: the row takes no part
-  const int row0 = blockIdx.x * p.row_run, n_rows = min(p.row_run, p.rows - row0), pairs = p.rot / 2;
-  const int l = threadIdx.x % L, group = threadIdx.x / L, groups = blockDim.x / L;
-  const int items = n_rows * p.heads, first = 8 * l;   // first: the lane's first pair
+  __shared__ uint64_t s_full[kHeadsStages], s_empty[kHeadsStages];
+  __shared__ int s_abort;
+  float* s_angle = reinterpret_cast<float*>(s_cs);
+  const int row0 = blockIdx.x * p.run, rows = min(p.run, p.rows - row0), pairs = p.rot / 2, turners = pairs / 8;
+  const int l = threadIdx.x % L, first = 8 * l;    // first: the lane's first pair
+  // this thread's head, and its row of those taken at once
+  uint32_t in_chunk;
+  const int sub = (int)p.by_chunk.divmod(threadIdx.x / L, in_chunk);
+  const int h = (int)(blockIdx.y * p.chunk + in_chunk);
+  const bool mine = sub < p.step && h < p.heads && l * 16 < p.hd;
+  const int kind = h < p.H ? 0 : h < p.H + p.H_kv ? 1 : 2;                     // q, k, v
+  const int g = h - (kind == 0 ? 0 : kind == 1 ? p.H : p.H + p.H_kv);
+  const bool turns = kind < 2 && first < pairs, norm = p.norm && kind < 2;
+  // elements a and b: the pairs' members, or 16 in a row
+  const int a = turns && !p.interleaved ? first : 2 * first, b = turns && !p.interleaved ? first + pairs : a + 8;
+  TO* out = kind == 0 ? static_cast<TO*>(p.q_out) + (long long)g * p.hd
+            : PAGED   ? reinterpret_cast<TO*>(kind == 1 ? p.c.k : p.c.v) + (((long long)g << p.c.page_shift)) * p.hd
+                      : static_cast<TO*>(p.k_out) + (long long)g * p.hd;
+  const long long out_rs = kind == 0 ? p.q_out_rs : p.k_out_rs;
+  const int steps = (rows + p.step - 1) / p.step;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], blockDim.x / 32);
+    }
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  // step k's rows to their stage, by one thread: the chunk's heads lie in up to three arrays
+  auto fetch = [&](int k, int at) {
+    const int r0 = k * p.step, n = min(p.step, rows - r0), h0 = blockIdx.y * p.chunk;
+    const int h1 = min(h0 + p.chunk, p.heads);
+    mbar_arrive_expect_tx(&s_full[at], (uint32_t)(n * (h1 - h0) * p.hd) * (uint32_t)sizeof(T));
+    for (int r = 0; r < n; ++r) {
+      const long long row = row0 + r0 + r;
+      uint8_t* to = s_ring + (at * p.step + r) * p.row_bytes;
+#pragma unroll
+      for (int i = 0; i < (PAGED ? 3 : 2); ++i) {
+        const int lo = i == 0 ? 0 : i == 1 ? p.H : p.H + p.H_kv, hi = lo + (i == 0 ? p.H : p.H_kv);
+        const int from = max(lo, h0), until = min(hi, h1);
+        if (from >= until) continue;
+        const T* src = static_cast<const T*>(i == 0 ? p.q : i == 1 ? p.k : p.v) +
+                       row * (i == 0 ? p.q_rs : i == 1 ? p.k_rs : p.v_rs) + (long long)(from - lo) * p.hd;
+        bulk_load(to + (from - h0) * p.hd * (int)sizeof(T), src, (uint32_t)((until - from) * p.hd) * (uint32_t)sizeof(T),
+                  &s_full[at]);
+      }
+    }
+  };
   griddep_launch_dependents();
   griddep_wait();
+  __syncthreads();
+  int issued = min(p.stages, steps);               // steps under way or done (thread 0)
+  if (threadIdx.x == 0)
+    for (int k = 0; k < issued; ++k) fetch(k, k);
+  const T* mine_at = reinterpret_cast<const T*>(s_ring) + (long long)sub * (p.row_bytes / (int)sizeof(T)) + in_chunk * p.hd;
+  Raw8<E> wa, wb;
+  const T* w = static_cast<const T*>(kind == 0 ? p.q_w : p.k_w);
+  const bool weighted = norm && w != nullptr && mine;
+  if (weighted) {
+    wa.load(w + a);
+    wb.load(w + b);
+  }
+  const int stage_elems = p.step * (p.row_bytes / (int)sizeof(T));
+  int stage = 0, last = -1;                        // of the ring: this step's, and the step's before
+  uint32_t phase = 0;
 
-  struct Item {
-    Raw8<E> a, b;
-    int r, kind, g;                                // row of the CTA; q, k, v; head
-    bool on;
-    __device__ __forceinline__ bool turns(int first, int pairs) const { return kind < 2 && first < pairs; }
-  };
-  // elements a and b: the pairs' members, or 16 in a row
-  auto at_a = [&](bool turns) { return turns && !p.interleaved ? first : 2 * first; };
-  auto at_b = [&](bool turns) { return turns && !p.interleaved ? first + pairs : 2 * first + 8; };
-  auto load = [&](Item& x, int it) {
-    x.on = it < items && l * 16 < p.hd;
-    uint32_t h = 0;
-    x.r = x.on ? (int)p.by_heads.divmod((uint32_t)it, h) : 0;
-    x.kind = (int)h < p.H ? 0 : (int)h < p.H + p.H_kv ? 1 : 2;
-    x.g = (int)h - (x.kind == 0 ? 0 : x.kind == 1 ? p.H : p.H + p.H_kv);
-    if (!x.on) return;
-    const long long row = row0 + x.r;
-    const T* src = (x.kind == 0   ? static_cast<const T*>(p.q) + row * p.q_rs
-                    : x.kind == 1 ? static_cast<const T*>(p.k) + row * p.k_rs
-                                  : static_cast<const T*>(p.v) + row * p.v_rs) +
-                   (long long)x.g * p.hd;
-    const bool t = x.turns(first, pairs);
-    x.a.load(src + at_a(t));
-    x.b.load(src + at_b(t));
-  };
-  auto finish = [&](const Item& x) {
-    float va[8], vb[8];
-    const bool on = x.on && (!PAGED || s_slot[x.r] >= 0), turns = x.turns(first, pairs);
-    if (on) {
-      x.a.floats(va);
-      x.b.floats(vb);
-    }
-    if (p.norm) {
-      float sum = 0.0f;
-      if (on) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum += va[e] * va[e] + vb[e] * vb[e];
+  for (int r0 = 0; r0 < rows; r0 += p.batch) {
+    const int n = min(p.batch, rows - r0);
+    if (r0 > 0) __syncthreads();
+    for (int r = threadIdx.x; PAGED && r < n; r += blockDim.x) {
+      uint32_t i;
+      const int s = (int)p.by_R.divmod((uint32_t)(row0 + r0 + r), i);
+      const int count = p.counts ? p.counts[s] : p.R;
+      const long long at = (long long)(p.starts ? p.starts[s] : 0) + i;
+      long long slot = -1;
+      if ((int)i < count && at >= 0 && at < p.c.positions) {
+        const int page = p.c.table[(long long)s * p.c.max_pages + (at >> p.c.page_shift)];
+        if ((unsigned)page < (unsigned)p.c.pages)
+          slot = (((long long)page * p.H_kv) << p.c.page_shift) + (at & ((1 << p.c.page_shift) - 1));
       }
-#pragma unroll
-      for (int d = L / 2; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      if (on && x.kind < 2) {
-        const float inv = 1.0f / sqrtf(sum * p.inv_hd + p.eps);
-        const T* w = static_cast<const T*>(x.kind == 0 ? p.q_w : p.k_w);
-        float wa[8], wb[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) wa[e] = wb[e] = 1.0f;
-        if (w) {
-          E::load8(w + at_a(turns), wa);
-          E::load8(w + at_b(turns), wb);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          va[e] = va[e] * inv * wa[e];
-          vb[e] = vb[e] * inv * wb[e];
-        }
-      }
+      s_slot[r] = slot;
     }
-    if (!on) return;
-    if (turns) {
-      const float2* cs = s_cs + x.r * pairs + first;
-      if (p.interleaved) {
+    for (int e = threadIdx.x; e < n * pairs; e += blockDim.x) {
+      const int r = e / pairs, i = e - r * pairs, row = row0 + r0 + r;
+      int pos = 0;
+      if (p.pos) {
+        pos = p.pos[row];
+      } else if (PAGED) {                           // its place in the cache
+        uint32_t k;
+        const int s = (int)p.by_R.divmod((uint32_t)row, k);
+        pos = (int)((p.starts ? p.starts[s] : 0) + (long long)k);
+      }
+      float c, s;
+      turn_cos_sin(p.turns[i], pos, p.amp, c, s);
+      float* to = s_angle + ((r * 4 + ((i >> 2) & 1)) * turners + (i >> 3)) * 4 + (i & 3);
+      to[0] = c;
+      to[8 * turners] = s;
+    }
+    __syncthreads();
+    for (int k = 0; k < n; k += p.step) {
+      const int r = k + sub;
+      mbar_wait(&s_full[stage], phase, &s_abort, g_heads_err, ERR_HEADS);
+      // the head's elements in pairs of neighbours
+      uint64_t va[4] = {}, vb[4] = {};
+      if (mine && r < n) {
+        const T* src = mine_at + stage * stage_elems;
+        float f[8];
+        E::load8(src + a, f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) va[e] = f32x2(f[2 * e], f[2 * e + 1]);
+        E::load8(src + b, f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) vb[e] = f32x2(f[2 * e], f[2 * e + 1]);
+      }
+      __syncwarp();
+      if (threadIdx.x % 32 == 0) mbar_arrive(&s_empty[stage]);
+      // the stage of the step before takes the rows that come `stages` behind it
+      if (threadIdx.x == 0 && last >= 0 && issued < steps &&
+          mbar_wait(&s_empty[last], last < stage ? phase : phase ^ 1u, &s_abort, g_heads_err, ERR_HEADS)) {
+        fetch(issued, last);
+        ++issued;
+      }
+      __syncwarp();
+      last = stage;
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+      float inv = 1.0f;
+      if (p.norm) {
+        uint64_t sq = mul_f32x2(va[0], va[0]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float a0 = va[2 * e], a1 = va[2 * e + 1], b0 = vb[2 * e], b1 = vb[2 * e + 1];
-          va[2 * e] = a0 * cs[e].x - a1 * cs[e].y;
-          va[2 * e + 1] = a1 * cs[e].x + a0 * cs[e].y;
-          vb[2 * e] = b0 * cs[e + 4].x - b1 * cs[e + 4].y;
-          vb[2 * e + 1] = b1 * cs[e + 4].x + b0 * cs[e + 4].y;
+          if (e > 0) sq = fma_f32x2(va[e], va[e], sq);
+          sq = fma_f32x2(vb[e], vb[e], sq);
         }
-      } else {
+        const float2 h2 = f32x2_get(sq);
+        float sum = h2.x + h2.y;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float x0 = va[e], x1 = vb[e];
-          va[e] = x0 * cs[e].x - x1 * cs[e].y;
-          vb[e] = x1 * cs[e].x + x0 * cs[e].y;
+        for (int d = L / 2; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (norm) inv = rsqrtf(sum * p.inv_hd + p.eps);
+      }
+      if (!mine || r >= n) continue;
+      const long long slot = PAGED ? s_slot[r] : 0;
+      if (PAGED && slot < 0) continue;
+      if (norm) {
+        const uint64_t inv2 = f32x2(inv, inv);
+        if (weighted) {
+          float f[8];
+          wa.floats(f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) va[e] = mul_f32x2(va[e], f32x2(f[2 * e], f[2 * e + 1]));
+          wb.floats(f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) vb[e] = mul_f32x2(vb[e], f32x2(f[2 * e], f[2 * e + 1]));
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          va[e] = mul_f32x2(va[e], inv2);
+          vb[e] = mul_f32x2(vb[e], inv2);
         }
       }
-    }
-    const long long row = row0 + x.r;
-    TO* out;
-    if (x.kind == 0)
-      out = static_cast<TO*>(p.q_out) + row * p.q_out_rs + (long long)x.g * p.hd;
-    else if constexpr (PAGED)
-      out = reinterpret_cast<TO*>(x.kind == 1 ? p.c.k : p.c.v) + (s_slot[x.r] + ((long long)x.g << p.c.page_shift)) * p.hd;
-    else
-      out = static_cast<TO*>(p.k_out) + row * p.k_out_rs + (long long)x.g * p.hd;
-    O::store8(out + at_a(turns), va);
-    O::store8(out + at_b(turns), vb);
-  };
-
-  // the first heads on their way while the rows' places and angles are worked out
-  Item x[ITEMS];
+      if (turns) {
+        const float4* cs = s_cs + r * 4 * turners + l;
+        if (p.interleaved) {
+          const float4 c0 = cs[0], c1 = cs[turners], s0 = cs[2 * turners], s1 = cs[3 * turners];
+          const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+          const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
-  for (int k = 0; k < ITEMS; ++k) load(x[k], group + k * groups);
-  for (int r = threadIdx.x; PAGED && r < n_rows; r += blockDim.x) {
-    uint32_t i;
-    const int s = (int)p.by_R.divmod((uint32_t)(row0 + r), i);
-    const int n = p.counts ? p.counts[s] : p.R;
-    const long long at = (long long)(p.starts ? p.starts[s] : 0) + i;
-    long long slot = -1;
-    if ((int)i < n && at >= 0 && at < p.c.positions) {
-      const int page = p.c.table[(long long)s * p.c.max_pages + (at >> p.c.page_shift)];
-      if ((unsigned)page < (unsigned)p.c.pages)
-        slot = (((long long)page * p.H_kv) << p.c.page_shift) + (at & ((1 << p.c.page_shift) - 1));
-    }
-    s_slot[r] = slot;
-  }
-  for (int a = threadIdx.x; a < n_rows * pairs; a += blockDim.x) {
-    const int r = a / pairs, i = a - r * pairs;
-    int pos = 0;
-    if (p.pos) {
-      pos = p.pos[row0 + r];
-    } else if (PAGED) {                             // its place in the cache
-      uint32_t k;
-      const int s = (int)p.by_R.divmod((uint32_t)(row0 + r), k);
-      pos = (int)((p.starts ? p.starts[s] : 0) + (long long)k);
-    }
-    float c, s;
-    turn_cos_sin(p.turns[i], pos, p.amp, c, s);
-    s_cs[a] = make_float2(c, s);
-  }
-  __syncthreads();
-  for (int base = 0; base < items; base += ITEMS * groups) {
-    if (base > 0) {
+          for (int e = 0; e < 4; ++e) {
+            const float2 x = f32x2_get(va[e]), y = f32x2_get(vb[e]);
+            va[e] = f32x2(x.x * c[e] - x.y * s[e], x.y * c[e] + x.x * s[e]);
+            vb[e] = f32x2(y.x * c[e + 4] - y.y * s[e + 4], y.y * c[e + 4] + y.x * s[e + 4]);
+          }
+        } else {
+          const uint64_t minus = f32x2(-1.0f, -1.0f);
 #pragma unroll
-      for (int k = 0; k < ITEMS; ++k) load(x[k], base + group + k * groups);
-    }
+          for (int e = 0; e < 4; ++e) {
+            const int at = (e >> 1) * turners;
+            const float4 c4 = cs[at], s4 = cs[2 * turners + at];
+            const uint64_t c = e & 1 ? f32x2(c4.z, c4.w) : f32x2(c4.x, c4.y);
+            const uint64_t s = e & 1 ? f32x2(s4.z, s4.w) : f32x2(s4.x, s4.y);
+            const uint64_t x0 = va[e], x1 = vb[e];
+            va[e] = fma_f32x2(x0, c, mul_f32x2(mul_f32x2(x1, s), minus));
+            vb[e] = fma_f32x2(x1, c, mul_f32x2(x0, s));
+          }
+        }
+      }
+      TO* to = out + (kind == 0 || !PAGED ? (row0 + r0 + r) * out_rs : slot * p.hd);
+      float f[8];
 #pragma unroll
-    for (int k = 0; k < ITEMS; ++k) finish(x[k]);
+      for (int e = 0; e < 4; ++e) {
+        const float2 x = f32x2_get(va[e]);
+        f[2 * e] = x.x;
+        f[2 * e + 1] = x.y;
+      }
+      O::store8(to + a, f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 x = f32x2_get(vb[e]);
+        f[2 * e] = x.x;
+        f[2 * e + 1] = x.y;
+      }
+      O::store8(to + b, f);
+    }
   }
+  if (threadIdx.x == 0 && *(volatile int*)&s_abort)   // let copies in flight land before the CTA's shared memory goes away
+    for (int k = max(issued - p.stages, 0); k < issued; ++k)
+      mbar_wait(&s_full[k % p.stages], (uint32_t)(k / p.stages) & 1u, nullptr, g_heads_err, ERR_HEADS);
 }
 
 dllm_status kv_paged_check(const dllm_kv_paged* c, const char* who) {
@@ -198,11 +279,15 @@ dllm_status kv_paged_check(const dllm_kv_paged* c, const char* who) {
   return DLLM_OK;
 }
 
+cudaError_t heads_err_word(int** p) { return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_heads_err); }
+
 namespace {
 
 template <typename E, typename O, int L, bool PAGED>
 cudaError_t launch_heads(const HeadsParams& p, dim3 grid, dim3 block, cudaStream_t st) {
-  return op_launch(heads_kernel<E, O, L, PAGED>, grid, block, 0, st, 1, p);
+  const cudaError_t e = op_smem_once(reinterpret_cast<const void*>(heads_kernel<E, O, L, PAGED>), kHeadsRing);
+  if (e != cudaSuccess) return e;
+  return op_launch(heads_kernel<E, O, L, PAGED>, grid, block, (size_t)p.stages * p.step * p.row_bytes, st, 1, p);
 }
 
 template <typename E, typename O>
@@ -260,17 +345,25 @@ dllm_status heads(HeadsParams& p, const char* who, bool paged, int dtype, int ou
   const long long heads = (long long)p.H + (paged ? 2LL : 1LL) * p.H_kv;
   int lanes = 1;
   while (lanes * 16 < p.hd) lanes *= 2;
-  if (heads > (1 << 24)) return op_fail(DLLM_EINVAL, "%s: H=%d H_kv=%d are too many heads", who, p.H, p.H_kv);
+  if (heads > (1 << 20)) return op_fail(DLLM_EINVAL, "%s: H=%d H_kv=%d are too many heads", who, p.H, p.H_kv);
   p.heads = (int)heads;
-  p.by_heads = FastDiv((uint32_t)heads);
-  // rows of a CTA: as many as give 256 threads two heads each, where that leaves the GPU's SMs a CTA each
-  p.row_run = 1;
-  while (p.row_run < kHeadsRows && 2 * p.row_run * heads * lanes <= 512 && 2 * p.row_run * (p.rot / 2) <= kHeadsAngles &&
-         p.rows / (2 * p.row_run) >= op_device_sms())
-    p.row_run *= 2;
-  const bool few = p.rows <= 2 * op_device_sms();       // a head a thread: its latency counts
-  const long long threads = std::min(512LL, (p.row_run * heads * lanes / (few ? 1 : 2) + 31) / 32 * 32);
-  const dim3 grid((unsigned)((p.rows + p.row_run - 1) / p.row_run)), block((unsigned)threads);
+  // heads of a CTA: up to 512 threads' worth, in equal chunks; rows at once: as many as give 256 threads a head each
+  const int chunks = (int)((heads * lanes + 511) / 512);
+  p.chunk = (int)((heads + chunks - 1) / chunks);
+  p.by_chunk = FastDiv((uint32_t)p.chunk);
+  const int pairs = p.rot / 2, sms = op_device_sms();
+  p.step = 1;
+  while (2 * p.step * p.chunk * lanes <= 256 && 2 * p.step * pairs <= kHeadsAngles && 2 * p.step <= kHeadsRows &&
+         p.rows / (2 * p.step) >= sms)
+    p.step *= 2;
+  const int threads = (p.step * p.chunk * lanes + 31) / 32 * 32;
+  // rows of a CTA: as few as leave every SM its threads
+  const long long ctas = std::max(1LL, (long long)sms * (1024 / threads) / chunks);
+  p.run = (int)(((p.rows + ctas - 1) / ctas + p.step - 1) / p.step * p.step);
+  p.batch = std::min(p.run, std::min(kHeadsRows, pairs ? kHeadsAngles / pairs : kHeadsRows) / p.step * p.step);
+  p.row_bytes = p.chunk * p.hd * es;                    // 32 KB at most
+  p.stages = std::min({kHeadsStages, kHeadsRing / (p.step * p.row_bytes), (p.run + p.step - 1) / p.step});
+  const dim3 grid((unsigned)((p.rows + p.run - 1) / p.run), (unsigned)chunks), block((unsigned)threads);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == DLLM_BF16)
     OP_CK((launch_heads<ElemBf16, ElemBf16>(p, paged, lanes, grid, block, st)));

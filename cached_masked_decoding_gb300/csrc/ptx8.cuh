@@ -245,6 +245,13 @@ __device__ __forceinline__ bool mbar_wait_long(uint64_t* bar, uint32_t parity, v
   return true;
 }
 
+// Contiguous bytes (a multiple of 16, both sides aligned to 16) to shared memory; they count on bar.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
 // ----------------------------------------------------------------- register shares
 // By every warp of a warpgroup (four warps); the shares of a CTA's warpgroups
 // must not add up to more than its threads were launched with.
