@@ -52,6 +52,7 @@ __global__ void __launch_bounds__(512, 2) heads_kernel(const __grid_constant__ H
   // [row][4][lanes]: cosines of a lane's first and last four pairs, then the sines
   __shared__ float4 s_cs[kHeadsAngles / 2];
   __shared__ long long s_slot[kHeadsRows];         // row of the cache's head 0, or -1: the row takes no part
+  __shared__ float4 s_w[2][64];                    // q's and k's weights in the order of a lane's four vectors: [4][lanes]
   __shared__ uint64_t s_full[kHeadsStages], s_empty[kHeadsStages];
   __shared__ int s_abort;
   float* s_angle = reinterpret_cast<float*>(s_cs);
@@ -107,13 +108,26 @@ __global__ void __launch_bounds__(512, 2) heads_kernel(const __grid_constant__ H
   if (threadIdx.x == 0)
     for (int k = 0; k < issued; ++k) fetch(k, k);
   const T* mine_at = reinterpret_cast<const T*>(s_ring) + (long long)sub * (p.row_bytes / (int)sizeof(T)) + in_chunk * p.hd;
-  Raw8<E> wa, wb;
-  const T* w = static_cast<const T*>(kind == 0 ? p.q_w : p.k_w);
-  const bool weighted = norm && w != nullptr && mine;
+  // a lane's elements a, a + 4, b, b + 4 and the three after each
+  const bool weighted = p.norm && (p.q_w || p.k_w);
   if (weighted) {
-    wa.load(w + a);
-    wb.load(w + b);
+    for (int e = threadIdx.x; e < 2 * p.hd; e += blockDim.x) {
+      const int k = e / p.hd, d = e - k * p.hd;
+      const T* w = static_cast<const T*>(k ? p.k_w : p.q_w);
+      // element d: the lane and the vector that hold it
+      int lane, at;
+      if (!p.interleaved && d < p.rot) {
+        const int i = d < pairs ? d : d - pairs;
+        lane = i >> 3;
+        at = (d < pairs ? 0 : 8) + (i & 7);
+      } else {
+        lane = d >> 4;
+        at = d & 15;
+      }
+      reinterpret_cast<float*>(&s_w[k][(at >> 2) * L + lane])[at & 3] = w ? E::get(w + d) : 1.0f;
+    }
   }
+  const float4* w4 = s_w[kind == 1] + l;
   const int stage_elems = p.step * (p.row_bytes / (int)sizeof(T));
   int stage = 0, last = -1;                        // of the ring: this step's, and the step's before
   uint32_t phase = 0;
@@ -200,13 +214,14 @@ __global__ void __launch_bounds__(512, 2) heads_kernel(const __grid_constant__ H
       if (norm) {
         const uint64_t inv2 = f32x2(inv, inv);
         if (weighted) {
-          float f[8];
-          wa.floats(f);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) va[e] = mul_f32x2(va[e], f32x2(f[2 * e], f[2 * e + 1]));
-          wb.floats(f);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) vb[e] = mul_f32x2(vb[e], f32x2(f[2 * e], f[2 * e + 1]));
+          for (int e = 0; e < 2; ++e) {
+            const float4 f = w4[e * L], g4 = w4[(2 + e) * L];
+            va[2 * e] = mul_f32x2(va[2 * e], f32x2(f.x, f.y));
+            va[2 * e + 1] = mul_f32x2(va[2 * e + 1], f32x2(f.z, f.w));
+            vb[2 * e] = mul_f32x2(vb[2 * e], f32x2(g4.x, g4.y));
+            vb[2 * e + 1] = mul_f32x2(vb[2 * e + 1], f32x2(g4.z, g4.w));
+          }
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
