@@ -2591,8 +2591,9 @@ extern "C" dllm_status dllm_op_check(int32_t* site, void* stream) {
   int dev = 0;
   CK(cudaGetDevice(&dev));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // error words: the library's workspace, the no-alloc scratch, the 8-bit kernels, the paged attention, the head norms
-  constexpr int kWords = 6;
+  // error words: the library's workspace, the no-alloc scratch, the 8-bit kernels, the paged attention, the head norms,
+  // the log probabilities
+  constexpr int kWords = 7;
   int* word[kWords] = {};
   int code_of[kWords] = {};
   {
@@ -2607,6 +2608,7 @@ extern "C" dllm_status dllm_op_check(int32_t* site, void* stream) {
   CK(attn_kv8_err_word(&word[3]));
   CK(attn_paged_err_word(&word[4]));
   CK(heads_err_word(&word[5]));
+  CK(logprobs_err_word(&word[6]));
   for (int i = 0; i < kWords; ++i)
     if (word[i]) CK(cudaMemcpyAsync(&code_of[i], word[i], 4, cudaMemcpyDeviceToHost, st));
   CK(cudaStreamSynchronize(st));

@@ -6,15 +6,20 @@
 // The largest term is left out of the sums, so a nearly certain row's S keeps its relative accuracy, and both
 // parts of the entropy are of one sign.
 //
-// Bound by HBM: the logits are read once.  A CTA (or a cluster of up to 8, where rows are few) takes a row and streams
-// it; every thread keeps the largest of its elements m and, relative to it, S and W of them all.  What needs the
-// elements again is a few threads' worth, which lies in L2 or L1 still:
-//   - the thread that holds the row's largest takes its S and W again without it;
-//   - the alternatives are among the elements of threads whose m is no less than the top-th largest of 128 group
-//     maxima (a lower bound of the top-th largest element): for 20 of 126464 about 22 threads of 512.  Elements above
-//     the bound are ranked by counting; its equals join in the order of their ids.
-// Rows that would give more than 1024 elements above the bound (one thread's elements are the largest by far) take a
-// pass of the row an alternative.
+// Bound by HBM: the logits are read once.  A CTA takes row after row (or a cluster of up to 8 one row, where rows are
+// few).  One warp copies the rows into a ring in shared memory, past the end of a row too; eight stream them: every
+// thread keeps the largest of its elements m and, relative to it, S and W of them all, leaves them in shared memory and
+// goes on to the next row.  Four warps work out a row's results meanwhile (the same threads one after the other took 212
+// us for the case below, with loads into registers and results apart 217).
+// What needs elements again is a few threads' worth, which lies in L2 still:
+//   - the alternatives are among the elements of units whose largest is no less than the top-th largest of 128 group
+//     maxima (a lower bound of the top-th largest element): for 20 of 126464 about 22 units of 64 elements.  Elements
+//     above the bound are ranked by counting; its equals join in the order of their ids.
+//   - where the others' S is less than the largest's 1, the thread that holds it takes its sums again without it.
+// Rows that would give more than 512 elements above the bound (a few threads' are the largest by far) take a pass of the
+// row an alternative.
+// LOGPROBS_TIMES
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
@@ -30,14 +35,30 @@ struct LogprobsParams {
   float *logp, *entropy, *top_logp;
   int32_t* top_ids;
   long long rs;
-  int vocab, top, cluster;
+  int rows, vocab, top, cluster, slots;
   float scale;
 };
 
 constexpr int kMostTop = 64;
-constexpr int kMostAbove = 1024;     // elements above the bound that are ranked
+constexpr int kMostAbove = 512;      // elements above the bound that are ranked
 constexpr int kMostEqual = 256;      // and equals that are, before the row is walked for them in order
 constexpr int kLogCluster = 8;
+constexpr int kLogAhead = 4;         // vectors of a thread in a chunk of the ring (a batch)
+constexpr int kLogRest = 128;        // threads that work out a row's results
+
+template <int MAIN>
+struct LogCfg {
+  static constexpr int THREADS = MAIN + kLogRest + 32;
+  static constexpr int CTAS = MAIN == 128 ? 4 : 2;               // an SM
+  static constexpr int CHUNK = kLogAhead * MAIN;                 // vectors
+  static constexpr int SLOTS = 6;                                // of the ring, at most
+};
+constexpr int kLogGroups = 128;
+constexpr int kLogFewTop = 24;
+constexpr int kLogUnits = 8;         // of a thread's batches, each with a largest element of its own (and one for the rest)
+constexpr int kMostUnits = 512;      // units that are looked through again, before all are
+
+static __device__ int g_logprobs_err[1];
 
 struct Best {
   float x;
@@ -46,6 +67,20 @@ struct Best {
 // a before b: larger, or of a lower index
 __device__ __forceinline__ bool before(const Best& a, const Best& b) {
   return a.i >= 0 && (b.i < 0 || a.x > b.x || (a.x == b.x && a.i < b.i));
+}
+
+// A float as a whole number of the same order (-0 as 0), and back.
+__device__ __forceinline__ int log_order(float x) {
+  const int b = __float_as_int(x + 0.0f);
+  return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float log_value(int o) { return __int_as_float(o ^ ((o >> 31) & 0x7fffffff)); }
+// An element and its id as one number: the larger element, then the lower id, is more.
+__device__ __forceinline__ unsigned long long log_key(float x, int i) {
+  return (unsigned long long)((uint32_t)log_order(x) ^ 0x80000000u) << 32 | (uint32_t)~i;
+}
+__device__ __forceinline__ Best log_best(unsigned long long key) {
+  return {log_value((int)((uint32_t)(key >> 32) ^ 0x80000000u)), (int)~(uint32_t)key};
 }
 
 // 2^x; results below the normal range are 0
@@ -138,7 +173,7 @@ struct LogSums {
     plain = to_plain;
   }
   template <typename E, int n>
-  __device__ __forceinline__ void add(const uint4 (&r)[n], float c2) {
+  __device__ __forceinline__ float add(const uint4 (&r)[n], float c2) {   // their largest
     const float top = LogWords<E>::largest(r);
     if (top > m) raise(top, c2);
     const uint64_t S0 = S, W0 = W;
@@ -165,6 +200,7 @@ struct LogSums {
         LogWords<E>::pairs(x4, [&](float2 x) { one(x.x, c2), one(x.y, c2); });
       }
     }
+    return top;
   }
   __device__ __forceinline__ void one(float x, float c2) {
     const float d = max_nan(plain ? fmaf(x, c2, -ref) : (x - (m == -INFINITY ? 0.0f : m)) * c2, -200.0f);
@@ -195,22 +231,29 @@ __device__ __forceinline__ void join_sums(LogRest& t, LogRest o, float c2) {
   t.W += (o.W + (1.0f + o.S) * d) * f;
 }
 
-template <int THREADS>
-struct LogShared {
-  float warp_S[THREADS / 32], warp_W[THREADS / 32];
-  int warp_n[THREADS / 32 + 1];
-  float group[128];                    // group maxima
-  float bound;
-  int owner, n_above, n_equal, n_hot;
-  int hot[THREADS];
-  Best above[kMostAbove];
+template <int MAIN>
+struct alignas(128) LogShared {
+  float m[2][MAIN], S[2][MAIN], W[2][MAIN];      // of the streaming threads, rows in turn
+  float unit[2][kLogUnits + 1][MAIN];            // largest elements of a thread's units
+  alignas(8) uint64_t ready[2], done[2], full[LogCfg<MAIN>::SLOTS], empty[LogCfg<MAIN>::SLOTS];
+  float own[4];                                  // the owner's S and W, with the largest and taken again without it
+  float warp_m[kLogRest / 32], warp_S[kLogRest / 32], warp_W[kLogRest / 32];
+  int warp_n[kLogRest / 32], warp_owner[kLogRest / 32];
+  alignas(16) int group[kLogGroups];             // group maxima, as whole numbers of their order
+  int bound;
+  int n_above, n_equal, n_hot;
+  int hot[kMostUnits];
+  unsigned long long above[kMostAbove];
   int equal[kMostEqual];
-  Best top[kLogCluster][kMostTop];     // lists of the cluster's CTAs, in order
-  float sums[kLogCluster][3];          // m, S, W
-  Best best[THREADS / 32];
+  Best top[kLogCluster][kMostTop];               // lists of the cluster's CTAs, in order
+  float sums[kLogCluster][3];                    // m, S, W
+  Best best[kLogRest / 32];
+  int abort;
 };
 
-template <typename E, int THREADS>
+__device__ __forceinline__ void rest_sync() { named_bar_sync(1, kLogRest); }
+
+template <typename E, int MAIN>
 struct LogRow {
   using T = typename E::T;
   static constexpr int VE = 16 / (int)sizeof(T);
@@ -222,9 +265,15 @@ struct LogRow {
     vocab = p.vocab;
     head = min(vocab, (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int)sizeof(T));
     nvec = (vocab - head) / VE;
-    v0 = (int)((long long)nvec * rank / ranks);
-    v1 = (int)((long long)nvec * (rank + 1) / ranks);
+    v0 = ranks == 1 ? 0 : (int)((long long)nvec * rank / ranks);
+    v1 = ranks == 1 ? nvec : (int)((long long)nvec * (rank + 1) / ranks);
     extra = rank == 0 ? vocab - nvec * VE : 0;
+  }
+  // of a thread: its vectors, and batches that make a unit
+  __device__ __forceinline__ int vectors(int t) const { return max(0, (v1 - v0 - t + MAIN - 1) / MAIN); }
+  __device__ __forceinline__ int span_log() const {
+    const int batches = vectors(0) / kLogAhead;
+    return batches <= kLogUnits ? 0 : 32 - __clz((batches - 1) / kLogUnits);
   }
   __device__ __forceinline__ int extra_index(int e) const { return e < head ? e : e + nvec * VE; }
   __device__ __forceinline__ int index(int v, int e) const { return head + v * VE + e; }
@@ -239,22 +288,11 @@ struct LogRow {
       f[3] = __uint_as_float(r.w);
     }
   }
-  // f(x, index) of every element of thread t, by the lanes of a warp
-  template <typename Fn>
-  __device__ __forceinline__ void each(int t, int lane, Fn f) const {
-    for (int v = v0 + t + lane * THREADS; v < v1; v += 32 * THREADS) {
-      float e[VE];
-      floats(load(v), e);
-#pragma unroll
-      for (int i = 0; i < VE; ++i) f(e[i], index(v, i));
-    }
-    if (lane == 0 && t < extra) f(E::get(x + extra_index(t)), extra_index(t));
-  }
 };
 
 // The `top` best of the CTA's elements, in order, one pass each.
-template <typename E, int THREADS>
-__device__ void top_by_passes(const LogRow<E, THREADS>& row, LogShared<THREADS>& sh, int top, Best* out) {
+template <typename E, int MAIN>
+__device__ void top_by_passes(const LogRow<E, MAIN>& row, LogShared<MAIN>& sh, int tid, int top, Best* out) {
   Best last = {INFINITY, -1};
   for (int k = 0; k < top; ++k) {
     Best b = {0.0f, -1};
@@ -262,28 +300,28 @@ __device__ void top_by_passes(const LogRow<E, THREADS>& row, LogShared<THREADS>&
       const Best c = {x, i};
       if (x == x && (k == 0 || before(last, c)) && before(c, b)) b = c;
     };
-    for (int v = row.v0 + (int)threadIdx.x; v < row.v1; v += THREADS) {
-      float e[LogRow<E, THREADS>::VE];
+    for (int v = row.v0 + tid; v < row.v1; v += kLogRest) {
+      float e[LogRow<E, MAIN>::VE];
       row.floats(row.load(v), e);
 #pragma unroll
-      for (int i = 0; i < LogRow<E, THREADS>::VE; ++i) look(e[i], row.index(v, i));
+      for (int i = 0; i < LogRow<E, MAIN>::VE; ++i) look(e[i], row.index(v, i));
     }
-    if ((int)threadIdx.x < row.extra) look(E::get(row.x + row.extra_index(threadIdx.x)), row.extra_index(threadIdx.x));
+    if (tid < row.extra) look(E::get(row.x + row.extra_index(tid)), row.extra_index(tid));
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) {
       const Best o = {__shfl_xor_sync(0xffffffffu, b.x, d), __shfl_xor_sync(0xffffffffu, b.i, d)};
       if (before(o, b)) b = o;
     }
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) sh.best[threadIdx.x / 32] = b;
-    __syncthreads();
+    rest_sync();
+    if (tid % 32 == 0) sh.best[tid / 32] = b;
+    rest_sync();
     b = sh.best[0];
-    for (int w = 1; w < THREADS / 32; ++w)
+    for (int w = 1; w < kLogRest / 32; ++w)
       if (before(sh.best[w], b)) b = sh.best[w];
-    if (threadIdx.x == 0) out[k] = b;
+    if (tid == 0) out[k] = b;
     last = b;
     if (b.i < 0) {                     // none left, here and in every further pass
-      for (int j = k + 1 + (int)threadIdx.x; j < top; j += THREADS) out[j] = b;
+      for (int j = k + 1 + tid; j < top; j += kLogRest) out[j] = b;
       break;
     }
   }
@@ -291,13 +329,13 @@ __device__ void top_by_passes(const LogRow<E, THREADS>& row, LogShared<THREADS>&
 
 // The first `need` elements equal to `bound` in the order of their ids, and how many there are; the CTA's elements
 // lie in the order head, vectors, tail.
-template <typename E, int THREADS>
-__device__ int equals_in_order(const LogRow<E, THREADS>& row, LogShared<THREADS>& sh, float bound, int need, Best* out) {
-  constexpr int VE = LogRow<E, THREADS>::VE;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, heads = row.extra ? row.head : 0;
+template <typename E, int MAIN>
+__device__ int equals_in_order(const LogRow<E, MAIN>& row, LogShared<MAIN>& sh, int tid, float bound, int need, Best* out) {
+  constexpr int VE = LogRow<E, MAIN>::VE;
+  const int lane = tid & 31, warp = tid >> 5, heads = row.extra ? row.head : 0;
   int found = 0;
-  for (int at = row.v0 - THREADS; at < row.v1 + THREADS && found < need; at += THREADS) {
-    // one step for the head, one of THREADS vectors each, one for the tail
+  for (int at = row.v0 - kLogRest; at < row.v1 + kLogRest && found < need; at += kLogRest) {
+    // one step for the head, one of kLogRest vectors each, one for the tail
     float e[VE];
     int n = 0, first = 0;
     if (at < row.v0) {
@@ -328,139 +366,100 @@ __device__ int equals_in_order(const LogRow<E, THREADS>& row, LogShared<THREADS>
       if (lane >= d) upto += v;
     }
     if (lane == 31) sh.warp_n[warp] = upto;
-    __syncthreads();
+    rest_sync();
     int pos = found + upto - __popc(mask);
     int total = 0;
-    for (int w = 0; w < THREADS / 32; ++w) {
+    for (int w = 0; w < kLogRest / 32; ++w) {
       if (w < warp) pos += sh.warp_n[w];
       total += sh.warp_n[w];
     }
     for (; mask && pos < need; mask &= mask - 1, ++pos) out[pos] = {bound, first + __ffs(mask) - 1};
     found += total;
-    __syncthreads();
+    rest_sync();
   }
   return min(found, need);
 }
 
-template <typename E, int THREADS>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const __grid_constant__ LogprobsParams p) {
-  constexpr int QUAD = THREADS / 128, AHEAD = 6;
-  __shared__ LogShared<THREADS> sh;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int ranks = p.cluster, rank = ranks > 1 ? (int)cluster_rank() : 0;
-  const long long r = ranks > 1 ? blockIdx.x / (unsigned)ranks : blockIdx.x;
-  const float c2 = p.scale * 1.4426950408889634f;
+// A row's results from the streaming threads' sums in buffer b; by kLogRest threads.  false: not this CTA's to give.
+template <typename E, int MAIN>
+__device__ __forceinline__ void row_results(const LogprobsParams& p, LogShared<MAIN>& sh, const LogRow<E, MAIN>& row, int r,
+                                            int b, int tid, int rank, int ranks, float c2) {
+  constexpr int VE = LogRow<E, MAIN>::VE, EACH = MAIN / kLogRest;
+  const int lane = tid & 31, warp = tid >> 5, top = p.top;
+  float m[EACH], M = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < EACH; ++k) {
+    m[k] = sh.m[b][tid + k * kLogRest];
+    M = fmaxf(M, m[k]);
+  }
+  sh.group[tid] = log_order(M);
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  if (lane == 0) sh.warp_m[warp] = M;
   if (tid == 0) {
-    sh.owner = THREADS;
     sh.n_above = sh.n_equal = sh.n_hot = 0;
-    sh.bound = INFINITY;
+    sh.bound = 0x7fffffff;
   }
-  if (ranks > 1) cluster_arrive();     // waited for before the first access of another CTA's memory
-  griddep_launch_dependents();
-  griddep_wait();
-  const LogRow<E, THREADS> row(p, r, rank, ranks);
-
-  // ------------------------------------------------------ one pass
-  LogSums mine;
-  int v = row.v0 + tid;
-  if (v + (AHEAD - 1) * THREADS < row.v1) {
-    // a batch in the sums, the next one on its way
-    uint4 raw[AHEAD];
+  rest_sync();
 #pragma unroll
-    for (int k = 0; k < AHEAD; ++k) raw[k] = row.load(v + k * THREADS);
-    for (v += AHEAD * THREADS; v + (AHEAD - 1) * THREADS < row.v1; v += AHEAD * THREADS) {
-      uint4 next[AHEAD];
+  for (int w = 0; w < kLogRest / 32; ++w) M = fmaxf(M, sh.warp_m[w]);
+  // everyone's sums relative to M; a holder of the largest, the first one, apart
+  float S = 0.0f, W = 0.0f, Sown = 0.0f, Wown = 0.0f;
+  int owner = MAIN;
 #pragma unroll
-      for (int k = 0; k < AHEAD; ++k) next[k] = row.load(v + k * THREADS);
-      mine.template add<E>(raw, c2);
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k) raw[k] = next[k];
+  for (int k = 0; k < EACH; ++k) {
+    const int t = tid + k * kLogRest;
+    float s = sh.S[b][t], w = sh.W[b][t];
+    if (m[k] > -INFINITY) {
+      const float d = max_nan((m[k] - M) * c2, -200.0f), f = exp2_fast(d);
+      w = (w + s * d) * f;
+      s *= f;
     }
-    mine.template add<E>(raw, c2);
+    if (m[k] == M && M > -INFINITY && owner == MAIN) {
+      owner = t;
+      Sown = s;
+      Wown = w;
+    } else {
+      S += s;
+      W += w;
+    }
   }
-  for (; v < row.v1; v += THREADS) {
-    const uint4 raw[1] = {row.load(v)};
-    mine.template add<E>(raw, c2);
-  }
-  if (tid < row.extra) {
-    const float x = E::get(row.x + row.extra_index(tid));
-    if (x > mine.m) mine.raise(x, c2);
-    mine.one(x, c2);
-  }
-
-  // ------------------------------------------------------ the largest, and a bound of the alternatives
-  float M = mine.m;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    if (2 * d == QUAD && lane % QUAD == 0) sh.group[tid / QUAD] = M;
-  }
-  if (QUAD == 1) sh.group[tid] = mine.m;
-  if (lane == 0) sh.warp_S[warp] = M;
-  __syncthreads();
-  for (int w = 0; w < THREADS / 32; ++w) M = fmaxf(M, sh.warp_S[w]);
-  if (mine.m == M && M > -INFINITY) atomicMin(&sh.owner, tid);
-  if (p.top > 0) {
-    // rank of this thread's group among all, a share of the comparisons each
-    const int g = tid / QUAD;
-    const float x = sh.group[g];
+  // The bound: the least of the group maxima that fewer than `top` others exceed; by every warp for itself from 32 groups
+  // where few alternatives are wanted, else from 128.
+  int order = 0x7fffffff;
+  if (top > kLogFewTop) {
+    const int x = sh.group[tid];
     int n = 0;
 #pragma unroll 8
-    for (int j = tid % QUAD; j < 128; j += QUAD) {
-      const float y = sh.group[j];
-      n += y > x || (y == x && j < g) ? 1 : 0;
+    for (int j = 0; j < kLogGroups; j += 4) {
+      const int4 y = *reinterpret_cast<const int4*>(&sh.group[j]);
+      n += (y.x > x) + (y.y > x) + (y.z > x) + (y.w > x);
     }
+    const int least = __reduce_min_sync(0xffffffffu, n < top ? x : 0x7fffffff);
+    if (lane == 0) atomicMin(&sh.bound, least);
+  } else if (top > 0) {
+    const int4 y = *reinterpret_cast<const int4*>(&sh.group[4 * lane]);
+    const int x = max(max(y.x, y.y), max(y.z, y.w));
+    int n = 0;
 #pragma unroll
-    for (int d = 1; d < QUAD; d <<= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
-    if (n == p.top - 1) sh.bound = x;
+    for (int j = 0; j < 32; ++j) n += __shfl_sync(0xffffffffu, x, j) > x ? 1 : 0;
+    order = __reduce_min_sync(0xffffffffu, n < top ? x : 0x7fffffff);
   }
-  __syncthreads();
-  const float bound = sh.bound;
-  const int owner = sh.owner;
-  // (elements of -inf that are alternatives all the same come by the walk in order)
-  if (tid == owner || (p.top > 0 && mine.m >= bound && mine.m > -INFINITY))
-    sh.hot[atomicAdd(&sh.n_hot, 1)] = tid;
-  // everyone's sums relative to M; the owner's come again without the largest
-  float S = 0.0f, W = 0.0f;
-  if (tid != owner) {
-    if (mine.m > -INFINITY) mine.scale(mine.rise(M, 0.0f, false, c2));
-    const float2 s = f32x2_get(mine.S), w = f32x2_get(mine.W);
-    S = s.x + s.y;
-    W = w.x + w.y;
+  const int best_owner = __reduce_min_sync(0xffffffffu, owner);
+  if (lane == 0) sh.warp_owner[warp] = best_owner;
+  rest_sync();
+  owner = MAIN;
+#pragma unroll
+  for (int w = 0; w < kLogRest / 32; ++w) owner = min(owner, sh.warp_owner[w]);
+  if (owner < MAIN && owner % kLogRest == tid) {
+    sh.own[0] = Sown;
+    sh.own[1] = Wown;
+  } else {                             // (another holder's sums are like everyone's)
+    S += Sown;
+    W += Wown;
   }
-  __syncthreads();
-  const int n_hot = sh.n_hot;
-  for (int h = warp; h < n_hot; h += THREADS / 32) {
-    const int t = sh.hot[h];
-    int top_count = 0;
-    row.each(t, lane, [&](float x, int i) {
-      if (p.top > 0 && x >= bound) {
-        // (no more than tells that there are too many)
-        if (x > bound) {
-          if (*(volatile int*)&sh.n_above <= kMostAbove) {
-            const int at = atomicAdd(&sh.n_above, 1);
-            if (at < kMostAbove) sh.above[at] = {x, i};
-          }
-        } else if (bound > -INFINITY && *(volatile int*)&sh.n_equal <= kMostEqual) {
-          const int at = atomicAdd(&sh.n_equal, 1);
-          if (at < kMostEqual) sh.equal[at] = i;
-        }
-      }
-      if (t == owner) {
-        if (x == M) {
-          ++top_count;
-        } else {
-          const float d = max_nan((x - M) * c2, -200.0f), e = exp2_fast(d);
-          S += e;
-          W += d * e;
-        }
-      }
-    });
-    if (t == owner) {
-      top_count = __reduce_add_sync(0xffffffffu, top_count);
-      if (lane == 0) S += (float)(top_count - 1);
-    }
-  }
+  if (top > kLogFewTop) order = sh.bound;
+  const float bound = top > 0 ? log_value(order) : INFINITY;
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) {
     S += __shfl_xor_sync(0xffffffffu, S, d);
@@ -470,55 +469,195 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     sh.warp_S[warp] = S;
     sh.warp_W[warp] = W;
   }
-  __syncthreads();
-
-  // ------------------------------------------------------ this CTA's alternatives, in order
-  Best* list = sh.top[rank];
-  if (p.top > 0) {
-    const int na = sh.n_above, ne = sh.n_equal;
-    if (na > kMostAbove) {
-      top_by_passes(row, sh, p.top, list);
-    } else {
-      for (int i = tid; i < na; i += THREADS) {
-        const Best b = sh.above[i];
-        int n = 0;
-        for (int j = 0; j < na; ++j) n += before(sh.above[j], b) ? 1 : 0;
-        if (n < p.top) list[n] = b;
-      }
-      const int need = p.top - na;
-      if (need > 0) {
-        int found = min(need, ne);
-        if (bound == -INFINITY || ne > kMostEqual) {
-          found = equals_in_order(row, sh, bound, need, list + na);
-        } else {
-          for (int t = tid; t < ne; t += THREADS) {
-            const int b = sh.equal[t];
-            int n = 0;
-            for (int j = 0; j < ne; ++j) n += sh.equal[j] < b ? 1 : 0;
-            if (n < need) list[na + n] = {bound, b};
-          }
-        }
-        for (int k = na + found + tid; k < p.top; k += THREADS) list[k] = {-INFINITY, -1};
+  // the units that may hold alternatives (elements of -inf that are some all the same come by the walk in order)
+  const int span_log = row.span_log();
+  if (top > 0) {
+#pragma unroll
+    for (int k = 0; k < EACH; ++k) {
+      const bool hot = m[k] >= bound && m[k] > -INFINITY;
+      if (!__any_sync(0xffffffffu, hot)) continue;
+      const int t = tid + k * kLogRest, units = ((row.vectors(t) / kLogAhead + (1 << span_log) - 1) >> span_log) + 1;
+      uint32_t mask = 0;
+#pragma unroll
+      for (int j = 0; j <= kLogUnits; ++j) mask |= j < units && sh.unit[b][j][t] >= bound ? 1u << j : 0;
+      if (!hot) mask = 0;
+      for (; mask; mask &= mask - 1) {
+        const int at = atomicAdd(&sh.n_hot, 1);
+        if (at < kMostUnits) sh.hot[at] = (__ffs(mask) - 1) * MAIN + t;
       }
     }
   }
+  rest_sync();
   LogRest sum = {M, 0.0f, 0.0f};
-  for (int w = 0; w < THREADS / 32; ++w) {
+#pragma unroll
+  for (int w = 0; w < kLogRest / 32; ++w) {
     sum.S += sh.warp_S[w];
     sum.W += sh.warp_W[w];
   }
-  __syncthreads();
+  // the owner's, without the largest's 1: taken again by the first warp where the subtraction would tell
+  const bool owned = owner < MAIN, again = owned && !(sum.S + sh.own[0] >= 2.0f);
+  if (owned && !again) {
+    sum.S += sh.own[0] - 1.0f;
+    sum.W += sh.own[1];
+  }
+  if (again && warp == 0) {
+    float s = 0.0f, w = 0.0f;
+    int same = 0;
+    auto other = [&](float x) {
+      if (x == M) {
+        ++same;
+        return;
+      }
+      const float d = max_nan((x - M) * c2, -200.0f), e = exp2_fast(d);
+      s += e;
+      w += d * e;
+    };
+    for (int v = row.v0 + owner + lane * MAIN; v < row.v1; v += 32 * MAIN) {
+      float e[VE];
+      row.floats(row.load(v), e);
+#pragma unroll
+      for (int i = 0; i < VE; ++i) other(e[i]);
+    }
+    if (lane == 0 && owner < row.extra) other(E::get(row.x + row.extra_index(owner)));
+    same = __reduce_add_sync(0xffffffffu, same);
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, d);
+      w += __shfl_xor_sync(0xffffffffu, w, d);
+    }
+    if (lane == 0) {
+      sh.own[2] = s + (float)(same - 1);
+      sh.own[3] = w;
+    }
+  }
+  // ------------------------------------------------------ alternatives: the hot threads' elements
+  if (top > 0) {
+    // a warp's elements, some of every lane: those above the bound and its equals find places together
+    auto look = [&](uint32_t above, uint32_t equal, auto element) {
+      if (!__any_sync(0xffffffffu, (above | equal) != 0)) return;
+      int upto = __popc(above) | __popc(equal) << 16;
+      const int own = upto;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += o;
+      }
+      int at = 0, ae = 0;
+      if (lane == 31) {                // (no more than tells that there are too many)
+        at = *(volatile int*)&sh.n_above <= kMostAbove && (upto & 0xffff) ? atomicAdd(&sh.n_above, upto & 0xffff) : kMostAbove;
+        ae = *(volatile int*)&sh.n_equal <= kMostEqual && upto >> 16 ? atomicAdd(&sh.n_equal, upto >> 16) : kMostEqual;
+      }
+      at = __shfl_sync(0xffffffffu, at, 31) + ((upto - own) & 0xffff);
+      ae = __shfl_sync(0xffffffffu, ae, 31) + ((upto - own) >> 16);
+      for (; above; above &= above - 1, ++at) {
+        float x;
+        const int i = element(__ffs(above) - 1, x);
+        if (at < kMostAbove) sh.above[at] = log_key(x, i);
+      }
+      for (; equal; equal &= equal - 1, ++ae) {
+        float x;
+        const int i = element(__ffs(equal) - 1, x);
+        if (ae < kMostEqual) sh.equal[ae] = i;
+      }
+    };
+    const int n_hot = sh.n_hot, each = kLogAhead << span_log;   // vectors of a unit, at most
+    auto look_vector = [&](int v) {    // (v1: none)
+      float e[VE] = {};
+      uint32_t above = 0, equal = 0;
+      if (v < row.v1) {
+        row.floats(row.load(v), e);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+          above |= e[i] > bound ? 1u << i : 0;
+          equal |= e[i] == bound && bound > -INFINITY ? 1u << i : 0;
+        }
+      }
+      look(above, equal, [&](int i, float& x) {
+        x = E::get(row.x + row.index(v, i));
+        return row.index(v, i);
+      });
+    };
+    if (n_hot <= kMostUnits) {
+      const int items = n_hot * each;
+      for (int i0 = warp * 32; i0 < items; i0 += kLogRest) {
+        const int i = i0 + lane, h = i >> (2 + span_log);
+        int v = row.v1;
+        if (i < items) {
+          const int code = sh.hot[h], j = code / MAIN, t = code - j * MAIN;
+          const int n = row.vectors(t), batches = n / kLogAhead, units = (batches + (1 << span_log) - 1) >> span_log;
+          // the unit's first vector, and the end of its own
+          const int first = j < units ? j * each : batches * kLogAhead;
+          const int end = j < units ? min(first + each, batches * kLogAhead) : n, at = first + i - h * each;
+          if (at < end) v = row.v0 + t + at * MAIN;
+        }
+        look_vector(v);
+      }
+    } else {
+      for (int v = row.v0 + warp * 32; v < row.v1; v += kLogRest) look_vector(min(v + lane, row.v1));
+    }
+    if (row.extra > 0 && warp == 0) {
+      const float x = lane < row.extra ? E::get(row.x + row.extra_index(lane)) : -INFINITY;
+      look(lane < row.extra && x > bound, lane < row.extra && x == bound && bound > -INFINITY, [&](int, float& y) {
+        y = x;
+        return row.extra_index(lane);
+      });
+    }
+  }
+  if (top > 0 || again) rest_sync();   // (again is the same for all)
+  if (again) {
+    sum.S += sh.own[2];
+    sum.W += sh.own[3];
+  }
+  Best* list = sh.top[rank];
+  if (top > 0) {
+    const int na = sh.n_above, ne = sh.n_equal;
+    if (na > kMostAbove) {
+      top_by_passes(row, sh, tid, top, list);
+    } else {
+      // how many come before an element: eight elements a warp at a time, against 64 in its lanes
+      for (int i0 = warp * 8; i0 < na; i0 += 8 * (kLogRest / 32)) {
+        int n = 0;                     // lane k: of element i0 + k
+        const unsigned long long mine = sh.above[min(i0 + (lane & 7), na - 1)];
+        for (int j = 0; j < na; j += 64) {
+          const unsigned long long a = j + lane < na ? sh.above[j + lane] : 0;
+          const unsigned long long c = j + 32 + lane < na ? sh.above[j + 32 + lane] : 0;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const unsigned long long x = __shfl_sync(0xffffffffu, mine, k);
+            const int more = __popc(__ballot_sync(0xffffffffu, a > x)) + __popc(__ballot_sync(0xffffffffu, c > x));
+            n += lane == k ? more : 0;
+          }
+        }
+        if (lane < 8 && i0 + lane < na && n < top) list[n] = log_best(mine);
+      }
+      const int need = top - na;
+      if (need > 0) {
+        int found = min(need, ne);
+        if (bound == -INFINITY || ne > kMostEqual) {
+          found = equals_in_order(row, sh, tid, bound, need, list + na);
+        } else {
+          for (int t = tid; t < ne; t += kLogRest) {
+            const int x = sh.equal[t];
+            int n = 0;
+            for (int j = 0; j < ne; ++j) n += sh.equal[j] < x ? 1 : 0;
+            if (n < need) list[na + n] = {bound, x};
+          }
+        }
+        for (int k = na + found + tid; k < top; k += kLogRest) list[k] = {-INFINITY, -1};
+      }
+    }
+    rest_sync();
+  }
 
   // ------------------------------------------------------ the cluster's
   if (ranks > 1) {
     cluster_wait();
     if (rank != 0) {
-      for (int i = tid; i < 2 * p.top; i += THREADS)
+      for (int i = tid; i < 2 * top; i += kLogRest)
         cluster_store(cluster_addr(smem_u32(reinterpret_cast<float*>(sh.top[rank]) + i), 0),
                       reinterpret_cast<const float*>(list)[i]);
       if (tid < 3)
-        cluster_store(cluster_addr(smem_u32(&sh.sums[rank][tid]), 0),
-                      tid == 0 ? sum.m : tid == 1 ? sum.S : sum.W);
+        cluster_store(cluster_addr(smem_u32(&sh.sums[rank][tid]), 0), tid == 0 ? sum.m : tid == 1 ? sum.S : sum.W);
     }
     cluster_sync();
     if (rank != 0) return;
@@ -533,19 +672,19 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     }
     if (p.entropy) p.entropy[r] = log_sum - sum.W * 0.6931471805599453f / (1.0f + sum.S);
   }
-  for (int i = tid; i < ranks * p.top; i += THREADS) {
+  for (int i = tid; i < ranks * top; i += kLogRest) {
     // an alternative's place: its own in its list, and how many of each other list come before it
-    const int k = i / p.top, at = i - k * p.top;
-    const Best b = sh.top[k][at];
+    const int k = ranks == 1 ? 0 : i / top, at = i - k * top;
+    const Best x = sh.top[k][at];
     int n = at;
     for (int o = 0; o < ranks; ++o) {
       if (o == k) continue;
-      int lo = 0, hi = p.top;
+      int lo = 0, hi = top;
       while (lo < hi) {
         const int mid = (lo + hi) / 2;
         // those that are none come last, in the order of the lists
         const Best c = sh.top[o][mid];
-        const bool first = b.i < 0 && c.i < 0 ? o < k : before(c, b);
+        const bool first = x.i < 0 && c.i < 0 ? o < k : before(c, x);
         if (first)
           lo = mid + 1;
         else
@@ -553,23 +692,200 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
       }
       n += lo;
     }
-    if (n < p.top) {
-      p.top_ids[r * p.top + n] = b.i;
-      p.top_logp[r * p.top + n] = b.i < 0 ? nan : (b.x - sum.m) * p.scale - log_sum;
+    if (n < top) {
+      p.top_ids[(long long)r * top + n] = x.i;
+      p.top_logp[(long long)r * top + n] = x.i < 0 ? nan : (x.x - sum.m) * p.scale - log_sum;
+    }
+  }
+}
+
+// MAIN: streaming threads
+template <typename E, int MAIN>
+__global__ void __launch_bounds__(LogCfg<MAIN>::THREADS, LogCfg<MAIN>::CTAS)
+    logprobs_kernel(const __grid_constant__ LogprobsParams p) {
+  using C = LogCfg<MAIN>;
+  constexpr int AHEAD = kLogAhead;
+  extern __shared__ __align__(128) uint8_t s_raw[];
+  LogShared<MAIN>& sh = *reinterpret_cast<LogShared<MAIN>*>(s_raw);
+  uint4* ring = reinterpret_cast<uint4*>(s_raw + sizeof(LogShared<MAIN>));   // p.slots chunks
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int ranks = p.cluster, rank = ranks > 1 ? (int)cluster_rank() : 0;
+  const float c2 = p.scale * 1.4426950408889634f;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.ready[i], MAIN / 32);
+      mbar_init(&sh.done[i], kLogRest / 32);
+    }
+    for (int i = 0; i < C::SLOTS; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], MAIN / 32);
+    }
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  if (ranks > 1) cluster_arrive();     // waited for before the first access of another CTA's memory
+  __syncthreads();
+  griddep_launch_dependents();
+  griddep_wait();
+  const int first_row = (int)(blockIdx.x / (unsigned)ranks), row_step = (int)(gridDim.x / (unsigned)ranks);
+  int k = 0, slot = 0;                 // rows so far (one where the CTA is of a cluster); the ring's place
+  uint32_t phase = 0;
+  if (tid < MAIN) {
+    for (int r = first_row; r < p.rows; r += row_step, ++k) {
+      const LogRow<E, MAIN> row(p, r, rank, ranks);
+      const int b = k & 1;
+      if (k >= 2) {
+        mbar_wait_long(&sh.done[b], (uint32_t)(k / 2 - 1) & 1u, &sh.abort, g_logprobs_err, ERR_LOGPROBS);
+        __syncwarp();
+      }
+      LogSums mine;
+      const int span = 1 << row.span_log();
+      int left = span;                 // batches until the unit is full
+      float largest = -INFINITY;       // the unit's
+      float* unit = &sh.unit[b][0][tid];
+      auto batch = [&](float top) {
+        largest = fmaxf(largest, top);
+        if (--left == 0) {
+          *unit = largest;
+          unit += MAIN;
+          largest = -INFINITY;
+          left = span;
+        }
+      };
+      for (int v0 = row.v0; v0 < row.v1; v0 += C::CHUNK) {
+        mbar_wait_long(&sh.full[slot], phase, &sh.abort, g_logprobs_err, ERR_LOGPROBS);
+        uint64_t* empty = &sh.empty[slot];
+        const uint4* chunk = ring + slot * C::CHUNK + tid;
+        if (++slot == p.slots) {
+          slot = 0;
+          phase ^= 1u;
+        }
+        const bool whole = v0 + (AHEAD - 1) * MAIN + tid < row.v1;   // a batch of this thread's
+        uint4 raw[AHEAD];
+        if (whole) {
+#pragma unroll
+          for (int i = 0; i < AHEAD; ++i) raw[i] = chunk[i * MAIN];
+        }
+        if (v0 + C::CHUNK > row.v1) {                                // the row's last chunk
+          if (whole) batch(mine.template add<E>(raw, c2));
+          if (left < span) {
+            *unit = largest;
+            unit += MAIN;
+            largest = -INFINITY;
+            left = span;
+          }
+          for (int i = 0; !whole && v0 + i * MAIN + tid < row.v1; ++i) {
+            const uint4 raw1[1] = {chunk[i * MAIN]};
+            largest = fmaxf(largest, mine.template add<E>(raw1, c2));
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty);
+        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty);
+          batch(mine.template add<E>(raw, c2));
+        }
+      }
+      if (left < span) {
+        *unit = largest;
+        unit += MAIN;
+        largest = -INFINITY;
+      }
+      *unit = largest;
+      if (tid < row.extra) {
+        const float x = E::get(row.x + row.extra_index(tid));
+        if (x > mine.m) mine.raise(x, c2);
+        mine.one(x, c2);
+      }
+      // relative to m c2 itself
+      if (mine.plain) mine.scale(mine.rise(mine.m, 0.0f, false, c2));
+      const float2 s = f32x2_get(mine.S), w = f32x2_get(mine.W);
+      sh.m[b][tid] = mine.m;
+      sh.S[b][tid] = s.x + s.y;
+      sh.W[b][tid] = w.x + w.y;
+      __syncwarp();
+      if (tid % 32 == 0) mbar_arrive(&sh.ready[b]);
+    }
+    __syncwarp();
+    if (ranks > 1) {                   // the cluster's barriers count every thread
+      cluster_wait();
+      cluster_sync();
+    }
+  } else if (tid >= MAIN + kLogRest) {
+    if (lane == 0) {
+      bool ok = true;
+      int u = 0;                       // chunks so far
+      for (int r = first_row; r < p.rows && ok; r += row_step) {
+        const LogRow<E, MAIN> row(p, r, rank, ranks);
+        for (int v = row.v0; v < row.v1; v += C::CHUNK, ++u) {
+          // (the first round over the ring finds it empty)
+          if (u >= p.slots &&
+              !(ok = mbar_wait_long(&sh.empty[slot], phase ^ 1u, &sh.abort, g_logprobs_err, ERR_LOGPROBS)))
+            break;
+          const uint32_t bytes = (uint32_t)min(C::CHUNK, row.v1 - v) * 16u;
+          mbar_arrive_expect_tx(&sh.full[slot], bytes);
+          bulk_load(ring + slot * C::CHUNK, row.x + row.index(v, 0), bytes, &sh.full[slot]);
+          if (++slot == p.slots) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (*(volatile int*)&sh.abort)   // let copies in flight land before the CTA's shared memory goes away
+        for (int i = max(u - p.slots, 0); i < u; ++i)
+          mbar_wait(&sh.full[i % p.slots], (uint32_t)(i / p.slots) & 1u, nullptr, g_logprobs_err, ERR_LOGPROBS);
+    }
+    __syncwarp();
+    if (ranks > 1) {
+      cluster_wait();
+      cluster_sync();
+    }
+  } else {
+    for (int r = first_row; r < p.rows; r += row_step, ++k) {
+      const LogRow<E, MAIN> row(p, r, rank, ranks);
+      const int b = k & 1;
+      // (after a wait that gave up the results are invalid, and reported)
+      mbar_wait_long(&sh.ready[b], (uint32_t)(k / 2) & 1u, &sh.abort, g_logprobs_err, ERR_LOGPROBS);
+      __syncwarp();
+      row_results(p, sh, row, r, b, tid - MAIN, rank, ranks, c2);
+      __syncwarp();
+      if (tid % 32 == 0) mbar_arrive(&sh.done[b]);
+      rest_sync();                     // what the results were made of is read: the next row's may be written
     }
   }
 }
 
 namespace {
 
+template <typename E, int MAIN>
+cudaError_t launch_logprobs(LogprobsParams& p, cudaStream_t st) {
+  using C = LogCfg<MAIN>;
+  // a cluster a row, or as many CTAs as fit, which take row after row
+  const int sms = op_device_sms(), grid = p.cluster > 1 ? p.rows * p.cluster : std::min(p.rows, C::CTAS * sms);
+  // the ring: what an SM's CTAs leave each other, and no more than a CTA has chunks (a small CTA starts beside the
+  // kernel before)
+  const int ctas = std::min(C::CTAS, (grid + sms - 1) / sms);
+  constexpr int chunk = C::CHUNK * 16, fixed = (int)sizeof(LogShared<MAIN>);
+  const int room = (228 * 1024 / ctas - 1024 - fixed) / chunk;
+  const long long vectors = p.vocab / (16 / (int)sizeof(typename E::T)) / p.cluster + 1;
+  const long long chunks = (vectors + C::CHUNK - 1) / C::CHUNK * ((p.rows * (long long)p.cluster + grid - 1) / grid);
+  p.slots = (int)std::min<long long>({room, C::SLOTS, chunks});
+  const cudaError_t e = op_smem_once(reinterpret_cast<const void*>(logprobs_kernel<E, MAIN>),
+                                     fixed + std::min(C::SLOTS, (227 * 1024 - fixed) / chunk) * chunk);
+  if (e != cudaSuccess) return e;
+  return op_launch(logprobs_kernel<E, MAIN>, dim3((unsigned)grid), dim3(C::THREADS), (size_t)(fixed + p.slots * chunk), st,
+                   p.cluster, p);
+}
+
+// Streaming threads: few where a row is short (8192 elements are 8 vectors each of 128 threads).
 template <typename E>
-cudaError_t launch_logprobs(const LogprobsParams& p, int rows, int threads, cudaStream_t st) {
-  const dim3 grid((unsigned)rows * (unsigned)p.cluster);
-  return threads == 128 ? op_launch(logprobs_kernel<E, 128>, grid, dim3(128), 0, st, p.cluster, p)
-                        : op_launch(logprobs_kernel<E, 512>, grid, dim3(512), 0, st, p.cluster, p);
+cudaError_t launch_logprobs(LogprobsParams& p, cudaStream_t st) {
+  return p.vocab <= 8192 ? launch_logprobs<E, 128>(p, st) : launch_logprobs<E, 256>(p, st);
 }
 
 }  // namespace
+cudaError_t logprobs_err_word(int** p) { return cudaGetSymbolAddress(reinterpret_cast<void**>(p), g_logprobs_err); }
+
 }  // namespace dllm
 
 using namespace dllm;
@@ -605,18 +921,17 @@ extern "C" dllm_status dllm_op_token_logprobs(const void* logits, int64_t row_st
   p.top_logp = top_logprobs;
   p.vocab = vocab;
   p.scale = inv_temperature;
-  // Threads of a row, and CTAs: as many as fill the GPU, each with 8192 elements at least.
-  const int threads = vocab <= 8192 ? 128 : 512;
+  p.rows = rows;
+  // CTAs of a row: as many as fill the GPU, each with 8192 elements at least
   p.cluster = 1;
-  while (p.cluster < kLogCluster && (long long)rows * p.cluster * 2 <= 3LL * op_device_sms() &&
+  while (p.cluster < kLogCluster && (long long)rows * p.cluster * 2 <= 2LL * op_device_sms() &&
          vocab / (p.cluster * 2) >= 8192)
     p.cluster *= 2;
-  if ((long long)rows * p.cluster > 0x7fffffff) p.cluster = 1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (dtype) {
-    case DLLM_F32: OP_CK(launch_logprobs<ElemF32>(p, rows, threads, st)); break;
-    case DLLM_BF16: OP_CK(launch_logprobs<ElemBf16>(p, rows, threads, st)); break;
-    default: OP_CK(launch_logprobs<ElemF16>(p, rows, threads, st)); break;
+    case DLLM_F32: OP_CK(launch_logprobs<ElemF32>(p, st)); break;
+    case DLLM_BF16: OP_CK(launch_logprobs<ElemBf16>(p, st)); break;
+    default: OP_CK(launch_logprobs<ElemF16>(p, st)); break;
   }
   return DLLM_OK;
 }

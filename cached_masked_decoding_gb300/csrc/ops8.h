@@ -31,6 +31,7 @@ cudaError_t gemm8_err_word(int** p);
 cudaError_t attn_kv8_err_word(int** p);
 cudaError_t attn_paged_err_word(int** p);
 cudaError_t heads_err_word(int** p);
+cudaError_t logprobs_err_word(int** p);
 
 // Launch with programmatic dependent launch: the kernel's prologue overlaps the
 // end of the kernel before it in the stream, and griddepcontrol.wait in the
