@@ -36,7 +36,7 @@ AttnPagedPlan plan_attn_paged(long long b, long long H_kv, long long rows, int h
   };
   a.o = take(a.whole ? 0 : (size_t)2 * a.ctas * a.N * hd * 4);
   a.ml = take(a.whole ? 0 : (size_t)2 * a.ctas * a.N * 8);
-  a.plan = take(a.whole ? 0 : (size_t)a.items * 8);
+  a.plan = take(a.whole ? 0 : (size_t)a.ctas * 16);
   a.lse = take(mass ? (size_t)a.items * a.N * 4 : 0);
   a.z = take(mass ? (size_t)a.items * a.tiles * kPagedKeys * a.nz * 4 : 0);
   a.bytes = at;
@@ -54,8 +54,7 @@ cudaError_t launch_attn_paged(const CUtensorMap& tk, const CUtensorMap& tv, cons
   e = op_launch(attn_paged_kernel<F, HD, N>, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, st, 1, tk, tv, p);
   if (e != cudaSuccess) return e;
   if (!a.whole) {
-    e = op_launch(attn_paged_join_kernel<F, HD>, dim3((unsigned)a.items, (unsigned)std::min(N, p.rows)), dim3(128), 0, st,
-                  1, p, N);
+    e = op_launch(attn_paged_join_kernel<F, HD>, dim3(grid, (unsigned)std::min(N, p.rows)), dim3(128), 0, st, 1, p, N);
     if (e != cudaSuccess) return e;
   }
   if (!p.mass) return cudaSuccess;
@@ -148,7 +147,7 @@ extern "C" dllm_status dllm_op_attention_paged(const void* q, int64_t q_row_stri
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.ws_o = reinterpret_cast<float*>(ws + a.o);
   p.ws_ml = reinterpret_cast<float*>(ws + a.ml);
-  p.ws_plan = reinterpret_cast<int2*>(ws + a.plan);
+  p.ws_plan = reinterpret_cast<int4*>(ws + a.plan);
   p.ws_lse = reinterpret_cast<float*>(ws + a.lse);
   p.ws_z = reinterpret_cast<float*>(ws + a.z);
   // bytes of a page's cached head: rows of hd * 2, in boxes of 128

@@ -18,8 +18,11 @@
 // part.
 //
 //   warp 0     TMA: the pages of a tile, a lane each, K and V through a ring of 128-key slots
-//   warp 1     MMAs, issued by one lane: scores two tiles ahead of the products, across items too
-//   warps 2..  softmax, one key and RW rows a thread; the next item's query tile; the output
+//   warp 1     MMAs, issued by one lane: scores up to two tiles ahead of the products, across items too
+//   warps 2..  softmax, one key and RW rows a thread
+//   the last four: an item's query tile while the one before is walked, and its output while the next one is (by the
+//              softmax warps these took 3.6 us an item, more than the ring bridges: 109 us for 32 rows of 16 sequences
+//              of 32 heads, 2048 keys)
 //
 // Positions at or past a sequence's length, or on no page, are not loaded (or come with a page's other rows): their
 // scores are taken as -inf and their V rows zeroed in shared memory, so that whatever bytes lie there meet no product.
@@ -47,7 +50,7 @@ struct AttnPagedParams {
   float scale_log2;
   int nz, z_tiles;            // scores kept for the weights: [item][z_tiles][128][nz]
   float *ws_o, *ws_ml, *ws_lse, *ws_z;   // [2 * CTAs][N][hd], [2 * CTAs][N][2], [item][N]
-  int2* ws_plan;              // [item] first and last CTA's slot of a split item, or -1
+  int4* ws_plan;              // [CTA] the split item that starts there, its first and last slots; or -1
 };
 
 static __device__ int g_attn_paged_err[1];
@@ -80,7 +83,8 @@ struct AttnPagedCfg {
   static constexpr int RW = N <= 16 ? 8 : 16;           // rows of a softmax thread
   static constexpr int WGS = N / RW;                    // groups of four softmax warps
   static constexpr int SOFT = 128 * WGS;                // softmax threads
-  static constexpr int THREADS = 64 + SOFT;
+  static constexpr int HELP = 128;                      // threads of the query tiles and the output
+  static constexpr int THREADS = 64 + SOFT + HELP;
   static constexpr int SLOT = KT * HD * 2;              // one K or V tile: HD / 64 parts of 128 keys x 128 bytes
   static constexpr int NP = N < 16 ? 16 : N;            // columns of a product
   static constexpr int Q_BYTES = NP * HD * 2;           // HD / 64 parts of NP rows x 128 bytes
@@ -89,16 +93,16 @@ struct AttnPagedCfg {
   static constexpr int P_BYTES = KT * P_ROW;            // one part
   static constexpr int CTAS = N <= 16 ? 2 : 1;          // an SM
   static constexpr int P_BUFS = N == 64 || (N == 16 && HD == 128) ? 1 : 2;
-  // warp maxima (4), m, rise, sums of the warps (4), places (2 buffers of 64 bits)
-  static constexpr int STAT_FLOATS = 4 * N + 2 * N + 4 * N + 4 * N;
+  // places (64 bits), warp maxima (4), m (2 buffers), rise, sums of the warps (4, 2 buffers), their inverse
+  static constexpr int STAT_FLOATS = 2 * N + 4 * N + 2 * N + N + 8 * N + N;
   static constexpr int FIXED = 1024 + Q_BYTES + P_BUFS * P_PARTS * P_BYTES + STAT_FLOATS * 4 + 384;
   static constexpr int MOST = (228 * 1024 / CTAS - 1024 - FIXED) / SLOT;
   static constexpr int SLOTS = MOST > 12 ? 12 : MOST;
   static constexpr int SMEM_BYTES = FIXED + SLOTS * SLOT;
   static constexpr int S_COL = 0;                       // two buffers of NP
-  static constexpr int O_COL = 2 * NP;                  // NP (8 rows: hi and lo products)
-  static constexpr int TMEM_COLS = 3 * NP <= 64 ? 64 : 3 * NP <= 128 ? 128 : 256;
-  static_assert(SLOTS >= 3 && SMEM_BYTES <= 232448 && 3 * NP <= TMEM_COLS && (2 * SLOTS + 10) * 8 + 28 <= 384, "shared and tensor memory");
+  static constexpr int O_COL = 2 * NP;                  // two buffers of NP (8 rows: hi and lo products)
+  static constexpr int TMEM_COLS = 4 * NP;
+  static_assert(SLOTS >= 3 && SMEM_BYTES <= 232448 && TMEM_COLS <= 256 && (2 * SLOTS + 17) * 8 + 28 <= 384, "shared and tensor memory");
 };
 
 // 2^x; results below the normal range are 0
@@ -174,19 +178,24 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
   uint8_t* sKV = smem;
   uint8_t* sQ = sKV + C::SLOTS * C::SLOT;
   uint8_t* sP = sQ + C::Q_BYTES;                        // buffers of hi, lo
-  long long* s_to = reinterpret_cast<long long*>(sP + C::P_BUFS * C::P_PARTS * C::P_BYTES);   // [2][N] where a row goes
-  float* s_wmax = reinterpret_cast<float*>(s_to + 2 * N);   // [4][N]
-  float* s_m = s_wmax + 4 * N;                          // [N] references
-  float* s_up = s_m + N;                                // [N] their rise
-  float* s_ls = s_up + N;                               // [4][N] the warps' sums
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_ls + 4 * N);
+  long long* s_to = reinterpret_cast<long long*>(sP + C::P_BUFS * C::P_PARTS * C::P_BYTES);   // [N] where a row goes
+  float* s_wmax = reinterpret_cast<float*>(s_to + N);   // [4][N]
+  float* s_ref = s_wmax + 4 * N;                        // [2][N] references, of parts in turn
+  float* s_up = s_ref + 2 * N;                          // [N] their rise
+  float* s_sums = s_up + N;                             // [2][4][N] the warps' sums
+  float* s_inv = s_sums + 8 * N;                        // [N] inverse sums
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_inv + N);
   uint64_t* empty = full + C::SLOTS;
-  uint64_t* qready = empty + C::SLOTS;
-  uint64_t* sfull = qready + 1;                         // [2]
+  uint64_t* qready = empty + C::SLOTS;                  // a part's queries are in place
+  uint64_t* qfree = qready + 1;                         // its last scores are there
+  uint64_t* sfull = qfree + 1;                          // [2]
   uint64_t* sfree = sfull + 2;                          // [2]
   uint64_t* pready = sfree + 2;                         // [2]
   uint64_t* pvdone = pready + 2;                        // [2]
-  uint64_t* mdone = pvdone + 2;                         // every MMA is done
+  uint64_t* lready = pvdone + 2;                        // [2] a part's references and sums are there
+  uint64_t* odone = lready + 2;                         // [2] its last product is done
+  uint64_t* ofree = odone + 2;                          // [2] its output is out
+  uint64_t* mdone = ofree + 2;                          // every MMA is done
   int* s_plan = reinterpret_cast<int*>(mdone + 1);      // first sequence, item, unit; how many units; a CTA's share
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_plan + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -198,8 +207,12 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(qready, C::SOFT / 32);
+    mbar_init(qready, C::HELP / 32);
+    mbar_init(qfree, 1);
     for (int s = 0; s < 2; ++s) {
+      mbar_init(&lready[s], C::SOFT / 32);
+      mbar_init(&odone[s], 1);
+      mbar_init(&ofree[s], C::HELP / 32);
       mbar_init(&sfull[s], 1);
       mbar_init(&sfree[s], C::SOFT / 32);
       mbar_init(&pready[s], C::SOFT / 32);
@@ -271,17 +284,19 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
       const uint64_t pol = p.row_tiles > 1 ? policy_evict_last() : policy_evict_first();
       const int box = min(1 << p.c.page_shift, KT), boxes = KT / box;
       int u = 0;                                          // ring position
-      bool ok = true;
-      do {
-        const int g = (int)p.by_tiles.div((uint32_t)w.item);
-        const int32_t* table = p.c.table + (long long)w.s * p.c.max_pages;
-        auto page_of = [&](int t) {
-          const int at = t * KT + lane * box;
-          return lane < boxes && t < w.t0 + w.nt && at < w.n ? table[at >> p.c.page_shift] : -1;
-        };
-        int page = page_of(w.t0);
-        for (int t = w.t0; t < w.t0 + w.nt && ok; ++t) {
-          const int next = page_of(t + 1);
+      bool ok = true, more = true;
+      // this lane's page of a tile, asked for a tile ahead, across parts too
+      auto page_of = [&](const PagedWalk& x, int t) {
+        const int at = t * KT + lane * box;
+        return lane < boxes && at < x.n ? p.c.table[(long long)x.s * p.c.max_pages + (at >> p.c.page_shift)] : -1;
+      };
+      int page = page_of(w, w.t0);
+      while (more && ok) {
+        const int g = (int)p.by_tiles.div((uint32_t)w.item), end = w.t0 + w.nt;
+        PagedWalk wn = w;
+        more = wn.next(p);
+        for (int t = w.t0; t < end && ok; ++t) {
+          const int next = t + 1 < end ? page_of(w, t + 1) : more ? page_of(wn, wn.t0) : -1;
           const bool there = (unsigned)page < (unsigned)p.c.pages;
           const int y = (t * KT + lane * box) & ((1 << p.c.page_shift) - 1), z = page * p.c.H_kv + g;
           const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, there)) * box) * (HD * 2);
@@ -305,144 +320,127 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
           }
           page = next;
         }
-      } while (ok && w.next(p));
+        w = wn;
+      }
       if (*abort_flag)   // let copies in flight land before the CTA's shared memory goes away
         for (int k = max(u - C::SLOTS, 0); k < u; ++k)
           mbar_wait_long(&full[k % C::SLOTS], (uint32_t)(k / C::SLOTS) & 1u, nullptr, err, ERR_ATTN_FULL);
     } else if (warp == 1) {
       // ------------------------------------------------------ products
       const uint32_t lead = elect_one();
-      auto wait = [&](uint64_t* bar, int phase) {
-        return __all_sync(0xffffffffu, mbar_wait_long(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
-      };
       constexpr uint32_t idesc = (1u << 4) | (F::kFormat << 7) | (F::kFormat << 10) | ((uint32_t)(C::NP >> 3) << 17) |
                                  ((128u >> 4) << 24);
       constexpr uint32_t idesc_o = idesc | (1u << 15) | (1u << 16);     // V and P MN-major
       const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV), p0 = smem_u32(sP);
-      PagedWalk ws = w;                                   // the scores' part, two tiles ahead
-      int s_left = ws.nt, o_left = w.nt;
-      bool s_new = true, o_new = true, s_done = false;
-      auto issue_s = [&](int t) {                         // nothing behind the last tile
-        if (!s_done && s_left == 0) {
-          s_done = !ws.next(p);
-          s_left = ws.nt;
-          s_new = true;
-        }
-        if (s_done) return true;
-        --s_left;
-        const int u = 2 * t, slot = u % C::SLOTS, sb = t & 1;
-        if (s_new && !wait(qready, ws.part)) return false;
-        s_new = false;
-        if (!wait(&full[slot], u / C::SLOTS) || (t >= 2 && !wait(&sfree[sb], (t >> 1) - 1))) return false;
-        tc_fence_after();
-        const uint32_t k = kv0 + slot * C::SLOT, d = tmem + C::S_COL + sb * C::NP;
-#pragma unroll
-        for (int h = 0; h < PARTS; ++h)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f16_ss(lead, d, sdesc_rows<128>(k + h * (KT * 128) + kk * 32),
-                       sdesc_rows<128>(q0 + h * (C::NP * 128) + kk * 32), idesc, (h > 0 || kk > 0) ? 1u : 0u);
-        mma_commit_lead(lead, &empty[slot]);
-        mma_commit_lead(lead, &sfull[sb]);
-        return true;
+      // Scores up to two tiles ahead of the products (a tile's S buffer, and its P buffer, are those of the tile before
+      // the last: S of a tile is issued behind that one's product), whichever finds its operands first.
+      PagedWalk ws = w;                                   // the scores' part
+      int s_left = ws.nt, o_left = w.nt, s_at = 0, o_at = 0;   // tiles of the parts to come; tiles done
+      bool s_new = true, o_new = true, s_done = false, o_done = false, ok = true;
+      auto ready = [&](uint64_t* bar, int phase) {
+        return mbar_test_wait(smem_u32(bar), (uint32_t)phase & 1u) != 0;
       };
-      bool ok = issue_s(0) && issue_s(1);
-      for (int t = 0; ok; ++t) {
-        if (o_left == 0) {
-          if (!w.next(p)) break;
-          o_left = w.nt;
-          o_new = true;
+      unsigned long long t0 = 0;                          // since when nothing was ready
+      while (ok && !o_done) {
+        bool did = false;
+        const int ku = 2 * s_at, kslot = ku % C::SLOTS, sb = s_at & 1;
+        bool s_go = !s_done && s_at <= o_at + 1 && ready(&full[kslot], ku / C::SLOTS) &&
+                    (s_at < 2 || ready(&sfree[sb], (s_at >> 1) - 1)) && (!s_new || ready(qready, ws.part));
+        if (__all_sync(0xffffffffu, s_go)) {
+          tc_fence_after();
+          const uint32_t k = kv0 + kslot * C::SLOT, d = tmem + C::S_COL + sb * C::NP;
+#pragma unroll
+          for (int h = 0; h < PARTS; ++h)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16_ss(lead, d, sdesc_rows<128>(k + h * (KT * 128) + kk * 32),
+                         sdesc_rows<128>(q0 + h * (C::NP * 128) + kk * 32), idesc, (h > 0 || kk > 0) ? 1u : 0u);
+          mma_commit_lead(lead, &empty[kslot]);
+          mma_commit_lead(lead, &sfull[sb]);
+          did = true;
+          ++s_at;
+          s_new = false;
+          if (--s_left == 0) {
+            mma_commit_lead(lead, qfree);
+            s_done = !ws.next(p);
+            s_left = ws.nt;
+            s_new = true;
+          }
         }
-        --o_left;
-        const int u = 2 * t + 1, slot = u % C::SLOTS, pb = C::P_BUFS == 2 ? t & 1 : 0;
-        if (!(ok = wait(&pready[t & 1], t >> 1) && wait(&full[slot], u / C::SLOTS))) break;
-        tc_fence_after();
-        const uint32_t v = kv0 + slot * C::SLOT, pp = p0 + pb * (C::P_PARTS * C::P_BYTES);
+        const int vu = 2 * o_at + 1, vslot = vu % C::SLOTS, b = o_at & 1, pb = C::P_BUFS == 2 ? b : 0;
+        const bool o_go = o_at < s_at && ready(&pready[b], o_at >> 1) && ready(&full[vslot], vu / C::SLOTS);
+        if (__all_sync(0xffffffffu, o_go)) {
+          tc_fence_after();
+          const uint32_t v = kv0 + vslot * C::SLOT, pp = p0 + pb * (C::P_PARTS * C::P_BYTES);
 #pragma unroll
-        for (int part = 0; part < C::P_PARTS; ++part)
+          for (int part = 0; part < C::P_PARTS; ++part)
 #pragma unroll
-          for (int kk = 0; kk < KT / 16; ++kk)
-            // a 64-wide head fills both halves of the 128 dims: the second repeats the first and is not read
-            mma_f16_ss(lead, tmem + C::O_COL, sdesc_rows<128>(v + kk * 2048, HD == 64 ? 0 : KT * 128),
-                       sdesc_rows<C::P_ROW>(pp + part * C::P_BYTES + kk * 16 * C::P_ROW), idesc_o,
-                       (!o_new || part > 0 || kk > 0) ? 1u : 0u);
-        o_new = false;
-        mma_commit_lead(lead, &empty[slot]);
-        mma_commit_lead(lead, &pvdone[t & 1]);
-        ok = issue_s(t + 2);
+            for (int kk = 0; kk < KT / 16; ++kk)
+              // a 64-wide head fills both halves of the 128 dims: the second repeats the first and is not read
+              mma_f16_ss(lead, tmem + C::O_COL + (w.part & 1) * C::NP, sdesc_rows<128>(v + kk * 2048, HD == 64 ? 0 : KT * 128),
+                         sdesc_rows<C::P_ROW>(pp + part * C::P_BYTES + kk * 16 * C::P_ROW), idesc_o,
+                         (!o_new || part > 0 || kk > 0) ? 1u : 0u);
+          mma_commit_lead(lead, &empty[vslot]);
+          mma_commit_lead(lead, &pvdone[b]);
+          did = true;
+          ++o_at;
+          o_new = false;
+          if (--o_left == 0) {
+            mma_commit_lead(lead, &odone[w.part & 1]);
+            o_done = !w.next(p);
+            o_left = w.nt;
+            o_new = true;
+          }
+        }
+        if (did) {
+          t0 = 0;
+        } else {
+          __nanosleep(20);
+          const unsigned long long now = globaltimer();
+          if (t0 == 0) t0 = now;
+          bool stop = *abort_flag != 0;
+          if (now - t0 > kWaitLimitNs) {
+            *abort_flag = 1;
+            record_error(err, ERR_ATTN_FULL);
+            stop = true;
+          }
+          ok = !__any_sync(0xffffffffu, stop);
+        }
       }
       mma_commit_lead(lead, mdone);
       mbar_wait_long(mdone, 0u, nullptr, err, ERR_ATTN_FULL);
-    } else {
+    } else if (warp < 2 + C::SOFT / 32) {
       // ------------------------------------------------------ softmax
       const int tid = (warp - 2) * 32 + lane, q4 = warp & 3, key_l = q4 * 32 + lane;   // this thread's key of a tile
       const int row0 = ((warp - 2) >> 2) * RW;            // its first row
       const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
-      constexpr int L = HD / 8, QV = N * L / C::SOFT > 0 ? N * L / C::SOFT : 1;   // lanes of a row; vectors of a thread
-      uint4 qv[QV];
-      // The query tile of a part: its rows' elements on their way, then in place.  One buffer does: the tile is
-      // stored when the scores of the part before are all there.
-      auto q_load = [&](const PagedWalk& x) {
-        uint32_t rt;
-        const int g = (int)p.by_tiles.divmod((uint32_t)x.item, rt);
-#pragma unroll
-        for (int k = 0; k < QV; ++k) {
-          const int e = tid + k * C::SOFT, row = e / L;
-          uint32_t j;
-          const int at = (int)rt * N + row;
-          const uint32_t i = p.by_group.divmod((uint32_t)min(at, p.rows - 1), j);
-          qv[k] = make_uint4(0, 0, 0, 0);
-          if (row < N && at < p.rows)
-            qv[k] = *reinterpret_cast<const uint4*>(p.q + ((long long)x.s * p.R + i) * p.q_rs +
-                                                    (long long)(g * p.group + (int)j) * HD + e % L * 8);
-        }
-      };
-      auto q_store = [&](const PagedWalk& x) {
-        uint32_t rt;
-        const int g = (int)p.by_tiles.divmod((uint32_t)x.item, rt), buf = x.part & 1;
-#pragma unroll
-        for (int k = 0; k < QV; ++k) {
-          const int e = tid + k * C::SOFT, row = e / L, c = e % L;
-          if (row < N)
-            *reinterpret_cast<uint4*>(sQ + (c >> 3) * (C::NP * 128) + swizzled<128>(row, c & 7)) = qv[k];
-        }
-        if (tid < N) {
-          uint32_t j;
-          const int at = (int)rt * N + tid;
-          const uint32_t i = p.by_group.divmod((uint32_t)min(at, p.rows - 1), j);
-          s_to[buf * N + tid] = ((long long)x.s * p.R + i) * p.o_rs + (long long)(g * p.group + (int)j) * HD;
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(qready);
-      };
-      q_load(w);
-      q_store(w);
       bool ok = true, more = true;
       // after a wait that gave up (ok false) the loop goes on without waiting, so that every warp meets every
       // barrier; the outputs are invalid and reported
       auto wait = [&](uint64_t* bar, int phase) {
         ok = __all_sync(0xffffffffu, mbar_wait_long(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) && ok;
       };
+      // the page of this thread's key of a tile, asked for a tile ahead, across parts too
+      auto page_of = [&](const PagedWalk& x, int t) {
+        const int key = t * KT + key_l;
+        return key < x.n ? p.c.table[(long long)x.s * p.c.max_pages + (key >> p.c.page_shift)] : -1;
+      };
+      int page = page_of(w, w.t0);
       int tt = 0;                                         // tiles so far
       while (more) {
         float l_sum[RW];
 #pragma unroll
         for (int j = 0; j < RW; ++j) l_sum[j] = 0.0f;
-        const int32_t* table = p.c.table + (long long)w.s * p.c.max_pages;
         const long long item = (long long)w.s * p.per_seq + w.item;
-        auto page_of = [&](int t) {
-          const int key = t * KT + key_l;
-          return t < w.t0 + w.nt && key < w.n ? table[key >> p.c.page_shift] : -1;
-        };
-        int page = page_of(w.t0);
         PagedWalk wn = w;
         more = wn.next(p);
-        if (more) q_load(wn);
+        float* m_at = s_ref + (w.part & 1) * N;
+        const uint32_t ocol = trow + C::O_COL + (w.part & 1) * C::NP;
+        if (w.part >= 2) wait(&ofree[w.part & 1], (w.part >> 1) - 1);   // the part before the last is out
         for (int t = 0; t < w.nt; ++t, ++tt) {
           const int b = tt & 1, pb = C::P_BUFS == 2 ? b : 0;
           const bool seen = (unsigned)page < (unsigned)p.c.pages;
-          page = page_of(w.t0 + t + 1);
+          page = t + 1 < w.nt ? page_of(w, w.t0 + t + 1) : more ? page_of(wn, wn.t0) : -1;
           wait(&sfull[b], tt >> 1);
           tc_fence_after();
           float z[RW];
@@ -462,7 +460,7 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
           if (t > 0) {
 #pragma unroll
             for (int j = 0; j < RW; j += 4) {
-              const float4 m = *reinterpret_cast<const float4*>(s_m + row0 + j);
+              const float4 m = *reinterpret_cast<const float4*>(m_at + row0 + j);
               z[j] -= m.x;
               z[j + 1] -= m.y;
               z[j + 2] -= m.z;
@@ -483,7 +481,7 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
               float up = fmaxf(fmaxf(s_wmax[tid], s_wmax[N + tid]), fmaxf(s_wmax[2 * N + tid], s_wmax[3 * N + tid]));
               if (!(up > -INFINITY) || (t > 0 && up < 0.0f)) up = 0.0f;
               s_up[tid] = up;
-              s_m[tid] = t == 0 ? up : s_m[tid] + up;
+              m_at[tid] = t == 0 ? up : m_at[tid] + up;
             }
             named_bar_sync(2, C::SOFT);
 #pragma unroll
@@ -499,10 +497,10 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
               }
 #pragma unroll
               for (int part = 0; part < (N < 16 ? 2 : 1); ++part) {
-                tmem_ld<RW>(trow + C::O_COL + part * N + row0, o);
+                tmem_ld<RW>(ocol + part * N + row0, o);
 #pragma unroll
                 for (int j = 0; j < RW; ++j) o[j] *= f[j];
-                tmem_st<RW>(trow + C::O_COL + part * N + row0, o);
+                tmem_st<RW>(ocol + part * N + row0, o);
               }
             }
             // (the maxima are read again only behind the next vote)
@@ -548,7 +546,6 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
           __syncwarp();
           if (lane == 0) mbar_arrive(&pready[b]);
         }
-        if (more) q_store(wn);
         // sum RW columns over the warp, lane c (modulo RW) ending with column c, while the last product runs
 #pragma unroll
         for (int s = RW / 2; s >= 1; s >>= 1) {
@@ -562,62 +559,126 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
         }
 #pragma unroll
         for (int s = RW; s < 32; s <<= 1) l_sum[0] += __shfl_xor_sync(0xffffffffu, l_sum[0], s);
-        if (lane < RW) s_ls[q4 * N + row0 + lane] = l_sum[0];
-        named_bar_sync(2, C::SOFT);
-        // ------------------------------------------------------ the part's output
-        const bool complete = w.complete();
-        const int n_rows = min(N, p.rows - (w.item - (int)p.by_tiles.div((uint32_t)w.item) * p.row_tiles) * N);
-        const int slot = 2 * blockIdx.x + (w.part > 0 ? 1 : 0);
-        if (tid < N) {
-          const float l = (s_ls[tid] + s_ls[N + tid]) + (s_ls[2 * N + tid] + s_ls[3 * N + tid]);
-          if (!complete)
-            *reinterpret_cast<float2*>(p.ws_ml + ((long long)slot * N + tid) * 2) = make_float2(s_m[tid], l);
-          else if (p.mass)
-            p.ws_lse[item * N + tid] = l == 0.0f ? INFINITY : s_m[tid] + log2f(l);
-          s_up[tid] = l == 0.0f ? 0.0f : 1.0f / l;
-        }
-        if (tid == 0 && w.t0 == 0 && !p.whole) {
-          // where the item's other parts lie: CTAs that follow, each with `share` tiles
-          int2 plan = make_int2(-1, -1);
-          if (!complete) {
-            const int rest = paged_tiles(w.n) - w.nt, share = s_plan[4];
-            plan = make_int2(slot, 2 * ((int)blockIdx.x + (rest + share - 1) / share));
-          }
-          p.ws_plan[item] = plan;
-        }
-        named_bar_sync(2, C::SOFT);
-        wait(&pvdone[(tt - 1) & 1], (tt - 1) >> 1);
-        tc_fence_after();
-        const int dim = q4 * 32 + lane;
-        const long long* to = s_to + (w.part & 1) * N;
-#pragma unroll
-        for (int n = 0; n < RW; n += 8) {
-          float o[8];
-          if constexpr (N < 16) {
-            float o2[8];
-            tmem_ld8x2(trow + C::O_COL, trow + C::O_COL + N, o, o2);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] += o2[j];
-          } else {
-            tmem_ld8(trow + C::O_COL + row0 + n, o);
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int r = row0 + n + j;
-            const float f = s_up[r], v = f == 0.0f ? 0.0f : o[j] * f;
-            if (dim < HD && r < n_rows) {
-              if (complete)
-                F::E::put(reinterpret_cast<T*>(p.out) + to[r] + dim, v);
-              else
-                p.ws_o[((long long)slot * N + r) * HD + dim] = v;
-            }
-          }
-        }
-        tc_fence_before();
+        if (lane < RW) s_sums[(w.part & 1) * 4 * N + q4 * N + row0 + lane] = l_sum[0];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&lready[w.part & 1]);
         if (more) w = wn;
       }
+    } else {
+      // ------------------------------------------------------ query tiles and output
+      const int tid = (warp - 2) * 32 + lane - C::SOFT, q4 = warp & 3, dim = q4 * 32 + lane;
+      const uint32_t trow = tmem + ((uint32_t)(q4 * 32) << 16);
+      constexpr int L = HD / 8, QV = N * L / C::HELP > 0 ? N * L / C::HELP : 1;   // lanes of a row; vectors of a thread
+      bool ok = true, more = true;
+      auto wait = [&](uint64_t* bar, int phase) {
+        ok = __all_sync(0xffffffffu, mbar_wait_long(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) && ok;
+      };
+      // a row of a part's tile: where it lies in q, and in out
+      auto row_at = [&](const PagedWalk& x, int row, long long stride) {
+        uint32_t rt, j;
+        const int g = (int)p.by_tiles.divmod((uint32_t)x.item, rt);
+        const uint32_t i = p.by_group.divmod((uint32_t)min((int)rt * N + row, p.rows - 1), j);
+        return ((long long)x.s * p.R + i) * stride + (long long)(g * p.group + (int)j) * HD;
+      };
+      auto rows_of = [&](const PagedWalk& x) {
+        return min(N, p.rows - (x.item - (int)p.by_tiles.div((uint32_t)x.item) * p.row_tiles) * N);
+      };
+      uint4 qv[QV];
+      auto q_load = [&](const PagedWalk& x) {
+        const int n_rows = rows_of(x);
+#pragma unroll
+        for (int k = 0; k < QV; ++k) {
+          const int e = tid + k * C::HELP, row = e / L;
+          qv[k] = make_uint4(0, 0, 0, 0);
+          if (row < n_rows) qv[k] = *reinterpret_cast<const uint4*>(p.q + row_at(x, row, p.q_rs) + e % L * 8);
+        }
+      };
+      auto q_store = [&] {
+#pragma unroll
+        for (int k = 0; k < QV; ++k) {
+          const int e = tid + k * C::HELP, row = e / L, c = e % L;
+          if (row < N) *reinterpret_cast<uint4*>(sQ + (c >> 3) * (C::NP * 128) + swizzled<128>(row, c & 7)) = qv[k];
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qready);
+      };
+      int4 plan = make_int4(-1, 0, 0, 0);                 // (an item that goes on in the next CTA is this one's last)
+      q_load(w);
+      q_store();
+      while (more) {
+        PagedWalk wn = w;
+        more = wn.next(p);
+        if (more) {
+          q_load(wn);
+          wait(qfree, w.part);
+          q_store();
+        }
+        const int b = w.part & 1, n_rows = rows_of(w), slot = 2 * blockIdx.x + (w.part > 0 ? 1 : 0);
+        const long long item = (long long)w.s * p.per_seq + w.item;
+        const bool complete = w.complete();
+        if (tid < N) s_to[tid] = complete ? row_at(w, tid, p.o_rs) : ((long long)slot * N + tid) * HD;
+        if (!complete && w.t0 == 0) {
+          // where the item's other parts lie: CTAs that follow, each with `share` units
+          const int rest = paged_tiles(w.n) - w.nt, share = s_plan[4];
+          plan = make_int4((int)item, slot, 2 * ((int)blockIdx.x + (rest + share - 1) / share), 0);
+        }
+        wait(&lready[b], w.part >> 1);
+        if (tid < N) {
+          const float* ls = s_sums + b * 4 * N + tid;
+          const float l = (ls[0] + ls[N]) + (ls[2 * N] + ls[3 * N]), m = s_ref[b * N + tid];
+          if (!complete)
+            *reinterpret_cast<float2*>(p.ws_ml + ((long long)slot * N + tid) * 2) = make_float2(m, l);
+          else if (p.mass)
+            p.ws_lse[item * N + tid] = l == 0.0f ? INFINITY : m + log2f(l);
+          s_inv[tid] = l == 0.0f ? 0.0f : 1.0f / l;
+        }
+        named_bar_sync(3, C::HELP);
+        wait(&odone[b], w.part >> 1);
+        tc_fence_after();
+        const uint32_t ocol = trow + C::O_COL + b * C::NP;
+        // (rolled: code that runs once a part costs its instruction fetches)
+        auto put = [&](auto store) {
+#pragma unroll 1
+          for (int n = 0; n < n_rows; n += 8) {
+            float o[8];
+            if constexpr (N < 16) {
+              float o2[8];
+              tmem_ld8x2(ocol, ocol + N, o, o2);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) o[j] += o2[j];
+            } else {
+              tmem_ld8(ocol + n, o);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float f = s_inv[n + j];
+              if (dim < HD && n + j < n_rows) store(s_to[n + j] + dim, f == 0.0f ? 0.0f : o[j] * f);
+            }
+          }
+        };
+        if (complete)
+          put([&](long long at, float v) { F::E::put(reinterpret_cast<T*>(p.out) + at, v); });
+        else
+          put([&](long long at, float v) { p.ws_o[at] = v; });
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ofree[b]);
+        named_bar_sync(3, C::HELP);                       // the places and sums are read: the next part's may be written
+        if (more) w = wn;
+      }
+      if (tid == 0 && !p.whole) p.ws_plan[blockIdx.x] = plan;
     }
+  } else if (threadIdx.x == 0 && !p.whole) {
+    p.ws_plan[blockIdx.x] = make_int4(-1, 0, 0, 0);
   }
+  // the rows of sequences without keys, which are nobody's items
+  if (!p.whole)
+    for (int s = blockIdx.x; s < p.c.b; s += gridDim.x)
+      if (p.c.len(p.lens, s) == 0)
+        for (int e = threadIdx.x; e < p.R * p.H * (HD / 8); e += C::THREADS)
+          *reinterpret_cast<uint4*>(p.out + ((long long)s * p.R + e / (p.H * (HD / 8))) * p.o_rs +
+                                    (long long)(e % (p.H * (HD / 8))) * 8) = make_uint4(0, 0, 0, 0);
   // lanes that skipped their role arrive here first: reconverge before the CTA-wide barrier
   __syncwarp();
   tc_fence_before();
@@ -629,27 +690,25 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
 }
 
 // Joins the parts of split items: weights l 2^m over their sum (l is 1 at least, 2^51 at most, and m the part's
-// reference: what a weight loses to underflow is nothing beside the largest).  A CTA a row; its warps share the parts.
+// reference: what a weight loses to underflow is nothing beside the largest).  A CTA of 4 warps, which share the parts, a
+// row of the item that goes on from one CTA of the kernel before to the next.
 template <typename F, int HD>
 __global__ void __launch_bounds__(128) attn_paged_join_kernel(const __grid_constant__ AttnPagedParams p, int N) {
   __shared__ float s_o[4][HD], s_w[4];
-  const long long item = blockIdx.x;
   const int r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_launch_dependents();
   griddep_wait();
-  const int s = (int)(item / p.per_seq);
+  const int4 at = p.ws_plan[blockIdx.x];
+  if (at.x < 0) return;
+  const long long item = at.x;
+  const int2 plan = make_int2(at.y, at.z);
+  const int s = at.x / p.per_seq;
   uint32_t rt, j;
-  const int g = (int)p.by_tiles.divmod((uint32_t)(item - (long long)s * p.per_seq), rt);
+  const int g = (int)p.by_tiles.divmod((uint32_t)(at.x - s * p.per_seq), rt);
   if ((int)rt * N + r >= p.rows) return;
   const uint32_t i = p.by_group.divmod(rt * (uint32_t)N + (uint32_t)r, j);
   typename F::E::T* out = reinterpret_cast<typename F::E::T*>(p.out) + ((long long)s * p.R + i) * p.o_rs +
                           (long long)(g * p.group + (int)j) * HD + threadIdx.x;
-  if (p.c.len(p.lens, s) == 0) {   // nobody's item
-    if (threadIdx.x < HD) F::E::put(out, 0.0f);
-    return;
-  }
-  const int2 plan = p.ws_plan[item];
-  if (plan.x < 0) return;
   // slots: the first CTA's, then every following one's first
   const int parts = (plan.y >> 1) - (plan.x >> 1) + 1;
   auto slot_of = [&](int k) { return k == 0 ? plan.x : ((plan.x >> 1) + k) * 2; };
