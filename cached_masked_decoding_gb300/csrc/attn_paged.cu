@@ -137,7 +137,7 @@ extern "C" dllm_status dllm_op_attention_paged(const void* q, int64_t q_row_stri
   p.whole = a.whole;
   p.min_share = a.whole ? 1 : 2;
   p.by_group = FastDiv((uint32_t)p.group);
-  p.by_tiles = FastDiv((uint32_t)a.row_tiles);
+  p.by_heads = FastDiv((uint32_t)cache->H_kv);
   p.by_chunks = FastDiv((uint32_t)((p.c.positions + 255) / 256));
   p.nz = a.nz;
   p.z_tiles = (int)a.tiles;

@@ -45,7 +45,8 @@ struct AttnPagedParams {
   int H, R, group, rows;      // rows: R * group of a cached head, in row_tiles tiles of N
   int row_tiles, per_seq;     // per_seq: items of a sequence, H_kv * row_tiles
   int min_share, whole;       // units a CTA takes at least; whole: items are not split
-  FastDiv by_group, by_tiles; // by_tiles: by row_tiles
+  FastDiv by_group, by_heads; // by_heads: by H_kv.  An item of a sequence: row tile * H_kv + cached head, so that the
+                              // row tiles of a head's keys run on different SMs at about the same time
   FastDiv by_chunks;          // by the 256-key chunks of a table
   float scale_log2;
   int nz, z_tiles;            // scores kept for the weights: [item][z_tiles][128][nz]
@@ -292,13 +293,15 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
       };
       int page = page_of(w, w.t0);
       while (more && ok) {
-        const int g = (int)p.by_tiles.div((uint32_t)w.item), end = w.t0 + w.nt;
+        uint32_t g;
+        p.by_heads.divmod((uint32_t)w.item, g);
+        const int end = w.t0 + w.nt;
         PagedWalk wn = w;
         more = wn.next(p);
         for (int t = w.t0; t < end && ok; ++t) {
           const int next = t + 1 < end ? page_of(w, t + 1) : more ? page_of(wn, wn.t0) : -1;
           const bool there = (unsigned)page < (unsigned)p.c.pages;
-          const int y = (t * KT + lane * box) & ((1 << p.c.page_shift) - 1), z = page * p.c.H_kv + g;
+          const int y = (t * KT + lane * box) & ((1 << p.c.page_shift) - 1), z = page * p.c.H_kv + (int)g;
           const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, there)) * box) * (HD * 2);
 #pragma unroll
           for (int v = 0; v < 2; ++v, ++u) {
@@ -575,13 +578,13 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
       };
       // a row of a part's tile: where it lies in q, and in out
       auto row_at = [&](const PagedWalk& x, int row, long long stride) {
-        uint32_t rt, j;
-        const int g = (int)p.by_tiles.divmod((uint32_t)x.item, rt);
-        const uint32_t i = p.by_group.divmod((uint32_t)min((int)rt * N + row, p.rows - 1), j);
-        return ((long long)x.s * p.R + i) * stride + (long long)(g * p.group + (int)j) * HD;
+        uint32_t g, j;
+        const int rt = (int)p.by_heads.divmod((uint32_t)x.item, g);
+        const uint32_t i = p.by_group.divmod((uint32_t)min(rt * N + row, p.rows - 1), j);
+        return ((long long)x.s * p.R + i) * stride + (long long)((int)g * p.group + (int)j) * HD;
       };
       auto rows_of = [&](const PagedWalk& x) {
-        return min(N, p.rows - (x.item - (int)p.by_tiles.div((uint32_t)x.item) * p.row_tiles) * N);
+        return min(N, p.rows - (int)p.by_heads.div((uint32_t)x.item) * N);
       };
       uint4 qv[QV];
       auto q_load = [&](const PagedWalk& x) {
@@ -703,12 +706,12 @@ __global__ void __launch_bounds__(128) attn_paged_join_kernel(const __grid_const
   const long long item = at.x;
   const int2 plan = make_int2(at.y, at.z);
   const int s = at.x / p.per_seq;
-  uint32_t rt, j;
-  const int g = (int)p.by_tiles.divmod((uint32_t)(at.x - s * p.per_seq), rt);
+  uint32_t g, j;
+  const uint32_t rt = p.by_heads.divmod((uint32_t)(at.x - s * p.per_seq), g);
   if ((int)rt * N + r >= p.rows) return;
   const uint32_t i = p.by_group.divmod(rt * (uint32_t)N + (uint32_t)r, j);
   typename F::E::T* out = reinterpret_cast<typename F::E::T*>(p.out) + ((long long)s * p.R + i) * p.o_rs +
-                          (long long)(g * p.group + (int)j) * HD + threadIdx.x;
+                          (long long)((int)g * p.group + (int)j) * HD + threadIdx.x;
   // slots: the first CTA's, then every following one's first
   const int parts = (plan.y >> 1) - (plan.x >> 1) + 1;
   auto slot_of = [&](int k) { return k == 0 ? plan.x : ((plan.x >> 1) + k) * 2; };
@@ -772,15 +775,15 @@ static __global__ void __launch_bounds__(256) attn_paged_mass_kernel(const __gri
   const int n = (int)min((long long)p.c.len(p.lens, s), p.mass_rs);
   const int t = (int)(chunk * 256 + threadIdx.x);
   if ((int)(chunk * 256) >= n) return;
-  const long long item0 = (long long)s * p.per_seq + (long long)g * p.row_tiles;
+  const long long item0 = (long long)s * p.per_seq + g;   // the head's first row tile; then H_kv apart
   float sum = 0.0f;
   for (int rt = 0; rt < p.row_tiles; ++rt) {
     const int n_rows = min(N, p.rows - rt * N);
     __syncthreads();
-    if ((int)threadIdx.x < N) s_lse[threadIdx.x] = p.ws_lse[(item0 + rt) * N + threadIdx.x];
+    if ((int)threadIdx.x < N) s_lse[threadIdx.x] = p.ws_lse[(item0 + (long long)rt * p.c.H_kv) * N + threadIdx.x];
     __syncthreads();
     if (t >= n) continue;
-    const float* z = p.ws_z + (((item0 + rt) * p.z_tiles + t / kPagedKeys) * kPagedKeys + t % kPagedKeys) * p.nz;
+    const float* z = p.ws_z + (((item0 + (long long)rt * p.c.H_kv) * p.z_tiles + t / kPagedKeys) * kPagedKeys + t % kPagedKeys) * p.nz;
     for (int r = 0; r < n_rows; r += 4) {
       const float4 v = *reinterpret_cast<const float4*>(z + r);
       sum += pow2_approx(v.x - s_lse[r]);
