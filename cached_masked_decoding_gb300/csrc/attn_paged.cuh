@@ -2,10 +2,10 @@
 //
 // Keys are the 128-row operand, so K and V go from HBM to the tensor cores as they are.  A tile of 128 keys gives
 //   S^T[key][row] = K Q^T,      O^T[dim][row] += V^T P^T        (tcgen05, kind::f16)
-// with N = 8, 16, 32 or 64 rows as the narrow operand (8: in products of 16 columns).  V is read MN-major from its
-// TMA tile.  A probability is the sum of two values of the cache's type, hi and lo, each a product of its own into
-// one sum (8 rows: the two side by side in 16 columns): one rounding of P to bf16 alone is as large an error as the
-// output's own rounding.
+// with N = 8, 16, 32 or 64 rows as the narrow operand (8: scores in 16 columns).  V is read MN-major from its
+// TMA tile.  A probability is the sum of two values of the cache's type, hi and lo, side by side in 2 N columns of one
+// product: one rounding of P to bf16 alone is as large an error as the output's own rounding.  (A product costs its
+// wide operand's reading, whatever N: hi and lo as products of their own made 24 a tile of 16, ATTN_HILO.)
 //
 // Bound by HBM: 4 hd bytes a key and cached head.  So the work is shared out evenly whatever the lengths: one CTA an
 // SM takes an equal run of tiles of the (sequence, cached head, row tile) items laid end to end, and its ring of TMA
@@ -89,11 +89,11 @@ struct AttnPagedCfg {
   static constexpr int SLOT = KT * HD * 2;              // one K or V tile: HD / 64 parts of 128 keys x 128 bytes
   static constexpr int NP = N < 16 ? 16 : N;            // columns of a product
   static constexpr int Q_BYTES = NP * HD * 2;           // HD / 64 parts of NP rows x 128 bytes
-  static constexpr int P_ROW = 2 * NP;                  // a key's probabilities (8 rows: hi, then lo)
-  static constexpr int P_PARTS = N < 16 ? 1 : 2;
+  static constexpr int P_ROW = 4 * N < 128 ? 4 * N : 128;   // a key's probabilities, hi, then lo (64 rows: a part each)
+  static constexpr int P_PARTS = N == 64 ? 2 : 1;
   static constexpr int P_BYTES = KT * P_ROW;            // one part
   static constexpr int CTAS = N <= 16 ? 2 : 1;          // an SM
-  static constexpr int P_BUFS = N == 64 || (N == 16 && HD == 128) ? 1 : 2;
+  static constexpr int P_BUFS = N == 16 && HD == 128 ? 1 : 2;
   // places (64 bits), warp maxima (4), m (2 buffers), rise, sums of the warps (4, 2 buffers), their inverse
   static constexpr int STAT_FLOATS = 2 * N + 4 * N + 2 * N + N + 8 * N + N;
   static constexpr int FIXED = 1024 + Q_BYTES + P_BUFS * P_PARTS * P_BYTES + STAT_FLOATS * 4 + 384;
@@ -101,9 +101,9 @@ struct AttnPagedCfg {
   static constexpr int SLOTS = MOST > 12 ? 12 : MOST;
   static constexpr int SMEM_BYTES = FIXED + SLOTS * SLOT;
   static constexpr int S_COL = 0;                       // two buffers of NP
-  static constexpr int O_COL = 2 * NP;                  // two buffers of NP (8 rows: hi and lo products)
-  static constexpr int TMEM_COLS = 4 * NP;
-  static_assert(SLOTS >= 3 && SMEM_BYTES <= 232448 && TMEM_COLS <= 256 && (2 * SLOTS + 17) * 8 + 28 <= 384, "shared and tensor memory");
+  static constexpr int O_COL = 2 * NP;                  // two buffers of 2 N, the products of hi and of lo
+  static constexpr int TMEM_COLS = N == 8 ? 64 : N == 16 ? 128 : N == 32 ? 256 : 512;
+  static_assert(SLOTS >= 3 && SMEM_BYTES <= 232448 && 2 * NP + 4 * N <= TMEM_COLS && CTAS * TMEM_COLS <= 512 && (2 * SLOTS + 17) * 8 + 28 <= 384, "shared and tensor memory");
 };
 
 // 2^x; results below the normal range are 0
@@ -333,7 +333,8 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
       const uint32_t lead = elect_one();
       constexpr uint32_t idesc = (1u << 4) | (F::kFormat << 7) | (F::kFormat << 10) | ((uint32_t)(C::NP >> 3) << 17) |
                                  ((128u >> 4) << 24);
-      constexpr uint32_t idesc_o = idesc | (1u << 15) | (1u << 16);     // V and P MN-major
+      constexpr uint32_t idesc_o = (1u << 4) | (F::kFormat << 7) | (F::kFormat << 10) | (1u << 15) | (1u << 16) |
+                                   ((uint32_t)(2 * N >> 3) << 17) | ((128u >> 4) << 24);     // V and P MN-major
       const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV), p0 = smem_u32(sP);
       // Scores up to two tiles ahead of the products (a tile's S buffer, and its P buffer, are those of the tile before
       // the last: S of a tile is issued behind that one's product), whichever finds its operands first.
@@ -376,13 +377,11 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
           tc_fence_after();
           const uint32_t v = kv0 + vslot * C::SLOT, pp = p0 + pb * (C::P_PARTS * C::P_BYTES);
 #pragma unroll
-          for (int part = 0; part < C::P_PARTS; ++part)
-#pragma unroll
-            for (int kk = 0; kk < KT / 16; ++kk)
-              // a 64-wide head fills both halves of the 128 dims: the second repeats the first and is not read
-              mma_f16_ss(lead, tmem + C::O_COL + (w.part & 1) * C::NP, sdesc_rows<128>(v + kk * 2048, HD == 64 ? 0 : KT * 128),
-                         sdesc_rows<C::P_ROW>(pp + part * C::P_BYTES + kk * 16 * C::P_ROW), idesc_o,
-                         (!o_new || part > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < KT / 16; ++kk)
+            // a 64-wide head fills both halves of the 128 dims: the second repeats the first and is not read
+            mma_f16_ss(lead, tmem + C::O_COL + (w.part & 1) * 2 * N, sdesc_rows<128>(v + kk * 2048, HD == 64 ? 0 : KT * 128),
+                       sdesc_rows<C::P_ROW>(pp + kk * 16 * C::P_ROW, C::P_PARTS == 2 ? C::P_BYTES : 16), idesc_o,
+                       (!o_new || kk > 0) ? 1u : 0u);
           mma_commit_lead(lead, &empty[vslot]);
           mma_commit_lead(lead, &pvdone[b]);
           did = true;
@@ -438,7 +437,7 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
         PagedWalk wn = w;
         more = wn.next(p);
         float* m_at = s_ref + (w.part & 1) * N;
-        const uint32_t ocol = trow + C::O_COL + (w.part & 1) * C::NP;
+        const uint32_t ocol = trow + C::O_COL + (w.part & 1) * 2 * N;
         if (w.part >= 2) wait(&ofree[w.part & 1], (w.part >> 1) - 1);   // the part before the last is out
         for (int t = 0; t < w.nt; ++t, ++tt) {
           const int b = tt & 1, pb = C::P_BUFS == 2 ? b : 0;
@@ -499,7 +498,7 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
                 l_sum[j] *= f[j];
               }
 #pragma unroll
-              for (int part = 0; part < (N < 16 ? 2 : 1); ++part) {
+              for (int part = 0; part < 2; ++part) {
                 tmem_ld<RW>(ocol + part * N + row0, o);
 #pragma unroll
                 for (int j = 0; j < RW; ++j) o[j] *= f[j];
@@ -527,8 +526,8 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
             const uint4 h = make_uint4(hi[j / 2], hi[j / 2 + 1], hi[j / 2 + 2], hi[j / 2 + 3]);
             const uint4 l = make_uint4(lo[j / 2], lo[j / 2 + 1], lo[j / 2 + 2], lo[j / 2 + 3]);
             *reinterpret_cast<uint4*>(pp + swizzled<C::P_ROW>(key_l, (row0 + j) >> 3)) = h;
-            if constexpr (N < 16)
-              *reinterpret_cast<uint4*>(pp + swizzled<C::P_ROW>(key_l, 1)) = l;
+            if constexpr (C::P_PARTS == 1)
+              *reinterpret_cast<uint4*>(pp + swizzled<C::P_ROW>(key_l, (N + row0 + j) >> 3)) = l;
             else
               *reinterpret_cast<uint4*>(pp + C::P_BYTES + swizzled<C::P_ROW>(key_l, (row0 + j) >> 3)) = l;
           }
@@ -639,20 +638,16 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
         named_bar_sync(3, C::HELP);
         wait(&odone[b], w.part >> 1);
         tc_fence_after();
-        const uint32_t ocol = trow + C::O_COL + b * C::NP;
+        const uint32_t ocol = trow + C::O_COL + b * 2 * N;
         // (rolled: code that runs once a part costs its instruction fetches)
         auto put = [&](auto store) {
 #pragma unroll 1
           for (int n = 0; n < n_rows; n += 8) {
             float o[8];
-            if constexpr (N < 16) {
-              float o2[8];
-              tmem_ld8x2(ocol, ocol + N, o, o2);
+            float o2[8];
+            tmem_ld8x2(ocol + n, ocol + N + n, o, o2);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) o[j] += o2[j];
-            } else {
-              tmem_ld8(ocol + n, o);
-            }
+            for (int j = 0; j < 8; ++j) o[j] += o2[j];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const float f = s_inv[n + j];
