@@ -4,8 +4,7 @@
 //   S^T[key][row] = K Q^T,      O^T[dim][row] += V^T P^T        (tcgen05, kind::f16)
 // with N = 8, 16, 32 or 64 rows as the narrow operand (8: scores in 16 columns).  V is read MN-major from its
 // TMA tile.  A probability is the sum of two values of the cache's type, hi and lo, side by side in 2 N columns of one
-// product: one rounding of P to bf16 alone is as large an error as the output's own rounding.  (A product costs its
-// wide operand's reading, whatever N: hi and lo as products of their own made 24 a tile of 16, ATTN_HILO.)
+// product: one rounding of P to bf16 alone is as large an error as the output's own rounding.
 //
 // Bound by HBM: 4 hd bytes a key and cached head.  So the work is shared out evenly whatever the lengths: one CTA an
 // SM takes an equal run of tiles of the (sequence, cached head, row tile) items laid end to end, and its ring of TMA
@@ -336,78 +335,61 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
       constexpr uint32_t idesc_o = (1u << 4) | (F::kFormat << 7) | (F::kFormat << 10) | (1u << 15) | (1u << 16) |
                                    ((uint32_t)(2 * N >> 3) << 17) | ((128u >> 4) << 24);     // V and P MN-major
       const uint32_t q0 = smem_u32(sQ), kv0 = smem_u32(sKV), p0 = smem_u32(sP);
-      // Scores up to two tiles ahead of the products (a tile's S buffer, and its P buffer, are those of the tile before
-      // the last: S of a tile is issued behind that one's product), whichever finds its operands first.
-      PagedWalk ws = w;                                   // the scores' part
-      int s_left = ws.nt, o_left = w.nt, s_at = 0, o_at = 0;   // tiles of the parts to come; tiles done
-      bool s_new = true, o_new = true, s_done = false, o_done = false, ok = true;
-      auto ready = [&](uint64_t* bar, int phase) {
-        return mbar_test_wait(smem_u32(bar), (uint32_t)phase & 1u) != 0;
+      auto wait = [&](uint64_t* bar, int phase) {
+        return __all_sync(0xffffffffu, mbar_wait_long(bar, (uint32_t)phase & 1u, abort_flag, err, ERR_ATTN_FULL)) != 0;
       };
-      unsigned long long t0 = 0;                          // since when nothing was ready
-      while (ok && !o_done) {
-        bool did = false;
-        const int ku = 2 * s_at, kslot = ku % C::SLOTS, sb = s_at & 1;
-        bool s_go = !s_done && s_at <= o_at + 1 && ready(&full[kslot], ku / C::SLOTS) &&
-                    (s_at < 2 || ready(&sfree[sb], (s_at >> 1) - 1)) && (!s_new || ready(qready, ws.part));
-        if (__all_sync(0xffffffffu, s_go)) {
-          tc_fence_after();
-          const uint32_t k = kv0 + kslot * C::SLOT, d = tmem + C::S_COL + sb * C::NP;
+      // Scores two tiles ahead of the products: a tile's S and P buffers are those of the tile before the last, and its
+      // S is issued behind that one's product.  (Issuing whichever finds its operands first was 5 % slower, hd 64.)
+      PagedWalk ws = w;                                   // the scores' part
+      int s_left = ws.nt, o_left = w.nt;
+      bool s_new = true, o_new = true, s_done = false;
+      auto issue_s = [&](int t) {                         // nothing behind the last tile
+        if (s_done) return true;
+        const int u = 2 * t, slot = u % C::SLOTS, sb = t & 1;
+        if ((s_new && !wait(qready, ws.part)) || !wait(&full[slot], u / C::SLOTS) ||
+            (t >= 2 && !wait(&sfree[sb], (t >> 1) - 1)))
+          return false;
+        s_new = false;
+        tc_fence_after();
+        const uint32_t k = kv0 + slot * C::SLOT, d = tmem + C::S_COL + sb * C::NP;
 #pragma unroll
-          for (int h = 0; h < PARTS; ++h)
+        for (int h = 0; h < PARTS; ++h)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f16_ss(lead, d, sdesc_rows<128>(k + h * (KT * 128) + kk * 32),
-                         sdesc_rows<128>(q0 + h * (C::NP * 128) + kk * 32), idesc, (h > 0 || kk > 0) ? 1u : 0u);
-          mma_commit_lead(lead, &empty[kslot]);
-          mma_commit_lead(lead, &sfull[sb]);
-          did = true;
-          ++s_at;
-          s_new = false;
-          if (--s_left == 0) {
-            mma_commit_lead(lead, qfree);
-            s_done = !ws.next(p);
-            s_left = ws.nt;
-            s_new = true;
-          }
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_ss(lead, d, sdesc_rows<128>(k + h * (KT * 128) + kk * 32),
+                       sdesc_rows<128>(q0 + h * (C::NP * 128) + kk * 32), idesc, (h > 0 || kk > 0) ? 1u : 0u);
+        mma_commit_lead(lead, &empty[slot]);
+        mma_commit_lead(lead, &sfull[sb]);
+        if (--s_left == 0) {
+          mma_commit_lead(lead, qfree);
+          s_done = !ws.next(p);
+          s_left = ws.nt;
+          s_new = true;
         }
-        const int vu = 2 * o_at + 1, vslot = vu % C::SLOTS, b = o_at & 1, pb = C::P_BUFS == 2 ? b : 0;
-        const bool o_go = o_at < s_at && ready(&pready[b], o_at >> 1) && ready(&full[vslot], vu / C::SLOTS);
-        if (__all_sync(0xffffffffu, o_go)) {
-          tc_fence_after();
-          const uint32_t v = kv0 + vslot * C::SLOT, pp = p0 + pb * (C::P_PARTS * C::P_BYTES);
+        return true;
+      };
+      bool ok = issue_s(0) && issue_s(1);
+      for (int t = 0; ok; ++t) {
+        const int u = 2 * t + 1, slot = u % C::SLOTS, b = t & 1, pb = C::P_BUFS == 2 ? b : 0;
+        if (!(ok = wait(&pready[b], t >> 1) && wait(&full[slot], u / C::SLOTS))) break;
+        tc_fence_after();
+        const uint32_t v = kv0 + slot * C::SLOT, pp = p0 + pb * (C::P_PARTS * C::P_BYTES);
 #pragma unroll
-          for (int kk = 0; kk < KT / 16; ++kk)
-            // a 64-wide head fills both halves of the 128 dims: the second repeats the first and is not read
-            mma_f16_ss(lead, tmem + C::O_COL + (w.part & 1) * 2 * N, sdesc_rows<128>(v + kk * 2048, HD == 64 ? 0 : KT * 128),
-                       sdesc_rows<C::P_ROW>(pp + kk * 16 * C::P_ROW, C::P_PARTS == 2 ? C::P_BYTES : 16), idesc_o,
-                       (!o_new || kk > 0) ? 1u : 0u);
-          mma_commit_lead(lead, &empty[vslot]);
-          mma_commit_lead(lead, &pvdone[b]);
-          did = true;
-          ++o_at;
-          o_new = false;
-          if (--o_left == 0) {
-            mma_commit_lead(lead, &odone[w.part & 1]);
-            o_done = !w.next(p);
-            o_left = w.nt;
-            o_new = true;
-          }
+        for (int kk = 0; kk < KT / 16; ++kk)
+          // a 64-wide head fills both halves of the 128 dims: the second repeats the first and is not read
+          mma_f16_ss(lead, tmem + C::O_COL + (w.part & 1) * 2 * N, sdesc_rows<128>(v + kk * 2048, HD == 64 ? 0 : KT * 128),
+                     sdesc_rows<C::P_ROW>(pp + kk * 16 * C::P_ROW, C::P_PARTS == 2 ? C::P_BYTES : 16), idesc_o,
+                     (!o_new || kk > 0) ? 1u : 0u);
+        o_new = false;
+        mma_commit_lead(lead, &empty[slot]);
+        mma_commit_lead(lead, &pvdone[b]);
+        if (--o_left == 0) {
+          mma_commit_lead(lead, &odone[w.part & 1]);
+          if (!w.next(p)) break;
+          o_left = w.nt;
+          o_new = true;
         }
-        if (did) {
-          t0 = 0;
-        } else {
-          __nanosleep(20);
-          const unsigned long long now = globaltimer();
-          if (t0 == 0) t0 = now;
-          bool stop = *abort_flag != 0;
-          if (now - t0 > kWaitLimitNs) {
-            *abort_flag = 1;
-            record_error(err, ERR_ATTN_FULL);
-            stop = true;
-          }
-          ok = !__any_sync(0xffffffffu, stop);
-        }
+        ok = issue_s(t + 2);
       }
       mma_commit_lead(lead, mdone);
       mbar_wait_long(mdone, 0u, nullptr, err, ERR_ATTN_FULL);
