@@ -16,7 +16,7 @@ namespace {
 struct AttnPagedPlan {
   int N, row_tiles, whole, ctas, nz;
   long long items, tiles;     // tiles: of an item, at most
-  size_t o, ml, plan, lse, z, bytes;
+  size_t o, ml, plan, items_at, lse, z, bytes;
 };
 
 AttnPagedPlan plan_attn_paged(long long b, long long H_kv, long long rows, int hd, long long T, bool mass) {
@@ -26,7 +26,7 @@ AttnPagedPlan plan_attn_paged(long long b, long long H_kv, long long rows, int h
   a.items = b * H_kv * a.row_tiles;
   a.tiles = std::max(1LL, (T + kPagedKeys - 1) / kPagedKeys);
   a.ctas = (a.N <= 16 ? 2 : 1) * op_device_sms();
-  a.whole = a.tiles <= 2;
+  a.whole = a.tiles <= 4;
   a.nz = (int)std::min<long long>((rows + 3) / 4 * 4, a.N);
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -37,6 +37,7 @@ AttnPagedPlan plan_attn_paged(long long b, long long H_kv, long long rows, int h
   a.o = take(a.whole ? 0 : (size_t)2 * a.ctas * a.N * hd * 4);
   a.ml = take(a.whole ? 0 : (size_t)2 * a.ctas * a.N * 8);
   a.plan = take(a.whole ? 0 : (size_t)a.ctas * 16);
+  a.items_at = take(mass && !a.whole ? (size_t)a.items * 8 : 0);
   a.lse = take(mass ? (size_t)a.items * a.N * 4 : 0);
   a.z = take(mass ? (size_t)a.items * a.tiles * kPagedKeys * a.nz * 4 : 0);
   a.bytes = at;
@@ -53,13 +54,14 @@ cudaError_t launch_attn_paged(const CUtensorMap& tk, const CUtensorMap& tv, cons
   const unsigned grid = (unsigned)std::min<long long>(a.ctas, (units + p.min_share - 1) / p.min_share);
   e = op_launch(attn_paged_kernel<F, HD, N>, dim3(grid), dim3(C::THREADS), C::SMEM_BYTES, st, 1, tk, tv, p);
   if (e != cudaSuccess) return e;
-  if (!a.whole) {
-    e = op_launch(attn_paged_join_kernel<F, HD>, dim3(grid, (unsigned)std::min(N, p.rows)), dim3(128), 0, st, 1, p, N);
-    if (e != cudaSuccess) return e;
-  }
-  if (!p.mass) return cudaSuccess;
-  return op_launch(attn_paged_mass_kernel, dim3((unsigned)((long long)p.c.b * p.c.H_kv * p.by_chunks.d)), dim3(256), 0, st,
-                   1, p, N);
+  if (a.whole && !p.mass) return cudaSuccess;
+  AttnPagedParams f = p;
+  f.join_ctas = (int)grid;
+  f.joins = a.whole ? 0 : (int)grid * std::min(N, p.rows);
+  const long long chunks = p.mass ? (long long)p.c.b * p.c.H_kv * p.by_chunks.d : 0;
+  const dim3 rest((unsigned)(f.joins + chunks));
+  return p.mass ? op_launch(attn_paged_finish_kernel<F, HD, true>, rest, dim3(128), 0, st, 1, f, N)
+                : op_launch(attn_paged_finish_kernel<F, HD, false>, rest, dim3(128), 0, st, 1, f, N);
 }
 
 template <typename F, int HD>
@@ -141,13 +143,14 @@ extern "C" dllm_status dllm_op_attention_paged(const void* q, int64_t q_row_stri
   p.by_chunks = FastDiv((uint32_t)((p.c.positions + 255) / 256));
   p.nz = a.nz;
   p.z_tiles = (int)a.tiles;
-  if (mass && (double)cache->b * cache->H_kv * p.by_chunks.d > 0x7fffffff)
+  if (mass && (double)cache->b * cache->H_kv * p.by_chunks.d > 0x7fff0000)
     return op_fail(DLLM_EINVAL, "attention_paged: b=%d H_kv=%d of %lld positions are too many weights for one call", cache->b,
                    cache->H_kv, p.c.positions);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.ws_o = reinterpret_cast<float*>(ws + a.o);
   p.ws_ml = reinterpret_cast<float*>(ws + a.ml);
   p.ws_plan = reinterpret_cast<int4*>(ws + a.plan);
+  p.ws_items = reinterpret_cast<int2*>(ws + a.items_at);
   p.ws_lse = reinterpret_cast<float*>(ws + a.lse);
   p.ws_z = reinterpret_cast<float*>(ws + a.z);
   // bytes of a page's cached head: rows of hd * 2, in boxes of 128

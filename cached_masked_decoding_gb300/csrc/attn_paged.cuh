@@ -51,6 +51,8 @@ struct AttnPagedParams {
   int nz, z_tiles;            // scores kept for the weights: [item][z_tiles][128][nz]
   float *ws_o, *ws_ml, *ws_lse, *ws_z;   // [2 * CTAs][N][hd], [2 * CTAs][N][2], [item][N]
   int4* ws_plan;              // [CTA] the split item that starts there, its first and last slots; or -1
+  int2* ws_items;             // [item] (for the weights) first and last slots of a split item, or -1
+  int joins, join_ctas;       // of the second kernel: CTAs that join; CTAs of the first one
 };
 
 static __device__ int g_attn_paged_err[1];
@@ -492,26 +494,23 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
           if (C::P_BUFS == 1 && tt > 0) wait(&pvdone[(tt - 1) & 1], (tt - 1) >> 1);
           // With two buffers this one is free: S of this tile was issued behind the product of the tile before the
           // last, and its commit stands for everything issued before it.
-          uint32_t hi[RW / 2], lo[RW / 2];
-#pragma unroll
-          for (int j = 0; j < RW; j += 2) {
-            const float a = pow2_approx(z[j]), c = pow2_approx(z[j + 1]);
-            l_sum[j] += a;
-            l_sum[j + 1] += c;
-            hi[j >> 1] = F::pack(a, c);
-            const float2 h = F::unpack(hi[j >> 1]);
-            lo[j >> 1] = F::pack(a - h.x, c - h.y);
-          }
           uint8_t* pp = sP + pb * (C::P_PARTS * C::P_BYTES);
 #pragma unroll
           for (int j = 0; j < RW; j += 8) {
-            const uint4 h = make_uint4(hi[j / 2], hi[j / 2 + 1], hi[j / 2 + 2], hi[j / 2 + 3]);
-            const uint4 l = make_uint4(lo[j / 2], lo[j / 2 + 1], lo[j / 2 + 2], lo[j / 2 + 3]);
-            *reinterpret_cast<uint4*>(pp + swizzled<C::P_ROW>(key_l, (row0 + j) >> 3)) = h;
-            if constexpr (C::P_PARTS == 1)
-              *reinterpret_cast<uint4*>(pp + swizzled<C::P_ROW>(key_l, (N + row0 + j) >> 3)) = l;
-            else
-              *reinterpret_cast<uint4*>(pp + C::P_BYTES + swizzled<C::P_ROW>(key_l, (row0 + j) >> 3)) = l;
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float a = pow2_approx(z[j + 2 * e]), c = pow2_approx(z[j + 2 * e + 1]);
+              l_sum[j + 2 * e] += a;
+              l_sum[j + 2 * e + 1] += c;
+              hi[e] = F::pack(a, c);
+              const float2 h = F::unpack(hi[e]);
+              lo[e] = F::pack(a - h.x, c - h.y);
+            }
+            *reinterpret_cast<uint4*>(pp + swizzled<C::P_ROW>(key_l, (row0 + j) >> 3)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(pp + (C::P_PARTS == 1 ? swizzled<C::P_ROW>(key_l, (N + row0 + j) >> 3)
+                                                            : C::P_BYTES + swizzled<C::P_ROW>(key_l, (row0 + j) >> 3))) =
+                make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
           if (row0 == 0 && !__all_sync(0xffffffffu, seen)) {
             const int u = 2 * tt + 1, slot = u % C::SLOTS;
@@ -607,6 +606,8 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
           const int rest = paged_tiles(w.n) - w.nt, share = s_plan[4];
           plan = make_int4((int)item, slot, 2 * ((int)blockIdx.x + (rest + share - 1) / share), 0);
         }
+        if (p.mass && !p.whole && tid == 0 && w.t0 == 0)
+          p.ws_items[item] = complete ? make_int2(-1, -1) : make_int2(plan.y, plan.z);
         wait(&lready[b], w.part >> 1);
         if (tid < N) {
           const float* ls = s_sums + b * 4 * N + tid;
@@ -669,32 +670,85 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
   }
 }
 
-// Joins the parts of split items: weights l 2^m over their sum (l is 1 at least, 2^51 at most, and m the part's
-// reference: what a weight loses to underflow is nothing beside the largest).  A CTA of 4 warps, which share the parts, a
-// row of the item that goes on from one CTA of the kernel before to the next.
-template <typename F, int HD>
-__global__ void __launch_bounds__(128) attn_paged_join_kernel(const __grid_constant__ AttnPagedParams p, int N) {
-  __shared__ float s_o[4][HD], s_w[4];
-  const int r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// The slots of a split item's parts: the first CTA's, then every following one's first.
+__device__ __forceinline__ int paged_slot(int first, int k) { return k == 0 ? first : ((first >> 1) + k) * 2; }
+__device__ __forceinline__ int paged_parts(int first, int last) { return (last >> 1) - (first >> 1) + 1; }
+
+// The second kernel: joins split items, and adds what every key received.  The first p.joins CTAs, a row of the item that
+// goes on from one CTA of the kernel before to the next: weights l 2^m over their sum (l is 1 at least, 2^51 at most, and
+// m the part's reference: what a weight loses to underflow is nothing beside the largest); the CTA's 4 warps share the
+// parts.  The others, 256 keys of a cached head: the rows' probabilities from their scores (base 2) and log sums.
+template <typename F, int HD, bool MASS>
+__global__ void __launch_bounds__(128, 12) attn_paged_finish_kernel(const __grid_constant__ AttnPagedParams p, int N) {
+  __shared__ float s_o[4][HD], s_w[4], s_lse[64];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_launch_dependents();
   griddep_wait();
-  const int4 at = p.ws_plan[blockIdx.x];
-  if (at.x < 0) return;
-  const long long item = at.x;
-  const int2 plan = make_int2(at.y, at.z);
-  const int s = at.x / p.per_seq;
+  if (MASS && (int)blockIdx.x >= p.joins) {
+    uint32_t chunk;
+    const int plane = (int)p.by_chunks.divmod(blockIdx.x - (uint32_t)p.joins, chunk), s = plane / p.c.H_kv, g = plane % p.c.H_kv;
+    const int n = (int)min((long long)p.c.len(p.lens, s), p.mass_rs), first = (int)(chunk * 256);
+    if (first >= n) return;
+    const long long item0 = (long long)s * p.per_seq + g;   // the head's first row tile; then H_kv apart
+    float sum[2] = {};
+    for (int rt = 0; rt < p.row_tiles; ++rt) {
+      const long long item = item0 + (long long)rt * p.c.H_kv;
+      const int n_rows = min(N, p.rows - rt * N);
+      __syncthreads();
+      if ((int)threadIdx.x < n_rows) {
+        const int r = threadIdx.x;
+        const int2 plan = p.whole ? make_int2(-1, -1) : p.ws_items[item];
+        float lse;
+        if (plan.x < 0) {
+          lse = p.ws_lse[item * N + r];
+        } else {
+          float M = -INFINITY, l = 0.0f;
+          for (int k = 0; k < paged_parts(plan.x, plan.y); ++k) {
+            const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + ((long long)paged_slot(plan.x, k) * N + r) * 2);
+            if (ml.y == 0.0f) continue;
+            const float top = fmaxf(M, ml.x);
+            l = l * exp2f(M - top) + ml.y * exp2f(ml.x - top);
+            M = top;
+          }
+          lse = l == 0.0f ? INFINITY : M + log2f(l);
+        }
+        s_lse[r] = lse;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int t = first + h * 128 + (int)threadIdx.x;
+        if (t >= n) continue;
+        const float* z = p.ws_z + ((item * p.z_tiles + t / kPagedKeys) * kPagedKeys + t % kPagedKeys) * p.nz;
+        for (int r = 0; r < n_rows; r += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(z + r);
+          sum[h] += pow2_approx(v.x - s_lse[r]);
+          if (r + 1 < n_rows) sum[h] += pow2_approx(v.y - s_lse[r + 1]);
+          if (r + 2 < n_rows) sum[h] += pow2_approx(v.z - s_lse[r + 2]);
+          if (r + 3 < n_rows) sum[h] += pow2_approx(v.w - s_lse[r + 3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = first + h * 128 + (int)threadIdx.x;
+      if (t < n) p.mass[plane * p.mass_rs + t] += sum[h];
+    }
+    return;
+  }
+
+  const int r = (int)blockIdx.x / p.join_ctas, cta = (int)blockIdx.x - r * p.join_ctas;
+  const int4 plan = p.ws_plan[cta];
+  if (plan.x < 0) return;
+  const int s = plan.x / p.per_seq;
   uint32_t g, j;
-  const uint32_t rt = p.by_heads.divmod((uint32_t)(at.x - s * p.per_seq), g);
+  const uint32_t rt = p.by_heads.divmod((uint32_t)(plan.x - s * p.per_seq), g);
   if ((int)rt * N + r >= p.rows) return;
   const uint32_t i = p.by_group.divmod(rt * (uint32_t)N + (uint32_t)r, j);
-  typename F::E::T* out = reinterpret_cast<typename F::E::T*>(p.out) + ((long long)s * p.R + i) * p.o_rs +
-                          (long long)((int)g * p.group + (int)j) * HD + threadIdx.x;
-  // slots: the first CTA's, then every following one's first
-  const int parts = (plan.y >> 1) - (plan.x >> 1) + 1;
-  auto slot_of = [&](int k) { return k == 0 ? plan.x : ((plan.x >> 1) + k) * 2; };
+  const int parts = paged_parts(plan.y, plan.z);
   float M = -INFINITY;
   for (int k = lane; k < parts; k += 32) {
-    const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + ((long long)slot_of(k) * N + r) * 2);
+    const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + ((long long)paged_slot(plan.y, k) * N + r) * 2);
     if (ml.y != 0.0f) M = fmaxf(M, ml.x);
   }
 #pragma unroll
@@ -707,7 +761,7 @@ __global__ void __launch_bounds__(128) attn_paged_join_kernel(const __grid_const
     float v[4][D];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const long long at = (long long)slot_of(min(k0 + 4 * e, parts - 1)) * N + r;
+      const long long at = (long long)paged_slot(plan.y, min(k0 + 4 * e, parts - 1)) * N + r;
       ml[e] = *reinterpret_cast<const float2*>(p.ws_ml + at * 2);
       const float* src = p.ws_o + at * HD + lane * D;
       if constexpr (D == 4) {
@@ -735,41 +789,12 @@ __global__ void __launch_bounds__(128) attn_paged_join_kernel(const __grid_const
   for (int d = 0; d < D; ++d) s_o[warp][lane * D + d] = o[d];
   if (lane == 0) s_w[warp] = sum;
   __syncthreads();
-  sum = (s_w[0] + s_w[1]) + (s_w[2] + s_w[3]);
-  if (threadIdx.x == 0 && p.mass) p.ws_lse[item * N + r] = sum == 0.0f ? INFINITY : M + log2f(sum);
   if (threadIdx.x >= HD) return;
+  sum = (s_w[0] + s_w[1]) + (s_w[2] + s_w[3]);
   const float v = (s_o[0][threadIdx.x] + s_o[1][threadIdx.x]) + (s_o[2][threadIdx.x] + s_o[3][threadIdx.x]);
-  F::E::put(out, sum == 0.0f ? 0.0f : v / sum);
-}
-
-// Adds what every key received: the rows' probabilities from their scores (base 2) and log sums.  A thread a key.
-static __global__ void __launch_bounds__(256) attn_paged_mass_kernel(const __grid_constant__ AttnPagedParams p, int N) {
-  __shared__ float s_lse[64];
-  griddep_launch_dependents();
-  griddep_wait();
-  uint32_t chunk;
-  const int plane = (int)p.by_chunks.divmod(blockIdx.x, chunk), s = plane / p.c.H_kv, g = plane % p.c.H_kv;
-  const int n = (int)min((long long)p.c.len(p.lens, s), p.mass_rs);
-  const int t = (int)(chunk * 256 + threadIdx.x);
-  if ((int)(chunk * 256) >= n) return;
-  const long long item0 = (long long)s * p.per_seq + g;   // the head's first row tile; then H_kv apart
-  float sum = 0.0f;
-  for (int rt = 0; rt < p.row_tiles; ++rt) {
-    const int n_rows = min(N, p.rows - rt * N);
-    __syncthreads();
-    if ((int)threadIdx.x < N) s_lse[threadIdx.x] = p.ws_lse[(item0 + (long long)rt * p.c.H_kv) * N + threadIdx.x];
-    __syncthreads();
-    if (t >= n) continue;
-    const float* z = p.ws_z + (((item0 + (long long)rt * p.c.H_kv) * p.z_tiles + t / kPagedKeys) * kPagedKeys + t % kPagedKeys) * p.nz;
-    for (int r = 0; r < n_rows; r += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(z + r);
-      sum += pow2_approx(v.x - s_lse[r]);
-      if (r + 1 < n_rows) sum += pow2_approx(v.y - s_lse[r + 1]);
-      if (r + 2 < n_rows) sum += pow2_approx(v.z - s_lse[r + 2]);
-      if (r + 3 < n_rows) sum += pow2_approx(v.w - s_lse[r + 3]);
-    }
-  }
-  if (t < n) p.mass[plane * p.mass_rs + t] += sum;
+  F::E::put(reinterpret_cast<typename F::E::T*>(p.out) + ((long long)s * p.R + i) * p.o_rs +
+                (long long)((int)g * p.group + (int)j) * HD + threadIdx.x,
+            sum == 0.0f ? 0.0f : v / sum);
 }
 
 }  // namespace dllm
