@@ -26,6 +26,8 @@ AttnPagedPlan plan_attn_paged(long long b, long long H_kv, long long rows, int h
   a.items = b * H_kv * a.row_tiles;
   a.tiles = std::max(1LL, (T + kPagedKeys - 1) / kPagedKeys);
   a.ctas = (a.N <= 16 ? 2 : 1) * op_device_sms();
+  // Few keys: items as they are, one kernel (32 rows of 32 heads, 512 keys: 11.0 us against 12.1 in shared runs; 768
+  // keys: 14.3 against 12.7).
   a.whole = a.tiles <= 4;
   a.nz = (int)std::min<long long>((rows + 3) / 4 * 4, a.N);
   size_t at = 0;
@@ -87,7 +89,7 @@ extern "C" dllm_status dllm_op_attention_paged_workspace(int32_t b, int32_t H, i
   if ((__int128)b * R * H > 0x7fffffff)
     return op_fail(DLLM_EINVAL, "attention_paged: b=%d R=%d H=%d are too many rows", b, R, H);
   const AttnPagedPlan a = plan_attn_paged(b, H_kv, (long long)R * (H / H_kv), hd, T, with_mass != 0);
-  if (a.items > 0x7fffffff || (double)a.items * (double)a.tiles > 1e11)
+  if (a.items > 0x7fffffff || (double)a.items * (double)a.tiles > 1e11 || (double)b * a.tiles > 2e9)
     return op_fail(DLLM_EINVAL, "attention_paged: b=%d R=%d H=%d T=%d are too many keys for one call", b, R, H, T);
   *bytes = (int64_t)a.bytes;
   return DLLM_OK;
@@ -137,7 +139,7 @@ extern "C" dllm_status dllm_op_attention_paged(const void* q, int64_t q_row_stri
   p.row_tiles = a.row_tiles;
   p.per_seq = cache->H_kv * a.row_tiles;
   p.whole = a.whole;
-  p.min_share = a.whole ? 1 : 2;
+  p.min_share = a.whole ? 1 : 2;   // (an item's start and a tile; 3: 13.6 us for 12.7, 32 rows of 32 heads, 768 keys)
   p.by_group = FastDiv((uint32_t)p.group);
   p.by_heads = FastDiv((uint32_t)cache->H_kv);
   p.by_chunks = FastDiv((uint32_t)((p.c.positions + 255) / 256));

@@ -97,14 +97,14 @@ struct AttnPagedCfg {
   static constexpr int P_BUFS = N == 16 && HD == 128 ? 1 : 2;
   // places (64 bits), warp maxima (4), m (2 buffers), rise, sums of the warps (4, 2 buffers), their inverse
   static constexpr int STAT_FLOATS = 2 * N + 4 * N + 2 * N + N + 8 * N + N;
-  static constexpr int FIXED = 1024 + Q_BYTES + P_BUFS * P_PARTS * P_BYTES + STAT_FLOATS * 4 + 384;
+  static constexpr int FIXED = 1024 + Q_BYTES + P_BUFS * P_PARTS * P_BYTES + STAT_FLOATS * 4 + 448;
   static constexpr int MOST = (228 * 1024 / CTAS - 1024 - FIXED) / SLOT;
   static constexpr int SLOTS = MOST > 12 ? 12 : MOST;
   static constexpr int SMEM_BYTES = FIXED + SLOTS * SLOT;
   static constexpr int S_COL = 0;                       // two buffers of NP
   static constexpr int O_COL = 2 * NP;                  // two buffers of 2 N, the products of hi and of lo
   static constexpr int TMEM_COLS = N == 8 ? 64 : N == 16 ? 128 : N == 32 ? 256 : 512;
-  static_assert(SLOTS >= 3 && SMEM_BYTES <= 232448 && 2 * NP + 4 * N <= TMEM_COLS && CTAS * TMEM_COLS <= 512 && (2 * SLOTS + 17) * 8 + 28 <= 384, "shared and tensor memory");
+  static_assert(SLOTS >= 3 && SMEM_BYTES <= 232448 && 2 * NP + 4 * N <= TMEM_COLS && CTAS * TMEM_COLS <= 512 && (2 * SLOTS + 17) * 8 + 28 + THREADS / 8 <= 448, "shared and tensor memory");
 };
 
 // 2^x; results below the normal range are 0
@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
   int* s_plan = reinterpret_cast<int*>(mdone + 1);      // first sequence, item, unit; how many units; a CTA's share
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_plan + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* s_units = reinterpret_cast<int*>(tmem_slot + 2); // [warps]
   int* err = g_attn_paged_err;
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -234,17 +235,33 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
     for (int e = threadIdx.x; e < C::Q_BYTES / 16; e += C::THREADS) reinterpret_cast<uint4*>(sQ)[e] = make_uint4(0, 0, 0, 0);
   }
   griddep_wait();
-  // this CTA's run of units
+  // This CTA's run of units: every warp adds up a segment of the sequences, then the first finds the run's start in the
+  // segment that holds it.
+  constexpr int WARPS = C::THREADS / 32;
+  const int segment = (p.c.b + WARPS * 32 - 1) / (WARPS * 32) * 32;
+  {
+    int sum = 0;
+    const int end = min((warp + 1) * segment, p.c.b);
+#pragma unroll 4
+    for (int s = warp * segment + lane; s < end; s += 32) sum += paged_units(p, p.c.len(p.lens, s));
+    // (of a segment's sums the low 32 bits: segments of more units than that are refused)
+    sum = (int)__reduce_add_sync(0xffffffffu, (uint32_t)sum);
+    if (lane == 0) s_units[warp] = sum;
+  }
+  __syncthreads();
   if (warp == 0) {
-    long long sum = 0;
-    for (int s0 = 0; s0 < p.c.b; s0 += 32)
-      sum += __reduce_add_sync(0xffffffffu, s0 + lane < p.c.b ? paged_units(p, p.c.len(p.lens, s0 + lane)) : 0);
-    const long long units = sum * p.per_seq;
+    long long units = 0;
+    for (int w = 0; w < WARPS; ++w) units += s_units[w];
+    units *= p.per_seq;
     const long long share = max((units + gridDim.x - 1) / gridDim.x, (long long)p.min_share);
     const long long first = min(units, share * blockIdx.x), last = min(units, first + share);
     long long base = 0;
-    int s_at = 0, item = 0, u0 = 0;
-    for (int s0 = 0; s0 < p.c.b && first < last; s0 += 32) {
+    int s0 = 0, s_at = 0, item = 0, u0 = 0;
+    while (s0 + segment < p.c.b && base + (long long)s_units[s0 / segment] * p.per_seq <= first) {
+      base += (long long)s_units[s0 / segment] * p.per_seq;
+      s0 += segment;
+    }
+    for (; s0 < p.c.b && first < last; s0 += 32) {
       const int t = s0 + lane < p.c.b ? paged_units(p, p.c.len(p.lens, s0 + lane)) : 0;
       int upto = t;
 #pragma unroll
@@ -657,9 +674,9 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
   if (!p.whole)
     for (int s = blockIdx.x; s < p.c.b; s += gridDim.x)
       if (p.c.len(p.lens, s) == 0)
-        for (int e = threadIdx.x; e < p.R * p.H * (HD / 8); e += C::THREADS)
-          *reinterpret_cast<uint4*>(p.out + ((long long)s * p.R + e / (p.H * (HD / 8))) * p.o_rs +
-                                    (long long)(e % (p.H * (HD / 8))) * 8) = make_uint4(0, 0, 0, 0);
+        for (int r = 0; r < p.R; ++r)
+          for (int e = threadIdx.x; e < p.H * (HD / 8); e += C::THREADS)
+            reinterpret_cast<uint4*>(p.out + ((long long)s * p.R + r) * p.o_rs)[e] = make_uint4(0, 0, 0, 0);
   // lanes that skipped their role arrive here first: reconverge before the CTA-wide barrier
   __syncwarp();
   tc_fence_before();

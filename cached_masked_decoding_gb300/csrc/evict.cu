@@ -257,6 +257,8 @@ extern "C" dllm_status dllm_op_kv_paged_evict(const dllm_kv_paged* src, const dl
   if (const dllm_status s = kv_paged_check(dst, "kv_paged_evict"); s != DLLM_OK) return s;
   if (src->b != dst->b || src->H_kv != dst->H_kv || src->hd != dst->hd || src->dtype != dst->dtype)
     return op_fail(DLLM_EINVAL, "kv_paged_evict: the caches differ in b, H_kv, hd or dtype");
+  if (src->k == dst->k && src->table == dst->table)
+    return op_fail(DLLM_EINVAL, "kv_paged_evict: dst is src: the kept rows go to pages of their own");
   EvictParams p = {};
   p.src = PagedKv(*src);
   p.dst = PagedKv(*dst);

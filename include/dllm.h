@@ -636,7 +636,8 @@ typedef struct dllm_kv_paged {
  * q_weight, k_weight: [hd] of dtype, NULL: ones; eps >= 0; eps < 0: no norm
  * (both weights NULL).  rope: NULL: nothing turns (positions may be NULL);
  * rot_dim a multiple of 16.  positions: device int32 [rows].  An output may be
- * its input with the same strides and type. */
+ * its input with the same strides and type.  Squares are float32: elements
+ * stay within 2^60. */
 dllm_status dllm_op_qk_norm_rope(const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride, void* q_out,
                                  int64_t q_out_row_stride, void* k_out, int64_t k_out_row_stride,
                                  const int32_t* positions, int32_t rows, int32_t H, int32_t H_kv, int32_t hd,
@@ -672,11 +673,11 @@ dllm_status dllm_op_qk_norm_rope_paged(const dllm_kv_paged* cache, const void* q
  * multiple of 8).  scale: > 0, finite.  Scores, statistics and sums are float32; a probability
  * enters the value product as the sum of two halves of the cache's type (16
  * bits of it in bf16).  K, V and q are finite, and so are the scores.
- *   mass (nullable): device float32 [b][H_kv][mass_stride], mass_stride at
- * least max_pages * page_size or the largest of lens;
- * mass[s][g][t] += the sum of p_t over the R rows and the heads of g, for
- * t < lens[s]; the rest stays as it was.  In a fixed order: the same inputs
- * give the same bits.
+ *   mass (nullable): device float32 [b][H_kv][mass_stride] (0: max_pages *
+ * page_size); mass[s][g][t] += the sum of p_t over the R rows and the heads of
+ * g, for t < lens[s]; the rest stays as it was, and weights of positions from
+ * mass_stride on are not kept.  In a fixed order: the same inputs give the same
+ * bits.
  *   workspace: device memory, 16-byte aligned, of at least
  * dllm_op_attention_paged_workspace bytes for the same shape on the current
  * device (T = max_pages * page_size, with_mass: whether mass is given; 0: may
@@ -698,10 +699,11 @@ dllm_status dllm_op_attention_paged_workspace(int32_t b, int32_t H, int32_t H_kv
  * dtype, page sizes of their own; dst's pages are not among src's (they may lie
  * in the same pool), and its table holds at least keep positions.
  *   lens: device int32 [b]; NULL, or more than src's table holds: all it holds.
- *   mass: device float32 [b][H_kv][mass_stride], mass_stride >= the largest of lens.
+ *   mass: device float32 [b][H_kv][mass_stride] (0: max_pages * page_size of
+ *   src); n is at most mass_stride.
  *   kept: device int32 [b][H_kv][keep], the positions kept, ascending, -1 from m on.
  *   new_lens: device int32 [b], m.
- *   mass_out (nullable): device float32 [b][H_kv][mass_out_stride],
+ *   mass_out (nullable): device float32 [b][H_kv][mass_out_stride] (0: keep),
  *   mass_out_stride >= keep: the weights of the kept, its other elements stay as they were.
  * A kept position that lies on no page gives a row of zeros.
  * keep >= 1, sinks, recent >= 0, sinks + recent <= keep. */

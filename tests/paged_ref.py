@@ -72,7 +72,7 @@ def logprobs(z, scale, target, top):
     all but the largest)."""
     z = z.astype(np.float64)
     nan = math.nan
-    order = sorted((i for i in range(len(z)) if not math.isnan(z[i])), key=lambda i: (-z[i], i)) if top else []
+    order = [int(i) for i in np.argsort(-z, kind="stable")[:top] if not math.isnan(z[i])]   # (NaN sorts last)
     ids = (order + [-1] * top)[:top]
     m = np.nanmax(z) if not np.isnan(z).all() else nan
     if np.isnan(z).any() or not math.isfinite(m):

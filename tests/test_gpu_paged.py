@@ -274,11 +274,15 @@ SHAPES = [
     (1, 1, 64, 1, 128, 16, [3000], "bf16"),
     (5, 2, 12, 4, 64, 16, [2049, 1, 0, -3, 900], "bf16"),
     (1, 1, 4, 4, 128, 16, [4100], "bf16"),
+    (1, 1, 8, 1, 64, 256, [30000], "bf16"),              # a part in every CTA
+    (1, 5, 3, 1, 128, 64, [2500], "f16"),
+    (70, 1, 2, 2, 64, 16, [(7 * i * i) % 650 - 20 for i in range(70)], "bf16"),
+    (45, 1, 4, 2, 64, 32, [(11 * i) % 420 for i in range(45)], "f16"),
 ]
 
 
 @pytest.mark.parametrize("with_mass", [False, True])
-@pytest.mark.parametrize("b,R,H,Hkv,hd,ps,lens,dtype", SHAPES)
+@pytest.mark.parametrize("b,R,H,Hkv,hd,ps,lens,dtype", SHAPES, ids=lambda v: str(v)[:24])
 def test_attention_paged(torch, b, R, H, Hkv, hd, ps, lens, dtype, with_mass):
     rng = np.random.default_rng(b * 100 + R + H + lens[0])
     most = -(-max(lens) // ps) + 1
@@ -404,6 +408,51 @@ def test_attention_in_a_large_pool(torch):
                                   starts_ptr=st.data_ptr(), eps=-1.0)
     assert torch.equal(c.k[pages - 1, :, 254:].transpose(0, 1).reshape(2, -1), x[:2])
     assert torch.equal(c.v[pages - 3, :, :2].transpose(0, 1).reshape(2, -1), x[2:])
+
+
+def test_attention_refuses_a_small_workspace(torch):
+    rng = np.random.default_rng(2)
+    c = Pages(torch, rng, 1, 2, 64, "bf16", 16, 64).fill(rng, [1000])
+    q = torch.zeros(1, 1, 4, 64, device="cuda", dtype=torch.bfloat16)
+    need = binding.attention_paged_workspace(1, 4, 2, 64, 1, 1024)
+    assert 0 < need < binding.attention_paged_workspace(1, 4, 2, 64, 1, 1024, mass=True)
+    ws = torch.empty(need + 16, device="cuda", dtype=torch.uint8)
+    for args in [dict(), dict(ws_ptr=ws.data_ptr(), ws_bytes=need - 1), dict(ws_ptr=ws.data_ptr() + 8, ws_bytes=need)]:
+        with pytest.raises(binding.DllmError) as e:
+            binding.op_attention_paged(q.data_ptr(), c.struct(), q.data_ptr(), 4, 1, **args)
+        assert e.value.status == binding.EINVAL and "workspace" in str(e.value)
+
+
+def test_attention_on_two_streams_at_once(torch):
+    """Calls that run at the same time, each with a workspace of its own: the bits of calls one after the other."""
+    rng = np.random.default_rng(14)
+    lens = [3000, 1234, 0, 4000]
+    cs = [Pages(torch, rng, 4, 2, 128, "bf16", 32, 126).fill(rng, lens) for _ in range(2)]
+    q = dev(torch, rng.standard_normal((4, 2, 8, 128)).astype(np.float32)).to(torch.bfloat16)
+    ln = dev(torch, np.array(lens, dtype=np.int32))
+    ws = [torch.empty(binding.attention_paged_workspace(4, 8, 2, 128, 2, 4032, mass=True), device="cuda",
+                      dtype=torch.uint8) for _ in range(2)]
+    want, want_m = [], []
+    for c in cs:
+        m = torch.zeros(4, 2, 4032, device="cuda")
+        want.append(attend(torch, c, q, lens, mass=m))
+        want_m.append(m)
+    structs = [c.struct() for c in cs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.empty_like(q) for _ in range(2)]
+    ms = [torch.zeros(4, 2, 4032, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                ms[i].zero_()
+                binding.op_attention_paged(q.data_ptr(), structs[i], outs[i].data_ptr(), 8, 2, lens_ptr=ln.data_ptr(),
+                                           mass_ptr=ms[i].data_ptr(), ws_ptr=ws[i].data_ptr(), ws_bytes=ws[i].numel(),
+                                           stream=streams[i].cuda_stream)
+    torch.cuda.synchronize()
+    binding.op_check()
+    for i in range(2):
+        assert torch.equal(outs[i], want[i]) and torch.equal(ms[i], want_m[i])
 
 
 # --------------------------------------------------------------------------- eviction
@@ -553,7 +602,8 @@ def logprobs_check(x, targets, top, scale, got):
 
 LOGITS = [(1, 1, 1, "f32", 1.0, 0), (3, 2, 2, "bf16", 2.0, 1), (5, 100, 64, "f16", 1.0, 3), (4, 1000, 5, "bf16", 0.7, 0),
           (2, 4096, 20, "f32", 1.3, 0), (3, 32001, 20, "f32", 1 / 0.7, 3), (2, 126464, 50, "bf16", 1.0, 0),
-          (33, 5003, 0, "f16", 1.0, 1), (2, 300007, 64, "bf16", 1.0, 5), (700, 1023, 3, "bf16", 1.0, 2),
+          (33, 5003, 0, "f16", 1.0, 1), (2, 300007, 64, "bf16", 1.0, 5), (310, 9001, 7, "bf16", 1.0, 1),
+          (40, 40000, 5, "f16", 1.0, 0), (153, 65003, 30, "f32", 1.0, 1), (90, 70001, 64, "bf16", 0.5, 1), (700, 1023, 3, "bf16", 1.0, 2),
           (400, 6001, 64, "f32", 1.0, 1)]
 
 
@@ -728,3 +778,42 @@ def test_two_graphs_on_two_streams(torch):
         _layer_check(torch, st)
         for k, v in want.items():
             assert torch.equal(st[k], v), k
+
+
+FIRST_CALLS = """
+import sys
+sys.path[:0] = ["tests", "."]
+import torch
+import test_gpu_paged as t
+from cached_masked_decoding_gb300 import binding
+binding.lib()
+st, go = t._layer(torch, 7)
+s = torch.cuda.Stream()
+torch.matmul(st["out"][0].float().view(2, -1), st["head"], out=st["logits"])   # (the matrix product's own set-up)
+torch.cuda.synchronize()
+with torch.cuda.stream(s):
+    torch.matmul(st["out"][0].float().view(2, -1), st["head"], out=st["logits"])
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g, stream=s):
+    go(s.cuda_stream)
+g.replay()
+torch.cuda.synchronize()
+keep = ("out", "mass", "kept", "lp", "en")
+got = {k: st[k].clone() for k in keep}
+t._layer_check(torch, st)
+go(torch.cuda.current_stream().cuda_stream)
+torch.cuda.synchronize()
+binding.op_check()
+print("same" if all(torch.equal(st[k], got[k]) for k in keep) else "not the same")
+"""
+
+
+def test_first_calls_of_a_process_can_be_captured(torch):
+    """Every kernel's first launch inside a capture, in a process of its own: the same bits as launched directly."""
+    import subprocess
+    import sys
+    from pathlib import Path
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=Path(__file__).resolve().parent.parent,
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stdout[-500:] + r.stderr[-2000:]

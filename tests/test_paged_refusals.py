@@ -42,8 +42,8 @@ def test_bad_caches_are_refused_everywhere(bad):
     c = cache(**bad)
     refused(binding.op_attention_paged, A, c, A, 8, 1, ws_ptr=A, ws_bytes=1 << 40)
     refused(binding.op_qk_norm_rope_paged, c, A, A, A, B, 8, 1, "bf16")
-    refused(binding.op_kv_paged_evict, c, cache(), A, 4, A, A)
-    refused(binding.op_kv_paged_evict, cache(), c, A, 4, A, A)
+    refused(binding.op_kv_paged_evict, c, cache(table=B), A, 4, A, A)
+    refused(binding.op_kv_paged_evict, cache(table=B), c, A, 4, A, A)
 
 
 def test_null_caches_are_refused():
@@ -114,7 +114,7 @@ EVICT_BAD = [dict(mass=0), dict(kept=0), dict(lens_out=0), dict(keep=0), dict(ke
 def test_evict_refuses(bad):
     a = dict(mass=A, keep=4, kept=A, lens_out=A, lens=0, sinks=1, recent=1, ms=0, mo=0, mos=0)
     a.update(bad)
-    refused(binding.op_kv_paged_evict, cache(), cache(), a["mass"], a["keep"], a["kept"], a["lens_out"],
+    refused(binding.op_kv_paged_evict, cache(), cache(table=B), a["mass"], a["keep"], a["kept"], a["lens_out"],
             lens_ptr=a["lens"], sinks=a["sinks"], recent=a["recent"], mass_stride=a["ms"], mass_out_ptr=a["mo"],
             mass_out_stride=a["mos"])
 
@@ -146,3 +146,7 @@ def test_loads_are_coherent(path):
     """These kernels are resident while the one before writes what they read."""
     code = re.sub(r"//[^\n]*|/\*.*?\*/", "", path.read_text(), flags=re.S)
     assert not re.search(r"__ldg|ld\.global(\.\w+)*\.nc|__restrict__", code)
+
+
+def test_evict_refuses_its_own_pages():
+    refused(binding.op_kv_paged_evict, cache(), cache(), A, 4, A, A, text="dst is src")
