@@ -29,7 +29,7 @@ AttnPagedPlan plan_attn_paged(long long b, long long H_kv, long long rows, int h
   // Few keys: items as they are, one kernel (32 rows of 32 heads, 512 keys: 11.0 us against 12.1 in shared runs; 768
   // keys: 14.3 against 12.7).
   a.whole = a.tiles <= 4;
-  a.nz = (int)std::min<long long>((rows + 3) / 4 * 4, a.N);
+  a.nz = rows <= 4 ? 4 : a.N;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t from = at;
@@ -59,11 +59,14 @@ cudaError_t launch_attn_paged(const CUtensorMap& tk, const CUtensorMap& tv, cons
   if (a.whole && !p.mass) return cudaSuccess;
   AttnPagedParams f = p;
   f.join_ctas = (int)grid;
-  f.joins = a.whole ? 0 : (int)grid * std::min(N, p.rows);
+  f.joins = a.whole ? 0 : (int)grid * (N > 8 ? (std::min(N, p.rows) + 3) / 4 : p.rows);
   const long long chunks = p.mass ? (long long)p.c.b * p.c.H_kv * p.by_chunks.d : 0;
   const dim3 rest((unsigned)(f.joins + chunks));
-  return p.mass ? op_launch(attn_paged_finish_kernel<F, HD, true>, rest, dim3(128), 0, st, 1, f, N)
-                : op_launch(attn_paged_finish_kernel<F, HD, false>, rest, dim3(128), 0, st, 1, f, N);
+  // (the same split of L1 and shared memory as the first kernel's: an SM need not drain to change it)
+  const auto finish = p.mass ? attn_paged_finish_kernel<F, HD, true> : attn_paged_finish_kernel<F, HD, false>;
+  e = op_smem_once(reinterpret_cast<const void*>(finish), 0);
+  if (e != cudaSuccess) return e;
+  return op_launch(finish, rest, dim3(128), 0, st, 1, f, N);
 }
 
 template <typename F, int HD>
@@ -142,8 +145,12 @@ extern "C" dllm_status dllm_op_attention_paged(const void* q, int64_t q_row_stri
   p.min_share = a.whole ? 1 : 2;   // (an item's start and a tile; 3: 13.6 us for 12.7, 32 rows of 32 heads, 768 keys)
   p.by_group = FastDiv((uint32_t)p.group);
   p.by_heads = FastDiv((uint32_t)cache->H_kv);
-  p.by_chunks = FastDiv((uint32_t)((p.c.positions + 255) / 256));
   p.nz = a.nz;
+  p.chunk_keys = a.nz <= 8 ? 256 : 2048 / a.nz;
+// (runs that leave every SM 16 CTAs: their rows' log sums are worked out once a run)
+  const long long chunks = (p.c.positions + p.chunk_keys - 1) / p.chunk_keys;
+  p.chunk_run = (int)std::max(1LL, std::min(32LL, cache->b * (long long)cache->H_kv * chunks / (16LL * op_device_sms())));
+  p.by_chunks = FastDiv((uint32_t)((chunks + p.chunk_run - 1) / p.chunk_run));
   p.z_tiles = (int)a.tiles;
   if (mass && (double)cache->b * cache->H_kv * p.by_chunks.d > 0x7fff0000)
     return op_fail(DLLM_EINVAL, "attention_paged: b=%d H_kv=%d of %lld positions are too many weights for one call", cache->b,

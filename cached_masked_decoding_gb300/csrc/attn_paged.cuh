@@ -46,7 +46,8 @@ struct AttnPagedParams {
   int min_share, whole;       // units a CTA takes at least; whole: items are not split
   FastDiv by_group, by_heads; // by_heads: by H_kv.  An item of a sequence: row tile * H_kv + cached head, so that the
                               // row tiles of a head's keys run on different SMs at about the same time
-  FastDiv by_chunks;          // by the 256-key chunks of a table
+  int chunk_keys, chunk_run;  // of the second kernel's CTAs that add up weights: keys at once, and how many times
+  FastDiv by_chunks;          // by a table's such CTAs
   float scale_log2;
   int nz, z_tiles;            // scores kept for the weights: [item][z_tiles][128][nz]
   float *ws_o, *ws_ml, *ws_lse, *ws_z;   // [2 * CTAs][N][hd], [2 * CTAs][N][2], [item][N]
@@ -691,127 +692,183 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
 __device__ __forceinline__ int paged_slot(int first, int k) { return k == 0 ? first : ((first >> 1) + k) * 2; }
 __device__ __forceinline__ int paged_parts(int first, int last) { return (last >> 1) - (first >> 1) + 1; }
 
-// The second kernel: joins split items, and adds what every key received.  The first p.joins CTAs, a row of the item that
-// goes on from one CTA of the kernel before to the next: weights l 2^m over their sum (l is 1 at least, 2^51 at most, and
-// m the part's reference: what a weight loses to underflow is nothing beside the largest); the CTA's 4 warps share the
-// parts.  The others, 256 keys of a cached head: the rows' probabilities from their scores (base 2) and log sums.
+// The second kernel: joins split items, and adds what every key received.  The first p.joins CTAs, rows of the item
+// that goes on from one CTA of the kernel before to the next: weights l 2^m over their sum (l is 1 at least, 2^51 at most,
+// and m the part's reference: what a weight loses to underflow is nothing beside the largest).  The others, runs
+// of keys of a cached head: the rows' probabilities from their scores (base 2) and log sums.
 template <typename F, int HD, bool MASS>
-__global__ void __launch_bounds__(128, 12) attn_paged_finish_kernel(const __grid_constant__ AttnPagedParams p, int N) {
-  __shared__ float s_o[4][HD], s_w[4], s_lse[64];
+__global__ void __launch_bounds__(128, MASS ? 8 : 12) attn_paged_finish_kernel(const __grid_constant__ AttnPagedParams p, int N) {
+  __shared__ float s_o[4][HD], s_w[4];
+  __shared__ __align__(16) float s_lse[64];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   griddep_launch_dependents();
   griddep_wait();
   if (MASS && (int)blockIdx.x >= p.joins) {
     uint32_t chunk;
     const int plane = (int)p.by_chunks.divmod(blockIdx.x - (uint32_t)p.joins, chunk), s = plane / p.c.H_kv, g = plane % p.c.H_kv;
-    const int n = (int)min((long long)p.c.len(p.lens, s), p.mass_rs), first = (int)(chunk * 256);
+    const int n = (int)min((long long)p.c.len(p.lens, s), p.mass_rs), step = p.chunk_keys;
+    const int first = (int)chunk * step * p.chunk_run, end = first + min(n - first, step * p.chunk_run);
     if (first >= n) return;
     const long long item0 = (long long)s * p.per_seq + g;   // the head's first row tile; then H_kv apart
-    float sum[2] = {};
+    // a key's scores are nq lanes' 16 bytes; a warp's keys are up to four accesses, all on their way at once
+    const int nq = p.nz / 4, q = lane & (nq - 1), keys = 32 / nq, mine = step / 4, k0 = warp * mine + lane / nq;
+    float* mass = p.mass + plane * p.mass_rs;
     for (int rt = 0; rt < p.row_tiles; ++rt) {
       const long long item = item0 + (long long)rt * p.c.H_kv;
       const int n_rows = min(N, p.rows - rt * N);
+      // the rows' log sums, +inf past the last: as the first kernel left them, or from the parts
       __syncthreads();
-      if ((int)threadIdx.x < n_rows) {
+      const int2 plan = p.whole ? make_int2(-1, -1) : p.ws_items[item];
+      const int parts = plan.x < 0 ? 0 : paged_parts(plan.x, plan.y);
+      if (parts <= 4) {
         const int r = threadIdx.x;
-        const int2 plan = p.whole ? make_int2(-1, -1) : p.ws_items[item];
-        float lse;
-        if (plan.x < 0) {
-          lse = p.ws_lse[item * N + r];
-        } else {
+        float lse = INFINITY;
+        if (r < n_rows) {
+          if (parts == 0) {
+            lse = p.ws_lse[item * N + r];
+          } else {
+            float2 ml[4];
+            float M = -INFINITY, l = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              ml[k] = *reinterpret_cast<const float2*>(p.ws_ml + ((long long)paged_slot(plan.x, min(k, parts - 1)) * N + r) * 2);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < parts && ml[k].y != 0.0f) M = fmaxf(M, ml[k].x);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < parts && ml[k].y != 0.0f) l += ml[k].y * exp2f(ml[k].x - M);
+            if (l != 0.0f) lse = M + log2f(l);
+          }
+        }
+        if (r < 64) s_lse[r] = lse;
+      } else {
+        for (int r = warp; r < 64; r += 4) {
           float M = -INFINITY, l = 0.0f;
-          for (int k = 0; k < paged_parts(plan.x, plan.y); ++k) {
+          for (int k = lane; k < parts && r < n_rows; k += 32) {
             const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + ((long long)paged_slot(plan.x, k) * N + r) * 2);
             if (ml.y == 0.0f) continue;
             const float top = fmaxf(M, ml.x);
             l = l * exp2f(M - top) + ml.y * exp2f(ml.x - top);
             M = top;
           }
-          lse = l == 0.0f ? INFINITY : M + log2f(l);
+          float top = M;
+#pragma unroll
+          for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+          if (M > -INFINITY) l *= exp2f(M - top);
+#pragma unroll
+          for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+          if (lane == 0) s_lse[r] = l == 0.0f ? INFINITY : top + log2f(l);
+          if (r >= n_rows) break;                         // (of the rows past the last up to three are read)
         }
-        s_lse[r] = lse;
       }
       __syncthreads();
+      const bool rows_here = 4 * q < n_rows;              // (else what lies there is nobody's)
+      const float4 l4 = rows_here ? *reinterpret_cast<const float4*>(&s_lse[4 * q]) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float* z = p.ws_z + item * p.z_tiles * kPagedKeys * p.nz + 4 * q;
+      for (int at = first; at < end; at += step) {
+        float4 v[4];
+        float old[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int t = first + h * 128 + (int)threadIdx.x;
-        if (t >= n) continue;
-        const float* z = p.ws_z + ((item * p.z_tiles + t / kPagedKeys) * kPagedKeys + t % kPagedKeys) * p.nz;
-        for (int r = 0; r < n_rows; r += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(z + r);
-          sum[h] += pow2_approx(v.x - s_lse[r]);
-          if (r + 1 < n_rows) sum[h] += pow2_approx(v.y - s_lse[r + 1]);
-          if (r + 2 < n_rows) sum[h] += pow2_approx(v.z - s_lse[r + 2]);
-          if (r + 3 < n_rows) sum[h] += pow2_approx(v.w - s_lse[r + 3]);
+        for (int e = 0; e < 4; ++e) {
+          const int k = k0 + e * keys;
+          const bool there = e * keys < mine && at + k < n;
+          v[e] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+          old[e] = 0.0f;
+          if (rows_here && there) v[e] = *reinterpret_cast<const float4*>(z + (long long)(at + k) * p.nz);
+          if (q == 0 && there) old[e] = mass[at + k];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int k = k0 + e * keys;
+          float sum = (pow2_approx(v[e].x - l4.x) + pow2_approx(v[e].y - l4.y)) +
+                      (pow2_approx(v[e].z - l4.z) + pow2_approx(v[e].w - l4.w));
+          for (int d = nq / 2; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+          if (q == 0 && e * keys < mine && at + k < n) mass[at + k] = old[e] + sum;
         }
       }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int t = first + h * 128 + (int)threadIdx.x;
-      if (t < n) p.mass[plane * p.mass_rs + t] += sum[h];
     }
     return;
   }
 
-  const int r = (int)blockIdx.x / p.join_ctas, cta = (int)blockIdx.x - r * p.join_ctas;
+  // A row of an item with its parts shared by the warps; or (16 rows of a tile and more) four, a warp each where the parts
+  // are few, else one after the other.
+  const int r0 = (int)blockIdx.x / p.join_ctas, cta = (int)blockIdx.x - r0 * p.join_ctas;
   const int4 plan = p.ws_plan[cta];
   if (plan.x < 0) return;
-  const int s = plan.x / p.per_seq;
-  uint32_t g, j;
-  const uint32_t rt = p.by_heads.divmod((uint32_t)(plan.x - s * p.per_seq), g);
-  if ((int)rt * N + r >= p.rows) return;
-  const uint32_t i = p.by_group.divmod(rt * (uint32_t)N + (uint32_t)r, j);
-  const int parts = paged_parts(plan.y, plan.z);
-  float M = -INFINITY;
-  for (int k = lane; k < parts; k += 32) {
-    const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + ((long long)paged_slot(plan.y, k) * N + r) * 2);
-    if (ml.y != 0.0f) M = fmaxf(M, ml.x);
-  }
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  const int s = plan.x / p.per_seq, parts = paged_parts(plan.y, plan.z);
+  uint32_t g;
+  const int rt = (int)p.by_heads.divmod((uint32_t)(plan.x - s * p.per_seq), g), n_rows = min(N, p.rows - rt * N);
   constexpr int D = HD / 32;
-  float o[D] = {}, sum = 0.0f;
-  for (int k0 = warp; k0 < parts; k0 += 16) {
-    // four parts' outputs at once
-    float2 ml[4];
-    float v[4][D];
+  const int each = N > 8 ? 4 : 1;
+  const bool few = N > 8 && parts <= 8;
+  for (int k = few ? warp : 0; k < (few ? warp + 1 : each); ++k) {
+    const int r = each * r0 + k;
+    if (r >= n_rows) break;
+    float o[D] = {}, sum = 0.0f, M = -INFINITY;
+    for (int k0 = lane; k0 < parts; k0 += 32) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + ((long long)paged_slot(plan.y, k0) * N + r) * 2);
+      if (ml.y != 0.0f) M = fmaxf(M, ml.x);
+    }
+    const int step = few ? 1 : 4;
+    for (int k0 = few ? 0 : warp; k0 < parts; k0 += 4 * step) {
+      // four parts' outputs at once
+      float2 ml[4];
+      float v[4][D];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const long long at = (long long)paged_slot(plan.y, min(k0 + 4 * e, parts - 1)) * N + r;
-      ml[e] = *reinterpret_cast<const float2*>(p.ws_ml + at * 2);
-      const float* src = p.ws_o + at * HD + lane * D;
-      if constexpr (D == 4) {
-        const float4 f = *reinterpret_cast<const float4*>(src);
-        v[e][0] = f.x;
-        v[e][1] = f.y;
-        v[e][2] = f.z;
-        v[e][3] = f.w;
-      } else {
-        const float2 f = *reinterpret_cast<const float2*>(src);
-        v[e][0] = f.x;
-        v[e][1] = f.y;
+      for (int e = 0; e < 4; ++e) {
+        const long long at = (long long)paged_slot(plan.y, min(k0 + e * step, parts - 1)) * N + r;
+        ml[e] = *reinterpret_cast<const float2*>(p.ws_ml + at * 2);
+        const float* src = p.ws_o + at * HD + lane * D;
+        if constexpr (D == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(src);
+          v[e][0] = f.x;
+          v[e][1] = f.y;
+          v[e][2] = f.z;
+          v[e][3] = f.w;
+        } else {
+          const float2 f = *reinterpret_cast<const float2*>(src);
+          v[e][0] = f.x;
+          v[e][1] = f.y;
+        }
+      }
+      if (k0 == (few ? 0 : warp)) {
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (k0 + e * step >= parts || ml[e].y == 0.0f) continue;
+        const float wk = ml[e].y * exp2f(ml[e].x - M);
+        sum += wk;
+#pragma unroll
+        for (int d = 0; d < D; ++d) o[d] += wk * v[e][d];
       }
     }
+    if (!few) {
+      __syncthreads();                                    // (the row's before are read)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (k0 + 4 * e >= parts || ml[e].y == 0.0f) continue;
-      const float wk = ml[e].y * exp2f(ml[e].x - M);
-      sum += wk;
+      for (int d = 0; d < D; ++d) s_o[warp][lane * D + d] = o[d];
+      if (lane == 0) s_w[warp] = sum;
+      __syncthreads();
+      if (warp > 0) continue;
+      sum = (s_w[0] + s_w[1]) + (s_w[2] + s_w[3]);
 #pragma unroll
-      for (int d = 0; d < D; ++d) o[d] += wk * v[e][d];
+      for (int d = 0; d < D; ++d)
+        o[d] = (s_o[0][lane * D + d] + s_o[1][lane * D + d]) + (s_o[2][lane * D + d] + s_o[3][lane * D + d]);
     }
-  }
+    uint32_t j;
+    const uint32_t i = p.by_group.divmod((uint32_t)(rt * N + r), j);
+    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint32_t word[D / 2];
 #pragma unroll
-  for (int d = 0; d < D; ++d) s_o[warp][lane * D + d] = o[d];
-  if (lane == 0) s_w[warp] = sum;
-  __syncthreads();
-  if (threadIdx.x >= HD) return;
-  sum = (s_w[0] + s_w[1]) + (s_w[2] + s_w[3]);
-  const float v = (s_o[0][threadIdx.x] + s_o[1][threadIdx.x]) + (s_o[2][threadIdx.x] + s_o[3][threadIdx.x]);
-  F::E::put(reinterpret_cast<typename F::E::T*>(p.out) + ((long long)s * p.R + i) * p.o_rs +
-                (long long)((int)g * p.group + (int)j) * HD + threadIdx.x,
-            sum == 0.0f ? 0.0f : v / sum);
+    for (int d = 0; d < D; d += 2) word[d / 2] = F::pack(o[d] * f, o[d + 1] * f);
+    uint16_t* out = p.out + ((long long)s * p.R + i) * p.o_rs + (long long)((int)g * p.group + (int)j) * HD + lane * D;
+    if constexpr (D == 4)
+      *reinterpret_cast<uint2*>(out) = make_uint2(word[0], word[1]);
+    else
+      *reinterpret_cast<uint32_t*>(out) = word[0];
+  }
 }
 
 }  // namespace dllm
