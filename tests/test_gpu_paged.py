@@ -648,6 +648,30 @@ def test_token_logprobs_ties_and_tokens_that_cannot_come(torch, vocab, dtype):
     logprobs_check(f64(buf), targets, 50, 1.0, got)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("vocab", [900, 33001])
+def test_token_logprobs_of_the_types_lowest_values(torch, vocab, dtype):
+    """Masks of the type's lowest value beside ordinary logits, alone, and beside -inf; huge logits; a row whose largest
+    changes from one to the other."""
+    rng = np.random.default_rng(vocab + 1)
+    low = {"bf16": -3.3895313892515355e38, "f16": -65504.0, "f32": -3.4028234663852886e38}[dtype]
+    x = rng.standard_normal((7, vocab))
+    x[0] = low
+    x[1, 10:] = low
+    x[2] = low
+    x[2, ::2] = -np.inf
+    x[3] = np.where(rng.random(vocab) < 0.5, low, -low)
+    x[4] = low
+    x[4, vocab - 3] = 3.0
+    x[5, : vocab // 2] = low / 2
+    x[6] = x[6] * 1e4 if dtype != "f16" else x[6] * 1e3
+    buf = dev(torch, x.astype(np.float32)).to(dt(torch, dtype))
+    targets = [3, 4, 1, 7, vocab - 3, vocab - 1, 0]
+    got = logprobs(torch, buf, dtype, targets, 12)
+    with np.errstate(over="ignore", invalid="ignore"):
+        logprobs_check(f64(buf), targets, 12, 1.0, got)
+
+
 def test_token_logprobs_each_output_alone(torch):
     rng = np.random.default_rng(1)
     x = dev(torch, rng.standard_normal((3, 999)).astype(np.float32))
