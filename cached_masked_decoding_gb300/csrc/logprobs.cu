@@ -13,7 +13,7 @@
 // us for the case below, with loads into registers and results apart 217).
 // What needs elements again is a few threads' worth, which lies in L2 still:
 //   - the alternatives are among the elements of units whose largest is no less than the top-th largest of 128 group
-//     maxima (a lower bound of the top-th largest element): for 20 of 126464 about 22 units of 64 elements.  Elements
+//     maxima (a lower bound of the top-th largest element): for 20 of 126464 about 22 units of 32 elements.  Elements
 //     above the bound are ranked by counting; its equals join in the order of their ids.
 //   - where the others' S is less than the largest's 1, the thread that holds it takes its sums again without it.
 // Rows that would give more than 512 elements above the bound (a few threads' are the largest by far) take a pass of the
@@ -38,7 +38,7 @@ struct LogprobsParams {
   float *logp, *entropy, *top_logp;
   int32_t* top_ids;
   long long rs;
-  int rows, vocab, top, cluster, slots;
+  int rows, vocab, top, cluster, slots, units;
   float scale;
 };
 
@@ -58,7 +58,7 @@ struct LogCfg {
 };
 constexpr int kLogGroups = 128;
 constexpr int kLogFewTop = 24;
-constexpr int kLogUnits = 8;         // of a thread's batches, each with a largest element of its own (and one for the rest)
+constexpr int kLogUnits = 16;        // of a thread's batches at most, each with a largest element of its own (and one for the rest)
 constexpr int kMostUnits = 512;      // units that are looked through again, before all are
 
 static __device__ int g_logprobs_err[1];
@@ -237,7 +237,6 @@ __device__ __forceinline__ void join_sums(LogRest& t, LogRest o, float c2) {
 template <int MAIN>
 struct alignas(128) LogShared {
   float m[2][MAIN], S[2][MAIN], W[2][MAIN];      // of the streaming threads, rows in turn
-  float unit[2][kLogUnits + 1][MAIN];            // largest elements of a thread's units
   alignas(8) uint64_t ready[2], done[2], full[LogCfg<MAIN>::SLOTS], empty[LogCfg<MAIN>::SLOTS];
   float own[4];                                  // the owner's S and W, with the largest and taken again without it
   float warp_m[kLogRest / 32], warp_S[kLogRest / 32], warp_W[kLogRest / 32];
@@ -386,7 +385,7 @@ __device__ int equals_in_order(const LogRow<E, MAIN>& row, LogShared<MAIN>& sh, 
 // A row's results from the streaming threads' sums in buffer b; by kLogRest threads.  false: not this CTA's to give.
 template <typename E, int MAIN>
 __device__ __forceinline__ void row_results(const LogprobsParams& p, LogShared<MAIN>& sh, const LogRow<E, MAIN>& row, int r,
-                                            int b, int tid, int rank, int ranks, float c2) {
+                                            int b, int tid, int rank, int ranks, float c2, const float* unit) {
   constexpr int VE = LogRow<E, MAIN>::VE, EACH = MAIN / kLogRest;
   const int lane = tid & 31, warp = tid >> 5, top = p.top;
   float m[EACH], M = -INFINITY;
@@ -482,7 +481,7 @@ __device__ __forceinline__ void row_results(const LogprobsParams& p, LogShared<M
       const int t = tid + k * kLogRest, units = ((row.vectors(t) / kLogAhead + (1 << span_log) - 1) >> span_log) + 1;
       uint32_t mask = 0;
 #pragma unroll
-      for (int j = 0; j <= kLogUnits; ++j) mask |= j < units && sh.unit[b][j][t] >= bound ? 1u << j : 0;
+      for (int j = 0; j <= kLogUnits; ++j) mask |= j < units && unit[j * MAIN + t] >= bound ? 1u << j : 0;
       if (!hot) mask = 0;
       for (; mask; mask &= mask - 1) {
         const int at = atomicAdd(&sh.n_hot, 1);
@@ -711,6 +710,7 @@ __global__ void __launch_bounds__(LogCfg<MAIN>::THREADS, LogCfg<MAIN>::CTAS)
   extern __shared__ __align__(128) uint8_t s_raw[];
   LogShared<MAIN>& sh = *reinterpret_cast<LogShared<MAIN>*>(s_raw);
   uint4* ring = reinterpret_cast<uint4*>(s_raw + sizeof(LogShared<MAIN>));   // p.slots chunks
+  float* unit0 = reinterpret_cast<float*>(ring + p.slots * C::CHUNK);        // [2][p.units][MAIN] largest elements
   const int tid = threadIdx.x, lane = tid & 31;
   const int ranks = p.cluster, rank = ranks > 1 ? (int)cluster_rank() : 0;
   const float c2 = p.scale * 1.4426950408889634f;
@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(LogCfg<MAIN>::THREADS, LogCfg<MAIN>::CTAS)
       const int span = 1 << row.span_log();
       int left = span;                 // batches until the unit is full
       float largest = -INFINITY;       // the unit's
-      float* unit = &sh.unit[b][0][tid];
+      float* unit = unit0 + b * p.units * MAIN + tid;
       auto batch = [&](float top) {
         largest = fmaxf(largest, top);
         if (--left == 0) {
@@ -850,7 +850,7 @@ __global__ void __launch_bounds__(LogCfg<MAIN>::THREADS, LogCfg<MAIN>::CTAS)
       // (after a wait that gave up the results are invalid, and reported)
       mbar_wait_long(&sh.ready[b], (uint32_t)(k / 2) & 1u, &sh.abort, g_logprobs_err, ERR_LOGPROBS);
       __syncwarp();
-      row_results(p, sh, row, r, b, tid - MAIN, rank, ranks, c2);
+      row_results(p, sh, row, r, b, tid - MAIN, rank, ranks, c2, unit0 + b * p.units * MAIN);
       __syncwarp();
       if (tid % 32 == 0) mbar_arrive(&sh.done[b]);
       rest_sync();                     // what the results were made of is read: the next row's may be written
@@ -865,16 +865,17 @@ cudaError_t launch_logprobs(LogprobsParams& p, cudaStream_t st) {
   using C = LogCfg<MAIN>;
   // a cluster a row, or as many CTAs as fit, which take row after row
   const int sms = op_device_sms(), grid = p.cluster > 1 ? p.rows * p.cluster : std::min(p.rows, C::CTAS * sms);
-  // the ring: what an SM's CTAs leave each other, and no more than a CTA has chunks (a small CTA starts beside the
-  // kernel before)
-  const int ctas = std::min(C::CTAS, (grid + sms - 1) / sms);
-  constexpr int chunk = C::CHUNK * 16, fixed = (int)sizeof(LogShared<MAIN>);
-  const int room = (228 * 1024 / ctas - 1024 - fixed) / chunk;
+  // A thread's units; the ring, what an SM's CTAs leave each other, and no more than a CTA has chunks: a small CTA starts
+  // beside the kernel before (32 rows of 126464: 12.3 us, with 12 KB more of units 16.4).
   const long long vectors = p.vocab / (16 / (int)sizeof(typename E::T)) / p.cluster + 1;
+  p.units = (int)std::min<long long>(kLogUnits, (vectors + MAIN - 1) / MAIN / kLogAhead) + 1;
+  const int ctas = std::min(C::CTAS, (grid + sms - 1) / sms);
   const long long chunks = (vectors + C::CHUNK - 1) / C::CHUNK * ((p.rows * (long long)p.cluster + grid - 1) / grid);
+  constexpr int chunk = C::CHUNK * 16, shared = (int)sizeof(LogShared<MAIN>), unit = 2 * MAIN * 4;
+  const int fixed = shared + p.units * unit, room = (228 * 1024 / ctas - 1024 - fixed) / chunk;
   p.slots = (int)std::min<long long>({room, C::SLOTS, chunks});
   const cudaError_t e = op_smem_once(reinterpret_cast<const void*>(logprobs_kernel<E, MAIN>),
-                                     fixed + std::min(C::SLOTS, (227 * 1024 - fixed) / chunk) * chunk);
+                                     std::min(shared + (kLogUnits + 1) * unit + C::SLOTS * chunk, 227 * 1024));
   if (e != cudaSuccess) return e;
   return op_launch(logprobs_kernel<E, MAIN>, dim3((unsigned)grid), dim3(C::THREADS), (size_t)(fixed + p.slots * chunk), st,
                    p.cluster, p);

@@ -574,6 +574,8 @@ def logprobs_check(x, targets, top, scale, got):
     lp, en, ids, tl = (f64(t) for t in got)
     for r in range(x.shape[0]):
         w_lp, w_en, w_ids, w_tl, S, W, D = ref.logprobs(x[r], scale, int(targets[r]), top)
+        # (outputs are float32: what is past its largest value is an infinity there)
+        w_lp, *w_tl = (math.copysign(math.inf, w) if abs(w) > 3.4028235e38 else w for w in [w_lp] + list(w_tl))
         assert ids[r].astype(int).tolist()[:top] == w_ids, (r, ids[r], w_ids)
         # a term e^d: d = scale (z - M) within 3 roundings of itself (one more to base 2), 2^d within 2^-22; sums of
         # terms of one sign in chains of up to 128 and trees; the largest term's chain starts from the others'
