@@ -18,10 +18,10 @@
 //   - where the others' S is less than the largest's 1, the thread that holds it takes its sums again without it.
 // Rows that would give more than 512 elements above the bound (a few threads' are the largest by far) take a pass of the
 // row an alternative.
-// 4096 rows of 126464 in bf16, 20 alternatives: 184 us, 5.6 TB/s (none: 167; 2048 rows of float32: 169); 32 rows, 5
-// alternatives: 12.3 us, of which a chain of reductions and a cluster's join are the most; 257 rows of 32001 in float32:
-// 12.8 us.  Bound by issue slots beside HBM: an element of 16 bits costs about 7 instructions.  Three CTAs an SM with 56
-// registers a thread: 212 us; 384 streaming threads: 189.
+// 4096 rows of 126464 in bf16, 20 alternatives: 172 us, 6.0 TB/s (none: 156, 50: 196; 2048 rows of float32: 156); 32 rows,
+// 5 alternatives: 12.4 us, of which a chain of reductions and a cluster's join are the most; 257 rows of 32001 in float32:
+// 12.8 us.  Beside HBM the issue slots bound it: the warps that work out results take them from those that stream.  At
+// an earlier step (184 us) three CTAs an SM with 56 registers a thread took 212, 384 streaming threads 189.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -53,7 +53,7 @@ template <int MAIN>
 struct LogCfg {
   static constexpr int THREADS = MAIN + kLogRest + 32;
   static constexpr int CTAS = MAIN == 128 ? 4 : 2;               // an SM
-  static constexpr int CHUNK = kLogAhead * MAIN;                 // vectors
+  static constexpr int CHUNK = kLogAhead * MAIN;                 // vectors, a batch of every thread's (two: 212 us)
   static constexpr int SLOTS = 6;                                // of the ring, at most
 };
 constexpr int kLogGroups = 128;
@@ -763,30 +763,34 @@ __global__ void __launch_bounds__(LogCfg<MAIN>::THREADS, LogCfg<MAIN>::CTAS)
           slot = 0;
           phase ^= 1u;
         }
-        const bool whole = v0 + (AHEAD - 1) * MAIN + tid < row.v1;   // a batch of this thread's
-        uint4 raw[AHEAD];
-        if (whole) {
+        if (v0 + C::CHUNK <= row.v1) {
+          uint4 raw[AHEAD];
 #pragma unroll
           for (int i = 0; i < AHEAD; ++i) raw[i] = chunk[i * MAIN];
-        }
-        if (v0 + C::CHUNK > row.v1) {                                // the row's last chunk
-          if (whole) batch(mine.template add<E>(raw, c2));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty);
+          batch(mine.template add<E>(raw, c2));
+        } else {                                                     // the row's last chunk
+          int v = v0 + tid;
+          if (v + (AHEAD - 1) * MAIN < row.v1) {
+            uint4 raw[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) raw[i] = chunk[i * MAIN];
+            batch(mine.template add<E>(raw, c2));
+            v += AHEAD * MAIN;
+          }
           if (left < span) {
             *unit = largest;
             unit += MAIN;
             largest = -INFINITY;
             left = span;
           }
-          for (int i = 0; !whole && v0 + i * MAIN + tid < row.v1; ++i) {
-            const uint4 raw1[1] = {chunk[i * MAIN]};
+          for (; v < row.v1; v += MAIN, chunk += MAIN) {
+            const uint4 raw1[1] = {*chunk};
             largest = fmaxf(largest, mine.template add<E>(raw1, c2));
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(empty);
-        } else {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(empty);
-          batch(mine.template add<E>(raw, c2));
         }
       }
       if (left < span) {
