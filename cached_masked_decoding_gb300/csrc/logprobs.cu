@@ -18,10 +18,11 @@
 //   - where the others' S is less than the largest's 1, the thread that holds it takes its sums again without it.
 // Rows that would give more than 512 elements above the bound (a few threads' are the largest by far) take a pass of the
 // row an alternative.
-// 4096 rows of 126464 in bf16, 20 alternatives: 172 us, 6.0 TB/s (none: 156, 50: 196; 2048 rows of float32: 156); 32 rows,
+// 4096 rows of 126464 in bf16, 20 alternatives: 172 us, 6.0 TB/s (none: 157, 50: 193; 2048 rows of float32: 156); 32 rows,
 // 5 alternatives: 12.4 us, of which a chain of reductions and a cluster's join are the most; 257 rows of 32001 in float32:
 // 12.8 us.  Beside HBM the issue slots bound it: the warps that work out results take them from those that stream.  At
-// an earlier step (184 us) three CTAs an SM with 56 registers a thread took 212, 384 streaming threads 189.
+// an earlier step (184 us) three CTAs an SM with 56 registers a thread took 212, 384 streaming threads 189.  A second
+// team for the results, rows in turn, takes 4096 rows of 32000 from 95 us to 88, but this case to 184.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -388,6 +389,11 @@ __device__ __forceinline__ void row_results(const LogprobsParams& p, LogShared<M
                                             int b, int tid, int rank, int ranks, float c2, const float* unit) {
   constexpr int VE = LogRow<E, MAIN>::VE, EACH = MAIN / kLogRest;
   const int lane = tid & 31, warp = tid >> 5, top = p.top;
+  // the given token's logit, on its way from the start: it is due at the end
+  const int target = p.logp && tid == 0 && rank == 0 ? p.targets[r] : -1;
+  const bool given = target >= 0 && target < p.vocab;
+  typename E::T given_x{};
+  if (given) given_x = row.x[target];
   float m[EACH], M = -INFINITY;
 #pragma unroll
   for (int k = 0; k < EACH; ++k) {
@@ -668,10 +674,7 @@ __device__ __forceinline__ void row_results(const LogprobsParams& p, LogShared<M
   const bool finite = fabsf(sum.m) != INFINITY && sum.S == sum.S;
   const float nan = __uint_as_float(0x7fffffffu), log_sum = finite ? log1pf(sum.S) : nan;
   if (tid == 0) {
-    if (p.logp) {
-      const int t = p.targets[r];
-      p.logp[r] = t >= 0 && t < p.vocab ? (E::get(row.x + t) - sum.m) * p.scale - log_sum : nan;
-    }
+    if (p.logp) p.logp[r] = given ? (E::get(&given_x) - sum.m) * p.scale - log_sum : nan;
     if (p.entropy) p.entropy[r] = log_sum - sum.W * 0.6931471805599453f / (1.0f + sum.S);
   }
   for (int i = tid; i < ranks * top; i += kLogRest) {
