@@ -3,7 +3,6 @@
 // g = h / (H / H_kv), and the weight that every key received, summed over the rows and heads of g.  The kernels are
 // in attn_paged.cuh; here is what runs, and on what.
 #include <algorithm>
-#include <cmath>
 
 #include "attn_paged.cuh"
 
@@ -103,10 +102,10 @@ extern "C" dllm_status dllm_op_attention_paged(const void* q, int64_t q_row_stri
                                                int32_t H, int32_t R, float* mass, int64_t mass_stride, void* workspace,
                                                int64_t workspace_bytes, void* stream) {
   if (const dllm_status s = kv_paged_check(cache, "attention_paged"); s != DLLM_OK) return s;
-  if (!q || !out || H < 1 || H % cache->H_kv || R < 1 || !(scale > 0.0f) || !std::isfinite(scale) ||
+  if (!q || !out || H < 1 || H % cache->H_kv || R < 1 || !(scale > 0.0f) || scale > 1e38f ||
       !op_aligned(q, 16) || !op_aligned(out, 16) || !op_aligned(lens, 4) || !op_aligned(mass, 4))
     return op_fail(DLLM_EINVAL,
-                   "bad attention_paged arguments: H=%d (a multiple of H_kv=%d) R=%d scale=%g (over 0, finite), q and "
+                   "bad attention_paged arguments: H=%d (a multiple of H_kv=%d) R=%d scale=%g (over 0, to 1e38), q and "
                    "out 16-byte aligned",
                    H, cache->H_kv, R, scale);
   AttnPagedParams p = {};

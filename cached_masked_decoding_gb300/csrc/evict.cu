@@ -273,6 +273,8 @@ extern "C" dllm_status dllm_op_kv_paged_evict(const dllm_kv_paged* src, const dl
     return op_fail(DLLM_EINVAL, "kv_paged_evict: bad strides: mass %lld, mass_out %lld (at least keep=%d)", p.mass_rs,
                    p.mass_out_rs, keep);
   if ((const void*)mass == mass_out) return op_fail(DLLM_EINVAL, "kv_paged_evict: mass_out is mass");
+  if (lens && lens == new_lens)   // (CTAs read lens while one writes m)
+    return op_fail(DLLM_EINVAL, "kv_paged_evict: new_lens is lens");
   const long long planes = (long long)src->b * src->H_kv;
   if (planes > 0x7fffffff || (double)planes * ((keep + 15) / 16) > 0x7fffffff)
     return op_fail(DLLM_EINVAL, "kv_paged_evict: b=%d H_kv=%d keep=%d are too many for one call", src->b, src->H_kv, keep);

@@ -326,7 +326,7 @@ cudaError_t launch_heads(const HeadsParams& p, bool paged, int lanes, dim3 grid,
 dllm_status heads(HeadsParams& p, const char* who, bool paged, int dtype, int out_dtype, const dllm_rope* r,
                   void* stream) {
   const int es = op_dtype_size(dtype), os = op_dtype_size(out_dtype);
-  if (!p.q || !p.k || !p.q_out || (paged ? !p.v : !p.k_out) || p.rows < 1 || p.H < 1 || p.H_kv < 1 || es == 0 ||
+  if (!p.q || !p.k || !p.q_out || (paged ? !p.v : !p.k_out) || p.rows < 1 || p.rows > kMostRows || p.H < 1 || p.H_kv < 1 || es == 0 ||
       os == 0 || (dtype != out_dtype && dtype != DLLM_F32) || p.hd < 16 || p.hd > 256 || p.hd % 16)
     return op_fail(DLLM_EINVAL,
                    "bad %s arguments: rows=%d H=%d H_kv=%d hd=%d (a multiple of 16, to 256) dtype=%d out_dtype=%d "
@@ -381,7 +381,7 @@ dllm_status heads(HeadsParams& p, const char* who, bool paged, int dtype, int ou
   p.batch = std::min(p.run, std::min(kHeadsRows, pairs ? kHeadsAngles / pairs : kHeadsRows) / p.step * p.step);
   p.row_bytes = p.chunk * p.hd * es;                    // 32 KB at most
   p.stages = std::min({kHeadsStages, kHeadsRing / (p.step * p.row_bytes), (p.run + p.step - 1) / p.step});
-  const dim3 grid((unsigned)((p.rows + p.run - 1) / p.run), (unsigned)chunks), block((unsigned)threads);
+  const dim3 grid((unsigned)(((long long)p.rows + p.run - 1) / p.run), (unsigned)chunks), block((unsigned)threads);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == DLLM_BF16)
     OP_CK((launch_heads<ElemBf16, ElemBf16>(p, paged, lanes, grid, block, st)));

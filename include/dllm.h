@@ -637,7 +637,7 @@ typedef struct dllm_kv_paged {
  * (both weights NULL).  rope: NULL: nothing turns (positions may be NULL);
  * rot_dim a multiple of 16.  positions: device int32 [rows].  An output may be
  * its input with the same strides and type.  Squares are float32: elements
- * stay within 2^60. */
+ * stay within 2^59. */
 dllm_status dllm_op_qk_norm_rope(const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride, void* q_out,
                                  int64_t q_out_row_stride, void* k_out, int64_t k_out_row_stride,
                                  const int32_t* positions, int32_t rows, int32_t H, int32_t H_kv, int32_t hd,
@@ -670,7 +670,7 @@ dllm_status dllm_op_qk_norm_rope_paged(const dllm_kv_paged* cache, const void* q
  * lens <= 0 gives zeros.  What lies at or past lens[s], or on no page, is not
  * used, whatever its bytes.  q, out: of the cache's type, [b*R][H][hd], 16-byte
  * aligned, rows q_row_stride / out_row_stride elements apart (0: dense; else a
- * multiple of 8).  scale: > 0, finite.  Scores, statistics and sums are float32; a probability
+ * multiple of 8).  scale: > 0, at most 1e38.  Scores, statistics and sums are float32; a probability
  * enters the value product as the sum of two halves of the cache's type (16
  * bits of it in bf16).  K, V and q are finite, and so are the scores.
  *   mass (nullable): device float32 [b][H_kv][mass_stride] (0: max_pages *
@@ -702,7 +702,7 @@ dllm_status dllm_op_attention_paged_workspace(int32_t b, int32_t H, int32_t H_kv
  *   mass: device float32 [b][H_kv][mass_stride] (0: max_pages * page_size of
  *   src); n is at most mass_stride.
  *   kept: device int32 [b][H_kv][keep], the positions kept, ascending, -1 from m on.
- *   new_lens: device int32 [b], m.
+ *   new_lens: device int32 [b], m; not lens itself.
  *   mass_out (nullable): device float32 [b][H_kv][mass_out_stride] (0: keep),
  *   mass_out_stride >= keep: the weights of the kept, its other elements stay as they were.
  * A kept position that lies on no page gives a row of zeros.
@@ -719,10 +719,11 @@ dllm_status dllm_op_kv_paged_evict(const dllm_kv_paged* src, const dllm_kv_paged
  *   top_ids[r][0..top), top_logprobs[r][0..top): the largest logits, ties the
  *   lowest id first, and their log p.
  * logits: device [rows][vocab] of dtype, rows row_stride elements apart (0:
- * vocab; else >= vocab), aligned to their elements.  targets: device int32
+ * vocab; else >= vocab), aligned to their elements; rows and vocab at most
+ * 2^31 - 4096.  targets: device int32
  * [rows], goes with logprobs; every output may be NULL, top_ids and
  * top_logprobs are given together when top > 0; top <= 64 and <= vocab.
- * inv_temperature: > 0, finite.  Sums are float32, taken apart from the largest
+ * inv_temperature: > 0, at most 1e38.  Sums are float32, taken apart from the largest
  * term, so that log p and entropy of a nearly certain row keep their relative
  * accuracy.  A logit of -inf is a token that cannot come: p = 0, and an
  * alternative only after all others.  A row with a NaN or +inf, or of nothing

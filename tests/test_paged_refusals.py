@@ -61,7 +61,7 @@ def test_attention_paged_refuses_bad_arguments():
     for q, out, H, R in [(0, A, 8, 1), (A, 0, 8, 1), (A + 8, A, 8, 1), (A, A + 4, 8, 1), (A, A, 0, 1), (A, A, 6, 1),
                          (A, A, 8, 0), (A, A, 8, -1)]:
         refused(op, q, cache(), out, H, R, **big)
-    for s in (0.0, -1.0, float("nan"), float("inf")):
+    for s in (0.0, -1.0, float("nan"), float("inf"), 2.5e38):
         refused(op, A, cache(), A, 8, 1, scale=s, text="scale", **big)
     for rs in (1016, 1028, -1024, 1 << 41):
         refused(op, A, cache(), A, 8, 1, q_row_stride=rs, text="stride", **big)
@@ -79,7 +79,8 @@ HEADS_BAD = [dict(q=0), dict(k=0), dict(qo=0), dict(ko=0), dict(q=A + 8), dict(k
              dict(dtype="bf16", out="f16"), dict(eps=float("nan")), dict(eps=float("inf")), dict(qw=A + 2),
              dict(eps=-1.0, qw=A), dict(eps=-1.0, kw=A), dict(pos=A + 1), dict(qs=8), dict(ks=8), dict(qs=1028),
              dict(qos=1 << 41), dict(kos=-512), dict(H=1 << 25), dict(rope=dict(rot_dim=24)), dict(rope=dict(rot_dim=192)),
-             dict(rope=dict(rot_dim=64), pos=0), dict(rope=dict(rot_dim=64, theta=0.5)), dict(qo=A, qos=2048)]
+             dict(rope=dict(rot_dim=64), pos=0), dict(rope=dict(rot_dim=64, theta=0.5)), dict(qo=A, qos=2048),
+             dict(rows=0x7fffffff)]
 
 
 @pytest.mark.parametrize("bad", HEADS_BAD, ids=lambda s: ",".join(f"{k}={v}" for k, v in s.items()))
@@ -107,7 +108,7 @@ def test_qk_norm_rope_paged_refuses():
 
 EVICT_BAD = [dict(mass=0), dict(kept=0), dict(lens_out=0), dict(keep=0), dict(keep=-1), dict(sinks=-1), dict(recent=-1),
              dict(sinks=3, recent=2), dict(keep=129), dict(mass=A + 2), dict(kept=A + 2), dict(lens=A + 1),
-             dict(ms=-1), dict(mo=B, mos=3), dict(mo=A), dict(mo=B + 2), dict(sinks=0x7fffffff, recent=0x7fffffff)]
+             dict(ms=-1), dict(mo=B, mos=3), dict(mo=A), dict(mo=B + 2), dict(lens=A), dict(sinks=0x7fffffff, recent=0x7fffffff)]
 
 
 @pytest.mark.parametrize("bad", EVICT_BAD, ids=lambda s: ",".join(f"{k}={v}" for k, v in s.items()))
@@ -124,8 +125,8 @@ def test_evict_refuses_caches_that_differ(other):
     refused(binding.op_kv_paged_evict, cache(), cache(**other), A, 4, A, A, text="differ")
 
 
-LOGPROBS_BAD = [dict(x=0), dict(x=A + 1), dict(rows=0), dict(vocab=0), dict(top=-1), dict(top=65, ids=A, lp=A),
-                dict(vocab=4, top=5, ids=A, lp=A), dict(t=0.0), dict(t=-1.0), dict(t=float("inf")),
+LOGPROBS_BAD = [dict(x=0), dict(x=A + 1), dict(rows=0), dict(rows=0x7fffffff), dict(vocab=0), dict(top=-1), dict(top=65, ids=A, lp=A),
+                dict(vocab=4, top=5, ids=A, lp=A), dict(t=0.0), dict(t=-1.0), dict(t=float("inf")), dict(t=2.5e38),
                 dict(t=float("nan")), dict(targets=A, logp=0), dict(targets=0, logp=A), dict(top=2), dict(top=2, ids=A),
                 dict(top=2, lp=A), dict(ids=A), dict(lp=A), dict(rs=99), dict(rs=-100), dict(rs=1 << 41),
                 dict(targets=A + 2, logp=A), dict(entropy=A + 1)]
