@@ -2,12 +2,14 @@
 //
 // Weights map to 32-bit whole numbers of the same order.  One CTA takes a (sequence, head) and reads its weights once,
 // into shared memory as far as they fit.  The weight of the last key that stays is found from the top: a histogram of
-// 12 bits over all keys that compete, then two of 10 bits over those that agree so far, which are few and kept in a
-// list.  A last walk writes the positions that stay in their order.
+// 12 bits over all keys that compete, then those that agree so far, which are few and kept in a list, are compared one by
+// one, or counted by two digits of 10 bits.  A last walk writes the positions that stay in their order: where all of the
+// threshold's weight stay, a warp packs its run of positions in place and writes it out; else it counts first.
 //
-// Latency and issue slots bound the selection (20 us for 32768 keys, 9 for 4097), HBM the copy: 8 sequences of 16 to 32
-// thousand keys of 8 heads of 128 in bf16 to 8192 keys: 110 us in all, 5.0 TB/s; one of 4097 to 1024: 9.5 us.  Clusters
-// of four CTAs a head, with histograms added up over distributed shared memory, took 40 us for the selection alone.
+// Latency and issue slots bound the selection (12 us for 32768 keys, 4.5 for 4097), HBM the copy: 8 sequences of 16 to 32
+// thousand keys of 8 heads of 128 in bf16 to 8192 keys: 104 us in all, 5.3 TB/s; one of 4097 to 1024: 7.6 us.  Clusters
+// of four CTAs a head, with histograms added up over distributed shared memory, took 40 us for the selection alone; the
+// first histogram in two copies, lanes in turn, nothing less; loops rolled up 107 us.
 #include <algorithm>
 
 #include "kv_paged.h"
@@ -29,9 +31,8 @@ struct EvictParams {
 
 // Weights as whole numbers of their order; a NaN is the least, -0 is 0.
 __device__ __forceinline__ uint32_t weight_order(float x) {
-  if (x != x) return 0;
-  const uint32_t b = __float_as_uint(x + 0.0f);
-  return (b >> 31) ? ~b : b | 0x80000000u;
+  const uint32_t b = __float_as_uint(x + 0.0f), o = b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+  return x == x ? o : 0;
 }
 
 __device__ __forceinline__ int evict_len(const EvictParams& p, int s) {
@@ -39,71 +40,252 @@ __device__ __forceinline__ int evict_len(const EvictParams& p, int s) {
 }
 
 constexpr int kEvictThreads = 1024, kEvictWarps = kEvictThreads / 32;
-constexpr int kEvictMost = 49152;      // positions whose weights stay in shared memory
+constexpr int kEvictStep = 8 * kEvictThreads;   // (32 runs of 256 positions)
+constexpr int kEvictMost = 6 * kEvictStep;      // positions whose weights stay in shared memory
 constexpr int kEvictList = 2048;       // keys that agree with the threshold's first bits, where they are no more
 constexpr int kEvictBins = 4096;
+constexpr int kEvictDirect = 128;      // keys of the list that are compared one by one
 constexpr uint32_t kEvictFixed = 0xffffffffu;   // the weight of what stays in any case
 
 struct EvictShared {
-  int hist[kEvictBins];
-  uint32_t list[kEvictList];
-  int warp[kEvictWarps];
-  int digit, left, n_list;             // of the threshold's digit; how many of its equals stay
+  alignas(16) int hist[kEvictBins];
+  alignas(16) uint32_t list[kEvictList];
+  int warp[kEvictWarps], equal[kEvictWarps];
+  int digit, left, same, n_list;       // of the threshold's digit; how many of its keys stay, of how many
+  uint32_t bits;
 };
 
-// Sum over the CTA's threads before this one, and the total.
-__device__ __forceinline__ int evict_scan(int v, int* s_warp, int& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int upto = v;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, upto, d);
-    if (lane >= d) upto += o;
-  }
-  __syncthreads();                     // (the last scan's sums are read)
-  if (lane == 31) s_warp[warp] = upto;
-  __syncthreads();
-  int sums = s_warp[lane];             // every warp scans the warps' sums
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, sums, d);
-    if (lane >= d) sums += o;
-  }
-  total = __shfl_sync(0xffffffffu, sums, 31);
-  const int base = __shfl_sync(0xffffffffu, sums, (warp + 31) & 31);
-  return (warp ? base : 0) + upto - v;
-}
-
 // From a histogram of SIZE bins: the bin from the top in which `left` of its and higher ones' keys are reached (into
-// sh.digit), and how many of its own that takes (sh.left).  The bins are zeros afterwards.
+// sh.digit), how many of its own that takes (sh.left) and how many it has.  The bins are zeros afterwards.
 template <int SIZE>
 __device__ __forceinline__ void evict_digit(EvictShared& sh, int left) {
   constexpr int B = SIZE / kEvictThreads;
+  static_assert(B == 1 || B == 4, "a thread's bins");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = SIZE - B * ((int)threadIdx.x + 1);
   __syncthreads();
-  int c[B], sum = 0;
+  int c[B];                            // from the top
+  if constexpr (B == 4) {
+    int4* at = reinterpret_cast<int4*>(&sh.hist[first]);
+    const int4 h = *at;
+    c[0] = h.w;
+    c[1] = h.z;
+    c[2] = h.y;
+    c[3] = h.x;
+    *at = make_int4(0, 0, 0, 0);
+  } else {
+    c[0] = sh.hist[first];
+    sh.hist[first] = 0;
+  }
+  int sum = 0;
 #pragma unroll
-  for (int k = 0; k < B; ++k) sum += c[k] = sh.hist[SIZE - 1 - ((int)threadIdx.x * B + k)];
-  int total;
-  int above = evict_scan(sum, sh.warp, total);
+  for (int k = 0; k < B; ++k) sum += c[k];
+  const int total = (int)__reduce_add_sync(0xffffffffu, (uint32_t)sum);
+  if (lane == 0) sh.warp[warp] = total;
+  __syncthreads();
+  int above = (int)__reduce_add_sync(0xffffffffu, lane < warp ? (uint32_t)sh.warp[lane] : 0u);
+  if (above < left && above + total >= left) {   // one warp's
+    int upto = sum;
 #pragma unroll
-  for (int k = 0; k < B; ++k) {
-    const int b = SIZE - 1 - ((int)threadIdx.x * B + k);
-    if (above < left && above + c[k] >= left) {
-      sh.digit = b;
-      sh.left = left - above;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += o;
     }
-    above += c[k];
-    sh.hist[b] = 0;
+    above += upto - sum;
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      if (above < left && above + c[k] >= left) {
+        sh.digit = first + B - 1 - k;
+        sh.left = left - above;
+        sh.same = c[k];
+      }
+      above += c[k];
+    }
   }
   __syncthreads();
+}
+
+// What follows the first digit, of the last kept one's weight `bits` and of those that agree `left` that stay: the rest of
+// it, and the kept positions.  HELD: all weights are in shared memory, with zeros behind them.
+template <bool HELD>
+__device__ __forceinline__ void evict_last(const EvictParams& p, EvictShared& sh, uint32_t* s_w, const float* mass,
+                                           int32_t* kept, int n, uint32_t bits, int left) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, lo = p.sinks, hi = n - p.recent;
+  auto weight = [&](int t) {
+    return HELD || t < p.cached ? s_w[t] : t < lo || t >= hi ? kEvictFixed : weight_order(mass[t]);
+  };
+  // four positions' weights and how many of them there are
+  auto four = [&](int f, uint32_t (&w)[4]) {
+    if (HELD || f + 4LL <= p.cached) {
+      const uint4 v = *reinterpret_cast<const uint4*>(s_w + f);
+      w[0] = v.x;
+      w[1] = v.y;
+      w[2] = v.z;
+      w[3] = v.w;
+      return 4;
+    }
+    const int there = max(min(n - f, 4), 0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = k < there ? weight(f + k) : 0;
+    return there;
+  };
+  // Those that agree; a list holds them where they are few.  A thread looks at 32 before it asks for places.
+  for (long long b0 = 0; b0 < n; b0 += 32 * kEvictThreads) {
+    uint32_t mask = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const long long at = b0 + k * 4 * kEvictThreads;
+      if (at >= n) break;
+      uint32_t w[4];
+      const int there = four((int)at + 4 * tid, w);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mask |= e < there && (w[e] ^ bits) < 1u << 20 ? 1u << (4 * k + e) : 0;
+    }
+    if (!__any_sync(0xffffffffu, mask != 0)) continue;
+    int upto = __popc(mask);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += o;
+    }
+    int to = 0;
+    if (lane == 31) to = *(volatile int*)&sh.n_list <= kEvictList ? atomicAdd(&sh.n_list, upto) : kEvictList;
+    to = __shfl_sync(0xffffffffu, to, 31) + upto - __popc(mask);
+    for (; mask && to < kEvictList; mask &= mask - 1, ++to) {
+      const int bit = __ffs(mask) - 1;
+      sh.list[to] = weight((int)b0 + (bit >> 2) * 4 * kEvictThreads + 4 * tid + (bit & 3));
+    }
+  }
+  __syncthreads();
+  const int n_list = sh.n_list;
+  if (n_list <= kEvictDirect) {        // few: the one that fewer than `left` exceed, and no fewer with its equals
+    if (tid < n_list) {
+      const uint32_t w = sh.list[tid];
+      int more = 0, same = 0;
+      for (int i = 0; i < n_list; i += 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(&sh.list[i]);
+        more += x.x > w;
+        same += x.x == w;
+        more += i + 1 < n_list && x.y > w;
+        same += i + 1 < n_list && x.y == w;
+        more += i + 2 < n_list && x.z > w;
+        same += i + 2 < n_list && x.z == w;
+        more += i + 3 < n_list && x.w > w;
+        same += i + 3 < n_list && x.w == w;
+      }
+      if (more < left && more + same >= left) {
+        sh.bits = w;
+        sh.left = left - more;
+        sh.same = same;
+      }
+    }
+    __syncthreads();
+    bits = sh.bits;
+    left = sh.left;
+  } else {
+    const bool listed = n_list <= kEvictList;
+#pragma unroll 1
+    for (int shift = 10; shift >= 0; shift -= 10) {
+      for (int i = tid; i < (listed ? n_list : n); i += kEvictThreads) {
+        const uint32_t w = listed ? sh.list[i] : weight(i);
+        if ((w >> (shift + 10)) == (bits >> (shift + 10))) atomicAdd(&sh.hist[(w >> shift) & 1023], 1);
+      }
+      evict_digit<1024>(sh, left);
+      bits |= (uint32_t)sh.digit << shift;
+      left = sh.left;
+    }
+  }
+  // The kept positions, in order, a run a warp.
+  const int run = (int)((n + kEvictStep - 1LL) / kEvictStep * 256), f0 = warp * run, f1 = (int)min((long long)f0 + run, (long long)n);
+  int stays = 0, equals = 0;
+  if (HELD && sh.same == left && bits != 0) {
+    // All of the threshold's weight stay: the run's positions take the place of its weights, then go to theirs.
+    uint32_t* own = s_w + f0;
+#pragma unroll 2
+    for (int f = 0; f < f1 - f0; f += 256) {
+      const uint4* at = reinterpret_cast<const uint4*>(own + f + 8 * lane);
+      const uint4 a = at[0], c = at[1];
+      const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+      int mine = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mine += w[k] >= bits ? 1 : 0;
+      int upto = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += o;
+      }
+      // (no further than weights that this and the lanes before have read)
+      uint32_t* to = own + stays + upto - mine;
+      const uint32_t t = (uint32_t)(f0 + f + 8 * lane);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (w[k] >= bits) *to++ = t + k;
+      stays += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (lane == 0) sh.warp[warp] = stays;
+    __syncthreads();
+    const int base = (int)__reduce_add_sync(0xffffffffu, lane < warp ? (uint32_t)sh.warp[lane] : 0u);
+    for (int i = lane; i < stays; i += 32) kept[base + i] = (int32_t)own[i];
+    return;
+  }
+  // Else a warp counts, and with the counts of the warps before writes its own.
+#pragma unroll 2
+  for (int f = f0; f < f1; f += 128) {
+    uint32_t w[4];
+    const int there = four(f + 4 * lane, w);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      stays += k < there && w[k] > bits;
+      equals += k < there && w[k] == bits;
+    }
+  }
+  stays = (int)__reduce_add_sync(0xffffffffu, (uint32_t)stays);
+  equals = (int)__reduce_add_sync(0xffffffffu, (uint32_t)equals);
+  if (lane == 0) {
+    sh.warp[warp] = stays;
+    sh.equal[warp] = equals;
+  }
+  __syncthreads();
+  stays = (int)__reduce_add_sync(0xffffffffu, lane < warp ? (uint32_t)sh.warp[lane] : 0u);
+  equals = (int)__reduce_add_sync(0xffffffffu, lane < warp ? (uint32_t)sh.equal[lane] : 0u);
+#pragma unroll 2
+  for (int f = f0; f < f1; f += 128) {
+    uint32_t w[4];
+    const int t = f + 4 * lane, there = four(t, w);
+    bool stay[4], same[4];
+    int own = 0;                       // that stay, and of equals in the upper half
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      stay[k] = k < there && w[k] > bits;
+      same[k] = k < there && w[k] == bits;
+      own += (stay[k] ? 1 : 0) + (same[k] ? 0x10000 : 0);
+    }
+    int upto = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += o;
+    }
+    const int total = __shfl_sync(0xffffffffu, upto, 31), own_before = upto - own;
+    int eq = equals + (own_before >> 16), at = stays + (own_before & 0xffff) + min(eq, left);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool stays_too = stay[k] || (same[k] && eq < left);   // of the equals, those that there is room for
+      if (stays_too) kept[at] = t + k;
+      at += stays_too ? 1 : 0;
+      eq += same[k] ? 1 : 0;
+    }
+    stays += total & 0xffff;
+    equals += total >> 16;
+  }
 }
 
 __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ __align__(16) uint32_t s_w[];   // weights by position, as far as they fit
   __shared__ EvictShared sh;
   const int tid = threadIdx.x, plane = blockIdx.x, s = plane / p.src.H_kv;
-#pragma unroll
-  for (int i = tid; i < kEvictBins; i += kEvictThreads) sh.hist[i] = 0;
+  static_assert(kEvictBins == 4 * kEvictThreads, "four bins a thread");
+  reinterpret_cast<int4*>(sh.hist)[tid] = make_int4(0, 0, 0, 0);
   if (tid == 0) sh.n_list = 0;
   griddep_launch_dependents();
   griddep_wait();
@@ -118,99 +300,52 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
   }
   // Those that stay whatever their weight count as heavier than all others; then keep of n stay.
   const int lo = p.sinks, hi = n - p.recent, held = min(n, p.cached);
-  auto weight = [&](int t) {
-    return t < p.cached ? s_w[t] : t < lo || t >= hi ? kEvictFixed : weight_order(mass[t]);
-  };
   for (int i = tid; i < lo + n - hi; i += kEvictThreads) {
     const int t = i < lo ? i : hi + i - lo;
     if (t < held) s_w[t] = kEvictFixed;
   }
   __syncthreads();
   if (tid == 0) atomicAdd(&sh.hist[kEvictBins - 1], lo + n - hi);
-  auto count = [&](int t, float x) {
-    const uint32_t w = weight_order(x);
-    if (t < held) s_w[t] = w;
-    atomicAdd(&sh.hist[w >> 20], 1);
-  };
-  int t = lo + tid;
-  for (; hi - t > 7 * kEvictThreads; t += 8 * kEvictThreads) {
-    float x[8];
+  constexpr int DEEP = 16;
+  uint32_t t = lo + tid;
+  if (n <= p.cached)
+    for (; (int)t + (DEEP - 1) * kEvictThreads < hi; t += DEEP * kEvictThreads) {   // whole batches, all held
+      float x[DEEP];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = mass[t + k * kEvictThreads];
+      for (int k = 0; k < DEEP; ++k) x[k] = mass[t + k * kEvictThreads];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) count(t + k * kEvictThreads, x[k]);
-  }
-  for (; t < hi; t += kEvictThreads) count(t, mass[t]);
-  int left = p.keep;
-  evict_digit<4096>(sh, left);
-  uint32_t bits = (uint32_t)sh.digit << 20;         // the last kept one's weight
-  left = sh.left;                                   // how many of those that agree stay
-  // Those that agree; a list holds them where they are few.
-  auto agree = [&](uint32_t w) {
-    if ((w >> 20) == (bits >> 20) && *(volatile int*)&sh.n_list <= kEvictList) {
-      const int at = atomicAdd(&sh.n_list, 1);
-      if (at < kEvictList) sh.list[at] = w;
-    }
-  };
-  for (int f = 4 * tid; f < held; f += 4 * kEvictThreads) {
-    const uint4 w = *reinterpret_cast<const uint4*>(s_w + f);   // (past held: of no account)
-    agree(w.x);
-    if (f + 1 < held) agree(w.y);
-    if (f + 2 < held) agree(w.z);
-    if (f + 3 < held) agree(w.w);
-  }
-  for (int f = held + tid; f < n; f += kEvictThreads) agree(weight(f));
-  __syncthreads();
-  const int n_list = sh.n_list;
-  const bool listed = n_list <= kEvictList;
-#pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    const int shift = pass == 0 ? 10 : 0, up = shift + 10;
-    for (int i = tid; i < (listed ? n_list : n); i += kEvictThreads) {
-      const uint32_t w = listed ? sh.list[i] : weight(i);
-      if ((w >> up) == (bits >> up)) atomicAdd(&sh.hist[(w >> shift) & 1023], 1);
-    }
-    evict_digit<1024>(sh, left);
-    bits |= (uint32_t)sh.digit << shift;
-    left = sh.left;
-  }
-  // the kept positions, in order: every thread takes a run of 8
-  constexpr int RUN = 8;
-  int stays_before = 0, equals_before = 0;
-  for (long long b0 = 0; b0 < n; b0 += RUN * kEvictThreads) {
-    const int f = (int)b0 + tid * RUN;
-    uint32_t above = 0, equal = 0;
-    if (f <= held - RUN) {
-      const uint4 a = reinterpret_cast<const uint4*>(s_w + f)[0], c = reinterpret_cast<const uint4*>(s_w + f)[1];
-      const uint32_t w[RUN] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
-#pragma unroll
-      for (int k = 0; k < RUN; ++k) {
-        above |= w[k] > bits ? 1u << k : 0;
-        equal |= w[k] == bits ? 1u << k : 0;
-      }
-    } else {
-      for (int k = 0; k < RUN && k < n - f; ++k) {
-        const uint32_t w = weight(f + k);
-        above |= w > bits ? 1u << k : 0;
-        equal |= w == bits ? 1u << k : 0;
+      for (int k = 0; k < DEEP; ++k) {
+        const uint32_t w = weight_order(x[k]);
+        s_w[t + k * kEvictThreads] = w;
+        atomicAdd(&sh.hist[w >> 20], 1);
       }
     }
-    // both counts in one scan (16 bits each hold RUN * threads)
-    int total;
-    const int base = evict_scan(__popc(above) | __popc(equal) << 16, sh.warp, total);
-    const int eq = equals_before + (base >> 16);
-    int at = stays_before + (base & 0xffff) + min(eq, left);
-    // of the run's equals, those that there is room for
-    uint32_t room = equal;
-    for (int over = __popc(equal) - max(left - eq, 0); over > 0 && room; --over) room &= ~(1u << (31 - __clz(room)));
-    for (uint32_t stay = above | room; stay; stay &= stay - 1) kept[at++] = f + __ffs(stay) - 1;
-    stays_before += total & 0xffff;
-    equals_before += total >> 16;
+  for (; t < (uint32_t)hi; t += DEEP * kEvictThreads) {
+    const int room = (hi - (int)t + kEvictThreads - 1) / kEvictThreads;   // of the batch, those that there are
+    float x[DEEP];
+#pragma unroll
+    for (int k = 0; k < DEEP; ++k) x[k] = k < room ? mass[t + k * kEvictThreads] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < DEEP; ++k) {
+      if (k >= room) break;
+      const uint32_t w = weight_order(x[k]), at = t + k * kEvictThreads;
+      if (at < (uint32_t)held) s_w[at] = w;
+      atomicAdd(&sh.hist[w >> 20], 1);
+    }
   }
+  // (what lies behind the last position up to where it is looked at: the least weight, which never finds room)
+  for (int t = n + tid; n <= p.cached && t < (n + kEvictStep - 1) / kEvictStep * kEvictStep; t += kEvictThreads) s_w[t] = 0;
+  evict_digit<kEvictBins>(sh, p.keep);
+  const uint32_t bits = (uint32_t)sh.digit << 20;   // the last kept one's weight
+  const int left = sh.left;                         // how many of those that agree stay
+  if (n <= p.cached)
+    evict_last<true>(p, sh, s_w, mass, kept, n, bits, left);
+  else
+    evict_last<false>(p, sh, s_w, mass, kept, n, bits, left);
 }
 
 // Copies kept positions' K and V: a group of HD / 8 lanes a row of both.  As many warps as fit keep HBM busy, at one row
-// a thread: 8 x 8192 rows of 8 heads of 128 with the selection 108 us, two rows in flight 113, four 117, eight 132.
+// a thread: 8 x 8192 rows of 8 heads of 128 with the selection of then 108 us, two rows in flight 113, four 117, eight 132.
 template <int HD>
 __global__ void __launch_bounds__(256, 8) evict_copy_kernel(const __grid_constant__ EvictParams p) {
   constexpr int L = HD / 8, PER = 256 / L;
@@ -287,7 +422,7 @@ extern "C" dllm_status dllm_op_kv_paged_evict(const dllm_kv_paged* src, const dl
   p.sinks = sinks;
   p.recent = recent;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  p.cached = (int)std::min<long long>((std::min(p.src.positions, p.mass_rs) + 7) / 8 * 8, kEvictMost);
+  p.cached = (int)std::min<long long>((std::min(p.src.positions, p.mass_rs) + kEvictStep - 1) / kEvictStep * kEvictStep, kEvictMost);
   OP_CK(op_smem_once(reinterpret_cast<const void*>(evict_select_kernel), kEvictMost * 4));
   OP_CK(op_launch(evict_select_kernel, dim3((unsigned)planes), dim3(kEvictThreads), (size_t)p.cached * 4, st, 1, p));
   OP_CK(src->hd == 64 ? launch_evict_copy<64>(p, planes, st) : launch_evict_copy<128>(p, planes, st));

@@ -484,6 +484,14 @@ EVICT = [
     (1, 2, 64, 128, 256, [40000], 5000, 4, 1000, "bf16", "few"),
     (1, 1, 64, 128, 256, [70001], 64, 0, 0, "bf16", "random"),
     (2, 2, 64, 16, 16, [50, 20], 64, 4, 4, "bf16", "random"),
+    # the least kept is a NaN; weights of one leading part, few, many and too many to be listed; ends of what is held
+    (1, 2, 64, 16, 16, [900], 400, 2, 3, "bf16", "nan"),
+    (2, 2, 64, 16, 16, [128, 129], 100, 0, 7, "bf16", "band"),
+    (2, 1, 64, 16, 16, [2048, 2049], 777, 1, 0, "bf16", "band"),
+    (2, 1, 64, 128, 128, [8192, 8193], 4096, 0, 9, "f16", "band"),
+    (2, 1, 64, 256, 128, [49152, 49153], 3000, 4, 5, "bf16", "band"),
+    (2, 1, 64, 256, 128, [49152, 49153], 3000, 4, 5, "bf16", "random"),
+    (1, 1, 64, 256, 256, [49160], 49153, 0, 0, "bf16", "few"),
 ]
 
 
@@ -496,6 +504,8 @@ def test_evict(torch, b, Hkv, hd, ps, ps2, lens, keep, sinks, recent, dtype, wei
     m = np.exp(2 * rng.standard_normal((b, Hkv, max(lens) + 3))).astype(np.float32)
     if weights == "equal":
         m[:] = 0.25
+    if weights == "band":
+        m = rng.uniform(1.0, 1.1, m.shape).astype(np.float32)
     if weights == "few":                                  # many ties, zeros of both signs among them
         m = rng.choice(np.array([0.0, -0.0, 0.5, 1.0, 1e-42], dtype=np.float32), m.shape)
     if weights == "nan":
