@@ -21,8 +21,8 @@
 // 4096 rows of 126464 in bf16, 20 alternatives: 172 us, 6.0 TB/s (none: 157, 50: 193; 2048 rows of float32: 156); 32 rows,
 // 5 alternatives: 12.4 us, of which a chain of reductions and a cluster's join are the most; 257 rows of 32001 in float32:
 // 12.8 us.  Beside HBM the issue slots bound it: the warps that work out results take them from those that stream.  At
-// an earlier step (184 us) three CTAs an SM with 56 registers a thread took 212, 384 streaming threads 189.  A second
-// team for the results, rows in turn, takes 4096 rows of 32000 from 95 us to 88, but this case to 184.
+// an earlier step (184 us) three CTAs an SM with 56 registers a thread took 212, 384 streaming threads 189.  A second team of
+// warps for the results, rows in turn, takes 184 here.
 #include <algorithm>
 #include <type_traits>
 
@@ -887,10 +887,14 @@ cudaError_t launch_logprobs(LogprobsParams& p, cudaStream_t st) {
                    p.cluster, p);
 }
 
-// Streaming threads: few where a row is short (8192 elements are 8 vectors each of 128 threads).
+// Streaming threads: few where a row is short (8192 elements are 8 vectors each of 128 threads), or where many rows of no
+// more than 128 KB wait for their results: four CTAs an SM work out as many rows at once (4096 rows of bf16, 20
+// alternatives: 12000 elements 58 us against 86, 32000 77 against 104, 65536 106 against 115, but 126464 187 against 173;
+// 600 rows of 32000 15.4 against 18.3, 257 rows of them in float32 14.8 against 12.8).
 template <typename E>
 cudaError_t launch_logprobs(LogprobsParams& p, cudaStream_t st) {
-  return p.vocab <= 8192 ? launch_logprobs<E, 128>(p, st) : launch_logprobs<E, 256>(p, st);
+  const bool many = p.rows > 2 * op_device_sms() && (long long)p.vocab * (long long)sizeof(typename E::T) <= 128 * 1024;
+  return p.vocab <= 8192 || many ? launch_logprobs<E, 128>(p, st) : launch_logprobs<E, 256>(p, st);
 }
 
 }  // namespace

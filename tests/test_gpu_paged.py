@@ -616,7 +616,9 @@ LOGITS = [(1, 1, 1, "f32", 1.0, 0), (3, 2, 2, "bf16", 2.0, 1), (5, 100, 64, "f16
           (2, 4096, 20, "f32", 1.3, 0), (3, 32001, 20, "f32", 1 / 0.7, 3), (2, 126464, 50, "bf16", 1.0, 0),
           (33, 5003, 0, "f16", 1.0, 1), (2, 300007, 64, "bf16", 1.0, 5), (310, 9001, 7, "bf16", 1.0, 1),
           (40, 40000, 5, "f16", 1.0, 0), (153, 65003, 30, "f32", 1.0, 1), (90, 70001, 64, "bf16", 0.5, 1), (700, 1023, 3, "bf16", 1.0, 2),
-          (400, 6001, 64, "f32", 1.0, 1)]
+          (400, 6001, 64, "f32", 1.0, 1),
+          # many rows: fewer threads a row
+          (650, 20011, 20, "bf16", 1.0, 0), (310, 30001, 64, "f32", 1.0, 5), (1300, 8193, 7, "f16", 0.7, 2)]
 
 
 @pytest.mark.parametrize("rows,vocab,top,dtype,scale,pad", LOGITS)
@@ -633,9 +635,7 @@ def test_token_logprobs(torch, rows, vocab, top, dtype, scale, pad):
     logprobs_check(f64(buf)[:, :vocab], targets, top, np.float32(scale).astype(np.float64), got)
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("vocab", [700, 40007])
-def test_token_logprobs_ties_and_tokens_that_cannot_come(torch, vocab, dtype):
+def odd_rows(vocab):
     rng = np.random.default_rng(vocab)
     x = rng.standard_normal((13, vocab))
     x[0] = 0.0                                             # all alike
@@ -654,10 +654,27 @@ def test_token_logprobs_ties_and_tokens_that_cannot_come(torch, vocab, dtype):
     x[10, ::2] = -0.0
     x[11, :] = np.where(np.arange(vocab) % 512 < 8, 5.0, x[11])        # one thread's tokens are the largest
     x[12, 256:] = -1e30
+    return x, [0, 77, 5, 12, 0, 7, 0, 3, vocab - 1, vocab - 1, -1, 0, 300]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("vocab", [700, 40007])
+def test_token_logprobs_ties_and_tokens_that_cannot_come(torch, vocab, dtype):
+    x, targets = odd_rows(vocab)
     buf = dev(torch, x.astype(np.float32)).to(dt(torch, dtype))
-    targets = [0, 77, 5, 12, 0, 7, 0, 3, vocab - 1, vocab - 1, -1, 0, 300]
     got = logprobs(torch, buf, dtype, targets, 50)
     logprobs_check(f64(buf), targets, 50, 1.0, got)
+
+
+@pytest.mark.parametrize("dtype,top", [("bf16", 5), ("f32", 50)])
+def test_token_logprobs_of_many_odd_rows(torch, dtype, top):
+    """Every kind of row behind every other in one call, more rows than run at once."""
+    x, targets = odd_rows(16001)
+    order = np.random.default_rng(4).integers(0, 13, 1300)
+    buf = dev(torch, x.astype(np.float32)).to(dt(torch, dtype))
+    rows = buf[torch.from_numpy(order).cuda()]
+    targets = [targets[k] for k in order]
+    logprobs_check(f64(rows), targets, top, 1.0, logprobs(torch, rows, dtype, targets, top))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
