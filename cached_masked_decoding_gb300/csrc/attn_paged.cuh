@@ -18,7 +18,7 @@
 // 39 us (21 us of keys).
 //
 // Softmax runs with one key a thread and RW rows in its registers.  A row's reference is the maximum over the first
-// tile of the CTA's part; it follows when a score exceeds it by 2^20 (2^12 in f16, whose probabilities end at 65504),
+// tile of the CTA's part that has a key to see (tiles whose positions all lie on no page have none); it follows when a score exceeds it by 2^20 (2^12 in f16, whose probabilities end at 65504),
 // which one vote a tile finds out; else the warps meet at no barrier.  Sums l are kept per key lane and joined once a
 // part.
 //
@@ -446,6 +446,7 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
         float* m_at = s_ref + (w.part & 1) * N;
         const uint32_t ocol = trow + C::O_COL + (w.part & 1) * 2 * N;
         if (w.part >= 2) wait(&ofree[w.part & 1], (w.part >> 1) - 1);   // the part before the last is out
+        bool unset = true;                                // no key of the part seen so far, by any of the threads
         for (int t = 0; t < w.nt; ++t, ++tt) {
           const int b = tt & 1, pb = C::P_BUFS == 2 ? b : 0;
           const bool seen = (unsigned)page < (unsigned)p.c.pages;
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
               if (row0 + j < p.nz) *reinterpret_cast<float4*>(zs + j) = make_float4(z[j], z[j + 1], z[j + 2], z[j + 3]);
           }
           float top = -INFINITY;
-          if (t > 0) {
+          if (!unset) {
 #pragma unroll
             for (int j = 0; j < RW; j += 4) {
               const float4 m = *reinterpret_cast<const float4*>(m_at + row0 + j);
@@ -478,8 +479,8 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
 #pragma unroll
             for (int j = 0; j < RW; ++j) top = fmaxf(top, z[j]);
           }
-          if (named_bar_or(2, C::SOFT, t == 0 || top > F::kSlack)) {
-            // references: the first tile's, or higher ones
+          if (named_bar_or(2, C::SOFT, unset ? seen : top > F::kSlack)) {
+            // references: those of the first tile with a key (until then sums and output are zeros), or higher ones
 #pragma unroll
             for (int j = 0; j < RW; ++j) {
               const int r = __reduce_max_sync(0xffffffffu, order_of(z[j]));
@@ -488,14 +489,14 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
             named_bar_sync(2, C::SOFT);
             if (tid < N) {
               float up = fmaxf(fmaxf(s_wmax[tid], s_wmax[N + tid]), fmaxf(s_wmax[2 * N + tid], s_wmax[3 * N + tid]));
-              if (!(up > -INFINITY) || (t > 0 && up < 0.0f)) up = 0.0f;
+              if (!(up > -INFINITY) || (!unset && up < 0.0f)) up = 0.0f;
               s_up[tid] = up;
-              m_at[tid] = t == 0 ? up : m_at[tid] + up;
+              m_at[tid] = unset ? up : m_at[tid] + up;
             }
             named_bar_sync(2, C::SOFT);
 #pragma unroll
             for (int j = 0; j < RW; ++j) z[j] -= s_up[row0 + j];
-            if (t > 0) {
+            if (!unset) {
               wait(&pvdone[(tt - 1) & 1], (tt - 1) >> 1);
               tc_fence_after();
               float f[RW], o[RW];
@@ -512,6 +513,7 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
                 tmem_st<RW>(ocol + part * N + row0, o);
               }
             }
+            unset = false;
             // (the maxima are read again only behind the next vote)
           }
           if (C::P_BUFS == 1 && tt > 0) wait(&pvdone[(tt - 1) & 1], (tt - 1) >> 1);
@@ -698,8 +700,9 @@ __device__ __forceinline__ int paged_slot(int first, int k) { return k == 0 ? fi
 __device__ __forceinline__ int paged_parts(int first, int last) { return (last >> 1) - (first >> 1) + 1; }
 
 // The second kernel: joins split items, and adds what every key received.  The first p.joins CTAs, rows of the item
-// that goes on from one CTA of the kernel before to the next: weights l 2^m over their sum (l is 1 at least, 2^51 at most,
-// and m the part's reference: what a weight loses to underflow is nothing beside the largest).  The others, runs
+// that goes on from one CTA of the kernel before to the next: weights l 2^m over their sum (l is 0 without a key,
+// when m means nothing, else 1 at least, 2^51 at most, and m the part's reference: what a weight loses to underflow is nothing
+// beside the largest).  The others, runs
 // of keys of a cached head: the rows' probabilities from their scores (base 2) and log sums.
 template <typename F, int HD, bool MASS>
 __global__ void __launch_bounds__(128, MASS ? 8 : 12) attn_paged_finish_kernel(const __grid_constant__ AttnPagedParams p, int N) {

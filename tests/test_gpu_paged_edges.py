@@ -1,0 +1,86 @@
+"""The operators of paged decoding where their numerics are at an end: keys on no page in front of a walk, weights far
+apart, long rows.  Against the plain 64-bit restatement (paged_ref); half a rounding step is 2^-8 of the value in bf16,
+2^-11 in f16, 2^-24 in float32.
+"""
+import math
+
+import numpy as np
+import pytest
+
+import paged_ref as ref
+from test_gpu_paged import HALF, TINY, U, Pages, attend, dev, dt, f64, torch  # noqa: F401 (torch: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+# --------------------------------------------------------------------------- attention
+
+def attention_close(c, q, lens, out, mass=None):
+    """out and mass (which began as zeros) against 64 bits; a probability counts to its own size however small it is."""
+    b, R, H, hd = q.shape
+    G = H // c.hkv
+    kp, vp = f64(c.k), f64(c.v)
+    for s in range(b):
+        n = int(lens[s])
+        k, there = ref.gather(kp, c.tab[s], n, c.ps)
+        v, _ = ref.gather(vp, c.tab[s], n, c.ps)
+        want, m, pv, sv, sk = ref.attention(f64(q[s]), k, v, there, hd ** -0.5)
+        # a score: a float32 sum of hd exact products (each within 2^-23 of the sum of their sizes, the tensor core
+        # truncates), scaled and put against its reference: 4 roundings of it; p = 2^z within 2^-22
+        dz = (hd + 8) * 2.0 ** -23 * sk + 2.0 ** -22
+        # p in two halves: 2^-16 of it (bf16); 2^-22 of it, or 2^-45 of the row's largest (f16).  Sums of n terms in
+        # trees and tiles, on both sides of the quotient
+        halves = 2.0 ** -16 * pv if c.dtype == "bf16" else 2.0 ** -22 * pv + 2.0 ** -45 * sv
+        tol = (2 * dz + (n / 16 + 24) * U) * pv + halves + HALF[c.dtype] * 1.01 * np.abs(want) + TINY[c.dtype]
+        err = np.abs(f64(out[s]) - want)
+        assert (err <= tol).all(), (s, float((err / np.maximum(tol, 1e-300)).max()))
+        if mass is not None:
+            got = f64(mass[s])
+            tol = m * (2 * float(dz.max()) + (n / 16 + 40 + R * G + 4) * U) + 1e-37
+            assert (np.abs(got[:, :n] - m) <= tol).all(), s
+            assert (got[:, n:] == 0).all()
+
+
+def at_level(torch, c, q, lens, level):
+    """Adds to the first dim of all keys and queries what takes every score to about `level` (hd^-0.5 is the scale)."""
+    a = math.sqrt(abs(level)) * c.hd ** 0.25
+    for s, n in enumerate(lens):
+        t = np.arange(n)
+        page, slot = (torch.from_numpy(x).cuda() for x in (c.tab[s, t // c.ps].astype(np.int64), t % c.ps))
+        c.k[page, :, slot, 0] = a
+    q[..., 0] = math.copysign(a, level)
+
+
+HOLES = [
+    # b, R, H, H_kv, hd, page, positions, no pages among them (first positions; "some": half of all, at random)
+    (1, 1, 8, 2, 64, 16, 512, 128),                        # items stay whole
+    (2, 2, 4, 1, 128, 32, 400, 300),
+    (1, 1, 4, 1, 64, 16, 4000, 2048),                      # the front parts see nothing, one starts in the hole
+    (2, 1, 8, 8, 64, 128, 8192, "some"),                   # parts that start in a hole anywhere
+    (2, 4, 16, 4, 128, 128, 4096, "some"),                 # 16 rows of a cached head, then 32 and 64
+    (2, 8, 16, 4, 128, 256, 8192, "some"),
+    (2, 16, 8, 2, 64, 256, 8192, "some"),
+]
+
+
+@pytest.mark.parametrize("with_mass", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("level", [-16.0, -25.0, -60.0, -200.0])
+@pytest.mark.parametrize("b,R,H,Hkv,hd,ps,n,holes", HOLES)
+def test_scores_below_zero_behind_keys_on_no_page(torch, b, R, H, Hkv, hd, ps, n, holes, level, dtype, with_mass):
+    """A window's first pages were given back, or pages anywhere: the others' weights are as if nothing else had been."""
+    rng = np.random.default_rng(n + R + int(-level))
+    most = -(-n // ps)
+    c = Pages(torch, rng, b, Hkv, hd, dtype, ps, most).fill(rng, [n] * b)
+    q = dev(torch, rng.standard_normal((b, R, H, hd)).astype(np.float32)).to(dt(torch, dtype))
+    at_level(torch, c, q, [n] * b, level)
+    if holes == "some":
+        gone = rng.random((b, most)) < 0.5
+        gone[:, 0], gone[:, -1] = True, False
+    else:
+        gone = np.broadcast_to(np.arange(most) * ps < holes, (b, most))
+    assert gone.any() and not gone.all(1).any()
+    c.tab[gone] = -1
+    mass = torch.zeros(b, Hkv, most * ps, device="cuda") if with_mass else None
+    out = attend(torch, c, q, [n] * b, mass=mass)
+    attention_close(c, q, [n] * b, out, mass)
