@@ -4,12 +4,17 @@
 //   S^T[key][row] = K Q^T,      O^T[dim][row] += V^T P^T        (tcgen05, kind::f16)
 // with N = 8, 16, 32 or 64 rows as the narrow operand (8: scores in 16 columns).  V is read MN-major from its
 // TMA tile.  A probability is the sum of two values of the cache's type, hi and lo, side by side in 2 N columns of one
-// product: one rounding of P to bf16 alone is as large an error as the output's own rounding.
+// product: one rounding of P to bf16 alone is as large an error as the output's own rounding.  f16 ends at 2^-24 and at
+// 65504: there the reference lies 2^8 under the maximum, probabilities go up to 2^15, and lo is 2^12 times what hi left
+// (half a step under 2^15 at most, 8: so 2^15 again), which the output's sum of both takes back.  P is then exact to
+// 2^-22 of itself, or half of 2^-24 / 2^12 where lo is subnormal: 2^-45 of the maximum.  (lo as it is and a reference at
+// the maximum lost what lies 2^24 under it: 8191 keys 17 nats below one with small values gave an output a third off.)
 //
 // Bound by HBM: 4 hd bytes a key and cached head.  So the work is shared out evenly whatever the lengths: the CTAs, one
 // an SM (two for 16 rows and fewer), take equal runs of the tiles of the (sequence, row tile, cached head) items laid
-// end to end, and a CTA's ring of TMA tiles runs on across the items' borders.  An item that lies in several CTAs leaves its parts - normalised outputs
-// with their reference m and sum l - in the workspace, and a second small kernel joins them.
+// end to end, and a CTA's ring of TMA tiles runs on across the items' borders.  An item that lies in several CTAs leaves
+// its parts - normalised outputs with their reference m and sum l - in the workspace, and a second small kernel joins
+// them.
 //
 // hd 128, bf16: one token of 64 sequences of 4 to 8 thousand keys, 32 heads on 8: 238 us, 6.8 TB/s (the measured copy
 // rate); one of 131071 keys: 86 us, 6.2 TB/s; 32 rows of 16 sequences of 32 heads, 2048 keys: 95 us, 5.8 TB/s; of one, 768
@@ -18,9 +23,9 @@
 // 39 us (21 us of keys).
 //
 // Softmax runs with one key a thread and RW rows in its registers.  A row's reference is the maximum over the first
-// tile of the CTA's part that has a key to see (tiles whose positions all lie on no page have none); it follows when a score exceeds it by 2^20 (2^12 in f16, whose probabilities end at 65504),
-// which one vote a tile finds out; else the warps meet at no barrier.  Sums l are kept per key lane and joined once a
-// part.
+// tile of the CTA's part that has a key to see (tiles whose positions all lie on no page have none; f16: 2^8 under it).
+// It follows when a probability would exceed 2^20 (f16: 2^15), which one vote a tile finds out; else the warps meet at no
+// barrier.  Sums l are kept per key lane and joined once a part.
 //
 //   warp 0     TMA: the pages of a tile, a lane each, K and V through a ring of 128-key slots
 //   warp 1     MMAs, issued by one lane: scores up to two tiles ahead of the products, across items too
@@ -68,7 +73,8 @@ constexpr int kPagedKeys = 128;
 struct PairBf16 {
   using E = ElemBf16;
   static constexpr uint32_t kFormat = 1;
-  static constexpr float kSlack = 20.0f;
+  static constexpr float kSlack = 20.0f, kBase = 0.0f;   // log2 of the largest probability, and of one at the maximum
+  static constexpr float kLo = 1.0f;                     // what lo is multiplied by
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
@@ -80,7 +86,8 @@ struct PairBf16 {
 struct PairF16 {
   using E = ElemF16;
   static constexpr uint32_t kFormat = 0;
-  static constexpr float kSlack = 12.0f;
+  static constexpr float kSlack = 15.0f, kBase = 8.0f;
+  static constexpr float kLo = 4096.0f;
   static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack_f16x2(a, b); }
   static __device__ __forceinline__ float2 unpack(uint32_t w) { return f16x2_to_f32(w); }
 };
@@ -489,7 +496,8 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
             named_bar_sync(2, C::SOFT);
             if (tid < N) {
               float up = fmaxf(fmaxf(s_wmax[tid], s_wmax[N + tid]), fmaxf(s_wmax[2 * N + tid], s_wmax[3 * N + tid]));
-              if (!(up > -INFINITY) || (!unset && up < 0.0f)) up = 0.0f;
+              up = up > -INFINITY ? up - F::kBase : 0.0f;
+              if (!unset && up < 0.0f) up = 0.0f;
               s_up[tid] = up;
               m_at[tid] = unset ? up : m_at[tid] + up;
             }
@@ -530,7 +538,7 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
               l_sum[j + 2 * e + 1] += c;
               hi[e] = F::pack(a, c);
               const float2 h = F::unpack(hi[e]);
-              lo[e] = F::pack(a - h.x, c - h.y);
+              lo[e] = F::pack((a - h.x) * F::kLo, (c - h.y) * F::kLo);
             }
             *reinterpret_cast<uint4*>(pp + swizzled<C::P_ROW>(key_l, (row0 + j) >> 3)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4*>(pp + (C::P_PARTS == 1 ? swizzled<C::P_ROW>(key_l, (N + row0 + j) >> 3)
@@ -655,7 +663,7 @@ __global__ void __launch_bounds__(AttnPagedCfg<HD, N>::THREADS, AttnPagedCfg<HD,
             float o2[8];
             tmem_ld8x2(ocol + n, ocol + N + n, o, o2);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] += o2[j];
+            for (int j = 0; j < 8; ++j) o[j] = fmaf(o2[j], 1.0f / F::kLo, o[j]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const float f = s_inv[n + j];
@@ -700,8 +708,8 @@ __device__ __forceinline__ int paged_slot(int first, int k) { return k == 0 ? fi
 __device__ __forceinline__ int paged_parts(int first, int last) { return (last >> 1) - (first >> 1) + 1; }
 
 // The second kernel: joins split items, and adds what every key received.  The first p.joins CTAs, rows of the item
-// that goes on from one CTA of the kernel before to the next: weights l 2^m over their sum (l is 0 without a key,
-// when m means nothing, else 1 at least, 2^51 at most, and m the part's reference: what a weight loses to underflow is nothing
+// that goes on from one CTA of the kernel before to the next: weights l 2^m over their sum (l is 0 without a key, when
+// m means nothing; else 1 at least, 2^51 at most, and m the part's reference: what a weight loses to underflow is nothing
 // beside the largest).  The others, runs
 // of keys of a cached head: the rows' probabilities from their scores (base 2) and log sums.
 template <typename F, int HD, bool MASS>

@@ -671,8 +671,9 @@ dllm_status dllm_op_qk_norm_rope_paged(const dllm_kv_paged* cache, const void* q
  * used, whatever its bytes.  q, out: of the cache's type, [b*R][H][hd], 16-byte
  * aligned, rows q_row_stride / out_row_stride elements apart (0: dense; else a
  * multiple of 8).  scale: > 0, at most 1e38.  Scores, statistics and sums are float32; a probability
- * enters the value product as the sum of two halves of the cache's type (16
- * bits of it in bf16).  K, V and q are finite, and so are the scores.
+ * enters the value product as the sum of two values of the cache's type: to
+ * 2^-16 of it in bf16; in f16 to 2^-22 of it, or 2^-45 of the row's largest.
+ * K, V and q are finite, and so are the scores.
  *   mass (nullable): device float32 [b][H_kv][mass_stride] (0: max_pages *
  * page_size); mass[s][g][t] += the sum of p_t over the R rows and the heads of
  * g, for t < lens[s]; the rest stays as it was, and weights of positions from

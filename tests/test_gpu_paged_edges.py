@@ -84,3 +84,26 @@ def test_scores_below_zero_behind_keys_on_no_page(torch, b, R, H, Hkv, hd, ps, n
     mass = torch.zeros(b, Hkv, most * ps, device="cuda") if with_mass else None
     out = attend(torch, c, q, [n] * b, mass=mass)
     attention_close(c, q, [n] * b, out, mass)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("where", [0, 130, 8191])
+@pytest.mark.parametrize("above,values", [(16.0, 1.0), (17.5, 1.0), (20.0, 30.0), (24.0, 1000.0)])
+@pytest.mark.parametrize("R", [1, 16])
+def test_many_light_keys_beside_a_heavy_one(torch, dtype, where, above, values, R):
+    """One key takes nearly all of the weight and has values of next to nothing: the output is the others'."""
+    rng = np.random.default_rng(int(above) + where)
+    n, hd = 8192, 64
+    c = Pages(torch, rng, 1, 1, hd, dtype, 64, 128).fill(rng, [n])
+    a = math.sqrt(above) * hd ** 0.25
+    t = np.arange(n)
+    page, slot = (torch.from_numpy(x).cuda() for x in (c.tab[0, t // 64].astype(np.int64), t % 64))
+    c.k[page, 0, slot] = c.k[page, 0, slot] * 0.25
+    c.k[page, 0, slot, 0] = 0.0
+    c.k[page[where], 0, slot[where], 0] = a
+    c.v[page, 0, slot] = (c.v[page, 0, slot].float() * 0.1 + 1.0).mul(values).to(c.v.dtype)
+    c.v[page[where], 0, slot[where]] = 0.0
+    q = dev(torch, (0.25 * rng.standard_normal((1, R, 2, hd))).astype(np.float32)).to(dt(torch, dtype))
+    q[..., 0] = a
+    out = attend(torch, c, q, [n])
+    attention_close(c, q, [n], out)
