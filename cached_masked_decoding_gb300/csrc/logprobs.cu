@@ -8,9 +8,10 @@
 //
 // Bound by HBM: the logits are read once.  A CTA takes row after row (or a cluster of up to 8 one row, where rows are
 // few).  One warp copies the rows into a ring in shared memory, past the end of a row too; eight stream them: every
-// thread keeps the largest of its elements m and, relative to it, S and W of them all, leaves them in shared memory and
-// goes on to the next row.  Four warps work out a row's results meanwhile (the same threads one after the other took 212
-// us for the case below, with loads into registers and results apart 217).
+// thread keeps the largest of its elements m and, relative to it, S and W of them all (in float32 chains of 256 terms, each
+// joined to those before), leaves them in shared memory and goes on to the next row.  Four warps work out a row's results
+// meanwhile (the same threads one after the other took 212 us for the case below, with loads into registers and results
+// apart 217).
 // What needs elements again is a few threads' worth, which lies in L2 still:
 //   - the alternatives are among the elements of units whose largest is no less than the top-th largest of 128 group
 //     maxima (a lower bound of the top-th largest element): for 20 of 126464 about 22 units of 32 elements.  Elements
@@ -49,6 +50,7 @@ constexpr int kLogCluster = 8;
 constexpr int kLogAhead = 4;         // vectors of a thread in a chunk of the ring (a batch)
 constexpr int kLogRest = 128;        // threads that work out a row's results
 
+// MAIN: streaming threads
 template <int MAIN>
 struct LogCfg {
   static constexpr int THREADS = MAIN + kLogRest + 32;
@@ -60,6 +62,7 @@ constexpr int kLogGroups = 128;
 constexpr int kLogFewTop = 24;
 constexpr int kLogUnits = 16;        // of a thread's batches at most, each with a largest element of its own (and one for the rest)
 constexpr int kMostUnits = 512;      // units that are looked through again, before all are
+constexpr int kLogChain = 256;       // additions of a chain of sums at most, before it joins the chains before
 
 static __device__ int g_logprobs_err[1];
 
@@ -204,6 +207,22 @@ struct LogSums {
       }
     }
     return top;
+  }
+  // What the sums are relative to m c2 itself, with t's, of no larger an m, joined where there are any; the chain starts
+  // anew.
+  __device__ __forceinline__ void fold(float& t_m, float& t_S, float& t_W, bool any, float c2) {
+    if (plain) scale(rise(m, 0.0f, false, c2));
+    const float2 s = f32x2_get(S), w = f32x2_get(W);
+    float S_all = s.x + s.y, W_all = w.x + w.y;
+    if (any) {
+      const float d = t_m == m ? 0.0f : max_nan((t_m - m) * c2, -200.0f), f = exp2_fast(d);
+      W_all += (t_W + t_S * d) * f;
+      S_all += t_S * f;
+    }
+    t_m = m;
+    t_S = S_all;
+    t_W = W_all;
+    S = W = 0;
   }
   __device__ __forceinline__ void one(float x, float c2) {
     const float d = max_nan(plain ? fmaf(x, c2, -ref) : (x - (m == -INFINITY ? 0.0f : m)) * c2, -200.0f);
@@ -382,8 +401,8 @@ __device__ int equals_in_order(const LogRow<E, MAIN>& row, LogShared<MAIN>& sh, 
   return min(found, need);
 }
 
-// A row's results from the streaming threads' sums in buffer b; by kLogRest threads.  false: not this CTA's to give.
-template <typename E, int MAIN>
+// A row's results from the streaming threads' sums in buffer b; by kLogRest threads.
+template <typename E, int MAIN, bool LONG>
 __device__ __forceinline__ void row_results(const LogprobsParams& p, LogShared<MAIN>& sh, const LogRow<E, MAIN>& row, int r,
                                             int b, int tid, int rank, int ranks, float c2, const float* unit) {
   constexpr int VE = LogRow<E, MAIN>::VE, EACH = MAIN / kLogRest;
@@ -519,13 +538,24 @@ __device__ __forceinline__ void row_results(const LogprobsParams& p, LogShared<M
       s += e;
       w += d * e;
     };
+    float s_all = 0.0f, w_all = 0.0f;  // of the chains before, of 32 vectors each
+    int n = 0;
     for (int v = row.v0 + owner + lane * MAIN; v < row.v1; v += 32 * MAIN) {
       float e[VE];
       row.floats(row.load(v), e);
 #pragma unroll
       for (int i = 0; i < VE; ++i) other(e[i]);
+      if (LONG && (++n & 31) == 0) {
+        s_all += s;
+        w_all += w;
+        s = w = 0.0f;
+      }
     }
     if (lane == 0 && owner < row.extra) other(E::get(row.x + row.extra_index(owner)));
+    if (LONG) {
+      s += s_all;
+      w += w_all;
+    }
     same = __reduce_add_sync(0xffffffffu, same);
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) {
@@ -703,8 +733,13 @@ __device__ __forceinline__ void row_results(const LogprobsParams& p, LogShared<M
   }
 }
 
-// MAIN: streaming threads
+// Vectors of a CTA whose sums are one chain: two elements of a batch an addition.
 template <typename E, int MAIN>
+constexpr int kLogChainVectors = kLogChain * 2 / (16 / (int)sizeof(typename E::T)) * MAIN;
+
+// (rows of one chain apart: with the joins in their loop 4096 rows of 126464 in bf16 take 180 us for 173; 256 rows of 1048576,
+// which need them, 111 us, 107 with one chain)
+template <typename E, int MAIN, bool LONG>
 __global__ void __launch_bounds__(LogCfg<MAIN>::THREADS, LogCfg<MAIN>::CTAS)
     logprobs_kernel(const __grid_constant__ LogprobsParams p) {
   using C = LogCfg<MAIN>;
@@ -757,43 +792,50 @@ __global__ void __launch_bounds__(LogCfg<MAIN>::THREADS, LogCfg<MAIN>::CTAS)
           left = span;
         }
       };
-      for (int v0 = row.v0; v0 < row.v1; v0 += C::CHUNK) {
-        mbar_wait_long(&sh.full[slot], phase, &sh.abort, g_logprobs_err, ERR_LOGPROBS);
-        uint64_t* empty = &sh.empty[slot];
-        const uint4* chunk = ring + slot * C::CHUNK + tid;
-        if (++slot == p.slots) {
-          slot = 0;
-          phase ^= 1u;
-        }
-        if (v0 + C::CHUNK <= row.v1) {
-          uint4 raw[AHEAD];
-#pragma unroll
-          for (int i = 0; i < AHEAD; ++i) raw[i] = chunk[i * MAIN];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(empty);
-          batch(mine.template add<E>(raw, c2));
-        } else {                                                     // the row's last chunk
-          int v = v0 + tid;
-          if (v + (AHEAD - 1) * MAIN < row.v1) {
+      for (int v0 = row.v0; v0 < row.v1;) {
+        constexpr int CHAIN = kLogChainVectors<E, MAIN>;
+        static_assert(CHAIN % C::CHUNK == 0, "a chain is whole chunks");
+        const int stop = LONG ? min(row.v1, v0 + CHAIN) : row.v1;
+        for (; v0 < stop; v0 += C::CHUNK) {
+          mbar_wait_long(&sh.full[slot], phase, &sh.abort, g_logprobs_err, ERR_LOGPROBS);
+          uint64_t* empty = &sh.empty[slot];
+          const uint4* chunk = ring + slot * C::CHUNK + tid;
+          if (++slot == p.slots) {
+            slot = 0;
+            phase ^= 1u;
+          }
+          if (v0 + C::CHUNK <= row.v1) {
             uint4 raw[AHEAD];
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) raw[i] = chunk[i * MAIN];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty);
             batch(mine.template add<E>(raw, c2));
-            v += AHEAD * MAIN;
+          } else {                                                     // the row's last chunk
+            int v = v0 + tid;
+            if (v + (AHEAD - 1) * MAIN < row.v1) {
+              uint4 raw[AHEAD];
+#pragma unroll
+              for (int i = 0; i < AHEAD; ++i) raw[i] = chunk[i * MAIN];
+              batch(mine.template add<E>(raw, c2));
+              v += AHEAD * MAIN;
+            }
+            if (left < span) {
+              *unit = largest;
+              unit += MAIN;
+              largest = -INFINITY;
+              left = span;
+            }
+            for (; v < row.v1; v += MAIN, chunk += MAIN) {
+              const uint4 raw1[1] = {*chunk};
+              largest = fmaxf(largest, mine.template add<E>(raw1, c2));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty);
           }
-          if (left < span) {
-            *unit = largest;
-            unit += MAIN;
-            largest = -INFINITY;
-            left = span;
-          }
-          for (; v < row.v1; v += MAIN, chunk += MAIN) {
-            const uint4 raw1[1] = {*chunk};
-            largest = fmaxf(largest, mine.template add<E>(raw1, c2));
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(empty);
         }
+        if (LONG && v0 < row.v1)       // the chain ends
+          mine.fold(sh.m[b][tid], sh.S[b][tid], sh.W[b][tid], stop - row.v0 > CHAIN, c2);
       }
       if (left < span) {
         *unit = largest;
@@ -806,12 +848,7 @@ __global__ void __launch_bounds__(LogCfg<MAIN>::THREADS, LogCfg<MAIN>::CTAS)
         if (x > mine.m) mine.raise(x, c2);
         mine.one(x, c2);
       }
-      // relative to m c2 itself
-      if (mine.plain) mine.scale(mine.rise(mine.m, 0.0f, false, c2));
-      const float2 s = f32x2_get(mine.S), w = f32x2_get(mine.W);
-      sh.m[b][tid] = mine.m;
-      sh.S[b][tid] = s.x + s.y;
-      sh.W[b][tid] = w.x + w.y;
+      mine.fold(sh.m[b][tid], sh.S[b][tid], sh.W[b][tid], LONG && row.v1 - row.v0 > kLogChainVectors<E, MAIN>, c2);
       __syncwarp();
       if (tid % 32 == 0) mbar_arrive(&sh.ready[b]);
     }
@@ -856,7 +893,7 @@ __global__ void __launch_bounds__(LogCfg<MAIN>::THREADS, LogCfg<MAIN>::CTAS)
       // (after a wait that gave up the results are invalid, and reported)
       mbar_wait_long(&sh.ready[b], (uint32_t)(k / 2) & 1u, &sh.abort, g_logprobs_err, ERR_LOGPROBS);
       __syncwarp();
-      row_results(p, sh, row, r, b, tid - MAIN, rank, ranks, c2, unit0 + b * p.units * MAIN);
+      row_results<E, MAIN, LONG>(p, sh, row, r, b, tid - MAIN, rank, ranks, c2, unit0 + b * p.units * MAIN);
       __syncwarp();
       if (tid % 32 == 0) mbar_arrive(&sh.done[b]);
       rest_sync();                     // what the results were made of is read: the next row's may be written
@@ -880,11 +917,15 @@ cudaError_t launch_logprobs(LogprobsParams& p, cudaStream_t st) {
   constexpr int chunk = C::CHUNK * 16, shared = (int)sizeof(LogShared<MAIN>), unit = 2 * MAIN * 4;
   const int fixed = shared + p.units * unit, room = (228 * 1024 / ctas - 1024 - fixed) / chunk;
   p.slots = (int)std::min<long long>({room, C::SLOTS, chunks});
-  const cudaError_t e = op_smem_once(reinterpret_cast<const void*>(logprobs_kernel<E, MAIN>),
+  auto kernel = logprobs_kernel<E, MAIN, false>;
+  if constexpr (MAIN > 128)            // (128 threads' rows, of 8192 vectors at most, are one chain each)
+    if ((p.vocab / (16 / (int)sizeof(typename E::T)) + p.cluster - 1) / p.cluster > kLogChainVectors<E, MAIN>)
+      kernel = logprobs_kernel<E, MAIN, true>;
+  static_assert(MAIN > 128 || kLogChainVectors<E, MAIN> >= 8192, "a chain a row");
+  const cudaError_t e = op_smem_once(reinterpret_cast<const void*>(kernel),
                                      std::min(shared + (kLogUnits + 1) * unit + C::SLOTS * chunk, 227 * 1024));
   if (e != cudaSuccess) return e;
-  return op_launch(logprobs_kernel<E, MAIN>, dim3((unsigned)grid), dim3(C::THREADS), (size_t)(fixed + p.slots * chunk), st,
-                   p.cluster, p);
+  return op_launch(kernel, dim3((unsigned)grid), dim3(C::THREADS), (size_t)(fixed + p.slots * chunk), st, p.cluster, p);
 }
 
 // Streaming threads: few where a row is short (8192 elements are 8 vectors each of 128 threads), or where many rows of no

@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 
 import paged_ref as ref
-from test_gpu_paged import HALF, TINY, U, Pages, attend, dev, dt, f64, torch  # noqa: F401 (torch: the fixture)
+from test_gpu_paged import HALF, TINY, U, Pages, attend, dev, dt, f64, logprobs, torch  # noqa: F401 (torch: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +107,55 @@ def test_many_light_keys_beside_a_heavy_one(torch, dtype, where, above, values, 
     q[..., 0] = a
     out = attend(torch, c, q, [n])
     attention_close(c, q, [n], out)
+
+
+# --------------------------------------------------------------------------- what long rows of logits say
+
+def logprobs_close(x, targets, top, got, rows=None):
+    """Some rows of x [rows][vocab] (64 bits) against their definition; rows long enough for chains of sums."""
+    lp, en, ids, tl = (f64(t) for t in got)
+    vocab = x.shape[1]
+    for r in range(x.shape[0]) if rows is None else rows:
+        w_lp, w_en, w_ids, w_tl, S, W, D = ref.logprobs(x[r], 1.0, int(targets[r]), top)
+        assert ids[r].astype(int).tolist()[:top] == w_ids, (r, ids[r], w_ids)
+        # a term e^d: d = z - M within 3 roundings of itself (one more to base 2), 2^d within 2^-22; sums of terms of
+        # one sign in chains of up to 256, which are joined one by one (2^16 elements of a row or more each; up to 8
+        # roundings where the reference rises), and in trees; the largest term's chain starts from the others'.
+        # A term under 2^-126, float32's least normal number, may be left out: |d| e^d is under 88 * 2^-126 there
+        c = (256 + 8 * (vocab // 65536) + 40) * U
+        least = vocab * 2.0 ** -119
+        dS, dW = c * S + 4 * U * W + least, c * W + 4 * U * D + least
+        dlog = dS / (1 + S) + 4 * U * math.log1p(S)
+        if not math.isfinite(w_lp):
+            np.testing.assert_equal(lp[r], w_lp)
+        else:
+            assert abs(lp[r] - w_lp) <= dlog + 4 * U * (2 * abs(w_lp) + math.log1p(S)), (r, lp[r], w_lp, dlog)
+        assert abs(en[r] - w_en) <= dlog + dW / (1 + S) + W * dS / (1 + S) ** 2 + 6 * U * (w_en + W), (r, en[r], w_en)
+        for a, w in zip(tl[r], w_tl):
+            assert abs(a - w) <= dlog + 4 * U * (2 * abs(w) + math.log1p(S)), (r, a, w)
+
+
+@pytest.mark.parametrize("vocab,dtype", [(1 << 20, "f32"), ((1 << 22) + 5, "f32"), ((1 << 20) + 4099, "bf16"),
+                                         (1 << 22, "f16")])
+def test_logprobs_of_rows_with_long_chains_of_sums(torch, vocab, dtype):
+    """A CTA a row; what every term adds is under half a step of a thread's sum from the start, or all are alike, or
+    one takes nearly all, or ever larger ones come."""
+    rng = np.random.default_rng(vocab)
+    kinds = np.empty((5, vocab), dtype=np.float32)
+    kinds[0] = -16.0 - 0.2 * rng.random(vocab)
+    kinds[0, :2048] = 0.0
+    kinds[1] = 3.0 * rng.standard_normal(vocab)
+    kinds[2] = rng.standard_normal(vocab)
+    kinds[2, vocab - 9] = 30.0
+    kinds[3] = np.linspace(-9.0, 9.0, vocab)
+    kinds[4] = np.where(np.arange(vocab) % 3 == 0, -np.inf, -12.0 - rng.random(vocab))
+    kinds[4, vocab // 2] = 0.0
+    five = dev(torch, kinds).to(dt(torch, dtype))
+    x = five[torch.arange(160, device="cuda") % 5].contiguous()
+    targets = rng.integers(0, vocab, 160)
+    targets[2] = vocab - 9
+    got = logprobs(torch, x, dtype, targets, 3)
+    logprobs_close(f64(x[:5]), targets, 3, got, range(5))
+    if vocab % 8 == 0:                                     # the same row at the same alignment: the same bits
+        for out in got[1:]:
+            assert torch.equal(out[:5].repeat(32, *[1] * (out.dim() - 1)), out)
