@@ -102,6 +102,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
+// (x - M) c, by half the difference: the whole may be more than float32 holds (c: up to 2^126.8).
+__device__ __forceinline__ float apart(float x, float M, float c) { return fmaf(x, 0.5f, -0.5f * M) * (2.0f * c); }
+
 // Words of 16 bytes as the element types have them: their largest (a NaN is none), and their pairs.
 template <typename E>
 struct LogWords {
@@ -215,7 +218,7 @@ struct LogSums {
     const float2 s = f32x2_get(S), w = f32x2_get(W);
     float S_all = s.x + s.y, W_all = w.x + w.y;
     if (any) {
-      const float d = t_m == m ? 0.0f : max_nan((t_m - m) * c2, -200.0f), f = exp2_fast(d);
+      const float d = t_m == m ? 0.0f : max_nan(apart(t_m, m, c2), -200.0f), f = exp2_fast(d);
       W_all += (t_W + t_S * d) * f;
       S_all += t_S * f;
     }
@@ -248,7 +251,7 @@ __device__ __forceinline__ void join_sums(LogRest& t, LogRest o, float c2) {
     t.S += o.S;                        // 0, or a NaN
     return;
   }
-  const float d = max_nan((o.m - t.m) * c2, -200.0f), f = exp2_fast(d);
+  const float d = max_nan(apart(o.m, t.m, c2), -200.0f), f = exp2_fast(d);
   t.S += (1.0f + o.S) * f;
   t.W += (o.W + (1.0f + o.S) * d) * f;
 }
@@ -437,7 +440,7 @@ __device__ __forceinline__ void row_results(const LogprobsParams& p, LogShared<M
     const int t = tid + k * kLogRest;
     float s = sh.S[b][t], w = sh.W[b][t];
     if (m[k] > -INFINITY) {
-      const float d = max_nan((m[k] - M) * c2, -200.0f), f = exp2_fast(d);
+      const float d = max_nan(apart(m[k], M, c2), -200.0f), f = exp2_fast(d);
       w = (w + s * d) * f;
       s *= f;
     }
@@ -534,7 +537,7 @@ __device__ __forceinline__ void row_results(const LogprobsParams& p, LogShared<M
         ++same;
         return;
       }
-      const float d = max_nan((x - M) * c2, -200.0f), e = exp2_fast(d);
+      const float d = max_nan(apart(x, M, c2), -200.0f), e = exp2_fast(d);
       s += e;
       w += d * e;
     };
@@ -703,7 +706,7 @@ __device__ __forceinline__ void row_results(const LogprobsParams& p, LogShared<M
   const bool finite = fabsf(sum.m) != INFINITY && sum.S == sum.S;
   const float nan = __uint_as_float(0x7fffffffu), log_sum = finite ? log1pf(sum.S) : nan;
   if (tid == 0) {
-    if (p.logp) p.logp[r] = given ? (E::get(&given_x) - sum.m) * p.scale - log_sum : nan;
+    if (p.logp) p.logp[r] = given ? apart(E::get(&given_x), sum.m, p.scale) - log_sum : nan;
     if (p.entropy) p.entropy[r] = log_sum - sum.W * 0.6931471805599453f / (1.0f + sum.S);
   }
   for (int i = tid; i < ranks * top; i += kLogRest) {
@@ -728,7 +731,7 @@ __device__ __forceinline__ void row_results(const LogprobsParams& p, LogShared<M
     }
     if (n < top) {
       p.top_ids[(long long)r * top + n] = x.i;
-      p.top_logp[(long long)r * top + n] = x.i < 0 ? nan : (x.x - sum.m) * p.scale - log_sum;
+      p.top_logp[(long long)r * top + n] = x.i < 0 ? nan : apart(x.x, sum.m, p.scale) - log_sum;
     }
   }
 }

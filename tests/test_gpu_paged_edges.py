@@ -111,12 +111,12 @@ def test_many_light_keys_beside_a_heavy_one(torch, dtype, where, above, values, 
 
 # --------------------------------------------------------------------------- what long rows of logits say
 
-def logprobs_close(x, targets, top, got, rows=None):
+def logprobs_close(x, targets, top, got, rows=None, scale=1.0):
     """Some rows of x [rows][vocab] (64 bits) against their definition; rows long enough for chains of sums."""
     lp, en, ids, tl = (f64(t) for t in got)
     vocab = x.shape[1]
     for r in range(x.shape[0]) if rows is None else rows:
-        w_lp, w_en, w_ids, w_tl, S, W, D = ref.logprobs(x[r], 1.0, int(targets[r]), top)
+        w_lp, w_en, w_ids, w_tl, S, W, D = ref.logprobs(x[r], scale, int(targets[r]), top)
         assert ids[r].astype(int).tolist()[:top] == w_ids, (r, ids[r], w_ids)
         # a term e^d: d = z - M within 3 roundings of itself (one more to base 2), 2^d within 2^-22; sums of terms of
         # one sign in chains of up to 256, which are joined one by one (2^16 elements of a row or more each; up to 8
@@ -159,3 +159,20 @@ def test_logprobs_of_rows_with_long_chains_of_sums(torch, vocab, dtype):
     if vocab % 8 == 0:                                     # the same row at the same alignment: the same bits
         for out in got[1:]:
             assert torch.equal(out[:5].repeat(32, *[1] * (out.dim() - 1)), out)
+
+
+@pytest.mark.parametrize("scale", [0.3, 2e-38, 1e-37])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,vocab", [(3, 501), (2, 40000), (200, 9001)])
+def test_logprobs_of_logits_further_apart_than_float32_holds(torch, rows, vocab, dtype, scale):
+    """The difference of two logits is past the type, but not what an inverse temperature under 1 makes of it."""
+    rng = np.random.default_rng(vocab)
+    x = 3e38 * rng.uniform(-1.0, 1.0, (rows, vocab)).astype(np.float32)
+    x[0, : vocab // 2] = -np.inf
+    x[1] = -3e38
+    x[1, vocab - 2] = 3e38
+    buf = dev(torch, x).to(dt(torch, dtype))
+    targets = rng.integers(0, vocab, rows)
+    targets[0], targets[1] = int(np.argmin(x[0, vocab // 2:])) + vocab // 2, 7
+    got = logprobs(torch, buf, dtype, targets, 60, scale=scale)
+    logprobs_close(f64(buf), targets, 60, got, range(min(rows, 8)), scale=float(np.float32(scale)))
