@@ -132,6 +132,9 @@ def logprobs_close(x, targets, top, got, rows=None, scale=1.0):
             assert abs(lp[r] - w_lp) <= dlog + 4 * U * (2 * abs(w_lp) + math.log1p(S)), (r, lp[r], w_lp, dlog)
         assert abs(en[r] - w_en) <= dlog + dW / (1 + S) + W * dS / (1 + S) ** 2 + 6 * U * (w_en + W), (r, en[r], w_en)
         for a, w in zip(tl[r], w_tl):
+            if not math.isfinite(w):
+                np.testing.assert_equal(a, w)
+                continue
             assert abs(a - w) <= dlog + 4 * U * (2 * abs(w) + math.log1p(S)), (r, a, w)
 
 
@@ -176,3 +179,47 @@ def test_logprobs_of_logits_further_apart_than_float32_holds(torch, rows, vocab,
     targets[0], targets[1] = int(np.argmin(x[0, vocab // 2:])) + vocab // 2, 7
     got = logprobs(torch, buf, dtype, targets, 60, scale=scale)
     logprobs_close(f64(buf), targets, 60, got, range(min(rows, 8)), scale=float(np.float32(scale)))
+
+
+@pytest.mark.parametrize("vocab,top,dtype", [(126471, 20, "f32"), (126471, 64, "f32"), (300007, 50, "bf16"),
+                                             (1000003, 7, "f16")])
+def test_logprobs_of_rows_whose_units_are_several_batches(torch, vocab, top, dtype):
+    """A CTA a row, long enough for units of 2, 4 and 8 batches of a thread, the last ones partly filled: ties in many
+    units, in the elements behind the last whole batch and behind the last vector, one thread's elements the largest."""
+    rng = np.random.default_rng(vocab + top)
+    x = np.empty((7, vocab), dtype=np.float32)
+    x[0] = 2.0 * rng.standard_normal(vocab)
+    x[1] = rng.integers(0, 9, vocab)
+    x[2] = np.where(np.arange(vocab) % 2048 < 8, 5.0 + rng.random(vocab), -1.0)
+    x[3] = np.linspace(-20.0, 4.0, vocab)
+    x[4] = -np.inf
+    x[4, rng.choice(vocab, 30, replace=False)] = 1.0
+    x[4, vocab - 1] = 2.0
+    x[5] = rng.standard_normal(vocab)
+    x[5, -3000:] = 9.0
+    x[5, -3000::7] = 9.5
+    x[6] = 0.0
+    buf = dev(torch, x).to(dt(torch, dtype))
+    targets = rng.integers(0, vocab, 160)
+    targets[4] = vocab - 1
+    got = logprobs(torch, buf[torch.arange(160, device="cuda") % 7].contiguous(), dtype, targets, top)
+    order = [0, 1, 2, 3, 4, 5, 6, 159]
+    logprobs_close(f64(buf[torch.tensor(order, device="cuda") % 7]), targets[order], top, [t[order] for t in got])
+
+
+# --------------------------------------------------------------------------- weights of many sequences
+
+@pytest.mark.parametrize("b,R,H,Hkv,dtype", [(32, 1, 8, 8, "bf16"), (48, 1, 8, 4, "f16"), (8, 16, 32, 8, "bf16"),
+                                             (10, 4, 16, 8, "f16")])
+def test_weights_of_runs_of_keys(torch, b, R, H, Hkv, dtype):
+    """So many keys that a CTA of the second kernel adds up the weights of several pieces of them: lengths that end in
+    the first, inside a run, at its ends and in the table's last page."""
+    rng = np.random.default_rng(b + R)
+    ps, most = 64, 128                                     # 8192 positions
+    lens = rng.integers(1, most * ps, b)
+    lens[:8] = [8192, 513, 511, 0, 8191, 1, 2049, 6145]
+    c = Pages(torch, rng, b, Hkv, 64, dtype, ps, most).fill(rng, lens)
+    q = dev(torch, (1.5 * rng.standard_normal((b, R, H, 64))).astype(np.float32)).to(dt(torch, dtype))
+    mass = torch.zeros(b, Hkv, most * ps, device="cuda")
+    out = attend(torch, c, q, lens, mass=mass)
+    attention_close(c, q, lens, out, mass)
