@@ -25,8 +25,10 @@ AttnPagedPlan plan_attn_paged(long long b, long long H_kv, long long rows, int h
   a.items = b * H_kv * a.row_tiles;
   a.tiles = std::max(1LL, (T + kPagedKeys - 1) / kPagedKeys);
   a.ctas = (a.N <= 16 ? 2 : 1) * op_device_sms();
-  // Few keys: items as they are, one kernel (32 rows of 32 heads, 512 keys: 11.0 us against 12.1 in shared runs; 768
-  // keys: 14.3 against 12.7).
+  // Few keys: items as they are, one kernel.  Whole items and shared runs, us, at 250, 500 and 1000 keys: 32 rows of 32
+  // heads 8.2 and 10.9, 11.1 and 11.4, 17.4 and 13.0; of 8 sequences 13.1 and 14.6, 18.6 and 23.2, 30.4 and 33.7; of 16
+  // with 32 heads on 8 (500, 1000) 24.6 and 33.3, 38.2 and 45.3; one token of 32 heads 6.9 and 9.3, 10.2 and 9.8, 17.3 and
+  // 10.9; of 64 sequences, 32 heads on 8, 16.1 and 17.3, 25.0 and 26.4, 42.1 and 40.4.
   a.whole = a.tiles <= 4;
   a.nz = rows <= 4 ? 4 : a.N;
   size_t at = 0;

@@ -6,7 +6,7 @@
 // one, or counted by two digits of 10 bits.  A last walk writes the positions that stay in their order: where all of the
 // threshold's weight stay, a warp packs its run of positions in place and writes it out; else it counts first.
 //
-// Latency and issue slots bound the selection (12 us for 32768 keys, 4.5 for 4097), HBM the copy: 8 sequences of 16 to 32
+// Latency and issue slots bound the selection (alone 11.8 us for 32768 keys of 8 heads, 5.2 for 4097), HBM the copy: 8 sequences of 16 to 32
 // thousand keys of 8 heads of 128 in bf16 to 8192 keys: 104 us in all, 5.3 TB/s; one of 4097 to 1024: 7.6 us.  Clusters
 // of four CTAs a head, with histograms added up over distributed shared memory, took 40 us for the selection alone; the
 // first histogram in two copies, lanes in turn, nothing less; loops rolled up 107 us.
@@ -44,7 +44,9 @@ constexpr int kEvictStep = 8 * kEvictThreads;   // (32 runs of 256 positions)
 constexpr int kEvictMost = 6 * kEvictStep;      // positions whose weights stay in shared memory
 constexpr int kEvictList = 2048;       // keys that agree with the threshold's first bits, where they are no more
 constexpr int kEvictBins = 4096;
-constexpr int kEvictDirect = 128;      // keys of the list that are compared one by one
+// keys of the list that are compared one by one, more by digits (none, 128, 512: 4097 keys of 8 heads 8.15, 7.57, 7.61
+// us; 1000 keys 6.74, 5.85, 5.80; 16000 of hd 64 10.5, 10.4, 11.1; the batch above 104, 104, 110)
+constexpr int kEvictDirect = 128;
 constexpr uint32_t kEvictFixed = 0xffffffffu;   // the weight of what stays in any case
 
 struct EvictShared {

@@ -9,7 +9,10 @@
 // by bulk copies, up to 64 KB ahead; the cosines and sines of up to 1024 pairs of rows to come
 // are worked out at once, one a thread.
 // 8191 rows of 32 + 8 heads of 128 in bf16 with their values to pages: 46.5 us, 4.3 TB/s; the same rows as they are,
-// neither normalised nor turned, 35.6 (a plain copy of them 31.6): what is left is arithmetic, at 60 % of the issue slots.
+// neither normalised nor turned, 35.6 (a plain copy of them 31.6).  Nothing is full there: DRAM 40 % of nominal, half of
+// the issue slots, no pipe over a third.  Latency bounds it: 5.4 warps a scheduler, each with one row under way, wait 9
+// cycles for every instruction they issue, for shared memory and shuffles, for the instruction before, for global memory
+// and at barriers.
 // 8 such rows: 3.5 us, a launch's latency.  Loads into registers instead of bulk copies: 56 us; three CTAs of 56
 // registers a thread for two of 64: 46.1, but float32 rows of 16 heads 72 us for 66.
 #include <algorithm>

@@ -7,11 +7,11 @@
 // parts of the entropy are of one sign.
 //
 // Bound by HBM: the logits are read once.  A CTA takes row after row (or a cluster of up to 8 one row, where rows are
-// few).  One warp copies the rows into a ring in shared memory, past the end of a row too; eight stream them: every
-// thread keeps the largest of its elements m and, relative to it, S and W of them all (in float32 chains of 256 terms, each
-// joined to those before), leaves them in shared memory and goes on to the next row.  Four warps work out a row's results
-// meanwhile (the same threads one after the other took 212 us for the case below, with loads into registers and results
-// apart 217).
+// few).  One warp copies the rows into a ring in shared memory, past the end of a row too; eight (four for short rows)
+// stream them: every thread keeps the largest of its elements m and, relative to it, S and W of them all (in float32
+// chains of 256 terms, each joined to those before), leaves them in shared memory and goes on to the next row.  Four
+// warps work out a row's results meanwhile (the same threads one after the other took 212 us for the case below, with
+// loads into registers and results apart 217).
 // What needs elements again is a few threads' worth, which lies in L2 still:
 //   - the alternatives are among the elements of units whose largest is no less than the top-th largest of 128 group
 //     maxima (a lower bound of the top-th largest element): for 20 of 126464 about 22 units of 32 elements.  Elements
@@ -59,6 +59,8 @@ struct LogCfg {
   static constexpr int SLOTS = 6;                                // of the ring, at most
 };
 constexpr int kLogGroups = 128;
+// alternatives up to which 32 groups give the bound, else 128 (32 / 128 groups, 4096 rows of 126464: 1 alternative 164, 169
+// us, 5 167, 172, 20 172.6, 175.4, 24 176.2, 175.8, 32 274, 180; 32 rows, 5 alternatives 12.2, 12.8, 20 18.9, 18.4)
 constexpr int kLogFewTop = 24;
 constexpr int kLogUnits = 16;        // of a thread's batches at most, each with a largest element of its own (and one for the rest)
 constexpr int kMostUnits = 512;      // units that are looked through again, before all are
@@ -740,8 +742,8 @@ __device__ __forceinline__ void row_results(const LogprobsParams& p, LogShared<M
 template <typename E, int MAIN>
 constexpr int kLogChainVectors = kLogChain * 2 / (16 / (int)sizeof(typename E::T)) * MAIN;
 
-// (rows of one chain apart: with the joins in their loop 4096 rows of 126464 in bf16 take 180 us for 173; 256 rows of 1048576,
-// which need them, 111 us, 107 with one chain)
+// (rows of one chain apart: with the joins in their loop 4096 rows of 126464 in bf16 take 180 us for 173; 256 rows of
+// 1048576, which need them, 111 us, 107 with one chain)
 template <typename E, int MAIN, bool LONG>
 __global__ void __launch_bounds__(LogCfg<MAIN>::THREADS, LogCfg<MAIN>::CTAS)
     logprobs_kernel(const __grid_constant__ LogprobsParams p) {

@@ -727,10 +727,11 @@ dllm_status dllm_op_kv_paged_evict(const dllm_kv_paged* src, const dllm_kv_paged
  * inv_temperature: > 0, at most 1e38.  Sums are float32, taken apart from the largest
  * term, so that log p and entropy of a nearly certain row keep their relative
  * accuracy, in chains of at most 256 terms that are joined one by one: about
- * (300 + vocab / 2^14) 2^-24 of a sum where all roundings go one way.  A logit of -inf is a token that cannot come: p = 0, and an
- * alternative only after all others.  A row with a NaN or +inf, or of nothing
- * but -inf, has NaN for every log p and entropy; a NaN is no alternative (id -1 where there are
- * too few others). */
+ * (300 + vocab / 2^14) 2^-24 of a sum where all roundings go one way.  A logit
+ * of -inf is a token that cannot come: p = 0, and an alternative only after all
+ * others.  A row with a NaN or +inf, or of nothing but -inf, has NaN for every
+ * log p and entropy; a NaN is no alternative (id -1 where there are too few
+ * others). */
 dllm_status dllm_op_token_logprobs(const void* logits, int64_t row_stride, int32_t dtype, int32_t rows, int32_t vocab,
                                    float inv_temperature, const int32_t* targets, float* logprobs, float* entropy,
                                    int32_t top, int32_t* top_ids, float* top_logprobs, void* cuda_stream);
