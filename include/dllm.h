@@ -637,7 +637,8 @@ typedef struct dllm_kv_paged {
  * (both weights NULL).  rope: NULL: nothing turns (positions may be NULL);
  * rot_dim a multiple of 16.  positions: device int32 [rows].  An output may be
  * its input with the same strides and type.  Squares are float32: elements
- * stay within 2^59. */
+ * stay within 2^59, and with eps = 0 a head that is not all zeros has one of
+ * 2^-50 at least. */
 dllm_status dllm_op_qk_norm_rope(const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride, void* q_out,
                                  int64_t q_out_row_stride, void* k_out, int64_t k_out_row_stride,
                                  const int32_t* positions, int32_t rows, int32_t H, int32_t H_kv, int32_t hd,
